@@ -301,6 +301,97 @@ k3moe_status k3moe_full_forward(const k3moe_config *cfg, const k3moe_full_dims *
                                 float *weight, int32_t *offsets, int32_t *perm, float *out,
                                 void *ws, size_t ws_bytes, k3moe_stream stream);
 
+/* ---- The token mixer beside the block: the projections of a decoder layer and the
+ * gated delta rule between them (the recurrence of the README's k3_kda_step, Part II,
+ * the layer's first half; its MoE half is the block above). */
+
+/* Activations of k3moe_linear, on z = x W^T + bias in float. */
+typedef enum k3moe_act {
+    K3MOE_ACT_NONE = 0,
+    K3MOE_ACT_RELU = 1,        /* max(z, 0) */
+    K3MOE_ACT_SILU = 2,        /* z / (1 + exp(-z)) */
+    K3MOE_ACT_GELU = 3,        /* z (1 + erf(z / sqrt 2)) / 2 */
+    K3MOE_ACT_SIGMOID = 4,     /* 1 / (1 + exp(-z)) */
+    K3MOE_ACT_LOGSIGMOID = 5   /* log(1 / (1 + exp(-z))): a decay's logarithm, always <= 0 */
+} k3moe_act;
+
+typedef struct k3moe_linear_config {
+    int32_t n;            /* output columns N, 1 .. 2^20 */
+    int32_t k;            /* input columns K, a multiple of 8, 8 .. 65536 */
+    int32_t act;          /* K3MOE_ACT_* */
+    int32_t y_f32;        /* 1: y and residual are f32; 0: bf16 */
+} k3moe_linear_config;
+
+/* Workspace bytes k3moe_linear needs for any 0 <= T <= T_max.  Status word, alignment
+ * and zero-filling as k3moe_workspace_bytes; a workspace of the other calls that is
+ * large enough serves as well (calls on one stream). */
+k3moe_status k3moe_linear_workspace_bytes(const k3moe_linear_config *lc, int32_t T_max, size_t *bytes);
+
+/* y = act(x W^T + bias) + residual, accumulated in float and rounded once:
+ *   x        [T][K] bf16, row stride x_stride elements (a multiple of 8, >= K)
+ *   w        [N][K] bf16, dense
+ *   bias     [N] f32 or NULL
+ *   residual [T][N] of y's type, row stride residual_stride >= N, or NULL; it may be y
+ *            itself (same pointer and stride) but not overlap it otherwise
+ *   y        [T][N] bf16 or f32 (lc->y_f32), row stride y_stride >= N, written
+ * x and w 16-byte aligned; bias, residual and y aligned to their element.  T may be 0
+ * (nothing written).  Every sum's order is fixed by T, N and K, so results repeat bit
+ * for bit.  ws per k3moe_linear_workspace_bytes(T_max >= T). */
+k3moe_status k3moe_linear(const k3moe_linear_config *lc, int32_t T, const uint16_t *x, int64_t x_stride,
+                          const uint16_t *w, const float *bias, const void *residual,
+                          int64_t residual_stride, void *y, int64_t y_stride, void *ws,
+                          size_t ws_bytes, k3moe_stream stream);
+
+typedef struct k3moe_delta_config {
+    int32_t n_heads;      /* value heads H, 1 .. 1024: each has a state, a decay and a step size */
+    int32_t n_qk_heads;   /* query and key heads; divides H, head h reads q/k head h / (H / n_qk_heads) */
+    int32_t head_dim;     /* D, width of a head's keys and of its values; must be 128 */
+    int32_t gate_dim;     /* 1: one decay per head; D: one per key channel */
+    int32_t qk_norm;      /* 1: q and k are divided by sqrt(sum x^2 + norm_eps) over the head; 0: as given */
+    float norm_eps;       /* finite and > 0 when qk_norm */
+    float scale;          /* finite; multiplies q */
+} k3moe_delta_config;
+
+/* K3MOE_OK when every field of *dc is in range, else K3MOE_EINVAL or K3MOE_ESHAPE. */
+k3moe_status k3moe_delta_validate_config(const k3moe_delta_config *dc);
+
+/* Workspace bytes k3moe_delta_rule needs for any call of at most n_seq_max sequences and
+ * T_max tokens in all (conventions as k3moe_workspace_bytes). */
+k3moe_status k3moe_delta_workspace_bytes(const k3moe_delta_config *dc, int32_t n_seq_max, int32_t T_max,
+                                         size_t *bytes);
+
+/* The gated delta rule over n_seq packed sequences, T tokens in all.  For each sequence
+ * and value head, with the state S [D keys][D values] and for each token t in order:
+ *   S = diag(exp(g_t)) S
+ *   u = beta_t (v_t - S^T k_t)
+ *   S = S + k_t u^T
+ *   o_t = scale * S^T q_t
+ *   seq_start [n_seq+1] int32: sequence i has tokens seq_start[i] .. seq_start[i+1]-1
+ *             (ascending within 0 .. T, lengths from 0 on).  NULL with T == n_seq means one token
+ *             each (a decode step), and with n_seq == 1 one sequence of T tokens
+ *   q, k      [T][n_qk_heads][D] bf16, v [T][H][D] bf16: heads dense within a token, token
+ *             strides q_stride, k_stride, v_stride elements (multiples of 8), so that all
+ *             three may be slices of one projection's rows
+ *   g         [T][H][gate_dim] f32, the decay's logarithm (<= 0; -infinity forgets all)
+ *   beta      [T][H] f32
+ *   state_in  [n_slots][H][D][D] f32 or NULL (every sequence starts from zero)
+ *   state_out [n_slots][H][D][D] f32, written for the slots of the call's sequences, the
+ *             others untouched; it may be state_in itself.  Sequence i uses slot slots[i]
+ *             (int32, each at most once), or slot i when slots is NULL
+ *   out       [T][H][D] bf16, dense, written for the sequences' tokens
+ * A sequence of length 0 has its state copied.  A slot outside [0, n_slots) sets
+ * K3MOE_DEV_BAD_INDEX, a seq_start pair that is not ascending within [0, T] sets
+ * K3MOE_DEV_BAD_OFFSETS, and that sequence is skipped.  States and every sum are float; out
+ * is rounded once to bf16.  q, k, v 16-byte aligned, g and the states 16-byte aligned, out
+ * 16-byte aligned.  T == 0 or n_seq == 0: with n_seq == 0 nothing is written.  ws per
+ * k3moe_delta_workspace_bytes. */
+k3moe_status k3moe_delta_rule(const k3moe_delta_config *dc, int32_t n_seq, int32_t T,
+                              const int32_t *seq_start, const uint16_t *q, int64_t q_stride,
+                              const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                              const float *g, const float *beta, const float *state_in,
+                              float *state_out, int32_t n_slots, const int32_t *slots, uint16_t *out,
+                              void *ws, size_t ws_bytes, k3moe_stream stream);
+
 /* Synchronises `stream`, returns the device status word of `ws` in *code,
  * and clears it: the report of the README's rule that corruption is counted,
  * never silent (kimi-k3-in-c README, Part II, section 9, the k3_moe listing's

@@ -1,5 +1,8 @@
 """Routed-expert layer of a Kimi-K3-style latent MoE on GB300 (sm_103a), and the
-full-width Stable LatentMoE block around it (``k3moe_full_forward``, ``MoEBlock``).
+full-width Stable LatentMoE block around it (``k3moe_full_forward``, ``MoEBlock``);
+and the token mixer beside the block: linear projections with their epilogue
+(``k3moe_linear``, ``Linear``) and the gated delta rule (``k3moe_delta_rule``,
+``DeltaRule``).
 
 A thin ctypes binding over ``libk3moe.so``; every function has the name of the C
 entry point it calls (``include/k3moe.h``) and only marshals arguments: torch
@@ -21,6 +24,9 @@ __all__ = [
     "k3moe_set_prefill_gemm", "k3moe_get_prefill_gemm", "PREFILL_GEMM_F16", "PREFILL_GEMM_BLOCK_SCALED",
     "library_path", "MoELayer", "K3MoEFullDims", "k3moe_full_dims", "k3moe_full_workspace_bytes",
     "k3moe_full_forward", "MoEBlock",
+    "K3MoELinearConfig", "k3moe_linear_config", "k3moe_linear_workspace_bytes", "k3moe_linear", "Linear",
+    "K3MoEDeltaConfig", "k3moe_delta_config", "k3moe_delta_validate_config", "k3moe_delta_workspace_bytes",
+    "k3moe_delta_rule", "DeltaRule", "ACTIVATIONS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -48,6 +54,16 @@ class K3MoEFullDims(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int32), ("latent_norm", ctypes.c_int32), ("rms_eps", ctypes.c_float)]
 
 
+class K3MoELinearConfig(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("k", ctypes.c_int32), ("act", ctypes.c_int32), ("y_f32", ctypes.c_int32)]
+
+
+class K3MoEDeltaConfig(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("n_qk_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("gate_dim", ctypes.c_int32), ("qk_norm", ctypes.c_int32), ("norm_eps", ctypes.c_float),
+                ("scale", ctypes.c_float)]
+
+
 class K3MoEError(RuntimeError):
     def __init__(self, what: str, status: int):
         super().__init__(f"{what}: {STATUS_NAMES.get(status, status)} ({k3moe_strerror(status)})")
@@ -72,6 +88,7 @@ def lib():
         L = ctypes.CDLL(path)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         cp = ctypes.POINTER(K3MoEConfig)
+        lp, dp = ctypes.POINTER(K3MoELinearConfig), ctypes.POINTER(K3MoEDeltaConfig)
         sig = {
             "k3moe_strerror": (ctypes.c_char_p, [ctypes.c_int]),
             "k3moe_validate_config": (ctypes.c_int, [cp]),
@@ -94,6 +111,12 @@ def lib():
             "k3moe_full_forward": (ctypes.c_int, [cp, ctypes.POINTER(K3MoEFullDims), i32, vp, vp, vp, vp,
                                                   vp, sz, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                                   sz, vp]),
+            "k3moe_linear_workspace_bytes": (ctypes.c_int, [lp, i32, ctypes.POINTER(sz)]),
+            "k3moe_linear": (ctypes.c_int, [lp, i32, vp, i64, vp, vp, vp, i64, vp, i64, vp, sz, vp]),
+            "k3moe_delta_validate_config": (ctypes.c_int, [dp]),
+            "k3moe_delta_workspace_bytes": (ctypes.c_int, [dp, i32, i32, ctypes.POINTER(sz)]),
+            "k3moe_delta_rule": (ctypes.c_int, [dp, i32, i32, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp,
+                                                i32, vp, vp, vp, sz, vp]),
             "k3moe_launch_count": (i64, []),
             "k3moe_set_prefill_gemm": (ctypes.c_int, [i32]),
             "k3moe_get_prefill_gemm": (i32, []),
@@ -255,6 +278,56 @@ def k3moe_full_forward(cfg, fd, T, h, w_router, bias, w_down, expert_table, norm
         _ptr(expert_table), tb, _ptr(norm_gain), _ptr(w_up), _ptr(sh_w1), _ptr(sh_w3), _ptr(sh_w2),
         _ptr(idx), _ptr(weight), _ptr(offsets), _ptr(perm), _ptr(out), _ptr(ws), wb,
         _stream(stream)))
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4, "logsigmoid": 5}
+
+
+def k3moe_linear_config(n, k, act="none", y_f32=False) -> K3MoELinearConfig:
+    """act: a name of ACTIVATIONS or its number."""
+    return K3MoELinearConfig(n, k, ACTIVATIONS[act] if isinstance(act, str) else act, int(y_f32))
+
+
+def k3moe_linear_workspace_bytes(lc: K3MoELinearConfig, T_max: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("k3moe_linear_workspace_bytes", lib().k3moe_linear_workspace_bytes(ctypes.byref(lc), T_max,
+                                                                              ctypes.byref(out)))
+    return out.value
+
+
+def k3moe_linear(lc, T, x, x_stride, w, bias, residual, residual_stride, y, y_stride, ws, ws_bytes=None,
+                 stream=None):
+    wb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check("k3moe_linear", lib().k3moe_linear(
+        ctypes.byref(lc), T, _ptr(x), x_stride, _ptr(w), _ptr(bias), _ptr(residual), residual_stride,
+        _ptr(y), y_stride, _ptr(ws), wb, _stream(stream)))
+
+
+def k3moe_delta_config(n_heads, n_qk_heads, head_dim=128, gate_dim=1, qk_norm=1, norm_eps=1e-6,
+                       scale=None) -> K3MoEDeltaConfig:
+    """scale: head_dim ** -0.5 when None."""
+    return K3MoEDeltaConfig(n_heads, n_qk_heads, head_dim, gate_dim, int(qk_norm), norm_eps,
+                            scale if scale is not None else max(head_dim, 1) ** -0.5)
+
+
+def k3moe_delta_validate_config(dc: K3MoEDeltaConfig) -> int:
+    return lib().k3moe_delta_validate_config(ctypes.byref(dc))
+
+
+def k3moe_delta_workspace_bytes(dc: K3MoEDeltaConfig, n_seq_max: int, T_max: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("k3moe_delta_workspace_bytes", lib().k3moe_delta_workspace_bytes(
+        ctypes.byref(dc), n_seq_max, T_max, ctypes.byref(out)))
+    return out.value
+
+
+def k3moe_delta_rule(dc, n_seq, T, seq_start, q, q_stride, k, k_stride, v, v_stride, g, beta, state_in,
+                     state_out, n_slots, slots, out, ws, ws_bytes=None, stream=None):
+    wb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check("k3moe_delta_rule", lib().k3moe_delta_rule(
+        ctypes.byref(dc), n_seq, T, _ptr(seq_start), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v),
+        v_stride, _ptr(g), _ptr(beta), _ptr(state_in), _ptr(state_out), n_slots, _ptr(slots), _ptr(out),
+        _ptr(ws), wb, _stream(stream)))
 
 
 def k3moe_device_status(ws, stream=None):
@@ -421,3 +494,143 @@ class MoEBlock:
         """k3moe_full_forward on the fixed buffers h [T][H] and out [T][H] as a CUDA graph
         (see _capture)."""
         return _capture(self, h, out)
+
+
+# ----------------------------------------------------------------------------- the token mixer's holders
+
+def _tensor(what, t, dtypes, dims, device):
+    """Raises ValueError unless t is a `dims`-dimensional tensor of one of dtypes on device
+    whose innermost dimension is dense: what the entry points take on trust from a pointer."""
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.dim() != dims:
+        raise ValueError(f"{what}: {t.dim()} dimensions, expected {dims}")
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: the last dimension has stride {t.stride(-1)}, expected 1")
+
+
+def _shape(what, t, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _row_stride(t):
+    """Elements from a row to the next; a single row has none of its own."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t[0].numel())
+
+
+def _cuda(device):
+    import torch
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+class Linear:
+    """One projection y = act(x W^T + bias) + residual (k3moe_linear): holds the weights w
+    [n][k] bf16 and the bias [n] f32 or None, both set by the caller, and a workspace."""
+
+    def __init__(self, lc: K3MoELinearConfig, T_max: int, device="cuda"):
+        import torch
+        self.lc = lc
+        self.device = _cuda(device)
+        self.T_max = T_max
+        self.w = self.bias = None
+        self.ws_bytes = k3moe_linear_workspace_bytes(lc, T_max)
+        self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+
+    def __call__(self, x, y, residual=None, stream=None):
+        """x [T][k] bf16 (rows may be slices of wider ones), y [T][n] written and returned;
+        residual [T][n] of y's type, which may be y."""
+        import torch
+        lc, T = self.lc, x.shape[0]
+        bf16, ytype = (torch.bfloat16, torch.int16), (torch.float32,) if lc.y_f32 else (torch.bfloat16, torch.int16)
+        if T > self.T_max:
+            raise ValueError(f"x: {T} rows, the holder is for {self.T_max}")
+        _tensor("x", x, bf16, 2, self.device)
+        _shape("x", x, (T, lc.k))
+        _tensor("w", self.w, bf16, 2, self.device)
+        _shape("w", self.w, (lc.n, lc.k))
+        if not self.w.is_contiguous():
+            raise ValueError("w: not contiguous")
+        _tensor("y", y, ytype, 2, self.device)
+        _shape("y", y, (T, lc.n))
+        if self.bias is not None:
+            _tensor("bias", self.bias, (torch.float32,), 1, self.device)
+            _shape("bias", self.bias, (lc.n,))
+        if residual is not None:
+            _tensor("residual", residual, ytype, 2, self.device)
+            _shape("residual", residual, (T, lc.n))
+        if T:
+            k3moe_linear(lc, T, x, _row_stride(x), self.w, self.bias, residual,
+                         _row_stride(residual) if residual is not None else 0, y, _row_stride(y), self.ws,
+                         self.ws_bytes, stream)
+        return y
+
+
+class DeltaRule:
+    """The gated delta rule (k3moe_delta_rule) for up to n_seq_max sequences and T_max tokens
+    a call: holds its workspace; the states are the caller's."""
+
+    def __init__(self, dc: K3MoEDeltaConfig, n_seq_max: int, T_max: int, device="cuda"):
+        import torch
+        self.dc = dc
+        self.device = _cuda(device)
+        self.n_seq_max, self.T_max = n_seq_max, T_max
+        self.ws_bytes = k3moe_delta_workspace_bytes(dc, n_seq_max, T_max)
+        self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+
+    def new_state(self, n_slots):
+        """A zeroed pool of n_slots states [n_slots][n_heads][head_dim][head_dim] f32."""
+        import torch
+        D = self.dc.head_dim
+        return torch.zeros((n_slots, self.dc.n_heads, D, D), dtype=torch.float32, device=self.device)
+
+    def __call__(self, q, k, v, g, beta, out, state_in, state_out, seq_start=None, slots=None, stream=None):
+        """q, k [T][n_qk_heads][D], v [T][n_heads][D] bf16, whose rows may be slices of wider
+        ones; g [T][n_heads][gate_dim], beta [T][n_heads] f32; out [T][n_heads][D] bf16,
+        written and returned; state_in (None: zeros) and state_out [slots][n_heads][D][D] f32,
+        which may be the same; slots [n_seq] int32 or None (sequence i in slot i); seq_start
+        [n_seq+1] int32, or None for one token each (with one slot: one sequence)."""
+        import torch
+        dc, T, D = self.dc, q.shape[0], self.dc.head_dim
+        bf16, f32, i32 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,)
+        for name, t, shape, types in (("q", q, (T, dc.n_qk_heads, D), bf16), ("k", k, (T, dc.n_qk_heads, D), bf16),
+                                      ("v", v, (T, dc.n_heads, D), bf16), ("g", g, (T, dc.n_heads, dc.gate_dim), f32),
+                                      ("beta", beta, (T, dc.n_heads), f32), ("out", out, (T, dc.n_heads, D), bf16)):
+            _tensor(name, t, types, len(shape), self.device)
+            _shape(name, t, shape)
+            if t.dim() == 3 and T and t.shape[1] > 1 and t.stride(1) != t.shape[2]:
+                raise ValueError(f"{name}: heads with stride {t.stride(1)}, expected {t.shape[2]}")
+        for name, t in (("g", g), ("beta", beta), ("out", out)):
+            if not t.is_contiguous():
+                raise ValueError(f"{name}: not contiguous")
+        for name, t in (("state_in", state_in), ("state_out", state_out)):
+            if t is None and name == "state_in":
+                continue
+            _tensor(name, t, f32, 4, self.device)
+            _shape(name, t, (state_out.shape[0], dc.n_heads, D, D))
+            if not t.is_contiguous():
+                raise ValueError(f"{name}: not contiguous")
+        n_slots = state_out.shape[0]
+        if slots is not None:
+            _tensor("slots", slots, i32, 1, self.device)
+        if seq_start is not None:
+            _tensor("seq_start", seq_start, i32, 1, self.device)
+            n_seq = seq_start.shape[0] - 1
+        else:
+            n_seq = slots.shape[0] if slots is not None else T
+        if slots is not None:
+            _shape("slots", slots, (n_seq,))
+        if n_seq > self.n_seq_max or T > self.T_max:
+            raise ValueError(f"{n_seq} sequences of {T} tokens, the holder is for {self.n_seq_max} and {self.T_max}")
+        if T:
+            strides = [_row_stride(t) for t in (q, k, v)]
+        else:
+            strides = [dc.n_qk_heads * D, dc.n_qk_heads * D, dc.n_heads * D]
+        k3moe_delta_rule(dc, n_seq, T, seq_start, q, strides[0], k, strides[1], v, strides[2], g, beta, state_in,
+                         state_out, n_slots, slots, out, self.ws, self.ws_bytes, stream)
+        return out

@@ -335,6 +335,103 @@ k3moe_status k3moe_full_forward(const k3moe_config *cfg, const k3moe_full_dims *
     return e == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
 }
 
+static k3moe_status check_linear(const k3moe_linear_config *lc)
+{
+    if (!lc) return K3MOE_EINVAL;
+    if (lc->n <= 0 || lc->k <= 0 || (lc->y_f32 != 0 && lc->y_f32 != 1)) return K3MOE_EINVAL;
+    if (lc->act < K3MOE_ACT_NONE || lc->act > K3MOE_ACT_LOGSIGMOID) return K3MOE_EINVAL;
+    if (lc->n > (1 << 20) || lc->k > 65536 || lc->k % 8) return K3MOE_ESHAPE;
+    return K3MOE_OK;
+}
+
+k3moe_status k3moe_linear_workspace_bytes(const k3moe_linear_config *lc, int32_t T_max, size_t *bytes)
+{
+    k3moe_status st = check_linear(lc);
+    if (st != K3MOE_OK) return st;
+    if (!bytes) return K3MOE_EINVAL;
+    if (T_max < 0 || T_max > kMaxT) return K3MOE_ESHAPE;
+    *bytes = kCtrOffset + kCtrBytes;
+    return K3MOE_OK;
+}
+
+k3moe_status k3moe_linear(const k3moe_linear_config *lc, int32_t T, const uint16_t *x, int64_t x_stride,
+                          const uint16_t *w, const float *bias, const void *residual,
+                          int64_t residual_stride, void *y, int64_t y_stride, void *ws,
+                          size_t ws_bytes, k3moe_stream stream)
+{
+    k3moe_status st = check_linear(lc);
+    if (st != K3MOE_OK) return st;
+    if (T < 0 || T > kMaxT) return K3MOE_ESHAPE;
+    if (T == 0) return K3MOE_OK;
+    if (!x || !w || !y) return K3MOE_EINVAL;
+    if (x_stride < lc->k || x_stride % 8 || x_stride > kMaxStride || y_stride < lc->n ||
+        y_stride > kMaxStride ||
+        (residual && (residual_stride < lc->n || residual_stride > kMaxStride)))
+        return K3MOE_ESHAPE;
+    if (residual == y && residual_stride != y_stride) return K3MOE_EINVAL;
+    const size_t ysz = lc->y_f32 ? 4 : 2;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, ysz) || (residual && !aligned(residual, ysz)) ||
+        (bias && !aligned(bias, 4)))
+        return K3MOE_EALIGN;
+    if (!ws || !aligned(ws, 256) || ws_bytes < kCtrOffset + kCtrBytes) return K3MOE_EWORKSPACE;
+    const LinearArgs a{T, lc->n, lc->k, lc->act, lc->y_f32, x, x_stride, w, bias, residual,
+                       residual ? residual_stride : 0, y, y_stride, static_cast<int32_t *>(ws)};
+    return launch_linear(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
+}
+
+k3moe_status k3moe_delta_validate_config(const k3moe_delta_config *dc)
+{
+    if (!dc) return K3MOE_EINVAL;
+    if (dc->n_heads <= 0 || dc->n_qk_heads <= 0 || dc->head_dim <= 0 || dc->gate_dim <= 0 ||
+        (dc->qk_norm != 0 && dc->qk_norm != 1) || !std::isfinite(dc->scale) ||
+        (dc->qk_norm && !finite_pos(dc->norm_eps)) || dc->n_heads % dc->n_qk_heads)
+        return K3MOE_EINVAL;
+    if (dc->gate_dim != 1 && dc->gate_dim != dc->head_dim) return K3MOE_EINVAL;
+    if (dc->head_dim != kDeltaD || dc->n_heads > kMaxDeltaHeads) return K3MOE_ESHAPE;
+    return K3MOE_OK;
+}
+
+k3moe_status k3moe_delta_workspace_bytes(const k3moe_delta_config *dc, int32_t n_seq_max, int32_t T_max,
+                                         size_t *bytes)
+{
+    k3moe_status st = k3moe_delta_validate_config(dc);
+    if (st != K3MOE_OK) return st;
+    if (!bytes) return K3MOE_EINVAL;
+    if (T_max < 0 || T_max > kMaxT || n_seq_max < 0 || n_seq_max > kMaxSeqs) return K3MOE_ESHAPE;
+    *bytes = delta_workspace(*dc, n_seq_max, T_max);
+    return K3MOE_OK;
+}
+
+k3moe_status k3moe_delta_rule(const k3moe_delta_config *dc, int32_t n_seq, int32_t T,
+                              const int32_t *seq_start, const uint16_t *q, int64_t q_stride,
+                              const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                              const float *g, const float *beta, const float *state_in,
+                              float *state_out, int32_t n_slots, const int32_t *slots, uint16_t *out,
+                              void *ws, size_t ws_bytes, k3moe_stream stream)
+{
+    k3moe_status st = k3moe_delta_validate_config(dc);
+    if (st != K3MOE_OK) return st;
+    if (T < 0 || T > kMaxT || n_seq < 0 || n_seq > kMaxSeqs) return K3MOE_ESHAPE;
+    if (n_seq == 0) return T == 0 ? K3MOE_OK : K3MOE_ESHAPE;
+    if (!seq_start && n_seq != 1 && T != n_seq) return K3MOE_EINVAL;
+    if (!state_out) return K3MOE_EINVAL;
+    if (T > 0 && (!q || !k || !v || !g || !beta || !out)) return K3MOE_EINVAL;
+    const int64_t wq = (int64_t)dc->n_qk_heads * kDeltaD, wv = (int64_t)dc->n_heads * kDeltaD;
+    if (q_stride < wq || k_stride < wq || v_stride < wv || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
+        q_stride > kMaxStride || k_stride > kMaxStride || v_stride > kMaxStride)
+        return K3MOE_ESHAPE;
+    if (n_slots < 1 || (!slots && n_slots < n_seq)) return K3MOE_ESHAPE;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(g, 16) || !aligned(beta, 4) ||
+        !aligned(state_in, 16) || !aligned(state_out, 16) || !aligned(out, 16) || !aligned(seq_start, 4) ||
+        !aligned(slots, 4))
+        return K3MOE_EALIGN;
+    if (!ws || !aligned(ws, 256) || ws_bytes < delta_workspace(*dc, n_seq, T)) return K3MOE_EWORKSPACE;
+    const DeltaArgs a{n_seq, T, dc->n_heads, dc->n_qk_heads, dc->gate_dim, dc->qk_norm, dc->norm_eps,
+                      dc->scale, seq_start, q, k, v, q_stride, k_stride, v_stride, g, beta, state_in,
+                      state_out, n_slots, slots, out, static_cast<uint8_t *>(ws)};
+    return launch_delta(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
+}
+
 k3moe_status k3moe_device_status(void *ws, k3moe_stream stream, int32_t *code)
 {
     if (!ws || !aligned(ws, 256) || !code) return K3MOE_EINVAL;

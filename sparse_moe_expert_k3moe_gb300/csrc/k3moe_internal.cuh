@@ -335,6 +335,43 @@ void timing_begin(const char *name, cudaStream_t s);
 void timing_end(const char *name, cudaStream_t s);
 void count_launch();
 
+constexpr int64_t kMaxStride = 1ll << 32;                 // row strides of strided inputs, elements
+// ---- linear projection with its epilogue (k3moe_linear.cu)
+struct LinearArgs {
+    int32_t T, N, K, act, f32;
+    const uint16_t *x;
+    int64_t x_stride;
+    const uint16_t *w;
+    const float *bias;
+    const void *residual;
+    int64_t residual_stride;
+    void *y;
+    int64_t y_stride;
+    int32_t *status;
+};
+cudaError_t launch_linear(const LinearArgs &a, cudaStream_t s);
+
+// ---- gated delta rule (k3moe_delta.cu)
+constexpr int kDeltaD = 128;                              // key and value width of a head
+constexpr int kMaxDeltaHeads = 1024;
+constexpr int32_t kMaxSeqs = 1 << 16;
+struct DeltaArgs {
+    int32_t n_seq, T, H, Hq, gate;                        // gate: 1 or kDeltaD
+    int32_t qk_norm;
+    float eps, scale;
+    const int32_t *seq_start;                             // NULL: T / n_seq tokens each
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *g, *beta, *state_in;
+    float *state_out;
+    int32_t n_slots;
+    const int32_t *slots;
+    uint16_t *out;
+    uint8_t *ws;
+};
+size_t delta_workspace(const k3moe_delta_config &dc, int n_seq, int T);
+cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t s);
+
 // Host launchers implemented in the kernel files.
 cudaError_t launch_pack(const k3moe_config &c, int expert_lo, int n, const uint8_t *w1p,
                         const uint8_t *w1s, const uint8_t *w3p, const uint8_t *w3s,
