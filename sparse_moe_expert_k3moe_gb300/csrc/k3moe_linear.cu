@@ -1,8 +1,19 @@
 // k3moe_linear.cu -- y = act(x W^T + bias) + residual, x [T][K] and W [N][K] bf16 (the
 // projections of a decoder layer around its token mixer).
+//
+// Two kernels:
+//   linear_rows_kernel   a few tokens: the weight stream, one warp a row, plain FMAs;
+//   linear_tc_kernel     all else on tcgen05, weights as the M side (128 rows a block, 256
+//                        a pair of blocks), tokens as the N side.  With the weights on M
+//                        a thread of the epilogue owns one output column and a warp's
+//                        lanes 32 neighbouring ones, so bias is a register and every
+//                        load of the residual and store of y is contiguous over the
+//                        lanes, whatever y's row stride: no staging through shared memory.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "k3moe_internal.cuh"
+#include "k3moe_tc.cuh"
 
 namespace k3moe {
 namespace {
@@ -20,59 +31,488 @@ __device__ __forceinline__ float lin_act(float z, int act)
     return z;
 }
 
-// One output: its sum through the epilogue, rounded once.
-__device__ __forceinline__ void lin_store(const LinearArgs &a, int t, int n, float z)
+__device__ __forceinline__ float lin_residual(const LinearArgs &a, int t, int n)
 {
-    if (a.bias) z += __ldg(a.bias + n);
-    z = lin_act(z, a.act);
-    const size_t o = (size_t)t * a.y_stride + n, r = (size_t)t * a.residual_stride + n;
-    if (a.f32) {
-        if (a.residual) z += reinterpret_cast<const float *>(a.residual)[r];
-        reinterpret_cast<float *>(a.y)[o] = z;
-    } else {
-        if (a.residual) z += bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(a.residual)[r]);
-        reinterpret_cast<__nv_bfloat16 *>(a.y)[o] = __float2bfloat16_rn(z);
-    }
+    if (!a.residual) return 0.0f;
+    const size_t r = (size_t)t * a.residual_stride + n;
+    return a.f32 ? reinterpret_cast<const float *>(a.residual)[r]
+                 : bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(a.residual)[r]);
 }
 
-// 64 x 64 outputs a block, 4 x 4 a thread, K in steps of 32 through shared memory.
-__global__ void __launch_bounds__(256) linear_simple_kernel(const LinearArgs a, int n_nt)
+// One output: its sum through the epilogue, rounded once.  b is the column's bias, r the
+// residual (0 without one: adding it changes at most the sign of a zero).
+__device__ __forceinline__ void lin_store(const LinearArgs &a, int t, int n, float z, float b, float r)
+{
+    z = lin_act(z + b, a.act) + r;
+    const size_t o = (size_t)t * a.y_stride + n;
+    if (a.f32)
+        reinterpret_cast<float *>(a.y)[o] = z;
+    else
+        reinterpret_cast<__nv_bfloat16 *>(a.y)[o] = __float2bfloat16_rn(z);
+}
+
+// ---------------------------------------------------------------- a few tokens
+// One warp an output column at a time, its weight row read with 16-byte loads, eight in
+// flight a lane, against the tokens held in shared memory; sums in float, per lane in
+// chunk order and then over the warp by a fixed butterfly.
+constexpr int kLrThreads = 256, kLrWarps = kLrThreads / 32, kLrDeep = 8;
+constexpr size_t kLrSmem = 200 * 1024;
+
+template <int NT>
+__global__ void __launch_bounds__(kLrThreads) linear_rows_kernel(const LinearArgs a)
 {
     pdl_wait();
     pdl_trigger();
-    __shared__ float xs[32][65], wsm[32][65];
-    const int t0 = (blockIdx.x / n_nt) * 64, n0 = (blockIdx.x % n_nt) * 64;
-    const int tr = threadIdx.x / 16, tc = threadIdx.x % 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += 32) {
-        for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-            const int r = i / 32, c = i % 32;
-            const bool kk = k0 + c < a.K;
-            xs[c][r] = kk && t0 + r < a.T ? bf16_bits_to_f32(a.x[(size_t)(t0 + r) * a.x_stride + k0 + c]) : 0.0f;
-            wsm[c][r] = kk && n0 + r < a.N ? bf16_bits_to_f32(a.w[(size_t)(n0 + r) * a.K + k0 + c]) : 0.0f;
-        }
-        __syncthreads();
-        for (int c = 0; c < 32; c++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) acc[i][j] = fmaf(xs[c][tr * 4 + i], wsm[c][tc + 16 * j], acc[i][j]);
-        __syncthreads();
+    extern __shared__ __align__(16) uint4 xsm[];         // NT x K bf16
+    const int nchunk = a.K / 8;
+    for (int q = threadIdx.x; q < NT * nchunk; q += kLrThreads) {
+        const int t = q / nchunk, c = q % nchunk;
+        xsm[q] = t < a.T ? __ldg(reinterpret_cast<const uint4 *>(a.x + (size_t)t * a.x_stride) + c)
+                         : make_uint4(0, 0, 0, 0);
     }
-    for (int i = 0; i < 4; i++)
-        for (int j = 0; j < 4; j++) {
-            const int t = t0 + tr * 4 + i, n = n0 + tc + 16 * j;
-            if (t < a.T && n < a.N) lin_store(a, t, n, acc[i][j]);
+    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int n = blockIdx.x * kLrWarps + warp; n < a.N; n += gridDim.x * kLrWarps) {
+        const uint4 *wr = reinterpret_cast<const uint4 *>(a.w + (size_t)n * a.K);
+        float acc[NT];
+#pragma unroll
+        for (int t = 0; t < NT; t++) acc[t] = 0.0f;
+        for (int c0 = lane; c0 < nchunk; c0 += 32 * kLrDeep) {
+            uint4 wv[kLrDeep];
+#pragma unroll
+            for (int j = 0; j < kLrDeep; j++)
+                wv[j] = c0 + 32 * j < nchunk ? __ldcs(wr + c0 + 32 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < kLrDeep; j++) {
+                const int c = c0 + 32 * j;
+                if (c >= nchunk) break;
+                const uint32_t wu[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w};
+#pragma unroll
+                for (int t = 0; t < NT; t++) {
+                    const uint4 xv = xsm[t * nchunk + c];
+                    const uint32_t xu[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        acc[t] = fmaf(__uint_as_float(xu[r] << 16), __uint_as_float(wu[r] << 16), acc[t]);
+                        acc[t] = fmaf(__uint_as_float(xu[r] & 0xFFFF0000u), __uint_as_float(wu[r] & 0xFFFF0000u),
+                                      acc[t]);
+                    }
+                }
+            }
         }
+        const float b = a.bias ? __ldg(a.bias + n) : 0.0f;
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+            if (lane == t && t < a.T) lin_store(a, t, n, acc[t], b, lin_residual(a, t, n));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- tensor cores
+constexpr int kLtBK = 64;                                    // K columns a stage: one 128-byte swizzled row
+constexpr int kLtABytes = 128 * kLtBK * 2;                   // a block's weight tile
+constexpr int kLtRing = 192 * 1024;                          // the stage ring
+constexpr int kLtMaxStg = 10;
+constexpr int kLtWarpProd = 0, kLtWarpMma = 1, kLtWarpEpi0 = 2, kLtNumEpi = 4;
+constexpr int kLtThreads = (kLtWarpEpi0 + kLtNumEpi) * 32;   // 192
+
+struct LinTile {
+    int bn;          // tokens a tile (of both blocks of a pair)
+    int n_rb, n_tt;  // weight row blocks (128 x CG rows) and token tiles
+    int P;           // K parts: blocks of a cluster that share one tile
+    int nks;         // K stages in all
+    int nstg, stage_bytes;
+    int group;       // weight row blocks visited together, for the L2
+};
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The cluster address of a shared-memory address in block `rank`.
+__device__ __forceinline__ uint32_t mapa(uint32_t a, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+// Tile copy whose bytes are counted on a barrier of either block of the pair.
+__device__ __forceinline__ void tma2d_pair(void *dst, const CUtensorMap *m, int c0, int c1, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3}], [%4];" ::"r"(saddr(dst)),
+        "l"(m), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc));
+}
+// Arrives on the barrier at this address in both blocks once the issued MMAs are done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            saddr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void mb_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// CG = 2: a pair of blocks computes 256 weight rows x bn tokens, each block holding 128
+// rows of the accumulator, its own weight rows and half of the token rows.  CG = 1 with
+// P > 1: the blocks of a cluster take a part of K each and add their sums through
+// distributed shared memory, in part order.  Persistent over tiles unless P > 1.
+template <int CG>
+__global__ void __launch_bounds__(kLtThreads, 1) linear_tc_kernel(const LinearArgs a, const LinTile tl,
+                                                                  const __grid_constant__ CUtensorMap mw,
+                                                                  const __grid_constant__ CUtensorMap mx)
+{
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ __align__(1024) uint8_t lsm_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lsm_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t full[kLtMaxStg], empty[kLtMaxStg], acc_full[2], acc_empty[2], drain;
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int bail;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int P = CG == 1 ? tl.P : 1, nstg = tl.nstg;
+    const uint32_t rank = (CG == 2 || P > 1) ? cluster_rank() : 0;
+    const bool leader = CG == 1 || rank == 0;
+    const int cid = CG == 2 ? blockIdx.x / 2 : blockIdx.x / P;       // this cluster, and how many there are
+    const int ncl = CG == 2 ? gridDim.x / 2 : gridDim.x / P;
+    const int n_items = tl.n_rb * tl.n_tt;
+    const int part = P > 1 ? (int)rank : 0;
+    const int ks0 = (int)((long long)tl.nks * part / P), ks1 = (int)((long long)tl.nks * (part + 1) / P);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < nstg; s++) { mb_init(&full[s], 1); mb_init(&empty[s], 1); }
+        for (int b = 0; b < 2; b++) { mb_init(&acc_full[b], 1); mb_init(&acc_empty[b], kLtNumEpi * CG); }
+        mb_init(&drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        bail = 0;
+    }
+    if (warp == kLtWarpMma) {
+        if (CG == 2) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&tmem_base)),
+                         "r"(512));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&tmem_base)),
+                         "r"(512));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2 || P > 1) cluster_sync_all();                        // the peers' barriers are set up
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    auto timeout = [&]() {
+        set_status(a.status, K3MOE_DEV_TIMEOUT);
+        bail = 1;
+    };
+    // tile i: `group` row blocks side by side, token tile by token tile, so that the blocks
+    // at work share both few weight rows and few token rows in the L2
+    auto tile_of = [&](int i, int *rb, int *tt) {
+        const int g = i / (tl.group * tl.n_tt), r = i % (tl.group * tl.n_tt);
+        const int w = min(tl.group, tl.n_rb - g * tl.group);
+        *rb = g * tl.group + r % w;
+        *tt = r / w;
+    };
+
+    if (warp == kLtWarpProd) {
+        if (lane == 0) {
+            const int bn_own = tl.bn / CG;                           // token rows this block loads
+            uint32_t st = 0;
+            for (int i = cid; i < n_items && !bail; i += ncl) {
+                int rb, tt;
+                tile_of(i, &rb, &tt);
+                const int n0 = rb * 128 * CG + (int)rank * 128 * (CG - 1);
+                const int t0 = tt * tl.bn + (int)rank * bn_own * (CG - 1);
+                for (int ks = ks0; ks < ks1; ks++, st++) {
+                    const int s = st % nstg;
+                    if (st >= (uint32_t)nstg && !mb_wait(&empty[s], ((st / nstg) - 1) & 1u)) {
+                        timeout();
+                        break;
+                    }
+                    uint8_t *stage = sm + (size_t)s * tl.stage_bytes;
+                    if (leader) mb_expect_tx(&full[s], (uint32_t)(tl.stage_bytes * CG));
+                    if (CG == 2) {
+                        const uint32_t fb = mapa(saddr(&full[s]), 0);
+                        tma2d_pair(stage, &mw, ks * kLtBK, n0, fb);
+                        tma2d_pair(stage + kLtABytes, &mx, ks * kLtBK, t0, fb);
+                    } else {
+                        tma2d(stage, &mw, ks * kLtBK, n0, &full[s]);
+                        tma2d(stage + kLtABytes, &mx, ks * kLtBK, t0, &full[s]);
+                    }
+                }
+            }
+            if (bail && leader)                                      // wait (bounded) for the copies already issued
+                for (uint32_t f = st > (uint32_t)nstg ? st - nstg : 0; f < st; f++)
+                    mb_wait(&full[f % nstg], (f / nstg) & 1u);
+        }
+    } else if (warp == kLtWarpMma) {
+        if (lane == 0 && leader) {
+            uint32_t st = 0, n = 0;
+            const uint32_t id = (idesc(1, tl.bn) & ~(31u << 24)) | ((uint32_t)(128 * CG >> 4) << 24);
+            for (int i = cid; i < n_items && !bail; i += ncl, n++) {
+                const int buf = n & 1;
+                if (n >= 2 && !mb_wait(&acc_empty[buf], ((n >> 1) - 1) & 1u)) { timeout(); break; }
+                tc_fence_after();
+                const uint32_t d0 = tmem + (uint32_t)buf * 256u;
+                for (int ks = ks0; ks < ks1; ks++, st++) {
+                    const int s = st % nstg;
+                    if (!mb_wait(&full[s], (st / nstg) & 1u)) { timeout(); break; }
+                    tc_fence_after();
+                    const uint32_t A = saddr(sm + (size_t)s * tl.stage_bytes), B = A + kLtABytes;
+#pragma unroll
+                    for (int kk = 0; kk < kLtBK / 16; kk++) {
+                        const uint32_t acc = (ks != ks0 || kk) ? 1u : 0u;
+                        if (CG == 2)
+                            umma_pair(d0, sdesc(A + kk * 32), sdesc(B + kk * 32), id, acc);
+                        else
+                            umma(d0, sdesc(A + kk * 32), sdesc(B + kk * 32), id, acc);
+                    }
+                    if (CG == 2)
+                        umma_commit_pair(&empty[s]);
+                    else
+                        umma_commit(&empty[s]);
+                }
+                if (bail) break;
+                if (CG == 2)
+                    umma_commit_pair(&acc_full[buf]);
+                else
+                    umma_commit(&acc_full[buf]);
+            }
+            if (CG == 2)
+                umma_commit_pair(&drain);                            // every issued MMA done before the dealloc
+            else
+                umma_commit(&drain);
+            mb_wait(&drain, 0);
+        }
+    } else {
+        // ---------------- epilogue: output column 32 q + lane of the row block per thread
+        const int q = warp & 3;                                      // tensor-memory lane quadrant of this warp
+        uint32_t n = 0;
+        for (int i = cid; i < n_items && !bail; i += ncl, n++) {
+            int rb, tt;
+            tile_of(i, &rb, &tt);
+            const int t0 = tt * tl.bn, ncols = min(tl.bn, a.T - t0);
+            const int col = rb * 128 * CG + (int)rank * 128 * (CG - 1) + 32 * q + lane;
+            const bool in = col < a.N;
+            const float b = a.bias && in ? __ldg(a.bias + col) : 0.0f;
+            const int buf = n & 1;
+            if (!mb_wait_warp(&acc_full[buf], (n >> 1) & 1u)) { timeout(); break; }
+            tc_fence_after();
+            const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)buf * 256u;
+            for (int c0 = 0; c0 < ncols; c0 += 16) {
+                float v[16], r[16];
+                if (P == 1)                          // every old value is loaded before any is stored (y may be the residual)
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        r[j] = in && c0 + j < ncols ? lin_residual(a, t0 + c0 + j, col) : 0.0f;
+                tmem_ld16(lane_addr + c0, v);
+                if (P > 1) {
+                    // this part's sums, [token][weight row], over the ring (its copies are consumed)
+                    float *dst = reinterpret_cast<float *>(sm) + (size_t)c0 * 128 + 32 * q + lane;
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        if (c0 + j < ncols) dst[(size_t)j * 128] = v[j];
+                } else if (in) {
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        if (c0 + j < ncols) lin_store(a, t0 + c0 + j, col, v[j], b, r[j]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2)
+                    mb_arrive_cluster(mapa(saddr(&acc_empty[buf]), 0));
+                else
+                    mb_arrive(&acc_empty[buf]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2 || P > 1) cluster_sync_all();       // peers' sums are written, and no block leaves with one still to come
+    tc_fence_after();
+    if (CG == 1 && P > 1) {
+        int rb, tt;
+        tile_of(cid, &rb, &tt);
+        const int t0 = tt * tl.bn, ncols = min(tl.bn, a.T - t0);
+        const int row = threadIdx.x & 127, col = rb * 128 + row;
+        if (!bail && threadIdx.x < 128 && col < a.N) {
+            const float b = a.bias ? __ldg(a.bias + col) : 0.0f;
+            for (int c = (int)rank; c < ncols; c += P) {             // a token in each P is this block's to finish
+                const uint32_t at = saddr(sm) + (uint32_t)(c * 128 + row) * 4u;
+                const float r = lin_residual(a, t0 + c, col);
+                float z = 0.0f;
+                for (int p = 0; p < P; p++) z += ld_cluster(mapa(at, (uint32_t)p));
+                lin_store(a, t0 + c, col, z, b, r);
+            }
+        }
+        cluster_sync_all();                                          // nobody leaves while its sums are read
+    }
+    if (warp == kLtWarpMma) {
+        __syncwarp();
+        if (CG == 2)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+// 16-bit matrix of `rows` rows of `cols` elements, `stride` elements apart: boxes of 64
+// columns x box_rows rows, 128-byte swizzle; what a box has outside reads as zero.
+bool lin_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_rows)
+{
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {stride * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kLtBK, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT>
+cudaError_t launch_rows(const LinearArgs &a, cudaStream_t s)
+{
+    const size_t smem = (size_t)NT * a.K * 2;
+    static size_t smem_set = 48 * 1024;
+    if (smem > smem_set) {
+        cudaFuncSetAttribute(linear_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLrSmem);
+        smem_set = kLrSmem;
+    }
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, linear_rows_kernel<NT>, kLrThreads, smem) !=
+            cudaSuccess ||
+        per_sm < 1)
+        per_sm = 1;
+    const int grid = std::max(1, std::min(num_sms() * per_sm, (a.N + kLrWarps - 1) / kLrWarps));
+    return launch_pdl(linear_rows_kernel<NT>, dim3(grid), dim3(kLrThreads), smem, s, a);
+}
+
+// The tile of a call: a pair of blocks (256 x 256) when the pairs have tiles for most of
+// the GPU; else the token tile and the K parts whose estimated time is least.  The
+// estimate, in SM clocks: a K stage of a tile takes 2 bn on the tensor cores and
+// (128 + bn) 128 bytes at about 48 a clock from the L2; a tile's start and epilogue about
+// 2500 + 16 bn; a cluster's joining 1500 more.
+int lin_plan(const LinearArgs &a, LinTile *tl)
+{
+    const int sms = num_sms();
+    tl->nks = (a.K + kLtBK - 1) / kLtBK;
+    tl->P = 1;
+    const long long pairs = (long long)((a.N + 255) / 256) * ((a.T + 255) / 256);
+    if (pairs * 4 >= 3LL * (sms / 2)) {
+        tl->bn = 256;
+        tl->n_rb = (a.N + 255) / 256;
+        tl->n_tt = (a.T + 255) / 256;
+        tl->stage_bytes = kLtABytes + 128 * kLtBK * 2;
+        tl->nstg = kLtRing / tl->stage_bytes;
+        tl->group = 8;
+        return 2;
+    }
+    tl->n_rb = (a.N + 127) / 128;
+    double best = 1e30;
+    for (int bn = 256; bn >= 16; bn >>= 1) {
+        if (bn >= 2 * a.T && bn > 16) continue;
+        const int n_tt = (a.T + bn - 1) / bn;
+        for (int P = 1; P <= 8; P *= 2) {
+            if (P > 1 && tl->nks / P < 4) break;
+            const long long items = (long long)tl->n_rb * n_tt * P;
+            const long long waves = (items + sms - 1) / sms;
+            const double stage = std::max(2.0 * bn, (128.0 + bn) * 128.0 / 48.0);
+            const double t = waves * ((double)((tl->nks + P - 1) / P) * stage + 2500.0 + 16.0 * bn / P +
+                                      (P > 1 ? 1500.0 + 8.0 * bn : 0.0));
+            if (t < best) {
+                best = t;
+                tl->bn = bn;
+                tl->n_tt = n_tt;
+                tl->P = P;
+            }
+        }
+    }
+    tl->stage_bytes = kLtABytes + tl->bn * kLtBK * 2;
+    tl->nstg = std::min(kLtMaxStg, kLtRing / tl->stage_bytes);
+    tl->group = 8;
+    return 1;
+}
+
+template <int CG>
+cudaError_t launch_tc(const LinearArgs &a, const LinTile &tl, cudaStream_t s)
+{
+    CUtensorMap mw{}, mx{};
+    if (!lin_map(&mw, a.w, (uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.K, 128) ||
+        !lin_map(&mx, a.x, (uint64_t)a.T, (uint64_t)a.K, (uint64_t)a.x_stride, (uint32_t)(tl.bn / CG)))
+        return cudaErrorInvalidValue;
+    constexpr size_t smem = 1024 + kLtRing;
+    static bool smem_set = false;
+    if (!smem_set) {
+        cudaFuncSetAttribute(linear_tc_kernel<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        smem_set = true;
+    }
+    const int csize = CG == 2 ? 2 : tl.P;
+    const int items = tl.n_rb * tl.n_tt;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(CG == 1 && tl.P > 1 ? items * tl.P : std::min(items, num_sms() / csize) * csize));
+    cfg.blockDim = dim3(kLtThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)csize;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = csize > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG>, a, tl, mw, mx);
 }
 
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs &a, cudaStream_t s)
 {
-    const int n_nt = (a.N + 63) / 64, n_tt = (a.T + 63) / 64;
     timing_begin("linear", s);
-    const cudaError_t err = launch_pdl(linear_simple_kernel, dim3((unsigned)n_nt * n_tt), dim3(256), 0, s, a, n_nt);
+    cudaError_t err;
+    if (a.T == 1 && (size_t)a.K * 2 <= kLrSmem) {
+        err = launch_rows<1>(a, s);
+    } else if (a.T <= 2 && (size_t)a.K * 4 <= kLrSmem) {
+        err = launch_rows<2>(a, s);
+    } else if (a.T <= 4 && (size_t)a.K * 8 <= kLrSmem) {
+        err = launch_rows<4>(a, s);
+    } else {
+        LinTile tl{};
+        err = lin_plan(a, &tl) == 2 ? launch_tc<2>(a, tl, s) : launch_tc<1>(a, tl, s);
+    }
     count_launch();
     timing_end("linear", s);
     return err;
