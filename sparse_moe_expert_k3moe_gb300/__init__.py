@@ -498,22 +498,24 @@ class MoEBlock:
 
 # ----------------------------------------------------------------------------- the token mixer's holders
 
-def _tensor(what, t, dtypes, dims, device):
-    """Raises ValueError unless t is a `dims`-dimensional tensor of one of dtypes on device
-    whose innermost dimension is dense: what the entry points take on trust from a pointer."""
-    if t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{what}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if t.dim() != dims:
-        raise ValueError(f"{what}: {t.dim()} dimensions, expected {dims}")
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{what}: the last dimension has stride {t.stride(-1)}, expected 1")
-
-
-def _shape(what, t, shape):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _tensor(what, t, dtypes, shape, device, dense=True):
+    """Raises ValueError unless t is a tensor of this shape, of one of dtypes, on device: what
+    the entry points take on trust from a pointer.  dense: contiguous; else only its rows
+    are, with any stride between them."""
+    if t.dtype in dtypes and t.device == device and t.shape == shape:
+        if t.is_contiguous():
+            return
+        if not dense:
+            row = 1
+            for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+                if n > 1 and s != row:
+                    break
+                row *= n
+            else:
+                return
+        raise ValueError(f"{what}: strides {tuple(t.stride())} of shape {tuple(shape)} are not dense")
+    raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected "
+                     f"{' or '.join(str(d) for d in dtypes)} {tuple(shape)} on {device}")
 
 
 def _row_stride(t):
@@ -547,23 +549,18 @@ class Linear:
         residual [T][n] of y's type, which may be y."""
         import torch
         lc, T = self.lc, x.shape[0]
-        bf16, ytype = (torch.bfloat16, torch.int16), (torch.float32,) if lc.y_f32 else (torch.bfloat16, torch.int16)
+        bf16 = (torch.bfloat16, torch.int16)
+        ytype = (torch.float32,) if lc.y_f32 else bf16
+        dev, n = self.device, lc.n
         if T > self.T_max:
             raise ValueError(f"x: {T} rows, the holder is for {self.T_max}")
-        _tensor("x", x, bf16, 2, self.device)
-        _shape("x", x, (T, lc.k))
-        _tensor("w", self.w, bf16, 2, self.device)
-        _shape("w", self.w, (lc.n, lc.k))
-        if not self.w.is_contiguous():
-            raise ValueError("w: not contiguous")
-        _tensor("y", y, ytype, 2, self.device)
-        _shape("y", y, (T, lc.n))
+        _tensor("x", x, bf16, (T, lc.k), dev, dense=False)
+        _tensor("w", self.w, bf16, (n, lc.k), dev)
+        _tensor("y", y, ytype, (T, n), dev, dense=False)
         if self.bias is not None:
-            _tensor("bias", self.bias, (torch.float32,), 1, self.device)
-            _shape("bias", self.bias, (lc.n,))
+            _tensor("bias", self.bias, (torch.float32,), (n,), dev)
         if residual is not None:
-            _tensor("residual", residual, ytype, 2, self.device)
-            _shape("residual", residual, (T, lc.n))
+            _tensor("residual", residual, ytype, (T, n), dev, dense=False)
         if T:
             k3moe_linear(lc, T, x, _row_stride(x), self.w, self.bias, residual,
                          _row_stride(residual) if residual is not None else 0, y, _row_stride(y), self.ws,
@@ -598,33 +595,25 @@ class DeltaRule:
         import torch
         dc, T, D = self.dc, q.shape[0], self.dc.head_dim
         bf16, f32, i32 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,)
-        for name, t, shape, types in (("q", q, (T, dc.n_qk_heads, D), bf16), ("k", k, (T, dc.n_qk_heads, D), bf16),
-                                      ("v", v, (T, dc.n_heads, D), bf16), ("g", g, (T, dc.n_heads, dc.gate_dim), f32),
-                                      ("beta", beta, (T, dc.n_heads), f32), ("out", out, (T, dc.n_heads, D), bf16)):
-            _tensor(name, t, types, len(shape), self.device)
-            _shape(name, t, shape)
-            if t.dim() == 3 and T and t.shape[1] > 1 and t.stride(1) != t.shape[2]:
-                raise ValueError(f"{name}: heads with stride {t.stride(1)}, expected {t.shape[2]}")
-        for name, t in (("g", g), ("beta", beta), ("out", out)):
-            if not t.is_contiguous():
-                raise ValueError(f"{name}: not contiguous")
-        for name, t in (("state_in", state_in), ("state_out", state_out)):
-            if t is None and name == "state_in":
-                continue
-            _tensor(name, t, f32, 4, self.device)
-            _shape(name, t, (state_out.shape[0], dc.n_heads, D, D))
-            if not t.is_contiguous():
-                raise ValueError(f"{name}: not contiguous")
+        dev, H, qk = self.device, dc.n_heads, (T, dc.n_qk_heads, D)
+        _tensor("q", q, bf16, qk, dev, dense=False)
+        _tensor("k", k, bf16, qk, dev, dense=False)
+        _tensor("v", v, bf16, (T, H, D), dev, dense=False)
+        _tensor("g", g, f32, (T, H, dc.gate_dim), dev)
+        _tensor("beta", beta, f32, (T, H), dev)
+        _tensor("out", out, bf16, (T, H, D), dev)
         n_slots = state_out.shape[0]
-        if slots is not None:
-            _tensor("slots", slots, i32, 1, self.device)
+        pool = (n_slots, H, D, D)
+        _tensor("state_out", state_out, f32, pool, dev)
+        if state_in is not None and state_in is not state_out:
+            _tensor("state_in", state_in, f32, pool, dev)
         if seq_start is not None:
-            _tensor("seq_start", seq_start, i32, 1, self.device)
             n_seq = seq_start.shape[0] - 1
+            _tensor("seq_start", seq_start, i32, (n_seq + 1,), dev)
         else:
             n_seq = slots.shape[0] if slots is not None else T
         if slots is not None:
-            _shape("slots", slots, (n_seq,))
+            _tensor("slots", slots, i32, (n_seq,), dev)
         if n_seq > self.n_seq_max or T > self.T_max:
             raise ValueError(f"{n_seq} sequences of {T} tokens, the holder is for {self.n_seq_max} and {self.T_max}")
         if T:

@@ -18,17 +18,58 @@
 namespace k3moe {
 namespace {
 
-// The activations in float, from their definitions; expf, erff and log1pf are CUDA's.
-__device__ __forceinline__ float lin_act(float z, int act)
+// The activations in float, branch-free (256 of them a thread in a tile's epilogue), each
+// within a few 2^-22 of max(|z|, 1) or better:
+//   sigmoid  1 / (1 + e), e = exp(-z); past z = -88 e is infinite and the result 0;
+//   gelu     the complementary error function by Abramowitz and Stegun 7.1.26,
+//            erfc(s) = (a1 t + .. + a5 t^5) exp(-s^2), t = 1 / (1 + p s), s >= 0 (absolute
+//            error at most 1.5e-7), so that the far negative side is a product, not a difference;
+//   logsigmoid  min(z, 0) - log(1 + e), e = exp(-|z|), with log(1 + e) = 2 atanh(s),
+//            s = e / (2 + e) <= 1/3, by atanh's series to s^15: relative error 2e-9 and the rounding.
+template <int ACT>
+__device__ __forceinline__ float lin_act(float z)
 {
-    switch (act) {
-    case K3MOE_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case K3MOE_ACT_SILU: return z / (1.0f + expf(-z));
-    case K3MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    case K3MOE_ACT_SIGMOID: return 1.0f / (1.0f + expf(-z));
-    case K3MOE_ACT_LOGSIGMOID: return fminf(z, 0.0f) - log1pf(expf(-fabsf(z)));
+    if (ACT == K3MOE_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+    if (ACT == K3MOE_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
+    if (ACT == K3MOE_ACT_SIGMOID) return __fdividef(1.0f, 1.0f + __expf(-z));
+    if (ACT == K3MOE_ACT_GELU) {
+        const float s = fabsf(z) * 0.70710678118654752f;
+        const float t = __fdividef(1.0f, fmaf(0.3275911f, s, 1.0f));
+        float p = fmaf(1.061405429f, t, -1.453152027f);
+        p = fmaf(p, t, 1.421413741f);
+        p = fmaf(p, t, -0.284496736f);
+        p = fmaf(p, t, 0.254829592f);
+        const float half_erfc = 0.5f * p * t * __expf(-s * s);
+        return z * (z > 0.0f ? 1.0f - half_erfc : half_erfc);
+    }
+    if (ACT == K3MOE_ACT_LOGSIGMOID) {
+        const float e = __expf(-fabsf(z));
+        const float s = __fdividef(e, 2.0f + e), w = s * s;
+        float p = fmaf(w, 1.0f / 15.0f, 1.0f / 13.0f);
+        p = fmaf(p, w, 1.0f / 11.0f);
+        p = fmaf(p, w, 1.0f / 9.0f);
+        p = fmaf(p, w, 1.0f / 7.0f);
+        p = fmaf(p, w, 1.0f / 5.0f);
+        p = fmaf(p, w, 1.0f / 3.0f);
+        p = fmaf(p, w, 1.0f);
+        return (z < 0.0f ? z : (z != z ? z : 0.0f)) - 2.0f * s * p;
     }
     return z;
+}
+
+// f(integral constant act) for a runtime act.
+template <int N> struct ActC { static constexpr int value = N; };
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f)
+{
+    switch (act) {
+    case K3MOE_ACT_RELU: f(ActC<K3MOE_ACT_RELU>{}); break;
+    case K3MOE_ACT_SILU: f(ActC<K3MOE_ACT_SILU>{}); break;
+    case K3MOE_ACT_GELU: f(ActC<K3MOE_ACT_GELU>{}); break;
+    case K3MOE_ACT_SIGMOID: f(ActC<K3MOE_ACT_SIGMOID>{}); break;
+    case K3MOE_ACT_LOGSIGMOID: f(ActC<K3MOE_ACT_LOGSIGMOID>{}); break;
+    default: f(ActC<K3MOE_ACT_NONE>{}); break;
+    }
 }
 
 __device__ __forceinline__ float lin_residual(const LinearArgs &a, int t, int n)
@@ -39,11 +80,9 @@ __device__ __forceinline__ float lin_residual(const LinearArgs &a, int t, int n)
                  : bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(a.residual)[r]);
 }
 
-// One output: its sum through the epilogue, rounded once.  b is the column's bias, r the
-// residual (0 without one: adding it changes at most the sign of a zero).
-__device__ __forceinline__ void lin_store(const LinearArgs &a, int t, int n, float z, float b, float r)
+// One output, rounded once.
+__device__ __forceinline__ void lin_put(const LinearArgs &a, int t, int n, float z)
 {
-    z = lin_act(z + b, a.act) + r;
     const size_t o = (size_t)t * a.y_stride + n;
     if (a.f32)
         reinterpret_cast<float *>(a.y)[o] = z;
@@ -105,8 +144,14 @@ __global__ void __launch_bounds__(kLrThreads) linear_rows_kernel(const LinearArg
         for (int t = 0; t < NT; t++) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-            if (lane == t && t < a.T) lin_store(a, t, n, acc[t], b, lin_residual(a, t, n));
         }
+        float z = acc[0];
+#pragma unroll
+        for (int t = 1; t < NT; t++) z = lane == t ? acc[t] : z;
+        if (lane < NT && lane < a.T)
+            with_act(a.act, [&](auto act) {
+                lin_put(a, lane, n, lin_act<decltype(act)::value>(z + b) + lin_residual(a, lane, n));
+            });
     }
 }
 
@@ -115,8 +160,8 @@ constexpr int kLtBK = 64;                                    // K columns a stag
 constexpr int kLtABytes = 128 * kLtBK * 2;                   // a block's weight tile
 constexpr int kLtRing = 192 * 1024;                          // the stage ring
 constexpr int kLtMaxStg = 10;
-constexpr int kLtWarpProd = 0, kLtWarpMma = 1, kLtWarpEpi0 = 2, kLtNumEpi = 4;
-constexpr int kLtThreads = (kLtWarpEpi0 + kLtNumEpi) * 32;   // 192
+constexpr int kLtWarpProd = 0, kLtWarpMma = 1, kLtWarpEpi0 = 2, kLtNumEpi = 8;
+constexpr int kLtThreads = (kLtWarpEpi0 + kLtNumEpi) * 32;   // 320
 
 struct LinTile {
     int bn;          // tokens a tile (of both blocks of a pair)
@@ -178,6 +223,65 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t *bar)
 __device__ __forceinline__ void mb_arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Sixteen tokens' accumulators of a warp's 32 output columns (lane = column) through the
+// epilogue.  In bf16, with rows that start on a word, neighbouring lanes trade a token
+// each, so that a store takes two columns of one token from a lane (half the stores, 64
+// contiguous bytes of two tokens each); the residual is read the same way.
+__device__ __forceinline__ void lin_chunk(const LinearArgs &a, uint32_t taddr, int t0, int left, int col, bool pairs,
+                                          float b)
+{
+    const bool odd = threadIdx.x & 1;
+    uint32_t v[16];
+    if (pairs) {
+        const int c2 = col & ~1, mine = odd ? 1 : 0;             // columns c2, c2 + 1 of tokens j + mine
+        const bool in0 = c2 < a.N, in1 = c2 + 1 < a.N;
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            r[j] = 0;
+            if (a.residual && in0 && 2 * j + mine < left) {
+                const uint16_t *p = reinterpret_cast<const uint16_t *>(a.residual) +
+                                    (size_t)(t0 + 2 * j + mine) * a.residual_stride + c2;
+                r[j] = in1 ? *reinterpret_cast<const uint32_t *>(p) : (uint32_t)*p;
+            }
+        }
+        tmem_ld16_nowait(taddr, v);
+        tmem_wait_ld();
+        with_act(a.act, [&](auto act) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float z0 = lin_act<decltype(act)::value>(__uint_as_float(v[2 * j]) + b);
+                const float z1 = lin_act<decltype(act)::value>(__uint_as_float(v[2 * j + 1]) + b);
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? z0 : z1, 1);
+                const float lo = (odd ? got : z0) + __uint_as_float(r[j] << 16);
+                const float hi = (odd ? z1 : got) + __uint_as_float(r[j] & 0xFFFF0000u);
+                const __nv_bfloat162 w = __floats2bfloat162_rn(lo, hi);
+                if (in0 && 2 * j + mine < left) {
+                    uint16_t *p = reinterpret_cast<uint16_t *>(a.y) + (size_t)(t0 + 2 * j + mine) * a.y_stride + c2;
+                    const uint32_t u = *reinterpret_cast<const uint32_t *>(&w);
+                    if (in1)
+                        *reinterpret_cast<uint32_t *>(p) = u;
+                    else
+                        *p = (uint16_t)u;
+                }
+            }
+        });
+        return;
+    }
+    float r[16];
+#pragma unroll
+    for (int j = 0; j < 16; j++) r[j] = col < a.N && j < left ? lin_residual(a, t0 + j, col) : 0.0f;
+    tmem_ld16_nowait(taddr, v);
+    tmem_wait_ld();
+    with_act(a.act, [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+            const float z = lin_act<decltype(act)::value>(__uint_as_float(v[j]) + b) + r[j];
+            if (col < a.N && j < left) lin_put(a, t0 + j, col, z);
+        }
+    });
 }
 
 // CG = 2: a pair of blocks computes 256 weight rows x bn tokens, each block holding 128
@@ -315,35 +419,32 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tc_kernel(const LinearAr
     } else {
         // ---------------- epilogue: output column 32 q + lane of the row block per thread
         const int q = warp & 3;                                      // tensor-memory lane quadrant of this warp
+        const int half = (warp - kLtWarpEpi0) >> 2;                  // which of every two 16-token chunks it takes
+        const bool pairs = !a.f32 && a.y_stride % 2 == 0 && reinterpret_cast<uintptr_t>(a.y) % 4 == 0 &&
+                           (!a.residual || (a.residual_stride % 2 == 0 &&
+                                            reinterpret_cast<uintptr_t>(a.residual) % 4 == 0));
         uint32_t n = 0;
         for (int i = cid; i < n_items && !bail; i += ncl, n++) {
             int rb, tt;
             tile_of(i, &rb, &tt);
             const int t0 = tt * tl.bn, ncols = min(tl.bn, a.T - t0);
             const int col = rb * 128 * CG + (int)rank * 128 * (CG - 1) + 32 * q + lane;
-            const bool in = col < a.N;
-            const float b = a.bias && in ? __ldg(a.bias + col) : 0.0f;
+            const float b = a.bias && col < a.N ? __ldg(a.bias + col) : 0.0f;
             const int buf = n & 1;
             if (!mb_wait_warp(&acc_full[buf], (n >> 1) & 1u)) { timeout(); break; }
             tc_fence_after();
             const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)buf * 256u;
-            for (int c0 = 0; c0 < ncols; c0 += 16) {
-                float v[16], r[16];
-                if (P == 1)                          // every old value is loaded before any is stored (y may be the residual)
-#pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        r[j] = in && c0 + j < ncols ? lin_residual(a, t0 + c0 + j, col) : 0.0f;
-                tmem_ld16(lane_addr + c0, v);
+            for (int c0 = 16 * half; c0 < ncols; c0 += 32) {
+                float v[16];
                 if (P > 1) {
                     // this part's sums, [token][weight row], over the ring (its copies are consumed)
+                    tmem_ld16(lane_addr + c0, v);
                     float *dst = reinterpret_cast<float *>(sm) + (size_t)c0 * 128 + 32 * q + lane;
 #pragma unroll
                     for (int j = 0; j < 16; j++)
                         if (c0 + j < ncols) dst[(size_t)j * 128] = v[j];
-                } else if (in) {
-#pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        if (c0 + j < ncols) lin_store(a, t0 + c0 + j, col, v[j], b, r[j]);
+                } else {
+                    lin_chunk(a, lane_addr + c0, t0 + c0, ncols - c0, col, pairs, b);
                 }
             }
             tc_fence_before();
@@ -372,7 +473,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tc_kernel(const LinearAr
                 const float r = lin_residual(a, t0 + c, col);
                 float z = 0.0f;
                 for (int p = 0; p < P; p++) z += ld_cluster(mapa(at, (uint32_t)p));
-                lin_store(a, t0 + c, col, z, b, r);
+                with_act(a.act, [&](auto act) { lin_put(a, t0 + c, col, lin_act<decltype(act)::value>(z + b) + r); });
             }
         }
         cluster_sync_all();                                          // nobody leaves while its sums are read
