@@ -8,9 +8,11 @@
 //   r = W^T k,  u = beta (v - r),  o = W^T q + (q . k) u,  S = W + k u^T,
 // so the block meets once a token (the sums of r and W^T q over the key rows), not twice.
 // Bound by the state's bytes: 2 x 64 KB a head and sequence against 3 KB a token.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "k3moe_internal.cuh"
+#include "k3moe_tc.cuh"
 
 namespace k3moe {
 namespace {
@@ -191,6 +193,549 @@ __global__ void __launch_bounds__(kRecThreads) delta_recurrent_kernel(const Delt
     for (int j = 0; j < RPT; j++) __stcs(reinterpret_cast<float4 *>(a.state_out + sbase + (size_t)j * kD), S[j]);
 }
 
+// ---------------------------------------------------------------- chunks of 64 tokens
+// For a chunk, with G_t the decay's logarithm summed from its start to token t:
+//   A_ti = beta_t exp(G_t - G_i) k_t . k_i  (i < t),   P_ti = scale exp(G_t - G_i) q_t . k_i  (i <= t)
+//   T = (I + A)^-1 diag(beta),  U = T (V - diag(exp(G)) K S),
+//   O = scale diag(exp(G)) Q S + P U,   S <- exp(G_C) S + (diag(exp(G_C - G)) K)^T U.
+// A unit lower triangular solve replaces 64 dependent steps, and all else is products on
+// the tensor cores.  Every exponent is a later token's sum minus an earlier one's, so no
+// factor exceeds one however strong the decay (a logarithm below -200 counts as -200: its
+// exponential is zero in float either way).
+//
+// One block per sequence and head walks its chunks; everything is transposed so that a
+// thread owns one value column v (a lane of tensor memory) and the state S^T [v][k] stays
+// with it: the A operands (S, R = V - .., U) go from registers to tensor memory and never
+// through shared memory, and the B operands (K and Q as they are, T, P) are shared tiles.
+// K and Q are exact in bf16; S, R, U, T and P enter as two bf16 terms each (hi + mid, 16
+// bits: 2^-18 of the element, where one term's 2^-9 would show in the float state), every
+// product of two such as hi hi + hi mid + mid hi.  Sums are float, in tensor memory; the
+// state's carry S exp(G_C) + .. is a float in a register.
+//
+// Warps: 0-3 prepare T and P of the next chunk while the chain of this one runs; 4-11 are
+// the chain S -> R -> U -> S; 12-15 write O; 16 loads K and Q; 17 issues the MMAs.
+constexpr int kC = 64;                                        // tokens a chunk
+constexpr int kChPrep = 4, kChChain = 8, kChOut = 4;
+constexpr int kChWarpChain = kChPrep, kChWarpOut = kChWarpChain + kChChain, kChWarpLoad = kChWarpOut + kChOut,
+              kChWarpMma = kChWarpLoad + 1;
+constexpr int kChThreads = (kChWarpMma + 1) * 32;             // 576
+constexpr int kChStages = 3;
+constexpr int kChBox = 2 * kC * 128;                          // 64 channels of K then of Q: 16 KB
+constexpr int kChStageBytes = 2 * kChBox;                     // 32 KB
+constexpr int kChTile = kC * 128;                             // one term of T or P: 8 KB
+constexpr int kChLd = 68;                                     // row stride of the float scratch
+constexpr size_t kChSmem = 1024 + kChStages * kChStageBytes + 4 * kChTile + 2 * kC * kChLd * 4;
+// tensor memory columns
+constexpr uint32_t kTmS = 0;      // S^T as an operand, [half of k][hi, mid][32]; the new S's sums over it
+constexpr uint32_t kTmR = 128;    // K S, then T R
+constexpr uint32_t kTmOq = 192;   // Q S
+constexpr uint32_t kTmOp = 256;   // P U
+constexpr uint32_t kTmRU = 320;   // R, then U scaled for the state, as an operand [hi, mid][32]
+constexpr uint32_t kTmU = 384;    // U as an operand [hi, mid][32]
+constexpr uint32_t kTmKK = 448;   // K K^T (lanes 0-63) and Q K^T (lanes 64-127) of the next chunk
+
+struct ChunkShared {
+    uint64_t kq_full[kChStages], kq_empty[kChStages];
+    uint64_t kk_full, kk_free, sc_ready[2], tp_ready, s_ready, d1_full, r_ready, d2_full, u_ready, d4_full, o_full, o_free,
+        drain;
+    uint32_t tmem;
+    volatile int bail;
+    float G[kC], rk[kC], beta[kC];
+    float kr[2][kC], kd[2][kC], qr[2][kC], dec[2];            // per chunk parity: see prepare
+};
+
+__device__ __forceinline__ uint32_t pack_hi(float lo, float hi)   // the upper halves of two words
+{
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+// (x, y) as two packed bf16 terms: hi rounded to nearest, mid the rounded remainder.
+__device__ __forceinline__ void split2(float x, float y, uint32_t *hi, uint32_t *mid)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(&h);
+    const __nv_bfloat162 m = __floats2bfloat162_rn(x - __uint_as_float(u << 16), y - __uint_as_float(u & 0xFFFF0000u));
+    *hi = u;
+    *mid = *reinterpret_cast<const uint32_t *>(&m);
+}
+// Eight values of row t, columns 8 c8.., as two terms of a swizzled tile.
+__device__ __forceinline__ void put_terms(uint8_t *tile, int t, int c8, const float (&x)[8])
+{
+    uint32_t h[4], m[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) split2(x[2 * j], x[2 * j + 1], &h[j], &m[j]);
+    uint8_t *p = tile + t * 128 + ((c8 ^ (t & 7)) << 4);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(p + kChTile) = make_uint4(m[0], m[1], m[2], m[3]);
+}
+__device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kChPrep * 32) : "memory"); }
+
+// X = (I + A)^-1 of the strictly lower triangular 64 x 64 A (rows kChLd floats apart), by
+// blocks: the 16 x 16 diagonal blocks by substitution, then twice
+// [X11 0; -X22 A21 X11, X22].  The upper blocks of A are scratch.  128 threads.
+__device__ void invert64(float *A, float *X, int tid)
+{
+    const int warp = tid >> 5, lane = tid & 31;
+    if (lane < 16) {                                          // column `lane` of diagonal block `warp`
+        const float *a = A + (16 * warp) * kChLd + 16 * warp;
+        float x[16];
+#pragma unroll
+        for (int t = 0; t < 16; t++) {
+            float s0 = t == lane ? 1.0f : 0.0f, s1 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < t; i++) {
+                if (i & 1)
+                    s1 = fmaf(-a[t * kChLd + i], x[i], s1);
+                else
+                    s0 = fmaf(-a[t * kChLd + i], x[i], s0);
+            }
+            x[t] = s0 + s1;
+            X[(16 * warp + t) * kChLd + 16 * warp + lane] = x[t];
+        }
+    }
+    prep_sync();
+    {   // 16 -> 32: pair p of blocks; each thread four of its 256 outputs
+        const int p = tid >> 6, r = (tid & 63) >> 2, c = (tid & 3) * 4, o = 32 * p;
+        float w[4] = {};
+        for (int i = 0; i < 16; i++) {
+            const float av = A[(o + 16 + r) * kChLd + o + i];
+            const float4 xv = *reinterpret_cast<const float4 *>(&X[(o + i) * kChLd + o + c]);
+            w[0] = fmaf(av, xv.x, w[0]);
+            w[1] = fmaf(av, xv.y, w[1]);
+            w[2] = fmaf(av, xv.z, w[2]);
+            w[3] = fmaf(av, xv.w, w[3]);
+        }
+        *reinterpret_cast<float4 *>(&A[(o + r) * kChLd + o + 16 + c]) = make_float4(w[0], w[1], w[2], w[3]);
+        prep_sync();
+        float x[4] = {};
+        for (int i = 0; i <= r; i++) {
+            const float xr = X[(o + 16 + r) * kChLd + o + 16 + i];
+            const float4 wv = *reinterpret_cast<const float4 *>(&A[(o + i) * kChLd + o + 16 + c]);
+            x[0] = fmaf(-xr, wv.x, x[0]);
+            x[1] = fmaf(-xr, wv.y, x[1]);
+            x[2] = fmaf(-xr, wv.z, x[2]);
+            x[3] = fmaf(-xr, wv.w, x[3]);
+        }
+        *reinterpret_cast<float4 *>(&X[(o + 16 + r) * kChLd + o + c]) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+    for (int e = tid; e < 2 * 16 * 16; e += 128)              // X is zero above its diagonal blocks
+        X[(32 * (e >> 8) + ((e >> 4) & 15)) * kChLd + 32 * (e >> 8) + 16 + (e & 15)] = 0.0f;
+    prep_sync();
+    {   // 32 -> 64: two rows and four columns a thread
+        const int r = (tid >> 3) * 2, c = (tid & 7) * 4;
+        float w[2][4] = {};
+        for (int i = 0; i < 32; i++) {
+            const float a0 = A[(32 + r) * kChLd + i], a1 = A[(33 + r) * kChLd + i];
+            const float4 xv = *reinterpret_cast<const float4 *>(&X[i * kChLd + c]);
+            w[0][0] = fmaf(a0, xv.x, w[0][0]); w[0][1] = fmaf(a0, xv.y, w[0][1]);
+            w[0][2] = fmaf(a0, xv.z, w[0][2]); w[0][3] = fmaf(a0, xv.w, w[0][3]);
+            w[1][0] = fmaf(a1, xv.x, w[1][0]); w[1][1] = fmaf(a1, xv.y, w[1][1]);
+            w[1][2] = fmaf(a1, xv.z, w[1][2]); w[1][3] = fmaf(a1, xv.w, w[1][3]);
+        }
+        *reinterpret_cast<float4 *>(&A[r * kChLd + 32 + c]) = make_float4(w[0][0], w[0][1], w[0][2], w[0][3]);
+        *reinterpret_cast<float4 *>(&A[(r + 1) * kChLd + 32 + c]) = make_float4(w[1][0], w[1][1], w[1][2], w[1][3]);
+        prep_sync();
+        float x[2][4] = {};
+        for (int i = 0; i < 32; i++) {
+            const float x0 = X[(32 + r) * kChLd + 32 + i], x1 = X[(33 + r) * kChLd + 32 + i];
+            const float4 wv = *reinterpret_cast<const float4 *>(&A[i * kChLd + 32 + c]);
+            x[0][0] = fmaf(-x0, wv.x, x[0][0]); x[0][1] = fmaf(-x0, wv.y, x[0][1]);
+            x[0][2] = fmaf(-x0, wv.z, x[0][2]); x[0][3] = fmaf(-x0, wv.w, x[0][3]);
+            x[1][0] = fmaf(-x1, wv.x, x[1][0]); x[1][1] = fmaf(-x1, wv.y, x[1][1]);
+            x[1][2] = fmaf(-x1, wv.z, x[1][2]); x[1][3] = fmaf(-x1, wv.w, x[1][3]);
+        }
+        *reinterpret_cast<float4 *>(&X[(32 + r) * kChLd + c]) = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
+        *reinterpret_cast<float4 *>(&X[(33 + r) * kChLd + c]) = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
+    }
+    prep_sync();
+}
+
+__global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaArgs a,
+                                                                    const __grid_constant__ CUtensorMap mq,
+                                                                    const __grid_constant__ CUtensorMap mk)
+{
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ __align__(1024) uint8_t csm_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(csm_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *tT = sm + kChStages * kChStageBytes, *tP = tT + 2 * kChTile;
+    float *As = reinterpret_cast<float *>(tP + 2 * kChTile), *Xs = As + kC * kChLd;
+    __shared__ ChunkShared sh;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x % a.H, seq = blockIdx.x / a.H;
+    int first, len, slot;
+    if (!delta_seq(a, seq, &first, &len, &slot)) return;
+    const size_t sbase = ((size_t)slot * a.H + h) * kD * kD;
+    if (len == 0) {
+        for (int e = threadIdx.x; e < kD * kD / 4; e += kChThreads)
+            reinterpret_cast<float4 *>(a.state_out + sbase)[e] =
+                a.state_in ? reinterpret_cast<const float4 *>(a.state_in + sbase)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+        return;
+    }
+    const int hq = h / (a.H / a.Hq), nc = (len + kC - 1) / kC;
+    int32_t *status = reinterpret_cast<int32_t *>(a.ws);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kChStages; s++) { mb_init(&sh.kq_full[s], 1); mb_init(&sh.kq_empty[s], 1); }
+        mb_init(&sh.kk_full, 1);
+        mb_init(&sh.kk_free, kChPrep);
+        for (int p = 0; p < 2; p++) mb_init(&sh.sc_ready[p], kChPrep);
+        mb_init(&sh.tp_ready, kChPrep);
+        mb_init(&sh.s_ready, kChChain);
+        mb_init(&sh.d1_full, 1);
+        mb_init(&sh.r_ready, kChChain);
+        mb_init(&sh.d2_full, 1);
+        mb_init(&sh.u_ready, kChChain);
+        mb_init(&sh.d4_full, 1);
+        mb_init(&sh.o_full, 1);
+        mb_init(&sh.o_free, kChOut);
+        mb_init(&sh.drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sh.bail = 0;
+    }
+    if (warp == kChWarpMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sh.tmem)),
+                     "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    // A wait of a whole warp; false (with the status bit) when it gave up or another did.
+    auto wait = [&](uint64_t &b, int phase) {
+        const bool ok = mb_wait_warp(&b, (uint32_t)phase & 1u);
+        if (!ok) {
+            set_status(status, K3MOE_DEV_TIMEOUT);
+            sh.bail = 1;
+        }
+        return ok && !sh.bail;
+    };
+    // A warp's accesses to tensor memory are done: tell the barrier's waiter.
+    auto arrive = [&](uint64_t &b) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mb_arrive(&b);
+    };
+
+    if (warp < kChPrep) {
+        // ---------------- T and P of chunk c, and its per-token scales:
+        //   kr = exp(G_t) / |k_t|, kd = exp(G_C - G_t) / |k_t|, qr = scale exp(G_t) / |q_t|, dec = exp(G_C)
+        const int row = threadIdx.x, t = row & (kC - 1);      // lanes 0-63: A's row t, 64-127: P's
+        const bool is_a = row < kC;
+        for (int c = 0; c < nc; c++) {
+            const int n = min(kC, len - kC * c), par = c & 1;
+            const size_t tok = (size_t)(first + kC * c);
+            float g0 = lane < n ? a.g[(tok + lane) * a.H + h] : 0.0f;
+            float g1 = lane + 32 < n ? a.g[(tok + lane + 32) * a.H + h] : 0.0f;
+            const float bt = t < n ? a.beta[(tok + t) * a.H + h] : 0.0f;
+            g0 = g0 < -200.0f ? -200.0f : g0;
+            g1 = g1 < -200.0f ? -200.0f : g1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float p0 = __shfl_up_sync(0xffffffffu, g0, o), p1 = __shfl_up_sync(0xffffffffu, g1, o);
+                if (lane >= o) { g0 += p0; g1 += p1; }
+            }
+            g1 += __shfl_sync(0xffffffffu, g0, 31);
+            const float Gt = (warp & 1) ? g1 : g0, GC = __shfl_sync(0xffffffffu, g1, 31);
+
+            const int st = c % kChStages;
+            if (!wait(sh.kq_full[st], c / kChStages)) break;
+            uint8_t *kq = sm + (size_t)st * kChStageBytes;
+            float norm = 1.0f;
+            if (a.qk_norm) {
+                float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 16; j++) {                // chunk order is the swizzle's: a sum does not mind
+                    const uint4 w = *reinterpret_cast<const uint4 *>(kq + (j >> 3) * kChBox + row * 128 + (((j & 7) ^ (row & 7)) << 4));
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        const float lo = __uint_as_float(u[r] << 16), hi = __uint_as_float(u[r] & 0xFFFF0000u);
+                        s0 = fmaf(lo, lo, s0);
+                        s1 = fmaf(hi, hi, s1);
+                    }
+                }
+                norm = 1.0f / sqrtf(s0 + s1 + a.eps);
+            }
+            if (t >= n) {
+                norm = 0.0f;
+                if (is_a)                                     // the rows past the sequence's end take no part in K^T U
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        *reinterpret_cast<uint4 *>(kq + (j >> 3) * kChBox + row * 128 + ((j & 7) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+            if (!wait(sh.kk_full, c)) break;                  // which also says that the scales of chunk c - 2 are read
+            if (is_a) {
+                sh.G[t] = Gt;
+                sh.rk[t] = norm;
+                sh.beta[t] = bt;
+                sh.kr[par][t] = norm * expf(Gt);
+                sh.kd[par][t] = norm * expf(GC - Gt);
+                if (t == 0) sh.dec[par] = expf(GC);
+            } else {
+                sh.qr[par][t] = a.scale * norm * expf(Gt);
+            }
+            __syncwarp();
+            if (lane == 0) mb_arrive(&sh.sc_ready[par]);
+            prep_sync();
+            const float rowf = is_a ? bt * norm : a.scale * norm;
+            const int last = is_a ? t - 1 : t;                // the row's last token
+            if (!is_a && c >= 1 && !wait(sh.o_full, c - 1)) break;     // P of chunk c - 1 is used
+            tc_fence_after();
+#pragma unroll 1
+            for (int i0 = 0; i0 < kC; i0 += 16) {
+                float v[16];
+                tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + kTmKK + i0, v);
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    const int i = i0 + j;
+                    v[j] = i <= last && t < n ? v[j] * (rowf * sh.rk[i] * __expf(fminf(Gt - sh.G[i], 0.0f))) : 0.0f;
+                }
+                if (is_a) {
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        *reinterpret_cast<float4 *>(&As[t * kChLd + i0 + 4 * j]) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                } else {
+                    const float(*v8)[8] = reinterpret_cast<const float(*)[8]>(v);
+                    put_terms(tP, t, i0 / 8, v8[0]);
+                    put_terms(tP, t, i0 / 8 + 1, v8[1]);
+                }
+            }
+            arrive(sh.kk_free);
+            prep_sync();
+            invert64(As, Xs, threadIdx.x);
+            if (c >= 1 && !wait(sh.d2_full, c - 1)) break;    // T of chunk c - 1 is used
+            {
+                const int r = threadIdx.x >> 1, c0 = (threadIdx.x & 1) * 32;
+#pragma unroll
+                for (int j8 = 0; j8 < 4; j8++) {
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const int i = c0 + 8 * j8 + j;
+                        x[j] = i <= r ? Xs[r * kChLd + i] * sh.beta[i] : 0.0f;
+                    }
+                    put_terms(tT, r, c0 / 8 + j8, x);
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mb_arrive(&sh.tp_ready);
+            prep_sync();                                      // the scratch and G, rk, beta are free again
+        }
+    } else if (warp < kChWarpOut) {
+        // ---------------- the chain: value column v, half of the channels or tokens
+        const int q = warp & 3, half = (warp - kChWarpChain) >> 2, v = 32 * q + lane;
+        const uint32_t la = tmem + ((uint32_t)(32 * q) << 16);
+        float S[64];
+#pragma unroll
+        for (int j = 0; j < 64; j++)
+            S[j] = a.state_in ? a.state_in[sbase + (size_t)(64 * half + j) * kD + v] : 0.0f;
+        auto put_state = [&]() {
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+                uint32_t hi[8], mid[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++) split2(S[16 * b + 2 * j], S[16 * b + 2 * j + 1], &hi[j], &mid[j]);
+                tmem_st8(la + kTmS + 64 * half + 8 * b, hi);
+                tmem_st8(la + kTmS + 64 * half + 32 + 8 * b, mid);
+            }
+            tmem_wait_st();
+            arrive(sh.s_ready);
+        };
+        put_state();
+        for (int c = 0; c < nc; c++) {
+            const int n = min(kC, len - kC * c), par = c & 1, t0 = 32 * half;
+            uint16_t vv[32];
+#pragma unroll
+            for (int j = 0; j < 32; j++)
+                vv[j] = t0 + j < n ? a.v[(size_t)(first + kC * c + t0 + j) * a.v_stride + h * kD + v] : 0;
+            if (!wait(sh.sc_ready[par], c >> 1) || !wait(sh.d1_full, c)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; b++) {
+                float d[16];
+                tmem_ld16(la + kTmR + t0 + 16 * b, d);
+                uint32_t hi[8], mid[8];
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    const int t = t0 + 16 * b + j;
+                    d[j] = t < n ? fmaf(-sh.kr[par][t], d[j], bf16_bits_to_f32(vv[16 * b + j])) : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j++) split2(d[2 * j], d[2 * j + 1], &hi[j], &mid[j]);
+                tmem_st8(la + kTmRU + 16 * half + 8 * b, hi);
+                tmem_st8(la + kTmRU + 32 + 16 * half + 8 * b, mid);
+            }
+            tmem_wait_st();
+            arrive(sh.r_ready);
+            if (!wait(sh.d2_full, c)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; b++) {
+                float d[16];
+                tmem_ld16(la + kTmR + t0 + 16 * b, d);
+                uint32_t hi[8], mid[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const int t = t0 + 16 * b + 2 * j;
+                    split2(d[2 * j] * sh.kd[par][t], d[2 * j + 1] * sh.kd[par][t + 1], &hi[j], &mid[j]);
+                }
+                tmem_st8(la + kTmRU + 16 * half + 8 * b, hi);
+                tmem_st8(la + kTmRU + 32 + 16 * half + 8 * b, mid);
+#pragma unroll
+                for (int j = 0; j < 8; j++) split2(d[2 * j], d[2 * j + 1], &hi[j], &mid[j]);
+                tmem_st8(la + kTmU + 16 * half + 8 * b, hi);
+                tmem_st8(la + kTmU + 32 + 16 * half + 8 * b, mid);
+            }
+            tmem_wait_st();
+            arrive(sh.u_ready);
+            if (!wait(sh.d4_full, c)) break;
+            tc_fence_after();
+            const float dec = sh.dec[par];
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+                float d[16];
+                tmem_ld16(la + kTmS + 64 * half + 16 * b, d);
+#pragma unroll
+                for (int j = 0; j < 16; j++) S[16 * b + j] = fmaf(dec, S[16 * b + j], d[j]);
+            }
+            if (c + 1 < nc) put_state();
+        }
+        if (!sh.bail)
+#pragma unroll
+            for (int j = 0; j < 64; j++) a.state_out[sbase + (size_t)(64 * half + j) * kD + v] = S[j];
+    } else if (warp < kChWarpLoad) {
+        // ---------------- O: value column v, every token of the chunk
+        const int q = warp & 3, v = 32 * q + lane;
+        const uint32_t la = tmem + ((uint32_t)(32 * q) << 16);
+        for (int c = 0; c < nc; c++) {
+            const int n = min(kC, len - kC * c), par = c & 1;
+            if (!wait(sh.o_full, c)) break;
+            tc_fence_after();
+            __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(a.out) + ((size_t)(first + kC * c) * a.H + h) * kD + v;
+#pragma unroll 1
+            for (int b = 0; b < 4; b++) {
+                float d[16], p[16];
+                tmem_ld16(la + kTmOq + 16 * b, d);
+                tmem_ld16(la + kTmOp + 16 * b, p);
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    const int t = 16 * b + j;
+                    if (t < n) o[(size_t)t * a.H * kD] = __float2bfloat16_rn(fmaf(sh.qr[par][t], d[j], p[j]));
+                }
+            }
+            arrive(sh.o_free);
+        }
+    } else if (warp == kChWarpLoad) {
+        for (int c = 0; c < nc && !sh.bail; c++) {
+            const int st = c % kChStages;
+            if (c >= kChStages && !wait(sh.kq_empty[st], c / kChStages - 1)) break;
+            if (lane == 0) {
+                uint8_t *kq = sm + (size_t)st * kChStageBytes;
+                mb_expect_tx(&sh.kq_full[st], kChStageBytes);
+                for (int b = 0; b < 2; b++) {
+                    tma2d(kq + b * kChBox, &mk, hq * kD + 64 * b, first + kC * c, &sh.kq_full[st]);
+                    tma2d(kq + b * kChBox + kC * 128, &mq, hq * kD + 64 * b, first + kC * c, &sh.kq_full[st]);
+                }
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---------------- MMA issue
+        const uint32_t idk = idesc(1, kC);                     // 128 x 64, both operands K-major
+        const uint32_t idn = idk | (1u << 16);                 // B with N contiguous (K^T U: channels)
+        const uint32_t aT = saddr(tT), aP = saddr(tP);
+        // K K^T and Q K^T of chunk c: rows of K over rows of Q, against K
+        auto kk = [&](int c) {
+            const uint32_t b = saddr(sm + (size_t)(c % kChStages) * kChStageBytes);
+            for (int s = 0; s < 8; s++) {
+                const uint32_t at = b + (s >> 2) * kChBox + (s & 3) * 32;
+                umma(tmem + kTmKK, sdesc(at), sdesc(at), idk, s > 0);
+            }
+        };
+        // D[v][t >= 16 j] += X[v][16 tokens j] tile[t][16 tokens j], the tile lower triangular:
+        // the terms of X at columns `x`, of the tile kChTile apart
+        auto tri = [&](uint32_t d, uint32_t x, uint32_t tile) {
+            uint32_t acc = 0;
+            for (int term = 0; term < 3; term++) {             // hi hi, hi mid, mid hi
+                const uint32_t xa = x + (term == 2 ? 32 : 0), ta = tile + (term == 1 ? kChTile : 0);
+                for (int j = 0; j < 4; j++) {
+                    umma_ts(d + 16 * j, xa + 8 * j, sdesc(ta + 16 * j * 128 + j * 32), idesc(1, kC - 16 * j), acc);
+                    acc = 1;
+                }
+            }
+        };
+        bool ok = wait(sh.kq_full[0], 0);
+        if (ok && lane == 0) {
+            kk(0);
+            umma_commit(&sh.kk_full);
+        }
+        __syncwarp();
+        for (int c = 0; c < nc && ok; c++) {
+            const uint32_t kq = saddr(sm + (size_t)(c % kChStages) * kChStageBytes);
+            if (!wait(sh.s_ready, c)) break;
+            tc_fence_after();
+            if (lane == 0) {
+                for (int s = 0; s < 16; s++)                   // K S, hi and mid
+                    umma_ts(tmem + kTmR, tmem + kTmS + 64 * ((s >> 2) & 1) + 32 * (s >> 3) + 8 * (s & 3),
+                            sdesc(kq + ((s >> 2) & 1) * kChBox + (s & 3) * 32), idk, s > 0);
+                umma_commit(&sh.d1_full);
+            }
+            __syncwarp();
+            if (c + 1 < nc) {
+                // the wait for chunk c - 1's O lets the preparation of chunk c + 1 write over that chunk's scales
+                if (!wait(sh.kq_full[(c + 1) % kChStages], (c + 1) / kChStages) || !wait(sh.kk_free, c) ||
+                    (c >= 1 && !wait(sh.o_free, c - 1)))
+                    break;
+                tc_fence_after();
+                if (lane == 0) {
+                    kk(c + 1);
+                    umma_commit(&sh.kk_full);
+                }
+                __syncwarp();
+            }
+            if (!wait(sh.tp_ready, c) || !wait(sh.r_ready, c)) break;
+            tc_fence_after();
+            if (lane == 0) {
+                tri(tmem + kTmR, tmem + kTmRU, aT);
+                umma_commit(&sh.d2_full);
+            }
+            __syncwarp();
+            if (c >= 1 && c + 1 == nc && !wait(sh.o_free, c - 1)) break;   // the last chunk has not waited above
+            tc_fence_after();
+            if (lane == 0)
+                for (int s = 0; s < 16; s++)                   // Q S
+                    umma_ts(tmem + kTmOq, tmem + kTmS + 64 * ((s >> 2) & 1) + 32 * (s >> 3) + 8 * (s & 3),
+                            sdesc(kq + ((s >> 2) & 1) * kChBox + kC * 128 + (s & 3) * 32), idk, s > 0);
+            __syncwarp();
+            if (!wait(sh.u_ready, c)) break;
+            tc_fence_after();
+            if (lane == 0) {
+                for (int s = 0; s < 16; s++)                   // K^T U into the state's sums, a half of k at a time
+                    umma_ts(tmem + kTmS + 64 * (s >> 3), tmem + kTmRU + 32 * ((s >> 2) & 1) + 8 * (s & 3),
+                            sdesc(kq + (s >> 3) * kChBox + (s & 3) * 16 * 128), idn, (s & 7) > 0);
+                umma_commit(&sh.d4_full);
+                umma_commit(&sh.kq_empty[c % kChStages]);
+                tri(tmem + kTmOp, tmem + kTmU, aP);
+                umma_commit(&sh.o_full);
+            }
+            __syncwarp();
+        }
+        if (lane == 0) {
+            umma_commit(&sh.drain);                            // every issued MMA done before the dealloc
+            mb_wait(&sh.drain, 0);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kChWarpMma)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
 }  // namespace
 
 size_t delta_workspace(const k3moe_delta_config &dc, int n_seq, int T)
@@ -201,8 +746,29 @@ size_t delta_workspace(const k3moe_delta_config &dc, int n_seq, int T)
     return kCtrOffset + kCtrBytes;
 }
 
+static cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
+{
+    CUtensorMap mq{}, mk{};
+    const uint64_t cols = (uint64_t)a.Hq * kD;
+    if (!map16s(&mq, a.q, (uint64_t)a.T, cols, (uint64_t)a.q_stride, kC) ||
+        !map16s(&mk, a.k, (uint64_t)a.T, cols, (uint64_t)a.k_stride, kC))
+        return cudaErrorInvalidValue;
+    static bool smem_set = false;
+    if (!smem_set) {
+        cudaFuncSetAttribute(delta_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChSmem);
+        smem_set = true;
+    }
+    timing_begin("delta_chunk", s);
+    const cudaError_t err =
+        launch_pdl(delta_chunk_kernel, dim3((unsigned)(a.n_seq * a.H)), dim3(kChThreads), kChSmem, s, a, mq, mk);
+    count_launch();
+    timing_end("delta_chunk", s);
+    return err;
+}
+
 cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t s)
 {
+    if (a.gate == 1 && a.T >= 24 * a.n_seq) return launch_chunks(a, s);
     // one block per head while they fill the GPU twice over; else 32 columns a block
     const long long blocks = (long long)a.n_seq * a.H;
     timing_begin("delta_recurrent", s);

@@ -487,21 +487,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tc_kernel(const LinearAr
     }
 }
 
-// 16-bit matrix of `rows` rows of `cols` elements, `stride` elements apart: boxes of 64
-// columns x box_rows rows, 128-byte swizzle; what a box has outside reads as zero.
-bool lin_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_rows)
-{
-    EncodeTiledFn fn = encode_tiled();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {stride * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)kLtBK, box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int NT>
 cudaError_t launch_rows(const LinearArgs &a, cudaStream_t s)
 {
@@ -570,8 +555,8 @@ template <int CG>
 cudaError_t launch_tc(const LinearArgs &a, const LinTile &tl, cudaStream_t s)
 {
     CUtensorMap mw{}, mx{};
-    if (!lin_map(&mw, a.w, (uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.K, 128) ||
-        !lin_map(&mx, a.x, (uint64_t)a.T, (uint64_t)a.K, (uint64_t)a.x_stride, (uint32_t)(tl.bn / CG)))
+    if (!map16s(&mw, a.w, (uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.K, 128) ||
+        !map16s(&mx, a.x, (uint64_t)a.T, (uint64_t)a.K, (uint64_t)a.x_stride, (uint32_t)(tl.bn / CG)))
         return cudaErrorInvalidValue;
     constexpr size_t smem = 1024 + kLtRing;
     static bool smem_set = false;
