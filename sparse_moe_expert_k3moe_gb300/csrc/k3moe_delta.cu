@@ -213,18 +213,22 @@ __global__ void __launch_bounds__(kRecThreads) delta_recurrent_kernel(const Delt
 // state's carry S exp(G_C) + .. is a float in a register.
 //
 // Warps: 0-3 prepare T and P of the next chunk while the chain of this one runs; 4-11 are
-// the chain S -> R -> U -> S; 12-15 write O; 16 loads K and Q; 17 issues the MMAs.
+// the chain S -> R -> U -> S; 12-15 write O; 16 issues the loads and the MMAs.
 constexpr int kC = 64;                                        // tokens a chunk
 constexpr int kChPrep = 4, kChChain = 8, kChOut = 4;
-constexpr int kChWarpChain = kChPrep, kChWarpOut = kChWarpChain + kChChain, kChWarpLoad = kChWarpOut + kChOut,
-              kChWarpMma = kChWarpLoad + 1;
-constexpr int kChThreads = (kChWarpMma + 1) * 32;             // 576
+constexpr int kChWarpChain = kChPrep, kChWarpOut = kChWarpChain + kChChain, kChWarpMma = kChWarpOut + kChOut;
+constexpr int kChThreads = (kChWarpMma + 4) * 32;             // 640: five warpgroups, the last with one warp at work
+// Registers a thread: 96 at launch (640 x 96 of the 65,536); the chain, with 64 of them for
+// the state, takes what the writers of O and the issuing warp give up.
+constexpr int kChRegs = 96, kChRegsChain = 136, kChRegsOut = 64, kChRegsMma = 40;
+static_assert(kChRegs + 2 * kChRegsChain + kChRegsOut + kChRegsMma <= 5 * kChRegs, "shares within the launch's");
 constexpr int kChStages = 3;
 constexpr int kChBox = 2 * kC * 128;                          // 64 channels of K then of Q: 16 KB
-constexpr int kChStageBytes = 2 * kChBox;                     // 32 KB
+constexpr int kChV = 2 * kChBox;                              // after both, V: two boxes of 64 columns
+constexpr int kChStageBytes = kChV + kC * kD * 2;             // 48 KB
 constexpr int kChTile = kC * 128;                             // one term of T or P: 8 KB
 constexpr int kChLd = 68;                                     // row stride of the float scratch
-constexpr size_t kChSmem = 1024 + kChStages * kChStageBytes + 4 * kChTile + 2 * kC * kChLd * 4;
+constexpr size_t kChSmem = 1024 + kChStages * kChStageBytes + 6 * kChTile + kC * kChLd * 4;   // T, two P, the scratch
 // tensor memory columns
 constexpr uint32_t kTmS = 0;      // S^T as an operand, [half of k][hi, mid][32]; the new S's sums over it
 constexpr uint32_t kTmR = 128;    // K S, then T R
@@ -235,18 +239,24 @@ constexpr uint32_t kTmU = 384;    // U as an operand [hi, mid][32]
 constexpr uint32_t kTmKK = 448;   // K K^T (lanes 0-63) and Q K^T (lanes 64-127) of the next chunk
 
 struct ChunkShared {
-    uint64_t kq_full[kChStages], kq_empty[kChStages];
+    uint64_t kq_full[kChStages];
     uint64_t kk_full, kk_free, sc_ready[2], tp_ready, s_ready, d1_full, r_ready, d2_full, u_ready, d4_full, o_full, o_free,
         drain;
     uint32_t tmem;
     volatile int bail;
-    float G[kC], rk[kC], beta[kC];
-    float kr[2][kC], kd[2][kC], qr[2][kC], dec[2];            // per chunk parity: see prepare
+    alignas(16) float G[kC], rk[kC], beta[kC];
+    alignas(16) float kr[2][kC], kd[2][kC], qr[2][kC];        // per chunk parity: the scales of the preparation
+    float dec[2];
 };
 
-__device__ __forceinline__ uint32_t pack_hi(float lo, float hi)   // the upper halves of two words
+constexpr float kLog2e = 1.4426950408889634f;
+// 2^x, x <= 0, within 2 ulp; volatile so that a select of its result stays a select (as a
+// branch around it, each of a row's 64 would be waited for by itself).
+__device__ __forceinline__ float exp2_approx(float x)
 {
-    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 // (x, y) as two packed bf16 terms: hi rounded to nearest, mid the rounded remainder.
 __device__ __forceinline__ void split2(float x, float y, uint32_t *hi, uint32_t *mid)
@@ -269,63 +279,68 @@ __device__ __forceinline__ void put_terms(uint8_t *tile, int t, int c8, const fl
 }
 __device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kChPrep * 32) : "memory"); }
 
-// X = (I + A)^-1 of the strictly lower triangular 64 x 64 A (rows kChLd floats apart), by
-// blocks: the 16 x 16 diagonal blocks by substitution, then twice
-// [X11 0; -X22 A21 X11, X22].  The upper blocks of A are scratch.  128 threads.
-__device__ void invert64(float *A, float *X, int tid)
+// A <- (I + A)^-1 of a strictly lower triangular 64 x 64 A (rows kChLd floats apart), in
+// place and by blocks: the 16 x 16 diagonal blocks by substitution, then twice
+// [X11 0; -X22 A21 X11, X22].  Above the diagonal blocks is scratch.  128 threads.
+__device__ __forceinline__ void invert64(float *A, int tid)
 {
     const int warp = tid >> 5, lane = tid & 31;
-    if (lane < 16) {                                          // column `lane` of diagonal block `warp`
-        const float *a = A + (16 * warp) * kChLd + 16 * warp;
+    {   // column `lane` of diagonal block `warp` (lanes from 16 on repeat the others' work)
+        float *a = A + (16 * warp) * kChLd + 16 * warp;
         float x[16];
+        const int col = lane & 15;
 #pragma unroll
         for (int t = 0; t < 16; t++) {
-            float s0 = t == lane ? 1.0f : 0.0f, s1 = 0.0f;
+            float r[16], p[4] = {t == col ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < t; i++) {
-                if (i & 1)
-                    s1 = fmaf(-a[t * kChLd + i], x[i], s1);
-                else
-                    s0 = fmaf(-a[t * kChLd + i], x[i], s0);
-            }
-            x[t] = s0 + s1;
-            X[(16 * warp + t) * kChLd + 16 * warp + lane] = x[t];
+            for (int i = 0; i < t; i += 4) *reinterpret_cast<float4 *>(&r[i]) = *reinterpret_cast<const float4 *>(&a[t * kChLd + i]);
+#pragma unroll
+            for (int i = 0; i < t; i++) p[i & 3] = fmaf(-r[i], x[i], p[i & 3]);
+            x[t] = (p[0] + p[1]) + (p[2] + p[3]);
         }
+        __syncwarp();
+        if (lane < 16)
+#pragma unroll
+            for (int t = 0; t < 16; t++) a[t * kChLd + col] = x[t];       // zero above the diagonal
     }
     prep_sync();
-    {   // 16 -> 32: pair p of blocks; each thread four of its 256 outputs
-        const int p = tid >> 6, r = (tid & 63) >> 2, c = (tid & 3) * 4, o = 32 * p;
+    {   // 16 -> 32: a pair of blocks for each half of the threads, four of its 256 outputs a thread
+        float *a = A + 32 * (tid >> 6) * (kChLd + 1);
+        const int r = (tid & 63) >> 2, c = (tid & 3) * 4;
         float w[4] = {};
+#pragma unroll
         for (int i = 0; i < 16; i++) {
-            const float av = A[(o + 16 + r) * kChLd + o + i];
-            const float4 xv = *reinterpret_cast<const float4 *>(&X[(o + i) * kChLd + o + c]);
+            const float av = a[(16 + r) * kChLd + i];
+            const float4 xv = *reinterpret_cast<const float4 *>(&a[i * kChLd + c]);
             w[0] = fmaf(av, xv.x, w[0]);
             w[1] = fmaf(av, xv.y, w[1]);
             w[2] = fmaf(av, xv.z, w[2]);
             w[3] = fmaf(av, xv.w, w[3]);
         }
-        *reinterpret_cast<float4 *>(&A[(o + r) * kChLd + o + 16 + c]) = make_float4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<float4 *>(&a[r * kChLd + 16 + c]) = make_float4(w[0], w[1], w[2], w[3]);
         prep_sync();
         float x[4] = {};
-        for (int i = 0; i <= r; i++) {
-            const float xr = X[(o + 16 + r) * kChLd + o + 16 + i];
-            const float4 wv = *reinterpret_cast<const float4 *>(&A[(o + i) * kChLd + o + 16 + c]);
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const float xr = a[(16 + r) * kChLd + 16 + i];
+            const float4 wv = *reinterpret_cast<const float4 *>(&a[i * kChLd + 16 + c]);
             x[0] = fmaf(-xr, wv.x, x[0]);
             x[1] = fmaf(-xr, wv.y, x[1]);
             x[2] = fmaf(-xr, wv.z, x[2]);
             x[3] = fmaf(-xr, wv.w, x[3]);
         }
-        *reinterpret_cast<float4 *>(&X[(o + 16 + r) * kChLd + o + c]) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(&a[(16 + r) * kChLd + c]) = make_float4(x[0], x[1], x[2], x[3]);
+        prep_sync();
+        *reinterpret_cast<float4 *>(&a[r * kChLd + 16 + c]) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int e = tid; e < 2 * 16 * 16; e += 128)              // X is zero above its diagonal blocks
-        X[(32 * (e >> 8) + ((e >> 4) & 15)) * kChLd + 32 * (e >> 8) + 16 + (e & 15)] = 0.0f;
     prep_sync();
     {   // 32 -> 64: two rows and four columns a thread
         const int r = (tid >> 3) * 2, c = (tid & 7) * 4;
         float w[2][4] = {};
+#pragma unroll 16
         for (int i = 0; i < 32; i++) {
             const float a0 = A[(32 + r) * kChLd + i], a1 = A[(33 + r) * kChLd + i];
-            const float4 xv = *reinterpret_cast<const float4 *>(&X[i * kChLd + c]);
+            const float4 xv = *reinterpret_cast<const float4 *>(&A[i * kChLd + c]);
             w[0][0] = fmaf(a0, xv.x, w[0][0]); w[0][1] = fmaf(a0, xv.y, w[0][1]);
             w[0][2] = fmaf(a0, xv.z, w[0][2]); w[0][3] = fmaf(a0, xv.w, w[0][3]);
             w[1][0] = fmaf(a1, xv.x, w[1][0]); w[1][1] = fmaf(a1, xv.y, w[1][1]);
@@ -335,30 +350,32 @@ __device__ void invert64(float *A, float *X, int tid)
         *reinterpret_cast<float4 *>(&A[(r + 1) * kChLd + 32 + c]) = make_float4(w[1][0], w[1][1], w[1][2], w[1][3]);
         prep_sync();
         float x[2][4] = {};
+#pragma unroll 16
         for (int i = 0; i < 32; i++) {
-            const float x0 = X[(32 + r) * kChLd + 32 + i], x1 = X[(33 + r) * kChLd + 32 + i];
+            const float x0 = A[(32 + r) * kChLd + 32 + i], x1 = A[(33 + r) * kChLd + 32 + i];
             const float4 wv = *reinterpret_cast<const float4 *>(&A[i * kChLd + 32 + c]);
             x[0][0] = fmaf(-x0, wv.x, x[0][0]); x[0][1] = fmaf(-x0, wv.y, x[0][1]);
             x[0][2] = fmaf(-x0, wv.z, x[0][2]); x[0][3] = fmaf(-x0, wv.w, x[0][3]);
             x[1][0] = fmaf(-x1, wv.x, x[1][0]); x[1][1] = fmaf(-x1, wv.y, x[1][1]);
             x[1][2] = fmaf(-x1, wv.z, x[1][2]); x[1][3] = fmaf(-x1, wv.w, x[1][3]);
         }
-        *reinterpret_cast<float4 *>(&X[(32 + r) * kChLd + c]) = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
-        *reinterpret_cast<float4 *>(&X[(33 + r) * kChLd + c]) = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
+        *reinterpret_cast<float4 *>(&A[(32 + r) * kChLd + c]) = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
+        *reinterpret_cast<float4 *>(&A[(33 + r) * kChLd + c]) = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
     }
     prep_sync();
 }
 
 __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaArgs a,
                                                                     const __grid_constant__ CUtensorMap mq,
-                                                                    const __grid_constant__ CUtensorMap mk)
+                                                                    const __grid_constant__ CUtensorMap mk,
+                                                                    const __grid_constant__ CUtensorMap mv)
 {
     pdl_wait();
     pdl_trigger();
     extern __shared__ __align__(1024) uint8_t csm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(csm_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *tT = sm + kChStages * kChStageBytes, *tP = tT + 2 * kChTile;
-    float *As = reinterpret_cast<float *>(tP + 2 * kChTile), *Xs = As + kC * kChLd;
+    float *As = reinterpret_cast<float *>(tP + 4 * kChTile);
     __shared__ ChunkShared sh;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -376,7 +393,7 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
     int32_t *status = reinterpret_cast<int32_t *>(a.ws);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kChStages; s++) { mb_init(&sh.kq_full[s], 1); mb_init(&sh.kq_empty[s], 1); }
+        for (int s = 0; s < kChStages; s++) mb_init(&sh.kq_full[s], 1);
         mb_init(&sh.kk_full, 1);
         mb_init(&sh.kk_free, kChPrep);
         for (int p = 0; p < 2; p++) mb_init(&sh.sc_ready[p], kChPrep);
@@ -401,7 +418,7 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    constexpr uint32_t tmem = 0;                              // all 512 columns: the allocation starts at the first
     // A wait of a whole warp; false (with the status bit) when it gave up or another did.
     auto wait = [&](uint64_t &b, int phase) {
         const bool ok = mb_wait_warp(&b, (uint32_t)phase & 1u);
@@ -417,6 +434,13 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
         __syncwarp();
         if (lane == 0) mb_arrive(&b);
     };
+
+    if (warp >= kChWarpChain && warp < kChWarpOut)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChRegsChain));
+    else if (warp >= kChWarpOut && warp < kChWarpMma)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChRegsOut));
+    else if (warp >= kChWarpMma)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChRegsMma));
 
     if (warp < kChPrep) {
         // ---------------- T and P of chunk c, and its per-token scales:
@@ -465,9 +489,9 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
                     for (int j = 0; j < 16; j++)
                         *reinterpret_cast<uint4 *>(kq + (j >> 3) * kChBox + row * 128 + ((j & 7) << 4)) = make_uint4(0, 0, 0, 0);
             }
-            if (!wait(sh.kk_full, c)) break;                  // which also says that the scales of chunk c - 2 are read
+            if (!wait(sh.kk_full, c)) break;                  // which also says that chunk c - 2's scales and P are used
             if (is_a) {
-                sh.G[t] = Gt;
+                sh.G[t] = Gt * kLog2e;
                 sh.rk[t] = norm;
                 sh.beta[t] = bt;
                 sh.kr[par][t] = norm * expf(Gt);
@@ -479,18 +503,25 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
             __syncwarp();
             if (lane == 0) mb_arrive(&sh.sc_ready[par]);
             prep_sync();
-            const float rowf = is_a ? bt * norm : a.scale * norm;
-            const int last = is_a ? t - 1 : t;                // the row's last token
-            if (!is_a && c >= 1 && !wait(sh.o_full, c - 1)) break;     // P of chunk c - 1 is used
+            const float rowf = is_a ? bt * norm : a.scale * norm, G2 = Gt * kLog2e;
+            const int last = t < n ? (is_a ? t - 1 : t) : -1;          // the row's last token
+            const int width = 32 * (warp & 1) + 32;           // no row of this warp reaches further
             tc_fence_after();
 #pragma unroll 1
-            for (int i0 = 0; i0 < kC; i0 += 16) {
+            for (int i0 = 0; i0 < (is_a ? width : kC); i0 += 16) {
                 float v[16];
                 tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + kTmKK + i0, v);
 #pragma unroll
-                for (int j = 0; j < 16; j++) {
-                    const int i = i0 + j;
-                    v[j] = i <= last && t < n ? v[j] * (rowf * sh.rk[i] * __expf(fminf(Gt - sh.G[i], 0.0f))) : 0.0f;
+                for (int j4 = 0; j4 < 4; j4++) {
+                    const float4 gi = *reinterpret_cast<const float4 *>(&sh.G[i0 + 4 * j4]);
+                    const float4 ri = *reinterpret_cast<const float4 *>(&sh.rk[i0 + 4 * j4]);
+                    const float g[4] = {gi.x, gi.y, gi.z, gi.w}, r[4] = {ri.x, ri.y, ri.z, ri.w};
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const float e = exp2_approx(fminf(G2 - g[j], 0.0f));
+                        const float x = v[4 * j4 + j] * r[j] * (rowf * e);
+                        v[4 * j4 + j] = i0 + 4 * j4 + j <= last ? x : 0.0f;
+                    }
                 }
                 if (is_a) {
 #pragma unroll
@@ -498,23 +529,28 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
                         *reinterpret_cast<float4 *>(&As[t * kChLd + i0 + 4 * j]) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 } else {
                     const float(*v8)[8] = reinterpret_cast<const float(*)[8]>(v);
-                    put_terms(tP, t, i0 / 8, v8[0]);
-                    put_terms(tP, t, i0 / 8 + 1, v8[1]);
+                    put_terms(tP + par * 2 * kChTile, t, i0 / 8, v8[0]);
+                    put_terms(tP + par * 2 * kChTile, t, i0 / 8 + 1, v8[1]);
                 }
             }
             arrive(sh.kk_free);
             prep_sync();
-            invert64(As, Xs, threadIdx.x);
+            invert64(As, threadIdx.x);
             if (c >= 1 && !wait(sh.d2_full, c - 1)) break;    // T of chunk c - 1 is used
             {
                 const int r = threadIdx.x >> 1, c0 = (threadIdx.x & 1) * 32;
 #pragma unroll
                 for (int j8 = 0; j8 < 4; j8++) {
-                    float x[8];
+                    float x[8], b[8];
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4) {
+                        *reinterpret_cast<float4 *>(&x[j]) = *reinterpret_cast<const float4 *>(&As[r * kChLd + c0 + 8 * j8 + j]);
+                        *reinterpret_cast<float4 *>(&b[j]) = *reinterpret_cast<const float4 *>(&sh.beta[c0 + 8 * j8 + j]);
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
-                        const int i = c0 + 8 * j8 + j;
-                        x[j] = i <= r ? Xs[r * kChLd + i] * sh.beta[i] : 0.0f;
+                        const float y = x[j] * b[j];
+                        x[j] = c0 + 8 * j8 + j <= r ? y : 0.0f;
                     }
                     put_terms(tT, r, c0 / 8 + j8, x);
                 }
@@ -547,47 +583,67 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
         put_state();
         for (int c = 0; c < nc; c++) {
             const int n = min(kC, len - kC * c), par = c & 1, t0 = 32 * half;
-            uint16_t vv[32];
+            const int st = c % kChStages;
+            // V[t][v] in its swizzled tile
+            const uint8_t *vt = sm + (size_t)st * kChStageBytes + kChV + (q >> 1) * kC * 128 + (v & 7) * 2;
+            const uint32_t v8 = (uint32_t)(v >> 3) & 7u;
+            if (!wait(sh.kq_full[st], c / kChStages)) break;
+            uint32_t vv[16];                                      // two tokens a word
 #pragma unroll
-            for (int j = 0; j < 32; j++)
-                vv[j] = t0 + j < n ? a.v[(size_t)(first + kC * c + t0 + j) * a.v_stride + h * kD + v] : 0;
+            for (int j = 0; j < 16; j++) {
+                const uint32_t t = t0 + 2 * j;
+                const uint32_t x = *reinterpret_cast<const uint16_t *>(vt + t * 128 + ((v8 ^ ((2 * j) & 7u)) << 4));
+                const uint32_t y = *reinterpret_cast<const uint16_t *>(vt + t * 128 + 128 + ((v8 ^ ((2 * j + 1) & 7u)) << 4));
+                vv[j] = x | (y << 16);
+            }
             if (!wait(sh.sc_ready[par], c >> 1) || !wait(sh.d1_full, c)) break;
             tc_fence_after();
+            {
+                uint32_t d[32];
+                tmem_ld16_nowait(la + kTmR + t0, *reinterpret_cast<uint32_t(*)[16]>(&d[0]));
+                tmem_ld16_nowait(la + kTmR + t0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&d[16]));
+                tmem_wait_ld();
 #pragma unroll
-            for (int b = 0; b < 2; b++) {
-                float d[16];
-                tmem_ld16(la + kTmR + t0 + 16 * b, d);
-                uint32_t hi[8], mid[8];
+                for (int b = 0; b < 4; b++) {
+                    uint32_t hi[4], mid[4];
 #pragma unroll
-                for (int j = 0; j < 16; j++) {
-                    const int t = t0 + 16 * b + j;
-                    d[j] = t < n ? fmaf(-sh.kr[par][t], d[j], bf16_bits_to_f32(vv[16 * b + j])) : 0.0f;
+                    for (int j2 = 0; j2 < 4; j2++) {
+                        const int j = 8 * b + 2 * j2;
+                        const float2 kr = *reinterpret_cast<const float2 *>(&sh.kr[par][t0 + j]);
+                        const float x = fmaf(-kr.x, __uint_as_float(d[j]), __uint_as_float(vv[j >> 1] << 16));
+                        const float y = fmaf(-kr.y, __uint_as_float(d[j + 1]), __uint_as_float(vv[j >> 1] & 0xFFFF0000u));
+                        split2(t0 + j < n ? x : 0.0f, t0 + j + 1 < n ? y : 0.0f, &hi[j2], &mid[j2]);
+                    }
+                    tmem_st4(la + kTmRU + 16 * half + 4 * b, hi);
+                    tmem_st4(la + kTmRU + 32 + 16 * half + 4 * b, mid);
                 }
-#pragma unroll
-                for (int j = 0; j < 8; j++) split2(d[2 * j], d[2 * j + 1], &hi[j], &mid[j]);
-                tmem_st8(la + kTmRU + 16 * half + 8 * b, hi);
-                tmem_st8(la + kTmRU + 32 + 16 * half + 8 * b, mid);
             }
             tmem_wait_st();
             arrive(sh.r_ready);
             if (!wait(sh.d2_full, c)) break;
             tc_fence_after();
+            {
+                uint32_t d[32];
+                tmem_ld16_nowait(la + kTmR + t0, *reinterpret_cast<uint32_t(*)[16]>(&d[0]));
+                tmem_ld16_nowait(la + kTmR + t0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&d[16]));
+                tmem_wait_ld();
 #pragma unroll
-            for (int b = 0; b < 2; b++) {
-                float d[16];
-                tmem_ld16(la + kTmR + t0 + 16 * b, d);
-                uint32_t hi[8], mid[8];
+                for (int b = 0; b < 4; b++) {
+                    uint32_t hi[4], mid[4];
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const int t = t0 + 16 * b + 2 * j;
-                    split2(d[2 * j] * sh.kd[par][t], d[2 * j + 1] * sh.kd[par][t + 1], &hi[j], &mid[j]);
+                    for (int j2 = 0; j2 < 4; j2++) {
+                        const int j = 8 * b + 2 * j2;
+                        const float2 kd = *reinterpret_cast<const float2 *>(&sh.kd[par][t0 + j]);
+                        split2(__uint_as_float(d[j]) * kd.x, __uint_as_float(d[j + 1]) * kd.y, &hi[j2], &mid[j2]);
+                    }
+                    tmem_st4(la + kTmRU + 16 * half + 4 * b, hi);
+                    tmem_st4(la + kTmRU + 32 + 16 * half + 4 * b, mid);
+#pragma unroll
+                    for (int j2 = 0; j2 < 4; j2++)
+                        split2(__uint_as_float(d[8 * b + 2 * j2]), __uint_as_float(d[8 * b + 2 * j2 + 1]), &hi[j2], &mid[j2]);
+                    tmem_st4(la + kTmU + 16 * half + 4 * b, hi);
+                    tmem_st4(la + kTmU + 32 + 16 * half + 4 * b, mid);
                 }
-                tmem_st8(la + kTmRU + 16 * half + 8 * b, hi);
-                tmem_st8(la + kTmRU + 32 + 16 * half + 8 * b, mid);
-#pragma unroll
-                for (int j = 0; j < 8; j++) split2(d[2 * j], d[2 * j + 1], &hi[j], &mid[j]);
-                tmem_st8(la + kTmU + 16 * half + 8 * b, hi);
-                tmem_st8(la + kTmU + 32 + 16 * half + 8 * b, mid);
             }
             tmem_wait_st();
             arrive(sh.u_ready);
@@ -595,18 +651,20 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
             tc_fence_after();
             const float dec = sh.dec[par];
 #pragma unroll
-            for (int b = 0; b < 4; b++) {
-                float d[16];
-                tmem_ld16(la + kTmS + 64 * half + 16 * b, d);
+            for (int b = 0; b < 2; b++) {
+                uint32_t d[32];
+                tmem_ld16_nowait(la + kTmS + 64 * half + 32 * b, *reinterpret_cast<uint32_t(*)[16]>(&d[0]));
+                tmem_ld16_nowait(la + kTmS + 64 * half + 32 * b + 16, *reinterpret_cast<uint32_t(*)[16]>(&d[16]));
+                tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; j++) S[16 * b + j] = fmaf(dec, S[16 * b + j], d[j]);
+                for (int j = 0; j < 32; j++) S[32 * b + j] = fmaf(dec, S[32 * b + j], __uint_as_float(d[j]));
             }
             if (c + 1 < nc) put_state();
         }
         if (!sh.bail)
 #pragma unroll
             for (int j = 0; j < 64; j++) a.state_out[sbase + (size_t)(64 * half + j) * kD + v] = S[j];
-    } else if (warp < kChWarpLoad) {
+    } else if (warp < kChWarpMma) {
         // ---------------- O: value column v, every token of the chunk
         const int q = warp & 3, v = 32 * q + lane;
         const uint32_t la = tmem + ((uint32_t)(32 * q) << 16);
@@ -614,126 +672,129 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
             const int n = min(kC, len - kC * c), par = c & 1;
             if (!wait(sh.o_full, c)) break;
             tc_fence_after();
-            __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(a.out) + ((size_t)(first + kC * c) * a.H + h) * kD + v;
+            // neighbouring lanes trade a token each: two columns of one token a store
+            const int mine = lane & 1;
+            uint32_t *o = reinterpret_cast<uint32_t *>(a.out + ((size_t)(first + kC * c + mine) * a.H + h) * kD + (v & ~1));
+            const size_t step = (size_t)a.H * kD;             // words of two tokens
 #pragma unroll 1
-            for (int b = 0; b < 4; b++) {
-                float d[16], p[16];
-                tmem_ld16(la + kTmOq + 16 * b, d);
-                tmem_ld16(la + kTmOp + 16 * b, p);
+            for (int b = 0; b < 4; b++, o += 8 * step) {
+                uint32_t d[16], p[16];
+                tmem_ld16_nowait(la + kTmOq + 16 * b, d);
+                tmem_ld16_nowait(la + kTmOp + 16 * b, p);
+                tmem_wait_ld();
+                uint32_t *ob = o;
 #pragma unroll
-                for (int j = 0; j < 16; j++) {
-                    const int t = 16 * b + j;
-                    if (t < n) o[(size_t)t * a.H * kD] = __float2bfloat16_rn(fmaf(sh.qr[par][t], d[j], p[j]));
+                for (int j4 = 0; j4 < 4; j4++) {
+                    const float4 qr = *reinterpret_cast<const float4 *>(&sh.qr[par][16 * b + 4 * j4]);
+                    const float r[4] = {qr.x, qr.y, qr.z, qr.w};
+                    float x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) x[j] = fmaf(r[j], __uint_as_float(d[4 * j4 + j]), __uint_as_float(p[4 * j4 + j]));
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+                        const float got = __shfl_xor_sync(0xffffffffu, mine ? x[2 * j] : x[2 * j + 1], 1);
+                        const __nv_bfloat162 w = __floats2bfloat162_rn(mine ? got : x[2 * j], mine ? x[2 * j + 1] : got);
+                        if (16 * b + 4 * j4 + 2 * j + mine < n) *ob = *reinterpret_cast<const uint32_t *>(&w);
+                        ob += step;
+                    }
                 }
             }
             arrive(sh.o_free);
         }
-    } else if (warp == kChWarpLoad) {
-        for (int c = 0; c < nc && !sh.bail; c++) {
-            const int st = c % kChStages;
-            if (c >= kChStages && !wait(sh.kq_empty[st], c / kChStages - 1)) break;
-            if (lane == 0) {
-                uint8_t *kq = sm + (size_t)st * kChStageBytes;
-                mb_expect_tx(&sh.kq_full[st], kChStageBytes);
-                for (int b = 0; b < 2; b++) {
-                    tma2d(kq + b * kChBox, &mk, hq * kD + 64 * b, first + kC * c, &sh.kq_full[st]);
-                    tma2d(kq + b * kChBox + kC * 128, &mq, hq * kD + 64 * b, first + kC * c, &sh.kq_full[st]);
-                }
-            }
-            __syncwarp();
-        }
-    } else {
-        // ---------------- MMA issue
+    } else if (warp == kChWarpMma) {
+        // ---------------- loads and MMA issue
         const uint32_t idk = idesc(1, kC);                     // 128 x 64, both operands K-major
         const uint32_t idn = idk | (1u << 16);                 // B with N contiguous (K^T U: channels)
         const uint32_t aT = saddr(tT), aP = saddr(tP);
         // K K^T and Q K^T of chunk c: rows of K over rows of Q, against K
         auto kk = [&](int c) {
             const uint32_t b = saddr(sm + (size_t)(c % kChStages) * kChStageBytes);
+            const uint64_t bd = sdesc(b);
+#pragma unroll
             for (int s = 0; s < 8; s++) {
-                const uint32_t at = b + (s >> 2) * kChBox + (s & 3) * 32;
-                umma(tmem + kTmKK, sdesc(at), sdesc(at), idk, s > 0);
+                const uint64_t at = bd + (((s >> 2) * kChBox + (s & 3) * 32) >> 4);
+                umma_warp(kTmKK, at, at, idk, s > 0);
             }
         };
         // D[v][t >= 16 j] += X[v][16 tokens j] tile[t][16 tokens j], the tile lower triangular:
         // the terms of X at columns `x`, of the tile kChTile apart
         auto tri = [&](uint32_t d, uint32_t x, uint32_t tile) {
-            uint32_t acc = 0;
-            for (int term = 0; term < 3; term++) {             // hi hi, hi mid, mid hi
-                const uint32_t xa = x + (term == 2 ? 32 : 0), ta = tile + (term == 1 ? kChTile : 0);
-                for (int j = 0; j < 4; j++) {
-                    umma_ts(d + 16 * j, xa + 8 * j, sdesc(ta + 16 * j * 128 + j * 32), idesc(1, kC - 16 * j), acc);
-                    acc = 1;
-                }
+            const uint64_t td = sdesc(tile);
+#pragma unroll
+            for (int term = 0; term < 3; term++)               // hi hi, hi mid, mid hi
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    umma_ts_warp(d + 16 * j, x + (term == 2 ? 32 : 0) + 8 * j,
+                            td + (((term == 1 ? kChTile : 0) + 16 * j * 128 + j * 32) >> 4), idesc(1, kC - 16 * j),
+                            term > 0 || j > 0);
+        };
+        auto load = [&](int c) {
+            uint8_t *p = sm + (size_t)(c % kChStages) * kChStageBytes;
+            uint64_t *bar = &sh.kq_full[c % kChStages];
+            mb_expect_tx(bar, kChStageBytes);
+            for (int b = 0; b < 2; b++) {
+                tma2d(p + b * kChBox, &mk, hq * kD + 64 * b, first + kC * c, bar);
+                tma2d(p + b * kChBox + kC * 128, &mq, hq * kD + 64 * b, first + kC * c, bar);
+                tma2d(p + kChV + b * kC * 128, &mv, h * kD + 64 * b, first + kC * c, bar);
             }
         };
-        bool ok = wait(sh.kq_full[0], 0);
-        if (ok && lane == 0) {
-            kk(0);
-            umma_commit(&sh.kk_full);
-        }
+        if (lane == 0)
+            for (int c = 0; c < min(nc, 2); c++) load(c);
         __syncwarp();
+        bool ok = wait(sh.kq_full[0], 0);
+        if (ok) {
+            kk(0);
+            umma_commit_warp(&sh.kk_full);
+        }
         for (int c = 0; c < nc && ok; c++) {
-            const uint32_t kq = saddr(sm + (size_t)(c % kChStages) * kChStageBytes);
+            const uint64_t kq = sdesc(saddr(sm + (size_t)(c % kChStages) * kChStageBytes));
             if (!wait(sh.s_ready, c)) break;
             tc_fence_after();
-            if (lane == 0) {
-                for (int s = 0; s < 16; s++)                   // K S, hi and mid
-                    umma_ts(tmem + kTmR, tmem + kTmS + 64 * ((s >> 2) & 1) + 32 * (s >> 3) + 8 * (s & 3),
-                            sdesc(kq + ((s >> 2) & 1) * kChBox + (s & 3) * 32), idk, s > 0);
-                umma_commit(&sh.d1_full);
-            }
-            __syncwarp();
+#pragma unroll
+            for (int s = 0; s < 16; s++)                       // K S, hi and mid
+                umma_ts_warp(kTmR, kTmS + 64 * ((s >> 2) & 1) + 32 * (s >> 3) + 8 * (s & 3),
+                             kq + ((((s >> 2) & 1) * kChBox + (s & 3) * 32) >> 4), idk, s > 0);
+            umma_commit_warp(&sh.d1_full);
             if (c + 1 < nc) {
-                // the wait for chunk c - 1's O lets the preparation of chunk c + 1 write over that chunk's scales
+                // the wait for chunk c - 1's O lets the preparation of chunk c + 1 write over that chunk's scales and P
                 if (!wait(sh.kq_full[(c + 1) % kChStages], (c + 1) / kChStages) || !wait(sh.kk_free, c) ||
                     (c >= 1 && !wait(sh.o_free, c - 1)))
                     break;
                 tc_fence_after();
-                if (lane == 0) {
-                    kk(c + 1);
-                    umma_commit(&sh.kk_full);
-                }
-                __syncwarp();
+                kk(c + 1);
+                umma_commit_warp(&sh.kk_full);
             }
+            if (c + 2 < nc && lane == 0) load(c + 2);          // chunk c - 1 is done with its stage: its state was here
+            __syncwarp();
             if (!wait(sh.tp_ready, c) || !wait(sh.r_ready, c)) break;
             tc_fence_after();
-            if (lane == 0) {
-                tri(tmem + kTmR, tmem + kTmRU, aT);
-                umma_commit(&sh.d2_full);
-            }
-            __syncwarp();
+            tri(kTmR, kTmRU, aT);
+            umma_commit_warp(&sh.d2_full);
             if (c >= 1 && c + 1 == nc && !wait(sh.o_free, c - 1)) break;   // the last chunk has not waited above
             tc_fence_after();
-            if (lane == 0)
-                for (int s = 0; s < 16; s++)                   // Q S
-                    umma_ts(tmem + kTmOq, tmem + kTmS + 64 * ((s >> 2) & 1) + 32 * (s >> 3) + 8 * (s & 3),
-                            sdesc(kq + ((s >> 2) & 1) * kChBox + kC * 128 + (s & 3) * 32), idk, s > 0);
-            __syncwarp();
+#pragma unroll
+            for (int s = 0; s < 16; s++)                       // Q S
+                umma_ts_warp(kTmOq, kTmS + 64 * ((s >> 2) & 1) + 32 * (s >> 3) + 8 * (s & 3),
+                             kq + ((((s >> 2) & 1) * kChBox + kC * 128 + (s & 3) * 32) >> 4), idk, s > 0);
             if (!wait(sh.u_ready, c)) break;
             tc_fence_after();
-            if (lane == 0) {
-                for (int s = 0; s < 16; s++)                   // K^T U into the state's sums, a half of k at a time
-                    umma_ts(tmem + kTmS + 64 * (s >> 3), tmem + kTmRU + 32 * ((s >> 2) & 1) + 8 * (s & 3),
-                            sdesc(kq + (s >> 3) * kChBox + (s & 3) * 16 * 128), idn, (s & 7) > 0);
-                umma_commit(&sh.d4_full);
-                umma_commit(&sh.kq_empty[c % kChStages]);
-                tri(tmem + kTmOp, tmem + kTmU, aP);
-                umma_commit(&sh.o_full);
-            }
-            __syncwarp();
-        }
-        if (lane == 0) {
-            umma_commit(&sh.drain);                            // every issued MMA done before the dealloc
-            mb_wait(&sh.drain, 0);
+#pragma unroll
+            for (int s = 0; s < 16; s++)                       // K^T U into the state's sums, a half of k at a time
+                umma_ts_warp(kTmS + 64 * (s >> 3), kTmRU + 32 * ((s >> 2) & 1) + 8 * (s & 3),
+                             kq + (((s >> 3) * kChBox + (s & 3) * 16 * 128) >> 4), idn, (s & 7) > 0);
+            umma_commit_warp(&sh.d4_full);
+            tri(kTmOp, kTmU, aP + (c & 1) * 2 * kChTile);
+            umma_commit_warp(&sh.o_full);
         }
         __syncwarp();
+        umma_commit_warp(&sh.drain);                           // every issued MMA done before the dealloc
+        mb_wait_warp(&sh.drain, 0);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == kChWarpMma)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(512));
 }
 
 }  // namespace
@@ -748,19 +809,24 @@ size_t delta_workspace(const k3moe_delta_config &dc, int n_seq, int T)
 
 static cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
 {
-    CUtensorMap mq{}, mk{};
+    CUtensorMap mq{}, mk{}, mv{};
     const uint64_t cols = (uint64_t)a.Hq * kD;
     if (!map16s(&mq, a.q, (uint64_t)a.T, cols, (uint64_t)a.q_stride, kC) ||
-        !map16s(&mk, a.k, (uint64_t)a.T, cols, (uint64_t)a.k_stride, kC))
+        !map16s(&mk, a.k, (uint64_t)a.T, cols, (uint64_t)a.k_stride, kC) ||
+        !map16s(&mv, a.v, (uint64_t)a.T, (uint64_t)a.H * kD, (uint64_t)a.v_stride, kC))
         return cudaErrorInvalidValue;
     static bool smem_set = false;
     if (!smem_set) {
+        // the shares of setmaxnreg are of the launch's registers: another count would wait forever
+        cudaFuncAttributes fa{};
+        if (cudaFuncGetAttributes(&fa, delta_chunk_kernel) != cudaSuccess || fa.numRegs != kChRegs)
+            return cudaErrorInvalidConfiguration;
         cudaFuncSetAttribute(delta_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChSmem);
         smem_set = true;
     }
     timing_begin("delta_chunk", s);
     const cudaError_t err =
-        launch_pdl(delta_chunk_kernel, dim3((unsigned)(a.n_seq * a.H)), dim3(kChThreads), kChSmem, s, a, mq, mk);
+        launch_pdl(delta_chunk_kernel, dim3((unsigned)(a.n_seq * a.H)), dim3(kChThreads), kChSmem, s, a, mq, mk, mv);
     count_launch();
     timing_end("delta_chunk", s);
     return err;
