@@ -212,16 +212,14 @@ __global__ void __launch_bounds__(kRecThreads) delta_recurrent_kernel(const Delt
 // product of two such as hi hi + hi mid + mid hi.  Sums are float, in tensor memory; the
 // state's carry S exp(G_C) + .. is a float in a register.
 //
-// Warps: 0-3 prepare T and P of the next chunk while the chain of this one runs; 4-11 are
-// the chain S -> R -> U -> S; 12-15 write O; 16 issues the loads and the MMAs.
+// Warps: 0-7 prepare T and P of the next chunk while the chain of this one runs; 8-23 are
+// the chain S -> R -> U -> S; 24-27 write O and compute the next but one chunk's scales; 28
+// issues the loads and the MMAs.  A single warp's dependent instructions issue every three
+// to five clocks, so each stage has as many warps as the registers allow (64 a thread).
 constexpr int kC = 64;                                        // tokens a chunk
-constexpr int kChPrep = 4, kChChain = 8, kChOut = 4;
+constexpr int kChPrep = 8, kChChain = 16, kChOut = 4;
 constexpr int kChWarpChain = kChPrep, kChWarpOut = kChWarpChain + kChChain, kChWarpMma = kChWarpOut + kChOut;
-constexpr int kChThreads = (kChWarpMma + 4) * 32;             // 640: five warpgroups, the last with one warp at work
-// Registers a thread: 96 at launch (640 x 96 of the 65,536); the chain, with 64 of them for
-// the state, takes what the writers of O and the issuing warp give up.
-constexpr int kChRegs = 96, kChRegsChain = 136, kChRegsOut = 64, kChRegsMma = 40;
-static_assert(kChRegs + 2 * kChRegsChain + kChRegsOut + kChRegsMma <= 5 * kChRegs, "shares within the launch's");
+constexpr int kChThreads = (kChWarpMma + 1) * 32;             // 928
 constexpr int kChStages = 3;
 constexpr int kChBox = 2 * kC * 128;                          // 64 channels of K then of Q: 16 KB
 constexpr int kChV = 2 * kChBox;                              // after both, V: two boxes of 64 columns
@@ -230,7 +228,7 @@ constexpr int kChTile = kC * 128;                             // one term of T o
 constexpr int kChLd = 68;                                     // row stride of the float scratch
 constexpr size_t kChSmem = 1024 + kChStages * kChStageBytes + 6 * kChTile + kC * kChLd * 4;   // T, two P, the scratch
 // tensor memory columns
-constexpr uint32_t kTmS = 0;      // S^T as an operand, [half of k][hi, mid][32]; the new S's sums over it
+constexpr uint32_t kTmS = 0;      // S^T as an operand, [quarter of k][hi, mid][16]; the new S's sums over it
 constexpr uint32_t kTmR = 128;    // K S, then T R
 constexpr uint32_t kTmOq = 192;   // Q S
 constexpr uint32_t kTmOp = 256;   // P U
@@ -238,15 +236,21 @@ constexpr uint32_t kTmRU = 320;   // R, then U scaled for the state, as an opera
 constexpr uint32_t kTmU = 384;    // U as an operand [hi, mid][32]
 constexpr uint32_t kTmKK = 448;   // K K^T (lanes 0-63) and Q K^T (lanes 64-127) of the next chunk
 
+constexpr int kChScales = 4;
 struct ChunkShared {
     uint64_t kq_full[kChStages];
-    uint64_t kk_full, kk_free, sc_ready[2], tp_ready, s_ready, d1_full, r_ready, d2_full, u_ready, d4_full, o_full, o_free,
+    uint64_t kk_full, kk_free, sc_ready[kChScales], tp_ready, s_ready, d1_full, r_ready, d2_full, u_ready, d4_full, o_full, o_free,
         drain;
     uint32_t tmem;
     volatile int bail;
-    alignas(16) float G[kC], rk[kC], beta[kC];
-    alignas(16) float kr[2][kC], kd[2][kC], qr[2][kC];        // per chunk parity: the scales of the preparation
-    float dec[2];
+    // a chunk's scales (of the chunk's number modulo kChScales), with G_t the decay's sum and
+    // r = 1 / |k_t| (1 without qk_norm):
+    //   g2 = log2(e) G_t, gk = g2 - log2 r, kb = beta_t r, kr = r exp(G_t), kd = r exp(G_C - G_t),
+    //   qn = scale / |q_t|, qr = qn exp(G_t), dec = exp(G_C); 0 (gk: infinity) past the end
+    struct Scales {
+        alignas(16) float g2[kC], gk[kC], beta[kC], kb[kC], kr[kC], kd[kC], qn[kC], qr[kC];
+        float dec, pad[3];
+    } sc[kChScales];
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -277,25 +281,47 @@ __device__ __forceinline__ void put_terms(uint8_t *tile, int t, int c8, const fl
     *reinterpret_cast<uint4 *>(p) = make_uint4(h[0], h[1], h[2], h[3]);
     *reinterpret_cast<uint4 *>(p + kChTile) = make_uint4(m[0], m[1], m[2], m[3]);
 }
-__device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kChPrep * 32) : "memory"); }
+// A whole warp's wait, asleep in the barrier's own wait (up to 20 us a time) rather than
+// polling beside the warps at work; bounded as mb_wait.
+__device__ __forceinline__ bool mb_wait_asleep(uint64_t *b, uint32_t parity)
+{
+    const uint32_t a = saddr(b);
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(a), "r"(parity), "r"(20000u)
+            : "memory");
+        const bool ok = __all_sync(0xffffffffu, done != 0);
+        if (ok) return true;
+        if (clock64() - t0 > kTcWaitCyc) return false;
+    }
+}
+__device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kChPrep * 32) : "memory"); }
 
 // A <- (I + A)^-1 of a strictly lower triangular 64 x 64 A (rows kChLd floats apart), in
 // place and by blocks: the 16 x 16 diagonal blocks by substitution, then twice
-// [X11 0; -X22 A21 X11, X22].  Above the diagonal blocks is scratch.  128 threads.
+// [X11 0; -X22 A21 X11, X22].  Above the diagonal blocks is scratch.  256 threads.
 __device__ __forceinline__ void invert64(float *A, int tid)
 {
     const int warp = tid >> 5, lane = tid & 31;
-    {   // column `lane` of diagonal block `warp` (lanes from 16 on repeat the others' work)
-        float *a = A + (16 * warp) * kChLd + 16 * warp;
+    if (warp < 4) {   // column `lane` of diagonal block `warp` (lanes from 16 on repeat the others' work)
+        float *a = A + (16 * warp) * (kChLd + 1);
         float x[16];
         const int col = lane & 15;
 #pragma unroll
         for (int t = 0; t < 16; t++) {
-            float r[16], p[4] = {t == col ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
+            float p[4] = {t == col ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < t; i += 4) *reinterpret_cast<float4 *>(&r[i]) = *reinterpret_cast<const float4 *>(&a[t * kChLd + i]);
+            for (int i4 = 0; i4 < t; i4 += 4) {
+                const float4 r4 = *reinterpret_cast<const float4 *>(&a[t * kChLd + i4]);
+                const float r[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll
-            for (int i = 0; i < t; i++) p[i & 3] = fmaf(-r[i], x[i], p[i & 3]);
+                for (int i = i4; i < t && i < i4 + 4; i++) p[i & 3] = fmaf(-r[i & 3], x[i], p[i & 3]);
+            }
             x[t] = (p[0] + p[1]) + (p[2] + p[3]);
         }
         __syncwarp();
@@ -304,63 +330,61 @@ __device__ __forceinline__ void invert64(float *A, int tid)
             for (int t = 0; t < 16; t++) a[t * kChLd + col] = x[t];       // zero above the diagonal
     }
     prep_sync();
-    {   // 16 -> 32: a pair of blocks for each half of the threads, four of its 256 outputs a thread
-        float *a = A + 32 * (tid >> 6) * (kChLd + 1);
-        const int r = (tid & 63) >> 2, c = (tid & 3) * 4;
-        float w[4] = {};
+    {   // 16 -> 32: a pair of blocks for each half of the threads, two of its 256 outputs a thread
+        float *a = A + 32 * (tid >> 7) * (kChLd + 1);
+        const int r = (tid & 127) >> 3, c = (tid & 7) * 2;
+        float w0 = 0.0f, w1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; i++) {
             const float av = a[(16 + r) * kChLd + i];
-            const float4 xv = *reinterpret_cast<const float4 *>(&a[i * kChLd + c]);
-            w[0] = fmaf(av, xv.x, w[0]);
-            w[1] = fmaf(av, xv.y, w[1]);
-            w[2] = fmaf(av, xv.z, w[2]);
-            w[3] = fmaf(av, xv.w, w[3]);
+            const float2 xv = *reinterpret_cast<const float2 *>(&a[i * kChLd + c]);
+            w0 = fmaf(av, xv.x, w0);
+            w1 = fmaf(av, xv.y, w1);
         }
-        *reinterpret_cast<float4 *>(&a[r * kChLd + 16 + c]) = make_float4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<float2 *>(&a[r * kChLd + 16 + c]) = make_float2(w0, w1);
         prep_sync();
-        float x[4] = {};
+        float x0 = 0.0f, x1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; i++) {
             const float xr = a[(16 + r) * kChLd + 16 + i];
-            const float4 wv = *reinterpret_cast<const float4 *>(&a[i * kChLd + 16 + c]);
-            x[0] = fmaf(-xr, wv.x, x[0]);
-            x[1] = fmaf(-xr, wv.y, x[1]);
-            x[2] = fmaf(-xr, wv.z, x[2]);
-            x[3] = fmaf(-xr, wv.w, x[3]);
+            const float2 wv = *reinterpret_cast<const float2 *>(&a[i * kChLd + 16 + c]);
+            x0 = fmaf(-xr, wv.x, x0);
+            x1 = fmaf(-xr, wv.y, x1);
         }
-        *reinterpret_cast<float4 *>(&a[(16 + r) * kChLd + c]) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float2 *>(&a[(16 + r) * kChLd + c]) = make_float2(x0, x1);
         prep_sync();
-        *reinterpret_cast<float4 *>(&a[r * kChLd + 16 + c]) = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float2 *>(&a[r * kChLd + 16 + c]) = make_float2(0.f, 0.f);
     }
     prep_sync();
-    {   // 32 -> 64: two rows and four columns a thread
-        const int r = (tid >> 3) * 2, c = (tid & 7) * 4;
-        float w[2][4] = {};
-#pragma unroll 16
-        for (int i = 0; i < 32; i++) {
-            const float a0 = A[(32 + r) * kChLd + i], a1 = A[(33 + r) * kChLd + i];
-            const float4 xv = *reinterpret_cast<const float4 *>(&A[i * kChLd + c]);
-            w[0][0] = fmaf(a0, xv.x, w[0][0]); w[0][1] = fmaf(a0, xv.y, w[0][1]);
-            w[0][2] = fmaf(a0, xv.z, w[0][2]); w[0][3] = fmaf(a0, xv.w, w[0][3]);
-            w[1][0] = fmaf(a1, xv.x, w[1][0]); w[1][1] = fmaf(a1, xv.y, w[1][1]);
-            w[1][2] = fmaf(a1, xv.z, w[1][2]); w[1][3] = fmaf(a1, xv.w, w[1][3]);
+    {   // 32 -> 64: four outputs of a row a thread
+        const int r = tid >> 3, c = (tid & 7) * 4;
+        float w[4] = {};
+#pragma unroll 8
+        for (int i = 0; i < 32; i += 4) {
+            const float4 a4 = *reinterpret_cast<const float4 *>(&A[(32 + r) * kChLd + i]);
+            const float av[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float4 xv = *reinterpret_cast<const float4 *>(&A[(i + k) * kChLd + c]);
+                w[0] = fmaf(av[k], xv.x, w[0]); w[1] = fmaf(av[k], xv.y, w[1]);
+                w[2] = fmaf(av[k], xv.z, w[2]); w[3] = fmaf(av[k], xv.w, w[3]);
+            }
         }
-        *reinterpret_cast<float4 *>(&A[r * kChLd + 32 + c]) = make_float4(w[0][0], w[0][1], w[0][2], w[0][3]);
-        *reinterpret_cast<float4 *>(&A[(r + 1) * kChLd + 32 + c]) = make_float4(w[1][0], w[1][1], w[1][2], w[1][3]);
+        *reinterpret_cast<float4 *>(&A[r * kChLd + 32 + c]) = make_float4(w[0], w[1], w[2], w[3]);
         prep_sync();
-        float x[2][4] = {};
-#pragma unroll 16
-        for (int i = 0; i < 32; i++) {
-            const float x0 = A[(32 + r) * kChLd + 32 + i], x1 = A[(33 + r) * kChLd + 32 + i];
-            const float4 wv = *reinterpret_cast<const float4 *>(&A[i * kChLd + 32 + c]);
-            x[0][0] = fmaf(-x0, wv.x, x[0][0]); x[0][1] = fmaf(-x0, wv.y, x[0][1]);
-            x[0][2] = fmaf(-x0, wv.z, x[0][2]); x[0][3] = fmaf(-x0, wv.w, x[0][3]);
-            x[1][0] = fmaf(-x1, wv.x, x[1][0]); x[1][1] = fmaf(-x1, wv.y, x[1][1]);
-            x[1][2] = fmaf(-x1, wv.z, x[1][2]); x[1][3] = fmaf(-x1, wv.w, x[1][3]);
+        float x[4] = {};
+#pragma unroll 8
+        for (int i = 0; i < 32; i += 4) {
+            const float4 a4 = *reinterpret_cast<const float4 *>(&A[(32 + r) * kChLd + 32 + i]);
+            const float av[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float4 wv = *reinterpret_cast<const float4 *>(&A[(i + k) * kChLd + 32 + c]);
+                x[0] = fmaf(-av[k], wv.x, x[0]); x[1] = fmaf(-av[k], wv.y, x[1]);
+                x[2] = fmaf(-av[k], wv.z, x[2]); x[3] = fmaf(-av[k], wv.w, x[3]);
+            }
         }
-        *reinterpret_cast<float4 *>(&A[(32 + r) * kChLd + c]) = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
-        *reinterpret_cast<float4 *>(&A[(33 + r) * kChLd + c]) = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
+        *reinterpret_cast<float4 *>(&A[(32 + r) * kChLd + c]) = make_float4(x[0], x[1], x[2], x[3]);
     }
     prep_sync();
 }
@@ -396,7 +420,7 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
         for (int s = 0; s < kChStages; s++) mb_init(&sh.kq_full[s], 1);
         mb_init(&sh.kk_full, 1);
         mb_init(&sh.kk_free, kChPrep);
-        for (int p = 0; p < 2; p++) mb_init(&sh.sc_ready[p], kChPrep);
+        for (int p = 0; p < kChScales; p++) mb_init(&sh.sc_ready[p], kChOut);
         mb_init(&sh.tp_ready, kChPrep);
         mb_init(&sh.s_ready, kChChain);
         mb_init(&sh.d1_full, 1);
@@ -421,7 +445,7 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
     constexpr uint32_t tmem = 0;                              // all 512 columns: the allocation starts at the first
     // A wait of a whole warp; false (with the status bit) when it gave up or another did.
     auto wait = [&](uint64_t &b, int phase) {
-        const bool ok = mb_wait_warp(&b, (uint32_t)phase & 1u);
+        const bool ok = mb_wait_asleep(&b, (uint32_t)phase & 1u);
         if (!ok) {
             set_status(status, K3MOE_DEV_TIMEOUT);
             sh.bail = 1;
@@ -435,91 +459,30 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
         if (lane == 0) mb_arrive(&b);
     };
 
-    if (warp >= kChWarpChain && warp < kChWarpOut)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChRegsChain));
-    else if (warp >= kChWarpOut && warp < kChWarpMma)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChRegsOut));
-    else if (warp >= kChWarpMma)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChRegsMma));
-
     if (warp < kChPrep) {
-        // ---------------- T and P of chunk c, and its per-token scales:
-        //   kr = exp(G_t) / |k_t|, kd = exp(G_C - G_t) / |k_t|, qr = scale exp(G_t) / |q_t|, dec = exp(G_C)
-        const int row = threadIdx.x, t = row & (kC - 1);      // lanes 0-63: A's row t, 64-127: P's
+        // ---------------- T and P of chunk c: lanes 0-63 of tensor memory hold A's rows, 64-127
+        // P's; a warp takes 32 rows of one of the two, half of their columns
+        const int row = 32 * (warp & 3) + lane, t = row & (kC - 1), i00 = 32 * (warp >> 2);
         const bool is_a = row < kC;
         for (int c = 0; c < nc; c++) {
-            const int n = min(kC, len - kC * c), par = c & 1;
-            const size_t tok = (size_t)(first + kC * c);
-            float g0 = lane < n ? a.g[(tok + lane) * a.H + h] : 0.0f;
-            float g1 = lane + 32 < n ? a.g[(tok + lane + 32) * a.H + h] : 0.0f;
-            const float bt = t < n ? a.beta[(tok + t) * a.H + h] : 0.0f;
-            g0 = g0 < -200.0f ? -200.0f : g0;
-            g1 = g1 < -200.0f ? -200.0f : g1;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float p0 = __shfl_up_sync(0xffffffffu, g0, o), p1 = __shfl_up_sync(0xffffffffu, g1, o);
-                if (lane >= o) { g0 += p0; g1 += p1; }
-            }
-            g1 += __shfl_sync(0xffffffffu, g0, 31);
-            const float Gt = (warp & 1) ? g1 : g0, GC = __shfl_sync(0xffffffffu, g1, 31);
-
-            const int st = c % kChStages;
-            if (!wait(sh.kq_full[st], c / kChStages)) break;
-            uint8_t *kq = sm + (size_t)st * kChStageBytes;
-            float norm = 1.0f;
-            if (a.qk_norm) {
-                float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 16; j++) {                // chunk order is the swizzle's: a sum does not mind
-                    const uint4 w = *reinterpret_cast<const uint4 *>(kq + (j >> 3) * kChBox + row * 128 + (((j & 7) ^ (row & 7)) << 4));
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int r = 0; r < 4; r++) {
-                        const float lo = __uint_as_float(u[r] << 16), hi = __uint_as_float(u[r] & 0xFFFF0000u);
-                        s0 = fmaf(lo, lo, s0);
-                        s1 = fmaf(hi, hi, s1);
-                    }
-                }
-                norm = 1.0f / sqrtf(s0 + s1 + a.eps);
-            }
-            if (t >= n) {
-                norm = 0.0f;
-                if (is_a)                                     // the rows past the sequence's end take no part in K^T U
-#pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        *reinterpret_cast<uint4 *>(kq + (j >> 3) * kChBox + row * 128 + ((j & 7) << 4)) = make_uint4(0, 0, 0, 0);
-            }
-            if (!wait(sh.kk_full, c)) break;                  // which also says that chunk c - 2's scales and P are used
-            if (is_a) {
-                sh.G[t] = Gt * kLog2e;
-                sh.rk[t] = norm;
-                sh.beta[t] = bt;
-                sh.kr[par][t] = norm * expf(Gt);
-                sh.kd[par][t] = norm * expf(GC - Gt);
-                if (t == 0) sh.dec[par] = expf(GC);
-            } else {
-                sh.qr[par][t] = a.scale * norm * expf(Gt);
-            }
-            __syncwarp();
-            if (lane == 0) mb_arrive(&sh.sc_ready[par]);
-            prep_sync();
-            const float rowf = is_a ? bt * norm : a.scale * norm, G2 = Gt * kLog2e;
+            const int n = min(kC, len - kC * c);
+            if (!wait(sh.sc_ready[c % kChScales], c / kChScales) || !wait(sh.kk_full, c)) break;
+            tc_fence_after();                                 // chunk c - 2's P is used: the MMAs' issue saw to it
+            const ChunkShared::Scales &sc = sh.sc[c % kChScales];
+            const float rowf = is_a ? sc.kb[t] : sc.qn[t], g2 = sc.g2[t];
             const int last = t < n ? (is_a ? t - 1 : t) : -1;          // the row's last token
-            const int width = 32 * (warp & 1) + 32;           // no row of this warp reaches further
-            tc_fence_after();
+            uint8_t *tPc = tP + (c & 1) * 2 * kChTile;
 #pragma unroll 1
-            for (int i0 = 0; i0 < (is_a ? width : kC); i0 += 16) {
+            for (int i0 = i00; i0 < i00 + 32; i0 += 16) {
                 float v[16];
-                tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + kTmKK + i0, v);
+                tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kTmKK + i0, v);
 #pragma unroll
                 for (int j4 = 0; j4 < 4; j4++) {
-                    const float4 gi = *reinterpret_cast<const float4 *>(&sh.G[i0 + 4 * j4]);
-                    const float4 ri = *reinterpret_cast<const float4 *>(&sh.rk[i0 + 4 * j4]);
-                    const float g[4] = {gi.x, gi.y, gi.z, gi.w}, r[4] = {ri.x, ri.y, ri.z, ri.w};
+                    const float4 gk4 = *reinterpret_cast<const float4 *>(&sc.gk[i0 + 4 * j4]);
+                    const float gk[4] = {gk4.x, gk4.y, gk4.z, gk4.w};
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        const float e = exp2_approx(fminf(G2 - g[j], 0.0f));
-                        const float x = v[4 * j4 + j] * r[j] * (rowf * e);
+                        const float x = v[4 * j4 + j] * (rowf * exp2_approx(g2 - gk[j]));
                         v[4 * j4 + j] = i0 + 4 * j4 + j <= last ? x : 0.0f;
                     }
                 }
@@ -529,8 +492,8 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
                         *reinterpret_cast<float4 *>(&As[t * kChLd + i0 + 4 * j]) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 } else {
                     const float(*v8)[8] = reinterpret_cast<const float(*)[8]>(v);
-                    put_terms(tP + par * 2 * kChTile, t, i0 / 8, v8[0]);
-                    put_terms(tP + par * 2 * kChTile, t, i0 / 8 + 1, v8[1]);
+                    put_terms(tPc, t, i0 / 8, v8[0]);
+                    put_terms(tPc, t, i0 / 8 + 1, v8[1]);
                 }
             }
             arrive(sh.kk_free);
@@ -538,14 +501,14 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
             invert64(As, threadIdx.x);
             if (c >= 1 && !wait(sh.d2_full, c - 1)) break;    // T of chunk c - 1 is used
             {
-                const int r = threadIdx.x >> 1, c0 = (threadIdx.x & 1) * 32;
+                const int r = threadIdx.x >> 2, c0 = (threadIdx.x & 3) * 16;
 #pragma unroll
-                for (int j8 = 0; j8 < 4; j8++) {
+                for (int j8 = 0; j8 < 2; j8++) {
                     float x[8], b[8];
 #pragma unroll
                     for (int j = 0; j < 8; j += 4) {
                         *reinterpret_cast<float4 *>(&x[j]) = *reinterpret_cast<const float4 *>(&As[r * kChLd + c0 + 8 * j8 + j]);
-                        *reinterpret_cast<float4 *>(&b[j]) = *reinterpret_cast<const float4 *>(&sh.beta[c0 + 8 * j8 + j]);
+                        *reinterpret_cast<float4 *>(&b[j]) = *reinterpret_cast<const float4 *>(&sc.beta[c0 + 8 * j8 + j]);
                     }
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
@@ -558,64 +521,63 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mb_arrive(&sh.tp_ready);
-            prep_sync();                                      // the scratch and G, rk, beta are free again
+            prep_sync();                                      // the scratch is free again
         }
     } else if (warp < kChWarpOut) {
-        // ---------------- the chain: value column v, half of the channels or tokens
-        const int q = warp & 3, half = (warp - kChWarpChain) >> 2, v = 32 * q + lane;
+        // ---------------- the chain: value column v, a quarter of the channels or tokens
+        const int q = warp & 3, part = (warp - kChWarpChain) >> 2, v = 32 * q + lane;
         const uint32_t la = tmem + ((uint32_t)(32 * q) << 16);
-        float S[64];
+        float S[32];
 #pragma unroll
-        for (int j = 0; j < 64; j++)
-            S[j] = a.state_in ? a.state_in[sbase + (size_t)(64 * half + j) * kD + v] : 0.0f;
+        for (int j = 0; j < 32; j++)
+            S[j] = a.state_in ? a.state_in[sbase + (size_t)(32 * part + j) * kD + v] : 0.0f;
         auto put_state = [&]() {
 #pragma unroll
             for (int b = 0; b < 4; b++) {
-                uint32_t hi[8], mid[8];
+                uint32_t hi[4], mid[4];
 #pragma unroll
-                for (int j = 0; j < 8; j++) split2(S[16 * b + 2 * j], S[16 * b + 2 * j + 1], &hi[j], &mid[j]);
-                tmem_st8(la + kTmS + 64 * half + 8 * b, hi);
-                tmem_st8(la + kTmS + 64 * half + 32 + 8 * b, mid);
+                for (int j = 0; j < 4; j++) split2(S[8 * b + 2 * j], S[8 * b + 2 * j + 1], &hi[j], &mid[j]);
+                tmem_st4(la + kTmS + 32 * part + 4 * b, hi);
+                tmem_st4(la + kTmS + 32 * part + 16 + 4 * b, mid);
             }
             tmem_wait_st();
             arrive(sh.s_ready);
         };
         put_state();
         for (int c = 0; c < nc; c++) {
-            const int n = min(kC, len - kC * c), par = c & 1, t0 = 32 * half;
+            const int n = min(kC, len - kC * c), t0 = 16 * part;
             const int st = c % kChStages;
+            const ChunkShared::Scales &sc = sh.sc[c % kChScales];
             // V[t][v] in its swizzled tile
-            const uint8_t *vt = sm + (size_t)st * kChStageBytes + kChV + (q >> 1) * kC * 128 + (v & 7) * 2;
+            const uint8_t *vt = sm + (size_t)st * kChStageBytes + kChV + (q >> 1) * kC * 128 + t0 * 128 + (v & 7) * 2;
             const uint32_t v8 = (uint32_t)(v >> 3) & 7u;
             if (!wait(sh.kq_full[st], c / kChStages)) break;
-            uint32_t vv[16];                                      // two tokens a word
+            uint32_t vv[8];                                       // two tokens a word
 #pragma unroll
-            for (int j = 0; j < 16; j++) {
-                const uint32_t t = t0 + 2 * j;
-                const uint32_t x = *reinterpret_cast<const uint16_t *>(vt + t * 128 + ((v8 ^ ((2 * j) & 7u)) << 4));
-                const uint32_t y = *reinterpret_cast<const uint16_t *>(vt + t * 128 + 128 + ((v8 ^ ((2 * j + 1) & 7u)) << 4));
+            for (int j = 0; j < 8; j++) {
+                const uint32_t x = *reinterpret_cast<const uint16_t *>(vt + 2 * j * 128 + ((v8 ^ ((2 * j) & 7u)) << 4));
+                const uint32_t y = *reinterpret_cast<const uint16_t *>(vt + 2 * j * 128 + 128 + ((v8 ^ ((2 * j + 1) & 7u)) << 4));
                 vv[j] = x | (y << 16);
             }
-            if (!wait(sh.sc_ready[par], c >> 1) || !wait(sh.d1_full, c)) break;
+            if (!wait(sh.sc_ready[c % kChScales], c / kChScales) || !wait(sh.d1_full, c)) break;
             tc_fence_after();
             {
-                uint32_t d[32];
-                tmem_ld16_nowait(la + kTmR + t0, *reinterpret_cast<uint32_t(*)[16]>(&d[0]));
-                tmem_ld16_nowait(la + kTmR + t0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&d[16]));
+                uint32_t d[16];
+                tmem_ld16_nowait(la + kTmR + t0, d);
                 tmem_wait_ld();
 #pragma unroll
-                for (int b = 0; b < 4; b++) {
+                for (int b = 0; b < 2; b++) {
                     uint32_t hi[4], mid[4];
 #pragma unroll
                     for (int j2 = 0; j2 < 4; j2++) {
                         const int j = 8 * b + 2 * j2;
-                        const float2 kr = *reinterpret_cast<const float2 *>(&sh.kr[par][t0 + j]);
+                        const float2 kr = *reinterpret_cast<const float2 *>(&sc.kr[t0 + j]);
                         const float x = fmaf(-kr.x, __uint_as_float(d[j]), __uint_as_float(vv[j >> 1] << 16));
                         const float y = fmaf(-kr.y, __uint_as_float(d[j + 1]), __uint_as_float(vv[j >> 1] & 0xFFFF0000u));
                         split2(t0 + j < n ? x : 0.0f, t0 + j + 1 < n ? y : 0.0f, &hi[j2], &mid[j2]);
                     }
-                    tmem_st4(la + kTmRU + 16 * half + 4 * b, hi);
-                    tmem_st4(la + kTmRU + 32 + 16 * half + 4 * b, mid);
+                    tmem_st4(la + kTmRU + 8 * part + 4 * b, hi);
+                    tmem_st4(la + kTmRU + 32 + 8 * part + 4 * b, mid);
                 }
             }
             tmem_wait_st();
@@ -623,53 +585,112 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
             if (!wait(sh.d2_full, c)) break;
             tc_fence_after();
             {
-                uint32_t d[32];
-                tmem_ld16_nowait(la + kTmR + t0, *reinterpret_cast<uint32_t(*)[16]>(&d[0]));
-                tmem_ld16_nowait(la + kTmR + t0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&d[16]));
+                uint32_t d[16];
+                tmem_ld16_nowait(la + kTmR + t0, d);
                 tmem_wait_ld();
 #pragma unroll
-                for (int b = 0; b < 4; b++) {
+                for (int b = 0; b < 2; b++) {
                     uint32_t hi[4], mid[4];
 #pragma unroll
                     for (int j2 = 0; j2 < 4; j2++) {
                         const int j = 8 * b + 2 * j2;
-                        const float2 kd = *reinterpret_cast<const float2 *>(&sh.kd[par][t0 + j]);
+                        const float2 kd = *reinterpret_cast<const float2 *>(&sc.kd[t0 + j]);
                         split2(__uint_as_float(d[j]) * kd.x, __uint_as_float(d[j + 1]) * kd.y, &hi[j2], &mid[j2]);
                     }
-                    tmem_st4(la + kTmRU + 16 * half + 4 * b, hi);
-                    tmem_st4(la + kTmRU + 32 + 16 * half + 4 * b, mid);
+                    tmem_st4(la + kTmRU + 8 * part + 4 * b, hi);
+                    tmem_st4(la + kTmRU + 32 + 8 * part + 4 * b, mid);
 #pragma unroll
                     for (int j2 = 0; j2 < 4; j2++)
                         split2(__uint_as_float(d[8 * b + 2 * j2]), __uint_as_float(d[8 * b + 2 * j2 + 1]), &hi[j2], &mid[j2]);
-                    tmem_st4(la + kTmU + 16 * half + 4 * b, hi);
-                    tmem_st4(la + kTmU + 32 + 16 * half + 4 * b, mid);
+                    tmem_st4(la + kTmU + 8 * part + 4 * b, hi);
+                    tmem_st4(la + kTmU + 32 + 8 * part + 4 * b, mid);
                 }
             }
             tmem_wait_st();
             arrive(sh.u_ready);
+            const float dec = sc.dec;
             if (!wait(sh.d4_full, c)) break;
             tc_fence_after();
-            const float dec = sh.dec[par];
 #pragma unroll
             for (int b = 0; b < 2; b++) {
-                uint32_t d[32];
-                tmem_ld16_nowait(la + kTmS + 64 * half + 32 * b, *reinterpret_cast<uint32_t(*)[16]>(&d[0]));
-                tmem_ld16_nowait(la + kTmS + 64 * half + 32 * b + 16, *reinterpret_cast<uint32_t(*)[16]>(&d[16]));
+                uint32_t d[16];
+                tmem_ld16_nowait(la + kTmS + 32 * part + 16 * b, d);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; j++) S[32 * b + j] = fmaf(dec, S[32 * b + j], __uint_as_float(d[j]));
+                for (int j = 0; j < 16; j++) S[16 * b + j] = fmaf(dec, S[16 * b + j], __uint_as_float(d[j]));
             }
             if (c + 1 < nc) put_state();
         }
         if (!sh.bail)
 #pragma unroll
-            for (int j = 0; j < 64; j++) a.state_out[sbase + (size_t)(64 * half + j) * kD + v] = S[j];
+            for (int j = 0; j < 32; j++) a.state_out[sbase + (size_t)(32 * part + j) * kD + v] = S[j];
     } else if (warp < kChWarpMma) {
-        // ---------------- O: value column v, every token of the chunk
+        // ---------------- O: value column v, every token of the chunk; and the scales
         const int q = warp & 3, v = 32 * q + lane;
         const uint32_t la = tmem + ((uint32_t)(32 * q) << 16);
-        for (int c = 0; c < nc; c++) {
-            const int n = min(kC, len - kC * c), par = c & 1;
+        // The scales of chunk c, a thread a row of K (0-63) or Q (64-127).
+        auto scales = [&](int c) {
+            const int n = min(kC, len - kC * c), t = v & (kC - 1), st = c % kChStages;
+            const bool is_k = v < kC;
+            const size_t tok = (size_t)(first + kC * c);
+            float g0 = lane < n ? a.g[(tok + lane) * a.H + h] : 0.0f;
+            float g1 = lane + 32 < n ? a.g[(tok + lane + 32) * a.H + h] : 0.0f;
+            const float bt = t < n ? a.beta[(tok + t) * a.H + h] : 0.0f;
+            g0 = g0 < -200.0f ? -200.0f : g0;
+            g1 = g1 < -200.0f ? -200.0f : g1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float p0 = __shfl_up_sync(0xffffffffu, g0, o), p1 = __shfl_up_sync(0xffffffffu, g1, o);
+                if (lane >= o) { g0 += p0; g1 += p1; }
+            }
+            g1 += __shfl_sync(0xffffffffu, g0, 31);
+            const float G = (q & 1) ? g1 : g0, GC = __shfl_sync(0xffffffffu, g1, 31);
+            if (!wait(sh.kq_full[st], c / kChStages)) return false;
+            uint8_t *x = sm + (size_t)st * kChStageBytes + v * 128;
+            float norm = 1.0f;
+            if (a.qk_norm) {
+                float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 16; j++) {                // chunk order is the swizzle's: a sum does not mind
+                    const uint4 w = *reinterpret_cast<const uint4 *>(x + (j >> 3) * kChBox + (((j & 7) ^ (v & 7)) << 4));
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        const float lo = __uint_as_float(u[r] << 16), hi = __uint_as_float(u[r] & 0xFFFF0000u);
+                        s0 = fmaf(lo, lo, s0);
+                        s1 = fmaf(hi, hi, s1);
+                    }
+                }
+                norm = 1.0f / sqrtf(s0 + s1 + a.eps);
+            }
+            const bool in = t < n;
+            if (!in && is_k)                                  // the rows past the sequence's end take no part in K^T U
+#pragma unroll
+                for (int j = 0; j < 16; j++)
+                    *reinterpret_cast<uint4 *>(x + (j >> 3) * kChBox + ((j & 7) << 4)) = make_uint4(0, 0, 0, 0);
+            ChunkShared::Scales &sc = sh.sc[c % kChScales];
+            const float eG = expf(G);
+            if (is_k) {
+                sc.g2[t] = G * kLog2e;
+                sc.gk[t] = in ? G * kLog2e - log2f(norm) : __int_as_float(0x7f800000);
+                sc.beta[t] = bt;
+                sc.kb[t] = in ? bt * norm : 0.0f;
+                sc.kr[t] = in ? norm * eG : 0.0f;
+                sc.kd[t] = in ? norm * expf(GC - G) : 0.0f;
+                if (t == 0) sc.dec = expf(GC);
+            } else {
+                sc.qn[t] = in ? a.scale * norm : 0.0f;
+                sc.qr[t] = in ? a.scale * norm * eG : 0.0f;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mb_arrive(&sh.sc_ready[c % kChScales]);
+            return true;
+        };
+        bool ok = scales(0) && (nc < 2 || scales(1));
+        for (int c = 0; c < nc && ok; c++) {
+            const int n = min(kC, len - kC * c);
+            const ChunkShared::Scales &sc = sh.sc[c % kChScales];
             if (!wait(sh.o_full, c)) break;
             tc_fence_after();
             // neighbouring lanes trade a token each: two columns of one token a store
@@ -677,15 +698,14 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
             uint32_t *o = reinterpret_cast<uint32_t *>(a.out + ((size_t)(first + kC * c + mine) * a.H + h) * kD + (v & ~1));
             const size_t step = (size_t)a.H * kD;             // words of two tokens
 #pragma unroll 1
-            for (int b = 0; b < 4; b++, o += 8 * step) {
-                uint32_t d[16], p[16];
-                tmem_ld16_nowait(la + kTmOq + 16 * b, d);
-                tmem_ld16_nowait(la + kTmOp + 16 * b, p);
+            for (int b = 0; b < 8; b++) {
+                uint32_t d[8], p[8];
+                tmem_ld8_nowait(la + kTmOq + 8 * b, d);
+                tmem_ld8_nowait(la + kTmOp + 8 * b, p);
                 tmem_wait_ld();
-                uint32_t *ob = o;
 #pragma unroll
-                for (int j4 = 0; j4 < 4; j4++) {
-                    const float4 qr = *reinterpret_cast<const float4 *>(&sh.qr[par][16 * b + 4 * j4]);
+                for (int j4 = 0; j4 < 2; j4++) {
+                    const float4 qr = *reinterpret_cast<const float4 *>(&sc.qr[8 * b + 4 * j4]);
                     const float r[4] = {qr.x, qr.y, qr.z, qr.w};
                     float x[4];
 #pragma unroll
@@ -694,12 +714,13 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
                     for (int j = 0; j < 2; j++) {
                         const float got = __shfl_xor_sync(0xffffffffu, mine ? x[2 * j] : x[2 * j + 1], 1);
                         const __nv_bfloat162 w = __floats2bfloat162_rn(mine ? got : x[2 * j], mine ? x[2 * j + 1] : got);
-                        if (16 * b + 4 * j4 + 2 * j + mine < n) *ob = *reinterpret_cast<const uint32_t *>(&w);
-                        ob += step;
+                        if (8 * b + 4 * j4 + 2 * j + mine < n) *o = *reinterpret_cast<const uint32_t *>(&w);
+                        o += step;
                     }
                 }
             }
             arrive(sh.o_free);
+            if (c + 2 < nc) ok = scales(c + 2);
         }
     } else if (warp == kChWarpMma) {
         // ---------------- loads and MMA issue
@@ -752,7 +773,7 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
             tc_fence_after();
 #pragma unroll
             for (int s = 0; s < 16; s++)                       // K S, hi and mid
-                umma_ts_warp(kTmR, kTmS + 64 * ((s >> 2) & 1) + 32 * (s >> 3) + 8 * (s & 3),
+                umma_ts_warp(kTmR, kTmS + 32 * ((s >> 1) & 3) + 16 * (s >> 3) + 8 * (s & 1),
                              kq + ((((s >> 2) & 1) * kChBox + (s & 3) * 32) >> 4), idk, s > 0);
             umma_commit_warp(&sh.d1_full);
             if (c + 1 < nc) {
@@ -774,7 +795,7 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
             tc_fence_after();
 #pragma unroll
             for (int s = 0; s < 16; s++)                       // Q S
-                umma_ts_warp(kTmOq, kTmS + 64 * ((s >> 2) & 1) + 32 * (s >> 3) + 8 * (s & 3),
+                umma_ts_warp(kTmOq, kTmS + 32 * ((s >> 1) & 3) + 16 * (s >> 3) + 8 * (s & 1),
                              kq + ((((s >> 2) & 1) * kChBox + kC * 128 + (s & 3) * 32) >> 4), idk, s > 0);
             if (!wait(sh.u_ready, c)) break;
             tc_fence_after();
@@ -817,10 +838,6 @@ static cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
         return cudaErrorInvalidValue;
     static bool smem_set = false;
     if (!smem_set) {
-        // the shares of setmaxnreg are of the launch's registers: another count would wait forever
-        cudaFuncAttributes fa{};
-        if (cudaFuncGetAttributes(&fa, delta_chunk_kernel) != cudaSuccess || fa.numRegs != kChRegs)
-            return cudaErrorInvalidConfiguration;
         cudaFuncSetAttribute(delta_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChSmem);
         smem_set = true;
     }
