@@ -194,68 +194,43 @@ __global__ void __launch_bounds__(kRecThreads) delta_recurrent_kernel(const Delt
 }
 
 // ---------------------------------------------------------------- chunks of 64 tokens
-// For a chunk, with G_t the decay's logarithm summed from its start to token t:
+// For a chunk, with G_t the decay's logarithm summed from its start to token t (a number, or
+// one a key channel; products over channels are then weighted channel by channel):
 //   A_ti = beta_t exp(G_t - G_i) k_t . k_i  (i < t),   P_ti = scale exp(G_t - G_i) q_t . k_i  (i <= t)
-//   T = (I + A)^-1 diag(beta),  U = T (V - diag(exp(G)) K S),
-//   O = scale diag(exp(G)) Q S + P U,   S <- exp(G_C) S + (diag(exp(G_C - G)) K)^T U.
+//   T = (I + A)^-1 diag(beta),  U = T (V - (exp(G) K) S),
+//   O = scale (exp(G) Q) S + P U,   S <- exp(G_C) S + (exp(G_C - G) K)^T U.
 // A unit lower triangular solve replaces 64 dependent steps, and all else is products on
-// the tensor cores.  Every exponent is a later token's sum minus an earlier one's, so no
-// factor exceeds one however strong the decay (a logarithm below -200 counts as -200: its
-// exponential is zero in float either way).
+// the tensor cores.  Two kernels: delta_prepare_kernel computes T and P of every chunk and
+// head at once (they do not need the state), delta_chunk_kernel walks a sequence and head
+// through its chunks.  T and P pass through the workspace, 20 KB a chunk and head: their
+// nonzero 16-column blocks only, in the layout the tensor core reads.
 //
-// One block per sequence and head walks its chunks; everything is transposed so that a
-// thread owns one value column v (a lane of tensor memory) and the state S^T [v][k] stays
-// with it: the A operands (S, R = V - .., U) go from registers to tensor memory and never
-// through shared memory, and the B operands (K and Q as they are, T, P) are shared tiles.
-// K and Q are exact in bf16; S, R, U, T and P enter as two bf16 terms each (hi + mid, 16
-// bits: 2^-18 of the element, where one term's 2^-9 would show in the float state), every
-// product of two such as hi hi + hi mid + mid hi.  Sums are float, in tensor memory; the
-// state's carry S exp(G_C) + .. is a float in a register.
-//
-// Warps: 0-7 prepare T and P of the next chunk while the chain of this one runs; 8-23 are
-// the chain S -> R -> U -> S; 24-27 write O and compute the next but one chunk's scales; 28
-// issues the loads and the MMAs.  A single warp's dependent instructions issue every three
-// to five clocks, so each stage has as many warps as the registers allow (64 a thread).
+// Numbers.  bf16 operands hold 8 bits, and one such rounding would show in the float state
+// (2^-9), so what is not a given bf16 tensor enters as two bf16 terms hi + mid (16 bits,
+// 2^-18 of the element), a product of two such as hi hi + hi mid + mid hi.  All sums are
+// float, in tensor memory; the state's carry exp(G_C) S + .. is float in registers.  A decay
+// below exp(-90) is zero in float beside 1: logarithms count as at least -90.
 constexpr int kC = 64;                                        // tokens a chunk
-constexpr int kChPrep = 8, kChChain = 16, kChOut = 4;
-constexpr int kChWarpChain = kChPrep, kChWarpOut = kChWarpChain + kChChain, kChWarpMma = kChWarpOut + kChOut;
-constexpr int kChThreads = (kChWarpMma + 1) * 32;             // 928
-constexpr int kChStages = 3;
-constexpr int kChBox = 2 * kC * 128;                          // 64 channels of K then of Q: 16 KB
-constexpr int kChV = 2 * kChBox;                              // after both, V: two boxes of 64 columns
-constexpr int kChStageBytes = kChV + kC * kD * 2;             // 48 KB
-constexpr int kChTile = kC * 128;                             // one term of T or P: 8 KB
-constexpr int kChLd = 68;                                     // row stride of the float scratch
-constexpr size_t kChSmem = 1024 + kChStages * kChStageBytes + 6 * kChTile + kC * kChLd * 4;   // T, two P, the scratch
-// tensor memory columns
-constexpr uint32_t kTmS = 0;      // S^T as an operand, [quarter of k][hi, mid][16]; the new S's sums over it
-constexpr uint32_t kTmR = 128;    // K S, then T R
-constexpr uint32_t kTmOq = 192;   // Q S
-constexpr uint32_t kTmOp = 256;   // P U
-constexpr uint32_t kTmRU = 320;   // R, then U scaled for the state, as an operand [hi, mid][32]
-constexpr uint32_t kTmU = 384;    // U as an operand [hi, mid][32]
-constexpr uint32_t kTmKK = 448;   // K K^T (lanes 0-63) and Q K^T (lanes 64-127) of the next chunk
-
-constexpr int kChScales = 4;
-struct ChunkShared {
-    uint64_t kq_full[kChStages];
-    uint64_t kk_full, kk_free, sc_ready[kChScales], tp_ready, s_ready, d1_full, r_ready, d2_full, u_ready, d4_full, o_full, o_free,
-        drain;
-    uint32_t tmem;
-    volatile int bail;
-    // a chunk's scales (of the chunk's number modulo kChScales), with G_t the decay's sum and
-    // r = 1 / |k_t| (1 without qk_norm):
-    //   g2 = log2(e) G_t, gk = g2 - log2 r, kb = beta_t r, kr = r exp(G_t), kd = r exp(G_C - G_t),
-    //   qn = scale / |q_t|, qr = qn exp(G_t), dec = exp(G_C); 0 (gk: infinity) past the end
-    struct Scales {
-        alignas(16) float g2[kC], gk[kC], beta[kC], kb[kC], kr[kC], kd[kC], qn[kC], qr[kC];
-        float dec, pad[3];
-    } sc[kChScales];
-};
-
 constexpr float kLog2e = 1.4426950408889634f;
-// 2^x, x <= 0, within 2 ulp; volatile so that a select of its result stays a select (as a
-// branch around it, each of a row's 64 would be waited for by itself).
+constexpr float kMinGate = -90.0f;
+constexpr int kTermBytes = 5120;                              // T or P, one term: 16-column blocks j of rows 16 j..63
+constexpr int kTpBytes = 4 * kTermBytes;                      // T hi, T mid, P hi, P mid
+constexpr int kRecFloats = 640;
+constexpr int kRecBytes = kTpBytes + kRecFloats * 4;          // a chunk and head's record in the workspace
+// The record's floats.  Decay per head: kr = exp(G_t) / |k_t|, kd = exp(G_C - G_t) / |k_t|,
+// qr = scale exp(G_t) / |q_t|, and exp(G_C); per channel: rk = 1 / |k_t|, qn = scale / |q_t|,
+// and log2 decays summed over each 16 tokens [4][D].  (Norms are 1 without qk_norm; all
+// are 0 past the sequence's end.)
+constexpr int kRecKr = 0, kRecKd = 64, kRecQr = 128, kRecDec = 192;
+constexpr int kRecRk = 0, kRecQn = 64, kRecSum = 128;
+__host__ __device__ constexpr int term_block(int j) { return 2048 * j - 256 * j * (j - 1); }
+
+// A sequence's chunk c has the workspace record (seq_start / 64 + seq + c, head): a sequence
+// of len tokens spans at most (end / 64 - start / 64) + 1 chunks, so records never overlap.
+__host__ __device__ inline long long chunk_records(long long n_seq, long long T) { return T / kC + n_seq; }
+
+// 2^x within 2 ulp; volatile so that a select of its result stays a select (as a branch
+// around it, each of a row's values would be waited for by itself).
 __device__ __forceinline__ float exp2_approx(float x)
 {
     float y;
@@ -270,16 +245,6 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t *hi, uint32_t 
     const __nv_bfloat162 m = __floats2bfloat162_rn(x - __uint_as_float(u << 16), y - __uint_as_float(u & 0xFFFF0000u));
     *hi = u;
     *mid = *reinterpret_cast<const uint32_t *>(&m);
-}
-// Eight values of row t, columns 8 c8.., as two terms of a swizzled tile.
-__device__ __forceinline__ void put_terms(uint8_t *tile, int t, int c8, const float (&x)[8])
-{
-    uint32_t h[4], m[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) split2(x[2 * j], x[2 * j + 1], &h[j], &m[j]);
-    uint8_t *p = tile + t * 128 + ((c8 ^ (t & 7)) << 4);
-    *reinterpret_cast<uint4 *>(p) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4 *>(p + kChTile) = make_uint4(m[0], m[1], m[2], m[3]);
 }
 // A whole warp's wait, asleep in the barrier's own wait (up to 20 us a time) rather than
 // polling beside the warps at work; bounded as mb_wait.
@@ -300,8 +265,26 @@ __device__ __forceinline__ bool mb_wait_asleep(uint64_t *b, uint32_t parity)
         if (clock64() - t0 > kTcWaitCyc) return false;
     }
 }
-__device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kChPrep * 32) : "memory"); }
+__device__ __forceinline__ float clamp_gate(float g) { return g < kMinGate ? kMinGate : g; }   // NaN stays
 
+// Eight values of row r, columns 8 c8.., of a lower triangular tile, as two terms in the
+// tensor core's unswizzled order: 16-column block j = c8 / 2 holds rows from 16 j on, in
+// pieces of 8 rows x 8 columns (128 bytes), the two column halves of 8 rows side by side.
+__device__ __forceinline__ void put_terms(uint8_t *tile, int r, int c8, const float (&x)[8])
+{
+    const int j = c8 >> 1;
+    if (r < 16 * j) return;
+    uint32_t h[4], m[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) split2(x[2 * i], x[2 * i + 1], &h[i], &m[i]);
+    uint8_t *p = tile + term_block(j) + ((r - 16 * j) >> 3) * 256 + (c8 & 1) * 128 + (r & 7) * 16;
+    *reinterpret_cast<uint4 *>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(p + kTermBytes) = make_uint4(m[0], m[1], m[2], m[3]);
+}
+
+// ---- the inverse
+constexpr int kPpThreads = 256;
+constexpr int kChLd = 68;                                     // row stride of the float scratch
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
 {
     asm volatile(
@@ -309,17 +292,18 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-// A warp's 16 x 8 tile of X Y over K, X and Y in shared memory with rows kChLd floats apart:
-// tf32 MMAs on two terms each (hi + lo, 22 bits; hi hi + hi lo + lo hi), which read an
-// element once a tile where plain FMAs, at four outputs a thread, read it once a thread
-// (the whole inverse: 7.4 thousand clocks of shared-memory reads, against 2).
+// A warp's 16 x 8 tile of sign X Y over columns k0 .. k1 of X, X and Y in shared memory with
+// rows kChLd floats apart, into D: tf32 MMAs on two terms each (hi + lo, 22 bits; hi hi +
+// hi lo + lo hi), which read an element once a tile where plain FMAs read it once a thread.
 template <int K>
-__device__ __forceinline__ void block_product(float (&d)[4], const float *X, const float *Y, int lane)
+__device__ __forceinline__ void block_product(float *D, float sign, const float *X, const float *Y, int k0, int k1,
+                                              int lane)
 {
     const int g = lane >> 2, t = lane & 3;
-    d[0] = d[1] = d[2] = d[3] = 0.0f;
+    float d[3][4] = {};
 #pragma unroll
     for (int k = 0; k < K; k += 8) {
+        if (k < k0 || k >= k1) continue;
         const float a[4] = {X[g * kChLd + k + t], X[(g + 8) * kChLd + k + t], X[g * kChLd + k + t + 4],
                             X[(g + 8) * kChLd + k + t + 4]};
         const float b[2] = {Y[(k + t) * kChLd + g], Y[(k + t + 4) * kChLd + g]};
@@ -334,16 +318,14 @@ __device__ __forceinline__ void block_product(float (&d)[4], const float *X, con
             bh[i] = __float_as_uint(b[i]) & 0xFFFFE000u;
             bl[i] = __float_as_uint(b[i] - __uint_as_float(bh[i]));
         }
-        mma_tf32(d, al, bh);
-        mma_tf32(d, ah, bl);
-        mma_tf32(d, ah, bh);
+        mma_tf32(d[0], al, bh);
+        mma_tf32(d[1], ah, bl);
+        mma_tf32(d[2], ah, bh);
     }
-}
-__device__ __forceinline__ void store_tile(float *D, const float (&d)[4], float sign, int lane)
-{
-    const int g = lane >> 2, t = (lane & 3) * 2;
-    *reinterpret_cast<float2 *>(&D[g * kChLd + t]) = make_float2(sign * d[0], sign * d[1]);
-    *reinterpret_cast<float2 *>(&D[(g + 8) * kChLd + t]) = make_float2(sign * d[2], sign * d[3]);
+#pragma unroll
+    for (int i = 0; i < 4; i++) d[2][i] = sign * ((d[0][i] + d[1][i]) + d[2][i]);
+    *reinterpret_cast<float2 *>(&D[g * kChLd + 2 * t]) = make_float2(d[2][0], d[2][1]);
+    *reinterpret_cast<float2 *>(&D[(g + 8) * kChLd + 2 * t]) = make_float2(d[2][2], d[2][3]);
 }
 
 // A <- (I + A)^-1 of a strictly lower triangular 64 x 64 A (rows kChLd floats apart), in
@@ -373,48 +355,489 @@ __device__ __forceinline__ void invert64(float *A, int tid)
 #pragma unroll
             for (int t = 0; t < 16; t++) a[t * kChLd + col] = x[t];       // zero above the diagonal
     }
-    prep_sync();
+    __syncthreads();
     {   // 16 -> 32: two pairs of blocks, two tiles of 16 x 8 each, a tile for each of four warps
         float *a = A + 32 * (warp >> 1) * (kChLd + 1);
         const int n0 = (warp & 1) * 8;
-        float w[4];
-        if (warp < 4) {
-            block_product<16>(w, &a[16 * kChLd], &a[n0], lane);           // A21 X11
-            store_tile(&a[16 + n0], w, 1.0f, lane);
-        }
-        prep_sync();
-        if (warp < 4) {
-            block_product<16>(w, &a[16 * kChLd + 16], &a[16 + n0], lane); // X22 (A21 X11)
-            store_tile(&a[16 * kChLd + n0], w, -1.0f, lane);
-        }
-        prep_sync();
-        const int r = (tid & 127) >> 3, c = (tid & 7) * 2;
-        *reinterpret_cast<float2 *>(&A[(32 * (tid >> 7) + r) * kChLd + 32 * (tid >> 7) + 16 + c]) = make_float2(0.f, 0.f);
+        if (warp < 4) block_product<16>(&a[16 + n0], 1.0f, &a[16 * kChLd], &a[n0], n0, 16, lane);            // A21 X11
+        __syncthreads();
+        if (warp < 4)
+            block_product<16>(&a[16 * kChLd + n0], -1.0f, &a[16 * kChLd + 16], &a[16 + n0], 0, 16, lane);    // X22 (..)
+        __syncthreads();
+        const int p = 32 * (tid >> 7), r = (tid & 127) >> 3, c = (tid & 7) * 2;
+        *reinterpret_cast<float2 *>(&A[(p + r) * kChLd + p + 16 + c]) = make_float2(0.f, 0.f);
     }
-    prep_sync();
-    {   // 32 -> 64: eight tiles of 16 x 8, one a warp
+    __syncthreads();
+    {   // 32 -> 64: eight tiles of 16 x 8, one a warp; X11 and X22 are lower triangular
         const int m0 = 16 * (warp >> 2), n0 = 8 * (warp & 3);
-        float w[4];
-        block_product<32>(w, &A[(32 + m0) * kChLd], &A[n0], lane);
-        store_tile(&A[m0 * kChLd + 32 + n0], w, 1.0f, lane);
-        prep_sync();
-        block_product<32>(w, &A[(32 + m0) * kChLd + 32], &A[32 + n0], lane);
-        store_tile(&A[(32 + m0) * kChLd + n0], w, -1.0f, lane);
+        block_product<32>(&A[m0 * kChLd + 32 + n0], 1.0f, &A[(32 + m0) * kChLd], &A[n0], n0, 32, lane);
+        __syncthreads();
+        block_product<32>(&A[(32 + m0) * kChLd + n0], -1.0f, &A[(32 + m0) * kChLd + 32], &A[32 + n0], 0, m0 + 16, lane);
     }
-    prep_sync();
+    __syncthreads();
 }
 
-__global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaArgs a,
-                                                                    const __grid_constant__ CUtensorMap mq,
-                                                                    const __grid_constant__ CUtensorMap mk,
-                                                                    const __grid_constant__ CUtensorMap mv)
+// ---------------------------------------------------------------- T and P
+// One block a chunk and head.  With the rows of K over those of Q as the 128 rows of a
+// tensor-core tile, one product against K's rows gives A's and P's dot products.
+//
+// Decay per head: K and Q go in as they are and the float dot products are weighted after,
+// with G as a pair of floats (a sum, and what it lost), so that differences of G hold
+// however strong an earlier decay was.
+//
+// Decay per channel: the weights are inside the products.  In each 32-token half b, with m
+// its G in the middle (after 16 tokens), rows are x_t exp(G_t - m), columns k_i exp(m - G_i),
+// and the first half's columns go in a second time against the second half's m; a pair's
+// two exponentials multiply to exp(G_t - G_i).  G counts from the half's start.  That holds
+// while no |G_t - m| passes 60 (a factor of 1e26 either way; a token's mean decay of 1e-2
+// over 16 tokens would reach it).  Where one does, the chunk's products are summed one by
+// one, the weight's logarithm accumulated backwards from t: slower, but exact for any decay.
+constexpr int kPpA = 128 * 128;                               // an operand's term, 64 channels: 128 rows
+constexpr int kPpB = 96 * 128;                                // and 96 rows
+constexpr float kPpRange = 60.0f * kLog2e;
+constexpr size_t pp_smem(bool channel) { return 1024 + (channel ? 2 * kPpA + 2 * kPpB : 2 * kPpA); }
+
+struct PrepShared {
+    uint64_t full, done;
+    uint32_t tmem;
+    int seq, far, bad;
+    alignas(16) float gh[kC], gl[kC], rk[kC], kb[kC], qn[kC], beta[kC];
+    alignas(16) float sum[8][kD];                             // log2 decays summed over each 8 tokens
+};
+
+// This block's sequence and first token, from its record's number; false when there is none.
+__device__ __forceinline__ bool find_chunk(const DeltaArgs &a, int rec, int *found, int *tok0, int *n)
+{
+    auto range = [&](int s, int *s0, int *len) {
+        *s0 = a.seq_start ? a.seq_start[s] : 0;
+        const int s1 = a.seq_start ? a.seq_start[s + 1] : a.T;
+        *len = s1 - *s0;
+        return *s0 >= 0 && s1 >= *s0 && s1 <= a.T && rec >= *s0 / kC + s && rec < *s0 / kC + s + (*len + kC - 1) / kC;
+    };
+    int s0, len, s = 0;
+    if (a.n_seq > 1) {
+        if (threadIdx.x == 0) *found = 0x7fffffff;
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.n_seq; i += kPpThreads)
+            if (range(i, &s0, &len)) atomicMin(found, i);
+        __syncthreads();
+        s = *found;
+        if (s == 0x7fffffff) return false;
+    }
+    if (!range(s, &s0, &len)) return false;
+    const int c = rec - (s0 / kC + s);
+    *tok0 = s0 + kC * c;
+    *n = min(kC, len - kC * c);
+    return true;
+}
+
+template <bool kChannel>
+__global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
+    delta_prepare_kernel(const DeltaArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk)
 {
     pdl_wait();
     pdl_trigger();
+    extern __shared__ __align__(1024) uint8_t psm_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(psm_raw) + 1023) & ~(uintptr_t)1023);
+    float *As = reinterpret_cast<float *>(sm);                // over the operands, once they are used
+    __shared__ PrepShared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rec = blockIdx.x / a.H, h = blockIdx.x % a.H, hq = h / (a.H / a.Hq);
+    int tok0, n;
+    if (!find_chunk(a, rec, &sh.seq, &tok0, &n)) return;
+    int32_t *status = reinterpret_cast<int32_t *>(a.ws);
+    uint8_t *out = a.ws + kCtrOffset + kCtrBytes + ((size_t)rec * a.H + h) * kRecBytes;
+    float *outf = reinterpret_cast<float *>(out + kTpBytes);
+    constexpr int kCols = kChannel ? 128 : 64;                // tensor memory
+    if (tid == 0) {
+        mb_init(&sh.full, 1);
+        mb_init(&sh.done, 1);
+        sh.far = 0;
+        sh.bad = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (!kChannel) {
+            mb_expect_tx(&sh.full, 2 * kPpA);
+            for (int b = 0; b < 2; b++) {
+                tma2d(sm + b * kPpA, &mk, hq * kD + 64 * b, tok0, &sh.full);
+                tma2d(sm + b * kPpA + kC * 128, &mq, hq * kD + 64 * b, tok0, &sh.full);
+            }
+        }
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sh.tmem)), "r"(kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    auto wait = [&](uint64_t &b, uint32_t parity) {
+        if (mb_wait_asleep(&b, parity)) return true;
+        set_status(status, K3MOE_DEV_TIMEOUT);
+        sh.bad = 1;
+        return false;
+    };
+    bool far = false;                                         // per channel: the weights reach too far
+
+    if (!kChannel) {
+        const int row = tid, t = row & (kC - 1);              // threads 0-63: K's rows, 64-127: Q's
+        if (warp < 4) {
+            // inclusive sums over the 64 tokens, two a lane, as sum + lost
+            float s[2], e[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                s[i] = lane + 32 * i < n ? clamp_gate(a.g[(size_t)(tok0 + lane + 32 * i) * a.H + h]) : 0.0f;
+            auto add = [](float &x, float &ex, float y, float ey) {      // two-sum, then the lost parts
+                const float z = x + y, v = z - x;
+                ex = ((x - (z - v)) + (y - v)) + (ex + ey);
+                x = z;
+            };
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const float p = __shfl_up_sync(0xffffffffu, s[i], o), ep = __shfl_up_sync(0xffffffffu, e[i], o);
+                    if (lane >= o) add(s[i], e[i], p, ep);
+                }
+            add(s[1], e[1], __shfl_sync(0xffffffffu, s[0], 31), __shfl_sync(0xffffffffu, e[0], 31));
+            const float gc = __shfl_sync(0xffffffffu, s[1], 31), ec = __shfl_sync(0xffffffffu, e[1], 31);
+            const float G = (warp & 1) ? s[1] : s[0], E = (warp & 1) ? e[1] : e[0];
+            const bool ok = wait(sh.full, 0);
+            float norm = 1.0f;
+            if (a.qk_norm && ok) {
+                float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 16; j++) {                // chunk order is the swizzle's: a sum does not mind
+                    const uint4 w = *reinterpret_cast<const uint4 *>(sm + (j >> 3) * kPpA + row * 128 + (((j & 7) ^ (row & 7)) << 4));
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        const float lo = __uint_as_float(u[r] << 16), hi = __uint_as_float(u[r] & 0xFFFF0000u);
+                        s0 = fmaf(lo, lo, s0);
+                        s1 = fmaf(hi, hi, s1);
+                    }
+                }
+                norm = 1.0f / sqrtf(s0 + s1 + a.eps);
+            }
+            const bool in = t < n;
+            const float eG = expf(G + E);
+            if (row < kC) {
+                const float b = in ? a.beta[(size_t)(tok0 + t) * a.H + h] : 0.0f;
+                sh.gh[t] = G;
+                sh.gl[t] = E;
+                sh.rk[t] = in ? norm : 0.0f;
+                sh.beta[t] = b;
+                sh.kb[t] = in ? b * norm : 0.0f;
+                outf[kRecKr + t] = in ? norm * eG : 0.0f;
+                outf[kRecKd + t] = in ? norm * expf((gc - G) + (ec - E)) : 0.0f;
+                if (t == 0) outf[kRecDec] = expf(gc + ec);
+            } else {
+                sh.qn[t] = in ? a.scale * norm : 0.0f;
+                outf[kRecQr + t] = in ? a.scale * norm * eG : 0.0f;
+            }
+        }
+        if (warp == 4 && wait(sh.full, 0)) {
+            const uint64_t d = sdesc(saddr(sm));
+#pragma unroll
+            for (int s = 0; s < 8; s++) {
+                const uint64_t at = d + (((s >> 2) * kPpA + (s & 3) * 32) >> 4);
+                umma_warp(tmem, at, at, idesc(1, kC), s > 0);
+            }
+            umma_commit_warp(&sh.done);
+        }
+        __syncthreads();
+        if (!sh.bad) wait(sh.done, 0);
+    } else {
+        // a warp 8 tokens, a lane two of the 64 channels at hand
+        const int t0 = 8 * warp;
+        float nk[8] = {}, nq[8] = {};
+        for (int half = 0; half < 2; half++) {
+            const int ch = 64 * half + 2 * lane;
+            uint32_t k[8], q[8];
+            float2 g[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const size_t tok = (size_t)tok0 + min(t0 + i, n - 1);
+                k[i] = *reinterpret_cast<const uint32_t *>(a.k + tok * a.k_stride + hq * kD + ch);
+                q[i] = *reinterpret_cast<const uint32_t *>(a.q + tok * a.q_stride + hq * kD + ch);
+                g[i] = *reinterpret_cast<const float2 *>(a.g + (tok * a.H + h) * kD + ch);
+            }
+            float2 L = make_float2(0.0f, 0.0f);               // sums over this warp's tokens so far, in log2
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const bool in = t0 + i < n;
+                L.x += in ? clamp_gate(g[i].x) * kLog2e : 0.0f;
+                L.y += in ? clamp_gate(g[i].y) * kLog2e : 0.0f;
+                g[i] = L;
+            }
+            *reinterpret_cast<float2 *>(&sh.sum[warp][ch]) = L;
+            if (half == 1) wait(sh.done, 0);                  // the first half's operands are used
+            __syncthreads();
+            if (sh.bad) break;
+            float2 s[8];
+#pragma unroll
+            for (int w = 0; w < 8; w++) s[w] = *reinterpret_cast<const float2 *>(&sh.sum[w][ch]);
+            // G at this warp's start less the middle of its 32 tokens; the second half's middle
+            // less the first half's end (both counted from their own half's start)
+            const int b = (warp >> 2) * 4;
+            float2 base = make_float2(0.f, 0.f);
+            float2 m1 = make_float2(s[4].x + s[5].x, s[4].y + s[5].y);
+            switch (warp & 3) {
+            case 0: base = make_float2(-(s[b].x + s[b + 1].x), -(s[b].y + s[b + 1].y)); break;
+            case 1: base = make_float2(-s[b + 1].x, -s[b + 1].y); break;
+            case 2: break;
+            default: base = make_float2(s[b + 2].x, s[b + 2].y); break;
+            }
+            // (first half only) the second's middle less G at this warp's start
+            float2 tail = m1;
+#pragma unroll
+            for (int w = 3; w >= 0; w--)
+                if (w >= warp) { tail.x += s[w].x; tail.y += s[w].y; }
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int t = t0 + i;
+                const float kx = __uint_as_float(k[i] << 16), ky = __uint_as_float(k[i] & 0xFFFF0000u);
+                const float qx = __uint_as_float(q[i] << 16), qy = __uint_as_float(q[i] & 0xFFFF0000u);
+                nk[i] = fmaf(kx, kx, fmaf(ky, ky, nk[i]));
+                nq[i] = fmaf(qx, qx, fmaf(qy, qy, nq[i]));
+                const float dx = base.x + g[i].x, dy = base.y + g[i].y;       // G_t - m
+                far |= !(fabsf(dx) <= kPpRange && fabsf(dy) <= kPpRange);
+                const float ex = exp2_approx(dx), ey = exp2_approx(dy);
+                const uint32_t at = t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
+                uint32_t hi, mid;
+                split2(kx * ex, ky * ey, &hi, &mid);
+                *reinterpret_cast<uint32_t *>(sm + at) = hi;
+                *reinterpret_cast<uint32_t *>(sm + kPpA + at) = mid;
+                split2(qx * ex, qy * ey, &hi, &mid);
+                *reinterpret_cast<uint32_t *>(sm + kC * 128 + at) = hi;
+                *reinterpret_cast<uint32_t *>(sm + kPpA + kC * 128 + at) = mid;
+                uint8_t *B = sm + 2 * kPpA;
+                split2(kx * exp2_approx(-dx), ky * exp2_approx(-dy), &hi, &mid);
+                *reinterpret_cast<uint32_t *>(B + at) = hi;
+                *reinterpret_cast<uint32_t *>(B + kPpB + at) = mid;
+                if (warp < 4) {
+                    split2(kx * exp2_approx(tail.x - g[i].x), ky * exp2_approx(tail.y - g[i].y), &hi, &mid);
+                    *reinterpret_cast<uint32_t *>(B + kC * 128 + at) = hi;
+                    *reinterpret_cast<uint32_t *>(B + kPpB + kC * 128 + at) = mid;
+                }
+            }
+            if (warp < 4) {                                   // 16 tokens' sums for the second kernel
+                float2 x = make_float2(s[0].x + s[1].x, s[0].y + s[1].y);
+                if (warp == 1) x = make_float2(s[2].x + s[3].x, s[2].y + s[3].y);
+                if (warp == 2) x = m1;
+                if (warp == 3) x = make_float2(s[6].x + s[7].x, s[6].y + s[7].y);
+                *reinterpret_cast<float2 *>(&outf[kRecSum + warp * kD + ch]) = x;
+            }
+            fence_async_smem();
+            __syncthreads();
+            if (warp == 0) {
+                const uint64_t A = sdesc(saddr(sm)), B = sdesc(saddr(sm + 2 * kPpA));
+#pragma unroll
+                for (int term = 0; term < 3; term++)
+#pragma unroll
+                    for (int s4 = 0; s4 < 4; s4++)
+                        umma_warp(tmem, A + (((term == 2 ? kPpA : 0) + s4 * 32) >> 4), B + (((term == 1 ? kPpB : 0) + s4 * 32) >> 4),
+                                  idesc(1, 96), half > 0 || term > 0 || s4 > 0);
+                umma_commit_warp(&sh.done);
+            }
+        }
+        if (far) sh.far = 1;
+        // the norms: a warp's eight rows of each
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            nk[i] = warp_sum(nk[i]);
+            nq[i] = warp_sum(nq[i]);
+        }
+        if (lane < 8) {
+            float k2 = nk[0], q2 = nq[0];
+#pragma unroll
+            for (int i = 1; i < 8; i++) {
+                k2 = lane == i ? nk[i] : k2;
+                q2 = lane == i ? nq[i] : q2;
+            }
+            const int t = t0 + lane;
+            const bool in = t < n;
+            const float b = in ? a.beta[(size_t)(tok0 + t) * a.H + h] : 0.0f;
+            const float rk = !in ? 0.0f : a.qk_norm ? 1.0f / sqrtf(k2 + a.eps) : 1.0f;
+            const float qn = !in ? 0.0f : a.scale * (a.qk_norm ? 1.0f / sqrtf(q2 + a.eps) : 1.0f);
+            sh.rk[t] = rk;
+            sh.kb[t] = b * rk;
+            sh.qn[t] = qn;
+            sh.beta[t] = b;
+            outf[kRecRk + t] = rk;
+            outf[kRecQn + t] = qn;
+        }
+        if (!sh.bad) wait(sh.done, 1);
+        __syncthreads();
+        far = sh.far != 0;
+    }
+    __syncthreads();
+
+    if (!sh.bad) {
+        // lanes 0-63 of tensor memory hold A's rows, 64-127 P's; a warp takes 32 rows of one of
+        // the two, half of their columns
+        tc_fence_after();
+        const int row = 32 * (warp & 3) + lane, t = row & (kC - 1), i00 = 32 * (warp >> 2);
+        const bool is_a = row < kC;
+        const float rowf = is_a ? sh.kb[t] : sh.qn[t];
+        const int last = t < n ? (is_a ? t - 1 : t) : -1;     // the row's last token
+        float v[32];
+        if (kChannel && far) {
+            // one product at a time, the weight's logarithm summed backwards from t
+            const uint16_t *x = (is_a ? a.k + (size_t)(tok0 + min(t, n - 1)) * a.k_stride
+                                      : a.q + (size_t)(tok0 + min(t, n - 1)) * a.q_stride) + hq * kD;
+#pragma unroll
+            for (int j = 0; j < 32; j++) v[j] = 0.0f;
+            for (int c = 0; c < kD; c++) {
+                const float xc = bf16_bits_to_f32(x[c]);
+                float D = 0.0f;
+                for (int i = t; i >= i00 + 32; i--)           // tokens between the columns and t
+                    if (i < n) D += clamp_gate(a.g[((size_t)(tok0 + i) * a.H + h) * kD + c]);
+#pragma unroll
+                for (int j = 31; j >= 0; j--) {
+                    const int i = i00 + j;
+                    if (i <= t && t < n) {
+                        v[j] = fmaf(xc * bf16_bits_to_f32(a.k[(size_t)(tok0 + i) * a.k_stride + hq * kD + c]),
+                                    exp2_approx(D * kLog2e), v[j]);
+                        D += clamp_gate(a.g[((size_t)(tok0 + i) * a.H + h) * kD + c]);
+                    }
+                }
+            }
+        } else {
+            const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (kChannel && t >= 32 && i00 == 0 ? 64 : i00);
+            tmem_ld16_nowait(at, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+            tmem_ld16_nowait(at + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+            tmem_wait_ld();
+        }
+        __syncthreads();                                      // the operands are used: the scratch lies over them
+        const float gh = kChannel ? 0.0f : sh.gh[t], gl = kChannel ? 0.0f : sh.gl[t];
+#pragma unroll
+        for (int j4 = 0; j4 < 8; j4++) {
+            const float4 r4 = *reinterpret_cast<const float4 *>(&sh.rk[i00 + 4 * j4]);
+            const float r[4] = {r4.x, r4.y, r4.z, r4.w};
+            float w[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+            if (!kChannel) {
+                const float4 h4 = *reinterpret_cast<const float4 *>(&sh.gh[i00 + 4 * j4]);
+                const float4 l4 = *reinterpret_cast<const float4 *>(&sh.gl[i00 + 4 * j4]);
+                w[0] = exp2_approx(((gh - h4.x) + (gl - l4.x)) * kLog2e);
+                w[1] = exp2_approx(((gh - h4.y) + (gl - l4.y)) * kLog2e);
+                w[2] = exp2_approx(((gh - h4.z) + (gl - l4.z)) * kLog2e);
+                w[3] = exp2_approx(((gh - h4.w) + (gl - l4.w)) * kLog2e);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float x = v[4 * j4 + j] * (rowf * r[j]) * w[j];
+                v[4 * j4 + j] = i00 + 4 * j4 + j <= last ? x : 0.0f;
+            }
+        }
+        if (is_a) {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                *reinterpret_cast<float4 *>(&As[t * kChLd + i00 + 4 * j]) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        } else {
+            const float(*v8)[8] = reinterpret_cast<const float(*)[8]>(v);
+#pragma unroll
+            for (int j = 0; j < 4; j++) put_terms(out + 2 * kTermBytes, t, i00 / 8 + j, v8[j]);
+        }
+        __syncthreads();
+        invert64(As, tid);
+        const int r = tid >> 2, c0 = (tid & 3) * 16;
+#pragma unroll
+        for (int j8 = 0; j8 < 2; j8++) {
+            float x[8], b[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+                *reinterpret_cast<float4 *>(&x[j]) = *reinterpret_cast<const float4 *>(&As[r * kChLd + c0 + 8 * j8 + j]);
+                *reinterpret_cast<float4 *>(&b[j]) = *reinterpret_cast<const float4 *>(&sh.beta[c0 + 8 * j8 + j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float y = x[j] * b[j];
+                x[j] = c0 + 8 * j8 + j <= r ? y : 0.0f;
+            }
+            put_terms(out, r, c0 / 8 + j8, x);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+}
+
+// ---------------------------------------------------------------- the chain
+// One block per sequence and head walks its chunks; everything is transposed so that a
+// thread owns one value column v (a lane of tensor memory) and a part of the state S^T
+// [v][k] stays in its registers: the A operands (S, R = V - exp(G) K S, U) go from registers
+// to tensor memory and never through shared memory, the B operands (K and Q, T, P) are
+// shared tiles.
+//   decay per head: K and Q as they are (exact in bf16); exp(G) weighs the results' columns,
+//     and U's a second time before K^T U;
+//   per channel: four warps' worth of threads more write exp(G) K, exp(G) Q and
+//     exp(G_C - G) K as two terms each, a chunk ahead.
+// A stage's latency is a chain of short dependent steps (a product, its sums to registers,
+// two terms back), so each has as many warps as the registers allow (64 a thread).
+constexpr int kChChain = 16, kChOut = 4, kChMake = 8;
+constexpr int kChStagesHead = 3, kChStagesChannel = 2;
+constexpr int kChBox = kC * 128;                              // 64 tokens x 64 channels: 8 KB
+constexpr int kChKq = 4 * kChBox;                             // decay per head: K and Q, [box][K, Q]
+constexpr int kChV = 2 * kChBox;
+constexpr int kChTp = 21 * 1024;                              // T and P, and decay per head the scales
+constexpr int kChTpCopyHead = kTpBytes + 1024;
+constexpr int kChStageHead = kChKq + kChV + kChTp, kChStageChannel = kChV + kChTp;
+constexpr int kChTerm = 2 * kChBox;                           // per channel: one term of 64 x 128
+constexpr int kChMade = 4 * kChTerm + 4 * kChTerm;            // K, Q [hi, mid]; the late K [chunk parity][hi, mid]
+static_assert(kTpBytes + (kRecDec + 1) * 4 <= kChTp && kTpBytes + 1024 <= kChTp, "a stage holds the record's head");
+template <bool kChannel> struct ChunkShape {
+    static constexpr int warps = kChChain + kChOut + (kChannel ? kChMake : 0) + 1;
+    static constexpr int threads = kChannel ? 1024 : warps * 32;       // per channel whole warpgroups: registers move
+    static constexpr int stages = kChannel ? kChStagesChannel : kChStagesHead;
+    static constexpr int stage = kChannel ? kChStageChannel : kChStageHead;
+    static constexpr int smem = 1024 + (kChannel ? kChMade : 0) + stages * stage;
+};
+constexpr int kChWarpOut = kChChain, kChWarpMake = kChWarpOut + kChOut;
+// Registers a thread per channel: 64 at launch, shares moved from the writers of O and the
+// issuing warp's group to the makers of operands (16 tokens' inputs in registers).
+constexpr int kChRegs = 64, kChRegsMake = 96, kChRegsOut = 40, kChRegsMma = 24;
+static_assert(4 * kChRegs + 2 * kChRegsMake + kChRegsOut + kChRegsMma <= 8 * kChRegs, "shares within the launch's");
+// tensor memory columns
+constexpr uint32_t kTmS = 0;      // S^T as an operand, [quarter of k][hi, mid][16]; the new S's sums over it
+constexpr uint32_t kTmR = 128;    // K S, then T R
+constexpr uint32_t kTmOq = 192;   // Q S (per channel: O)
+constexpr uint32_t kTmOp = 256;   // P U
+constexpr uint32_t kTmRU = 320;   // R, then U (per head: weighted for the state), as an operand [hi, mid][32]
+constexpr uint32_t kTmU = 384;    // per head: U as an operand [hi, mid][32]
+
+struct ChunkShared {
+    uint64_t in_full[3];
+    uint64_t s_ready, d1_full, q_done, r_ready, d2_full, u_ready, d4_full, o_full, o_free, made, drain;
+    uint32_t tmem;
+    volatile int bail;
+    alignas(16) float dec[2][kD];                             // per channel: exp(G_C), by chunk parity
+};
+
+// Unswizzled K-major descriptor of a T or P block: 8-row groups 256 bytes apart, their two
+// 8-column halves 128.
+__device__ __forceinline__ uint64_t tdesc(uint32_t addr)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(128u >> 4) << 16 | (uint64_t)(256u >> 4) << 32 |
+           (uint64_t)1u << 46;
+}
+
+template <bool kChannel>
+__global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
+    delta_chunk_kernel(const DeltaArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                       const __grid_constant__ CUtensorMap mv)
+{
+    pdl_wait();
+    pdl_trigger();
+    using Shape = ChunkShape<kChannel>;
+    constexpr int kWarpMma = Shape::warps - 1, kStages = Shape::stages;
     extern __shared__ __align__(1024) uint8_t csm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(csm_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *tT = sm + kChStages * kChStageBytes, *tP = tT + 2 * kChTile;
-    float *As = reinterpret_cast<float *>(tP + 4 * kChTile);
+    uint8_t *made = sm;                                       // per channel
+    uint8_t *ring = sm + (kChannel ? kChMade : 0);
+    constexpr int kOffV = kChannel ? 0 : kChKq, kOffTp = kOffV + kChV;
     __shared__ ChunkShared sh;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -423,33 +846,35 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
     if (!delta_seq(a, seq, &first, &len, &slot)) return;
     const size_t sbase = ((size_t)slot * a.H + h) * kD * kD;
     if (len == 0) {
-        for (int e = threadIdx.x; e < kD * kD / 4; e += kChThreads)
+        for (int e = threadIdx.x; e < kD * kD / 4; e += Shape::threads)
             reinterpret_cast<float4 *>(a.state_out + sbase)[e] =
                 a.state_in ? reinterpret_cast<const float4 *>(a.state_in + sbase)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
         return;
     }
     const int hq = h / (a.H / a.Hq), nc = (len + kC - 1) / kC;
     int32_t *status = reinterpret_cast<int32_t *>(a.ws);
+    // chunk c's record
+    const uint8_t *rec0 = a.ws + kCtrOffset + kCtrBytes + ((size_t)(first / kC + seq) * a.H + h) * kRecBytes;
+    auto record = [&](int c) { return rec0 + (size_t)c * a.H * kRecBytes; };
+    auto stage = [&](int c) { return ring + (size_t)(c % kStages) * Shape::stage; };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kChStages; s++) mb_init(&sh.kq_full[s], 1);
-        mb_init(&sh.kk_full, 1);
-        mb_init(&sh.kk_free, kChPrep);
-        for (int p = 0; p < kChScales; p++) mb_init(&sh.sc_ready[p], kChOut);
-        mb_init(&sh.tp_ready, kChPrep);
+        for (int s = 0; s < kStages; s++) mb_init(&sh.in_full[s], 1);
         mb_init(&sh.s_ready, kChChain);
         mb_init(&sh.d1_full, 1);
+        mb_init(&sh.q_done, 1);
         mb_init(&sh.r_ready, kChChain);
         mb_init(&sh.d2_full, 1);
         mb_init(&sh.u_ready, kChChain);
         mb_init(&sh.d4_full, 1);
         mb_init(&sh.o_full, 1);
         mb_init(&sh.o_free, kChOut);
+        mb_init(&sh.made, kChMake);
         mb_init(&sh.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.bail = 0;
     }
-    if (warp == kChWarpMma) {
+    if (warp == kWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sh.tmem)),
                      "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -473,74 +898,18 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
         __syncwarp();
         if (lane == 0) mb_arrive(&b);
     };
+    if (kChannel) {
+        if (warp >= kChWarpMake && warp < kChWarpMake + kChMake)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChRegsMake));
+        else if (warp >= kWarpMma)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChRegsMma));
+        else if (warp >= kChWarpOut)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChRegsOut));
+    }
 
-    if (warp < kChPrep) {
-        // ---------------- T and P of chunk c: lanes 0-63 of tensor memory hold A's rows, 64-127
-        // P's; a warp takes 32 rows of one of the two, half of their columns
-        const int row = 32 * (warp & 3) + lane, t = row & (kC - 1), i00 = 32 * (warp >> 2);
-        const bool is_a = row < kC;
-        for (int c = 0; c < nc; c++) {
-            const int n = min(kC, len - kC * c);
-            if (!wait(sh.sc_ready[c % kChScales], c / kChScales) || !wait(sh.kk_full, c)) break;
-            tc_fence_after();                                 // chunk c - 2's P is used: the MMAs' issue saw to it
-            const ChunkShared::Scales &sc = sh.sc[c % kChScales];
-            const float rowf = is_a ? sc.kb[t] : sc.qn[t], g2 = sc.g2[t];
-            const int last = t < n ? (is_a ? t - 1 : t) : -1;          // the row's last token
-            uint8_t *tPc = tP + (c & 1) * 2 * kChTile;
-#pragma unroll 1
-            for (int i0 = i00; i0 < i00 + 32; i0 += 16) {
-                float v[16];
-                tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kTmKK + i0, v);
-#pragma unroll
-                for (int j4 = 0; j4 < 4; j4++) {
-                    const float4 gk4 = *reinterpret_cast<const float4 *>(&sc.gk[i0 + 4 * j4]);
-                    const float gk[4] = {gk4.x, gk4.y, gk4.z, gk4.w};
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const float x = v[4 * j4 + j] * (rowf * exp2_approx(g2 - gk[j]));
-                        v[4 * j4 + j] = i0 + 4 * j4 + j <= last ? x : 0.0f;
-                    }
-                }
-                if (is_a) {
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        *reinterpret_cast<float4 *>(&As[t * kChLd + i0 + 4 * j]) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                } else {
-                    const float(*v8)[8] = reinterpret_cast<const float(*)[8]>(v);
-                    put_terms(tPc, t, i0 / 8, v8[0]);
-                    put_terms(tPc, t, i0 / 8 + 1, v8[1]);
-                }
-            }
-            arrive(sh.kk_free);
-            prep_sync();
-            invert64(As, threadIdx.x);
-            if (c >= 1 && !wait(sh.d2_full, c - 1)) break;    // T of chunk c - 1 is used
-            {
-                const int r = threadIdx.x >> 2, c0 = (threadIdx.x & 3) * 16;
-#pragma unroll
-                for (int j8 = 0; j8 < 2; j8++) {
-                    float x[8], b[8];
-#pragma unroll
-                    for (int j = 0; j < 8; j += 4) {
-                        *reinterpret_cast<float4 *>(&x[j]) = *reinterpret_cast<const float4 *>(&As[r * kChLd + c0 + 8 * j8 + j]);
-                        *reinterpret_cast<float4 *>(&b[j]) = *reinterpret_cast<const float4 *>(&sc.beta[c0 + 8 * j8 + j]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const float y = x[j] * b[j];
-                        x[j] = c0 + 8 * j8 + j <= r ? y : 0.0f;
-                    }
-                    put_terms(tT, r, c0 / 8 + j8, x);
-                }
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mb_arrive(&sh.tp_ready);
-            prep_sync();                                      // the scratch is free again
-        }
-    } else if (warp < kChWarpOut) {
+    if (warp < kChChain) {
         // ---------------- the chain: value column v, a quarter of the channels or tokens
-        const int q = warp & 3, part = (warp - kChWarpChain) >> 2, v = 32 * q + lane;
+        const int q = warp & 3, part = warp >> 2, v = 32 * q + lane, t0 = 16 * part;
         const uint32_t la = tmem + ((uint32_t)(32 * q) << 16);
         float S[32];
 #pragma unroll
@@ -560,13 +929,12 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
         };
         put_state();
         for (int c = 0; c < nc; c++) {
-            const int n = min(kC, len - kC * c), t0 = 16 * part;
-            const int st = c % kChStages;
-            const ChunkShared::Scales &sc = sh.sc[c % kChScales];
+            const int n = min(kC, len - kC * c);
+            const float *sc = reinterpret_cast<const float *>(stage(c) + kOffTp + kTpBytes) + t0;     // per head
             // V[t][v] in its swizzled tile
-            const uint8_t *vt = sm + (size_t)st * kChStageBytes + kChV + (q >> 1) * kC * 128 + t0 * 128 + (v & 7) * 2;
+            const uint8_t *vt = stage(c) + kOffV + (q >> 1) * kChBox + t0 * 128 + (v & 7) * 2;
             const uint32_t v8 = (uint32_t)(v >> 3) & 7u;
-            if (!wait(sh.kq_full[st], c / kChStages)) break;
+            if (!wait(sh.in_full[c % kStages], c / kStages)) break;
             uint32_t vv[8];                                       // two tokens a word
 #pragma unroll
             for (int j = 0; j < 8; j++) {
@@ -574,7 +942,7 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
                 const uint32_t y = *reinterpret_cast<const uint16_t *>(vt + 2 * j * 128 + 128 + ((v8 ^ ((2 * j + 1) & 7u)) << 4));
                 vv[j] = x | (y << 16);
             }
-            if (!wait(sh.sc_ready[c % kChScales], c / kChScales) || !wait(sh.d1_full, c)) break;
+            if (!wait(sh.d1_full, c)) break;
             tc_fence_after();
             {
                 uint32_t d[16];
@@ -586,7 +954,7 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
 #pragma unroll
                     for (int j2 = 0; j2 < 4; j2++) {
                         const int j = 8 * b + 2 * j2;
-                        const float2 kr = *reinterpret_cast<const float2 *>(&sc.kr[t0 + j]);
+                        const float2 kr = kChannel ? make_float2(1.0f, 1.0f) : *reinterpret_cast<const float2 *>(&sc[kRecKr + j]);
                         const float x = fmaf(-kr.x, __uint_as_float(d[j]), __uint_as_float(vv[j >> 1] << 16));
                         const float y = fmaf(-kr.y, __uint_as_float(d[j + 1]), __uint_as_float(vv[j >> 1] & 0xFFFF0000u));
                         split2(t0 + j < n ? x : 0.0f, t0 + j + 1 < n ? y : 0.0f, &hi[j2], &mid[j2]);
@@ -607,23 +975,25 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
                 for (int b = 0; b < 2; b++) {
                     uint32_t hi[4], mid[4];
 #pragma unroll
-                    for (int j2 = 0; j2 < 4; j2++) {
-                        const int j = 8 * b + 2 * j2;
-                        const float2 kd = *reinterpret_cast<const float2 *>(&sc.kd[t0 + j]);
-                        split2(__uint_as_float(d[j]) * kd.x, __uint_as_float(d[j + 1]) * kd.y, &hi[j2], &mid[j2]);
-                    }
-                    tmem_st4(la + kTmRU + 8 * part + 4 * b, hi);
-                    tmem_st4(la + kTmRU + 32 + 8 * part + 4 * b, mid);
-#pragma unroll
                     for (int j2 = 0; j2 < 4; j2++)
                         split2(__uint_as_float(d[8 * b + 2 * j2]), __uint_as_float(d[8 * b + 2 * j2 + 1]), &hi[j2], &mid[j2]);
-                    tmem_st4(la + kTmU + 8 * part + 4 * b, hi);
-                    tmem_st4(la + kTmU + 32 + 8 * part + 4 * b, mid);
+                    tmem_st4(la + (kChannel ? kTmRU : kTmU) + 8 * part + 4 * b, hi);
+                    tmem_st4(la + (kChannel ? kTmRU : kTmU) + 32 + 8 * part + 4 * b, mid);
+                    if (!kChannel) {
+#pragma unroll
+                        for (int j2 = 0; j2 < 4; j2++) {
+                            const int j = 8 * b + 2 * j2;
+                            const float2 kd = *reinterpret_cast<const float2 *>(&sc[kRecKd + j]);
+                            split2(__uint_as_float(d[j]) * kd.x, __uint_as_float(d[j + 1]) * kd.y, &hi[j2], &mid[j2]);
+                        }
+                        tmem_st4(la + kTmRU + 8 * part + 4 * b, hi);
+                        tmem_st4(la + kTmRU + 32 + 8 * part + 4 * b, mid);
+                    }
                 }
             }
             tmem_wait_st();
             arrive(sh.u_ready);
-            const float dec = sc.dec;
+            const float dec = kChannel ? 0.0f : sc[kRecDec - t0];
             if (!wait(sh.d4_full, c)) break;
             tc_fence_after();
 #pragma unroll
@@ -632,80 +1002,28 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
                 tmem_ld16_nowait(la + kTmS + 32 * part + 16 * b, d);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; j++) S[16 * b + j] = fmaf(dec, S[16 * b + j], __uint_as_float(d[j]));
+                for (int j4 = 0; j4 < 4; j4++) {
+                    float4 e = make_float4(dec, dec, dec, dec);
+                    if (kChannel) e = *reinterpret_cast<const float4 *>(&sh.dec[c & 1][32 * part + 16 * b + 4 * j4]);
+                    float *s = &S[16 * b + 4 * j4];
+                    s[0] = fmaf(e.x, s[0], __uint_as_float(d[4 * j4]));
+                    s[1] = fmaf(e.y, s[1], __uint_as_float(d[4 * j4 + 1]));
+                    s[2] = fmaf(e.z, s[2], __uint_as_float(d[4 * j4 + 2]));
+                    s[3] = fmaf(e.w, s[3], __uint_as_float(d[4 * j4 + 3]));
+                }
             }
             if (c + 1 < nc) put_state();
         }
         if (!sh.bail)
 #pragma unroll
             for (int j = 0; j < 32; j++) a.state_out[sbase + (size_t)(32 * part + j) * kD + v] = S[j];
-    } else if (warp < kChWarpMma) {
-        // ---------------- O: value column v, every token of the chunk; and the scales
+    } else if (warp < kChWarpMake) {
+        // ---------------- O: value column v, every token of the chunk
         const int q = warp & 3, v = 32 * q + lane;
         const uint32_t la = tmem + ((uint32_t)(32 * q) << 16);
-        // The scales of chunk c, a thread a row of K (0-63) or Q (64-127).
-        auto scales = [&](int c) {
-            const int n = min(kC, len - kC * c), t = v & (kC - 1), st = c % kChStages;
-            const bool is_k = v < kC;
-            const size_t tok = (size_t)(first + kC * c);
-            float g0 = lane < n ? a.g[(tok + lane) * a.H + h] : 0.0f;
-            float g1 = lane + 32 < n ? a.g[(tok + lane + 32) * a.H + h] : 0.0f;
-            const float bt = t < n ? a.beta[(tok + t) * a.H + h] : 0.0f;
-            g0 = g0 < -200.0f ? -200.0f : g0;
-            g1 = g1 < -200.0f ? -200.0f : g1;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float p0 = __shfl_up_sync(0xffffffffu, g0, o), p1 = __shfl_up_sync(0xffffffffu, g1, o);
-                if (lane >= o) { g0 += p0; g1 += p1; }
-            }
-            g1 += __shfl_sync(0xffffffffu, g0, 31);
-            const float G = (q & 1) ? g1 : g0, GC = __shfl_sync(0xffffffffu, g1, 31);
-            if (!wait(sh.kq_full[st], c / kChStages)) return false;
-            uint8_t *x = sm + (size_t)st * kChStageBytes + v * 128;
-            float norm = 1.0f;
-            if (a.qk_norm) {
-                float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 16; j++) {                // chunk order is the swizzle's: a sum does not mind
-                    const uint4 w = *reinterpret_cast<const uint4 *>(x + (j >> 3) * kChBox + (((j & 7) ^ (v & 7)) << 4));
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int r = 0; r < 4; r++) {
-                        const float lo = __uint_as_float(u[r] << 16), hi = __uint_as_float(u[r] & 0xFFFF0000u);
-                        s0 = fmaf(lo, lo, s0);
-                        s1 = fmaf(hi, hi, s1);
-                    }
-                }
-                norm = 1.0f / sqrtf(s0 + s1 + a.eps);
-            }
-            const bool in = t < n;
-            if (!in && is_k)                                  // the rows past the sequence's end take no part in K^T U
-#pragma unroll
-                for (int j = 0; j < 16; j++)
-                    *reinterpret_cast<uint4 *>(x + (j >> 3) * kChBox + ((j & 7) << 4)) = make_uint4(0, 0, 0, 0);
-            ChunkShared::Scales &sc = sh.sc[c % kChScales];
-            const float eG = expf(G);
-            if (is_k) {
-                sc.g2[t] = G * kLog2e;
-                sc.gk[t] = in ? G * kLog2e - log2f(norm) : __int_as_float(0x7f800000);
-                sc.beta[t] = bt;
-                sc.kb[t] = in ? bt * norm : 0.0f;
-                sc.kr[t] = in ? norm * eG : 0.0f;
-                sc.kd[t] = in ? norm * expf(GC - G) : 0.0f;
-                if (t == 0) sc.dec = expf(GC);
-            } else {
-                sc.qn[t] = in ? a.scale * norm : 0.0f;
-                sc.qr[t] = in ? a.scale * norm * eG : 0.0f;
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mb_arrive(&sh.sc_ready[c % kChScales]);
-            return true;
-        };
-        bool ok = scales(0) && (nc < 2 || scales(1));
-        for (int c = 0; c < nc && ok; c++) {
+        for (int c = 0; c < nc; c++) {
             const int n = min(kC, len - kC * c);
-            const ChunkShared::Scales &sc = sh.sc[c % kChScales];
+            const float *sc = reinterpret_cast<const float *>(stage(c) + kOffTp + kTpBytes);
             if (!wait(sh.o_full, c)) break;
             tc_fence_after();
             // neighbouring lanes trade a token each: two columns of one token a store
@@ -716,15 +1034,20 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
             for (int b = 0; b < 8; b++) {
                 uint32_t d[8], p[8];
                 tmem_ld8_nowait(la + kTmOq + 8 * b, d);
-                tmem_ld8_nowait(la + kTmOp + 8 * b, p);
+                if (!kChannel) tmem_ld8_nowait(la + kTmOp + 8 * b, p);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j4 = 0; j4 < 2; j4++) {
-                    const float4 qr = *reinterpret_cast<const float4 *>(&sc.qr[8 * b + 4 * j4]);
-                    const float r[4] = {qr.x, qr.y, qr.z, qr.w};
                     float x[4];
+                    if (kChannel) {
 #pragma unroll
-                    for (int j = 0; j < 4; j++) x[j] = fmaf(r[j], __uint_as_float(d[4 * j4 + j]), __uint_as_float(p[4 * j4 + j]));
+                        for (int j = 0; j < 4; j++) x[j] = __uint_as_float(d[4 * j4 + j]);
+                    } else {
+                        const float4 qr = *reinterpret_cast<const float4 *>(&sc[kRecQr + 8 * b + 4 * j4]);
+                        const float r[4] = {qr.x, qr.y, qr.z, qr.w};
+#pragma unroll
+                        for (int j = 0; j < 4; j++) x[j] = fmaf(r[j], __uint_as_float(d[4 * j4 + j]), __uint_as_float(p[4 * j4 + j]));
+                    }
 #pragma unroll
                     for (int j = 0; j < 2; j++) {
                         const float got = __shfl_xor_sync(0xffffffffu, mine ? x[2 * j] : x[2 * j + 1], 1);
@@ -735,91 +1058,153 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
                 }
             }
             arrive(sh.o_free);
-            if (c + 2 < nc) ok = scales(c + 2);
         }
-    } else if (warp == kChWarpMma) {
+    } else if (kChannel && warp < kChWarpMake + kChMake) {
+        // ---------------- per channel: the weighted operands of chunk c, two channels and 16
+        // tokens a thread
+        const int id = threadIdx.x - kChWarpMake * 32, pair = id & 63, tq = id >> 6, ch = 2 * pair, t0 = 16 * tq;
+        for (int c = 0; c < nc; c++) {
+            const int n = min(kC, len - kC * c);
+            const size_t tok0 = (size_t)(first + kC * c);
+            const float *rf = reinterpret_cast<const float *>(record(c) + kTpBytes);
+            uint32_t k[16], q[16];
+            float2 g[16];
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const size_t tok = tok0 + min(t0 + i, n - 1);
+                k[i] = *reinterpret_cast<const uint32_t *>(a.k + tok * a.k_stride + hq * kD + ch);
+                q[i] = *reinterpret_cast<const uint32_t *>(a.q + tok * a.q_stride + hq * kD + ch);
+                g[i] = *reinterpret_cast<const float2 *>(a.g + (tok * a.H + h) * kD + ch);
+            }
+            // the decay's sums before and after this thread's tokens
+            float2 L = make_float2(0.f, 0.f), E = L, all = L;
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+                const float2 x = *reinterpret_cast<const float2 *>(&rf[kRecSum + w * kD + ch]);
+                if (w < tq) { L.x += x.x; L.y += x.y; }
+                if (w > tq) { E.x += x.x; E.y += x.y; }
+                all.x += x.x;
+                all.y += x.y;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const bool in = t0 + i < n;
+                g[i].x = in ? clamp_gate(g[i].x) * kLog2e : 0.0f;
+                g[i].y = in ? clamp_gate(g[i].y) * kLog2e : 0.0f;
+            }
+            if (c >= 1 && !wait(sh.q_done, c - 1)) break;     // the last chunk's K and Q are used
+            if (tq == 0) *reinterpret_cast<float2 *>(&sh.dec[c & 1][ch]) = make_float2(exp2_approx(all.x), exp2_approx(all.y));
+            uint8_t *kq = made + (pair >> 5) * kChBox;
+            uint8_t *late = made + 4 * kChTerm + (c & 1) * 2 * kChTerm + (pair >> 5) * kChBox;
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const int t = t0 + i;
+                const uint32_t at = t * 128 + ((((uint32_t)lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
+                const float rk = rf[kRecRk + t], qn = rf[kRecQn + t];
+                L.x += g[i].x;
+                L.y += g[i].y;
+                const float ex = exp2_approx(L.x), ey = exp2_approx(L.y);
+                uint32_t hi, mid;
+                split2(__uint_as_float(k[i] << 16) * (rk * ex), __uint_as_float(k[i] & 0xFFFF0000u) * (rk * ey), &hi, &mid);
+                *reinterpret_cast<uint32_t *>(kq + at) = hi;
+                *reinterpret_cast<uint32_t *>(kq + kChTerm + at) = mid;
+                split2(__uint_as_float(q[i] << 16) * (qn * ex), __uint_as_float(q[i] & 0xFFFF0000u) * (qn * ey), &hi, &mid);
+                *reinterpret_cast<uint32_t *>(kq + 2 * kChTerm + at) = hi;
+                *reinterpret_cast<uint32_t *>(kq + 3 * kChTerm + at) = mid;
+            }
+#pragma unroll
+            for (int i = 15; i >= 0; i--) {                   // backwards: exp(G_C - G_t), from the end's sum
+                const int t = t0 + i;
+                const uint32_t at = t * 128 + ((((uint32_t)lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
+                const float rk = rf[kRecRk + t];              // 0 past the sequence's end
+                uint32_t hi, mid;
+                const float x = __uint_as_float(k[i] << 16) * (rk * exp2_approx(E.x));
+                const float y = __uint_as_float(k[i] & 0xFFFF0000u) * (rk * exp2_approx(E.y));
+                split2(t < n ? x : 0.0f, t < n ? y : 0.0f, &hi, &mid);
+                *reinterpret_cast<uint32_t *>(late + at) = hi;
+                *reinterpret_cast<uint32_t *>(late + kChTerm + at) = mid;
+                E.x += g[i].x;
+                E.y += g[i].y;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mb_arrive(&sh.made);
+        }
+    } else if (warp == kWarpMma) {
         // ---------------- loads and MMA issue
         const uint32_t idk = idesc(1, kC);                     // 128 x 64, both operands K-major
         const uint32_t idn = idk | (1u << 16);                 // B with N contiguous (K^T U: channels)
-        const uint32_t aT = saddr(tT), aP = saddr(tP);
-        // K K^T and Q K^T of chunk c: rows of K over rows of Q, against K
-        auto kk = [&](int c) {
-            const uint32_t b = saddr(sm + (size_t)(c % kChStages) * kChStageBytes);
-            const uint64_t bd = sdesc(b);
-#pragma unroll
-            for (int s = 0; s < 8; s++) {
-                const uint64_t at = bd + (((s >> 2) * kChBox + (s & 3) * 32) >> 4);
-                umma_warp(kTmKK, at, at, idk, s > 0);
+        auto load = [&](int c) {
+            uint8_t *p = stage(c);
+            uint64_t *bar = &sh.in_full[c % kStages];
+            const uint32_t tp = kChannel ? kTpBytes : kChTpCopyHead;
+            mb_expect_tx(bar, (kChannel ? 0 : kChKq) + kChV + tp);
+            for (int b = 0; b < 2; b++) {
+                if (!kChannel) {
+                    tma2d(p + 2 * b * kChBox, &mk, hq * kD + 64 * b, first + kC * c, bar);
+                    tma2d(p + 2 * b * kChBox + kChBox, &mq, hq * kD + 64 * b, first + kC * c, bar);
+                }
+                tma2d(p + kOffV + b * kChBox, &mv, h * kD + 64 * b, first + kC * c, bar);
             }
+            bulk_g2s(p + kOffTp, record(c), tp, bar);
         };
-        // D[v][t >= 16 j] += X[v][16 tokens j] tile[t][16 tokens j], the tile lower triangular:
-        // the terms of X at columns `x`, of the tile kChTile apart
-        auto tri = [&](uint32_t d, uint32_t x, uint32_t tile) {
-            const uint64_t td = sdesc(tile);
+        // D[v][t >= 16 j] += X[v][16 tokens j] tile[t][16 tokens j], the tile lower triangular
+        // (hi, mid terms), X's terms at columns `x`
+        auto tri = [&](uint32_t d, uint32_t x, uint32_t tile, bool acc) {
+            const uint64_t td = tdesc(tile);
 #pragma unroll
             for (int term = 0; term < 3; term++)               // hi hi, hi mid, mid hi
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     umma_ts_warp(d + 16 * j, x + (term == 2 ? 32 : 0) + 8 * j,
-                            td + (((term == 1 ? kChTile : 0) + 16 * j * 128 + j * 32) >> 4), idesc(1, kC - 16 * j),
-                            term > 0 || j > 0);
+                                 td + (((term == 1 ? kTermBytes : 0) + term_block(j)) >> 4), idesc(1, kC - 16 * j),
+                                 acc || term > 0 || j > 0);
         };
-        auto load = [&](int c) {
-            uint8_t *p = sm + (size_t)(c % kChStages) * kChStageBytes;
-            uint64_t *bar = &sh.kq_full[c % kChStages];
-            mb_expect_tx(bar, kChStageBytes);
-            for (int b = 0; b < 2; b++) {
-                tma2d(p + b * kChBox, &mk, hq * kD + 64 * b, first + kC * c, bar);
-                tma2d(p + b * kChBox + kC * 128, &mq, hq * kD + 64 * b, first + kC * c, bar);
-                tma2d(p + kChV + b * kC * 128, &mv, h * kD + 64 * b, first + kC * c, bar);
-            }
+        // X S^T: X's boxes at `x` (a box of 64 channels `box` bytes after the other); per channel
+        // its mid term kChTerm behind
+        auto with_state = [&](uint32_t d, uint64_t x, int box) {
+#pragma unroll
+            for (int term = 0; term < (kChannel ? 3 : 2); term++)   // S hi, S mid, and S hi with X mid
+#pragma unroll
+                for (int s = 0; s < 8; s++)
+                    umma_ts_warp(d, kTmS + 32 * (s >> 1) + 16 * (term == 1) + 8 * (s & 1),
+                                 x + (((term == 2 ? kChTerm : 0) + (s >> 2) * box + (s & 3) * 32) >> 4), idk, term > 0 || s > 0);
         };
         if (lane == 0)
-            for (int c = 0; c < min(nc, 2); c++) load(c);
+            for (int c = 0; c < min(nc, kStages - 1); c++) load(c);
         __syncwarp();
-        bool ok = wait(sh.kq_full[0], 0);
-        if (ok) {
-            kk(0);
-            umma_commit_warp(&sh.kk_full);
-        }
-        for (int c = 0; c < nc && ok; c++) {
-            const uint64_t kq = sdesc(saddr(sm + (size_t)(c % kChStages) * kChStageBytes));
-            if (!wait(sh.s_ready, c)) break;
+        for (int c = 0; c < nc; c++) {
+            if (!wait(sh.in_full[c % kStages], c / kStages) || (kChannel && !wait(sh.made, c)) || !wait(sh.s_ready, c)) break;
             tc_fence_after();
-#pragma unroll
-            for (int s = 0; s < 16; s++)                       // K S, hi and mid
-                umma_ts_warp(kTmR, kTmS + 32 * ((s >> 1) & 3) + 16 * (s >> 3) + 8 * (s & 1),
-                             kq + ((((s >> 2) & 1) * kChBox + (s & 3) * 32) >> 4), idk, s > 0);
+            const uint32_t st = saddr(stage(c)), mk0 = saddr(made);
+            const uint64_t kx = sdesc(kChannel ? mk0 : st), qx = sdesc(kChannel ? mk0 + 2 * kChTerm : st + kChBox);
+            with_state(kTmR, kx, kChannel ? kChBox : 2 * kChBox);
             umma_commit_warp(&sh.d1_full);
-            if (c + 1 < nc) {
-                // the wait for chunk c - 1's O lets the preparation of chunk c + 1 write over that chunk's scales and P
-                if (!wait(sh.kq_full[(c + 1) % kChStages], (c + 1) / kChStages) || !wait(sh.kk_free, c) ||
-                    (c >= 1 && !wait(sh.o_free, c - 1)))
-                    break;
-                tc_fence_after();
-                kk(c + 1);
-                umma_commit_warp(&sh.kk_full);
-            }
-            if (c + 2 < nc && lane == 0) load(c + 2);          // chunk c - 1 is done with its stage: its state was here
+            if (c >= 1 && !wait(sh.o_free, c - 1)) break;      // chunk c - 1 is done with O's columns and its stage
+            tc_fence_after();
+            with_state(kTmOq, qx, kChannel ? kChBox : 2 * kChBox);
+            umma_commit_warp(&sh.q_done);
+            if (c + kStages - 1 < nc && lane == 0) load(c + kStages - 1);
             __syncwarp();
-            if (!wait(sh.tp_ready, c) || !wait(sh.r_ready, c)) break;
+            if (!wait(sh.r_ready, c)) break;
             tc_fence_after();
-            tri(kTmR, kTmRU, aT);
+            const uint32_t tp = st + kOffTp;
+            tri(kTmR, kTmRU, tp, false);
             umma_commit_warp(&sh.d2_full);
-            if (c >= 1 && c + 1 == nc && !wait(sh.o_free, c - 1)) break;   // the last chunk has not waited above
-            tc_fence_after();
-#pragma unroll
-            for (int s = 0; s < 16; s++)                       // Q S
-                umma_ts_warp(kTmOq, kTmS + 32 * ((s >> 1) & 3) + 16 * (s >> 3) + 8 * (s & 1),
-                             kq + ((((s >> 2) & 1) * kChBox + kC * 128 + (s & 3) * 32) >> 4), idk, s > 0);
             if (!wait(sh.u_ready, c)) break;
             tc_fence_after();
+            const uint64_t lx = sdesc(kChannel ? mk0 + 4 * kChTerm + (c & 1) * 2 * kChTerm : st);
 #pragma unroll
-            for (int s = 0; s < 16; s++)                       // K^T U into the state's sums, a half of k at a time
-                umma_ts_warp(kTmS + 64 * (s >> 3), kTmRU + 32 * ((s >> 2) & 1) + 8 * (s & 3),
-                             kq + (((s >> 3) * kChBox + (s & 3) * 16 * 128) >> 4), idn, (s & 7) > 0);
+            for (int half = 0; half < 2; half++)               // K^T U into the state's sums, a half of k at a time
+#pragma unroll
+                for (int term = 0; term < (kChannel ? 3 : 2); term++)
+#pragma unroll
+                    for (int s = 0; s < 4; s++)
+                        umma_ts_warp(kTmS + 64 * half, kTmRU + 32 * (term == 1) + 8 * s,
+                                     lx + (((term == 2 ? kChTerm : 0) + half * (kChannel ? kChBox : 2 * kChBox) + s * 16 * 128) >> 4),
+                                     idn, term > 0 || s > 0);
             umma_commit_warp(&sh.d4_full);
-            tri(kTmOp, kTmU, aP + (c & 1) * 2 * kChTile);
+            tri(kChannel ? kTmOq : kTmOp, kChannel ? kTmRU : kTmU, tp + 2 * kTermBytes, kChannel);
             umma_commit_warp(&sh.o_full);
         }
         __syncwarp();
@@ -829,21 +1214,15 @@ __global__ void __launch_bounds__(kChThreads, 1) delta_chunk_kernel(const DeltaA
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kChWarpMma)
+    if (warp == kWarpMma)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(512));
 }
 
-}  // namespace
+// From this many tokens a sequence on average, chunks.
+constexpr int kChunkTokensAvg = 24;
 
-size_t delta_workspace(const k3moe_delta_config &dc, int n_seq, int T)
-{
-    (void)dc;
-    (void)n_seq;
-    (void)T;
-    return kCtrOffset + kCtrBytes;
-}
-
-static cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
+template <bool kChannel>
+cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
 {
     CUtensorMap mq{}, mk{}, mv{};
     const uint64_t cols = (uint64_t)a.Hq * kD;
@@ -851,22 +1230,51 @@ static cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
         !map16s(&mk, a.k, (uint64_t)a.T, cols, (uint64_t)a.k_stride, kC) ||
         !map16s(&mv, a.v, (uint64_t)a.T, (uint64_t)a.H * kD, (uint64_t)a.v_stride, kC))
         return cudaErrorInvalidValue;
-    static bool smem_set = false;
-    if (!smem_set) {
-        cudaFuncSetAttribute(delta_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChSmem);
-        smem_set = true;
+    using Shape = ChunkShape<kChannel>;
+    static bool ready = false;
+    if (!ready) {
+        // the shares of setmaxnreg are of the launch's registers: with another count they would never be there
+        cudaFuncAttributes fa{};
+        if (kChannel && (cudaFuncGetAttributes(&fa, delta_chunk_kernel<kChannel>) != cudaSuccess || fa.numRegs != kChRegs))
+            return cudaErrorInvalidConfiguration;
+        cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<kChannel>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(delta_prepare_kernel<kChannel>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)pp_smem(kChannel));
+        if (e != cudaSuccess) return e;
+        ready = true;
     }
+    const long long recs = chunk_records(a.n_seq, a.T);
+    timing_begin("delta_prepare", s);
+    cudaError_t err = launch_pdl(delta_prepare_kernel<kChannel>, dim3((unsigned)(recs * a.H)), dim3(kPpThreads),
+                                 pp_smem(kChannel), s, a, mq, mk);
+    count_launch();
+    timing_end("delta_prepare", s);
+    if (err != cudaSuccess) return err;
     timing_begin("delta_chunk", s);
-    const cudaError_t err =
-        launch_pdl(delta_chunk_kernel, dim3((unsigned)(a.n_seq * a.H)), dim3(kChThreads), kChSmem, s, a, mq, mk, mv);
+    err = launch_pdl(delta_chunk_kernel<kChannel>, dim3((unsigned)(a.n_seq * a.H)), dim3(Shape::threads), Shape::smem, s,
+                     a, mq, mk, mv);
     count_launch();
     timing_end("delta_chunk", s);
     return err;
 }
 
+}  // namespace
+
+size_t delta_workspace(const k3moe_delta_config &dc, int n_seq, int T)
+{
+    // the most records of any call of at most n_seq sequences and T tokens: chunks need
+    // kChunkTokensAvg tokens a sequence
+    size_t bytes = kCtrOffset + kCtrBytes;
+    if (T >= kChunkTokensAvg && n_seq > 0)
+        bytes += (size_t)chunk_records(std::min(n_seq, T / kChunkTokensAvg), T) * dc.n_heads * kRecBytes;
+    return bytes;
+}
+
 cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t s)
 {
-    if (a.gate == 1 && a.T >= 24 * a.n_seq) return launch_chunks(a, s);
+    if (a.T >= kChunkTokensAvg * a.n_seq)
+        return a.gate == 1 ? launch_chunks<false>(a, s) : launch_chunks<true>(a, s);
     // one block per head while they fill the GPU twice over; else 32 columns a block
     const long long blocks = (long long)a.n_seq * a.H;
     timing_begin("delta_recurrent", s);
