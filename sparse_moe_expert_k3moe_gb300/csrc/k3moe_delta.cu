@@ -215,14 +215,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinGate = -90.0f;
 constexpr int kTermBytes = 5120;                              // T or P, one term: 16-column blocks j of rows 16 j..63
 constexpr int kTpBytes = 4 * kTermBytes;                      // T hi, T mid, P hi, P mid
-constexpr int kRecFloats = 640;
+constexpr int kRecFloats = 768;
 constexpr int kRecBytes = kTpBytes + kRecFloats * 4;          // a chunk and head's record in the workspace
-// The record's floats.  Decay per head: kr = exp(G_t) / |k_t|, kd = exp(G_C - G_t) / |k_t|,
-// qr = scale exp(G_t) / |q_t|, and exp(G_C); per channel: rk = 1 / |k_t|, qn = scale / |q_t|,
-// and log2 decays summed over each 16 tokens [4][D].  (Norms are 1 without qk_norm; all
-// are 0 past the sequence's end.)
-constexpr int kRecKr = 0, kRecKd = 64, kRecQr = 128, kRecDec = 192;
-constexpr int kRecRk = 0, kRecQn = 64, kRecSum = 128;
+// The record's floats, a token each: kr and qr weigh the columns of K S and Q S, kd what
+// enters the state.  Decay per head: kr = exp(G_t) / |k_t|, qr = scale exp(G_t) / |q_t|, kd =
+// exp(G_C - G_t) / |k_t|, and one exp(G_C).  Per channel, where the operands carry the decay:
+// kr = 1 / |k_t|, qr = scale / |q_t|, kd = log2 kr, and the log2 decays' sums over each 16
+// tokens [4][D].  (Norms are 1 without qk_norm; past the sequence's end all are 0, log2 kr
+// minus infinity.)
+constexpr int kRecKr = 0, kRecKd = 64, kRecQr = 128, kRecDec = 192, kRecSum = 256;
 __host__ __device__ constexpr int term_block(int j) { return 2048 * j - 256 * j * (j - 1); }
 
 // A sequence's chunk c has the workspace record (seq_start / 64 + seq + c, head): a sequence
@@ -235,6 +236,12 @@ __device__ __forceinline__ float exp2_approx(float x)
 {
     float y;
     asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float exp2_fast(float x)          // the same, free to move
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 // (x, y) as two packed bf16 terms: hi rounded to nearest, mid the rounded remainder.
@@ -664,8 +671,9 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
             sh.kb[t] = b * rk;
             sh.qn[t] = qn;
             sh.beta[t] = b;
-            outf[kRecRk + t] = rk;
-            outf[kRecQn + t] = qn;
+            outf[kRecKr + t] = rk;
+            outf[kRecKd + t] = log2f(rk);
+            outf[kRecQr + t] = qn;
         }
         if (!sh.bad) wait(sh.done, 1);
         __syncthreads();
@@ -773,8 +781,10 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
 // shared tiles.
 //   decay per head: K and Q as they are (exact in bf16); exp(G) weighs the results' columns,
 //     and U's a second time before K^T U;
-//   per channel: four warps' worth of threads more write exp(G) K, exp(G) Q and
-//     exp(G_C - G) K as two terms each, a chunk ahead.
+//   per channel: eight warps more write exp(G) K, exp(G) Q and exp(G_C - G) K / |k| as two
+//     terms each, a chunk ahead.
+// K S and Q S are one product with the 64 rows of K over those of Q as its 128 columns (an
+// MMA of 64 columns takes as long as one of 128 here: about 65 clocks).
 // A stage's latency is a chain of short dependent steps (a product, its sums to registers,
 // two terms back), so each has as many warps as the registers allow (64 a thread).
 constexpr int kChChain = 16, kChOut = 4, kChMake = 8;
@@ -782,11 +792,11 @@ constexpr int kChStagesHead = 3, kChStagesChannel = 2;
 constexpr int kChBox = kC * 128;                              // 64 tokens x 64 channels: 8 KB
 constexpr int kChKq = 4 * kChBox;                             // decay per head: K and Q, [box][K, Q]
 constexpr int kChV = 2 * kChBox;
-constexpr int kChTp = 21 * 1024;                              // T and P, and decay per head the scales
-constexpr int kChTpCopyHead = kTpBytes + 1024;
+constexpr int kChTp = 21 * 1024;                              // T and P and the scales
+constexpr int kChTpCopy = kTpBytes + 1024;                    // with the record's first floats
 constexpr int kChStageHead = kChKq + kChV + kChTp, kChStageChannel = kChV + kChTp;
 constexpr int kChTerm = 2 * kChBox;                           // per channel: one term of 64 x 128
-constexpr int kChMade = 4 * kChTerm + 4 * kChTerm;            // K, Q [hi, mid]; the late K [chunk parity][hi, mid]
+constexpr int kChMade = 4 * kChTerm + 4 * kChTerm;            // [hi, mid][box][K, Q]; the late K [chunk parity][hi, mid][box]
 static_assert(kTpBytes + (kRecDec + 1) * 4 <= kChTp && kTpBytes + 1024 <= kChTp, "a stage holds the record's head");
 template <bool kChannel> struct ChunkShape {
     static constexpr int warps = kChChain + kChOut + (kChannel ? kChMake : 0) + 1;
@@ -803,14 +813,14 @@ static_assert(4 * kChRegs + 2 * kChRegsMake + kChRegsOut + kChRegsMma <= 8 * kCh
 // tensor memory columns
 constexpr uint32_t kTmS = 0;      // S^T as an operand, [quarter of k][hi, mid][16]; the new S's sums over it
 constexpr uint32_t kTmR = 128;    // K S, then T R
-constexpr uint32_t kTmOq = 192;   // Q S (per channel: O)
+constexpr uint32_t kTmOq = 192;   // Q S
 constexpr uint32_t kTmOp = 256;   // P U
 constexpr uint32_t kTmRU = 320;   // R, then U (per head: weighted for the state), as an operand [hi, mid][32]
 constexpr uint32_t kTmU = 384;    // per head: U as an operand [hi, mid][32]
 
 struct ChunkShared {
     uint64_t in_full[3];
-    uint64_t s_ready, d1_full, q_done, r_ready, d2_full, u_ready, d4_full, o_full, o_free, made, drain;
+    uint64_t s_ready, d1_full, r_ready, d2_full, u_ready, d4_full, o_full, o_free, made, drain;
     uint32_t tmem;
     volatile int bail;
     alignas(16) float dec[2][kD];                             // per channel: exp(G_C), by chunk parity
@@ -862,7 +872,6 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         for (int s = 0; s < kStages; s++) mb_init(&sh.in_full[s], 1);
         mb_init(&sh.s_ready, kChChain);
         mb_init(&sh.d1_full, 1);
-        mb_init(&sh.q_done, 1);
         mb_init(&sh.r_ready, kChChain);
         mb_init(&sh.d2_full, 1);
         mb_init(&sh.u_ready, kChChain);
@@ -930,7 +939,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         put_state();
         for (int c = 0; c < nc; c++) {
             const int n = min(kC, len - kC * c);
-            const float *sc = reinterpret_cast<const float *>(stage(c) + kOffTp + kTpBytes) + t0;     // per head
+            const float *sc = reinterpret_cast<const float *>(stage(c) + kOffTp + kTpBytes) + t0;
             // V[t][v] in its swizzled tile
             const uint8_t *vt = stage(c) + kOffV + (q >> 1) * kChBox + t0 * 128 + (v & 7) * 2;
             const uint32_t v8 = (uint32_t)(v >> 3) & 7u;
@@ -954,7 +963,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
 #pragma unroll
                     for (int j2 = 0; j2 < 4; j2++) {
                         const int j = 8 * b + 2 * j2;
-                        const float2 kr = kChannel ? make_float2(1.0f, 1.0f) : *reinterpret_cast<const float2 *>(&sc[kRecKr + j]);
+                        const float2 kr = *reinterpret_cast<const float2 *>(&sc[kRecKr + j]);
                         const float x = fmaf(-kr.x, __uint_as_float(d[j]), __uint_as_float(vv[j >> 1] << 16));
                         const float y = fmaf(-kr.y, __uint_as_float(d[j + 1]), __uint_as_float(vv[j >> 1] & 0xFFFF0000u));
                         split2(t0 + j < n ? x : 0.0f, t0 + j + 1 < n ? y : 0.0f, &hi[j2], &mid[j2]);
@@ -1026,38 +1035,31 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             const float *sc = reinterpret_cast<const float *>(stage(c) + kOffTp + kTpBytes);
             if (!wait(sh.o_full, c)) break;
             tc_fence_after();
+            uint32_t w[32];                                   // two tokens a word
+#pragma unroll
+            for (int b = 0; b < 8; b++) {
+                uint32_t d[8], p[8];
+                tmem_ld8_nowait(la + kTmOq + 8 * b, d);
+                tmem_ld8_nowait(la + kTmOp + 8 * b, p);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 r = *reinterpret_cast<const float2 *>(&sc[kRecQr + 8 * b + j]);
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(fmaf(r.x, __uint_as_float(d[j]), __uint_as_float(p[j])),
+                                                                   fmaf(r.y, __uint_as_float(d[j + 1]), __uint_as_float(p[j + 1])));
+                    w[4 * b + j / 2] = *reinterpret_cast<const uint32_t *>(&x);
+                }
+            }
+            arrive(sh.o_free);
             // neighbouring lanes trade a token each: two columns of one token a store
             const int mine = lane & 1;
             uint32_t *o = reinterpret_cast<uint32_t *>(a.out + ((size_t)(first + kC * c + mine) * a.H + h) * kD + (v & ~1));
             const size_t step = (size_t)a.H * kD;             // words of two tokens
-#pragma unroll 1
-            for (int b = 0; b < 8; b++) {
-                uint32_t d[8], p[8];
-                tmem_ld8_nowait(la + kTmOq + 8 * b, d);
-                if (!kChannel) tmem_ld8_nowait(la + kTmOp + 8 * b, p);
-                tmem_wait_ld();
 #pragma unroll
-                for (int j4 = 0; j4 < 2; j4++) {
-                    float x[4];
-                    if (kChannel) {
-#pragma unroll
-                        for (int j = 0; j < 4; j++) x[j] = __uint_as_float(d[4 * j4 + j]);
-                    } else {
-                        const float4 qr = *reinterpret_cast<const float4 *>(&sc[kRecQr + 8 * b + 4 * j4]);
-                        const float r[4] = {qr.x, qr.y, qr.z, qr.w};
-#pragma unroll
-                        for (int j = 0; j < 4; j++) x[j] = fmaf(r[j], __uint_as_float(d[4 * j4 + j]), __uint_as_float(p[4 * j4 + j]));
-                    }
-#pragma unroll
-                    for (int j = 0; j < 2; j++) {
-                        const float got = __shfl_xor_sync(0xffffffffu, mine ? x[2 * j] : x[2 * j + 1], 1);
-                        const __nv_bfloat162 w = __floats2bfloat162_rn(mine ? got : x[2 * j], mine ? x[2 * j + 1] : got);
-                        if (8 * b + 4 * j4 + 2 * j + mine < n) *o = *reinterpret_cast<const uint32_t *>(&w);
-                        o += step;
-                    }
-                }
+            for (int j = 0; j < 32; j++, o += step) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, w[j], 1);
+                if (2 * j + mine < n) *o = mine ? __byte_perm(got, w[j], 0x7632) : __byte_perm(w[j], got, 0x5410);
             }
-            arrive(sh.o_free);
         }
     } else if (kChannel && warp < kChWarpMake + kChMake) {
         // ---------------- per channel: the weighted operands of chunk c, two channels and 16
@@ -1072,15 +1074,15 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
 #pragma unroll
             for (int i = 0; i < 16; i++) {
                 const size_t tok = tok0 + min(t0 + i, n - 1);
-                k[i] = *reinterpret_cast<const uint32_t *>(a.k + tok * a.k_stride + hq * kD + ch);
-                q[i] = *reinterpret_cast<const uint32_t *>(a.q + tok * a.q_stride + hq * kD + ch);
-                g[i] = *reinterpret_cast<const float2 *>(a.g + (tok * a.H + h) * kD + ch);
+                k[i] = __ldg(reinterpret_cast<const uint32_t *>(a.k + tok * a.k_stride + hq * kD + ch));
+                q[i] = __ldg(reinterpret_cast<const uint32_t *>(a.q + tok * a.q_stride + hq * kD + ch));
+                g[i] = __ldg(reinterpret_cast<const float2 *>(a.g + (tok * a.H + h) * kD + ch));
             }
             // the decay's sums before and after this thread's tokens
             float2 L = make_float2(0.f, 0.f), E = L, all = L;
 #pragma unroll
             for (int w = 0; w < 4; w++) {
-                const float2 x = *reinterpret_cast<const float2 *>(&rf[kRecSum + w * kD + ch]);
+                const float2 x = __ldg(reinterpret_cast<const float2 *>(&rf[kRecSum + w * kD + ch]));
                 if (w < tq) { L.x += x.x; L.y += x.y; }
                 if (w > tq) { E.x += x.x; E.y += x.y; }
                 all.x += x.x;
@@ -1092,39 +1094,41 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                 g[i].x = in ? clamp_gate(g[i].x) * kLog2e : 0.0f;
                 g[i].y = in ? clamp_gate(g[i].y) * kLog2e : 0.0f;
             }
-            if (c >= 1 && !wait(sh.q_done, c - 1)) break;     // the last chunk's K and Q are used
-            if (tq == 0) *reinterpret_cast<float2 *>(&sh.dec[c & 1][ch]) = make_float2(exp2_approx(all.x), exp2_approx(all.y));
-            uint8_t *kq = made + (pair >> 5) * kChBox;
+            if (c >= 1 && !wait(sh.d1_full, c - 1)) break;    // the last chunk's K and Q are used
+            if (tq == 0) *reinterpret_cast<float2 *>(&sh.dec[c & 1][ch]) = make_float2(exp2_fast(all.x), exp2_fast(all.y));
+            uint8_t *kq = made + (pair >> 5) * 2 * kChBox;
             uint8_t *late = made + 4 * kChTerm + (c & 1) * 2 * kChTerm + (pair >> 5) * kChBox;
 #pragma unroll
             for (int i = 0; i < 16; i++) {
                 const int t = t0 + i;
                 const uint32_t at = t * 128 + ((((uint32_t)lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
-                const float rk = rf[kRecRk + t], qn = rf[kRecQn + t];
                 L.x += g[i].x;
                 L.y += g[i].y;
-                const float ex = exp2_approx(L.x), ey = exp2_approx(L.y);
+                const float ex = exp2_fast(L.x), ey = exp2_fast(L.y);
                 uint32_t hi, mid;
-                split2(__uint_as_float(k[i] << 16) * (rk * ex), __uint_as_float(k[i] & 0xFFFF0000u) * (rk * ey), &hi, &mid);
+                split2(__uint_as_float(k[i] << 16) * ex, __uint_as_float(k[i] & 0xFFFF0000u) * ey, &hi, &mid);
                 *reinterpret_cast<uint32_t *>(kq + at) = hi;
-                *reinterpret_cast<uint32_t *>(kq + kChTerm + at) = mid;
-                split2(__uint_as_float(q[i] << 16) * (qn * ex), __uint_as_float(q[i] & 0xFFFF0000u) * (qn * ey), &hi, &mid);
-                *reinterpret_cast<uint32_t *>(kq + 2 * kChTerm + at) = hi;
-                *reinterpret_cast<uint32_t *>(kq + 3 * kChTerm + at) = mid;
+                *reinterpret_cast<uint32_t *>(kq + 2 * kChTerm + at) = mid;
+                split2(__uint_as_float(q[i] << 16) * ex, __uint_as_float(q[i] & 0xFFFF0000u) * ey, &hi, &mid);
+                *reinterpret_cast<uint32_t *>(kq + kChBox + at) = hi;
+                *reinterpret_cast<uint32_t *>(kq + 2 * kChTerm + kChBox + at) = mid;
             }
 #pragma unroll
-            for (int i = 15; i >= 0; i--) {                   // backwards: exp(G_C - G_t), from the end's sum
-                const int t = t0 + i;
-                const uint32_t at = t * 128 + ((((uint32_t)lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
-                const float rk = rf[kRecRk + t];              // 0 past the sequence's end
-                uint32_t hi, mid;
-                const float x = __uint_as_float(k[i] << 16) * (rk * exp2_approx(E.x));
-                const float y = __uint_as_float(k[i] & 0xFFFF0000u) * (rk * exp2_approx(E.y));
-                split2(t < n ? x : 0.0f, t < n ? y : 0.0f, &hi, &mid);
-                *reinterpret_cast<uint32_t *>(late + at) = hi;
-                *reinterpret_cast<uint32_t *>(late + kChTerm + at) = mid;
-                E.x += g[i].x;
-                E.y += g[i].y;
+            for (int i4 = 12; i4 >= 0; i4 -= 4) {             // backwards: exp(G_C - G_t), from the end's sum
+                const float4 l4 = __ldg(reinterpret_cast<const float4 *>(&rf[kRecKd + t0 + i4]));
+                const float l[4] = {l4.x, l4.y, l4.z, l4.w};  // minus infinity past the sequence's end
+#pragma unroll
+                for (int j = 3; j >= 0; j--) {
+                    const int i = i4 + j, t = t0 + i;
+                    const uint32_t at = t * 128 + ((((uint32_t)lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
+                    uint32_t hi, mid;
+                    split2(__uint_as_float(k[i] << 16) * exp2_fast(E.x + l[j]),
+                           __uint_as_float(k[i] & 0xFFFF0000u) * exp2_fast(E.y + l[j]), &hi, &mid);
+                    *reinterpret_cast<uint32_t *>(late + at) = hi;
+                    *reinterpret_cast<uint32_t *>(late + kChTerm + at) = mid;
+                    E.x += g[i].x;
+                    E.y += g[i].y;
+                }
             }
             fence_async_smem();
             __syncwarp();
@@ -1132,13 +1136,12 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         }
     } else if (warp == kWarpMma) {
         // ---------------- loads and MMA issue
-        const uint32_t idk = idesc(1, kC);                     // 128 x 64, both operands K-major
-        const uint32_t idn = idk | (1u << 16);                 // B with N contiguous (K^T U: channels)
+        const uint32_t idk = idesc(1, 2 * kC);                 // 128 x 128, both operands K-major
+        const uint32_t idn = idk | (1u << 16);                 // B with N contiguous (K^T U: 128 channels)
         auto load = [&](int c) {
             uint8_t *p = stage(c);
             uint64_t *bar = &sh.in_full[c % kStages];
-            const uint32_t tp = kChannel ? kTpBytes : kChTpCopyHead;
-            mb_expect_tx(bar, (kChannel ? 0 : kChKq) + kChV + tp);
+            mb_expect_tx(bar, (kChannel ? 0 : kChKq) + kChV + kChTpCopy);
             for (int b = 0; b < 2; b++) {
                 if (!kChannel) {
                     tma2d(p + 2 * b * kChBox, &mk, hq * kD + 64 * b, first + kC * c, bar);
@@ -1146,11 +1149,11 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                 }
                 tma2d(p + kOffV + b * kChBox, &mv, h * kD + 64 * b, first + kC * c, bar);
             }
-            bulk_g2s(p + kOffTp, record(c), tp, bar);
+            bulk_g2s(p + kOffTp, record(c), kChTpCopy, bar);
         };
         // D[v][t >= 16 j] += X[v][16 tokens j] tile[t][16 tokens j], the tile lower triangular
         // (hi, mid terms), X's terms at columns `x`
-        auto tri = [&](uint32_t d, uint32_t x, uint32_t tile, bool acc) {
+        auto tri = [&](uint32_t d, uint32_t x, uint32_t tile) {
             const uint64_t td = tdesc(tile);
 #pragma unroll
             for (int term = 0; term < 3; term++)               // hi hi, hi mid, mid hi
@@ -1158,53 +1161,48 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                 for (int j = 0; j < 4; j++)
                     umma_ts_warp(d + 16 * j, x + (term == 2 ? 32 : 0) + 8 * j,
                                  td + (((term == 1 ? kTermBytes : 0) + term_block(j)) >> 4), idesc(1, kC - 16 * j),
-                                 acc || term > 0 || j > 0);
-        };
-        // X S^T: X's boxes at `x` (a box of 64 channels `box` bytes after the other); per channel
-        // its mid term kChTerm behind
-        auto with_state = [&](uint32_t d, uint64_t x, int box) {
-#pragma unroll
-            for (int term = 0; term < (kChannel ? 3 : 2); term++)   // S hi, S mid, and S hi with X mid
-#pragma unroll
-                for (int s = 0; s < 8; s++)
-                    umma_ts_warp(d, kTmS + 32 * (s >> 1) + 16 * (term == 1) + 8 * (s & 1),
-                                 x + (((term == 2 ? kChTerm : 0) + (s >> 2) * box + (s & 3) * 32) >> 4), idk, term > 0 || s > 0);
+                                 term > 0 || j > 0);
         };
         if (lane == 0)
             for (int c = 0; c < min(nc, kStages - 1); c++) load(c);
         __syncwarp();
         for (int c = 0; c < nc; c++) {
-            if (!wait(sh.in_full[c % kStages], c / kStages) || (kChannel && !wait(sh.made, c)) || !wait(sh.s_ready, c)) break;
+            // chunk c - 1's O is out: its columns and its stage are free
+            if (!wait(sh.in_full[c % kStages], c / kStages) || (kChannel && !wait(sh.made, c)) ||
+                (c >= 1 && !wait(sh.o_free, c - 1)) || !wait(sh.s_ready, c))
+                break;
             tc_fence_after();
             const uint32_t st = saddr(stage(c)), mk0 = saddr(made);
-            const uint64_t kx = sdesc(kChannel ? mk0 : st), qx = sdesc(kChannel ? mk0 + 2 * kChTerm : st + kChBox);
-            with_state(kTmR, kx, kChannel ? kChBox : 2 * kChBox);
+            const uint64_t kq = sdesc(kChannel ? mk0 : st);
+#pragma unroll
+            for (int term = 0; term < (kChannel ? 3 : 2); term++)   // K S and Q S: S hi, S mid, and S hi with K, Q mid
+#pragma unroll
+                for (int s = 0; s < 8; s++)
+                    umma_ts_warp(kTmR, kTmS + 32 * (s >> 1) + 16 * (term == 1) + 8 * (s & 1),
+                                 kq + (((term == 2 ? 2 * kChTerm : 0) + (s >> 2) * 2 * kChBox + (s & 3) * 32) >> 4), idk,
+                                 term > 0 || s > 0);
             umma_commit_warp(&sh.d1_full);
-            if (c >= 1 && !wait(sh.o_free, c - 1)) break;      // chunk c - 1 is done with O's columns and its stage
-            tc_fence_after();
-            with_state(kTmOq, qx, kChannel ? kChBox : 2 * kChBox);
-            umma_commit_warp(&sh.q_done);
             if (c + kStages - 1 < nc && lane == 0) load(c + kStages - 1);
             __syncwarp();
             if (!wait(sh.r_ready, c)) break;
             tc_fence_after();
             const uint32_t tp = st + kOffTp;
-            tri(kTmR, kTmRU, tp, false);
+            tri(kTmR, kTmRU, tp);
             umma_commit_warp(&sh.d2_full);
             if (!wait(sh.u_ready, c)) break;
             tc_fence_after();
-            const uint64_t lx = sdesc(kChannel ? mk0 + 4 * kChTerm + (c & 1) * 2 * kChTerm : st);
+            // B with N contiguous: 64 channels a box, the boxes a leading offset apart
+            constexpr int box = kChannel ? kChBox : 2 * kChBox;
+            const uint64_t lx = (sdesc(kChannel ? mk0 + 4 * kChTerm + (c & 1) * 2 * kChTerm : st) & ~((uint64_t)0x3FFFu << 16)) |
+                                (uint64_t)(box >> 4) << 16;
 #pragma unroll
-            for (int half = 0; half < 2; half++)               // K^T U into the state's sums, a half of k at a time
+            for (int term = 0; term < (kChannel ? 3 : 2); term++)   // K^T U into the state's sums
 #pragma unroll
-                for (int term = 0; term < (kChannel ? 3 : 2); term++)
-#pragma unroll
-                    for (int s = 0; s < 4; s++)
-                        umma_ts_warp(kTmS + 64 * half, kTmRU + 32 * (term == 1) + 8 * s,
-                                     lx + (((term == 2 ? kChTerm : 0) + half * (kChannel ? kChBox : 2 * kChBox) + s * 16 * 128) >> 4),
-                                     idn, term > 0 || s > 0);
+                for (int s = 0; s < 4; s++)
+                    umma_ts_warp(kTmS, kTmRU + 32 * (term == 1) + 8 * s, lx + (((term == 2 ? kChTerm : 0) + s * 16 * 128) >> 4),
+                                 idn, term > 0 || s > 0);
             umma_commit_warp(&sh.d4_full);
-            tri(kChannel ? kTmOq : kTmOp, kChannel ? kTmRU : kTmU, tp + 2 * kTermBytes, kChannel);
+            tri(kTmOp, kChannel ? kTmRU : kTmU, tp + 2 * kTermBytes);
             umma_commit_warp(&sh.o_full);
         }
         __syncwarp();
