@@ -215,13 +215,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinGate = -90.0f;
 constexpr int kTermBytes = 5120;                              // T or P, one term: 16-column blocks j of rows 16 j..63
 constexpr int kTpBytes = 4 * kTermBytes;                      // T hi, T mid, P hi, P mid
-constexpr int kRecFloats = 768;
+constexpr int kRecFloats = 256 + 8 * kDeltaD;
 constexpr int kRecBytes = kTpBytes + kRecFloats * 4;          // a chunk and head's record in the workspace
 // The record's floats, a token each: kr and qr weigh the columns of K S and Q S, kd what
 // enters the state.  Decay per head: kr = exp(G_t) / |k_t|, qr = scale exp(G_t) / |q_t|, kd =
 // exp(G_C - G_t) / |k_t|, and one exp(G_C).  Per channel, where the operands carry the decay:
-// kr = 1 / |k_t|, qr = scale / |q_t|, kd = log2 kr, and the log2 decays' sums over each 16
-// tokens [4][D].  (Norms are 1 without qk_norm; past the sequence's end all are 0, log2 kr
+// kr = 1 / |k_t|, qr = scale / |q_t|, kd = log2 kr, and the log2 decays' sums over each 8
+// tokens [8][D].  (Norms are 1 without qk_norm; past the sequence's end all are 0, log2 kr
 // minus infinity.)
 constexpr int kRecKr = 0, kRecKd = 64, kRecQr = 128, kRecDec = 192, kRecSum = 256;
 __host__ __device__ constexpr int term_block(int j) { return 2048 * j - 256 * j * (j - 1); }
@@ -578,6 +578,7 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
                 g[i] = L;
             }
             *reinterpret_cast<float2 *>(&sh.sum[warp][ch]) = L;
+            *reinterpret_cast<float2 *>(&outf[kRecSum + warp * kD + ch]) = L;
             if (half == 1) wait(sh.done, 0);                  // the first half's operands are used
             __syncthreads();
             if (sh.bad) break;
@@ -627,13 +628,6 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
                     *reinterpret_cast<uint32_t *>(B + kC * 128 + at) = hi;
                     *reinterpret_cast<uint32_t *>(B + kPpB + kC * 128 + at) = mid;
                 }
-            }
-            if (warp < 4) {                                   // 16 tokens' sums for the second kernel
-                float2 x = make_float2(s[0].x + s[1].x, s[0].y + s[1].y);
-                if (warp == 1) x = make_float2(s[2].x + s[3].x, s[2].y + s[3].y);
-                if (warp == 2) x = m1;
-                if (warp == 3) x = make_float2(s[6].x + s[7].x, s[6].y + s[7].y);
-                *reinterpret_cast<float2 *>(&outf[kRecSum + warp * kD + ch]) = x;
             }
             fence_async_smem();
             __syncthreads();
@@ -783,11 +777,12 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
 //     and U's a second time before K^T U;
 //   per channel: eight warps more write exp(G) K, exp(G) Q and exp(G_C - G) K / |k| as two
 //     terms each, a chunk ahead.
-// K S and Q S are one product with the 64 rows of K over those of Q as its 128 columns (an
-// MMA of 64 columns takes as long as one of 128 here: about 65 clocks).
-// A stage's latency is a chain of short dependent steps (a product, its sums to registers,
-// two terms back), so each has as many warps as the registers allow (64 a thread).
-constexpr int kChChain = 16, kChOut = 4, kChMake = 8;
+// The chain's eight warps keep 64 floats of the state a thread, in registers or, per channel,
+// in tensor memory (there 22 warps share the registers; with the state among them they spilled
+// to local memory, which made a chunk three times as long).  Sixteen warps with 32 each took as
+// long a phase: they share four schedulers.
+constexpr int kChChain = 8, kChOut = 4, kChMake = 8;
+constexpr int kChPartK = kD / (kChChain / 4), kChPartT = kC / (kChChain / 4);     // channels and tokens of a chain warp
 constexpr int kChStagesHead = 3, kChStagesChannel = 2;
 constexpr int kChBox = kC * 128;                              // 64 tokens x 64 channels: 8 KB
 constexpr int kChKq = 4 * kChBox;                             // decay per head: K and Q, [box][K, Q]
@@ -799,17 +794,13 @@ constexpr int kChTerm = 2 * kChBox;                           // per channel: on
 constexpr int kChMade = 4 * kChTerm + 4 * kChTerm;            // [hi, mid][box][K, Q]; the late K [chunk parity][hi, mid][box]
 static_assert(kTpBytes + (kRecDec + 1) * 4 <= kChTp && kTpBytes + 1024 <= kChTp, "a stage holds the record's head");
 template <bool kChannel> struct ChunkShape {
-    static constexpr int warps = kChChain + kChOut + (kChannel ? kChMake : 0) + 1;
-    static constexpr int threads = kChannel ? 1024 : warps * 32;       // per channel whole warpgroups: registers move
+    static constexpr int warps = kChChain + kChOut + (kChannel ? kChMake : 0) + 2;    // and MMA issue, loads
+    static constexpr int threads = warps * 32;                // 448 (128 registers each), per channel 704 (80)
     static constexpr int stages = kChannel ? kChStagesChannel : kChStagesHead;
     static constexpr int stage = kChannel ? kChStageChannel : kChStageHead;
     static constexpr int smem = 1024 + (kChannel ? kChMade : 0) + stages * stage;
 };
 constexpr int kChWarpOut = kChChain, kChWarpMake = kChWarpOut + kChOut;
-// Registers a thread per channel: 64 at launch, shares moved from the writers of O and the
-// issuing warp's group to the makers of operands (16 tokens' inputs in registers).
-constexpr int kChRegs = 64, kChRegsMake = 96, kChRegsOut = 40, kChRegsMma = 24;
-static_assert(4 * kChRegs + 2 * kChRegsMake + kChRegsOut + kChRegsMma <= 8 * kChRegs, "shares within the launch's");
 // tensor memory columns
 constexpr uint32_t kTmS = 0;      // S^T as an operand, [quarter of k][hi, mid][16]; the new S's sums over it
 constexpr uint32_t kTmR = 128;    // K S, then T R
@@ -817,13 +808,16 @@ constexpr uint32_t kTmOq = 192;   // Q S
 constexpr uint32_t kTmOp = 256;   // P U
 constexpr uint32_t kTmRU = 320;   // R, then U (per head: weighted for the state), as an operand [hi, mid][32]
 constexpr uint32_t kTmU = 384;    // per head: U as an operand [hi, mid][32]
+constexpr uint32_t kTmF = 384;    // per channel: the state, float [128]
 
+constexpr int kRankSeqs = 256;                                // up to this many sequences are taken by length
 struct ChunkShared {
-    uint64_t in_full[3];
-    uint64_t s_ready, d1_full, r_ready, d2_full, u_ready, d4_full, o_full, o_free, made, drain;
+    uint64_t in_full[3], in_free[3];
+    uint64_t s_ready, d1_full, q_done, r_ready, d2_full, u_ready, d4_full, o_full, o_free, made, drain;
     uint32_t tmem;
     volatile int bail;
     alignas(16) float dec[2][kD];                             // per channel: exp(G_C), by chunk parity
+    int seq, len[kRankSeqs];
 };
 
 // Unswizzled K-major descriptor of a T or P block: 8-row groups 256 bytes apart, their two
@@ -842,7 +836,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
     pdl_wait();
     pdl_trigger();
     using Shape = ChunkShape<kChannel>;
-    constexpr int kWarpMma = Shape::warps - 1, kStages = Shape::stages;
+    constexpr int kWarpMma = Shape::warps - 2, kWarpLoad = kWarpMma + 1, kStages = Shape::stages;
     extern __shared__ __align__(1024) uint8_t csm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(csm_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *made = sm;                                       // per channel
@@ -851,7 +845,20 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
     __shared__ ChunkShared sh;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x % a.H, seq = blockIdx.x / a.H;
+    const int h = blockIdx.x % a.H;
+    int seq = blockIdx.x / a.H;
+    if (a.n_seq > 1 && a.n_seq <= kRankSeqs && a.seq_start) {
+        // the long sequences first: this block's is the one as many others come before
+        for (int i = threadIdx.x; i < a.n_seq; i += Shape::threads) sh.len[i] = a.seq_start[i + 1] - a.seq_start[i];
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.n_seq; i += Shape::threads) {
+            int before = 0;
+            for (int j = 0; j < a.n_seq; j++) before += sh.len[j] > sh.len[i] || (sh.len[j] == sh.len[i] && j < i);
+            if (before == seq) sh.seq = i;
+        }
+        __syncthreads();
+        seq = sh.seq;
+    }
     int first, len, slot;
     if (!delta_seq(a, seq, &first, &len, &slot)) return;
     const size_t sbase = ((size_t)slot * a.H + h) * kD * kD;
@@ -869,9 +876,10 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
     auto stage = [&](int c) { return ring + (size_t)(c % kStages) * Shape::stage; };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; s++) mb_init(&sh.in_full[s], 1);
+        for (int s = 0; s < kStages; s++) { mb_init(&sh.in_full[s], 1); mb_init(&sh.in_free[s], kChOut); }
         mb_init(&sh.s_ready, kChChain);
         mb_init(&sh.d1_full, 1);
+        mb_init(&sh.q_done, 1);
         mb_init(&sh.r_ready, kChChain);
         mb_init(&sh.d2_full, 1);
         mb_init(&sh.u_ready, kChChain);
@@ -907,36 +915,43 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         __syncwarp();
         if (lane == 0) mb_arrive(&b);
     };
-    if (kChannel) {
-        if (warp >= kChWarpMake && warp < kChWarpMake + kChMake)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChRegsMake));
-        else if (warp >= kWarpMma)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChRegsMma));
-        else if (warp >= kChWarpOut)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChRegsOut));
-    }
-
     if (warp < kChChain) {
-        // ---------------- the chain: value column v, a quarter of the channels or tokens
-        const int q = warp & 3, part = warp >> 2, v = 32 * q + lane, t0 = 16 * part;
+        // ---------------- the chain: value column v, half of the channels or tokens
+        const int q = warp & 3, part = warp >> 2, v = 32 * q + lane, t0 = kChPartT * part;
         const uint32_t la = tmem + ((uint32_t)(32 * q) << 16);
-        float S[32];
+        const uint32_t la_s = la + kTmS + kChPartK * part;
+        const uint32_t la_f = la + kTmF + kChPartK * part;
+        float S[kChannel ? 1 : kChPartK];
+        // 32 channels of the state from b on as two terms
+        auto put_terms32 = [&](int b, const float *x) {
 #pragma unroll
-        for (int j = 0; j < 32; j++)
-            S[j] = a.state_in ? a.state_in[sbase + (size_t)(32 * part + j) * kD + v] : 0.0f;
-        auto put_state = [&]() {
-#pragma unroll
-            for (int b = 0; b < 4; b++) {
+            for (int i = 0; i < 4; i++) {
                 uint32_t hi[4], mid[4];
 #pragma unroll
-                for (int j = 0; j < 4; j++) split2(S[8 * b + 2 * j], S[8 * b + 2 * j + 1], &hi[j], &mid[j]);
-                tmem_st4(la + kTmS + 32 * part + 4 * b, hi);
-                tmem_st4(la + kTmS + 32 * part + 16 + 4 * b, mid);
+                for (int j = 0; j < 4; j++) split2(x[8 * i + 2 * j], x[8 * i + 2 * j + 1], &hi[j], &mid[j]);
+                tmem_st4(la_s + b + 4 * i, hi);
+                tmem_st4(la_s + b + 16 + 4 * i, mid);
+            }
+        };
+        {
+            const float *from = a.state_in ? a.state_in + sbase + (size_t)(kChPartK * part) * kD + v : nullptr;
+#pragma unroll
+            for (int b = 0; b < kChPartK; b += 32) {
+                float x[32];
+#pragma unroll
+                for (int j = 0; j < 32; j++) {
+                    x[j] = from ? from[(size_t)(b + j) * kD] : 0.0f;
+                    if (!kChannel) S[b + j] = x[j];
+                }
+                if (kChannel) {
+                    tmem_st16(la_f + b, &x[0]);
+                    tmem_st16(la_f + b + 16, &x[16]);
+                }
+                put_terms32(b, x);
             }
             tmem_wait_st();
             arrive(sh.s_ready);
-        };
-        put_state();
+        }
         for (int c = 0; c < nc; c++) {
             const int n = min(kC, len - kC * c);
             const float *sc = reinterpret_cast<const float *>(stage(c) + kOffTp + kTpBytes) + t0;
@@ -944,59 +959,62 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             const uint8_t *vt = stage(c) + kOffV + (q >> 1) * kChBox + t0 * 128 + (v & 7) * 2;
             const uint32_t v8 = (uint32_t)(v >> 3) & 7u;
             if (!wait(sh.in_full[c % kStages], c / kStages)) break;
-            uint32_t vv[8];                                       // two tokens a word
+            uint32_t vv[kChPartT / 2];                            // two tokens a word
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
+            for (int j = 0; j < kChPartT / 2; j++) {
                 const uint32_t x = *reinterpret_cast<const uint16_t *>(vt + 2 * j * 128 + ((v8 ^ ((2 * j) & 7u)) << 4));
                 const uint32_t y = *reinterpret_cast<const uint16_t *>(vt + 2 * j * 128 + 128 + ((v8 ^ ((2 * j + 1) & 7u)) << 4));
                 vv[j] = x | (y << 16);
             }
             if (!wait(sh.d1_full, c)) break;
             tc_fence_after();
-            {
+#pragma unroll
+            for (int b16 = 0; b16 < kChPartT; b16 += 16) {
                 uint32_t d[16];
-                tmem_ld16_nowait(la + kTmR + t0, d);
+                tmem_ld16_nowait(la + kTmR + t0 + b16, d);
                 tmem_wait_ld();
 #pragma unroll
                 for (int b = 0; b < 2; b++) {
                     uint32_t hi[4], mid[4];
 #pragma unroll
                     for (int j2 = 0; j2 < 4; j2++) {
-                        const int j = 8 * b + 2 * j2;
+                        const int i = 8 * b + 2 * j2, j = b16 + i;
                         const float2 kr = *reinterpret_cast<const float2 *>(&sc[kRecKr + j]);
-                        const float x = fmaf(-kr.x, __uint_as_float(d[j]), __uint_as_float(vv[j >> 1] << 16));
-                        const float y = fmaf(-kr.y, __uint_as_float(d[j + 1]), __uint_as_float(vv[j >> 1] & 0xFFFF0000u));
+                        const float x = fmaf(-kr.x, __uint_as_float(d[i]), __uint_as_float(vv[j >> 1] << 16));
+                        const float y = fmaf(-kr.y, __uint_as_float(d[i + 1]), __uint_as_float(vv[j >> 1] & 0xFFFF0000u));
                         split2(t0 + j < n ? x : 0.0f, t0 + j + 1 < n ? y : 0.0f, &hi[j2], &mid[j2]);
                     }
-                    tmem_st4(la + kTmRU + 8 * part + 4 * b, hi);
-                    tmem_st4(la + kTmRU + 32 + 8 * part + 4 * b, mid);
+                    tmem_st4(la + kTmRU + (t0 + b16) / 2 + 4 * b, hi);
+                    tmem_st4(la + kTmRU + 32 + (t0 + b16) / 2 + 4 * b, mid);
                 }
             }
             tmem_wait_st();
             arrive(sh.r_ready);
             if (!wait(sh.d2_full, c)) break;
             tc_fence_after();
-            {
+#pragma unroll
+            for (int b16 = 0; b16 < kChPartT; b16 += 16) {
                 uint32_t d[16];
-                tmem_ld16_nowait(la + kTmR + t0, d);
+                tmem_ld16_nowait(la + kTmR + t0 + b16, d);
                 tmem_wait_ld();
 #pragma unroll
                 for (int b = 0; b < 2; b++) {
                     uint32_t hi[4], mid[4];
+                    const uint32_t at = (t0 + b16) / 2 + 4 * b;
 #pragma unroll
                     for (int j2 = 0; j2 < 4; j2++)
                         split2(__uint_as_float(d[8 * b + 2 * j2]), __uint_as_float(d[8 * b + 2 * j2 + 1]), &hi[j2], &mid[j2]);
-                    tmem_st4(la + (kChannel ? kTmRU : kTmU) + 8 * part + 4 * b, hi);
-                    tmem_st4(la + (kChannel ? kTmRU : kTmU) + 32 + 8 * part + 4 * b, mid);
+                    tmem_st4(la + (kChannel ? kTmRU : kTmU) + at, hi);
+                    tmem_st4(la + (kChannel ? kTmRU : kTmU) + 32 + at, mid);
                     if (!kChannel) {
 #pragma unroll
                         for (int j2 = 0; j2 < 4; j2++) {
-                            const int j = 8 * b + 2 * j2;
-                            const float2 kd = *reinterpret_cast<const float2 *>(&sc[kRecKd + j]);
-                            split2(__uint_as_float(d[j]) * kd.x, __uint_as_float(d[j + 1]) * kd.y, &hi[j2], &mid[j2]);
+                            const int i = 8 * b + 2 * j2;
+                            const float2 kd = *reinterpret_cast<const float2 *>(&sc[kRecKd + b16 + i]);
+                            split2(__uint_as_float(d[i]) * kd.x, __uint_as_float(d[i + 1]) * kd.y, &hi[j2], &mid[j2]);
                         }
-                        tmem_st4(la + kTmRU + 8 * part + 4 * b, hi);
-                        tmem_st4(la + kTmRU + 32 + 8 * part + 4 * b, mid);
+                        tmem_st4(la + kTmRU + at, hi);
+                        tmem_st4(la + kTmRU + 32 + at, mid);
                     }
                 }
             }
@@ -1006,26 +1024,42 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             if (!wait(sh.d4_full, c)) break;
             tc_fence_after();
 #pragma unroll
-            for (int b = 0; b < 2; b++) {
-                uint32_t d[16];
-                tmem_ld16_nowait(la + kTmS + 32 * part + 16 * b, d);
-                tmem_wait_ld();
+            for (int b = 0; b < kChPartK; b += 32) {          // the operand's terms go over the sums they come from
+                uint32_t d[32];
+                tmem_ld16_nowait(la_s + b, *reinterpret_cast<uint32_t(*)[16]>(&d[0]));
+                tmem_ld16_nowait(la_s + b + 16, *reinterpret_cast<uint32_t(*)[16]>(&d[16]));
+                float x[32];
 #pragma unroll
-                for (int j4 = 0; j4 < 4; j4++) {
-                    float4 e = make_float4(dec, dec, dec, dec);
-                    if (kChannel) e = *reinterpret_cast<const float4 *>(&sh.dec[c & 1][32 * part + 16 * b + 4 * j4]);
-                    float *s = &S[16 * b + 4 * j4];
-                    s[0] = fmaf(e.x, s[0], __uint_as_float(d[4 * j4]));
-                    s[1] = fmaf(e.y, s[1], __uint_as_float(d[4 * j4 + 1]));
-                    s[2] = fmaf(e.z, s[2], __uint_as_float(d[4 * j4 + 2]));
-                    s[3] = fmaf(e.w, s[3], __uint_as_float(d[4 * j4 + 3]));
+                for (int b16 = 0; b16 < 32; b16 += 16) {
+                    uint32_t f[16];
+                    if (kChannel) tmem_ld16_nowait(la_f + b + b16, f);
+                    if (kChannel || b16 == 0) tmem_wait_ld();
+#pragma unroll
+                    for (int j4 = 0; j4 < 4; j4++) {
+                        float4 e4 = make_float4(dec, dec, dec, dec);
+                        if (kChannel) e4 = *reinterpret_cast<const float4 *>(&sh.dec[c & 1][kChPartK * part + b + b16 + 4 * j4]);
+                        const float e[4] = {e4.x, e4.y, e4.z, e4.w};
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const int i = b16 + 4 * j4 + j;
+                            x[i] = fmaf(e[j], kChannel ? __uint_as_float(f[4 * j4 + j]) : S[b + i], __uint_as_float(d[i]));
+                            if (!kChannel) S[b + i] = x[i];
+                        }
+                    }
+                    if (kChannel && c + 1 < nc) tmem_st16(la_f + b + b16, &x[b16]);
+                }
+                if (c + 1 < nc) {
+                    put_terms32(b, x);
+                } else if (!sh.bail) {
+#pragma unroll
+                    for (int j = 0; j < 32; j++) a.state_out[sbase + (size_t)(kChPartK * part + b + j) * kD + v] = x[j];
                 }
             }
-            if (c + 1 < nc) put_state();
+            if (c + 1 < nc) {
+                tmem_wait_st();
+                arrive(sh.s_ready);
+            }
         }
-        if (!sh.bail)
-#pragma unroll
-            for (int j = 0; j < 32; j++) a.state_out[sbase + (size_t)(32 * part + j) * kD + v] = S[j];
     } else if (warp < kChWarpMake) {
         // ---------------- O: value column v, every token of the chunk
         const int q = warp & 3, v = 32 * q + lane;
@@ -1035,121 +1069,127 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             const float *sc = reinterpret_cast<const float *>(stage(c) + kOffTp + kTpBytes);
             if (!wait(sh.o_full, c)) break;
             tc_fence_after();
-            uint32_t w[32];                                   // two tokens a word
-#pragma unroll
-            for (int b = 0; b < 8; b++) {
-                uint32_t d[8], p[8];
-                tmem_ld8_nowait(la + kTmOq + 8 * b, d);
-                tmem_ld8_nowait(la + kTmOp + 8 * b, p);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const float2 r = *reinterpret_cast<const float2 *>(&sc[kRecQr + 8 * b + j]);
-                    const __nv_bfloat162 x = __floats2bfloat162_rn(fmaf(r.x, __uint_as_float(d[j]), __uint_as_float(p[j])),
-                                                                   fmaf(r.y, __uint_as_float(d[j + 1]), __uint_as_float(p[j + 1])));
-                    w[4 * b + j / 2] = *reinterpret_cast<const uint32_t *>(&x);
-                }
-            }
-            arrive(sh.o_free);
-            // neighbouring lanes trade a token each: two columns of one token a store
             const int mine = lane & 1;
             uint32_t *o = reinterpret_cast<uint32_t *>(a.out + ((size_t)(first + kC * c + mine) * a.H + h) * kD + (v & ~1));
             const size_t step = (size_t)a.H * kD;             // words of two tokens
+#pragma unroll 1
+            for (int b16 = 0; b16 < kC; b16 += 16) {
+                uint32_t w[8];                                // two tokens a word
 #pragma unroll
-            for (int j = 0; j < 32; j++, o += step) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, w[j], 1);
-                if (2 * j + mine < n) *o = mine ? __byte_perm(got, w[j], 0x7632) : __byte_perm(w[j], got, 0x5410);
+                for (int b = 0; b < 2; b++) {
+                    uint32_t d[8], p[8];
+                    tmem_ld8_nowait(la + kTmOq + b16 + 8 * b, d);
+                    tmem_ld8_nowait(la + kTmOp + b16 + 8 * b, p);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const float2 r = *reinterpret_cast<const float2 *>(&sc[kRecQr + b16 + 8 * b + j]);
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(fmaf(r.x, __uint_as_float(d[j]), __uint_as_float(p[j])),
+                                                                       fmaf(r.y, __uint_as_float(d[j + 1]), __uint_as_float(p[j + 1])));
+                        w[4 * b + j / 2] = *reinterpret_cast<const uint32_t *>(&x);
+                    }
+                }
+                if (b16 == kC - 16) {
+                    arrive(sh.o_free);
+                    if (lane == 0) mb_arrive(&sh.in_free[c % kStages]);
+                }
+                // neighbouring lanes trade a token each: two columns of one token a store
+#pragma unroll
+                for (int j = 0; j < 8; j++, o += step) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, w[j], 1);
+                    if (b16 + 2 * j + mine < n) *o = mine ? __byte_perm(got, w[j], 0x7632) : __byte_perm(w[j], got, 0x5410);
+                }
             }
         }
     } else if (kChannel && warp < kChWarpMake + kChMake) {
-        // ---------------- per channel: the weighted operands of chunk c, two channels and 16
-        // tokens a thread
-        const int id = threadIdx.x - kChWarpMake * 32, pair = id & 63, tq = id >> 6, ch = 2 * pair, t0 = 16 * tq;
+        // ---------------- per channel: the weighted operands of chunk c, two channels and twice
+        // 8 tokens a thread
+        const int id = threadIdx.x - kChWarpMake * 32, pair = id & 63, ch = 2 * pair;
         for (int c = 0; c < nc; c++) {
             const int n = min(kC, len - kC * c);
             const size_t tok0 = (size_t)(first + kC * c);
             const float *rf = reinterpret_cast<const float *>(record(c) + kTpBytes);
-            uint32_t k[16], q[16];
-            float2 g[16];
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-                const size_t tok = tok0 + min(t0 + i, n - 1);
-                k[i] = __ldg(reinterpret_cast<const uint32_t *>(a.k + tok * a.k_stride + hq * kD + ch));
-                q[i] = __ldg(reinterpret_cast<const uint32_t *>(a.q + tok * a.q_stride + hq * kD + ch));
-                g[i] = __ldg(reinterpret_cast<const float2 *>(a.g + (tok * a.H + h) * kD + ch));
-            }
-            // the decay's sums before and after this thread's tokens
-            float2 L = make_float2(0.f, 0.f), E = L, all = L;
-#pragma unroll
-            for (int w = 0; w < 4; w++) {
-                const float2 x = __ldg(reinterpret_cast<const float2 *>(&rf[kRecSum + w * kD + ch]));
-                if (w < tq) { L.x += x.x; L.y += x.y; }
-                if (w > tq) { E.x += x.x; E.y += x.y; }
-                all.x += x.x;
-                all.y += x.y;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-                const bool in = t0 + i < n;
-                g[i].x = in ? clamp_gate(g[i].x) * kLog2e : 0.0f;
-                g[i].y = in ? clamp_gate(g[i].y) * kLog2e : 0.0f;
-            }
-            if (c >= 1 && !wait(sh.d1_full, c - 1)) break;    // the last chunk's K and Q are used
-            if (tq == 0) *reinterpret_cast<float2 *>(&sh.dec[c & 1][ch]) = make_float2(exp2_fast(all.x), exp2_fast(all.y));
             uint8_t *kq = made + (pair >> 5) * 2 * kChBox;
             uint8_t *late = made + 4 * kChTerm + (c & 1) * 2 * kChTerm + (pair >> 5) * kChBox;
+            bool ok = true;
+#pragma unroll 1
+            for (int part = 0; part < 2; part++) {
+                const int e = (id >> 6) + 4 * part, t0 = 8 * e;
+                uint32_t k[8], q[8];
+                float2 g[8];
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-                const int t = t0 + i;
-                const uint32_t at = t * 128 + ((((uint32_t)lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
-                L.x += g[i].x;
-                L.y += g[i].y;
-                const float ex = exp2_fast(L.x), ey = exp2_fast(L.y);
-                uint32_t hi, mid;
-                split2(__uint_as_float(k[i] << 16) * ex, __uint_as_float(k[i] & 0xFFFF0000u) * ey, &hi, &mid);
-                *reinterpret_cast<uint32_t *>(kq + at) = hi;
-                *reinterpret_cast<uint32_t *>(kq + 2 * kChTerm + at) = mid;
-                split2(__uint_as_float(q[i] << 16) * ex, __uint_as_float(q[i] & 0xFFFF0000u) * ey, &hi, &mid);
-                *reinterpret_cast<uint32_t *>(kq + kChBox + at) = hi;
-                *reinterpret_cast<uint32_t *>(kq + 2 * kChTerm + kChBox + at) = mid;
-            }
+                for (int i = 0; i < 8; i++) {
+                    const size_t tok = tok0 + min(t0 + i, n - 1);
+                    k[i] = __ldg(reinterpret_cast<const uint32_t *>(a.k + tok * a.k_stride + hq * kD + ch));
+                    q[i] = __ldg(reinterpret_cast<const uint32_t *>(a.q + tok * a.q_stride + hq * kD + ch));
+                    g[i] = __ldg(reinterpret_cast<const float2 *>(a.g + (tok * a.H + h) * kD + ch));
+                }
+                float l[8];                                   // log2 of 1 / |k|; minus infinity past the sequence's end
+                *reinterpret_cast<float4 *>(&l[0]) = __ldg(reinterpret_cast<const float4 *>(&rf[kRecKd + t0]));
+                *reinterpret_cast<float4 *>(&l[4]) = __ldg(reinterpret_cast<const float4 *>(&rf[kRecKd + t0 + 4]));
+                // the decay's sums before and after this thread's tokens
+                float2 L = make_float2(0.f, 0.f), E = L;
 #pragma unroll
-            for (int i4 = 12; i4 >= 0; i4 -= 4) {             // backwards: exp(G_C - G_t), from the end's sum
-                const float4 l4 = __ldg(reinterpret_cast<const float4 *>(&rf[kRecKd + t0 + i4]));
-                const float l[4] = {l4.x, l4.y, l4.z, l4.w};  // minus infinity past the sequence's end
+                for (int w = 0; w < 8; w++) {
+                    const float2 x = __ldg(reinterpret_cast<const float2 *>(&rf[kRecSum + w * kD + ch]));
+                    L.x += w < e ? x.x : 0.0f;
+                    L.y += w < e ? x.y : 0.0f;
+                    E.x += w > e ? x.x : 0.0f;
+                    E.y += w > e ? x.y : 0.0f;
+                }
 #pragma unroll
-                for (int j = 3; j >= 0; j--) {
-                    const int i = i4 + j, t = t0 + i;
-                    const uint32_t at = t * 128 + ((((uint32_t)lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
+                for (int i = 0; i < 8; i++) {
+                    const bool in = t0 + i < n;
+                    g[i].x = in ? clamp_gate(g[i].x) * kLog2e : 0.0f;
+                    g[i].y = in ? clamp_gate(g[i].y) * kLog2e : 0.0f;
+                }
+                if (part == 0 && c >= 1) ok = wait(sh.q_done, c - 1);      // the last chunk's K and Q are used
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const uint32_t at = (t0 + i) * 128 + ((((uint32_t)lane >> 2) ^ i) << 4) + (lane & 3) * 4;
+                    L.x += g[i].x;
+                    L.y += g[i].y;
+                    const float ex = exp2_fast(L.x), ey = exp2_fast(L.y);
                     uint32_t hi, mid;
-                    split2(__uint_as_float(k[i] << 16) * exp2_fast(E.x + l[j]),
-                           __uint_as_float(k[i] & 0xFFFF0000u) * exp2_fast(E.y + l[j]), &hi, &mid);
+                    split2(__uint_as_float(k[i] << 16) * ex, __uint_as_float(k[i] & 0xFFFF0000u) * ey, &hi, &mid);
+                    *reinterpret_cast<uint32_t *>(kq + at) = hi;
+                    *reinterpret_cast<uint32_t *>(kq + 2 * kChTerm + at) = mid;
+                    split2(__uint_as_float(q[i] << 16) * ex, __uint_as_float(q[i] & 0xFFFF0000u) * ey, &hi, &mid);
+                    *reinterpret_cast<uint32_t *>(kq + kChBox + at) = hi;
+                    *reinterpret_cast<uint32_t *>(kq + 2 * kChTerm + kChBox + at) = mid;
+                }
+                if (e == 7) *reinterpret_cast<float2 *>(&sh.dec[c & 1][ch]) = make_float2(exp2_fast(L.x), exp2_fast(L.y));
+#pragma unroll
+                for (int i = 7; i >= 0; i--) {                // backwards: exp(G_C - G_t), from the end's sum
+                    const uint32_t at = (t0 + i) * 128 + ((((uint32_t)lane >> 2) ^ i) << 4) + (lane & 3) * 4;
+                    uint32_t hi, mid;
+                    split2(__uint_as_float(k[i] << 16) * exp2_fast(E.x + l[i]),
+                           __uint_as_float(k[i] & 0xFFFF0000u) * exp2_fast(E.y + l[i]), &hi, &mid);
                     *reinterpret_cast<uint32_t *>(late + at) = hi;
                     *reinterpret_cast<uint32_t *>(late + kChTerm + at) = mid;
                     E.x += g[i].x;
                     E.y += g[i].y;
                 }
             }
+            if (!ok) break;
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mb_arrive(&sh.made);
         }
     } else if (warp == kWarpMma) {
-        // ---------------- loads and MMA issue
-        const uint32_t idk = idesc(1, 2 * kC);                 // 128 x 128, both operands K-major
-        const uint32_t idn = idk | (1u << 16);                 // B with N contiguous (K^T U: 128 channels)
-        auto load = [&](int c) {
-            uint8_t *p = stage(c);
-            uint64_t *bar = &sh.in_full[c % kStages];
-            mb_expect_tx(bar, (kChannel ? 0 : kChKq) + kChV + kChTpCopy);
-            for (int b = 0; b < 2; b++) {
-                if (!kChannel) {
-                    tma2d(p + 2 * b * kChBox, &mk, hq * kD + 64 * b, first + kC * c, bar);
-                    tma2d(p + 2 * b * kChBox + kChBox, &mq, hq * kD + 64 * b, first + kC * c, bar);
-                }
-                tma2d(p + kOffV + b * kChBox, &mv, h * kD + 64 * b, first + kC * c, bar);
-            }
-            bulk_g2s(p + kOffTp, record(c), kChTpCopy, bar);
+        // ---------------- MMA issue
+        const uint32_t idk = idesc(1, kC);                     // 128 x 64, both operands K-major
+        const uint32_t idn = idesc(1, 2 * kC) | (1u << 16);    // 128 x 128, B with N contiguous (K^T U: channels)
+        // X S^T, X's 64-channel boxes two apart: S hi, S mid, and (per channel) S hi with X mid
+        auto with_state = [&](uint32_t d, uint64_t x) {
+#pragma unroll
+            for (int term = 0; term < (kChannel ? 3 : 2); term++)
+#pragma unroll
+                for (int s = 0; s < 8; s++)
+                    umma_ts_warp(d, kTmS + 32 * (s >> 1) + 16 * (term == 1) + 8 * (s & 1),
+                                 x + (((term == 2 ? 2 * kChTerm : 0) + (s >> 2) * 2 * kChBox + (s & 3) * 32) >> 4), idk,
+                                 term > 0 || s > 0);
         };
         // D[v][t >= 16 j] += X[v][16 tokens j] tile[t][16 tokens j], the tile lower triangular
         // (hi, mid terms), X's terms at columns `x`
@@ -1163,27 +1203,18 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                                  td + (((term == 1 ? kTermBytes : 0) + term_block(j)) >> 4), idesc(1, kC - 16 * j),
                                  term > 0 || j > 0);
         };
-        if (lane == 0)
-            for (int c = 0; c < min(nc, kStages - 1); c++) load(c);
-        __syncwarp();
         for (int c = 0; c < nc; c++) {
-            // chunk c - 1's O is out: its columns and its stage are free
+            // chunk c - 1's O is read: its columns are free
             if (!wait(sh.in_full[c % kStages], c / kStages) || (kChannel && !wait(sh.made, c)) ||
                 (c >= 1 && !wait(sh.o_free, c - 1)) || !wait(sh.s_ready, c))
                 break;
             tc_fence_after();
             const uint32_t st = saddr(stage(c)), mk0 = saddr(made);
             const uint64_t kq = sdesc(kChannel ? mk0 : st);
-#pragma unroll
-            for (int term = 0; term < (kChannel ? 3 : 2); term++)   // K S and Q S: S hi, S mid, and S hi with K, Q mid
-#pragma unroll
-                for (int s = 0; s < 8; s++)
-                    umma_ts_warp(kTmR, kTmS + 32 * (s >> 1) + 16 * (term == 1) + 8 * (s & 1),
-                                 kq + (((term == 2 ? 2 * kChTerm : 0) + (s >> 2) * 2 * kChBox + (s & 3) * 32) >> 4), idk,
-                                 term > 0 || s > 0);
+            with_state(kTmR, kq);                              // K S
             umma_commit_warp(&sh.d1_full);
-            if (c + kStages - 1 < nc && lane == 0) load(c + kStages - 1);
-            __syncwarp();
+            with_state(kTmOq, kq + (kChBox >> 4));             // Q S, under the chain's next step
+            if (kChannel) umma_commit_warp(&sh.q_done);
             if (!wait(sh.r_ready, c)) break;
             tc_fence_after();
             const uint32_t tp = st + kOffTp;
@@ -1208,6 +1239,39 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         __syncwarp();
         umma_commit_warp(&sh.drain);                           // every issued MMA done before the dealloc
         mb_wait_warp(&sh.drain, 0);
+    } else if (warp == kWarpLoad) {
+        // ---------------- loads
+        auto load = [&](int c) {
+            uint8_t *p = stage(c);
+            uint64_t *bar = &sh.in_full[c % kStages];
+            mb_expect_tx(bar, (kChannel ? 0 : kChKq) + kChV + kChTpCopy);
+            for (int b = 0; b < 2; b++) {
+                if (!kChannel) {
+                    tma2d(p + 2 * b * kChBox, &mk, hq * kD + 64 * b, first + kC * c, bar);
+                    tma2d(p + 2 * b * kChBox + kChBox, &mq, hq * kD + 64 * b, first + kC * c, bar);
+                }
+                tma2d(p + kOffV + b * kChBox, &mv, h * kD + 64 * b, first + kC * c, bar);
+            }
+            bulk_g2s(p + kOffTp, record(c), kChTpCopy, bar);
+        };
+        // per channel: what the makers of chunk c's operands read, brought to the L2 (from DRAM
+        // their loads, a dependent step in every chunk, took three thousand clocks)
+        auto ahead = [&](int c) {
+            const int t0 = first + kC * c;
+            for (int t = lane; t < kC; t += 32)
+                if (t0 + t < first + len) prefetch_bulk(a.g + ((size_t)(t0 + t) * a.H + h) * kD, kD * 4);
+            if (lane < 2) {
+                prefetch2d(&mk, hq * kD + 64 * lane, t0);
+                prefetch2d(&mq, hq * kD + 64 * lane, t0);
+            }
+            if (lane == 0) prefetch_bulk(record(c), kRecBytes);
+        };
+        for (int c = 0; c < nc; c++) {
+            if (c >= kStages && !wait(sh.in_free[c % kStages], c / kStages - 1)) break;
+            if (lane == 0) load(c);
+            if (kChannel && c + 1 < nc) ahead(c + 1);
+            __syncwarp();
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -1231,10 +1295,6 @@ cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
     using Shape = ChunkShape<kChannel>;
     static bool ready = false;
     if (!ready) {
-        // the shares of setmaxnreg are of the launch's registers: with another count they would never be there
-        cudaFuncAttributes fa{};
-        if (kChannel && (cudaFuncGetAttributes(&fa, delta_chunk_kernel<kChannel>) != cudaSuccess || fa.numRegs != kChRegs))
-            return cudaErrorInvalidConfiguration;
         cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<kChannel>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::smem);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(delta_prepare_kernel<kChannel>, cudaFuncAttributeMaxDynamicSharedMemorySize,
