@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kRecThreads) delta_recurrent_kernel(const Delt
 // Numbers.  bf16 operands hold 8 bits, and one such rounding would show in the float state
 // (2^-9), so what is not a given bf16 tensor enters as two bf16 terms hi + mid (16 bits,
 // 2^-18 of the element), a product of two such as hi hi + hi mid + mid hi.  All sums are
-// float, in tensor memory; the state's carry exp(G_C) S + .. is float in registers.  A decay
+// float, in tensor memory; the state's carry exp(G_C) S + .. is a float sum.  A decay
 // below exp(-90) is zero in float beside 1: logarithms count as at least -90.
 constexpr int kC = 64;                                        // tokens a chunk
 constexpr float kLog2e = 1.4426950408889634f;
@@ -769,18 +769,16 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
 
 // ---------------------------------------------------------------- the chain
 // One block per sequence and head walks its chunks; everything is transposed so that a
-// thread owns one value column v (a lane of tensor memory) and a part of the state S^T
-// [v][k] stays in its registers: the A operands (S, R = V - exp(G) K S, U) go from registers
-// to tensor memory and never through shared memory, the B operands (K and Q, T, P) are
-// shared tiles.
+// thread owns one value column v (a lane of tensor memory) of the state S^T [v][k], and the A
+// operands (S, R = V - exp(G) K S, U) go from tensor memory to registers and back, never
+// through shared memory; the B operands (K and Q, T, P) are shared tiles.
 //   decay per head: K and Q as they are (exact in bf16); exp(G) weighs the results' columns,
 //     and U's a second time before K^T U;
 //   per channel: eight warps more write exp(G) K, exp(G) Q and exp(G_C - G) K / |k| as two
 //     terms each, a chunk ahead.
-// The chain's eight warps keep 64 floats of the state a thread, in registers or, per channel,
-// in tensor memory (there 22 warps share the registers; with the state among them they spilled
-// to local memory, which made a chunk three times as long).  Sixteen warps with 32 each took as
-// long a phase: they share four schedulers.
+// The chain's eight warps keep 64 floats of the state a thread, in tensor memory: in
+// registers they made the other roles spill, and the spills' way through the L2 made a chunk
+// three times as long.  Sixteen warps with 32 each took as long a phase: they share four schedulers.
 constexpr int kChChain = 8, kChOut = 4, kChMake = 8;
 constexpr int kChPartK = kD / (kChChain / 4), kChPartT = kC / (kChChain / 4);     // channels and tokens of a chain warp
 constexpr int kChStagesHead = 3, kChStagesChannel = 2;
@@ -803,12 +801,11 @@ template <bool kChannel> struct ChunkShape {
 constexpr int kChWarpOut = kChChain, kChWarpMake = kChWarpOut + kChOut;
 // tensor memory columns
 constexpr uint32_t kTmS = 0;      // S^T as an operand, [quarter of k][hi, mid][16]; the new S's sums over it
-constexpr uint32_t kTmR = 128;    // K S, then T R
+constexpr uint32_t kTmR = 128;    // K S, then T R; per head then U as an operand
 constexpr uint32_t kTmOq = 192;   // Q S
 constexpr uint32_t kTmOp = 256;   // P U
-constexpr uint32_t kTmRU = 320;   // R, then U (per head: weighted for the state), as an operand [hi, mid][32]
-constexpr uint32_t kTmU = 384;    // per head: U as an operand [hi, mid][32]
-constexpr uint32_t kTmF = 384;    // per channel: the state, float [128]
+constexpr uint32_t kTmRU = 320;   // R, then U (per head: weighted for the state), as an operand [half of t][hi, mid][16]
+constexpr uint32_t kTmF = 384;    // the state, float [128]
 
 constexpr int kRankSeqs = 256;                                // up to this many sequences are taken by length
 struct ChunkShared {
@@ -921,7 +918,6 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         const uint32_t la = tmem + ((uint32_t)(32 * q) << 16);
         const uint32_t la_s = la + kTmS + kChPartK * part;
         const uint32_t la_f = la + kTmF + kChPartK * part;
-        float S[kChannel ? 1 : kChPartK];
         // 32 channels of the state from b on as two terms
         auto put_terms32 = [&](int b, const float *x) {
 #pragma unroll
@@ -939,14 +935,9 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             for (int b = 0; b < kChPartK; b += 32) {
                 float x[32];
 #pragma unroll
-                for (int j = 0; j < 32; j++) {
-                    x[j] = from ? from[(size_t)(b + j) * kD] : 0.0f;
-                    if (!kChannel) S[b + j] = x[j];
-                }
-                if (kChannel) {
-                    tmem_st16(la_f + b, &x[0]);
-                    tmem_st16(la_f + b + 16, &x[16]);
-                }
+                for (int j = 0; j < 32; j++) x[j] = from ? from[(size_t)(b + j) * kD] : 0.0f;
+                tmem_st16(la_f + b, &x[0]);
+                tmem_st16(la_f + b + 16, &x[16]);
                 put_terms32(b, x);
             }
             tmem_wait_st();
@@ -968,53 +959,52 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             }
             if (!wait(sh.d1_full, c)) break;
             tc_fence_after();
-#pragma unroll
-            for (int b16 = 0; b16 < kChPartT; b16 += 16) {
-                uint32_t d[16];
-                tmem_ld16_nowait(la + kTmR + t0 + b16, d);
+            {
+                uint32_t d[kChPartT];
+                tmem_ld16_nowait(la + kTmR + t0, *reinterpret_cast<uint32_t(*)[16]>(&d[0]));
+                tmem_ld16_nowait(la + kTmR + t0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&d[16]));
                 tmem_wait_ld();
 #pragma unroll
-                for (int b = 0; b < 2; b++) {
+                for (int b = 0; b < kChPartT / 8; b++) {
                     uint32_t hi[4], mid[4];
 #pragma unroll
                     for (int j2 = 0; j2 < 4; j2++) {
-                        const int i = 8 * b + 2 * j2, j = b16 + i;
+                        const int j = 8 * b + 2 * j2;
                         const float2 kr = *reinterpret_cast<const float2 *>(&sc[kRecKr + j]);
-                        const float x = fmaf(-kr.x, __uint_as_float(d[i]), __uint_as_float(vv[j >> 1] << 16));
-                        const float y = fmaf(-kr.y, __uint_as_float(d[i + 1]), __uint_as_float(vv[j >> 1] & 0xFFFF0000u));
+                        const float x = fmaf(-kr.x, __uint_as_float(d[j]), __uint_as_float(vv[j >> 1] << 16));
+                        const float y = fmaf(-kr.y, __uint_as_float(d[j + 1]), __uint_as_float(vv[j >> 1] & 0xFFFF0000u));
                         split2(t0 + j < n ? x : 0.0f, t0 + j + 1 < n ? y : 0.0f, &hi[j2], &mid[j2]);
                     }
-                    tmem_st4(la + kTmRU + (t0 + b16) / 2 + 4 * b, hi);
-                    tmem_st4(la + kTmRU + 32 + (t0 + b16) / 2 + 4 * b, mid);
+                    tmem_st4(la + kTmRU + t0 + 4 * b, hi);
+                    tmem_st4(la + kTmRU + t0 + 16 + 4 * b, mid);
                 }
             }
             tmem_wait_st();
             arrive(sh.r_ready);
             if (!wait(sh.d2_full, c)) break;
             tc_fence_after();
-#pragma unroll
-            for (int b16 = 0; b16 < kChPartT; b16 += 16) {
-                uint32_t d[16];
-                tmem_ld16_nowait(la + kTmR + t0 + b16, d);
+            {
+                uint32_t d[kChPartT];                         // all read: per head U's terms go over them
+                tmem_ld16_nowait(la + kTmR + t0, *reinterpret_cast<uint32_t(*)[16]>(&d[0]));
+                tmem_ld16_nowait(la + kTmR + t0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&d[16]));
                 tmem_wait_ld();
 #pragma unroll
-                for (int b = 0; b < 2; b++) {
+                for (int b = 0; b < kChPartT / 8; b++) {
                     uint32_t hi[4], mid[4];
-                    const uint32_t at = (t0 + b16) / 2 + 4 * b;
 #pragma unroll
                     for (int j2 = 0; j2 < 4; j2++)
                         split2(__uint_as_float(d[8 * b + 2 * j2]), __uint_as_float(d[8 * b + 2 * j2 + 1]), &hi[j2], &mid[j2]);
-                    tmem_st4(la + (kChannel ? kTmRU : kTmU) + at, hi);
-                    tmem_st4(la + (kChannel ? kTmRU : kTmU) + 32 + at, mid);
+                    tmem_st4(la + (kChannel ? kTmRU : kTmR) + t0 + 4 * b, hi);
+                    tmem_st4(la + (kChannel ? kTmRU : kTmR) + t0 + 16 + 4 * b, mid);
                     if (!kChannel) {
 #pragma unroll
                         for (int j2 = 0; j2 < 4; j2++) {
                             const int i = 8 * b + 2 * j2;
-                            const float2 kd = *reinterpret_cast<const float2 *>(&sc[kRecKd + b16 + i]);
+                            const float2 kd = *reinterpret_cast<const float2 *>(&sc[kRecKd + i]);
                             split2(__uint_as_float(d[i]) * kd.x, __uint_as_float(d[i + 1]) * kd.y, &hi[j2], &mid[j2]);
                         }
-                        tmem_st4(la + kTmRU + at, hi);
-                        tmem_st4(la + kTmRU + 32 + at, mid);
+                        tmem_st4(la + kTmRU + t0 + 4 * b, hi);
+                        tmem_st4(la + kTmRU + t0 + 16 + 4 * b, mid);
                     }
                 }
             }
@@ -1032,21 +1022,18 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
 #pragma unroll
                 for (int b16 = 0; b16 < 32; b16 += 16) {
                     uint32_t f[16];
-                    if (kChannel) tmem_ld16_nowait(la_f + b + b16, f);
-                    if (kChannel || b16 == 0) tmem_wait_ld();
+                    tmem_ld16_nowait(la_f + b + b16, f);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int j4 = 0; j4 < 4; j4++) {
                         float4 e4 = make_float4(dec, dec, dec, dec);
                         if (kChannel) e4 = *reinterpret_cast<const float4 *>(&sh.dec[c & 1][kChPartK * part + b + b16 + 4 * j4]);
                         const float e[4] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            const int i = b16 + 4 * j4 + j;
-                            x[i] = fmaf(e[j], kChannel ? __uint_as_float(f[4 * j4 + j]) : S[b + i], __uint_as_float(d[i]));
-                            if (!kChannel) S[b + i] = x[i];
-                        }
+                        for (int j = 0; j < 4; j++)
+                            x[b16 + 4 * j4 + j] = fmaf(e[j], __uint_as_float(f[4 * j4 + j]), __uint_as_float(d[b16 + 4 * j4 + j]));
                     }
-                    if (kChannel && c + 1 < nc) tmem_st16(la_f + b + b16, &x[b16]);
+                    if (c + 1 < nc) tmem_st16(la_f + b + b16, &x[b16]);
                 }
                 if (c + 1 < nc) {
                     put_terms32(b, x);
@@ -1069,36 +1056,31 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             const float *sc = reinterpret_cast<const float *>(stage(c) + kOffTp + kTpBytes);
             if (!wait(sh.o_full, c)) break;
             tc_fence_after();
+            uint32_t w[kC / 2];                               // two tokens a word; all read before any is stored
+#pragma unroll
+            for (int b = 0; b < kC / 8; b++) {
+                uint32_t d[8], p[8];
+                tmem_ld8_nowait(la + kTmOq + 8 * b, d);
+                tmem_ld8_nowait(la + kTmOp + 8 * b, p);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 r = *reinterpret_cast<const float2 *>(&sc[kRecQr + 8 * b + j]);
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(fmaf(r.x, __uint_as_float(d[j]), __uint_as_float(p[j])),
+                                                                   fmaf(r.y, __uint_as_float(d[j + 1]), __uint_as_float(p[j + 1])));
+                    w[4 * b + j / 2] = *reinterpret_cast<const uint32_t *>(&x);
+                }
+            }
+            arrive(sh.o_free);
+            if (lane == 0) mb_arrive(&sh.in_free[c % kStages]);
+            // neighbouring lanes trade a token each: two columns of one token a store
             const int mine = lane & 1;
             uint32_t *o = reinterpret_cast<uint32_t *>(a.out + ((size_t)(first + kC * c + mine) * a.H + h) * kD + (v & ~1));
             const size_t step = (size_t)a.H * kD;             // words of two tokens
-#pragma unroll 1
-            for (int b16 = 0; b16 < kC; b16 += 16) {
-                uint32_t w[8];                                // two tokens a word
 #pragma unroll
-                for (int b = 0; b < 2; b++) {
-                    uint32_t d[8], p[8];
-                    tmem_ld8_nowait(la + kTmOq + b16 + 8 * b, d);
-                    tmem_ld8_nowait(la + kTmOp + b16 + 8 * b, p);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const float2 r = *reinterpret_cast<const float2 *>(&sc[kRecQr + b16 + 8 * b + j]);
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(fmaf(r.x, __uint_as_float(d[j]), __uint_as_float(p[j])),
-                                                                       fmaf(r.y, __uint_as_float(d[j + 1]), __uint_as_float(p[j + 1])));
-                        w[4 * b + j / 2] = *reinterpret_cast<const uint32_t *>(&x);
-                    }
-                }
-                if (b16 == kC - 16) {
-                    arrive(sh.o_free);
-                    if (lane == 0) mb_arrive(&sh.in_free[c % kStages]);
-                }
-                // neighbouring lanes trade a token each: two columns of one token a store
-#pragma unroll
-                for (int j = 0; j < 8; j++, o += step) {
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, w[j], 1);
-                    if (b16 + 2 * j + mine < n) *o = mine ? __byte_perm(got, w[j], 0x7632) : __byte_perm(w[j], got, 0x5410);
-                }
+            for (int j = 0; j < kC / 2; j++, o += step) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, w[j], 1);
+                if (2 * j + mine < n) *o = mine ? __byte_perm(got, w[j], 0x7632) : __byte_perm(w[j], got, 0x5410);
             }
         }
     } else if (kChannel && warp < kChWarpMake + kChMake) {
@@ -1199,7 +1181,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             for (int term = 0; term < 3; term++)               // hi hi, hi mid, mid hi
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                    umma_ts_warp(d + 16 * j, x + (term == 2 ? 32 : 0) + 8 * j,
+                    umma_ts_warp(d + 16 * j, x + 32 * (j >> 1) + (term == 2 ? 16 : 0) + 8 * (j & 1),
                                  td + (((term == 1 ? kTermBytes : 0) + term_block(j)) >> 4), idesc(1, kC - 16 * j),
                                  term > 0 || j > 0);
         };
@@ -1230,10 +1212,10 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             for (int term = 0; term < (kChannel ? 3 : 2); term++)   // K^T U into the state's sums
 #pragma unroll
                 for (int s = 0; s < 4; s++)
-                    umma_ts_warp(kTmS, kTmRU + 32 * (term == 1) + 8 * s, lx + (((term == 2 ? kChTerm : 0) + s * 16 * 128) >> 4),
+                    umma_ts_warp(kTmS, kTmRU + 32 * (s >> 1) + 16 * (term == 1) + 8 * (s & 1), lx + (((term == 2 ? kChTerm : 0) + s * 16 * 128) >> 4),
                                  idn, term > 0 || s > 0);
             umma_commit_warp(&sh.d4_full);
-            tri(kTmOp, kChannel ? kTmRU : kTmU, tp + 2 * kTermBytes);
+            tri(kTmOp, kChannel ? kTmRU : kTmR, tp + 2 * kTermBytes);
             umma_commit_warp(&sh.o_full);
         }
         __syncwarp();
