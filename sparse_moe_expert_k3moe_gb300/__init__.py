@@ -498,37 +498,47 @@ class MoEBlock:
 
 # ----------------------------------------------------------------------------- the token mixer's holders
 
-def _tensor(what, t, dtypes, shape, device, dense=True):
-    """Raises ValueError unless t is a tensor of this shape, of one of dtypes, on device: what
-    the entry points take on trust from a pointer.  dense: contiguous; else only its rows
-    are, with any stride between them."""
-    if t.dtype in dtypes and t.device == device and t.shape == shape:
-        if t.is_contiguous():
-            return
-        if not dense:
-            row = 1
-            for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-                if n > 1 and s != row:
-                    break
-                row *= n
-            else:
-                return
-        raise ValueError(f"{what}: strides {tuple(t.stride())} of shape {tuple(shape)} are not dense")
-    raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected "
-                     f"{' or '.join(str(d) for d in dtypes)} {tuple(shape)} on {device}")
+def _fits(t, dtypes, shape, index):
+    """Whether t has this shape, one of dtypes and is on the device of this index (-1: the host)."""
+    return t.dtype in dtypes and t.shape == shape and t.get_device() == index
 
 
-def _row_stride(t):
-    """Elements from a row to the next; a single row has none of its own."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t[0].numel())
+def _require(what, t, dtypes, shape, index, rows=False):
+    """Raises ValueError unless t fits and is contiguous (rows: each of its rows is, with any
+    stride between them): what the entry points take on trust from a pointer.  Returns the
+    elements from a row to the next."""
+    if not _fits(t, dtypes, shape, index):
+        raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected "
+                         f"{' or '.join(str(d) for d in dtypes)} {tuple(shape)} on "
+                         f"{'the host' if index < 0 else f'cuda:{index}'}")
+    row = 1
+    for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if n > 1 and s != row:
+            break
+        row *= n
+    else:
+        if shape[0] <= 1 or t.is_contiguous():
+            return row
+        if rows:
+            return t.stride(0)
+    raise ValueError(f"{what}: strides {tuple(t.stride())} of shape {tuple(shape)} are not dense")
 
 
-def _cuda(device):
+def _device(device):
+    """(torch.device with its index, index or -1 for the host)."""
     import torch
     device = torch.device(device)
     if device.type == "cuda" and device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    return device
+    return device, device.index if device.type == "cuda" else -1
+
+
+def _stream_of(stream, index):
+    """The handle of `stream`, of the current stream when it is None."""
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(index).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 class Linear:
@@ -538,33 +548,44 @@ class Linear:
     def __init__(self, lc: K3MoELinearConfig, T_max: int, device="cuda"):
         import torch
         self.lc = lc
-        self.device = _cuda(device)
+        self.device, self._index = _device(device)
         self.T_max = T_max
         self.w = self.bias = None
         self.ws_bytes = k3moe_linear_workspace_bytes(lc, T_max)
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self._bf16, self._f32 = (torch.bfloat16, torch.int16), (torch.float32,)
+        self._n, self._k, self._ytype = lc.n, lc.k, self._f32 if lc.y_f32 else self._bf16
+        self._lc, self._call = ctypes.byref(lc), lib().k3moe_linear
+
+    def _rows(self, what, t, types, shape):
+        """The row stride of x, y or the residual."""
+        if _fits(t, types, shape, self._index):
+            if t.is_contiguous():
+                return shape[1]
+            if t.stride(1) == 1 and shape[0] > 1:
+                return t.stride(0)
+        return _require(what, t, types, shape, self._index, True)
 
     def __call__(self, x, y, residual=None, stream=None):
         """x [T][k] bf16 (rows may be slices of wider ones), y [T][n] written and returned;
         residual [T][n] of y's type, which may be y."""
-        import torch
-        lc, T = self.lc, x.shape[0]
-        bf16 = (torch.bfloat16, torch.int16)
-        ytype = (torch.float32,) if lc.y_f32 else bf16
-        dev, n = self.device, lc.n
+        T, n, k, dev, w, bias = x.shape[0], self._n, self._k, self._index, self.w, self.bias
         if T > self.T_max:
             raise ValueError(f"x: {T} rows, the holder is for {self.T_max}")
-        _tensor("x", x, bf16, (T, lc.k), dev, dense=False)
-        _tensor("w", self.w, bf16, (n, lc.k), dev)
-        _tensor("y", y, ytype, (T, n), dev, dense=False)
-        if self.bias is not None:
-            _tensor("bias", self.bias, (torch.float32,), (n,), dev)
+        xs = self._rows("x", x, self._bf16, (T, k))
+        ys = self._rows("y", y, self._ytype, (T, n))
+        if not (_fits(w, self._bf16, (n, k), dev) and w.is_contiguous()):
+            _require("w", w, self._bf16, (n, k), dev)
+        rs = 0
         if residual is not None:
-            _tensor("residual", residual, ytype, (T, n), dev, dense=False)
+            rs = ys if residual is y else self._rows("residual", residual, self._ytype, (T, n))
+        if bias is not None and not (_fits(bias, self._f32, (n,), dev) and bias.is_contiguous()):
+            _require("bias", bias, self._f32, (n,), dev)
         if T:
-            k3moe_linear(lc, T, x, _row_stride(x), self.w, self.bias, residual,
-                         _row_stride(residual) if residual is not None else 0, y, _row_stride(y), self.ws,
-                         self.ws_bytes, stream)
+            _check("k3moe_linear", self._call(
+                self._lc, T, x.data_ptr(), xs, w.data_ptr(), None if bias is None else bias.data_ptr(),
+                None if residual is None else residual.data_ptr(), rs, y.data_ptr(), ys, self.ws.data_ptr(),
+                self.ws_bytes, _stream_of(stream, dev)))
         return y
 
 
@@ -575,16 +596,26 @@ class DeltaRule:
     def __init__(self, dc: K3MoEDeltaConfig, n_seq_max: int, T_max: int, device="cuda"):
         import torch
         self.dc = dc
-        self.device = _cuda(device)
+        self.device, self._index = _device(device)
         self.n_seq_max, self.T_max = n_seq_max, T_max
         self.ws_bytes = k3moe_delta_workspace_bytes(dc, n_seq_max, T_max)
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self._bf16, self._f32, self._i32 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,)
+        self._H, self._Hq, self._D, self._G = dc.n_heads, dc.n_qk_heads, dc.head_dim, dc.gate_dim
+        self._dc, self._call = ctypes.byref(dc), lib().k3moe_delta_rule
 
     def new_state(self, n_slots):
         """A zeroed pool of n_slots states [n_slots][n_heads][head_dim][head_dim] f32."""
         import torch
-        D = self.dc.head_dim
-        return torch.zeros((n_slots, self.dc.n_heads, D, D), dtype=torch.float32, device=self.device)
+        return torch.zeros((n_slots, self._H, self._D, self._D), dtype=torch.float32, device=self.device)
+
+    def _rows(self, what, t, shape):
+        """The row stride of q, k or v."""
+        if _fits(t, self._bf16, shape, self._index) and shape[0] > 1:
+            s = t.stride()
+            if s[2] == 1 and s[1] == self._D:
+                return s[0]
+        return _require(what, t, self._bf16, shape, self._index, True)
 
     def __call__(self, q, k, v, g, beta, out, state_in, state_out, seq_start=None, slots=None, stream=None):
         """q, k [T][n_qk_heads][D], v [T][n_heads][D] bf16, whose rows may be slices of wider
@@ -592,34 +623,25 @@ class DeltaRule:
         written and returned; state_in (None: zeros) and state_out [slots][n_heads][D][D] f32,
         which may be the same; slots [n_seq] int32 or None (sequence i in slot i); seq_start
         [n_seq+1] int32, or None for one token each (with one slot: one sequence)."""
-        import torch
-        dc, T, D = self.dc, q.shape[0], self.dc.head_dim
-        bf16, f32, i32 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,)
-        dev, H, qk = self.device, dc.n_heads, (T, dc.n_qk_heads, D)
-        _tensor("q", q, bf16, qk, dev, dense=False)
-        _tensor("k", k, bf16, qk, dev, dense=False)
-        _tensor("v", v, bf16, (T, H, D), dev, dense=False)
-        _tensor("g", g, f32, (T, H, dc.gate_dim), dev)
-        _tensor("beta", beta, f32, (T, H), dev)
-        _tensor("out", out, bf16, (T, H, D), dev)
+        T, H, D, dev = q.shape[0], self._H, self._D, self._index
+        f32, i32 = self._f32, self._i32
+        qs = self._rows("q", q, (T, self._Hq, D))
+        ks = self._rows("k", k, (T, self._Hq, D))
+        vs = self._rows("v", v, (T, H, D))
         n_slots = state_out.shape[0]
         pool = (n_slots, H, D, D)
-        _tensor("state_out", state_out, f32, pool, dev)
-        if state_in is not None and state_in is not state_out:
-            _tensor("state_in", state_in, f32, pool, dev)
-        if seq_start is not None:
-            n_seq = seq_start.shape[0] - 1
-            _tensor("seq_start", seq_start, i32, (n_seq + 1,), dev)
-        else:
-            n_seq = slots.shape[0] if slots is not None else T
-        if slots is not None:
-            _tensor("slots", slots, i32, (n_seq,), dev)
+        n_seq = seq_start.shape[0] - 1 if seq_start is not None else slots.shape[0] if slots is not None else T
+        for what, t, types, shape in (("g", g, f32, (T, H, self._G)), ("beta", beta, f32, (T, H)),
+                                      ("out", out, self._bf16, (T, H, D)), ("state_out", state_out, f32, pool),
+                                      ("state_in", state_in, f32, pool), ("seq_start", seq_start, i32, (n_seq + 1,)),
+                                      ("slots", slots, i32, (n_seq,))):
+            if t is not None and not (_fits(t, types, shape, dev) and t.is_contiguous()):
+                _require(what, t, types, shape, dev)
         if n_seq > self.n_seq_max or T > self.T_max:
             raise ValueError(f"{n_seq} sequences of {T} tokens, the holder is for {self.n_seq_max} and {self.T_max}")
-        if T:
-            strides = [_row_stride(t) for t in (q, k, v)]
-        else:
-            strides = [dc.n_qk_heads * D, dc.n_qk_heads * D, dc.n_heads * D]
-        k3moe_delta_rule(dc, n_seq, T, seq_start, q, strides[0], k, strides[1], v, strides[2], g, beta, state_in,
-                         state_out, n_slots, slots, out, self.ws, self.ws_bytes, stream)
+        _check("k3moe_delta_rule", self._call(
+            self._dc, n_seq, T, None if seq_start is None else seq_start.data_ptr(), q.data_ptr(), qs, k.data_ptr(), ks,
+            v.data_ptr(), vs, g.data_ptr(), beta.data_ptr(), None if state_in is None else state_in.data_ptr(),
+            state_out.data_ptr(), n_slots, None if slots is None else slots.data_ptr(), out.data_ptr(),
+            self.ws.data_ptr(), self.ws_bytes, _stream_of(stream, dev)))
         return out

@@ -496,11 +496,15 @@ cudaError_t launch_rows(const LinearArgs &a, cudaStream_t s)
         cudaFuncSetAttribute(linear_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLrSmem);
         smem_set = kLrSmem;
     }
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, linear_rows_kernel<NT>, kLrThreads, smem) !=
-            cudaSuccess ||
-        per_sm < 1)
-        per_sm = 1;
+    static thread_local size_t asked = 0;                     // the occupancy of the last shared-memory size
+    static thread_local int per_sm = 0;
+    if (per_sm == 0 || asked != smem) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, linear_rows_kernel<NT>, kLrThreads, smem) !=
+                cudaSuccess ||
+            per_sm < 1)
+            per_sm = 1;
+        asked = smem;
+    }
     const int grid = std::max(1, std::min(num_sms() * per_sm, (a.N + kLrWarps - 1) / kLrWarps));
     return launch_pdl(linear_rows_kernel<NT>, dim3(grid), dim3(kLrThreads), smem, s, a);
 }
