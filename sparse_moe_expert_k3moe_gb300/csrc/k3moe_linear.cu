@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kLrThreads) linear_rows_kernel(const LinearArg
 // ---------------------------------------------------------------- tensor cores
 constexpr int kLtBK = 64;                                    // K columns a stage: one 128-byte swizzled row
 constexpr int kLtABytes = 128 * kLtBK * 2;                   // a block's weight tile
-constexpr int kLtRing = 192 * 1024;                          // the stage ring
+constexpr int kLtRing = 192 * 1024, kLtRing2 = 96 * 1024;    // the stage ring: one block an SM, or two
 constexpr int kLtMaxStg = 10;
 constexpr int kLtWarpProd = 0, kLtWarpMma = 1, kLtWarpEpi0 = 2, kLtNumEpi = 8;
 constexpr int kLtThreads = (kLtWarpEpi0 + kLtNumEpi) * 32;   // 320
@@ -167,6 +167,9 @@ struct LinTile {
     int bn;          // tokens a tile (of both blocks of a pair)
     int n_rb, n_tt;  // weight row blocks (128 x CG rows) and token tiles
     int P;           // K parts: blocks of a cluster that share one tile
+    int per_sm;      // blocks an SM: 1, or 2 with half the ring and half the tensor memory
+    int acc;         // columns from one accumulator to the next (two, or one when P > 1)
+    int cols;        // columns of tensor memory
     int nks;         // K stages in all
     int nstg, stage_bytes;
     int group;       // weight row blocks visited together, for the L2
@@ -189,10 +192,13 @@ __device__ __forceinline__ uint32_t mapa(uint32_t a, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t a)
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
     return v;
 }
 // Tile copy whose bytes are counted on a barrier of either block of the pair.
@@ -223,6 +229,43 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t *bar)
 __device__ __forceinline__ void mb_arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Sixteen tokens' accumulators, the first `left` of them wanted, of a lane's output column.
+template <typename Y>
+__device__ __forceinline__ void lin_column(const LinearArgs &a, uint32_t taddr, int t0, int left, int col, float b)
+{
+    constexpr bool kF32 = sizeof(Y) == 4;
+    float r[16];
+    if (a.residual) {                                        // all loaded before any is stored (y may be the residual)
+        const Y *p = reinterpret_cast<const Y *>(a.residual) + (size_t)t0 * a.residual_stride + col;
+#pragma unroll
+        for (int j = 0; j < 16; j++, p += a.residual_stride) {
+            r[j] = 0.0f;
+            if (j < left) r[j] = kF32 ? (float)*reinterpret_cast<const float *>(p) : bf16_bits_to_f32((uint32_t)*p);
+        }
+    }
+    uint32_t v[16];
+    tmem_ld16_nowait(taddr, v);
+    tmem_wait_ld();
+    with_act(a.act, [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < 16; j++) v[j] = __float_as_uint(lin_act<decltype(act)::value>(__uint_as_float(v[j]) + b));
+    });
+    if (a.residual)
+#pragma unroll
+        for (int j = 0; j < 16; j++) v[j] = __float_as_uint(__uint_as_float(v[j]) + r[j]);
+    Y *p = reinterpret_cast<Y *>(a.y) + (size_t)t0 * a.y_stride + col;
+#pragma unroll
+    for (int j = 0; j < 16; j++, p += a.y_stride) {
+        if (j >= left) break;
+        if (kF32) {
+            *reinterpret_cast<uint32_t *>(p) = v[j];
+        } else {
+            const __nv_bfloat16 w = __float2bfloat16_rn(__uint_as_float(v[j]));
+            *reinterpret_cast<__nv_bfloat16 *>(p) = w;
+        }
+    }
 }
 
 // Sixteen tokens' accumulators of a warp's 32 output columns (lane = column) through the
@@ -270,18 +313,11 @@ __device__ __forceinline__ void lin_chunk(const LinearArgs &a, uint32_t taddr, i
         });
         return;
     }
-    float r[16];
-#pragma unroll
-    for (int j = 0; j < 16; j++) r[j] = col < a.N && j < left ? lin_residual(a, t0 + j, col) : 0.0f;
-    tmem_ld16_nowait(taddr, v);
-    tmem_wait_ld();
-    with_act(a.act, [&](auto act) {
-#pragma unroll
-        for (int j = 0; j < 16; j++) {
-            const float z = lin_act<decltype(act)::value>(__uint_as_float(v[j]) + b) + r[j];
-            if (col < a.N && j < left) lin_put(a, t0 + j, col, z);
-        }
-    });
+    const bool in = col < a.N;
+    if (a.f32)
+        lin_column<float>(a, taddr, t0, in ? left : 0, col, b);
+    else
+        lin_column<uint16_t>(a, taddr, t0, in ? left : 0, col, b);
 }
 
 // CG = 2: a pair of blocks computes 256 weight rows x bn tokens, each block holding 128
@@ -289,12 +325,10 @@ __device__ __forceinline__ void lin_chunk(const LinearArgs &a, uint32_t taddr, i
 // P > 1: the blocks of a cluster take a part of K each and add their sums through
 // distributed shared memory, in part order.  Persistent over tiles unless P > 1.
 template <int CG>
-__global__ void __launch_bounds__(kLtThreads, 1) linear_tc_kernel(const LinearArgs a, const LinTile tl,
+__global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(const LinearArgs a, const LinTile tl,
                                                                   const __grid_constant__ CUtensorMap mw,
                                                                   const __grid_constant__ CUtensorMap mx)
 {
-    pdl_wait();
-    pdl_trigger();
     extern __shared__ __align__(1024) uint8_t lsm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(lsm_raw) + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t full[kLtMaxStg], empty[kLtMaxStg], acc_full[2], acc_empty[2], drain;
@@ -316,7 +350,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tc_kernel(const LinearAr
         mb_init(&drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         bail = 0;
+        prefetch_map(&mw);
+        prefetch_map(&mx);
     }
+    pdl_wait();                       // nothing above touches memory or takes what the kernel before may still need
+    pdl_trigger();
     if (warp == kLtWarpMma) {
         if (CG == 2) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&tmem_base)),
@@ -324,7 +362,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tc_kernel(const LinearAr
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
         } else {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&tmem_base)),
-                         "r"(512));
+                         "r"(tl.cols));
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         }
     }
@@ -385,7 +423,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tc_kernel(const LinearAr
                 const int buf = n & 1;
                 if (n >= 2 && !mb_wait(&acc_empty[buf], ((n >> 1) - 1) & 1u)) { timeout(); break; }
                 tc_fence_after();
-                const uint32_t d0 = tmem + (uint32_t)buf * 256u;
+                const uint32_t d0 = tmem + (uint32_t)(buf * tl.acc);
                 for (int ks = ks0; ks < ks1; ks++, st++) {
                     const int s = st % nstg;
                     if (!mb_wait(&full[s], (st / nstg) & 1u)) { timeout(); break; }
@@ -433,7 +471,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tc_kernel(const LinearAr
             const int buf = n & 1;
             if (!mb_wait_warp(&acc_full[buf], (n >> 1) & 1u)) { timeout(); break; }
             tc_fence_after();
-            const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)buf * 256u;
+            const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * tl.acc);
             for (int c0 = 16 * half; c0 < ncols; c0 += 32) {
                 float v[16];
                 if (P > 1) {
@@ -465,17 +503,36 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tc_kernel(const LinearAr
         int rb, tt;
         tile_of(cid, &rb, &tt);
         const int t0 = tt * tl.bn, ncols = min(tl.bn, a.T - t0);
-        const int row = threadIdx.x & 127, col = rb * 128 + row;
-        if (!bail && threadIdx.x < 128 && col < a.N) {
-            const float b = a.bias ? __ldg(a.bias + col) : 0.0f;
-            for (int c = (int)rank; c < ncols; c += P) {             // a token in each P is this block's to finish
+        // a token in each P is this block's to finish: a thread four columns of it, every part's
+        // sums asked for before any is added (a load from another block takes a few hundred clocks)
+        const int mine = (ncols - (int)rank + P - 1) / P;
+        if (!bail)
+            for (int i = threadIdx.x; i < mine * 32; i += kLtThreads) {
+                const int c = (int)rank + (i >> 5) * P, row = (i & 31) * 4, col = rb * 128 + row;
+                if (col >= a.N) continue;
                 const uint32_t at = saddr(sm) + (uint32_t)(c * 128 + row) * 4u;
-                const float r = lin_residual(a, t0 + c, col);
-                float z = 0.0f;
-                for (int p = 0; p < P; p++) z += ld_cluster(mapa(at, (uint32_t)p));
-                with_act(a.act, [&](auto act) { lin_put(a, t0 + c, col, lin_act<decltype(act)::value>(z + b) + r); });
+                float4 v[8];
+#pragma unroll
+                for (int p = 0; p < 8; p++)
+                    if (p < P) v[p] = ld_cluster4(mapa(at, (uint32_t)p));
+                float z[4] = {}, r[4] = {};
+                const int w = min(4, a.N - col);
+                for (int j = 0; j < w; j++) r[j] = lin_residual(a, t0 + c, col + j);
+#pragma unroll
+                for (int p = 0; p < 8; p++)
+                    if (p < P) {
+                        z[0] += v[p].x;
+                        z[1] += v[p].y;
+                        z[2] += v[p].z;
+                        z[3] += v[p].w;
+                    }
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    if (j < w) {
+                        const float b = a.bias ? __ldg(a.bias + col + j) : 0.0f;
+                        with_act(a.act, [&](auto act) { lin_put(a, t0 + c, col + j, lin_act<decltype(act)::value>(z[j] + b) + r[j]); });
+                    }
             }
-        }
         cluster_sync_all();                                          // nobody leaves while its sums are read
     }
     if (warp == kLtWarpMma) {
@@ -483,7 +540,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) linear_tc_kernel(const LinearAr
         if (CG == 2)
             asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
         else
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tl.cols));
     }
 }
 
@@ -510,15 +567,19 @@ cudaError_t launch_rows(const LinearArgs &a, cudaStream_t s)
 }
 
 // The tile of a call: a pair of blocks (256 x 256) when the pairs have tiles for most of
-// the GPU; else the token tile and the K parts whose estimated time is least.  The
-// estimate, in SM clocks: a K stage of a tile takes 2 bn on the tensor cores and
-// (128 + bn) 128 bytes at about 48 a clock from the L2; a tile's start and epilogue about
-// 2500 + 16 bn; a cluster's joining 1500 more.
+// the GPU; else the token tile, the K parts and the blocks an SM whose estimated time is
+// least.  The estimate, in SM clocks: a block's K stage takes 2 bn on the tensor cores and
+// (128 + bn) 128 bytes at about 48 a clock from the L2, the latter shared by the blocks of an
+// SM; a tile's start and epilogue about 2500 + 16 bn; a cluster's joining 1500 more.
 int lin_plan(const LinearArgs &a, LinTile *tl)
 {
     const int sms = num_sms();
     tl->nks = (a.K + kLtBK - 1) / kLtBK;
     tl->P = 1;
+    tl->per_sm = 1;
+    tl->acc = 256;
+    tl->cols = 512;
+    tl->group = 8;
     const long long pairs = (long long)((a.N + 255) / 256) * ((a.T + 255) / 256);
     if (pairs * 4 >= 3LL * (sms / 2)) {
         tl->bn = 256;
@@ -526,32 +587,35 @@ int lin_plan(const LinearArgs &a, LinTile *tl)
         tl->n_tt = (a.T + 255) / 256;
         tl->stage_bytes = kLtABytes + 128 * kLtBK * 2;
         tl->nstg = kLtRing / tl->stage_bytes;
-        tl->group = 8;
         return 2;
     }
     tl->n_rb = (a.N + 127) / 128;
     double best = 1e30;
-    for (int bn = 256; bn >= 16; bn >>= 1) {
-        if (bn >= 2 * a.T && bn > 16) continue;
-        const int n_tt = (a.T + bn - 1) / bn;
-        for (int P = 1; P <= 8; P *= 2) {
+    for (int n_tt = (a.T + 255) / 256; n_tt <= 64; n_tt++) {
+        const int bn = ((a.T + n_tt - 1) / n_tt + 15) & ~15;
+        if (n_tt > 1 && bn < 64) break;
+        for (int P = 1; P <= 8; P++) {
             if (P > 1 && tl->nks / P < 4) break;
-            const long long items = (long long)tl->n_rb * n_tt * P;
-            const long long waves = (items + sms - 1) / sms;
-            const double stage = std::max(2.0 * bn, (128.0 + bn) * 128.0 / 48.0);
-            const double t = waves * ((double)((tl->nks + P - 1) / P) * stage + 2500.0 + 16.0 * bn / P +
-                                      (P > 1 ? 1500.0 + 8.0 * bn : 0.0));
-            if (t < best) {
-                best = t;
-                tl->bn = bn;
-                tl->n_tt = n_tt;
-                tl->P = P;
+            for (int per_sm = 1; per_sm <= (bn <= 128 ? 2 : 1); per_sm++) {
+                const long long items = (long long)tl->n_rb * n_tt * P, slots = (long long)sms * per_sm;
+                const long long waves = (items + slots - 1) / slots;
+                const double load = (128.0 + bn) * 128.0 / 48.0 * (items > sms ? per_sm : 1);
+                const double t = waves * ((double)((tl->nks + P - 1) / P) * std::max(2.0 * bn, load) + 2500.0 + 16.0 * bn / P +
+                                          (P > 1 ? 1500.0 + 8.0 * bn : 0.0));
+                if (t < best) {
+                    best = t;
+                    tl->bn = bn;
+                    tl->n_tt = n_tt;
+                    tl->P = P;
+                    tl->per_sm = per_sm;
+                }
             }
         }
     }
+    tl->acc = tl->bn <= 32 ? 32 : tl->bn <= 64 ? 64 : tl->bn <= 128 ? 128 : 256;
+    tl->cols = tl->P > 1 ? tl->acc : 2 * tl->acc;
     tl->stage_bytes = kLtABytes + tl->bn * kLtBK * 2;
-    tl->nstg = std::min(kLtMaxStg, kLtRing / tl->stage_bytes);
-    tl->group = 8;
+    tl->nstg = std::min(kLtMaxStg, (tl->per_sm == 2 ? kLtRing2 : kLtRing) / tl->stage_bytes);
     return 1;
 }
 
@@ -562,16 +626,16 @@ cudaError_t launch_tc(const LinearArgs &a, const LinTile &tl, cudaStream_t s)
     if (!map16s(&mw, a.w, (uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.K, 128) ||
         !map16s(&mx, a.x, (uint64_t)a.T, (uint64_t)a.K, (uint64_t)a.x_stride, (uint32_t)(tl.bn / CG)))
         return cudaErrorInvalidValue;
-    constexpr size_t smem = 1024 + kLtRing;
+    const size_t smem = 1024 + (tl.per_sm == 2 ? kLtRing2 : kLtRing);
     static bool smem_set = false;
     if (!smem_set) {
-        cudaFuncSetAttribute(linear_tc_kernel<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(linear_tc_kernel<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kLtRing);
         smem_set = true;
     }
     const int csize = CG == 2 ? 2 : tl.P;
     const int items = tl.n_rb * tl.n_tt;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(CG == 1 && tl.P > 1 ? items * tl.P : std::min(items, num_sms() / csize) * csize));
+    cfg.gridDim = dim3((unsigned)(CG == 1 && tl.P > 1 ? items * tl.P : std::min(items, num_sms() * tl.per_sm / csize) * csize));
     cfg.blockDim = dim3(kLtThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;

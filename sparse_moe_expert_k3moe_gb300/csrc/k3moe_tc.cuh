@@ -81,6 +81,10 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t by
         "l"(src), "r"(bytes), "r"(saddr(bar))
         : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
 // The same boxes and ranges brought to the L2 only.
 __device__ __forceinline__ void prefetch2d(const CUtensorMap *m, int c0, int c1)
 {
