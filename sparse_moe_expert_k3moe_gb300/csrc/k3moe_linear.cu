@@ -210,18 +210,21 @@ __device__ __forceinline__ void tma2d_pair(void *dst, const CUtensorMap *m, int 
         "l"(m), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
+// The pair's forms of umma_warp and umma_commit_warp; the commit arrives on the barrier at
+// this address in both blocks once the issued MMAs are done.
+__device__ __forceinline__ void umma_pair_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc));
+        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
 }
-// Arrives on the barrier at this address in both blocks once the issued MMAs are done.
-__device__ __forceinline__ void umma_commit_pair(uint64_t *bar)
+__device__ __forceinline__ void umma_commit_pair_warp(uint64_t *bar)
 {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
             saddr(bar)),
         "h"((uint16_t)3)
         : "memory");
@@ -416,43 +419,42 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
                     mb_wait(&full[f % nstg], (f / nstg) & 1u);
         }
     } else if (warp == kLtWarpMma) {
-        if (lane == 0 && leader) {
+        if (leader) {
             uint32_t st = 0, n = 0;
             const uint32_t id = (idesc(1, tl.bn) & ~(31u << 24)) | ((uint32_t)(128 * CG >> 4) << 24);
+            const uint32_t base = __reduce_max_sync(0xffffffffu, tmem);      // the same on every lane: a uniform register
+            auto commit = [&](uint64_t *b) {
+                if (CG == 2)
+                    umma_commit_pair_warp(b);
+                else
+                    umma_commit_warp(b);
+            };
             for (int i = cid; i < n_items && !bail; i += ncl, n++) {
                 const int buf = n & 1;
-                if (n >= 2 && !mb_wait(&acc_empty[buf], ((n >> 1) - 1) & 1u)) { timeout(); break; }
+                if (n >= 2 && !mb_wait_warp(&acc_empty[buf], ((n >> 1) - 1) & 1u)) { timeout(); break; }
                 tc_fence_after();
-                const uint32_t d0 = tmem + (uint32_t)(buf * tl.acc);
+                const uint32_t d0 = base + (uint32_t)(buf * tl.acc);
                 for (int ks = ks0; ks < ks1; ks++, st++) {
                     const int s = st % nstg;
-                    if (!mb_wait(&full[s], (st / nstg) & 1u)) { timeout(); break; }
+                    if (!mb_wait_warp(&full[s], (st / nstg) & 1u)) { timeout(); break; }
                     tc_fence_after();
-                    const uint32_t A = saddr(sm + (size_t)s * tl.stage_bytes), B = A + kLtABytes;
+                    const uint64_t A = sdesc(saddr(sm + (size_t)s * tl.stage_bytes)), B = A + (kLtABytes >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kLtBK / 16; kk++) {
                         const uint32_t acc = (ks != ks0 || kk) ? 1u : 0u;
                         if (CG == 2)
-                            umma_pair(d0, sdesc(A + kk * 32), sdesc(B + kk * 32), id, acc);
+                            umma_pair_warp(d0, A + kk * 2, B + kk * 2, id, acc);
                         else
-                            umma(d0, sdesc(A + kk * 32), sdesc(B + kk * 32), id, acc);
+                            umma_warp(d0, A + kk * 2, B + kk * 2, id, acc);
                     }
-                    if (CG == 2)
-                        umma_commit_pair(&empty[s]);
-                    else
-                        umma_commit(&empty[s]);
+                    commit(&empty[s]);
                 }
                 if (bail) break;
-                if (CG == 2)
-                    umma_commit_pair(&acc_full[buf]);
-                else
-                    umma_commit(&acc_full[buf]);
+                commit(&acc_full[buf]);
             }
-            if (CG == 2)
-                umma_commit_pair(&drain);                            // every issued MMA done before the dealloc
-            else
-                umma_commit(&drain);
-            mb_wait(&drain, 0);
+            __syncwarp();
+            commit(&drain);                                          // every issued MMA done before the dealloc
+            mb_wait_warp(&drain, 0);
         }
     } else {
         // ---------------- epilogue: output column 32 q + lane of the row block per thread
