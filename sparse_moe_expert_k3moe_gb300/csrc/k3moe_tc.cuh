@@ -135,6 +135,23 @@ __device__ __forceinline__ void umma_warp(uint32_t dtmem, uint64_t a, uint64_t b
         "l"(a), "l"(b), "r"(id), "r"(acc)
         : "memory");
 }
+__device__ __forceinline__ void mb_expect_tx_warp(uint64_t *b, uint32_t bytes)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(saddr(b)),
+        "r"(bytes)
+        : "memory");
+}
+__device__ __forceinline__ void tma2d_warp(void *dst, const CUtensorMap *m, int c0, int c1, uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];\n\t}" ::"r"(saddr(dst)),
+        "l"(m), "r"(c0), "r"(c1), "r"(saddr(bar))
+        : "memory");
+}
 // A operand in tensor memory (two 16-bit elements of K a column), B in shared memory.
 __device__ __forceinline__ void umma_ts_warp(uint32_t dtmem, uint32_t atmem, uint64_t b, uint32_t id, uint32_t acc)
 {
