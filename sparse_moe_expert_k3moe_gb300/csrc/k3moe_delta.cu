@@ -62,17 +62,12 @@ __device__ __forceinline__ float4 bf4(uint2 w)
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
                        __uint_as_float(w.y & 0xFFFF0000u));
 }
-
-// One token's vectors as a lane holds them: four channels of q, k and the decay.
-struct TokenRaw {
-    uint2 q, k;
-    float4 g;
-    uint2 v;
-    float beta;
-};
+__device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + (a.z * b.z + a.w * b.w); }
 
 // One block per (sequence, head, CW value columns).  A thread holds RPT key rows x 4 value
-// columns of the state; a warp covers 32 / (CW / 4) groups of rows.
+// columns of the state; a warp covers 32 / (CW / 4) groups of rows.  The tokens' k, q and
+// exp(g) are made ready eight at a time, one by each warp, so that a token's own steps are
+// the two products over the state, their sums over the block and the update.
 template <int CW>
 __global__ void __launch_bounds__(kRecThreads) delta_recurrent_kernel(const DeltaArgs a)
 {
@@ -82,8 +77,9 @@ __global__ void __launch_bounds__(kRecThreads) delta_recurrent_kernel(const Delt
     constexpr int kGroups = kRecThreads / kLanes;        // groups of rows
     constexpr int RPT = kD / kGroups;                    // rows a thread holds
     constexpr int kSplit = kD / CW;
-    __shared__ float red[2][kRecWarps][2][CW];           // partial sums of r and W^T q, two tokens' worth
-    __shared__ float vec[kRecWarps][3][kD];              // each warp's copy of k, q and exp(g)
+    __shared__ __align__(16) float red[2][kRecWarps][2][CW];     // partial sums of r and W^T q, two tokens' worth
+    __shared__ __align__(16) float vec[kRecWarps][3][kD];        // eight tokens' k, q and exp(g)
+    __shared__ float qks[kRecWarps], bts[kRecWarps];             // their q . k and beta
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cs = blockIdx.x % kSplit, h = (blockIdx.x / kSplit) % a.H, seq = blockIdx.x / (kSplit * a.H);
     int first, len, slot;
@@ -97,54 +93,68 @@ __global__ void __launch_bounds__(kRecThreads) delta_recurrent_kernel(const Delt
     for (int j = 0; j < RPT; j++)
         S[j] = a.state_in ? __ldcs(reinterpret_cast<const float4 *>(a.state_in + sbase + (size_t)j * kD))
                           : make_float4(0.f, 0.f, 0.f, 0.f);
-
     const int hq = h / (a.H / a.Hq);
-    auto fetch = [&](int i) {
-        TokenRaw t;
+    // token i of the sequence, by this warp, into its place
+    auto ready = [&](int i) {
         const size_t tok = (size_t)(first + i);
-        t.q = *reinterpret_cast<const uint2 *>(a.q + tok * a.q_stride + hq * kD + 4 * lane);
-        t.k = *reinterpret_cast<const uint2 *>(a.k + tok * a.k_stride + hq * kD + 4 * lane);
-        t.v = *reinterpret_cast<const uint2 *>(a.v + tok * a.v_stride + h * kD + col);
+        float4 q = bf4(*reinterpret_cast<const uint2 *>(a.q + tok * a.q_stride + hq * kD + 4 * lane));
+        float4 k = bf4(*reinterpret_cast<const uint2 *>(a.k + tok * a.k_stride + hq * kD + 4 * lane));
+        float4 g;
         if (a.gate == 1) {
-            const float g = a.g[tok * a.H + h];
-            t.g = make_float4(g, g, g, g);
+            const float g1 = a.g[tok * a.H + h];
+            g = make_float4(g1, g1, g1, g1);
         } else {
-            t.g = *reinterpret_cast<const float4 *>(a.g + (tok * a.H + h) * kD + 4 * lane);
+            g = *reinterpret_cast<const float4 *>(a.g + (tok * a.H + h) * kD + 4 * lane);
         }
-        t.beta = a.beta[tok * a.H + h];
-        return t;
+        const float beta = a.beta[tok * a.H + h];
+        float qk = dot4(q, k), qq = dot4(q, q), kk = dot4(k, k);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            qk += __shfl_xor_sync(0xffffffffu, qk, o);
+            qq += __shfl_xor_sync(0xffffffffu, qq, o);
+            kk += __shfl_xor_sync(0xffffffffu, kk, o);
+        }
+        const float qs = a.qk_norm ? a.scale / sqrtf(qq + a.eps) : a.scale, ks = a.qk_norm ? 1.0f / sqrtf(kk + a.eps) : 1.0f;
+        reinterpret_cast<float4 *>(vec[warp][0])[lane] = make_float4(k.x * ks, k.y * ks, k.z * ks, k.w * ks);
+        reinterpret_cast<float4 *>(vec[warp][1])[lane] = make_float4(q.x * qs, q.y * qs, q.z * qs, q.w * qs);
+        reinterpret_cast<float4 *>(vec[warp][2])[lane] = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
+        if (lane == 0) {
+            qks[warp] = qk * qs * ks;
+            bts[warp] = beta;
+        }
     };
-    TokenRaw nxt;
-    if (len > 0) nxt = fetch(0);
+    auto value = [&](int i) {
+        return *reinterpret_cast<const uint2 *>(a.v + (size_t)(first + i) * a.v_stride + h * kD + col);
+    };
+    uint2 vnext = make_uint2(0, 0);
+    if (len > 0) vnext = value(0);
     for (int i = 0; i < len; i++) {
-        const TokenRaw cur = nxt;
-        if (i + 1 < len) nxt = fetch(i + 1);             // in flight under this token's work
-        float4 q = bf4(cur.q), k = bf4(cur.k);
-        float qs = a.scale, ks = 1.0f;
-        if (a.qk_norm) {
-            const float qq = warp_sum(q.x * q.x + q.y * q.y + q.z * q.z + q.w * q.w);
-            const float kk = warp_sum(k.x * k.x + k.y * k.y + k.z * k.z + k.w * k.w);
-            qs = a.scale / sqrtf(qq + a.eps);
-            ks = 1.0f / sqrtf(kk + a.eps);
+        const int w8 = i & (kRecWarps - 1);
+        if (w8 == 0) {
+            if (i > 0) __syncthreads();                  // the last eight are used
+            if (i + warp < len) ready(i + warp);
+            __syncthreads();
         }
-        q = make_float4(q.x * qs, q.y * qs, q.z * qs, q.w * qs);
-        k = make_float4(k.x * ks, k.y * ks, k.z * ks, k.w * ks);
-        const float qk = warp_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w);
-        __syncwarp();
-        reinterpret_cast<float4 *>(vec[warp][0])[lane] = k;
-        reinterpret_cast<float4 *>(vec[warp][1])[lane] = q;
-        reinterpret_cast<float4 *>(vec[warp][2])[lane] =
-            make_float4(expf(cur.g.x), expf(cur.g.y), expf(cur.g.z), expf(cur.g.w));
-        __syncwarp();
+        const float4 v = bf4(vnext);
+        if (i + 1 < len) vnext = value(i + 1);           // in flight under this token's work
+        const float qk = qks[w8], beta = bts[w8];
         float4 r = make_float4(0.f, 0.f, 0.f, 0.f), o = r;
 #pragma unroll
-        for (int j = 0; j < RPT; j++) {
-            const float kj = vec[warp][0][row0 + j], qj = vec[warp][1][row0 + j], dj = vec[warp][2][row0 + j];
-            S[j].x *= dj; S[j].y *= dj; S[j].z *= dj; S[j].w *= dj;
-            r.x = fmaf(kj, S[j].x, r.x); r.y = fmaf(kj, S[j].y, r.y);
-            r.z = fmaf(kj, S[j].z, r.z); r.w = fmaf(kj, S[j].w, r.w);
-            o.x = fmaf(qj, S[j].x, o.x); o.y = fmaf(qj, S[j].y, o.y);
-            o.z = fmaf(qj, S[j].z, o.z); o.w = fmaf(qj, S[j].w, o.w);
+        for (int j4 = 0; j4 < RPT; j4 += 4) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(&vec[w8][0][row0 + j4]);
+            const float4 q4 = *reinterpret_cast<const float4 *>(&vec[w8][1][row0 + j4]);
+            const float4 d4 = *reinterpret_cast<const float4 *>(&vec[w8][2][row0 + j4]);
+            const float kj[4] = {k4.x, k4.y, k4.z, k4.w}, qj[4] = {q4.x, q4.y, q4.z, q4.w},
+                        dj[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                float4 &s = S[j4 + j];
+                s.x *= dj[j]; s.y *= dj[j]; s.z *= dj[j]; s.w *= dj[j];
+                r.x = fmaf(kj[j], s.x, r.x); r.y = fmaf(kj[j], s.y, r.y);
+                r.z = fmaf(kj[j], s.z, r.z); r.w = fmaf(kj[j], s.w, r.w);
+                o.x = fmaf(qj[j], s.x, o.x); o.y = fmaf(qj[j], s.y, o.y);
+                o.z = fmaf(qj[j], s.z, o.z); o.w = fmaf(qj[j], s.w, o.w);
+            }
         }
         // over the warp's groups of rows, then over the warps (in warp order)
 #pragma unroll
@@ -160,22 +170,26 @@ __global__ void __launch_bounds__(kRecThreads) delta_recurrent_kernel(const Delt
             *reinterpret_cast<float4 *>(&rd[warp][1][4 * cl]) = o;
         }
         __syncthreads();
-        r = o = make_float4(0.f, 0.f, 0.f, 0.f);
+        r = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kRecWarps; w++) {
             const float4 p = *reinterpret_cast<const float4 *>(&rd[w][0][4 * cl]);
             r.x += p.x; r.y += p.y; r.z += p.z; r.w += p.w;
         }
-        const float4 v = bf4(cur.v);
-        const float4 u = make_float4(cur.beta * (v.x - r.x), cur.beta * (v.y - r.y), cur.beta * (v.z - r.z),
-                                     cur.beta * (v.w - r.w));
+        const float4 u = make_float4(beta * (v.x - r.x), beta * (v.y - r.y), beta * (v.z - r.z), beta * (v.w - r.w));
 #pragma unroll
-        for (int j = 0; j < RPT; j++) {
-            const float kj = vec[warp][0][row0 + j];
-            S[j].x = fmaf(kj, u.x, S[j].x); S[j].y = fmaf(kj, u.y, S[j].y);
-            S[j].z = fmaf(kj, u.z, S[j].z); S[j].w = fmaf(kj, u.w, S[j].w);
+        for (int j4 = 0; j4 < RPT; j4 += 4) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(&vec[w8][0][row0 + j4]);
+            const float kj[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                float4 &s = S[j4 + j];
+                s.x = fmaf(kj[j], u.x, s.x); s.y = fmaf(kj[j], u.y, s.y);
+                s.z = fmaf(kj[j], u.z, s.z); s.w = fmaf(kj[j], u.w, s.w);
+            }
         }
         if (grp == 0) {
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kRecWarps; w++) {
                 const float4 p = *reinterpret_cast<const float4 *>(&rd[w][1][4 * cl]);

@@ -164,8 +164,7 @@ constexpr int kLtWarpProd = 0, kLtWarpMma = 1, kLtWarpEpi0 = 2, kLtNumEpi = 8;
 constexpr int kLtThreads = (kLtWarpEpi0 + kLtNumEpi) * 32;   // 320
 
 struct LinTile {
-    int bn;          // tokens an accumulator (of both blocks of a pair)
-    int subs;        // accumulators a tile: 1, double-buffered, or a pair's 2 side by side
+    int bn;          // tokens a tile (of both blocks of a pair)
     int n_rb, n_tt;  // weight row blocks (128 x CG rows) and token tiles
     int P;           // K parts: blocks of a cluster that share one tile
     int per_sm;      // blocks an SM: 1, or 2 with half the ring and half the tensor memory
@@ -392,28 +391,33 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
 
     if (warp == kLtWarpProd) {
         const int bn_own = tl.bn / CG;                               // token rows this block loads
-        uint32_t st = 0;
+        uint32_t st = 0, s = 0, phase = 1;                           // stages so far, its slot, the phase its slot was freed in
+        const uint32_t full0 = CG == 2 ? mapa(saddr(&full[0]), 0) : 0;
+        uint8_t *stage = sm;
         for (int i = cid; i < n_items && !bail; i += ncl) {
             int rb, tt;
             tile_of(i, &rb, &tt);
             const int n0 = rb * 128 * CG + (int)rank * 128 * (CG - 1);
-            const int t0 = tt * tl.bn * tl.subs + (int)rank * bn_own * (CG - 1);
-            for (int ks = ks0; ks < ks1; ks++, st++) {
-                const int s = st % nstg;
-                if (st >= (uint32_t)nstg && !mb_wait_warp(&empty[s], ((st / nstg) - 1) & 1u)) {
+            const int t0 = tt * tl.bn + (int)rank * bn_own * (CG - 1);
+            for (int k = ks0 * kLtBK; k < ks1 * kLtBK; k += kLtBK, st++) {
+                if (st >= (uint32_t)nstg && !mb_wait_warp(&empty[s], phase)) {
                     timeout();
                     break;
                 }
-                uint8_t *stage = sm + (size_t)s * tl.stage_bytes;
                 if (leader) mb_expect_tx_warp(&full[s], (uint32_t)(tl.stage_bytes * CG));
                 if (CG == 2) {
-                    const uint32_t fb = mapa(saddr(&full[s]), 0);
-                    tma2d_pair_warp(stage, &mw, ks * kLtBK, n0, fb);
-                    tma2d_pair_warp(stage + kLtABytes, &mx, ks * kLtBK, t0, fb);
-                    if (tl.subs == 2) tma2d_pair_warp(stage + 2 * kLtABytes, &mx, ks * kLtBK, t0 + tl.bn, fb);
+                    const uint32_t fb = full0 + 8 * s;
+                    tma2d_pair_warp(stage, &mw, k, n0, fb);
+                    tma2d_pair_warp(stage + kLtABytes, &mx, k, t0, fb);
                 } else {
-                    tma2d_warp(stage, &mw, ks * kLtBK, n0, &full[s]);
-                    tma2d_warp(stage + kLtABytes, &mx, ks * kLtBK, t0, &full[s]);
+                    tma2d_warp(stage, &mw, k, n0, &full[s]);
+                    tma2d_warp(stage + kLtABytes, &mx, k, t0, &full[s]);
+                }
+                stage += tl.stage_bytes;
+                if (++s == (uint32_t)nstg) {
+                    s = 0;
+                    stage = sm;
+                    phase ^= 1;
                 }
             }
         }
@@ -422,7 +426,9 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
                 mb_wait_warp(&full[f % nstg], (f / nstg) & 1u);
     } else if (warp == kLtWarpMma) {
         if (leader) {
-            uint32_t st = 0, n = 0;
+            uint32_t s = 0, phase = 0, n = 0;                        // slot, the phase it is filled in, tiles so far
+            const uint64_t first = sdesc(saddr(sm));
+            uint64_t A = first;
             const uint32_t id = (idesc(1, tl.bn) & ~(31u << 24)) | ((uint32_t)(128 * CG >> 4) << 24);
             const uint32_t base = __reduce_max_sync(0xffffffffu, tmem);      // the same on every lane: a uniform register
             auto commit = [&](uint64_t *b) {
@@ -432,18 +438,14 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
                     umma_commit_warp(b);
             };
             for (int i = cid; i < n_items && !bail; i += ncl, n++) {
-                const bool two = CG == 2 && tl.subs == 2;
-                const int buf = two ? 0 : n & 1;
-                if (!two && n >= 2 && !mb_wait_warp(&acc_empty[buf], ((n >> 1) - 1) & 1u)) { timeout(); break; }
+                const int buf = n & 1;
+                if (n >= 2 && !mb_wait_warp(&acc_empty[buf], ((n >> 1) - 1) & 1u)) { timeout(); break; }
                 tc_fence_after();
                 const uint32_t d0 = base + (uint32_t)(buf * tl.acc);
-                for (int ks = ks0; ks < ks1; ks++, st++) {
-                    const int s = st % nstg;
-                    if (!mb_wait_warp(&full[s], (st / nstg) & 1u)) { timeout(); break; }
+                for (int ks = ks0; ks < ks1; ks++) {
+                    if (!mb_wait_warp(&full[s], phase)) { timeout(); break; }
                     tc_fence_after();
-                    const uint64_t A = sdesc(saddr(sm + (size_t)s * tl.stage_bytes)), B = A + (kLtABytes >> 4);
-                    if (two && ks == ks0 && n > 0 && !mb_wait_warp(&acc_empty[0], (n - 1) & 1u)) { timeout(); break; }
-                    if (two) tc_fence_after();
+                    const uint64_t B = A + (kLtABytes >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kLtBK / 16; kk++) {
                         const uint32_t acc = (ks != ks0 || kk) ? 1u : 0u;
@@ -452,18 +454,16 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
                         else
                             umma_warp(d0, A + kk * 2, B + kk * 2, id, acc);
                     }
-                    if (two) {
-                        if (ks == ks0 && n > 0 && !mb_wait_warp(&acc_empty[1], (n - 1) & 1u)) { timeout(); break; }
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < kLtBK / 16; kk++)
-                            umma_pair_warp(d0 + tl.acc, A + kk * 2, B + (kLtABytes >> 4) + kk * 2, id, (ks != ks0 || kk) ? 1u : 0u);
-                    }
                     commit(&empty[s]);
+                    A += (uint64_t)(tl.stage_bytes >> 4);
+                    if (++s == (uint32_t)nstg) {
+                        s = 0;
+                        A = first;
+                        phase ^= 1;
+                    }
                 }
                 if (bail) break;
                 commit(&acc_full[buf]);
-                if (two) commit(&acc_full[1]);
             }
             __syncwarp();
             commit(&drain);                                          // every issued MMA done before the dealloc
@@ -482,33 +482,31 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
             tile_of(i, &rb, &tt);
             const int col = rb * 128 * CG + (int)rank * 128 * (CG - 1) + 32 * q + lane;
             const float b = a.bias && col < a.N ? __ldg(a.bias + col) : 0.0f;
-            for (int u = 0; u < tl.subs; u++) {
-                const int t0 = (tt * tl.subs + u) * tl.bn, ncols = min(tl.bn, a.T - t0);
-                const int buf = tl.subs == 2 ? u : (int)(n & 1);
-                if (!mb_wait_warp(&acc_full[buf], (tl.subs == 2 ? n : n >> 1) & 1u)) { timeout(); break; }
-                tc_fence_after();
-                const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * tl.acc);
-                for (int c0 = 16 * half; c0 < ncols; c0 += 32) {
-                    if (P > 1) {
-                        // this part's sums, [token][weight row], over the ring (its copies are consumed)
-                        float v[16];
-                        tmem_ld16(lane_addr + c0, v);
-                        float *dst = reinterpret_cast<float *>(sm) + (size_t)c0 * 128 + 32 * q + lane;
+            const int t0 = tt * tl.bn, ncols = min(tl.bn, a.T - t0);
+            const int buf = n & 1;
+            if (!mb_wait_warp(&acc_full[buf], (n >> 1) & 1u)) { timeout(); break; }
+            tc_fence_after();
+            const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * tl.acc);
+            for (int c0 = 16 * half; c0 < ncols; c0 += 32) {
+                if (P > 1) {
+                    // this part's sums, [token][weight row], over the ring (its copies are consumed)
+                    float v[16];
+                    tmem_ld16(lane_addr + c0, v);
+                    float *dst = reinterpret_cast<float *>(sm) + (size_t)c0 * 128 + 32 * q + lane;
 #pragma unroll
-                        for (int j = 0; j < 16; j++)
-                            if (c0 + j < ncols) dst[(size_t)j * 128] = v[j];
-                    } else {
-                        lin_chunk(a, lane_addr + c0, t0 + c0, ncols - c0, col, pairs, b);
-                    }
+                    for (int j = 0; j < 16; j++)
+                        if (c0 + j < ncols) dst[(size_t)j * 128] = v[j];
+                } else {
+                    lin_chunk(a, lane_addr + c0, t0 + c0, ncols - c0, col, pairs, b);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2)
-                        mb_arrive_cluster(mapa(saddr(&acc_empty[buf]), 0));
-                    else
-                        mb_arrive(&acc_empty[buf]);
-                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2)
+                    mb_arrive_cluster(mapa(saddr(&acc_empty[buf]), 0));
+                else
+                    mb_arrive(&acc_empty[buf]);
             }
         }
     }
@@ -583,15 +581,13 @@ cudaError_t launch_rows(const LinearArgs &a, cudaStream_t s)
     return launch_pdl(linear_rows_kernel<NT>, dim3(grid), dim3(kLrThreads), smem, s, a);
 }
 
-// The tile of a call.  A pair of blocks when the pairs have tiles for most of the GPU: 256
-// weight rows against 256 tokens, the next tile's products under this one's epilogue, or
-// against 512 in two accumulators, which fetches a quarter less a product but leaves the
-// epilogue (about 6000 clocks) bare.  Else the token tile, the K parts and the blocks an SM
-// whose estimated time is least.  The estimates are in SM clocks: a block's K stage takes its
-// products' time on the tensor cores (2 a token of 128 rows) or its bytes' at kLtRate from the
-// L2, shared by the blocks of an SM; a tile's start and epilogue about 2500 + 16 bn; a
-// cluster's joining 1500 more.
-constexpr double kLtRate = 42.0;      // bytes a clock an SM, measured with every SM fetching tiles
+// The tile of a call: a pair of blocks (256 x 256) when the pairs have tiles for most of
+// the GPU; else the token tile, the K parts and the blocks an SM whose estimated time is
+// least.  The estimate, in SM clocks: a block's K stage takes its products' time on the tensor
+// cores (2 a token of 128 rows) or its bytes' at kLtRate from the L2, shared by the blocks of
+// an SM; a tile's start and epilogue about 2500 + 16 bn; a cluster's launch and joining 8000.
+constexpr double kLtRate = 48.0;      // bytes a clock an SM
+
 int lin_plan(const LinearArgs &a, LinTile *tl)
 {
     const int sms = num_sms();
@@ -601,25 +597,12 @@ int lin_plan(const LinearArgs &a, LinTile *tl)
     tl->acc = 256;
     tl->cols = 512;
     tl->group = 8;
-    tl->subs = 1;
     const long long pairs = (long long)((a.N + 255) / 256) * ((a.T + 255) / 256);
     if (pairs * 4 >= 3LL * (sms / 2)) {
-        const int rb = (a.N + 255) / 256;
-        double best = 1e30;
-        for (int subs = 1; subs <= 2; subs++) {
-            const int n_tt = (a.T + 256 * subs - 1) / (256 * subs);
-            const long long waves = ((long long)rb * n_tt + sms / 2 - 1) / (sms / 2);
-            const double stage = std::max(512.0 * subs, (1.0 + subs) * kLtABytes / kLtRate);
-            const double t = waves * (tl->nks * stage + (subs == 2 ? 6000.0 : 0.0));
-            if (t < best) {
-                best = t;
-                tl->subs = subs;
-                tl->n_tt = n_tt;
-            }
-        }
         tl->bn = 256;
-        tl->n_rb = rb;
-        tl->stage_bytes = (1 + tl->subs) * kLtABytes;
+        tl->n_rb = (a.N + 255) / 256;
+        tl->n_tt = (a.T + 255) / 256;
+        tl->stage_bytes = 2 * kLtABytes;
         tl->nstg = kLtRing / tl->stage_bytes;
         return 2;
     }
@@ -635,7 +618,7 @@ int lin_plan(const LinearArgs &a, LinTile *tl)
                 const long long waves = (items + slots - 1) / slots;
                 const double load = (128.0 + bn) * 128.0 / kLtRate * (items > sms ? per_sm : 1);
                 const double t = waves * ((double)((tl->nks + P - 1) / P) * std::max(2.0 * bn, load) + 2500.0 + 16.0 * bn / P +
-                                          (P > 1 ? 1500.0 + 8.0 * bn : 0.0));
+                                          (P > 1 ? 8000.0 + 16.0 * bn : 0.0));
                 if (t < best) {
                     best = t;
                     tl->bn = bn;

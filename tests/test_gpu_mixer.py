@@ -94,6 +94,10 @@ LINEAR = [  # T, N, K, act, bias, residual, f32, x pad, y pad
     (2048, 2048, 2048, "gelu", True, True, False, 0, 0),
     (4097, 1, 64, "sigmoid", True, False, True, 0, 0),
     (5000, 260, 136, "none", True, True, True, 8, 4),
+    (4100, 1300, 520, "silu", True, True, False, 0, 0),      # two pairs of blocks a cluster, ragged both ways
+    (3001, 1537, 1096, "none", False, True, True, 8, 1),
+    (19969, 200, 136, "gelu", True, False, False, 0, 0),     # one pair a cluster
+    (640, 6500, 264, "relu", True, True, False, 0, 0),
 ]
 
 
