@@ -11,6 +11,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "k3moe_internal.cuh"
 #include "k3moe_tc.cuh"
 
@@ -18,7 +20,7 @@ namespace k3moe {
 namespace {
 
 constexpr int kD = kDeltaD;
-constexpr int kRecThreads = 256, kRecWarps = kRecThreads / 32;
+constexpr int kRecThreads = 256, kRecWarps = kRecThreads / 32, kRecCols = 64;
 
 // Tokens [first, first + len) and the state slot of sequence i; false (with a status bit)
 // when the caller's arrays do not describe one.
@@ -64,15 +66,17 @@ __device__ __forceinline__ float4 bf4(uint2 w)
 }
 __device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + (a.z * b.z + a.w * b.w); }
 
-// One block per (sequence, head, CW value columns).  A thread holds RPT key rows x 4 value
-// columns of the state; a warp covers 32 / (CW / 4) groups of rows.  The tokens' k, q and
-// exp(g) are made ready eight at a time, one by each warp, so that a token's own steps are
-// the two products over the state, their sums over the block and the update.
-template <int CW>
-__global__ void __launch_bounds__(kRecThreads) delta_recurrent_kernel(const DeltaArgs a)
+// One block per (sequence, head, 64 value columns).  A thread holds 8 key rows x 4 value
+// columns of the state; a warp covers two groups of rows.  The tokens' k, q and exp(g) are
+// made ready eight at a time, one by each warp, so that a token's own steps are the two
+// products over the state, their sums over the block and the update.  64 columns and three
+// blocks an SM (80 registers): 96 single-token sequences of 32 heads take 61.8 us, 6.55 TB/s;
+// with two blocks 72, with 32 columns 67, with 128 81.
+__global__ void __launch_bounds__(kRecThreads, 3) delta_recurrent_kernel(const DeltaArgs a)
 {
     pdl_wait();
     pdl_trigger();
+    constexpr int CW = kRecCols;
     constexpr int kLanes = CW / 4;                       // lanes across the columns
     constexpr int kGroups = kRecThreads / kLanes;        // groups of rows
     constexpr int RPT = kD / kGroups;                    // rows a thread holds
@@ -1276,8 +1280,10 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(512));
 }
 
-// From this many tokens a sequence on average, chunks.
-constexpr int kChunkTokensAvg = 24;
+// From this many tokens a sequence on average, chunks.  Per head they win from 13 tokens on with
+// 64 sequences of 32 heads (16 tokens: 183 us against 218) and from 21 with two; per channel from 19
+// with 37 sequences of 56 heads (32 tokens: 288 us against 435) and from 26 with two.
+constexpr int chunk_tokens_avg(bool channel) { return channel ? 22 : 16; }
 
 template <bool kChannel>
 cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
@@ -1317,24 +1323,21 @@ cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
 
 size_t delta_workspace(const k3moe_delta_config &dc, int n_seq, int T)
 {
-    // the most records of any call of at most n_seq sequences and T tokens: chunks need
-    // kChunkTokensAvg tokens a sequence
+    // the most records of any call of at most n_seq sequences and T tokens: chunks need that
+    // many tokens a sequence
     size_t bytes = kCtrOffset + kCtrBytes;
-    if (T >= kChunkTokensAvg && n_seq > 0)
-        bytes += (size_t)chunk_records(std::min(n_seq, T / kChunkTokensAvg), T) * dc.n_heads * kRecBytes;
+    const int avg = chunk_tokens_avg(dc.gate_dim > 1);
+    if (T >= avg && n_seq > 0) bytes += (size_t)chunk_records(std::min(n_seq, T / avg), T) * dc.n_heads * kRecBytes;
     return bytes;
 }
 
 cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t s)
 {
-    if (a.T >= kChunkTokensAvg * a.n_seq)
+    if (a.T >= chunk_tokens_avg(a.gate > 1) * a.n_seq)
         return a.gate == 1 ? launch_chunks<false>(a, s) : launch_chunks<true>(a, s);
-    // one block per head while they fill the GPU twice over; else 32 columns a block
-    const long long blocks = (long long)a.n_seq * a.H;
     timing_begin("delta_recurrent", s);
-    const cudaError_t err = blocks >= 2 * 152
-        ? launch_pdl(delta_recurrent_kernel<128>, dim3((unsigned)blocks), dim3(kRecThreads), 0, s, a)
-        : launch_pdl(delta_recurrent_kernel<32>, dim3((unsigned)blocks * 4), dim3(kRecThreads), 0, s, a);
+    const long long blocks = (long long)a.n_seq * a.H * (kD / kRecCols);
+    const cudaError_t err = launch_pdl(delta_recurrent_kernel, dim3((unsigned)blocks), dim3(kRecThreads), 0, s, a);
     count_launch();
     timing_end("delta_recurrent", s);
     return err;
