@@ -262,15 +262,54 @@ __device__ __forceinline__ float exp2_fast(float x)          // the same, free t
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// (x, y) as two packed bf16 terms: hi rounded to nearest, mid the rounded remainder.
-__device__ __forceinline__ void split2(float x, float y, uint32_t *hi, uint32_t *mid)
+// Two floats side by side, for the instructions that work on both.
+__device__ __forceinline__ uint64_t pack2(float x, float y)
 {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t p)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// The two bf16 of a word.
+__device__ __forceinline__ uint64_t pair_bf16(uint32_t w)
+{
+    return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// A pair as two packed bf16 terms: hi rounded to nearest, mid the rounded remainder.
+__device__ __forceinline__ void split2(uint64_t xy, uint32_t *hi, uint32_t *mid)
+{
+    const float2 v = unpack2(xy);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
     const uint32_t u = *reinterpret_cast<const uint32_t *>(&h);
-    const __nv_bfloat162 m = __floats2bfloat162_rn(x - __uint_as_float(u << 16), y - __uint_as_float(u & 0xFFFF0000u));
+    const float2 r = unpack2(fma2(pair_bf16(u), pack2(-1.0f, -1.0f), xy));
+    const __nv_bfloat162 m = __floats2bfloat162_rn(r.x, r.y);
     *hi = u;
     *mid = *reinterpret_cast<const uint32_t *>(&m);
 }
+__device__ __forceinline__ void split2(float x, float y, uint32_t *hi, uint32_t *mid) { split2(pack2(x, y), hi, mid); }
 // A whole warp's wait, asleep in the barrier's own wait (up to 20 us a time) rather than
 // polling beside the warps at work; bounded as mb_wait.
 __device__ __forceinline__ bool mb_wait_asleep(uint64_t *b, uint32_t parity)
@@ -922,7 +961,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             set_status(status, K3MOE_DEV_TIMEOUT);
             sh.bail = 1;
         }
-        return ok && !sh.bail;
+        return (bool)__all_sync(0xffffffffu, ok && !sh.bail);
     };
     // A warp's accesses to tensor memory are done: tell the barrier's waiter.
     auto arrive = [&](uint64_t &b) {
@@ -989,9 +1028,9 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                     for (int j2 = 0; j2 < 4; j2++) {
                         const int j = 8 * b + 2 * j2;
                         const float2 kr = *reinterpret_cast<const float2 *>(&sc[kRecKr + j]);
-                        const float x = fmaf(-kr.x, __uint_as_float(d[j]), __uint_as_float(vv[j >> 1] << 16));
-                        const float y = fmaf(-kr.y, __uint_as_float(d[j + 1]), __uint_as_float(vv[j >> 1] & 0xFFFF0000u));
-                        split2(t0 + j < n ? x : 0.0f, t0 + j + 1 < n ? y : 0.0f, &hi[j2], &mid[j2]);
+                        const float2 x = unpack2(fma2(pack2(-kr.x, -kr.y), pack2(__uint_as_float(d[j]), __uint_as_float(d[j + 1])),
+                                                     pair_bf16(vv[j >> 1])));
+                        split2(t0 + j < n ? x.x : 0.0f, t0 + j + 1 < n ? x.y : 0.0f, &hi[j2], &mid[j2]);
                     }
                     tmem_st4(la + kTmRU + t0 + 4 * b, hi);
                     tmem_st4(la + kTmRU + t0 + 16 + 4 * b, mid);
@@ -1019,7 +1058,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                         for (int j2 = 0; j2 < 4; j2++) {
                             const int i = 8 * b + 2 * j2;
                             const float2 kd = *reinterpret_cast<const float2 *>(&sc[kRecKd + i]);
-                            split2(__uint_as_float(d[i]) * kd.x, __uint_as_float(d[i + 1]) * kd.y, &hi[j2], &mid[j2]);
+                            split2(mul2(pack2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), pack2(kd.x, kd.y)), &hi[j2], &mid[j2]);
                         }
                         tmem_st4(la + kTmRU + t0 + 4 * b, hi);
                         tmem_st4(la + kTmRU + t0 + 16 + 4 * b, mid);
@@ -1048,8 +1087,13 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                         if (kChannel) e4 = *reinterpret_cast<const float4 *>(&sh.dec[c & 1][kChPartK * part + b + b16 + 4 * j4]);
                         const float e[4] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
-                        for (int j = 0; j < 4; j++)
-                            x[b16 + 4 * j4 + j] = fmaf(e[j], __uint_as_float(f[4 * j4 + j]), __uint_as_float(d[b16 + 4 * j4 + j]));
+                        for (int j = 0; j < 4; j += 2) {
+                            const int i = 4 * j4 + j;
+                            const float2 z = unpack2(fma2(pack2(e[j], e[j + 1]), pack2(__uint_as_float(f[i]), __uint_as_float(f[i + 1])),
+                                                         pack2(__uint_as_float(d[b16 + i]), __uint_as_float(d[b16 + i + 1]))));
+                            x[b16 + i] = z.x;
+                            x[b16 + i + 1] = z.y;
+                        }
                     }
                     if (c + 1 < nc) tmem_st16(la_f + b + b16, &x[b16]);
                 }
@@ -1116,60 +1160,61 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             for (int part = 0; part < 2; part++) {
                 const int e = (id >> 6) + 4 * part, t0 = 8 * e;
                 uint32_t k[8], q[8];
-                float2 g[8];
+                uint64_t g[8];
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     const size_t tok = tok0 + min(t0 + i, n - 1);
                     k[i] = __ldg(reinterpret_cast<const uint32_t *>(a.k + tok * a.k_stride + hq * kD + ch));
                     q[i] = __ldg(reinterpret_cast<const uint32_t *>(a.q + tok * a.q_stride + hq * kD + ch));
-                    g[i] = __ldg(reinterpret_cast<const float2 *>(a.g + (tok * a.H + h) * kD + ch));
+                    const float2 x = __ldg(reinterpret_cast<const float2 *>(a.g + (tok * a.H + h) * kD + ch));
+                    g[i] = pack2(x.x, x.y);
                 }
                 float l[8];                                   // log2 of 1 / |k|; minus infinity past the sequence's end
                 *reinterpret_cast<float4 *>(&l[0]) = __ldg(reinterpret_cast<const float4 *>(&rf[kRecKd + t0]));
                 *reinterpret_cast<float4 *>(&l[4]) = __ldg(reinterpret_cast<const float4 *>(&rf[kRecKd + t0 + 4]));
                 // the decay's sums before and after this thread's tokens
-                float2 L = make_float2(0.f, 0.f), E = L;
+                uint64_t L = pack2(0.0f, 0.0f), E = L;
 #pragma unroll
                 for (int w = 0; w < 8; w++) {
                     const float2 x = __ldg(reinterpret_cast<const float2 *>(&rf[kRecSum + w * kD + ch]));
-                    L.x += w < e ? x.x : 0.0f;
-                    L.y += w < e ? x.y : 0.0f;
-                    E.x += w > e ? x.x : 0.0f;
-                    E.y += w > e ? x.y : 0.0f;
+                    L = add2(L, w < e ? pack2(x.x, x.y) : pack2(0.0f, 0.0f));
+                    E = add2(E, w > e ? pack2(x.x, x.y) : pack2(0.0f, 0.0f));
                 }
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    const bool in = t0 + i < n;
-                    g[i].x = in ? clamp_gate(g[i].x) * kLog2e : 0.0f;
-                    g[i].y = in ? clamp_gate(g[i].y) * kLog2e : 0.0f;
+                    const float2 x = unpack2(g[i]);
+                    g[i] = t0 + i < n ? mul2(pack2(clamp_gate(x.x), clamp_gate(x.y)), pack2(kLog2e, kLog2e)) : pack2(0.0f, 0.0f);
                 }
                 if (part == 0 && c >= 1) ok = wait(sh.q_done, c - 1);      // the last chunk's K and Q are used
                 if (!ok) break;
+                const uint32_t row = (uint32_t)t0 * 128 + (lane & 3) * 4, c8 = (uint32_t)lane >> 2;
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    const uint32_t at = (t0 + i) * 128 + ((((uint32_t)lane >> 2) ^ i) << 4) + (lane & 3) * 4;
-                    L.x += g[i].x;
-                    L.y += g[i].y;
-                    const float ex = exp2_fast(L.x), ey = exp2_fast(L.y);
+                    const uint32_t at = row + i * 128 + ((c8 ^ i) << 4);
+                    L = add2(L, g[i]);
+                    const float2 s = unpack2(L);
+                    const uint64_t w = pack2(exp2_fast(s.x), exp2_fast(s.y));
                     uint32_t hi, mid;
-                    split2(__uint_as_float(k[i] << 16) * ex, __uint_as_float(k[i] & 0xFFFF0000u) * ey, &hi, &mid);
+                    split2(mul2(pair_bf16(k[i]), w), &hi, &mid);
                     *reinterpret_cast<uint32_t *>(kq + at) = hi;
                     *reinterpret_cast<uint32_t *>(kq + 2 * kChTerm + at) = mid;
-                    split2(__uint_as_float(q[i] << 16) * ex, __uint_as_float(q[i] & 0xFFFF0000u) * ey, &hi, &mid);
+                    split2(mul2(pair_bf16(q[i]), w), &hi, &mid);
                     *reinterpret_cast<uint32_t *>(kq + kChBox + at) = hi;
                     *reinterpret_cast<uint32_t *>(kq + 2 * kChTerm + kChBox + at) = mid;
                 }
-                if (e == 7) *reinterpret_cast<float2 *>(&sh.dec[c & 1][ch]) = make_float2(exp2_fast(L.x), exp2_fast(L.y));
+                if (e == 7) {
+                    const float2 s = unpack2(L);
+                    *reinterpret_cast<float2 *>(&sh.dec[c & 1][ch]) = make_float2(exp2_fast(s.x), exp2_fast(s.y));
+                }
 #pragma unroll
                 for (int i = 7; i >= 0; i--) {                // backwards: exp(G_C - G_t), from the end's sum
-                    const uint32_t at = (t0 + i) * 128 + ((((uint32_t)lane >> 2) ^ i) << 4) + (lane & 3) * 4;
+                    const uint32_t at = row + i * 128 + ((c8 ^ i) << 4);
+                    const float2 s = unpack2(add2(E, pack2(l[i], l[i])));
                     uint32_t hi, mid;
-                    split2(__uint_as_float(k[i] << 16) * exp2_fast(E.x + l[i]),
-                           __uint_as_float(k[i] & 0xFFFF0000u) * exp2_fast(E.y + l[i]), &hi, &mid);
+                    split2(mul2(pair_bf16(k[i]), pack2(exp2_fast(s.x), exp2_fast(s.y))), &hi, &mid);
                     *reinterpret_cast<uint32_t *>(late + at) = hi;
                     *reinterpret_cast<uint32_t *>(late + kChTerm + at) = mid;
-                    E.x += g[i].x;
-                    E.y += g[i].y;
+                    E = add2(E, g[i]);
                 }
             }
             if (!ok) break;
@@ -1203,16 +1248,18 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                                  td + (((term == 1 ? kTermBytes : 0) + term_block(j)) >> 4), idesc(1, kC - 16 * j),
                                  term > 0 || j > 0);
         };
-        for (int c = 0; c < nc; c++) {
-            // chunk c - 1's O is read: its columns are free
-            if (!wait(sh.in_full[c % kStages], c / kStages) || (kChannel && !wait(sh.made, c)) ||
-                (c >= 1 && !wait(sh.o_free, c - 1)) || !wait(sh.s_ready, c))
-                break;
+        // the count and the stages' place as uniform values, so that descriptors are too
+        const int chunks = (int)__reduce_max_sync(0xffffffffu, (unsigned)nc);
+        int slot_st = 0;
+        for (int c = 0; c < chunks; c++, slot_st = slot_st + 1 == kStages ? 0 : slot_st + 1) {
+            if (!wait(sh.in_full[c % kStages], c / kStages) || (kChannel && !wait(sh.made, c)) || !wait(sh.s_ready, c)) break;
             tc_fence_after();
-            const uint32_t st = saddr(stage(c)), mk0 = saddr(made);
+            const uint32_t st = saddr(ring) + (uint32_t)(slot_st * Shape::stage), mk0 = saddr(made);
             const uint64_t kq = sdesc(kChannel ? mk0 : st);
             with_state(kTmR, kq);                              // K S
             umma_commit_warp(&sh.d1_full);
+            if (c >= 1 && !wait(sh.o_free, c - 1)) break;      // chunk c - 1's O is read: its columns are free
+            tc_fence_after();
             with_state(kTmOq, kq + (kChBox >> 4));             // Q S, under the chain's next step
             if (kChannel) umma_commit_warp(&sh.q_done);
             if (!wait(sh.r_ready, c)) break;
