@@ -601,10 +601,10 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
             }
         }
         if (warp == 4 && wait(sh.full, 0)) {
-            const uint64_t d = sdesc(saddr(sm));
+            const uint32_t d = desc_lo(saddr(sm));
 #pragma unroll
             for (int s = 0; s < 8; s++) {
-                const uint64_t at = d + (((s >> 2) * kPpA + (s & 3) * 32) >> 4);
+                const uint32_t at = d + (((s >> 2) * kPpA + (s & 3) * 32) >> 4);
                 umma_warp(tmem, at, at, idesc(1, kC), s > 0);
             }
             umma_commit_warp(&sh.done);
@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
             fence_async_smem();
             __syncthreads();
             if (warp == 0) {
-                const uint64_t A = sdesc(saddr(sm)), B = sdesc(saddr(sm + 2 * kPpA));
+                const uint32_t A = desc_lo(saddr(sm)), B = desc_lo(saddr(sm + 2 * kPpA));
 #pragma unroll
                 for (int term = 0; term < 3; term++)
 #pragma unroll
@@ -874,13 +874,9 @@ struct ChunkShared {
     int seq, len[kRankSeqs];
 };
 
-// Unswizzled K-major descriptor of a T or P block: 8-row groups 256 bytes apart, their two
-// 8-column halves 128.
-__device__ __forceinline__ uint64_t tdesc(uint32_t addr)
-{
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(128u >> 4) << 16 | (uint64_t)(256u >> 4) << 32 |
-           (uint64_t)1u << 46;
-}
+// Unswizzled K-major descriptors of T and P blocks: 8-row groups 256 bytes apart, their two
+// 8-column halves (the leading offset) 128.
+constexpr uint32_t kDescTp = (256u >> 4) | (1u << 14);
 
 template <bool kChannel>
 __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
@@ -1227,7 +1223,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         const uint32_t idk = idesc(1, kC);                     // 128 x 64, both operands K-major
         const uint32_t idn = idesc(1, 2 * kC) | (1u << 16);    // 128 x 128, B with N contiguous (K^T U: channels)
         // X S^T, X's 64-channel boxes two apart: S hi, S mid, and (per channel) S hi with X mid
-        auto with_state = [&](uint32_t d, uint64_t x) {
+        auto with_state = [&](uint32_t d, uint32_t x) {
 #pragma unroll
             for (int term = 0; term < (kChannel ? 3 : 2); term++)
 #pragma unroll
@@ -1239,12 +1235,12 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         // D[v][t >= 16 j] += X[v][16 tokens j] tile[t][16 tokens j], the tile lower triangular
         // (hi, mid terms), X's terms at columns `x`
         auto tri = [&](uint32_t d, uint32_t x, uint32_t tile) {
-            const uint64_t td = tdesc(tile);
+            const uint32_t td = desc_lo(tile, 128);
 #pragma unroll
             for (int term = 0; term < 3; term++)               // hi hi, hi mid, mid hi
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                    umma_ts_warp(d + 16 * j, x + 32 * (j >> 1) + (term == 2 ? 16 : 0) + 8 * (j & 1),
+                    umma_ts_warp<kDescTp>(d + 16 * j, x + 32 * (j >> 1) + (term == 2 ? 16 : 0) + 8 * (j & 1),
                                  td + (((term == 1 ? kTermBytes : 0) + term_block(j)) >> 4), idesc(1, kC - 16 * j),
                                  term > 0 || j > 0);
         };
@@ -1255,7 +1251,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             if (!wait(sh.in_full[c % kStages], c / kStages) || (kChannel && !wait(sh.made, c)) || !wait(sh.s_ready, c)) break;
             tc_fence_after();
             const uint32_t st = saddr(ring) + (uint32_t)(slot_st * Shape::stage), mk0 = saddr(made);
-            const uint64_t kq = sdesc(kChannel ? mk0 : st);
+            const uint32_t kq = desc_lo(kChannel ? mk0 : st);
             with_state(kTmR, kq);                              // K S
             umma_commit_warp(&sh.d1_full);
             if (c >= 1 && !wait(sh.o_free, c - 1)) break;      // chunk c - 1's O is read: its columns are free
@@ -1271,8 +1267,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             tc_fence_after();
             // B with N contiguous: 64 channels a box, the boxes a leading offset apart
             constexpr int box = kChannel ? kChBox : 2 * kChBox;
-            const uint64_t lx = (sdesc(kChannel ? mk0 + 4 * kChTerm + (c & 1) * 2 * kChTerm : st) & ~((uint64_t)0x3FFFu << 16)) |
-                                (uint64_t)(box >> 4) << 16;
+            const uint32_t lx = desc_lo(kChannel ? mk0 + 4 * kChTerm + (c & 1) * 2 * kChTerm : st, box);
 #pragma unroll
             for (int term = 0; term < (kChannel ? 3 : 2); term++)   // K^T U into the state's sums
 #pragma unroll

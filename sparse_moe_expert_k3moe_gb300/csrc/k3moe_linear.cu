@@ -214,12 +214,13 @@ __device__ __forceinline__ void tma2d_pair_warp(void *dst, const CUtensorMap *m,
 }
 // The pair's forms of umma_warp and umma_commit_warp; the commit arrives on the barrier at
 // this address in both blocks once the issued MMAs are done.
-__device__ __forceinline__ void umma_pair_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
+__device__ __forceinline__ void umma_pair_warp(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescSw128)
         : "memory");
 }
 __device__ __forceinline__ void umma_commit_pair_warp(uint64_t *bar)
@@ -427,8 +428,8 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
     } else if (warp == kLtWarpMma) {
         if (leader) {
             uint32_t s = 0, phase = 0, n = 0;                        // slot, the phase it is filled in, tiles so far
-            const uint64_t first = sdesc(saddr(sm));
-            uint64_t A = first;
+            const uint32_t first = desc_lo(saddr(sm));
+            uint32_t A = first;
             const uint32_t id = (idesc(1, tl.bn) & ~(31u << 24)) | ((uint32_t)(128 * CG >> 4) << 24);
             const uint32_t base = __reduce_max_sync(0xffffffffu, tmem);      // the same on every lane: a uniform register
             auto commit = [&](uint64_t *b) {
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
                 for (int ks = ks0; ks < ks1; ks++) {
                     if (!mb_wait_warp(&full[s], phase)) { timeout(); break; }
                     tc_fence_after();
-                    const uint64_t B = A + (kLtABytes >> 4);
+                    const uint32_t B = A + (kLtABytes >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kLtBK / 16; kk++) {
                         const uint32_t acc = (ks != ks0 || kk) ? 1u : 0u;
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
                             umma_warp(d0, A + kk * 2, B + kk * 2, id, acc);
                     }
                     commit(&empty[s]);
-                    A += (uint64_t)(tl.stage_bytes >> 4);
+                    A += (uint32_t)(tl.stage_bytes >> 4);
                     if (++s == (uint32_t)nstg) {
                         s = 0;
                         A = first;

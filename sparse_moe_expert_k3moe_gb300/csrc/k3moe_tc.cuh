@@ -127,12 +127,18 @@ __device__ __forceinline__ void umma(uint32_t dtmem, uint64_t a, uint64_t b, uin
 // addresses stay uniform over the warp, which makes the issue of a small MMA several times
 // cheaper than from inside a single lane's branch (measured 160 clocks apart there for
 // 128 x 64 x 16 MMAs that take 32).
-__device__ __forceinline__ void umma_warp(uint32_t dtmem, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
+// A descriptor's halves: `lo` has the address (and the leading offset), the upper half is a
+// constant of the layout, so that one addition makes the next descriptor.
+constexpr uint32_t kDescSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);      // 128-byte swizzle, 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t leading = 16) { return (addr >> 4) | ((leading >> 4) << 16); }
+template <uint32_t kHi = kDescSw128>
+__device__ __forceinline__ void umma_warp(uint32_t dtmem, uint32_t a, uint32_t b, uint32_t id, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtmem),
-        "l"(a), "l"(b), "r"(id), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(dtmem),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kHi)
         : "memory");
 }
 __device__ __forceinline__ void mb_expect_tx_warp(uint64_t *b, uint32_t bytes)
@@ -153,12 +159,14 @@ __device__ __forceinline__ void tma2d_warp(void *dst, const CUtensorMap *m, int 
         : "memory");
 }
 // A operand in tensor memory (two 16-bit elements of K a column), B in shared memory.
-__device__ __forceinline__ void umma_ts_warp(uint32_t dtmem, uint32_t atmem, uint64_t b, uint32_t id, uint32_t acc)
+template <uint32_t kHi = kDescSw128>
+__device__ __forceinline__ void umma_ts_warp(uint32_t dtmem, uint32_t atmem, uint32_t b, uint32_t id, uint32_t acc)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(dtmem),
-        "r"(atmem), "l"(b), "r"(id), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(dtmem),
+        "r"(atmem), "r"(b), "r"(id), "r"(acc), "r"(kHi)
         : "memory");
 }
 __device__ __forceinline__ void umma_commit_warp(uint64_t *bar)
