@@ -329,7 +329,12 @@ __device__ __forceinline__ bool mb_wait_asleep(uint64_t *b, uint32_t parity)
         if (clock64() - t0 > kTcWaitCyc) return false;
     }
 }
-__device__ __forceinline__ float clamp_gate(float g) { return g < kMinGate ? kMinGate : g; }   // NaN stays
+__device__ __forceinline__ float clamp_gate(float g)           // at least kMinGate; NaN stays
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(g), "f"(kMinGate));
+    return r;
+}
 
 // Eight values of row r, columns 8 c8.., of a lower triangular tile, as two terms in the
 // tensor core's unswizzled order: 16-column block j = c8 / 2 holds rows from 16 j on, in
@@ -850,12 +855,19 @@ constexpr int kChMade = 4 * kChTerm + 4 * kChTerm;            // [hi, mid][box][
 static_assert(kTpBytes + (kRecDec + 1) * 4 <= kChTp && kTpBytes + 1024 <= kChTp, "a stage holds the record's head");
 template <bool kChannel> struct ChunkShape {
     static constexpr int warps = kChChain + kChOut + (kChannel ? kChMake : 0) + 2;    // and MMA issue, loads
-    static constexpr int threads = warps * 32;                // 448 (128 registers each), per channel 704 (80)
+    static constexpr int threads = kChannel ? (warps + 3) / 4 * 128 : warps * 32;     // per channel whole warpgroups: registers move
     static constexpr int stages = kChannel ? kChStagesChannel : kChStagesHead;
     static constexpr int stage = kChannel ? kChStageChannel : kChStageHead;
     static constexpr int smem = 1024 + (kChannel ? kChMade : 0) + stages * stage;
 };
 constexpr int kChWarpOut = kChChain, kChWarpMake = kChWarpOut + kChOut;
+// Registers a thread per channel: 80 at launch (768 threads), shares moved between the
+// warpgroups so that no role spills in a chunk's way.
+constexpr int kChRegs = 80, kChRegsChain = 96, kChRegsOut = 88, kChRegsMake = 80, kChRegsLast = 40;
+static_assert(kChRegsChain >= kChRegs && kChRegsOut >= kChRegs && kChRegsMake <= kChRegs && kChRegsLast <= kChRegs,
+              "inc only from below, dec only from above");
+static_assert(2 * kChRegsChain + kChRegsOut + 2 * kChRegsMake + kChRegsLast <= 6 * kChRegs, "shares within the launch's");
+static_assert(kChChain == 8 && kChOut == 4 && kChMake == 8, "the shares are of whole warpgroups");
 // tensor memory columns
 constexpr uint32_t kTmS = 0;      // S^T as an operand, [quarter of k][hi, mid][16]; the new S's sums over it
 constexpr uint32_t kTmR = 128;    // K S, then T R; per head then U as an operand
@@ -965,6 +977,16 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         __syncwarp();
         if (lane == 0) mb_arrive(&b);
     };
+    if (kChannel) {
+        if (warp < kChChain)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChRegsChain));
+        else if (warp < kChWarpMake)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChRegsOut));
+        else if (warp < kWarpMma)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChRegsMake));
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChRegsLast));
+    }
     if (warp < kChChain) {
         // ---------------- the chain: value column v, half of the channels or tokens
         const int q = warp & 3, part = warp >> 2, v = 32 * q + lane, t0 = kChPartT * part;
@@ -1006,6 +1028,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             uint32_t vv[kChPartT / 2];                            // two tokens a word
 #pragma unroll
             for (int j = 0; j < kChPartT / 2; j++) {
+                asm volatile("" : "+l"(vt));
                 const uint32_t x = *reinterpret_cast<const uint16_t *>(vt + 2 * j * 128 + ((v8 ^ ((2 * j) & 7u)) << 4));
                 const uint32_t y = *reinterpret_cast<const uint16_t *>(vt + 2 * j * 128 + 128 + ((v8 ^ ((2 * j + 1) & 7u)) << 4));
                 vv[j] = x | (y << 16);
@@ -1137,6 +1160,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             const size_t step = (size_t)a.H * kD;             // words of two tokens
 #pragma unroll
             for (int j = 0; j < kC / 2; j++, o += step) {
+                asm volatile("" : "+l"(o));                   // one address at a time: all 32 at once would spill
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, w[j], 1);
                 if (2 * j + mine < n) *o = mine ? __byte_perm(got, w[j], 0x7632) : __byte_perm(w[j], got, 0x5410);
             }
@@ -1157,13 +1181,23 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                 const int e = (id >> 6) + 4 * part, t0 = 8 * e;
                 uint32_t k[8], q[8];
                 uint64_t g[8];
+                {   // a token past the end reads the last one instead, and its decay counts as none
+                    const size_t tok = tok0 + min(t0, n - 1);
+                    const uint16_t *pk = a.k + tok * a.k_stride + hq * kD + ch, *pq = a.q + tok * a.q_stride + hq * kD + ch;
+                    const float *pg = a.g + (tok * a.H + h) * kD + ch;
+                    const int left = n - 1 - t0;              // steps there are after this thread's first token
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const size_t tok = tok0 + min(t0 + i, n - 1);
-                    k[i] = __ldg(reinterpret_cast<const uint32_t *>(a.k + tok * a.k_stride + hq * kD + ch));
-                    q[i] = __ldg(reinterpret_cast<const uint32_t *>(a.q + tok * a.q_stride + hq * kD + ch));
-                    const float2 x = __ldg(reinterpret_cast<const float2 *>(a.g + (tok * a.H + h) * kD + ch));
-                    g[i] = pack2(x.x, x.y);
+                    for (int i = 0; i < 8; i++) {
+                        k[i] = __ldg(reinterpret_cast<const uint32_t *>(pk));
+                        q[i] = __ldg(reinterpret_cast<const uint32_t *>(pq));
+                        const float2 x = __ldg(reinterpret_cast<const float2 *>(pg));
+                        g[i] = pack2(x.x, x.y);
+                        if (i < left) {
+                            pk += a.k_stride;
+                            pq += a.q_stride;
+                            pg += (size_t)a.H * kD;
+                        }
+                    }
                 }
                 float l[8];                                   // log2 of 1 / |k|; minus infinity past the sequence's end
                 *reinterpret_cast<float4 *>(&l[0]) = __ldg(reinterpret_cast<const float4 *>(&rf[kRecKd + t0]));
@@ -1224,7 +1258,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         const uint32_t idn = idesc(1, 2 * kC) | (1u << 16);    // 128 x 128, B with N contiguous (K^T U: channels)
         // X S^T, X's 64-channel boxes two apart: S hi, S mid, and (per channel) S hi with X mid
         auto with_state = [&](uint32_t d, uint32_t x) {
-#pragma unroll
+#pragma unroll 1
             for (int term = 0; term < (kChannel ? 3 : 2); term++)
 #pragma unroll
                 for (int s = 0; s < 8; s++)
@@ -1236,7 +1270,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         // (hi, mid terms), X's terms at columns `x`
         auto tri = [&](uint32_t d, uint32_t x, uint32_t tile) {
             const uint32_t td = desc_lo(tile, 128);
-#pragma unroll
+#pragma unroll 1
             for (int term = 0; term < 3; term++)               // hi hi, hi mid, mid hi
 #pragma unroll
                 for (int j = 0; j < 4; j++)
@@ -1268,7 +1302,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             // B with N contiguous: 64 channels a box, the boxes a leading offset apart
             constexpr int box = kChannel ? kChBox : 2 * kChBox;
             const uint32_t lx = desc_lo(kChannel ? mk0 + 4 * kChTerm + (c & 1) * 2 * kChTerm : st, box);
-#pragma unroll
+#pragma unroll 1
             for (int term = 0; term < (kChannel ? 3 : 2); term++)   // K^T U into the state's sums
 #pragma unroll
                 for (int s = 0; s < 4; s++)
@@ -1339,6 +1373,10 @@ cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
     using Shape = ChunkShape<kChannel>;
     static bool ready = false;
     if (!ready) {
+        // the shares of setmaxnreg are of the launch's registers: with another count they would never be there
+        cudaFuncAttributes fa{};
+        if (kChannel && (cudaFuncGetAttributes(&fa, delta_chunk_kernel<kChannel>) != cudaSuccess || fa.numRegs != kChRegs))
+            return cudaErrorInvalidConfiguration;
         cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<kChannel>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::smem);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(delta_prepare_kernel<kChannel>, cudaFuncAttributeMaxDynamicSharedMemorySize,
