@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(kRecThreads, 3) delta_recurrent_kernel(const D
 // float, in tensor memory; the state's carry exp(G_C) S + .. is a float sum.  A decay
 // below exp(-90) is zero in float beside 1: logarithms count as at least -90.
 constexpr int kC = 64;                                        // tokens a chunk
+constexpr int kAllChunks = 0x7fffffff;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinGate = -90.0f;
 constexpr int kTermBytes = 5120;                              // T or P, one term: 16-column blocks j of rows 16 j..63
@@ -474,27 +475,39 @@ struct PrepShared {
     alignas(16) float sum[8][kD];                             // log2 decays summed over each 8 tokens
 };
 
-// This block's sequence and first token, from its record's number; false when there is none.
-__device__ __forceinline__ bool find_chunk(const DeltaArgs &a, int rec, int *found, int *tok0, int *n)
+// The record, first token and length of chunk `unit`, false when there is none.  All chunks at
+// once (the call's only stretch): units are records.  A stretch: units are its chunks of
+// each sequence in turn.
+__device__ __forceinline__ bool find_chunk(const DeltaArgs &a, int unit, int *found, int *rec, int *tok0, int *n)
 {
     auto range = [&](int s, int *s0, int *len) {
         *s0 = a.seq_start ? a.seq_start[s] : 0;
         const int s1 = a.seq_start ? a.seq_start[s + 1] : a.T;
         *len = s1 - *s0;
-        return *s0 >= 0 && s1 >= *s0 && s1 <= a.T && rec >= *s0 / kC + s && rec < *s0 / kC + s + (*len + kC - 1) / kC;
+        return *s0 >= 0 && s1 >= *s0 && s1 <= a.T;
     };
-    int s0, len, s = 0;
-    if (a.n_seq > 1) {
-        if (threadIdx.x == 0) *found = 0x7fffffff;
-        __syncthreads();
-        for (int i = threadIdx.x; i < a.n_seq; i += kPpThreads)
-            if (range(i, &s0, &len)) atomicMin(found, i);
-        __syncthreads();
-        s = *found;
-        if (s == 0x7fffffff) return false;
+    auto holds = [&](int s, int *s0, int *len) {
+        return range(s, s0, len) && unit >= *s0 / kC + s && unit < *s0 / kC + s + (*len + kC - 1) / kC;
+    };
+    int s0, len, s = 0, c;
+    if (a.chunk1 < kAllChunks) {
+        s = unit / (a.chunk1 - a.chunk0);
+        c = a.chunk0 + unit % (a.chunk1 - a.chunk0);
+        if (!range(s, &s0, &len) || kC * c >= len) return false;
+    } else {
+        if (a.n_seq > 1) {
+            if (threadIdx.x == 0) *found = 0x7fffffff;
+            __syncthreads();
+            for (int i = threadIdx.x; i < a.n_seq; i += kPpThreads)
+                if (holds(i, &s0, &len)) atomicMin(found, i);
+            __syncthreads();
+            s = *found;
+            if (s == 0x7fffffff) return false;
+        }
+        if (!holds(s, &s0, &len)) return false;
+        c = unit - (s0 / kC + s);
     }
-    if (!range(s, &s0, &len)) return false;
-    const int c = rec - (s0 / kC + s);
+    *rec = s0 / kC + s + c;
     *tok0 = s0 + kC * c;
     *n = min(kC, len - kC * c);
     return true;
@@ -504,16 +517,21 @@ template <bool kChannel>
 __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
     delta_prepare_kernel(const DeltaArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk)
 {
-    pdl_wait();
+    // A later stretch is prepared beside the chain of the one before, launched when all of that
+    // chain's blocks run: its inputs were there before they did.
+    if (a.chunk0 == 0) pdl_wait();
     pdl_trigger();
     extern __shared__ __align__(1024) uint8_t psm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(psm_raw) + 1023) & ~(uintptr_t)1023);
     float *As = reinterpret_cast<float *>(sm);                // over the operands, once they are used
     __shared__ PrepShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rec = blockIdx.x / a.H, h = blockIdx.x % a.H, hq = h / (a.H / a.Hq);
-    int tok0, n;
-    if (!find_chunk(a, rec, &sh.seq, &tok0, &n)) return;
+    const int h = blockIdx.x % a.H, hq = h / (a.H / a.Hq);
+    int rec, tok0, n;
+    if (!find_chunk(a, blockIdx.x / a.H, &sh.seq, &rec, &tok0, &n)) {
+        if (a.chunk0 > 0 && blockIdx.x == gridDim.x - 1) pdl_wait();
+        return;
+    }
     int32_t *status = reinterpret_cast<int32_t *>(a.ws);
     uint8_t *out = a.ws + kCtrOffset + kCtrBytes + ((size_t)rec * a.H + h) * kRecBytes;
     float *outf = reinterpret_cast<float *>(out + kTpBytes);
@@ -827,6 +845,8 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
     tc_fence_after();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+    // the last block of such a launch ends after that chain: what follows finds both complete
+    if (a.chunk0 > 0 && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // ---------------------------------------------------------------- the chain
@@ -909,6 +929,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x % a.H;
     int seq = blockIdx.x / a.H;
+    if (seq >= a.n_seq) return;                               // the last pair's second block
     if (a.n_seq > 1 && a.n_seq <= kRankSeqs && a.seq_start) {
         // the long sequences first: this block's is the one as many others come before
         for (int i = threadIdx.x; i < a.n_seq; i += Shape::threads) sh.len[i] = a.seq_start[i + 1] - a.seq_start[i];
@@ -925,15 +946,20 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
     if (!delta_seq(a, seq, &first, &len, &slot)) return;
     const size_t sbase = ((size_t)slot * a.H + h) * kD * kD;
     if (len == 0) {
+        if (a.chunk0 > 0) return;
         for (int e = threadIdx.x; e < kD * kD / 4; e += Shape::threads)
             reinterpret_cast<float4 *>(a.state_out + sbase)[e] =
                 a.state_in ? reinterpret_cast<const float4 *>(a.state_in + sbase)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
         return;
     }
+    // chunk c's record; this launch's stretch stands for the sequence from here on
+    const uint8_t *rec0 = a.ws + kCtrOffset + kCtrBytes + ((size_t)(first / kC + seq + a.chunk0) * a.H + h) * kRecBytes;
+    if (a.chunk0 >= (len + kC - 1) / kC) return;
+    first += kC * a.chunk0;
+    len -= kC * a.chunk0;
+    if (a.chunk1 < kAllChunks) len = min(len, kC * (a.chunk1 - a.chunk0));
     const int hq = h / (a.H / a.Hq), nc = (len + kC - 1) / kC;
     int32_t *status = reinterpret_cast<int32_t *>(a.ws);
-    // chunk c's record
-    const uint8_t *rec0 = a.ws + kCtrOffset + kCtrBytes + ((size_t)(first / kC + seq) * a.H + h) * kRecBytes;
     auto record = [&](int c) { return rec0 + (size_t)c * a.H * kRecBytes; };
     auto stage = [&](int c) { return ring + (size_t)(c % kStages) * Shape::stage; };
 
@@ -1005,7 +1031,8 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             }
         };
         {
-            const float *from = a.state_in ? a.state_in + sbase + (size_t)(kChPartK * part) * kD + v : nullptr;
+            const float *in = a.chunk0 > 0 ? a.state_out : a.state_in;
+            const float *from = in ? in + sbase + (size_t)(kChPartK * part) * kD + v : nullptr;
 #pragma unroll
             for (int b = 0; b < kChPartK; b += 32) {
                 float x[32];
@@ -1361,6 +1388,43 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
 // with 37 sequences of 56 heads (32 tokens: 288 us against 435) and from 26 with two.
 constexpr int chunk_tokens_avg(bool channel) { return channel ? 22 : 16; }
 
+// Where the chains leave SMs free, the sequences are walked in stretches (one sequence of 8192
+// tokens x 56 heads: 546 us in one, 452 in four; per channel 875 and 687): while the chains go
+// through one, the SMs that are left prepare the next.  A stretch is as much longer than the
+// one before as preparing on those SMs is faster than the chains; the number of stretches is
+// the one with the least estimated time (microseconds: a chunk and head prepared on one SM,
+// a chain's chunk, and what one stretch more costs), ends[i] the chunk that ends the i-th.
+constexpr int kMaxStretches = 8;
+template <bool kChannel>
+int plan_stretches(const DeltaArgs &a, int (&ends)[kMaxStretches])
+{
+    ends[0] = kAllChunks;
+    const long long jobs = (long long)a.n_seq * a.H;
+    const int sms = num_sms(), last = (a.T + kC - 1) / kC;
+    if (jobs >= sms) return 1;
+    constexpr double prepare = kChannel ? 5.5 : 2.8, chain = kChannel ? 4.6 : 3.2;
+    constexpr double extra = 8.0;
+    const double chunks = (double)last / a.n_seq, grow = chain * (double)(sms - jobs) / (prepare * jobs);
+    int n = 1;
+    double least = 0.0, first = chunks, sum = 1.0, power = 1.0;
+    for (int k = 1; k <= kMaxStretches; k++, sum += power *= grow) {
+        const double us = chunks / sum * prepare * jobs / sms + (k - 1) * extra;
+        if (k == 1 || us < least) {
+            n = k;
+            least = us;
+            first = chunks / sum;
+        }
+    }
+    if (n == 1) return 1;
+    double end = 0.0;
+    for (int i = 0; i + 1 < n; i++, first *= grow) {
+        end += first;
+        ends[i] = std::min(std::max((int)(end + 0.5), 1), last);
+    }
+    ends[n - 1] = last;
+    return n;
+}
+
 template <bool kChannel>
 cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
 {
@@ -1384,18 +1448,42 @@ cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
         if (e != cudaSuccess) return e;
         ready = true;
     }
-    const long long recs = chunk_records(a.n_seq, a.T);
-    timing_begin("delta_prepare", s);
-    cudaError_t err = launch_pdl(delta_prepare_kernel<kChannel>, dim3((unsigned)(recs * a.H)), dim3(kPpThreads),
-                                 pp_smem(kChannel), s, a, mq, mk);
-    count_launch();
-    timing_end("delta_prepare", s);
-    if (err != cudaSuccess) return err;
-    timing_begin("delta_chunk", s);
-    err = launch_pdl(delta_chunk_kernel<kChannel>, dim3((unsigned)(a.n_seq * a.H)), dim3(Shape::threads), Shape::smem, s,
-                     a, mq, mk, mv);
-    count_launch();
-    timing_end("delta_chunk", s);
+    int ends[kMaxStretches];
+    const int stretches = plan_stretches<kChannel>(a, ends);
+    cudaError_t err = cudaSuccess;
+    DeltaArgs x = a;
+    for (int i = 0; i < stretches && err == cudaSuccess; i++) {
+        x.chunk0 = i > 0 ? ends[i - 1] : 0;
+        x.chunk1 = ends[i];
+        if (x.chunk1 <= x.chunk0) continue;
+        const long long units = x.chunk1 < kAllChunks ? (long long)(x.chunk1 - x.chunk0) * x.n_seq : chunk_records(a.n_seq, a.T);
+        timing_begin("delta_prepare", s);
+        err = launch_pdl(delta_prepare_kernel<kChannel>, dim3((unsigned)(units * a.H)), dim3(kPpThreads), pp_smem(kChannel), s, x, mq, mk);
+        count_launch();
+        timing_end("delta_prepare", s);
+        if (err != cudaSuccess) return err;
+        timing_begin("delta_chunk", s);
+        // Beside a prepare the chains go in pairs, a cluster of two on the SMs of a TPC: a chain whose
+        // neighbour there runs other code takes a quarter to a half longer (per channel 330 against 262 us
+        // for 53 chunks, per head 183 against 142 for 43).
+        const bool pairs = stretches > 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(pairs ? (a.n_seq * a.H + 1) & ~1 : a.n_seq * a.H));
+        cfg.blockDim = dim3(Shape::threads);
+        cfg.dynamicSmemBytes = Shape::smem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 2;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = pairs ? 2 : 1;
+        err = cudaLaunchKernelEx(&cfg, delta_chunk_kernel<kChannel>, x, mq, mk, mv);
+        count_launch();
+        timing_end("delta_chunk", s);
+    }
     return err;
 }
 

@@ -128,9 +128,10 @@ __device__ __forceinline__ void umma(uint32_t dtmem, uint64_t a, uint64_t b, uin
 // cheaper than from inside a single lane's branch (measured 160 clocks apart there for
 // 128 x 64 x 16 MMAs that take 32).
 // A descriptor's halves: `lo` has the address (and the leading offset), the upper half is a
-// constant of the layout, so that one addition makes the next descriptor.
+// constant of the layout, so that one addition makes the next descriptor.  In a cluster a
+// shared address holds the block's rank above its low 18 bits, which are all that go in.
 constexpr uint32_t kDescSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);      // 128-byte swizzle, 8-row groups 1024 bytes apart
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t leading = 16) { return (addr >> 4) | ((leading >> 4) << 16); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t leading = 16) { return ((addr >> 4) & 0x3FFFu) | ((leading >> 4) << 16); }
 template <uint32_t kHi = kDescSw128>
 __device__ __forceinline__ void umma_warp(uint32_t dtmem, uint32_t a, uint32_t b, uint32_t id, uint32_t acc)
 {

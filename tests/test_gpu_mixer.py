@@ -307,6 +307,31 @@ def test_delta_rule_in_pieces_matches_whole(k3):
     check_delta(parts, S, ref, ref_S, "pieces")
 
 
+@pytest.mark.parametrize("channel", [False, True])
+@pytest.mark.parametrize("lens,H,Hq", [([2500], 25, 5), ([1500, 0, 1101, 333], 19, 19), ([64 * 24], 75, 75)])
+def test_delta_rule_in_stretches(k3, lens, H, Hq, channel):
+    """Few long sequences: chains and the preparation of what follows go side by side."""
+    run_delta(k3, lens, H, Hq, channel, seed=17, in_place=len(lens) == 1)
+
+
+@pytest.mark.parametrize("channel", [False, True])
+def test_delta_rule_stretches_bit_for_bit(k3, channel):
+    """However a long sequence is walked, whole chunks at a time, the bits are the same."""
+    T, H = 4096, 27
+    q, k, v, g, beta = delta_inputs([T], H, H, channel, 23)
+    op = k3.DeltaRule(k3.k3moe_delta_config(H, H, gate_dim=D if channel else 1), 1, T)
+    got = []
+    for cuts in ([0, T], [0, 64, 1024, 1216, T], [0, T]):
+        out, state = torch.full((T, H, D), 9.0, dtype=torch.bfloat16, device="cuda"), op.new_state(1)
+        for t0, t1 in zip(cuts, cuts[1:]):
+            op(q[t0:t1], k[t0:t1], v[t0:t1], g[t0:t1], beta[t0:t1], out[t0:t1], state, state,
+               seq_start=torch.tensor([0, t1 - t0], dtype=torch.int32, device="cuda"))
+        assert k3.k3moe_device_status(op.ws) == (0, 0)
+        got.append((out, state))
+    for out, state in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(state, got[0][1])
+
+
 def test_delta_rule_repeats_bit_for_bit(k3):
     for lens in ([1] * 20, [300, 77, 1]):
         a = run_delta(k3, lens, 4, 2, True, seed=3)
