@@ -330,12 +330,13 @@ __device__ __forceinline__ bool mb_wait_asleep(uint64_t *b, uint32_t parity)
         if (clock64() - t0 > kTcWaitCyc) return false;
     }
 }
-__device__ __forceinline__ float clamp_gate(float g)           // at least kMinGate; NaN stays
+__device__ __forceinline__ float max_nan(float x, float y)
 {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(g), "f"(kMinGate));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
+__device__ __forceinline__ float clamp_gate(float g) { return max_nan(g, kMinGate); }   // NaN stays
 
 // Eight values of row r, columns 8 c8.., of a lower triangular tile, as two terms in the
 // tensor core's unswizzled order: 16-column block j = c8 / 2 holds rows from 16 j on, in
@@ -400,12 +401,13 @@ __device__ __forceinline__ void block_product(float *D, float sign, const float 
 
 // A <- (I + A)^-1 of a strictly lower triangular 64 x 64 A (rows kChLd floats apart), in
 // place and by blocks: the 16 x 16 diagonal blocks by substitution, then twice
-// [X11 0; -X22 A21 X11, X22].  Above the diagonal blocks is scratch.  256 threads.
-__device__ __forceinline__ void invert64(float *A, int tid)
+// [X11 0; -X22 A21 X11, X22].  Above the diagonal blocks is scratch.
+// Up to 32 x 32: four warps (w of them), which meet at barrier 1.
+__device__ __forceinline__ void four_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void invert32(float *A, int w, int lane)
 {
-    const int warp = tid >> 5, lane = tid & 31;
-    if (warp < 4) {   // column `lane` of diagonal block `warp` (lanes from 16 on repeat the others' work)
-        float *a = A + (16 * warp) * (kChLd + 1);
+    {   // column `lane` of diagonal block w (lanes from 16 on repeat the others' work)
+        float *a = A + (16 * w) * (kChLd + 1);
         float x[16];
         const int col = lane & 15;
 #pragma unroll
@@ -425,25 +427,26 @@ __device__ __forceinline__ void invert64(float *A, int tid)
 #pragma unroll
             for (int t = 0; t < 16; t++) a[t * kChLd + col] = x[t];       // zero above the diagonal
     }
-    __syncthreads();
-    {   // 16 -> 32: two pairs of blocks, two tiles of 16 x 8 each, a tile for each of four warps
-        float *a = A + 32 * (warp >> 1) * (kChLd + 1);
-        const int n0 = (warp & 1) * 8;
-        if (warp < 4) block_product<16>(&a[16 + n0], 1.0f, &a[16 * kChLd], &a[n0], n0, 16, lane);            // A21 X11
-        __syncthreads();
-        if (warp < 4)
-            block_product<16>(&a[16 * kChLd + n0], -1.0f, &a[16 * kChLd + 16], &a[16 + n0], 0, 16, lane);    // X22 (..)
-        __syncthreads();
-        const int p = 32 * (tid >> 7), r = (tid & 127) >> 3, c = (tid & 7) * 2;
-        *reinterpret_cast<float2 *>(&A[(p + r) * kChLd + p + 16 + c]) = make_float2(0.f, 0.f);
+    four_warps();
+    {   // 16 -> 32: two pairs of blocks, two tiles of 16 x 8 each
+        float *a = A + 32 * (w >> 1) * (kChLd + 1);
+        const int n0 = (w & 1) * 8;
+        block_product<16>(&a[16 + n0], 1.0f, &a[16 * kChLd], &a[n0], n0, 16, lane);                     // A21 X11
+        four_warps();
+        block_product<16>(&a[16 * kChLd + n0], -1.0f, &a[16 * kChLd + 16], &a[16 + n0], 0, 16, lane);   // X22 (..)
+        four_warps();
+#pragma unroll
+        for (int r = w & 1; r < 16; r += 8)
+            *reinterpret_cast<float2 *>(&a[(r + 2 * (lane >> 3)) * kChLd + 16 + (lane & 7) * 2]) = make_float2(0.f, 0.f);
     }
+}
+// 32 -> 64, by eight warps: eight tiles of 16 x 8; X11 and X22 are lower triangular
+__device__ __forceinline__ void invert64(float *A, int warp, int lane)
+{
+    const int m0 = 16 * (warp >> 2), n0 = 8 * (warp & 3);
+    block_product<32>(&A[m0 * kChLd + 32 + n0], 1.0f, &A[(32 + m0) * kChLd], &A[n0], n0, 32, lane);
     __syncthreads();
-    {   // 32 -> 64: eight tiles of 16 x 8, one a warp; X11 and X22 are lower triangular
-        const int m0 = 16 * (warp >> 2), n0 = 8 * (warp & 3);
-        block_product<32>(&A[m0 * kChLd + 32 + n0], 1.0f, &A[(32 + m0) * kChLd], &A[n0], n0, 32, lane);
-        __syncthreads();
-        block_product<32>(&A[(32 + m0) * kChLd + n0], -1.0f, &A[(32 + m0) * kChLd + 32], &A[32 + n0], 0, m0 + 16, lane);
-    }
+    block_product<32>(&A[(32 + m0) * kChLd + n0], -1.0f, &A[(32 + m0) * kChLd + 32], &A[32 + n0], 0, m0 + 16, lane);
     __syncthreads();
 }
 
@@ -592,19 +595,18 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
             const bool ok = wait(sh.full, 0);
             float norm = 1.0f;
             if (a.qk_norm && ok) {
-                float s0 = 0.0f, s1 = 0.0f;
+                uint64_t s0 = pack2(0.0f, 0.0f), s1 = s0;
 #pragma unroll
                 for (int j = 0; j < 16; j++) {                // chunk order is the swizzle's: a sum does not mind
                     const uint4 w = *reinterpret_cast<const uint4 *>(sm + (j >> 3) * kPpA + row * 128 + (((j & 7) ^ (row & 7)) << 4));
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int r = 0; r < 4; r++) {
-                        const float lo = __uint_as_float(u[r] << 16), hi = __uint_as_float(u[r] & 0xFFFF0000u);
-                        s0 = fmaf(lo, lo, s0);
-                        s1 = fmaf(hi, hi, s1);
-                    }
+                    const uint64_t x0 = pair_bf16(w.x), x1 = pair_bf16(w.y), x2 = pair_bf16(w.z), x3 = pair_bf16(w.w);
+                    s0 = fma2(x0, x0, s0);
+                    s1 = fma2(x1, x1, s1);
+                    s0 = fma2(x2, x2, s0);
+                    s1 = fma2(x3, x3, s1);
                 }
-                norm = 1.0f / sqrtf(s0 + s1 + a.eps);
+                const float2 sum = unpack2(add2(s0, s1));
+                norm = 1.0f / sqrtf(sum.x + sum.y + a.eps);
             }
             const bool in = t < n;
             const float eG = expf(G + E);
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
     } else {
         // a warp 8 tokens, a lane two of the 64 channels at hand
         const int t0 = 8 * warp;
-        float nk[8] = {}, nq[8] = {};
+        float nk[8] = {}, nq[8] = {}, reach = 0.0f;
         for (int half = 0; half < 2; half++) {
             const int ch = 64 * half + 2 * lane;
             uint32_t k[8], q[8];
@@ -684,27 +686,27 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 const int t = t0 + i;
-                const float kx = __uint_as_float(k[i] << 16), ky = __uint_as_float(k[i] & 0xFFFF0000u);
-                const float qx = __uint_as_float(q[i] << 16), qy = __uint_as_float(q[i] & 0xFFFF0000u);
-                nk[i] = fmaf(kx, kx, fmaf(ky, ky, nk[i]));
-                nq[i] = fmaf(qx, qx, fmaf(qy, qy, nq[i]));
+                const uint64_t kk = pair_bf16(k[i]), qq = pair_bf16(q[i]);
+                const float2 kf = unpack2(kk), qf = unpack2(qq);
+                nk[i] = fmaf(kf.x, kf.x, fmaf(kf.y, kf.y, nk[i]));
+                nq[i] = fmaf(qf.x, qf.x, fmaf(qf.y, qf.y, nq[i]));
                 const float dx = base.x + g[i].x, dy = base.y + g[i].y;       // G_t - m
-                far |= !(fabsf(dx) <= kPpRange && fabsf(dy) <= kPpRange);
-                const float ex = exp2_approx(dx), ey = exp2_approx(dy);
+                reach = max_nan(reach, max_nan(fabsf(dx), fabsf(dy)));
+                const uint64_t e = pack2(exp2_fast(dx), exp2_fast(dy));
                 const uint32_t at = t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
                 uint32_t hi, mid;
-                split2(kx * ex, ky * ey, &hi, &mid);
+                split2(mul2(kk, e), &hi, &mid);
                 *reinterpret_cast<uint32_t *>(sm + at) = hi;
                 *reinterpret_cast<uint32_t *>(sm + kPpA + at) = mid;
-                split2(qx * ex, qy * ey, &hi, &mid);
+                split2(mul2(qq, e), &hi, &mid);
                 *reinterpret_cast<uint32_t *>(sm + kC * 128 + at) = hi;
                 *reinterpret_cast<uint32_t *>(sm + kPpA + kC * 128 + at) = mid;
                 uint8_t *B = sm + 2 * kPpA;
-                split2(kx * exp2_approx(-dx), ky * exp2_approx(-dy), &hi, &mid);
+                split2(mul2(kk, pack2(exp2_fast(-dx), exp2_fast(-dy))), &hi, &mid);
                 *reinterpret_cast<uint32_t *>(B + at) = hi;
                 *reinterpret_cast<uint32_t *>(B + kPpB + at) = mid;
                 if (warp < 4) {
-                    split2(kx * exp2_approx(tail.x - g[i].x), ky * exp2_approx(tail.y - g[i].y), &hi, &mid);
+                    split2(mul2(kk, pack2(exp2_fast(tail.x - g[i].x), exp2_fast(tail.y - g[i].y))), &hi, &mid);
                     *reinterpret_cast<uint32_t *>(B + kC * 128 + at) = hi;
                     *reinterpret_cast<uint32_t *>(B + kPpB + kC * 128 + at) = mid;
                 }
@@ -722,32 +724,37 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
                 umma_commit_warp(&sh.done);
             }
         }
-        if (far) sh.far = 1;
-        // the norms: a warp's eight rows of each
+        if (!(reach <= kPpRange)) sh.far = 1;
+        // the norms, a warp's eight rows of each: every exchange halves the rows a lane still sums
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            nk[i] = warp_sum(nk[i]);
-            nq[i] = warp_sum(nq[i]);
+            const bool up = lane & 16;
+            nk[i] = (up ? nq[i] : nk[i]) + __shfl_xor_sync(0xffffffffu, up ? nk[i] : nq[i], 16);
         }
-        if (lane < 8) {
-            float k2 = nk[0], q2 = nq[0];
 #pragma unroll
-            for (int i = 1; i < 8; i++) {
-                k2 = lane == i ? nk[i] : k2;
-                q2 = lane == i ? nq[i] : q2;
-            }
-            const int t = t0 + lane;
+        for (int o = 8; o >= 2; o >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < o / 2; i++)
+                nk[i] = (up ? nk[i + o / 2] : nk[i]) + __shfl_xor_sync(0xffffffffu, up ? nk[i] : nk[i + o / 2], o);
+        }
+        const float n2 = nk[0] + __shfl_xor_sync(0xffffffffu, nk[0], 1);      // lanes below 16 K's, the others Q's
+        if (!(lane & 1)) {
+            const int t = t0 + ((lane >> 1) & 7);
             const bool in = t < n;
-            const float b = in ? a.beta[(size_t)(tok0 + t) * a.H + h] : 0.0f;
-            const float rk = !in ? 0.0f : a.qk_norm ? 1.0f / sqrtf(k2 + a.eps) : 1.0f;
-            const float qn = !in ? 0.0f : a.scale * (a.qk_norm ? 1.0f / sqrtf(q2 + a.eps) : 1.0f);
-            sh.rk[t] = rk;
-            sh.kb[t] = b * rk;
-            sh.qn[t] = qn;
-            sh.beta[t] = b;
-            outf[kRecKr + t] = rk;
-            outf[kRecKd + t] = log2f(rk);
-            outf[kRecQr + t] = qn;
+            const float norm = a.qk_norm ? 1.0f / sqrtf(n2 + a.eps) : 1.0f;
+            if (lane < 16) {
+                const float b = in ? a.beta[(size_t)(tok0 + t) * a.H + h] : 0.0f, rk = in ? norm : 0.0f;
+                sh.rk[t] = rk;
+                sh.kb[t] = b * rk;
+                sh.beta[t] = b;
+                outf[kRecKr + t] = rk;
+                outf[kRecKd + t] = log2f(rk);
+            } else {
+                const float qn = in ? a.scale * norm : 0.0f;
+                sh.qn[t] = qn;
+                outf[kRecQr + t] = qn;
+            }
         }
         if (!sh.bad) wait(sh.done, 1);
         __syncthreads();
@@ -757,14 +764,17 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
 
     if (!sh.bad) {
         // lanes 0-63 of tensor memory hold A's rows, 64-127 P's; a warp takes 32 rows of one of
-        // the two, half of their columns
+        // the two, half of their columns (the upper right quarter of either is zero: not done).
+        // A's four warps go on to invert its 32 x 32 blocks while the others write P.
         tc_fence_after();
         const int row = 32 * (warp & 3) + lane, t = row & (kC - 1), i00 = 32 * (warp >> 2);
         const bool is_a = row < kC;
         const float rowf = is_a ? sh.kb[t] : sh.qn[t];
         const int last = t < n ? (is_a ? t - 1 : t) : -1;     // the row's last token
+        const bool zero = i00 == 32 && (warp & 1) == 0;
         float v[32];
-        if (kChannel && far) {
+        if (zero) {
+        } else if (kChannel && far) {
             // one product at a time, the weight's logarithm summed backwards from t
             const uint16_t *x = (is_a ? a.k + (size_t)(tok0 + min(t, n - 1)) * a.k_stride
                                       : a.q + (size_t)(tok0 + min(t, n - 1)) * a.q_stride) + hq * kD;
@@ -791,54 +801,68 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
             tmem_ld16_nowait(at + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
             tmem_wait_ld();
         }
-        __syncthreads();                                      // the operands are used: the scratch lies over them
-        const float gh = kChannel ? 0.0f : sh.gh[t], gl = kChannel ? 0.0f : sh.gl[t];
+        if (!zero) {
+            const float gh = kChannel ? 0.0f : sh.gh[t], gl = kChannel ? 0.0f : sh.gl[t];
+            const uint64_t minus = pack2(-1.0f, -1.0f);
 #pragma unroll
-        for (int j4 = 0; j4 < 8; j4++) {
-            const float4 r4 = *reinterpret_cast<const float4 *>(&sh.rk[i00 + 4 * j4]);
-            const float r[4] = {r4.x, r4.y, r4.z, r4.w};
-            float w[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-            if (!kChannel) {
-                const float4 h4 = *reinterpret_cast<const float4 *>(&sh.gh[i00 + 4 * j4]);
-                const float4 l4 = *reinterpret_cast<const float4 *>(&sh.gl[i00 + 4 * j4]);
-                w[0] = exp2_approx(((gh - h4.x) + (gl - l4.x)) * kLog2e);
-                w[1] = exp2_approx(((gh - h4.y) + (gl - l4.y)) * kLog2e);
-                w[2] = exp2_approx(((gh - h4.z) + (gl - l4.z)) * kLog2e);
-                w[3] = exp2_approx(((gh - h4.w) + (gl - l4.w)) * kLog2e);
-            }
+            for (int j4 = 0; j4 < 32; j4 += 4) {
+                const float4 r4 = *reinterpret_cast<const float4 *>(&sh.rk[i00 + j4]);
+                const float r[4] = {r4.x, r4.y, r4.z, r4.w};
+                float gi[4] = {}, li[4] = {};
+                if (!kChannel) {
+                    const float4 h4 = *reinterpret_cast<const float4 *>(&sh.gh[i00 + j4]);
+                    const float4 l4 = *reinterpret_cast<const float4 *>(&sh.gl[i00 + j4]);
+                    gi[0] = h4.x; gi[1] = h4.y; gi[2] = h4.z; gi[3] = h4.w;
+                    li[0] = l4.x; li[1] = l4.y; li[2] = l4.z; li[3] = l4.w;
+                }
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float x = v[4 * j4 + j] * (rowf * r[j]) * w[j];
-                v[4 * j4 + j] = i00 + 4 * j4 + j <= last ? x : 0.0f;
+                for (int j = 0; j < 4; j += 2) {
+                    const int at = j4 + j;
+                    uint64_t x = mul2(pack2(v[at], v[at + 1]), mul2(pack2(rowf, rowf), pack2(r[j], r[j + 1])));
+                    if (!kChannel) {
+                        const uint64_t e = add2(fma2(pack2(gi[j], gi[j + 1]), minus, pack2(gh, gh)),
+                                                fma2(pack2(li[j], li[j + 1]), minus, pack2(gl, gl)));
+                        const float2 w = unpack2(mul2(e, pack2(kLog2e, kLog2e)));
+                        x = mul2(x, pack2(exp2_fast(w.x), exp2_fast(w.y)));
+                    }
+                    const float2 y = unpack2(x);
+                    v[at] = i00 + at <= last ? y.x : 0.0f;
+                    v[at + 1] = i00 + at + 1 <= last ? y.y : 0.0f;
+                }
             }
         }
         if (is_a) {
+            if (!zero)
 #pragma unroll
-            for (int j = 0; j < 8; j++)
-                *reinterpret_cast<float4 *>(&As[t * kChLd + i00 + 4 * j]) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        } else {
+                for (int j = 0; j < 8; j++)                   // over the operands: they are used
+                    *reinterpret_cast<float4 *>(&As[t * kChLd + i00 + 4 * j]) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            four_warps();
+            invert32(As, (warp & 1) + 2 * (warp >> 2), lane);
+        } else if (!zero) {
             const float(*v8)[8] = reinterpret_cast<const float(*)[8]>(v);
 #pragma unroll
             for (int j = 0; j < 4; j++) put_terms(out + 2 * kTermBytes, t, i00 / 8 + j, v8[j]);
         }
         __syncthreads();
-        invert64(As, tid);
-        const int r = tid >> 2, c0 = (tid & 3) * 16;
+        invert64(As, warp, lane);
+        // T = (I + A)^-1 diag(beta): a warp 16 columns of half the rows
+        const int r = 32 * (warp >> 2) + lane, c0 = 16 * (warp & 3);
+        if (c0 < 32 * (warp >> 2) + 32)
 #pragma unroll
-        for (int j8 = 0; j8 < 2; j8++) {
-            float x[8], b[8];
+            for (int j8 = 0; j8 < 2; j8++) {
+                float x[8], b[8];
 #pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-                *reinterpret_cast<float4 *>(&x[j]) = *reinterpret_cast<const float4 *>(&As[r * kChLd + c0 + 8 * j8 + j]);
-                *reinterpret_cast<float4 *>(&b[j]) = *reinterpret_cast<const float4 *>(&sh.beta[c0 + 8 * j8 + j]);
+                for (int j = 0; j < 8; j += 4) {
+                    *reinterpret_cast<float4 *>(&x[j]) = *reinterpret_cast<const float4 *>(&As[r * kChLd + c0 + 8 * j8 + j]);
+                    *reinterpret_cast<float4 *>(&b[j]) = *reinterpret_cast<const float4 *>(&sh.beta[c0 + 8 * j8 + j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const float y = x[j] * b[j];
+                    x[j] = c0 + 8 * j8 + j <= r ? y : 0.0f;
+                }
+                put_terms(out, r, c0 / 8 + j8, x);
             }
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const float y = x[j] * b[j];
-                x[j] = c0 + 8 * j8 + j <= r ? y : 0.0f;
-            }
-            put_terms(out, r, c0 / 8 + j8, x);
-        }
     }
     tc_fence_before();
     __syncthreads();
