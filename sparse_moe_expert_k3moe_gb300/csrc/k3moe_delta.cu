@@ -14,7 +14,7 @@
 #include <algorithm>
 
 #include "k3moe_internal.cuh"
-#include "k3moe_tc.cuh"
+#include "k3moe_tc_warp.cuh"
 
 namespace k3moe {
 namespace {
@@ -49,13 +49,6 @@ __device__ __forceinline__ bool delta_seq(const DeltaArgs &a, int i, int *first,
     *len = s1 - s0;
     *slot = sl;
     return true;
-}
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
 }
 
 // Four bf16 of an 8-byte word.
@@ -249,15 +242,7 @@ __host__ __device__ constexpr int term_block(int j) { return 2048 * j - 256 * j 
 // of len tokens spans at most (end / 64 - start / 64) + 1 chunks, so records never overlap.
 __host__ __device__ inline long long chunk_records(long long n_seq, long long T) { return T / kC + n_seq; }
 
-// 2^x within 2 ulp; volatile so that a select of its result stays a select (as a branch
-// around it, each of a row's values would be waited for by itself).
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float exp2_fast(float x)          // the same, free to move
+__device__ __forceinline__ float exp2_fast(float x)          // within 2 ulp
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -640,6 +625,7 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
         // a warp 8 tokens, a lane two of the 64 channels at hand
         const int t0 = 8 * warp;
         float nk[8] = {}, nq[8] = {}, reach = 0.0f;
+        if (tid < kC) sh.beta[tid] = tid < n ? a.beta[(size_t)(tok0 + tid) * a.H + h] : 0.0f;
         for (int half = 0; half < 2; half++) {
             const int ch = 64 * half + 2 * lane;
             uint32_t k[8], q[8];
@@ -744,10 +730,9 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
             const bool in = t < n;
             const float norm = a.qk_norm ? 1.0f / sqrtf(n2 + a.eps) : 1.0f;
             if (lane < 16) {
-                const float b = in ? a.beta[(size_t)(tok0 + t) * a.H + h] : 0.0f, rk = in ? norm : 0.0f;
+                const float rk = in ? norm : 0.0f;
                 sh.rk[t] = rk;
-                sh.kb[t] = b * rk;
-                sh.beta[t] = b;
+                sh.kb[t] = sh.beta[t] * rk;
                 outf[kRecKr + t] = rk;
                 outf[kRecKd + t] = log2f(rk);
             } else {
@@ -790,7 +775,7 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
                     const int i = i00 + j;
                     if (i <= t && t < n) {
                         v[j] = fmaf(xc * bf16_bits_to_f32(a.k[(size_t)(tok0 + i) * a.k_stride + hq * kD + c]),
-                                    exp2_approx(D * kLog2e), v[j]);
+                                    exp2_fast(D * kLog2e), v[j]);
                         D += clamp_gate(a.g[((size_t)(tok0 + i) * a.H + h) * kD + c]);
                     }
                 }
@@ -1407,10 +1392,12 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(512));
 }
 
-// From this many tokens a sequence on average, chunks.  Per head they win from 13 tokens on with
-// 64 sequences of 32 heads (16 tokens: 183 us against 218) and from 21 with two; per channel from 19
-// with 37 sequences of 56 heads (32 tokens: 288 us against 435) and from 26 with two.
-constexpr int chunk_tokens_avg(bool channel) { return channel ? 22 : 16; }
+// From this many tokens a sequence on average, chunks; `alone` where the recurrent kernel's
+// blocks have an SM each.  Recurrent against chunks, us, per head: 64 sequences x 32 heads of 12
+// tokens 147, 175 and of 16 187, 177; 8 x 32 heads of 12 25, 25; alone (one sequence, 56
+// heads) of 16 11.7, 13.9 and of 24 16.2, 13.9.  Per channel: 37 x 56 heads of 20 tokens 244,
+// 263 and of 24 286, 264; alone of 24 16.1, 20.7 and of 32 20.7, 20.8.
+constexpr int chunk_tokens_avg(bool channel, bool alone) { return channel ? (alone ? 32 : 22) : (alone ? 20 : 15); }
 
 // Where the chains leave SMs free, the sequences are walked in stretches (one sequence of 8192
 // tokens x 56 heads: 546 us in one, 452 in four; per channel 875 and 687): while the chains go
@@ -1518,17 +1505,17 @@ size_t delta_workspace(const k3moe_delta_config &dc, int n_seq, int T)
     // the most records of any call of at most n_seq sequences and T tokens: chunks need that
     // many tokens a sequence
     size_t bytes = kCtrOffset + kCtrBytes;
-    const int avg = chunk_tokens_avg(dc.gate_dim > 1);
+    const int avg = chunk_tokens_avg(dc.gate_dim > 1, false);
     if (T >= avg && n_seq > 0) bytes += (size_t)chunk_records(std::min(n_seq, T / avg), T) * dc.n_heads * kRecBytes;
     return bytes;
 }
 
 cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t s)
 {
-    if (a.T >= chunk_tokens_avg(a.gate > 1) * a.n_seq)
+    const long long blocks = (long long)a.n_seq * a.H * (kD / kRecCols);
+    if (a.T >= (long long)chunk_tokens_avg(a.gate > 1, blocks <= num_sms()) * a.n_seq)
         return a.gate == 1 ? launch_chunks<false>(a, s) : launch_chunks<true>(a, s);
     timing_begin("delta_recurrent", s);
-    const long long blocks = (long long)a.n_seq * a.H * (kD / kRecCols);
     const cudaError_t err = launch_pdl(delta_recurrent_kernel, dim3((unsigned)blocks), dim3(kRecThreads), 0, s, a);
     count_launch();
     timing_end("delta_recurrent", s);

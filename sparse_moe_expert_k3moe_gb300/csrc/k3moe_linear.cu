@@ -13,7 +13,7 @@
 #include <cuda_bf16.h>
 
 #include "k3moe_internal.cuh"
-#include "k3moe_tc.cuh"
+#include "k3moe_tc_warp.cuh"
 
 namespace k3moe {
 namespace {
