@@ -59,37 +59,74 @@ __device__ __forceinline__ float4 bf4(uint2 w)
 }
 __device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + (a.z * b.z + a.w * b.w); }
 
-// One block per (sequence, head, 64 value columns).  A thread holds 8 key rows x 4 value
-// columns of the state; a warp covers two groups of rows.  The tokens' k, q and exp(g) are
-// made ready eight at a time, one by each warp, so that a token's own steps are the two
-// products over the state, their sums over the block and the update.  64 columns and three
-// blocks an SM (80 registers): 96 single-token sequences of 32 heads take 61.8 us, 6.55 TB/s;
-// with two blocks 72, with 32 columns 67, with 128 81.
-__global__ void __launch_bounds__(kRecThreads, 3) delta_recurrent_kernel(const DeltaArgs a)
+// Two floats side by side, for the instructions that work on both.
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t p)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// One block per (sequence, head, 64 value columns).  A warp holds 16 key rows of the state, a
+// lane two value columns of them, rows in pairs for the instructions that take two floats.
+// The tokens' k, q and exp(g) are made ready eight at a time, one by each warp, so that a
+// token's own steps are the two products over the state, their sums over the block (one
+// barrier) and the update.  What bounds it: with one token a sequence the state's bytes, with more the
+// barrier and the sums.  64 columns and four blocks an SM (64 registers): 96 single-token
+// sequences of 32 heads take 60.6 us, 6.6 TB/s, 37 x 4 tokens of 56 heads 56.5 us; three blocks
+// 62.7 and 60.7.  A lane with four columns and eight rows: 62.2 and 69.4 (twice the sums
+// to add), two tokens a barrier there 72.8.
+__global__ void __launch_bounds__(kRecThreads, 4) delta_recurrent_kernel(const DeltaArgs a)
 {
     pdl_wait();
     pdl_trigger();
     constexpr int CW = kRecCols;
-    constexpr int kLanes = CW / 4;                       // lanes across the columns
-    constexpr int kGroups = kRecThreads / kLanes;        // groups of rows
-    constexpr int RPT = kD / kGroups;                    // rows a thread holds
+    constexpr int RPT = kD / kRecWarps;                  // rows a warp holds
     constexpr int kSplit = kD / CW;
-    __shared__ __align__(16) float red[2][kRecWarps][2][CW];     // partial sums of r and W^T q, two tokens' worth
+    static_assert(CW == 64, "two columns a lane");
+    __shared__ __align__(16) float red[2][2][kRecWarps][CW];     // partial sums of r and W^T q, two tokens' worth
     __shared__ __align__(16) float vec[kRecWarps][3][kD];        // eight tokens' k, q and exp(g)
     __shared__ float qks[kRecWarps], bts[kRecWarps];             // their q . k and beta
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cs = blockIdx.x % kSplit, h = (blockIdx.x / kSplit) % a.H, seq = blockIdx.x / (kSplit * a.H);
     int first, len, slot;
     if (!delta_seq(a, seq, &first, &len, &slot)) return;
-    const int cl = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-    const int col = cs * CW + 4 * cl, row0 = grp * RPT;
+    const int col = cs * CW + 2 * lane, row0 = warp * RPT;
     const size_t sbase = ((size_t)slot * a.H + h) * kD * kD + (size_t)row0 * kD + col;
 
-    float4 S[RPT];
+    uint64_t S[RPT / 2][2];                              // pairs of rows, two columns
 #pragma unroll
-    for (int j = 0; j < RPT; j++)
-        S[j] = a.state_in ? __ldcs(reinterpret_cast<const float4 *>(a.state_in + sbase + (size_t)j * kD))
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < RPT; j += 2) {
+        float2 x[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            x[i] = a.state_in ? __ldcs(reinterpret_cast<const float2 *>(a.state_in + sbase + (size_t)(j + i) * kD)) : make_float2(0.f, 0.f);
+        S[j / 2][0] = pack2(x[0].x, x[1].x);
+        S[j / 2][1] = pack2(x[0].y, x[1].y);
+    }
     const int hq = h / (a.H / a.Hq);
     // token i of the sequence, by this warp, into its place
     auto ready = [&](int i) {
@@ -121,9 +158,9 @@ __global__ void __launch_bounds__(kRecThreads, 3) delta_recurrent_kernel(const D
         }
     };
     auto value = [&](int i) {
-        return *reinterpret_cast<const uint2 *>(a.v + (size_t)(first + i) * a.v_stride + h * kD + col);
+        return *reinterpret_cast<const uint32_t *>(a.v + (size_t)(first + i) * a.v_stride + h * kD + col);
     };
-    uint2 vnext = make_uint2(0, 0);
+    uint32_t vnext = 0;
     if (len > 0) vnext = value(0);
     for (int i = 0; i < len; i++) {
         const int w8 = i & (kRecWarps - 1);
@@ -132,76 +169,64 @@ __global__ void __launch_bounds__(kRecThreads, 3) delta_recurrent_kernel(const D
             if (i + warp < len) ready(i + warp);
             __syncthreads();
         }
-        const float4 v = bf4(vnext);
+        const float v0 = __uint_as_float(vnext << 16), v1 = __uint_as_float(vnext & 0xFFFF0000u);
         if (i + 1 < len) vnext = value(i + 1);           // in flight under this token's work
         const float qk = qks[w8], beta = bts[w8];
-        float4 r = make_float4(0.f, 0.f, 0.f, 0.f), o = r;
+        uint64_t r0 = pack2(0.0f, 0.0f), r1 = r0, o0 = r0, o1 = r0;
 #pragma unroll
         for (int j4 = 0; j4 < RPT; j4 += 4) {
-            const float4 k4 = *reinterpret_cast<const float4 *>(&vec[w8][0][row0 + j4]);
-            const float4 q4 = *reinterpret_cast<const float4 *>(&vec[w8][1][row0 + j4]);
-            const float4 d4 = *reinterpret_cast<const float4 *>(&vec[w8][2][row0 + j4]);
-            const float kj[4] = {k4.x, k4.y, k4.z, k4.w}, qj[4] = {q4.x, q4.y, q4.z, q4.w},
-                        dj[4] = {d4.x, d4.y, d4.z, d4.w};
+            const ulonglong2 k4 = *reinterpret_cast<const ulonglong2 *>(&vec[w8][0][row0 + j4]);
+            const ulonglong2 q4 = *reinterpret_cast<const ulonglong2 *>(&vec[w8][1][row0 + j4]);
+            const ulonglong2 d4 = *reinterpret_cast<const ulonglong2 *>(&vec[w8][2][row0 + j4]);
+            const uint64_t kj[2] = {k4.x, k4.y}, qj[2] = {q4.x, q4.y}, dj[2] = {d4.x, d4.y};
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                float4 &s = S[j4 + j];
-                s.x *= dj[j]; s.y *= dj[j]; s.z *= dj[j]; s.w *= dj[j];
-                r.x = fmaf(kj[j], s.x, r.x); r.y = fmaf(kj[j], s.y, r.y);
-                r.z = fmaf(kj[j], s.z, r.z); r.w = fmaf(kj[j], s.w, r.w);
-                o.x = fmaf(qj[j], s.x, o.x); o.y = fmaf(qj[j], s.y, o.y);
-                o.z = fmaf(qj[j], s.z, o.z); o.w = fmaf(qj[j], s.w, o.w);
+            for (int j = 0; j < 2; j++) {
+                uint64_t &x = S[j4 / 2 + j][0], &y = S[j4 / 2 + j][1];
+                x = mul2(x, dj[j]);
+                y = mul2(y, dj[j]);
+                r0 = fma2(kj[j], x, r0);
+                r1 = fma2(kj[j], y, r1);
+                o0 = fma2(qj[j], x, o0);
+                o1 = fma2(qj[j], y, o1);
             }
         }
-        // over the warp's groups of rows, then over the warps (in warp order)
-#pragma unroll
-        for (int s = kLanes; s < 32; s <<= 1) {
-            r.x += __shfl_xor_sync(0xffffffffu, r.x, s); r.y += __shfl_xor_sync(0xffffffffu, r.y, s);
-            r.z += __shfl_xor_sync(0xffffffffu, r.z, s); r.w += __shfl_xor_sync(0xffffffffu, r.w, s);
-            o.x += __shfl_xor_sync(0xffffffffu, o.x, s); o.y += __shfl_xor_sync(0xffffffffu, o.y, s);
-            o.z += __shfl_xor_sync(0xffffffffu, o.z, s); o.w += __shfl_xor_sync(0xffffffffu, o.w, s);
-        }
-        float (*rd)[2][CW] = red[i & 1];                 // the other buffer is still being read
-        if (lane < kLanes) {
-            *reinterpret_cast<float4 *>(&rd[warp][0][4 * cl]) = r;
-            *reinterpret_cast<float4 *>(&rd[warp][1][4 * cl]) = o;
+        // over the warps, in warp order
+        float (*rd)[kRecWarps][CW] = red[i & 1];         // the other buffer is still being read
+        {
+            const float2 a0 = unpack2(r0), a1 = unpack2(r1), b0 = unpack2(o0), b1 = unpack2(o1);
+            *reinterpret_cast<float2 *>(&rd[0][warp][2 * lane]) = make_float2(a0.x + a0.y, a1.x + a1.y);
+            *reinterpret_cast<float2 *>(&rd[1][warp][2 * lane]) = make_float2(b0.x + b0.y, b1.x + b1.y);
         }
         __syncthreads();
-        r = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto total = [&](int which) {
+            uint64_t x = *reinterpret_cast<const uint64_t *>(&rd[which][0][2 * lane]);
 #pragma unroll
-        for (int w = 0; w < kRecWarps; w++) {
-            const float4 p = *reinterpret_cast<const float4 *>(&rd[w][0][4 * cl]);
-            r.x += p.x; r.y += p.y; r.z += p.z; r.w += p.w;
-        }
-        const float4 u = make_float4(beta * (v.x - r.x), beta * (v.y - r.y), beta * (v.z - r.z), beta * (v.w - r.w));
+            for (int w = 1; w < kRecWarps; w++) x = add2(x, *reinterpret_cast<const uint64_t *>(&rd[which][w][2 * lane]));
+            return unpack2(x);
+        };
+        const float2 r = total(0);
+        const float u0 = beta * (v0 - r.x), u1 = beta * (v1 - r.y);
+        const uint64_t uu0 = pack2(u0, u0), uu1 = pack2(u1, u1);
 #pragma unroll
         for (int j4 = 0; j4 < RPT; j4 += 4) {
-            const float4 k4 = *reinterpret_cast<const float4 *>(&vec[w8][0][row0 + j4]);
-            const float kj[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                float4 &s = S[j4 + j];
-                s.x = fmaf(kj[j], u.x, s.x); s.y = fmaf(kj[j], u.y, s.y);
-                s.z = fmaf(kj[j], u.z, s.z); s.w = fmaf(kj[j], u.w, s.w);
-            }
+            const ulonglong2 k4 = *reinterpret_cast<const ulonglong2 *>(&vec[w8][0][row0 + j4]);
+            S[j4 / 2][0] = fma2(k4.x, uu0, S[j4 / 2][0]);
+            S[j4 / 2][1] = fma2(k4.x, uu1, S[j4 / 2][1]);
+            S[j4 / 2 + 1][0] = fma2(k4.y, uu0, S[j4 / 2 + 1][0]);
+            S[j4 / 2 + 1][1] = fma2(k4.y, uu1, S[j4 / 2 + 1][1]);
         }
-        if (grp == 0) {
-            o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kRecWarps; w++) {
-                const float4 p = *reinterpret_cast<const float4 *>(&rd[w][1][4 * cl]);
-                o.x += p.x; o.y += p.y; o.z += p.z; o.w += p.w;
-            }
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(fmaf(qk, u.x, o.x), fmaf(qk, u.y, o.y));
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(fmaf(qk, u.z, o.z), fmaf(qk, u.w, o.w));
-            uint2 st;
-            st.x = *reinterpret_cast<const uint32_t *>(&lo);
-            st.y = *reinterpret_cast<const uint32_t *>(&hi);
-            *reinterpret_cast<uint2 *>(a.out + ((size_t)(first + i) * a.H + h) * kD + col) = st;
+        if (warp == (i & (kRecWarps - 1))) {             // a warp in turn
+            const float2 o = total(1);
+            const __nv_bfloat162 x = __floats2bfloat162_rn(fmaf(qk, u0, o.x), fmaf(qk, u1, o.y));
+            *reinterpret_cast<__nv_bfloat162 *>(a.out + ((size_t)(first + i) * a.H + h) * kD + col) = x;
         }
     }
 #pragma unroll
-    for (int j = 0; j < RPT; j++) __stcs(reinterpret_cast<float4 *>(a.state_out + sbase + (size_t)j * kD), S[j]);
+    for (int j = 0; j < RPT; j += 2) {
+        const float2 x = unpack2(S[j / 2][0]), y = unpack2(S[j / 2][1]);
+        __stcs(reinterpret_cast<float2 *>(a.state_out + sbase + (size_t)j * kD), make_float2(x.x, y.x));
+        __stcs(reinterpret_cast<float2 *>(a.state_out + sbase + (size_t)(j + 1) * kD), make_float2(x.y, y.y));
+    }
 }
 
 // ---------------------------------------------------------------- chunks of 64 tokens
@@ -247,37 +272,6 @@ __device__ __forceinline__ float exp2_fast(float x)          // within 2 ulp
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-// Two floats side by side, for the instructions that work on both.
-__device__ __forceinline__ uint64_t pack2(float x, float y)
-{
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
-    return p;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t p)
-{
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
 }
 // The two bf16 of a word.
 __device__ __forceinline__ uint64_t pair_bf16(uint32_t w)
@@ -1393,11 +1387,11 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
 }
 
 // From this many tokens a sequence on average, chunks; `alone` where the recurrent kernel's
-// blocks have an SM each.  Recurrent against chunks, us, per head: 64 sequences x 32 heads of 12
-// tokens 147, 175 and of 16 187, 177; 8 x 32 heads of 12 25, 25; alone (one sequence, 56
-// heads) of 16 11.7, 13.9 and of 24 16.2, 13.9.  Per channel: 37 x 56 heads of 20 tokens 244,
-// 263 and of 24 286, 264; alone of 24 16.1, 20.7 and of 32 20.7, 20.8.
-constexpr int chunk_tokens_avg(bool channel, bool alone) { return channel ? (alone ? 32 : 22) : (alone ? 20 : 15); }
+// blocks have an SM each.  Recurrent against chunks, us, per head: 64 sequences x 32 heads of 16
+// tokens 153, 176 and of 20 189, 178; 8 x 32 heads of 16 25, 25; alone (one sequence, 56
+// heads) of 20 13.1, 13.8 and of 24 14.8, 13.8.  Per channel: 37 x 56 heads of 26 tokens 252,
+// 265 and of 32 302, 270; alone of 32 18.0, 20.7 and of 40 22.5, 20.9.
+constexpr int chunk_tokens_avg(bool channel, bool alone) { return channel ? (alone ? 37 : 28) : (alone ? 23 : 18); }
 
 // Where the chains leave SMs free, the sequences are walked in stretches (one sequence of 8192
 // tokens x 56 heads: 546 us in one, 452 in four; per channel 875 and 687): while the chains go
