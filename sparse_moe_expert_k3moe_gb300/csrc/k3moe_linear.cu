@@ -96,6 +96,10 @@ __device__ __forceinline__ void lin_put(const LinearArgs &a, int t, int n, float
 // chunk order and then over the warp by a fixed butterfly.
 constexpr int kLrThreads = 256, kLrWarps = kLrThreads / 32, kLrDeep = 8;
 constexpr size_t kLrSmem = 200 * 1024;
+// Weights up to which three and four tokens go this way; one and two always do.  This kernel
+// against the tensor cores, us: four tokens, K 2048, N 2048 6.1, 11.7, N 4096 9.1, 9.2; K = N =
+// 4096 14.2, 10.9; two tokens there 8.8, 10.9 and K 7168, N 3584 13.4, 13.5; one 11.4, 13.6.
+constexpr long long kLrFour = 8 << 20;
 
 template <int NT>
 __global__ void __launch_bounds__(kLrThreads) linear_rows_kernel(const LinearArgs a)
@@ -582,12 +586,46 @@ cudaError_t launch_rows(const LinearArgs &a, cudaStream_t s)
     return launch_pdl(linear_rows_kernel<NT>, dim3(grid), dim3(kLrThreads), smem, s, a);
 }
 
-// The tile of a call: a pair of blocks (256 x 256) when the pairs have tiles for most of
-// the GPU; else the token tile, the K parts and the blocks an SM whose estimated time is
-// least.  The estimate, in SM clocks: a block's K stage takes its products' time on the tensor
-// cores (2 a token of 128 rows) or its bytes' at kLtRate from the L2, shared by the blocks of
-// an SM; a tile's start and epilogue about 2500 + 16 bn; a cluster's launch and joining 8000.
+// The tile of a call: the token tile, the K parts and the blocks an SM whose estimated time is
+// least, or a pair of blocks (256 x 256) where that is estimated faster still.  The
+// estimate, in SM clocks: a block's K stage takes its products' time on the tensor cores (2 a token
+// of 128 rows) or its bytes' at kLtRate from the L2, shared by the blocks of an SM; a tile's
+// start and epilogue about 2500 + 16 bn; a cluster's launch and joining 8000.  Single blocks in
+// full waves load a third faster than that, so pairs have to be 1.3 times ahead.  Single
+// against pairs, us: T 512, K = N = 7168 52, 41; T 600 52, 71; T 1024 81, 72; T 4096 256, 215; T
+// 1024, K 3584, N 3584 24.8, 25.6, N 4096 27.0, 25.5, N 5120 33, 40; T 300, K 1024, N 4096 8.6, 13.8.
 constexpr double kLtRate = 48.0;      // bytes a clock an SM
+
+template <int CG> cudaError_t allow_tc()
+{
+    static const cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kLtRing);
+    return e;
+}
+
+// Blocks at work at once in clusters of P: a cluster stays within a group of SMs, so that
+// fewer fit than the SMs would hold (P = 8: 15 clusters where 152 SMs have room for 19; 8 x 2048 x
+// 2048 in 16 of them took 10.9 us, in two goes, and in 16 of P = 6 6.2).
+int lin_slots(int P)
+{
+    static int known[9];
+    int &n = known[P];
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(num_sms() / P * P));
+        cfg.blockDim = dim3(kLtThreads);
+        cfg.dynamicSmemBytes = 1024 + kLtRing;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)P;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int fit = 0;
+        if (P > 1 && (allow_tc<1>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&fit, linear_tc_kernel<1>, &cfg) != cudaSuccess)) fit = 0;
+        n = (fit > 0 ? fit : num_sms() / P) * P;
+    }
+    return n;
+}
 
 int lin_plan(const LinearArgs &a, LinTile *tl)
 {
@@ -598,15 +636,6 @@ int lin_plan(const LinearArgs &a, LinTile *tl)
     tl->acc = 256;
     tl->cols = 512;
     tl->group = 8;
-    const long long pairs = (long long)((a.N + 255) / 256) * ((a.T + 255) / 256);
-    if (pairs * 4 >= 3LL * (sms / 2)) {
-        tl->bn = 256;
-        tl->n_rb = (a.N + 255) / 256;
-        tl->n_tt = (a.T + 255) / 256;
-        tl->stage_bytes = 2 * kLtABytes;
-        tl->nstg = kLtRing / tl->stage_bytes;
-        return 2;
-    }
     tl->n_rb = (a.N + 127) / 128;
     double best = 1e30;
     for (int n_tt = (a.T + 255) / 256; n_tt <= 64; n_tt++) {
@@ -615,9 +644,9 @@ int lin_plan(const LinearArgs &a, LinTile *tl)
         for (int P = 1; P <= 8; P++) {
             if (P > 1 && tl->nks / P < 4) break;
             for (int per_sm = 1; per_sm <= (bn <= 128 ? 2 : 1); per_sm++) {
-                const long long items = (long long)tl->n_rb * n_tt * P, slots = (long long)sms * per_sm;
-                const long long waves = (items + slots - 1) / slots;
-                const double load = (128.0 + bn) * 128.0 / kLtRate * (items > sms ? per_sm : 1);
+                const long long items = (long long)tl->n_rb * n_tt * P, slots = lin_slots(P);
+                const long long waves = (items + slots * per_sm - 1) / (slots * per_sm);
+                const double load = (128.0 + bn) * 128.0 / kLtRate * (items > slots ? per_sm : 1);
                 const double t = waves * ((double)((tl->nks + P - 1) / P) * std::max(2.0 * bn, load) + 2500.0 + 16.0 * bn / P +
                                           (P > 1 ? 8000.0 + 16.0 * bn : 0.0));
                 if (t < best) {
@@ -629,6 +658,19 @@ int lin_plan(const LinearArgs &a, LinTile *tl)
                 }
             }
         }
+    }
+    const long long pairs = (long long)((a.N + 255) / 256) * ((a.T + 255) / 256), waves = (pairs + sms / 2 - 1) / (sms / 2);
+    const double paired = waves * tl->nks * std::max(512.0, 2.0 * kLtABytes / kLtRate) + 2500.0 + 16.0 * 256;
+    if (best > 1.3 * paired) {
+        tl->P = tl->per_sm = 1;
+        tl->bn = 256;
+        tl->acc = 256;
+        tl->cols = 512;
+        tl->n_rb = (a.N + 255) / 256;
+        tl->n_tt = (a.T + 255) / 256;
+        tl->stage_bytes = 2 * kLtABytes;
+        tl->nstg = kLtRing / tl->stage_bytes;
+        return 2;
     }
     tl->acc = tl->bn <= 32 ? 32 : tl->bn <= 64 ? 64 : tl->bn <= 128 ? 128 : 256;
     tl->cols = tl->P > 1 ? tl->acc : 2 * tl->acc;
@@ -645,11 +687,7 @@ cudaError_t launch_tc(const LinearArgs &a, const LinTile &tl, cudaStream_t s)
         !map16s(&mx, a.x, (uint64_t)a.T, (uint64_t)a.K, (uint64_t)a.x_stride, (uint32_t)(tl.bn / CG)))
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + (tl.per_sm == 2 ? kLtRing2 : kLtRing);
-    static bool smem_set = false;
-    if (!smem_set) {
-        cudaFuncSetAttribute(linear_tc_kernel<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kLtRing);
-        smem_set = true;
-    }
+    if (allow_tc<CG>() != cudaSuccess) return cudaErrorInvalidConfiguration;
     const int csize = CG == 2 ? 2 : tl.P;
     const int items = tl.n_rb * tl.n_tt;
     cudaLaunchConfig_t cfg = {};
@@ -679,7 +717,7 @@ cudaError_t launch_linear(const LinearArgs &a, cudaStream_t s)
         err = launch_rows<1>(a, s);
     } else if (a.T <= 2 && (size_t)a.K * 4 <= kLrSmem) {
         err = launch_rows<2>(a, s);
-    } else if (a.T <= 4 && (size_t)a.K * 8 <= kLrSmem) {
+    } else if (a.T <= 4 && (size_t)a.K * 8 <= kLrSmem && (long long)a.N * a.K <= kLrFour) {
         err = launch_rows<4>(a, s);
     } else {
         LinTile tl{};

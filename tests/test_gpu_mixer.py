@@ -94,10 +94,17 @@ LINEAR = [  # T, N, K, act, bias, residual, f32, x pad, y pad
     (2048, 2048, 2048, "gelu", True, True, False, 0, 0),
     (4097, 1, 64, "sigmoid", True, False, True, 0, 0),
     (5000, 260, 136, "none", True, True, True, 8, 4),
-    (4100, 1300, 520, "silu", True, True, False, 0, 0),      # two pairs of blocks a cluster, ragged both ways
+    (4100, 1300, 520, "silu", True, True, False, 0, 0),      # several waves of tiles, ragged both ways
     (3001, 1537, 1096, "none", False, True, True, 8, 1),
-    (19969, 200, 136, "gelu", True, False, False, 0, 0),     # one pair a cluster
+    (19969, 200, 136, "gelu", True, False, False, 0, 0),
     (640, 6500, 264, "relu", True, True, False, 0, 0),
+    (500, 9001, 2000, "none", True, True, True, 8, 3),       # pairs of blocks, ragged both ways
+    (501, 9000, 2000, "gelu", True, True, False, 0, 0),
+    (2047, 7169, 2048, "silu", True, False, False, 0, 1),    # and tile after tile
+    (3, 2100, 4096, "silu", True, True, False, 0, 0),        # a few tokens, weights on either side of the rule
+    (4, 2000, 4096, "silu", True, True, False, 0, 0),
+    (9, 2000, 2048, "none", True, False, True, 0, 0),        # a cluster of six, eight
+    (10, 1800, 8192, "none", True, True, False, 0, 0),
 ]
 
 
