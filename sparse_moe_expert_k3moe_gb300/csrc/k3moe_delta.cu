@@ -444,6 +444,10 @@ __device__ __forceinline__ void invert64(float *A, int warp, int lane)
 // while no |G_t - m| passes 60 (a factor of 1e26 either way; a token's mean decay of 1e-2
 // over 16 tokens would reach it).  Where one does, the chunk's products are summed one by
 // one, the weight's logarithm accumulated backwards from t: slower, but exact for any decay.
+//
+// What bounds it: its barriers and instructions (half of the issue slots, a tenth of the tensor
+// cores, a quarter of the DRAM).  8192 tokens of eight sequences of 56 heads: 129 us, per channel 255;
+// blocks of 256 threads, four an SM (64 registers), per channel three (operands of two terms, 56 KB).
 constexpr int kPpA = 128 * 128;                               // an operand's term, 64 channels: 128 rows
 constexpr int kPpB = 96 * 128;                                // and 96 rows
 constexpr float kPpRange = 60.0f * kLog2e;
@@ -864,6 +868,10 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
 // The chain's eight warps keep 64 floats of the state a thread, in tensor memory: in
 // registers they made the other roles spill, and the spills' way through the L2 made a chunk
 // three times as long.  Sixteen warps with 32 each took as long a phase: they share four schedulers.
+// What bounds it: the steps follow from one another, 3.3 us a chunk and 4.7 per channel with the
+// tensor cores busy a quarter of it; the loops over the terms stay rolled, as straight code misses
+// the instruction cache every chunk (eight sequences of 1024 tokens x 56 heads: 186 -> 178 us, per
+// channel 287 -> 263).  One sequence of 8192 tokens takes 419 us, per channel 615.
 constexpr int kChChain = 8, kChOut = 4, kChMake = 8;
 constexpr int kChPartK = kD / (kChChain / 4), kChPartT = kC / (kChChain / 4);     // channels and tokens of a chain warp
 constexpr int kChStagesHead = 3, kChStagesChannel = 2;
@@ -886,7 +894,7 @@ template <bool kChannel> struct ChunkShape {
 constexpr int kChWarpOut = kChChain, kChWarpMake = kChWarpOut + kChOut;
 // Registers a thread per channel: 80 at launch (768 threads), shares moved between the
 // warpgroups so that no role spills in a chunk's way.
-constexpr int kChRegs = 80, kChRegsChain = 96, kChRegsOut = 88, kChRegsMake = 80, kChRegsLast = 40;
+constexpr int kChRegs = 80, kChRegsChain = 88, kChRegsOut = 88, kChRegsMake = 80, kChRegsLast = 56;
 static_assert(kChRegsChain >= kChRegs && kChRegsOut >= kChRegs && kChRegsMake <= kChRegs && kChRegsLast <= kChRegs,
               "inc only from below, dec only from above");
 static_assert(2 * kChRegsChain + kChRegsOut + 2 * kChRegsMake + kChRegsLast <= 6 * kChRegs, "shares within the launch's");
@@ -899,7 +907,9 @@ constexpr uint32_t kTmOp = 256;   // P U
 constexpr uint32_t kTmRU = 320;   // R, then U (per head: weighted for the state), as an operand [half of t][hi, mid][16]
 constexpr uint32_t kTmF = 384;    // the state, float [128]
 
-constexpr int kRankSeqs = 256;                                // up to this many sequences are taken by length
+// Up to this many sequences are taken by length (every block ranks them): 8 sequences of 50 to 2000
+// tokens x 56 heads take 211 us by length and 238 as given, 40 x 32 heads 503 and 504, 250 1060 and 932.
+constexpr int kRankSeqs = 32;
 struct ChunkShared {
     uint64_t in_full[3], in_free[3];
     uint64_t s_ready, d1_full, q_done, r_ready, d2_full, u_ready, d4_full, o_full, o_free, made, drain;
@@ -907,6 +917,7 @@ struct ChunkShared {
     volatile int bail;
     alignas(16) float dec[2][kD];                             // per channel: exp(G_C), by chunk parity
     int seq, len[kRankSeqs];
+    int first, tokens, slot, head, record;                    // the block's stretch, for the roles
 };
 
 // Unswizzled K-major descriptors of T and P blocks: 8-row groups 256 bytes apart, their two
@@ -955,15 +966,20 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                 a.state_in ? reinterpret_cast<const float4 *>(a.state_in + sbase)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
         return;
     }
-    // chunk c's record; this launch's stretch stands for the sequence from here on
-    const uint8_t *rec0 = a.ws + kCtrOffset + kCtrBytes + ((size_t)(first / kC + seq + a.chunk0) * a.H + h) * kRecBytes;
+    // this launch's stretch stands for the sequence from here on; the roles read it from shared
+    // memory, as what they held in common would be kept in the registers of all
     if (a.chunk0 >= (len + kC - 1) / kC) return;
-    first += kC * a.chunk0;
-    len -= kC * a.chunk0;
-    if (a.chunk1 < kAllChunks) len = min(len, kC * (a.chunk1 - a.chunk0));
-    const int hq = h / (a.H / a.Hq), nc = (len + kC - 1) / kC;
-    int32_t *status = reinterpret_cast<int32_t *>(a.ws);
-    auto record = [&](int c) { return rec0 + (size_t)c * a.H * kRecBytes; };
+    if (threadIdx.x == 0) {
+        sh.first = first + kC * a.chunk0;
+        sh.tokens = a.chunk1 < kAllChunks ? min(len - kC * a.chunk0, kC * (a.chunk1 - a.chunk0)) : len - kC * a.chunk0;
+        sh.slot = slot;
+        sh.head = h;
+        sh.record = first / kC + seq + a.chunk0;
+    }
+    auto own = [](const int &x) { return *const_cast<const volatile int *>(&x); };
+    auto record = [&](int c) {                                // chunk c's
+        return a.ws + kCtrOffset + kCtrBytes + ((size_t)(own(sh.record) + c) * a.H + own(sh.head)) * kRecBytes;
+    };
     auto stage = [&](int c) { return ring + (size_t)(c % kStages) * Shape::stage; };
 
     if (threadIdx.x == 0) {
@@ -995,7 +1011,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
     auto wait = [&](uint64_t &b, int phase) {
         const bool ok = mb_wait_asleep(&b, (uint32_t)phase & 1u);
         if (!ok) {
-            set_status(status, K3MOE_DEV_TIMEOUT);
+            set_status(reinterpret_cast<int32_t *>(a.ws), K3MOE_DEV_TIMEOUT);
             sh.bail = 1;
         }
         return (bool)__all_sync(0xffffffffu, ok && !sh.bail);
@@ -1019,6 +1035,8 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
     if (warp < kChChain) {
         // ---------------- the chain: value column v, half of the channels or tokens
         const int q = warp & 3, part = warp >> 2, v = 32 * q + lane, t0 = kChPartT * part;
+        const int len = own(sh.tokens), nc = (len + kC - 1) / kC;
+        auto state_at = [&]() { return ((size_t)own(sh.slot) * a.H + own(sh.head)) * kD * kD + (size_t)(kChPartK * part) * kD + v; };
         const uint32_t la = tmem + ((uint32_t)(32 * q) << 16);
         const uint32_t la_s = la + kTmS + kChPartK * part;
         const uint32_t la_f = la + kTmF + kChPartK * part;
@@ -1035,7 +1053,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         };
         {
             const float *in = a.chunk0 > 0 ? a.state_out : a.state_in;
-            const float *from = in ? in + sbase + (size_t)(kChPartK * part) * kD + v : nullptr;
+            const float *from = in ? in + state_at() : nullptr;
 #pragma unroll
             for (int b = 0; b < kChPartK; b += 32) {
                 float x[32];
@@ -1149,8 +1167,9 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                 if (c + 1 < nc) {
                     put_terms32(b, x);
                 } else if (!sh.bail) {
+                    float *to = a.state_out + state_at() + (size_t)b * kD;
 #pragma unroll
-                    for (int j = 0; j < 32; j++) a.state_out[sbase + (size_t)(kChPartK * part + b + j) * kD + v] = x[j];
+                    for (int j = 0; j < 32; j++) to[(size_t)j * kD] = x[j];
                 }
             }
             if (c + 1 < nc) {
@@ -1162,6 +1181,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         // ---------------- O: value column v, every token of the chunk
         const int q = warp & 3, v = 32 * q + lane;
         const uint32_t la = tmem + ((uint32_t)(32 * q) << 16);
+        const int len = own(sh.tokens), nc = (len + kC - 1) / kC;
         for (int c = 0; c < nc; c++) {
             const int n = min(kC, len - kC * c);
             const float *sc = reinterpret_cast<const float *>(stage(c) + kOffTp + kTpBytes);
@@ -1186,7 +1206,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             if (lane == 0) mb_arrive(&sh.in_free[c % kStages]);
             // neighbouring lanes trade a token each: two columns of one token a store
             const int mine = lane & 1;
-            uint32_t *o = reinterpret_cast<uint32_t *>(a.out + ((size_t)(first + kC * c + mine) * a.H + h) * kD + (v & ~1));
+            uint32_t *o = reinterpret_cast<uint32_t *>(a.out + ((size_t)(own(sh.first) + kC * c + mine) * a.H + own(sh.head)) * kD + (v & ~1));
             const size_t step = (size_t)a.H * kD;             // words of two tokens
 #pragma unroll
             for (int j = 0; j < kC / 2; j++, o += step) {
@@ -1199,6 +1219,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         // ---------------- per channel: the weighted operands of chunk c, two channels and twice
         // 8 tokens a thread
         const int id = threadIdx.x - kChWarpMake * 32, pair = id & 63, ch = 2 * pair;
+        const int len = own(sh.tokens), nc = (len + kC - 1) / kC, first = own(sh.first), h = own(sh.head), hq = h / (a.H / a.Hq);
         for (int c = 0; c < nc; c++) {
             const int n = min(kC, len - kC * c);
             const size_t tok0 = (size_t)(first + kC * c);
@@ -1309,7 +1330,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                                  term > 0 || j > 0);
         };
         // the count and the stages' place as uniform values, so that descriptors are too
-        const int chunks = (int)__reduce_max_sync(0xffffffffu, (unsigned)nc);
+        const int chunks = (int)__reduce_max_sync(0xffffffffu, (unsigned)(own(sh.tokens) + kC - 1) / kC);
         int slot_st = 0;
         for (int c = 0; c < chunks; c++, slot_st = slot_st + 1 == kStages ? 0 : slot_st + 1) {
             if (!wait(sh.in_full[c % kStages], c / kStages) || (kChannel && !wait(sh.made, c)) || !wait(sh.s_ready, c)) break;
@@ -1347,6 +1368,7 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
         mb_wait_warp(&sh.drain, 0);
     } else if (warp == kWarpLoad) {
         // ---------------- loads
+        const int len = own(sh.tokens), nc = (len + kC - 1) / kC, first = own(sh.first), h = own(sh.head), hq = h / (a.H / a.Hq);
         auto load = [&](int c) {
             uint8_t *p = stage(c);
             uint64_t *bar = &sh.in_full[c % kStages];
