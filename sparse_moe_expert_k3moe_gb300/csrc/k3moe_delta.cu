@@ -385,8 +385,8 @@ __device__ __forceinline__ void block_product(float *D, float sign, const float 
 __device__ __forceinline__ void four_warps() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ void invert32(float *A, int w, int lane)
 {
-    {   // column `lane` of diagonal block w (lanes from 16 on repeat the others' work)
-        float *a = A + (16 * w) * (kChLd + 1);
+    if (w < 2) {   // a lane a column of one of two diagonal blocks
+        float *a = A + 16 * (2 * w + (lane >> 4)) * (kChLd + 1);
         float x[16];
         const int col = lane & 15;
 #pragma unroll
@@ -402,9 +402,8 @@ __device__ __forceinline__ void invert32(float *A, int w, int lane)
             x[t] = (p[0] + p[1]) + (p[2] + p[3]);
         }
         __syncwarp();
-        if (lane < 16)
 #pragma unroll
-            for (int t = 0; t < 16; t++) a[t * kChLd + col] = x[t];       // zero above the diagonal
+        for (int t = 0; t < 16; t++) a[t * kChLd + col] = x[t];       // zero above the diagonal
     }
     four_warps();
     {   // 16 -> 32: two pairs of blocks, two tiles of 16 x 8 each
@@ -430,12 +429,14 @@ __device__ __forceinline__ void invert64(float *A, int warp, int lane)
 }
 
 // ---------------------------------------------------------------- T and P
-// One block a chunk and head.  With the rows of K over those of Q as the 128 rows of a
+// A block one chunk and head at a time.  With the rows of K over those of Q as the 128 rows of a
 // tensor-core tile, one product against K's rows gives A's and P's dot products.
 //
 // Decay per head: K and Q go in as they are and the float dot products are weighted after,
 // with G as a pair of floats (a sum, and what it lost), so that differences of G hold
-// however strong an earlier decay was.
+// however strong an earlier decay was.  The product goes against all 128 rows, whose
+// diagonal is the squared norms.  Blocks stay, four an SM, and load their next chunk under this
+// one's weighing and inversion.
 //
 // Decay per channel: the weights are inside the products.  In each 32-token half b, with m
 // its G in the middle (after 16 tokens), rows are x_t exp(G_t - m), columns k_i exp(m - G_i),
@@ -446,25 +447,30 @@ __device__ __forceinline__ void invert64(float *A, int warp, int lane)
 // one, the weight's logarithm accumulated backwards from t: slower, but exact for any decay.
 //
 // What bounds it: its barriers and instructions (half of the issue slots, a tenth of the tensor
-// cores, a quarter of the DRAM).  8192 tokens of eight sequences of 56 heads: 129 us, per channel 255;
-// blocks of 256 threads, four an SM (64 registers), per channel three (operands of two terms, 56 KB).
+// cores, a quarter of the DRAM).  8192 tokens of eight sequences of 56 heads: 108 us (a block a
+// chunk 129; norms from the rows instead of the diagonal 121), per channel 261, a block a chunk, three
+// an SM (80 registers, operands of two terms; blocks that stay 264: their loads have nowhere to wait).
 constexpr int kPpA = 128 * 128;                               // an operand's term, 64 channels: 128 rows
 constexpr int kPpB = 96 * 128;                                // and 96 rows
 constexpr float kPpRange = 60.0f * kLog2e;
-constexpr size_t pp_smem(bool channel) { return 1024 + (channel ? 2 * kPpA + 2 * kPpB : 2 * kPpA); }
+constexpr int kPpScratch = kC * kChLd * 4;                    // per channel over the operands, once they are used
+constexpr size_t pp_smem(bool channel) { return 1024 + (channel ? 2 * kPpA + 2 * kPpB : 2 * kPpA + kPpScratch); }
+template <bool kChannel> constexpr int kPpBlocks = kChannel ? 3 : 4;           // of them an SM
 
-struct PrepShared {
+template <bool kChannel> struct PrepShared {
     uint64_t full, done;
     uint32_t tmem;
-    int seq, far, bad;
+    int far, bad;
+    struct { int rec, tok0, n, head; } unit[2];               // this turn's chunk and the next; n = 0: none
+    alignas(16) float gin[kC], bin[kC];                       // the next one's decays (per head) and steps
     alignas(16) float gh[kC], gl[kC], rk[kC], kb[kC], qn[kC], beta[kC];
-    alignas(16) float sum[8][kD];                             // log2 decays summed over each 8 tokens
+    alignas(16) float sum[8][kChannel ? kD : 2];              // log2 decays summed over each 8 tokens
 };
 
-// The record, first token and length of chunk `unit`, false when there is none.  All chunks at
-// once (the call's only stretch): units are records.  A stretch: units are its chunks of
-// each sequence in turn.
-__device__ __forceinline__ bool find_chunk(const DeltaArgs &a, int unit, int *found, int *rec, int *tok0, int *n)
+// The record, first token and length of chunk `unit`, false when there is none; by a whole
+// warp.  All chunks at once (the call's only stretch): units are records.  A stretch: units
+// are its chunks of each sequence in turn.
+__device__ __forceinline__ bool find_chunk(const DeltaArgs &a, int unit, int lane, int *rec, int *tok0, int *n)
 {
     auto range = [&](int s, int *s0, int *len) {
         *s0 = a.seq_start ? a.seq_start[s] : 0;
@@ -472,25 +478,21 @@ __device__ __forceinline__ bool find_chunk(const DeltaArgs &a, int unit, int *fo
         *len = s1 - *s0;
         return *s0 >= 0 && s1 >= *s0 && s1 <= a.T;
     };
-    auto holds = [&](int s, int *s0, int *len) {
-        return range(s, s0, len) && unit >= *s0 / kC + s && unit < *s0 / kC + s + (*len + kC - 1) / kC;
-    };
     int s0, len, s = 0, c;
     if (a.chunk1 < kAllChunks) {
         s = unit / (a.chunk1 - a.chunk0);
         c = a.chunk0 + unit % (a.chunk1 - a.chunk0);
         if (!range(s, &s0, &len) || kC * c >= len) return false;
     } else {
-        if (a.n_seq > 1) {
-            if (threadIdx.x == 0) *found = 0x7fffffff;
-            __syncthreads();
-            for (int i = threadIdx.x; i < a.n_seq; i += kPpThreads)
-                if (holds(i, &s0, &len)) atomicMin(found, i);
-            __syncthreads();
-            s = *found;
-            if (s == 0x7fffffff) return false;
+        unsigned held = 0;
+        for (int b = 0; b < a.n_seq && !held; b += 32) {
+            const int i = b + lane;
+            const bool holds = i < a.n_seq && range(i, &s0, &len) && unit >= s0 / kC + i && unit < s0 / kC + i + (len + kC - 1) / kC;
+            held = __ballot_sync(0xffffffffu, holds);
+            s = b + __ffs(held) - 1;
         }
-        if (!holds(s, &s0, &len)) return false;
+        if (!held) return false;
+        range(s, &s0, &len);
         c = unit - (s0 / kC + s);
     }
     *rec = s0 / kC + s + c;
@@ -500,7 +502,7 @@ __device__ __forceinline__ bool find_chunk(const DeltaArgs &a, int unit, int *fo
 }
 
 template <bool kChannel>
-__global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
+__global__ void __launch_bounds__(kPpThreads, kPpBlocks<kChannel>)
     delta_prepare_kernel(const DeltaArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk)
 {
     // A later stretch is prepared beside the chain of the one before, launched when all of that
@@ -509,32 +511,23 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
     pdl_trigger();
     extern __shared__ __align__(1024) uint8_t psm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(psm_raw) + 1023) & ~(uintptr_t)1023);
-    float *As = reinterpret_cast<float *>(sm);                // over the operands, once they are used
-    __shared__ PrepShared sh;
+    float *As = reinterpret_cast<float *>(sm + (kChannel ? 0 : 2 * kPpA));
+    __shared__ PrepShared<kChannel> sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % a.H, hq = h / (a.H / a.Hq);
-    int rec, tok0, n;
-    if (!find_chunk(a, blockIdx.x / a.H, &sh.seq, &rec, &tok0, &n)) {
+    int32_t *status = reinterpret_cast<int32_t *>(a.ws);
+    constexpr int kCols = 128;                                // tensor memory
+    int rec0 = 0, first0 = 0, n0 = 0;                         // per channel the block's only chunk
+    if (kChannel && !find_chunk(a, blockIdx.x / a.H, lane, &rec0, &first0, &n0)) {
         if (a.chunk0 > 0 && blockIdx.x == gridDim.x - 1) pdl_wait();
         return;
     }
-    int32_t *status = reinterpret_cast<int32_t *>(a.ws);
-    uint8_t *out = a.ws + kCtrOffset + kCtrBytes + ((size_t)rec * a.H + h) * kRecBytes;
-    float *outf = reinterpret_cast<float *>(out + kTpBytes);
-    constexpr int kCols = kChannel ? 128 : 64;                // tensor memory
+    if (kChannel && tid < kC) sh.beta[tid] = tid < n0 ? a.beta[(size_t)(first0 + tid) * a.H + blockIdx.x % a.H] : 0.0f;
     if (tid == 0) {
         mb_init(&sh.full, 1);
         mb_init(&sh.done, 1);
         sh.far = 0;
         sh.bad = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        if (!kChannel) {
-            mb_expect_tx(&sh.full, 2 * kPpA);
-            for (int b = 0; b < 2; b++) {
-                tma2d(sm + b * kPpA, &mk, hq * kD + 64 * b, tok0, &sh.full);
-                tma2d(sm + b * kPpA + kC * 128, &mq, hq * kD + 64 * b, tok0, &sh.full);
-            }
-        }
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sh.tmem)), "r"(kCols));
@@ -550,306 +543,371 @@ __global__ void __launch_bounds__(kPpThreads, kChannel ? 3 : 4)
         sh.bad = 1;
         return false;
     };
-    bool far = false;                                         // per channel: the weights reach too far
-
-    if (!kChannel) {
-        const int row = tid, t = row & (kC - 1);              // threads 0-63: K's rows, 64-127: Q's
-        if (warp < 4) {
-            // inclusive sums over the 64 tokens, two a lane, as sum + lost
-            float s[2], e[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < 2; i++)
-                s[i] = lane + 32 * i < n ? clamp_gate(a.g[(size_t)(tok0 + lane + 32 * i) * a.H + h]) : 0.0f;
-            auto add = [](float &x, float &ex, float y, float ey) {      // two-sum, then the lost parts
-                const float z = x + y, v = z - x;
-                ex = ((x - (z - v)) + (y - v)) + (ex + ey);
-                x = z;
-            };
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const float p = __shfl_up_sync(0xffffffffu, s[i], o), ep = __shfl_up_sync(0xffffffffu, e[i], o);
-                    if (lane >= o) add(s[i], e[i], p, ep);
-                }
-            add(s[1], e[1], __shfl_sync(0xffffffffu, s[0], 31), __shfl_sync(0xffffffffu, e[0], 31));
-            const float gc = __shfl_sync(0xffffffffu, s[1], 31), ec = __shfl_sync(0xffffffffu, e[1], 31);
-            const float G = (warp & 1) ? s[1] : s[0], E = (warp & 1) ? e[1] : e[0];
-            const bool ok = wait(sh.full, 0);
-            float norm = 1.0f;
-            if (a.qk_norm && ok) {
-                uint64_t s0 = pack2(0.0f, 0.0f), s1 = s0;
-#pragma unroll
-                for (int j = 0; j < 16; j++) {                // chunk order is the swizzle's: a sum does not mind
-                    const uint4 w = *reinterpret_cast<const uint4 *>(sm + (j >> 3) * kPpA + row * 128 + (((j & 7) ^ (row & 7)) << 4));
-                    const uint64_t x0 = pair_bf16(w.x), x1 = pair_bf16(w.y), x2 = pair_bf16(w.z), x3 = pair_bf16(w.w);
-                    s0 = fma2(x0, x0, s0);
-                    s1 = fma2(x1, x1, s1);
-                    s0 = fma2(x2, x2, s0);
-                    s1 = fma2(x3, x3, s1);
-                }
-                const float2 sum = unpack2(add2(s0, s1));
-                norm = 1.0f / sqrtf(sum.x + sum.y + a.eps);
-            }
-            const bool in = t < n;
-            const float eG = expf(G + E);
-            if (row < kC) {
-                const float b = in ? a.beta[(size_t)(tok0 + t) * a.H + h] : 0.0f;
-                sh.gh[t] = G;
-                sh.gl[t] = E;
-                sh.rk[t] = in ? norm : 0.0f;
-                sh.beta[t] = b;
-                sh.kb[t] = in ? b * norm : 0.0f;
-                outf[kRecKr + t] = in ? norm * eG : 0.0f;
-                outf[kRecKd + t] = in ? norm * expf((gc - G) + (ec - E)) : 0.0f;
-                if (t == 0) outf[kRecDec] = expf(gc + ec);
-            } else {
-                sh.qn[t] = in ? a.scale * norm : 0.0f;
-                outf[kRecQr + t] = in ? a.scale * norm * eG : 0.0f;
+    // Per head, by one warp, under the turn before: the block's turn-th chunk, its decays and steps
+    // and, into the operands' place, K and Q.
+    int at = blockIdx.x;
+    float bnext[2] = {}, gnext[2] = {};
+    auto next = [&](int turn) {
+        auto &unit = sh.unit[turn & 1];
+        int rec = 0, tok0 = 0, n = 0, head = 0;
+        for (; at < a.units; at += gridDim.x) {
+            head = at % a.H;
+            if (find_chunk(a, at / a.H, lane, &rec, &tok0, &n)) break;
+        }
+        const bool any = at < a.units;
+        at += gridDim.x;
+        if (lane == 0) {
+            unit.rec = rec;
+            unit.tok0 = tok0;
+            unit.n = any ? n : 0;
+            unit.head = head;
+        }
+        if (!any) return;
+        if (lane == 0) {
+            const int hq = head / (a.H / a.Hq);
+            mb_expect_tx(&sh.full, 2 * kPpA);
+            for (int b = 0; b < 2; b++) {
+                tma2d(sm + b * kPpA, &mk, hq * kD + 64 * b, tok0, &sh.full);
+                tma2d(sm + b * kPpA + kC * 128, &mq, hq * kD + 64 * b, tok0, &sh.full);
             }
         }
-        if (warp == 4 && wait(sh.full, 0)) {
-            const uint32_t d = desc_lo(saddr(sm));
 #pragma unroll
-            for (int s = 0; s < 8; s++) {
-                const uint32_t at = d + (((s >> 2) * kPpA + (s & 3) * 32) >> 4);
-                umma_warp(tmem, at, at, idesc(1, kC), s > 0);
-            }
-            umma_commit_warp(&sh.done);
+        for (int i = 0; i < 2; i++) {
+            const int t = lane + 32 * i;
+            const size_t tok = (size_t)(tok0 + min(t, n - 1)) * a.H + head;
+            bnext[i] = t < n ? a.beta[tok] : 0.0f;
+            gnext[i] = t < n ? a.g[tok] : 0.0f;
+        }
+    };
+    auto keep = [&]() {                                       // later: the loads are then there
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            sh.bin[lane + 32 * i] = bnext[i];
+            sh.gin[lane + 32 * i] = clamp_gate(gnext[i]);
+        }
+    };
+    constexpr int kWarpNext = 6;                              // idle while the others weigh
+    if (!kChannel) {
+        if (warp == kWarpNext) {
+            next(0);
+            keep();
         }
         __syncthreads();
-        if (!sh.bad) wait(sh.done, 0);
-    } else {
-        // a warp 8 tokens, a lane two of the 64 channels at hand
-        const int t0 = 8 * warp;
-        float nk[8] = {}, nq[8] = {}, reach = 0.0f;
-        if (tid < kC) sh.beta[tid] = tid < n ? a.beta[(size_t)(tok0 + tid) * a.H + h] : 0.0f;
-        for (int half = 0; half < 2; half++) {
-            const int ch = 64 * half + 2 * lane;
-            uint32_t k[8], q[8];
-            float2 g[8];
+    }
+    for (int turn = 0; turn < (kChannel ? 1 : 0x7fffffff); turn++) {
+        const int n = kChannel ? n0 : sh.unit[turn & 1].n;
+        if (n == 0) break;
+        const int rec = kChannel ? rec0 : sh.unit[turn & 1].rec, tok0 = kChannel ? first0 : sh.unit[turn & 1].tok0;
+        const int h = kChannel ? blockIdx.x % a.H : sh.unit[turn & 1].head, hq = h / (a.H / a.Hq);
+        uint8_t *out = a.ws + kCtrOffset + kCtrBytes + ((size_t)rec * a.H + h) * kRecBytes;
+        float *outf = reinterpret_cast<float *>(out + kTpBytes);
+        bool far = false;                                         // per channel: the weights reach too far
+
+        if (!kChannel) {
+            if (warp == 4 && wait(sh.full, turn & 1)) {
+                const uint32_t d = desc_lo(saddr(sm));
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const size_t tok = (size_t)tok0 + min(t0 + i, n - 1);
-                k[i] = *reinterpret_cast<const uint32_t *>(a.k + tok * a.k_stride + hq * kD + ch);
-                q[i] = *reinterpret_cast<const uint32_t *>(a.q + tok * a.q_stride + hq * kD + ch);
-                g[i] = *reinterpret_cast<const float2 *>(a.g + (tok * a.H + h) * kD + ch);
-            }
-            float2 L = make_float2(0.0f, 0.0f);               // sums over this warp's tokens so far, in log2
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const bool in = t0 + i < n;
-                L.x += in ? clamp_gate(g[i].x) * kLog2e : 0.0f;
-                L.y += in ? clamp_gate(g[i].y) * kLog2e : 0.0f;
-                g[i] = L;
-            }
-            *reinterpret_cast<float2 *>(&sh.sum[warp][ch]) = L;
-            *reinterpret_cast<float2 *>(&outf[kRecSum + warp * kD + ch]) = L;
-            if (half == 1) wait(sh.done, 0);                  // the first half's operands are used
-            __syncthreads();
-            if (sh.bad) break;
-            float2 s[8];
-#pragma unroll
-            for (int w = 0; w < 8; w++) s[w] = *reinterpret_cast<const float2 *>(&sh.sum[w][ch]);
-            // G at this warp's start less the middle of its 32 tokens; the second half's middle
-            // less the first half's end (both counted from their own half's start)
-            const int b = (warp >> 2) * 4;
-            float2 base = make_float2(0.f, 0.f);
-            float2 m1 = make_float2(s[4].x + s[5].x, s[4].y + s[5].y);
-            switch (warp & 3) {
-            case 0: base = make_float2(-(s[b].x + s[b + 1].x), -(s[b].y + s[b + 1].y)); break;
-            case 1: base = make_float2(-s[b + 1].x, -s[b + 1].y); break;
-            case 2: break;
-            default: base = make_float2(s[b + 2].x, s[b + 2].y); break;
-            }
-            // (first half only) the second's middle less G at this warp's start
-            float2 tail = m1;
-#pragma unroll
-            for (int w = 3; w >= 0; w--)
-                if (w >= warp) { tail.x += s[w].x; tail.y += s[w].y; }
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int t = t0 + i;
-                const uint64_t kk = pair_bf16(k[i]), qq = pair_bf16(q[i]);
-                const float2 kf = unpack2(kk), qf = unpack2(qq);
-                nk[i] = fmaf(kf.x, kf.x, fmaf(kf.y, kf.y, nk[i]));
-                nq[i] = fmaf(qf.x, qf.x, fmaf(qf.y, qf.y, nq[i]));
-                const float dx = base.x + g[i].x, dy = base.y + g[i].y;       // G_t - m
-                reach = max_nan(reach, max_nan(fabsf(dx), fabsf(dy)));
-                const uint64_t e = pack2(exp2_fast(dx), exp2_fast(dy));
-                const uint32_t at = t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
-                uint32_t hi, mid;
-                split2(mul2(kk, e), &hi, &mid);
-                *reinterpret_cast<uint32_t *>(sm + at) = hi;
-                *reinterpret_cast<uint32_t *>(sm + kPpA + at) = mid;
-                split2(mul2(qq, e), &hi, &mid);
-                *reinterpret_cast<uint32_t *>(sm + kC * 128 + at) = hi;
-                *reinterpret_cast<uint32_t *>(sm + kPpA + kC * 128 + at) = mid;
-                uint8_t *B = sm + 2 * kPpA;
-                split2(mul2(kk, pack2(exp2_fast(-dx), exp2_fast(-dy))), &hi, &mid);
-                *reinterpret_cast<uint32_t *>(B + at) = hi;
-                *reinterpret_cast<uint32_t *>(B + kPpB + at) = mid;
-                if (warp < 4) {
-                    split2(mul2(kk, pack2(exp2_fast(tail.x - g[i].x), exp2_fast(tail.y - g[i].y))), &hi, &mid);
-                    *reinterpret_cast<uint32_t *>(B + kC * 128 + at) = hi;
-                    *reinterpret_cast<uint32_t *>(B + kPpB + kC * 128 + at) = mid;
+                for (int s = 0; s < 8; s++) {
+                    const uint32_t at = d + (((s >> 2) * kPpA + (s & 3) * 32) >> 4);
+                    umma_warp(tmem, at, at, idesc(1, 2 * kC), s > 0);
                 }
-            }
-            fence_async_smem();
-            __syncthreads();
-            if (warp == 0) {
-                const uint32_t A = desc_lo(saddr(sm)), B = desc_lo(saddr(sm + 2 * kPpA));
-#pragma unroll
-                for (int term = 0; term < 3; term++)
-#pragma unroll
-                    for (int s4 = 0; s4 < 4; s4++)
-                        umma_warp(tmem, A + (((term == 2 ? kPpA : 0) + s4 * 32) >> 4), B + (((term == 1 ? kPpB : 0) + s4 * 32) >> 4),
-                                  idesc(1, 96), half > 0 || term > 0 || s4 > 0);
                 umma_commit_warp(&sh.done);
             }
-        }
-        if (!(reach <= kPpRange)) sh.far = 1;
-        // the norms, a warp's eight rows of each: every exchange halves the rows a lane still sums
+            const int row = tid, t = row & (kC - 1);              // threads 0-63: K's rows, 64-127: Q's
+            if (warp < 4) {
+                // inclusive sums over the 64 tokens, two a lane, as sum + lost
+                float s[2], e[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const bool up = lane & 16;
-            nk[i] = (up ? nq[i] : nk[i]) + __shfl_xor_sync(0xffffffffu, up ? nk[i] : nq[i], 16);
-        }
+                for (int i = 0; i < 2; i++)
+                    s[i] = sh.gin[lane + 32 * i];
+                auto add = [](float &x, float &ex, float y, float ey) {      // two-sum, then the lost parts
+                    const float z = x + y, v = z - x;
+                    ex = ((x - (z - v)) + (y - v)) + (ex + ey);
+                    x = z;
+                };
 #pragma unroll
-        for (int o = 8; o >= 2; o >>= 1) {
-            const bool up = lane & o;
+                for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-            for (int i = 0; i < o / 2; i++)
-                nk[i] = (up ? nk[i + o / 2] : nk[i]) + __shfl_xor_sync(0xffffffffu, up ? nk[i] : nk[i + o / 2], o);
-        }
-        const float n2 = nk[0] + __shfl_xor_sync(0xffffffffu, nk[0], 1);      // lanes below 16 K's, the others Q's
-        if (!(lane & 1)) {
-            const int t = t0 + ((lane >> 1) & 7);
-            const bool in = t < n;
-            const float norm = a.qk_norm ? 1.0f / sqrtf(n2 + a.eps) : 1.0f;
-            if (lane < 16) {
-                const float rk = in ? norm : 0.0f;
-                sh.rk[t] = rk;
-                sh.kb[t] = sh.beta[t] * rk;
-                outf[kRecKr + t] = rk;
-                outf[kRecKd + t] = log2f(rk);
-            } else {
-                const float qn = in ? a.scale * norm : 0.0f;
-                sh.qn[t] = qn;
-                outf[kRecQr + t] = qn;
-            }
-        }
-        if (!sh.bad) wait(sh.done, 1);
-        __syncthreads();
-        far = sh.far != 0;
-    }
-    __syncthreads();
-
-    if (!sh.bad) {
-        // lanes 0-63 of tensor memory hold A's rows, 64-127 P's; a warp takes 32 rows of one of
-        // the two, half of their columns (the upper right quarter of either is zero: not done).
-        // A's four warps go on to invert its 32 x 32 blocks while the others write P.
-        tc_fence_after();
-        const int row = 32 * (warp & 3) + lane, t = row & (kC - 1), i00 = 32 * (warp >> 2);
-        const bool is_a = row < kC;
-        const float rowf = is_a ? sh.kb[t] : sh.qn[t];
-        const int last = t < n ? (is_a ? t - 1 : t) : -1;     // the row's last token
-        const bool zero = i00 == 32 && (warp & 1) == 0;
-        float v[32];
-        if (zero) {
-        } else if (kChannel && far) {
-            // one product at a time, the weight's logarithm summed backwards from t
-            const uint16_t *x = (is_a ? a.k + (size_t)(tok0 + min(t, n - 1)) * a.k_stride
-                                      : a.q + (size_t)(tok0 + min(t, n - 1)) * a.q_stride) + hq * kD;
-#pragma unroll
-            for (int j = 0; j < 32; j++) v[j] = 0.0f;
-            for (int c = 0; c < kD; c++) {
-                const float xc = bf16_bits_to_f32(x[c]);
-                float D = 0.0f;
-                for (int i = t; i >= i00 + 32; i--)           // tokens between the columns and t
-                    if (i < n) D += clamp_gate(a.g[((size_t)(tok0 + i) * a.H + h) * kD + c]);
-#pragma unroll
-                for (int j = 31; j >= 0; j--) {
-                    const int i = i00 + j;
-                    if (i <= t && t < n) {
-                        v[j] = fmaf(xc * bf16_bits_to_f32(a.k[(size_t)(tok0 + i) * a.k_stride + hq * kD + c]),
-                                    exp2_fast(D * kLog2e), v[j]);
-                        D += clamp_gate(a.g[((size_t)(tok0 + i) * a.H + h) * kD + c]);
+                    for (int i = 0; i < 2; i++) {
+                        const float p = __shfl_up_sync(0xffffffffu, s[i], o), ep = __shfl_up_sync(0xffffffffu, e[i], o);
+                        if (lane >= o) add(s[i], e[i], p, ep);
                     }
+                add(s[1], e[1], __shfl_sync(0xffffffffu, s[0], 31), __shfl_sync(0xffffffffu, e[0], 31));
+                const float gc = __shfl_sync(0xffffffffu, s[1], 31), ec = __shfl_sync(0xffffffffu, e[1], 31);
+                const float G = (warp & 1) ? s[1] : s[0], E = (warp & 1) ? e[1] : e[0];
+                float norm = 1.0f;
+                if (a.qk_norm && wait(sh.done, turn & 1)) {   // the diagonal: lane l has its own in column l of 32
+                    tc_fence_after();
+                    float x[32];
+                    const uint32_t at32 = tmem + ((uint32_t)(32 * warp) << 16) + 32 * warp;
+                    tmem_ld16_nowait(at32, *reinterpret_cast<uint32_t(*)[16]>(&x[0]));
+                    tmem_ld16_nowait(at32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&x[16]));
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                        for (int i = 0; i < o; i++) x[i] = lane & o ? x[i + o] : x[i];
+                    norm = 1.0f / sqrtf(x[0] + a.eps);
+                }
+                const bool in = t < n;
+                const float eG = expf(G + E);
+                if (row < kC) {
+                    const float b = sh.bin[t];
+                    sh.gh[t] = G;
+                    sh.gl[t] = E;
+                    sh.rk[t] = in ? norm : 0.0f;
+                    sh.beta[t] = b;
+                    sh.kb[t] = in ? b * norm : 0.0f;
+                    outf[kRecKr + t] = in ? norm * eG : 0.0f;
+                    outf[kRecKd + t] = in ? norm * expf((gc - G) + (ec - E)) : 0.0f;
+                    if (t == 0) outf[kRecDec] = expf(gc + ec);
+                } else {
+                    sh.qn[t] = in ? a.scale * norm : 0.0f;
+                    outf[kRecQr + t] = in ? a.scale * norm * eG : 0.0f;
                 }
             }
+            __syncthreads();
+            if (!sh.bad) wait(sh.done, turn & 1);
         } else {
-            const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (kChannel && t >= 32 && i00 == 0 ? 64 : i00);
-            tmem_ld16_nowait(at, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
-            tmem_ld16_nowait(at + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
-            tmem_wait_ld();
-        }
-        if (!zero) {
-            const float gh = kChannel ? 0.0f : sh.gh[t], gl = kChannel ? 0.0f : sh.gl[t];
-            const uint64_t minus = pack2(-1.0f, -1.0f);
+            // a warp 8 tokens, a lane two of the 64 channels at hand
+            const int t0 = 8 * warp;
+            float nk[8] = {}, nq[8] = {}, reach = 0.0f;
+            for (int half = 0; half < 2; half++) {
+                const int ch = 64 * half + 2 * lane;
+                uint32_t k[8], q[8];
+                float2 g[8];
 #pragma unroll
-            for (int j4 = 0; j4 < 32; j4 += 4) {
-                const float4 r4 = *reinterpret_cast<const float4 *>(&sh.rk[i00 + j4]);
-                const float r[4] = {r4.x, r4.y, r4.z, r4.w};
-                float gi[4] = {}, li[4] = {};
-                if (!kChannel) {
-                    const float4 h4 = *reinterpret_cast<const float4 *>(&sh.gh[i00 + j4]);
-                    const float4 l4 = *reinterpret_cast<const float4 *>(&sh.gl[i00 + j4]);
-                    gi[0] = h4.x; gi[1] = h4.y; gi[2] = h4.z; gi[3] = h4.w;
-                    li[0] = l4.x; li[1] = l4.y; li[2] = l4.z; li[3] = l4.w;
+                for (int i = 0; i < 8; i++) {
+                    const size_t tok = (size_t)tok0 + min(t0 + i, n - 1);
+                    k[i] = *reinterpret_cast<const uint32_t *>(a.k + tok * a.k_stride + hq * kD + ch);
+                    q[i] = *reinterpret_cast<const uint32_t *>(a.q + tok * a.q_stride + hq * kD + ch);
+                    g[i] = *reinterpret_cast<const float2 *>(a.g + (tok * a.H + h) * kD + ch);
                 }
+                float2 L = make_float2(0.0f, 0.0f);               // sums over this warp's tokens so far, in log2
 #pragma unroll
-                for (int j = 0; j < 4; j += 2) {
-                    const int at = j4 + j;
-                    uint64_t x = mul2(pack2(v[at], v[at + 1]), mul2(pack2(rowf, rowf), pack2(r[j], r[j + 1])));
-                    if (!kChannel) {
-                        const uint64_t e = add2(fma2(pack2(gi[j], gi[j + 1]), minus, pack2(gh, gh)),
-                                                fma2(pack2(li[j], li[j + 1]), minus, pack2(gl, gl)));
-                        const float2 w = unpack2(mul2(e, pack2(kLog2e, kLog2e)));
-                        x = mul2(x, pack2(exp2_fast(w.x), exp2_fast(w.y)));
+                for (int i = 0; i < 8; i++) {
+                    const bool in = t0 + i < n;
+                    L.x += in ? clamp_gate(g[i].x) * kLog2e : 0.0f;
+                    L.y += in ? clamp_gate(g[i].y) * kLog2e : 0.0f;
+                    g[i] = L;
+                }
+                *reinterpret_cast<float2 *>(&sh.sum[warp][ch]) = L;
+                *reinterpret_cast<float2 *>(&outf[kRecSum + warp * kD + ch]) = L;
+                if (half == 1) wait(sh.done, 0);                  // the first half's operands are used
+                __syncthreads();
+                if (sh.bad) break;
+                float2 s[8];
+#pragma unroll
+                for (int w = 0; w < 8; w++) s[w] = *reinterpret_cast<const float2 *>(&sh.sum[w][ch]);
+                // G at this warp's start less the middle of its 32 tokens; the second half's middle
+                // less the first half's end (both counted from their own half's start)
+                const int b = (warp >> 2) * 4;
+                float2 base = make_float2(0.f, 0.f);
+                float2 m1 = make_float2(s[4].x + s[5].x, s[4].y + s[5].y);
+                switch (warp & 3) {
+                case 0: base = make_float2(-(s[b].x + s[b + 1].x), -(s[b].y + s[b + 1].y)); break;
+                case 1: base = make_float2(-s[b + 1].x, -s[b + 1].y); break;
+                case 2: break;
+                default: base = make_float2(s[b + 2].x, s[b + 2].y); break;
+                }
+                // (first half only) the second's middle less G at this warp's start
+                float2 tail = m1;
+#pragma unroll
+                for (int w = 3; w >= 0; w--)
+                    if (w >= warp) { tail.x += s[w].x; tail.y += s[w].y; }
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int t = t0 + i;
+                    const uint64_t kk = pair_bf16(k[i]), qq = pair_bf16(q[i]);
+                    const float2 kf = unpack2(kk), qf = unpack2(qq);
+                    nk[i] = fmaf(kf.x, kf.x, fmaf(kf.y, kf.y, nk[i]));
+                    nq[i] = fmaf(qf.x, qf.x, fmaf(qf.y, qf.y, nq[i]));
+                    const float dx = base.x + g[i].x, dy = base.y + g[i].y;       // G_t - m
+                    reach = max_nan(reach, max_nan(fabsf(dx), fabsf(dy)));
+                    const uint64_t e = pack2(exp2_fast(dx), exp2_fast(dy));
+                    const uint32_t at = t * 128 + (((lane >> 2) ^ (t & 7)) << 4) + (lane & 3) * 4;
+                    uint32_t hi, mid;
+                    split2(mul2(kk, e), &hi, &mid);
+                    *reinterpret_cast<uint32_t *>(sm + at) = hi;
+                    *reinterpret_cast<uint32_t *>(sm + kPpA + at) = mid;
+                    split2(mul2(qq, e), &hi, &mid);
+                    *reinterpret_cast<uint32_t *>(sm + kC * 128 + at) = hi;
+                    *reinterpret_cast<uint32_t *>(sm + kPpA + kC * 128 + at) = mid;
+                    uint8_t *B = sm + 2 * kPpA;
+                    split2(mul2(kk, pack2(exp2_fast(-dx), exp2_fast(-dy))), &hi, &mid);
+                    *reinterpret_cast<uint32_t *>(B + at) = hi;
+                    *reinterpret_cast<uint32_t *>(B + kPpB + at) = mid;
+                    if (warp < 4) {
+                        split2(mul2(kk, pack2(exp2_fast(tail.x - g[i].x), exp2_fast(tail.y - g[i].y))), &hi, &mid);
+                        *reinterpret_cast<uint32_t *>(B + kC * 128 + at) = hi;
+                        *reinterpret_cast<uint32_t *>(B + kPpB + kC * 128 + at) = mid;
                     }
-                    const float2 y = unpack2(x);
-                    v[at] = i00 + at <= last ? y.x : 0.0f;
-                    v[at + 1] = i00 + at + 1 <= last ? y.y : 0.0f;
+                }
+                fence_async_smem();
+                __syncthreads();
+                if (warp == 0) {
+                    const uint32_t A = desc_lo(saddr(sm)), B = desc_lo(saddr(sm + 2 * kPpA));
+#pragma unroll
+                    for (int term = 0; term < 3; term++)
+#pragma unroll
+                        for (int s4 = 0; s4 < 4; s4++)
+                            umma_warp(tmem, A + (((term == 2 ? kPpA : 0) + s4 * 32) >> 4), B + (((term == 1 ? kPpB : 0) + s4 * 32) >> 4),
+                                      idesc(1, 96), half > 0 || term > 0 || s4 > 0);
+                    umma_commit_warp(&sh.done);
                 }
             }
-        }
-        if (is_a) {
-            if (!zero)
+            if (!(reach <= kPpRange)) sh.far = 1;
+            // the norms, a warp's eight rows of each: every exchange halves the rows a lane still sums
 #pragma unroll
-                for (int j = 0; j < 8; j++)                   // over the operands: they are used
-                    *reinterpret_cast<float4 *>(&As[t * kChLd + i00 + 4 * j]) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            four_warps();
-            invert32(As, (warp & 1) + 2 * (warp >> 2), lane);
-        } else if (!zero) {
-            const float(*v8)[8] = reinterpret_cast<const float(*)[8]>(v);
+            for (int i = 0; i < 8; i++) {
+                const bool up = lane & 16;
+                nk[i] = (up ? nq[i] : nk[i]) + __shfl_xor_sync(0xffffffffu, up ? nk[i] : nq[i], 16);
+            }
 #pragma unroll
-            for (int j = 0; j < 4; j++) put_terms(out + 2 * kTermBytes, t, i00 / 8 + j, v8[j]);
+            for (int o = 8; o >= 2; o >>= 1) {
+                const bool up = lane & o;
+#pragma unroll
+                for (int i = 0; i < o / 2; i++)
+                    nk[i] = (up ? nk[i + o / 2] : nk[i]) + __shfl_xor_sync(0xffffffffu, up ? nk[i] : nk[i + o / 2], o);
+            }
+            const float n2 = nk[0] + __shfl_xor_sync(0xffffffffu, nk[0], 1);      // lanes below 16 K's, the others Q's
+            if (!(lane & 1)) {
+                const int t = t0 + ((lane >> 1) & 7);
+                const bool in = t < n;
+                const float norm = a.qk_norm ? 1.0f / sqrtf(n2 + a.eps) : 1.0f;
+                if (lane < 16) {
+                    const float rk = in ? norm : 0.0f;
+                    sh.rk[t] = rk;
+                    sh.kb[t] = sh.beta[t] * rk;
+                    outf[kRecKr + t] = rk;
+                    outf[kRecKd + t] = log2f(rk);
+                } else {
+                    const float qn = in ? a.scale * norm : 0.0f;
+                    sh.qn[t] = qn;
+                    outf[kRecQr + t] = qn;
+                }
+            }
+            if (!sh.bad) wait(sh.done, 1);
+            __syncthreads();
+            far = sh.far != 0;
         }
         __syncthreads();
-        invert64(As, warp, lane);
-        // T = (I + A)^-1 diag(beta): a warp 16 columns of half the rows
-        const int r = 32 * (warp >> 2) + lane, c0 = 16 * (warp & 3);
-        if (c0 < 32 * (warp >> 2) + 32)
+
+        if (!sh.bad) {
+            // the operands are used (per channel the scratch goes over them), and what the block had of
+            // this chunk's steps and decays
+            if (!kChannel && warp == kWarpNext) next(turn + 1);
+            if (tid == 0) sh.far = 0;
+            // lanes 0-63 of tensor memory hold A's rows, 64-127 P's; a warp takes 32 rows of one of
+            // the two, half of their columns (the upper right quarter of either is zero: not done).
+            // A's four warps go on to invert its 32 x 32 blocks while the others write P.
+            tc_fence_after();
+            const int row = 32 * (warp & 3) + lane, t = row & (kC - 1), i00 = 32 * (warp >> 2);
+            const bool is_a = row < kC;
+            const float rowf = is_a ? sh.kb[t] : sh.qn[t];
+            const int last = t < n ? (is_a ? t - 1 : t) : -1;     // the row's last token
+            const bool zero = i00 == 32 && (warp & 1) == 0;
+            float v[32];
+            if (zero) {
+            } else if (kChannel && far) {
+                // one product at a time, the weight's logarithm summed backwards from t
+                const uint16_t *x = (is_a ? a.k + (size_t)(tok0 + min(t, n - 1)) * a.k_stride
+                                          : a.q + (size_t)(tok0 + min(t, n - 1)) * a.q_stride) + hq * kD;
 #pragma unroll
-            for (int j8 = 0; j8 < 2; j8++) {
-                float x[8], b[8];
+                for (int j = 0; j < 32; j++) v[j] = 0.0f;
+                for (int c = 0; c < kD; c++) {
+                    const float xc = bf16_bits_to_f32(x[c]);
+                    float D = 0.0f;
+                    for (int i = t; i >= i00 + 32; i--)           // tokens between the columns and t
+                        if (i < n) D += clamp_gate(a.g[((size_t)(tok0 + i) * a.H + h) * kD + c]);
 #pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    *reinterpret_cast<float4 *>(&x[j]) = *reinterpret_cast<const float4 *>(&As[r * kChLd + c0 + 8 * j8 + j]);
-                    *reinterpret_cast<float4 *>(&b[j]) = *reinterpret_cast<const float4 *>(&sh.beta[c0 + 8 * j8 + j]);
+                    for (int j = 31; j >= 0; j--) {
+                        const int i = i00 + j;
+                        if (i <= t && t < n) {
+                            v[j] = fmaf(xc * bf16_bits_to_f32(a.k[(size_t)(tok0 + i) * a.k_stride + hq * kD + c]),
+                                        exp2_fast(D * kLog2e), v[j]);
+                            D += clamp_gate(a.g[((size_t)(tok0 + i) * a.H + h) * kD + c]);
+                        }
+                    }
                 }
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float y = x[j] * b[j];
-                    x[j] = c0 + 8 * j8 + j <= r ? y : 0.0f;
-                }
-                put_terms(out, r, c0 / 8 + j8, x);
+            } else {
+                const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (kChannel && t >= 32 && i00 == 0 ? 64 : i00);
+                tmem_ld16_nowait(at, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+                tmem_ld16_nowait(at + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+                tmem_wait_ld();
             }
+            if (!zero) {
+                const float gh = kChannel ? 0.0f : sh.gh[t], gl = kChannel ? 0.0f : sh.gl[t];
+                const uint64_t minus = pack2(-1.0f, -1.0f);
+#pragma unroll
+                for (int j4 = 0; j4 < 32; j4 += 4) {
+                    const float4 r4 = *reinterpret_cast<const float4 *>(&sh.rk[i00 + j4]);
+                    const float r[4] = {r4.x, r4.y, r4.z, r4.w};
+                    float gi[4] = {}, li[4] = {};
+                    if (!kChannel) {
+                        const float4 h4 = *reinterpret_cast<const float4 *>(&sh.gh[i00 + j4]);
+                        const float4 l4 = *reinterpret_cast<const float4 *>(&sh.gl[i00 + j4]);
+                        gi[0] = h4.x; gi[1] = h4.y; gi[2] = h4.z; gi[3] = h4.w;
+                        li[0] = l4.x; li[1] = l4.y; li[2] = l4.z; li[3] = l4.w;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; j += 2) {
+                        const int at = j4 + j;
+                        uint64_t x = mul2(pack2(v[at], v[at + 1]), mul2(pack2(rowf, rowf), pack2(r[j], r[j + 1])));
+                        if (!kChannel) {
+                            const uint64_t e = add2(fma2(pack2(gi[j], gi[j + 1]), minus, pack2(gh, gh)),
+                                                    fma2(pack2(li[j], li[j + 1]), minus, pack2(gl, gl)));
+                            const float2 w = unpack2(mul2(e, pack2(kLog2e, kLog2e)));
+                            x = mul2(x, pack2(exp2_fast(w.x), exp2_fast(w.y)));
+                        }
+                        const float2 y = unpack2(x);
+                        v[at] = i00 + at <= last ? y.x : 0.0f;
+                        v[at + 1] = i00 + at + 1 <= last ? y.y : 0.0f;
+                    }
+                }
+            }
+            if (is_a) {
+                if (!zero)
+#pragma unroll
+                    for (int j = 0; j < 8; j++)                   // over the operands: they are used
+                        *reinterpret_cast<float4 *>(&As[t * kChLd + i00 + 4 * j]) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                four_warps();
+                invert32(As, (warp & 1) + 2 * (warp >> 2), lane);
+            } else if (!zero) {
+                const float(*v8)[8] = reinterpret_cast<const float(*)[8]>(v);
+#pragma unroll
+                for (int j = 0; j < 4; j++) put_terms(out + 2 * kTermBytes, t, i00 / 8 + j, v8[j]);
+            }
+            __syncthreads();
+            invert64(As, warp, lane);
+            if (!kChannel && warp == kWarpNext) keep();
+            // T = (I + A)^-1 diag(beta): a warp 16 columns of half the rows
+            const int r = 32 * (warp >> 2) + lane, c0 = 16 * (warp & 3);
+            if (c0 < 32 * (warp >> 2) + 32)
+#pragma unroll
+                for (int j8 = 0; j8 < 2; j8++) {
+                    float x[8], b[8];
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4) {
+                        *reinterpret_cast<float4 *>(&x[j]) = *reinterpret_cast<const float4 *>(&As[r * kChLd + c0 + 8 * j8 + j]);
+                        *reinterpret_cast<float4 *>(&b[j]) = *reinterpret_cast<const float4 *>(&sh.beta[c0 + 8 * j8 + j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const float y = x[j] * b[j];
+                        x[j] = c0 + 8 * j8 + j <= r ? y : 0.0f;
+                    }
+                    put_terms(out, r, c0 / 8 + j8, x);
+                }
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (sh.bad) {                                             // given up: not before the copies on their way
+            if (!kChannel && sh.unit[(turn + 1) & 1].n > 0) wait(sh.full, (turn + 1) & 1);
+            break;
+        }
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
     // the last block of such a launch ends after that chain: what follows finds both complete
@@ -1429,7 +1487,7 @@ int plan_stretches(const DeltaArgs &a, int (&ends)[kMaxStretches])
     const long long jobs = (long long)a.n_seq * a.H;
     const int sms = num_sms(), last = (a.T + kC - 1) / kC;
     if (jobs >= sms) return 1;
-    constexpr double prepare = kChannel ? 5.5 : 2.8, chain = kChannel ? 4.6 : 3.2;
+    constexpr double prepare = kChannel ? 5.5 : 2.3, chain = kChannel ? 4.6 : 3.2;
     constexpr double extra = 8.0;
     const double chunks = (double)last / a.n_seq, grow = chain * (double)(sms - jobs) / (prepare * jobs);
     int n = 1;
@@ -1483,9 +1541,10 @@ cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
         x.chunk0 = i > 0 ? ends[i - 1] : 0;
         x.chunk1 = ends[i];
         if (x.chunk1 <= x.chunk0) continue;
-        const long long units = x.chunk1 < kAllChunks ? (long long)(x.chunk1 - x.chunk0) * x.n_seq : chunk_records(a.n_seq, a.T);
+        x.units = (int32_t)((x.chunk1 < kAllChunks ? (long long)(x.chunk1 - x.chunk0) * x.n_seq : chunk_records(a.n_seq, a.T)) * a.H);
+        const int sms = i > 0 ? std::max(1, num_sms() - ((a.n_seq * a.H + 1) & ~1)) : num_sms();         // later stretches have those without a chain
         timing_begin("delta_prepare", s);
-        err = launch_pdl(delta_prepare_kernel<kChannel>, dim3((unsigned)(units * a.H)), dim3(kPpThreads), pp_smem(kChannel), s, x, mq, mk);
+        err = launch_pdl(delta_prepare_kernel<kChannel>, dim3((unsigned)(kChannel ? x.units : std::min(x.units, sms * kPpBlocks<false>))), dim3(kPpThreads), pp_smem(kChannel), s, x, mq, mk);
         count_launch();
         timing_end("delta_prepare", s);
         if (err != cudaSuccess) return err;

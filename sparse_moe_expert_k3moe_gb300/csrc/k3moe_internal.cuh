@@ -369,6 +369,7 @@ struct DeltaArgs {
     uint16_t *out;
     uint8_t *ws;
     int32_t chunk0, chunk1;                               // in chunks: the launch's stretch of each sequence
+    int32_t units;                                        // and its chunks and heads
 };
 size_t delta_workspace(const k3moe_delta_config &dc, int n_seq, int T);
 cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t s);
