@@ -1468,10 +1468,10 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
 
 // From this many tokens a sequence on average, chunks; `alone` where the recurrent kernel's
 // blocks have an SM each.  Recurrent against chunks, us, per head: 64 sequences x 32 heads of 16
-// tokens 153, 176 and of 20 189, 178; 8 x 32 heads of 16 25, 25; alone (one sequence, 56
-// heads) of 20 13.1, 13.8 and of 24 14.8, 13.8.  Per channel: 37 x 56 heads of 26 tokens 252,
-// 265 and of 32 302, 270; alone of 32 18.0, 20.7 and of 40 22.5, 20.9.
-constexpr int chunk_tokens_avg(bool channel, bool alone) { return channel ? (alone ? 37 : 28) : (alone ? 23 : 18); }
+// tokens 153, 159 and of 18 173, 161; 8 x 32 heads of 14 23, 24 and of 18 29, 24; alone (one
+// sequence, 56 heads) of 22 13.3, 14.3 and of 26 15.5, 14.3.  Per channel: 37 x 56 heads of 26
+// tokens 252, 253 and of 28 268, 254; alone of 36 20.2, 20.6.
+constexpr int chunk_tokens_avg(bool channel, bool alone) { return channel ? (alone ? 37 : 27) : (alone ? 24 : 17); }
 
 // Where the chains leave SMs free, the sequences are walked in stretches (one sequence of 8192
 // tokens x 56 heads: 546 us in one, 452 in four; per channel 875 and 687): while the chains go
