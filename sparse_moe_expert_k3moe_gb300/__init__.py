@@ -533,11 +533,17 @@ def _device(device):
     return device, device.index if device.type == "cuda" else -1
 
 
-def _stream_of(stream, index):
-    """The handle of `stream`, of the current stream when it is None."""
-    if stream is None:
-        import torch
-        return torch.cuda.current_stream(index).cuda_stream
+def _current_stream(index):
+    """A function that returns the handle of the device's current stream: torch's own one
+    without the Stream object around it, where it has that."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        return lambda: raw(index)
+    return lambda: torch.cuda.current_stream(index).cuda_stream
+
+
+def _handle(stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -555,11 +561,11 @@ class Linear:
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
         self._bf16, self._f32 = (torch.bfloat16, torch.int16), (torch.float32,)
         self._n, self._k, self._ytype = lc.n, lc.k, self._f32 if lc.y_f32 else self._bf16
-        self._lc, self._call = ctypes.byref(lc), lib().k3moe_linear
+        self._lc, self._call, self._current = ctypes.byref(lc), lib().k3moe_linear, _current_stream(self._index)
 
     def _rows(self, what, t, types, shape):
         """The row stride of x, y or the residual."""
-        if _fits(t, types, shape, self._index):
+        if t.dtype in types and t.shape == shape and t.get_device() == self._index:
             if t.is_contiguous():
                 return shape[1]
             if t.stride(1) == 1 and shape[0] > 1:
@@ -574,18 +580,19 @@ class Linear:
             raise ValueError(f"x: {T} rows, the holder is for {self.T_max}")
         xs = self._rows("x", x, self._bf16, (T, k))
         ys = self._rows("y", y, self._ytype, (T, n))
-        if not (_fits(w, self._bf16, (n, k), dev) and w.is_contiguous()):
+        if not (w.dtype in self._bf16 and w.shape == (n, k) and w.get_device() == dev and w.is_contiguous()):
             _require("w", w, self._bf16, (n, k), dev)
         rs = 0
         if residual is not None:
             rs = ys if residual is y else self._rows("residual", residual, self._ytype, (T, n))
-        if bias is not None and not (_fits(bias, self._f32, (n,), dev) and bias.is_contiguous()):
+        if bias is not None and not (bias.dtype in self._f32 and bias.shape == (n,) and bias.get_device() == dev and bias.is_contiguous()):
             _require("bias", bias, self._f32, (n,), dev)
         if T:
-            _check("k3moe_linear", self._call(
-                self._lc, T, x.data_ptr(), xs, w.data_ptr(), None if bias is None else bias.data_ptr(),
-                None if residual is None else residual.data_ptr(), rs, y.data_ptr(), ys, self.ws.data_ptr(),
-                self.ws_bytes, _stream_of(stream, dev)))
+            st = self._call(self._lc, T, x.data_ptr(), xs, w.data_ptr(), None if bias is None else bias.data_ptr(),
+                            None if residual is None else residual.data_ptr(), rs, y.data_ptr(), ys, self.ws.data_ptr(),
+                            self.ws_bytes, self._current() if stream is None else _handle(stream))
+            if st:
+                _check("k3moe_linear", st)
         return y
 
 
@@ -602,7 +609,7 @@ class DeltaRule:
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
         self._bf16, self._f32, self._i32 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,)
         self._H, self._Hq, self._D, self._G = dc.n_heads, dc.n_qk_heads, dc.head_dim, dc.gate_dim
-        self._dc, self._call = ctypes.byref(dc), lib().k3moe_delta_rule
+        self._dc, self._call, self._current = ctypes.byref(dc), lib().k3moe_delta_rule, _current_stream(self._index)
 
     def new_state(self, n_slots):
         """A zeroed pool of n_slots states [n_slots][n_heads][head_dim][head_dim] f32."""
@@ -611,10 +618,10 @@ class DeltaRule:
 
     def _rows(self, what, t, shape):
         """The row stride of q, k or v."""
-        if _fits(t, self._bf16, shape, self._index) and shape[0] > 1:
+        if t.dtype in self._bf16 and t.shape == shape and t.get_device() == self._index:
             s = t.stride()
             if s[2] == 1 and s[1] == self._D:
-                return s[0]
+                return s[0] if shape[0] > 1 else shape[1] * self._D
         return _require(what, t, self._bf16, shape, self._index, True)
 
     def __call__(self, q, k, v, g, beta, out, state_in, state_out, seq_start=None, slots=None, stream=None):
@@ -631,17 +638,31 @@ class DeltaRule:
         n_slots = state_out.shape[0]
         pool = (n_slots, H, D, D)
         n_seq = seq_start.shape[0] - 1 if seq_start is not None else slots.shape[0] if slots is not None else T
-        for what, t, types, shape in (("g", g, f32, (T, H, self._G)), ("beta", beta, f32, (T, H)),
-                                      ("out", out, self._bf16, (T, H, D)), ("state_out", state_out, f32, pool),
-                                      ("state_in", state_in, f32, pool), ("seq_start", seq_start, i32, (n_seq + 1,)),
-                                      ("slots", slots, i32, (n_seq,))):
-            if t is not None and not (_fits(t, types, shape, dev) and t.is_contiguous()):
-                _require(what, t, types, shape, dev)
+        # one line a tensor: what _require says at length when it does not hold
+        if not (g.dtype in f32 and g.shape == (T, H, self._G) and g.get_device() == dev and g.is_contiguous()):
+            _require("g", g, f32, (T, H, self._G), dev)
+        if not (beta.dtype in f32 and beta.shape == (T, H) and beta.get_device() == dev and beta.is_contiguous()):
+            _require("beta", beta, f32, (T, H), dev)
+        if not (out.dtype in self._bf16 and out.shape == (T, H, D) and out.get_device() == dev and out.is_contiguous()):
+            _require("out", out, self._bf16, (T, H, D), dev)
+        if not (state_out.dtype in f32 and state_out.shape == pool and state_out.get_device() == dev and state_out.is_contiguous()):
+            _require("state_out", state_out, f32, pool, dev)
+        if state_in is not None and state_in is not state_out and not (
+                state_in.dtype in f32 and state_in.shape == pool and state_in.get_device() == dev and state_in.is_contiguous()):
+            _require("state_in", state_in, f32, pool, dev)
+        if seq_start is not None and not (
+                seq_start.dtype in i32 and seq_start.dim() == 1 and seq_start.get_device() == dev and seq_start.is_contiguous()):
+            _require("seq_start", seq_start, i32, (n_seq + 1,), dev)
+        if slots is not None and not (
+                slots.dtype in i32 and slots.shape == (n_seq,) and slots.get_device() == dev and slots.is_contiguous()):
+            _require("slots", slots, i32, (n_seq,), dev)
         if n_seq > self.n_seq_max or T > self.T_max:
             raise ValueError(f"{n_seq} sequences of {T} tokens, the holder is for {self.n_seq_max} and {self.T_max}")
-        _check("k3moe_delta_rule", self._call(
+        st = self._call(
             self._dc, n_seq, T, None if seq_start is None else seq_start.data_ptr(), q.data_ptr(), qs, k.data_ptr(), ks,
             v.data_ptr(), vs, g.data_ptr(), beta.data_ptr(), None if state_in is None else state_in.data_ptr(),
             state_out.data_ptr(), n_slots, None if slots is None else slots.data_ptr(), out.data_ptr(),
-            self.ws.data_ptr(), self.ws_bytes, _stream_of(stream, dev)))
+            self.ws.data_ptr(), self.ws_bytes, self._current() if stream is None else _handle(stream))
+        if st:
+            _check("k3moe_delta_rule", st)
         return out

@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(kPpThreads, kPpBlocks<kChannel>)
 // What bounds it: the steps follow from one another, 3.3 us a chunk and 4.7 per channel with the
 // tensor cores busy a quarter of it; the loops over the terms stay rolled, as straight code misses
 // the instruction cache every chunk (eight sequences of 1024 tokens x 56 heads: 186 -> 178 us, per
-// channel 287 -> 263).  One sequence of 8192 tokens takes 419 us, per channel 615.
+// channel 287 -> 263).
 constexpr int kChChain = 8, kChOut = 4, kChMake = 8;
 constexpr int kChPartK = kD / (kChChain / 4), kChPartT = kC / (kChChain / 4);     // channels and tokens of a chain warp
 constexpr int kChStagesHead = 3, kChStagesChannel = 2;
@@ -1474,8 +1474,8 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
 constexpr int chunk_tokens_avg(bool channel, bool alone) { return channel ? (alone ? 37 : 27) : (alone ? 24 : 17); }
 
 // Where the chains leave SMs free, the sequences are walked in stretches (one sequence of 8192
-// tokens x 56 heads: 546 us in one, 452 in four; per channel 875 and 687): while the chains go
-// through one, the SMs that are left prepare the next.  A stretch is as much longer than the
+// tokens x 56 heads: 524 us in one, 451 so; x 140 heads 666, 649; per channel 856, 667 and 1256,
+// 1218; 512 tokens per channel 61, 63): while the chains go through one, the SMs that are left prepare the next.  A stretch is as much longer than the
 // one before as preparing on those SMs is faster than the chains; the number of stretches is
 // the one with the least estimated time (microseconds: a chunk and head prepared on one SM,
 // a chain's chunk, and what one stretch more costs), ends[i] the chunk that ends the i-th.
@@ -1550,8 +1550,8 @@ cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
         if (err != cudaSuccess) return err;
         timing_begin("delta_chunk", s);
         // Beside a prepare the chains go in pairs, a cluster of two on the SMs of a TPC: a chain whose
-        // neighbour there runs other code takes a quarter to a half longer (per channel 330 against 262 us
-        // for 53 chunks, per head 183 against 142 for 43).
+        // neighbour there runs other code takes a quarter to a half longer (8192 tokens x 56 heads: 451
+        // us in pairs, 490 singly; per channel 667, 793; two sequences 298, 323 and 547, 640).
         const bool pairs = stretches > 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(pairs ? (a.n_seq * a.H + 1) & ~1 : a.n_seq * a.H));
