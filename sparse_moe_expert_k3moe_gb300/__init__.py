@@ -585,7 +585,8 @@ class Linear:
         rs = 0
         if residual is not None:
             rs = ys if residual is y else self._rows("residual", residual, self._ytype, (T, n))
-        if bias is not None and not (bias.dtype in self._f32 and bias.shape == (n,) and bias.get_device() == dev and bias.is_contiguous()):
+        if bias is not None and not (
+                bias.dtype in self._f32 and bias.shape == (n,) and bias.get_device() == dev and bias.is_contiguous()):
             _require("bias", bias, self._f32, (n,), dev)
         if T:
             st = self._call(self._lc, T, x.data_ptr(), xs, w.data_ptr(), None if bias is None else bias.data_ptr(),

@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kRecThreads, 4) delta_recurrent_kernel(const D
         float2 x[2];
 #pragma unroll
         for (int i = 0; i < 2; i++)
-            x[i] = a.state_in ? __ldcs(reinterpret_cast<const float2 *>(a.state_in + sbase + (size_t)(j + i) * kD)) : make_float2(0.f, 0.f);
+            x[i] = a.state_in ? __ldcs(reinterpret_cast<const float2 *>(a.state_in + sbase + (size_t)(j + i) * kD))
+                              : make_float2(0.f, 0.f);
         S[j / 2][0] = pack2(x[0].x, x[1].x);
         S[j / 2][1] = pack2(x[0].y, x[1].y);
     }
@@ -870,7 +871,8 @@ __global__ void __launch_bounds__(kPpThreads, kPpBlocks<kChannel>)
                 if (!zero)
 #pragma unroll
                     for (int j = 0; j < 8; j++)                   // over the operands: they are used
-                        *reinterpret_cast<float4 *>(&As[t * kChLd + i00 + 4 * j]) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                        *reinterpret_cast<float4 *>(&As[t * kChLd + i00 + 4 * j]) =
+                        make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 four_warps();
                 invert32(As, (warp & 1) + 2 * (warp >> 2), lane);
             } else if (!zero) {
@@ -1473,12 +1475,13 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
 // tokens 252, 253 and of 28 268, 254; alone of 36 20.2, 20.6.
 constexpr int chunk_tokens_avg(bool channel, bool alone) { return channel ? (alone ? 37 : 27) : (alone ? 24 : 17); }
 
-// Where the chains leave SMs free, the sequences are walked in stretches (one sequence of 8192
-// tokens x 56 heads: 524 us in one, 451 so; x 140 heads 666, 649; per channel 856, 667 and 1256,
-// 1218; 512 tokens per channel 61, 63): while the chains go through one, the SMs that are left prepare the next.  A stretch is as much longer than the
+// Where the chains leave SMs free, the sequences are walked in stretches: while the chains go
+// through one, the SMs that are left prepare the next.  A stretch is as much longer than the
 // one before as preparing on those SMs is faster than the chains; the number of stretches is
 // the one with the least estimated time (microseconds: a chunk and head prepared on one SM,
 // a chain's chunk, and what one stretch more costs), ends[i] the chunk that ends the i-th.
+// In one and so, us: one sequence of 8192 tokens x 56 heads 524, 451, x 140 heads 666, 649;
+// per channel 856, 667 and 1256, 1218; 512 tokens x 56 heads per channel 61, 63.
 constexpr int kMaxStretches = 8;
 template <bool kChannel>
 int plan_stretches(const DeltaArgs &a, int (&ends)[kMaxStretches])
@@ -1541,10 +1544,13 @@ cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
         x.chunk0 = i > 0 ? ends[i - 1] : 0;
         x.chunk1 = ends[i];
         if (x.chunk1 <= x.chunk0) continue;
-        x.units = (int32_t)((x.chunk1 < kAllChunks ? (long long)(x.chunk1 - x.chunk0) * x.n_seq : chunk_records(a.n_seq, a.T)) * a.H);
-        const int sms = i > 0 ? std::max(1, num_sms() - ((a.n_seq * a.H + 1) & ~1)) : num_sms();         // later stretches have those without a chain
+        const long long units = x.chunk1 < kAllChunks ? (long long)(x.chunk1 - x.chunk0) * a.n_seq : chunk_records(a.n_seq, a.T);
+        x.units = (int32_t)(units * a.H);
+        // blocks that stay: on every SM, or on those that a later stretch has beside the chains
+        const int sms = i > 0 ? std::max(1, num_sms() - ((a.n_seq * a.H + 1) & ~1)) : num_sms();
+        const int blocks = kChannel ? x.units : std::min(x.units, sms * kPpBlocks<kChannel>);
         timing_begin("delta_prepare", s);
-        err = launch_pdl(delta_prepare_kernel<kChannel>, dim3((unsigned)(kChannel ? x.units : std::min(x.units, sms * kPpBlocks<false>))), dim3(kPpThreads), pp_smem(kChannel), s, x, mq, mk);
+        err = launch_pdl(delta_prepare_kernel<kChannel>, dim3((unsigned)blocks), dim3(kPpThreads), pp_smem(kChannel), s, x, mq, mk);
         count_launch();
         timing_end("delta_prepare", s);
         if (err != cudaSuccess) return err;
