@@ -75,6 +75,79 @@ void timing_end(const char *name, cudaStream_t s)
     t.launches++;
 }
 
+// ----------------------------------------------------------------------------------- results still being written
+// A mixer's call (k3moe_linear, k3moe_delta_rule) lets the next kernel launch when its own
+// has begun, before it has written its result.  Every kernel of the library waits before it reads,
+// but for the forward's mat-vec path, which converts x ahead of that wait.  So the streams whose
+// latest call is a mixer's are kept here, apart for each capture, and the forward does not read
+// ahead on them.  What is not known counts as pending, as does a new stream with the handle of one
+// that is gone: the forward then starts a little later, never too early.
+struct StreamKey {
+    const void *stream;
+    unsigned long long capture;                          // its id; 0: launched, not captured
+    bool operator==(const StreamKey &o) const { return stream == o.stream && capture == o.capture; }
+};
+constexpr size_t kMaxPending = 1024;
+static std::mutex g_pmu;
+static std::vector<StreamKey> g_pending;
+static std::atomic<bool> g_any_pending{false}, g_all_pending{false};     // some; more than are kept
+
+static bool stream_key(cudaStream_t s, StreamKey *key)
+{
+    static thread_local char own;                        // stands for this thread's default stream
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamGetCaptureInfo(s, &cap, &id) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    key->stream = s == cudaStreamLegacy ? nullptr : s == cudaStreamPerThread ? (const void *)&own : (const void *)s;
+    key->capture = cap == cudaStreamCaptureStatusNone ? 0 : id;
+    return true;
+}
+
+void result_pending_begin(cudaStream_t s)
+{
+    StreamKey key;
+    const bool known = stream_key(s, &key);
+    std::lock_guard<std::mutex> lk(g_pmu);
+    if (!known || (g_pending.size() >= kMaxPending && std::find(g_pending.begin(), g_pending.end(), key) == g_pending.end()))
+        g_all_pending = true;
+    else if (std::find(g_pending.begin(), g_pending.end(), key) == g_pending.end())
+        g_pending.push_back(key);
+    g_any_pending = true;
+}
+
+void result_pending_end(cudaStream_t s)
+{
+    StreamKey key;
+    if (!g_any_pending || !stream_key(s, &key)) return;
+    std::lock_guard<std::mutex> lk(g_pmu);
+    const auto at = std::find(g_pending.begin(), g_pending.end(), key);
+    if (at != g_pending.end()) {
+        *at = g_pending.back();
+        g_pending.pop_back();
+    }
+    g_any_pending = g_all_pending || !g_pending.empty();
+}
+
+bool result_pending(cudaStream_t s)
+{
+    StreamKey key;
+    if (!g_any_pending) return false;
+    if (g_all_pending || !stream_key(s, &key)) return true;
+    std::lock_guard<std::mutex> lk(g_pmu);
+    return std::find(g_pending.begin(), g_pending.end(), key) != g_pending.end();
+}
+
+// The end of a call whose first kernel waits before it lets the next one launch.
+static k3moe_status waited(cudaError_t e, cudaStream_t s)
+{
+    if (e != cudaSuccess) return K3MOE_ECUDA;
+    result_pending_end(s);
+    return K3MOE_OK;
+}
+
 // ----------------------------------------------------------------------------------- validation
 static bool finite_pos(float v) { return std::isfinite(v) && v > 0.0f; }
 
@@ -221,7 +294,7 @@ k3moe_status k3moe_route(const k3moe_config *cfg, int32_t T, const uint16_t *x,
     if (ws_bytes < L.total) return K3MOE_EWORKSPACE;
     cudaError_t e = launch_route(*cfg, T, x, w_router, bias, idx, weight, offsets, perm,
                                  static_cast<uint8_t *>(ws), L, (cudaStream_t)stream);
-    return e == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
+    return waited(e, (cudaStream_t)stream);
 }
 
 k3moe_status k3moe_router_scores(const k3moe_config *cfg, int32_t T, const uint16_t *x,
@@ -269,7 +342,7 @@ k3moe_status k3moe_forward(const k3moe_config *cfg, int32_t T, const uint16_t *x
     cudaError_t e = launch_forward(*cfg, T, x, idx, weight, offsets, perm,
                                         static_cast<const uint8_t *>(expert_table), sh_w1, sh_w3,
                                         sh_w2, out, static_cast<uint8_t *>(ws), L, (cudaStream_t)stream);
-    return e == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
+    return waited(e, (cudaStream_t)stream);
 }
 
 static k3moe_status check_full(const k3moe_config *cfg, const k3moe_full_dims *fd)
@@ -332,7 +405,7 @@ k3moe_status k3moe_full_forward(const k3moe_config *cfg, const k3moe_full_dims *
                                 w_down, static_cast<const uint8_t *>(expert_table), norm_gain, w_up,
                                 sh_w1, sh_w3, sh_w2, idx, weight, offsets, perm, out,
                                 static_cast<uint8_t *>(ws), F, (cudaStream_t)stream);
-    return e == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
+    return waited(e, (cudaStream_t)stream);
 }
 
 static k3moe_status check_linear(const k3moe_linear_config *lc)
@@ -376,6 +449,7 @@ k3moe_status k3moe_linear(const k3moe_linear_config *lc, int32_t T, const uint16
     if (!ws || !aligned(ws, 256) || ws_bytes < kCtrOffset + kCtrBytes) return K3MOE_EWORKSPACE;
     const LinearArgs a{T, lc->n, lc->k, lc->act, lc->y_f32, x, x_stride, w, bias, residual,
                        residual ? residual_stride : 0, y, y_stride, static_cast<int32_t *>(ws)};
+    result_pending_begin((cudaStream_t)stream);
     return launch_linear(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
 }
 
@@ -429,6 +503,7 @@ k3moe_status k3moe_delta_rule(const k3moe_delta_config *dc, int32_t n_seq, int32
     const DeltaArgs a{n_seq, T, dc->n_heads, dc->n_qk_heads, dc->gate_dim, dc->qk_norm, dc->norm_eps,
                       dc->scale, seq_start, q, k, v, q_stride, k_stride, v_stride, g, beta, state_in,
                       state_out, n_slots, slots, out, static_cast<uint8_t *>(ws)};
+    result_pending_begin((cudaStream_t)stream);
     return launch_delta(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
 }
 

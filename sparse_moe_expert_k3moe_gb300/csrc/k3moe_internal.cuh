@@ -335,6 +335,13 @@ void timing_begin(const char *name, cudaStream_t s);
 void timing_end(const char *name, cudaStream_t s);
 void count_launch();
 
+// Whether the stream's latest call may still be writing its result when the next kernel of
+// the stream starts (k3moe_api.cu): begun by the mixer's calls before they launch, ended by calls that
+// wait first.
+void result_pending_begin(cudaStream_t s);
+void result_pending_end(cudaStream_t s);
+bool result_pending(cudaStream_t s);
+
 constexpr int64_t kMaxStride = 1ll << 32;                 // row strides of strided inputs, elements
 // ---- linear projection with its epilogue (k3moe_linear.cu)
 struct LinearArgs {
@@ -419,9 +426,10 @@ inline cudaError_t launch_forward(const k3moe_config &c, int T, const uint16_t *
                                   const uint8_t *table, const uint16_t *sh_w1, const uint16_t *sh_w3,
                                   const uint16_t *sh_w2, float *out, uint8_t *ws, const WsLayout &L,
                                   cudaStream_t s, bool x_is_input = true);
-// x_is_input: x is complete when the call is made (not written by the kernel launched just
-// before with programmatic dependent launch), so the mat-vec path may read it before its
-// wait for the routing.
+// x_is_input: x is complete when the call is made (not written by a kernel of the same call
+// launched just before with programmatic dependent launch), so the mat-vec path may read it
+// before its wait for the routing, unless the call before may still be writing it
+// (result_pending).
 cudaError_t launch_forward_gemv(const k3moe_config &c, int T, const uint16_t *x,
                                 const int32_t *idx, const float *weight, const int32_t *offsets,
                                 const int32_t *perm, const uint8_t *table, const uint16_t *sh_w1,
@@ -437,7 +445,7 @@ inline cudaError_t launch_forward(const k3moe_config &c, int T, const uint16_t *
     return L.gemm ? launch_forward_gemm(c, T, x, idx, weight, offsets, perm, table, sh_w1, sh_w3, sh_w2,
                                         out, ws, L, s)
                   : launch_forward_gemv(c, T, x, idx, weight, offsets, perm, table, sh_w1, sh_w3, sh_w2,
-                                        out, ws, L, s, x_is_input);
+                                        out, ws, L, s, x_is_input && !result_pending(s));
 }
 
 // ----------------------------------------------------------------------------------- device helpers

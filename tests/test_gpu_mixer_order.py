@@ -1,0 +1,122 @@
+"""The mixer's operators among the library's other calls: a call that follows reads what
+they wrote, whatever it may do before its own wait for them.
+
+The forward's mat-vec path converts its tokens ahead of its wait for the routing.  After a
+projection or a delta rule that writes these tokens it must not: here the tokens' buffer is
+poisoned before the call that writes them, so that one element read too early makes the
+output NaN, and the output is compared bit for bit with that of synchronised calls.
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+D, HEADS = 128, 8
+WIDTH = D * HEADS                       # of the experts' tokens
+LONG = 32768                            # the projection's input width: it runs for tens of microseconds
+
+
+@pytest.fixture(scope="module")
+def k3():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_moe_expert_k3moe_gb300 import build as kbuild
+    kbuild.build()
+    import sparse_moe_expert_k3moe_gb300 as k3
+    return k3
+
+
+def make_layer(k3, T, n_shared):
+    """Random experts of moderate weights."""
+    E, f = 64, 256
+    g = torch.Generator("cuda").manual_seed(T)
+    m = k3.MoELayer(k3.k3moe_config(d=WIDTH, f=f, n_experts=E, top_k=4, n_shared=n_shared), T)
+    codes = lambda *s: torch.randint(0, 256, s, generator=g, dtype=torch.uint8, device="cuda")  # noqa: E731
+    scale = lambda *s: torch.full(s, 121, dtype=torch.uint8, device="cuda")  # noqa: E731
+    w = lambda *s: (torch.randn(*s, generator=g, device="cuda") / s[-1] ** 0.5).bfloat16()  # noqa: E731
+    m.pack_experts(0, E, codes(E, f, WIDTH // 2), scale(E, f, WIDTH // 32), codes(E, f, WIDTH // 2),
+                   scale(E, f, WIDTH // 32), codes(E, WIDTH, f // 2), scale(E, WIDTH, f // 32))
+    m.w_router = w(E, WIDTH)
+    if n_shared:
+        m.sh_w1, m.sh_w3, m.sh_w2 = w(n_shared, f, WIDTH), w(n_shared, f, WIDTH), w(n_shared, WIDTH, f)
+    return m
+
+
+def writers(k3, T):
+    """Calls that write the tokens x [T][WIDTH]: a projection of a long row, and the delta
+    rule of one sequence of T tokens, or of single tokens."""
+    h = torch.randn(T, LONG, device="cuda").bfloat16()
+    proj = k3.Linear(k3.k3moe_linear_config(WIDTH, LONG), T)
+    proj.w = (torch.randn(WIDTH, LONG, device="cuda") / LONG ** 0.5).bfloat16()
+    mix = k3.DeltaRule(k3.k3moe_delta_config(HEADS, HEADS, gate_dim=D), T, T)
+    q, k, v = (torch.randn(T, HEADS, D, device="cuda").bfloat16() for _ in range(3))
+    gate, beta = torch.full((T, HEADS, D), -0.1, device="cuda"), torch.rand(T, HEADS, device="cuda")
+    pool, after = torch.randn(T, HEADS, D, D, device="cuda"), torch.empty(T, HEADS, D, D, device="cuda")
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = lambda x: x.view(T, HEADS, D)  # noqa: E731
+    return {"linear": lambda x: proj(h, x),
+            "delta": lambda x: mix(q, k, v, gate, beta, out(x), pool, after),
+            "sequence": lambda x: mix(q, k, v, gate, beta, out(x), pool, after, slots=one)}
+
+
+@pytest.mark.parametrize("n_shared", [0, 2])
+@pytest.mark.parametrize("T", [1, 3, 8, 24])
+def test_forward_reads_what_the_mixer_wrote(k3, T, n_shared):
+    layer = make_layer(k3, T, n_shared)
+    x = torch.randn(T, WIDTH, device="cuda").bfloat16()
+    layer.route(x)                                        # the routing is there before, as after a wider router
+    out = torch.empty(T, WIDTH, device="cuda")
+    for name, write in writers(k3, T).items():
+        write(x)
+        torch.cuda.synchronize()
+        want_x = x.clone()
+        torch.cuda.synchronize()
+        want = layer.forward(x, out) or out.clone()
+        torch.cuda.synchronize()
+        assert torch.isfinite(want).all()
+        for _ in range(20):
+            x.fill_(float("nan"))
+            write(x)
+            layer.forward(x, out)
+            assert torch.equal(x, want_x) and torch.equal(out, want), name
+        # in a captured graph, where the calls are launched back to back
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            x.fill_(float("nan"))
+            write(x)
+            layer.forward(x, out)
+            layer.forward(x, out)                         # and once more on the same tokens
+        for _ in range(20):
+            out.fill_(float("nan"))
+            graph.replay()
+            assert torch.equal(x, want_x) and torch.equal(out, want), name
+    assert k3.k3moe_device_status(layer.ws) == (0, 0)
+
+
+def test_forward_after_a_capture_that_routed(k3):
+    """What a capture recorded says nothing of the calls around it: a projection before the
+    capture, on its stream, is still waited for after it."""
+    T = 8
+    layer, write = make_layer(k3, T, 1), writers(k3, T)["linear"]
+    x = torch.randn(T, WIDTH, device="cuda").bfloat16()
+    layer.route(x)
+    write(x)
+    out, other, dst = torch.empty(T, WIDTH, device="cuda"), x.clone(), torch.empty(T, WIDTH, device="cuda")
+    spare = make_layer(k3, T, 1)
+    want = layer.forward(x, out) or out.clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        for _ in range(10):
+            x.fill_(float("nan"))
+            write(x)
+            graph = torch.cuda.CUDAGraph()
+            graph.capture_begin()
+            spare.route(other)
+            spare.forward(other, dst)
+            graph.capture_end()
+            layer.forward(x, out)
+            s.synchronize()
+            assert torch.equal(out, want)
