@@ -1193,8 +1193,8 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
                 }
             }
             tmem_wait_st();
+            const float dec = kChannel ? 0.0f : sc[kRecDec - t0];     // the stage's last read: it is given back after this arrival
             arrive(sh.u_ready);
-            const float dec = kChannel ? 0.0f : sc[kRecDec - t0];
             if (!wait(sh.d4_full, c)) break;
             tc_fence_after();
 #pragma unroll
