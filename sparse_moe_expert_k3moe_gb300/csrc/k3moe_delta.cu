@@ -1454,12 +1454,15 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             }
             if (lane == 0) prefetch_bulk(record(c), kRecBytes);
         };
-        for (int c = 0; c < nc; c++) {
-            if (c >= kStages && !wait(sh.in_free[c % kStages], c / kStages - 1)) break;
-            if (lane == 0) load(c);
-            if (kChannel && c + 1 < nc) ahead(c + 1);
+        int loaded = 0;
+        for (; loaded < nc; loaded++) {
+            if (loaded >= kStages && !wait(sh.in_free[loaded % kStages], loaded / kStages - 1)) break;
+            if (lane == 0) load(loaded);
+            if (kChannel && loaded + 1 < nc) ahead(loaded + 1);
             __syncwarp();
         }
+        // the block's shared memory stays until its last copies have landed, when another role gave up too
+        for (int c = max(0, loaded - kStages); c < loaded; c++) wait(sh.in_full[c % kStages], c / kStages);
     }
     tc_fence_before();
     __syncthreads();
