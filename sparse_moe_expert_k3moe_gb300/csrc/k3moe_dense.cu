@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kDnThreads, 1) dense_tc_kernel(const DenseArgs
 constexpr int kRowsThreads = 256;
 
 template <int NT>
-__global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DenseArgs a, const uint16_t *__restrict__ x,
+__global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DenseArgs a, const uint16_t *x,
                                                                  const uint16_t *__restrict__ w,
                                                                  const uint16_t *__restrict__ w3)
 {
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kRowsThreads) dense_rows_kernel(const DenseArg
     const bool gated = a.epi == kDenseSitu;
     for (int q = threadIdx.x; q < NT * nchunk; q += kRowsThreads) {
         const int t = q / nchunk, c = q % nchunk;
-        xsm[q] = t < a.T ? __ldg(reinterpret_cast<const uint4 *>(x + (size_t)t * a.K) + c) : make_uint4(0, 0, 0, 0);
+        xsm[q] = t < a.T ? *(reinterpret_cast<const uint4 *>(x + (size_t)t * a.K) + c) : make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

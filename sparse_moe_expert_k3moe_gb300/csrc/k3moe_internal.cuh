@@ -309,6 +309,8 @@ inline FullLayout full_layout(const k3moe_config &c, int hidden, int T)
 // previous kernel in the stream has completed and its writes are visible, before touching
 // memory, so the kernel may be launched early (launch_pdl) and its launch latency overlaps
 // the previous kernel.  pdl_trigger() then lets the next kernel launch the same way.
+// What the kernel before may write is then read by plain loads: not through __ldg or a const
+// __restrict__ pointer, which promise data that nobody writes while the kernel is there.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

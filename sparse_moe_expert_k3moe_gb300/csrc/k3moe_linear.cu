@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kLrThreads) linear_rows_kernel(const LinearArg
     const int nchunk = a.K / 8;
     for (int q = threadIdx.x; q < NT * nchunk; q += kLrThreads) {
         const int t = q / nchunk, c = q % nchunk;
-        xsm[q] = t < a.T ? __ldg(reinterpret_cast<const uint4 *>(a.x + (size_t)t * a.x_stride) + c)
+        xsm[q] = t < a.T ? *(reinterpret_cast<const uint4 *>(a.x + (size_t)t * a.x_stride) + c)
                          : make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kLrThreads) linear_rows_kernel(const LinearArg
                 }
             }
         }
-        const float b = a.bias ? __ldg(a.bias + n) : 0.0f;
+        const float b = a.bias ? a.bias[n] : 0.0f;
 #pragma unroll
         for (int t = 0; t < NT; t++) {
 #pragma unroll
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
             int rb, tt;
             tile_of(i, &rb, &tt);
             const int col = rb * 128 * CG + (int)rank * 128 * (CG - 1) + 32 * q + lane;
-            const float b = a.bias && col < a.N ? __ldg(a.bias + col) : 0.0f;
+            const float b = a.bias && col < a.N ? a.bias[col] : 0.0f;
             const int t0 = tt * tl.bn, ncols = min(tl.bn, a.T - t0);
             const int buf = n & 1;
             if (!mb_wait_warp(&acc_full[buf], (n >> 1) & 1u)) { timeout(); break; }
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     if (j < w) {
-                        const float b = a.bias ? __ldg(a.bias + col + j) : 0.0f;
+                        const float b = a.bias ? a.bias[col + j] : 0.0f;
                         with_act(a.act, [&](auto act) { lin_put(a, t0 + c, col + j, lin_act<decltype(act)::value>(z[j] + b) + r[j]); });
                     }
             }

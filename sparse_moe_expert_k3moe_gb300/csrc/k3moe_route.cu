@@ -139,7 +139,7 @@ __device__ __forceinline__ float exact_logit_warp(const uint4 *xs, const uint4 *
 // -------------------------------------------------------------------------------- exact scores
 // grid (ceil(E / 4), ceil(T / 8)); block y owns tokens [8 y, 8 y + 8).
 __global__ void __launch_bounds__(kScoreWarps * 32) router_scores_kernel(
-    int T, int d, int E, const uint16_t *__restrict__ x, const uint16_t *__restrict__ wr,
+    int T, int d, int E, const uint16_t *x, const uint16_t *__restrict__ wr,
     const float *__restrict__ bias, float *__restrict__ sc_out, float *__restrict__ ch_out)
 {
     pdl_wait();
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) router_scores_kernel(
         __syncthreads();
         for (int q = threadIdx.x; q < nt * nchunk; q += blockDim.x) {
             const int i = q / nchunk, c = q % nchunk;
-            xs[i * nchunk + c] = __ldg(reinterpret_cast<const uint4 *>(x + (size_t)(t0 + i) * d) + c);
+            xs[i * nchunk + c] = *(reinterpret_cast<const uint4 *>(x + (size_t)(t0 + i) * d) + c);
         }
         __syncthreads();
         // one token at a time (a loop, not unrolled: the unrolled body of all tokens would
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kSelThreads) router_select_kernel(TopkArgs a)
     const uint4 *xg = reinterpret_cast<const uint4 *>(a.x + (size_t)t * a.d);
     float ss = 0.0f;
     for (int q = i; q < nchunk; q += kSelThreads) {
-        const uint4 v = __ldg(xg + q);
+        const uint4 v = xg[q];
         xs[q] = v;
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

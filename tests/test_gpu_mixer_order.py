@@ -120,3 +120,62 @@ def test_forward_after_a_capture_that_routed(k3):
             layer.forward(x, out)
             s.synchronize()
             assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T,n_seq", [(1, 1), (2, 2), (40, 1), (300, 2), (2000, 1)])
+def test_a_chain_of_calls_reads_this_turns_results(k3, T, n_seq):
+    """Projections, the delta rule, a projection and the router back to back on buffers that are
+    used again: every turn's inputs differ, and nothing of the turn before is read."""
+    heads = 4
+    d = heads * D
+    lin = lambda n, k, act, f32=False: k3.Linear(k3.k3moe_linear_config(n, k, act, f32), T)  # noqa: E731
+    qkv, gate, step, proj = lin(3 * d, 512, "silu"), lin(d, 512, "logsigmoid", True), lin(heads, 512, "sigmoid", True), lin(d, d, "none")
+    for op in (qkv, gate, step, proj):
+        op.w = (torch.randn(op.lc.n, op.lc.k, device="cuda") / op.lc.k ** 0.5).bfloat16()
+    gate.bias = torch.empty(d, device="cuda")
+    mix = k3.DeltaRule(k3.k3moe_delta_config(heads, heads, gate_dim=D), n_seq, T)
+    moe = k3.MoELayer(k3.k3moe_config(d=d, f=128, n_experts=32, top_k=4, n_shared=0), T)
+    moe.w_router = (torch.randn(32, d, device="cuda") / d ** 0.5).bfloat16()
+    start = torch.tensor([T * i // n_seq for i in range(n_seq + 1)], dtype=torch.int32, device="cuda")
+    new = lambda n, kind=torch.bfloat16: torch.empty(T, n, dtype=kind, device="cuda")  # noqa: E731
+    x, a, o, y = new(512), new(3 * d), new(d), new(d)
+    g, b, bias = new(d, torch.float32), new(heads, torch.float32), torch.empty(d, device="cuda")
+    state = mix.new_state(n_seq)
+
+    def calls(meet):
+        steps = [lambda: gate.bias.copy_(bias), lambda: qkv(x, a), lambda: gate(x, g), lambda: step(x, b),
+                 lambda: mix(*(t.view(T, heads, D) for t in (a[:, :d], a[:, d:2 * d], a[:, 2 * d:])), g.view(T, heads, D), b,
+                             o.view(T, heads, D), state, state, seq_start=start),
+                 lambda: proj(o, y), lambda: moe.route(y)]
+        for s in steps:
+            s()
+            if meet:
+                torch.cuda.synchronize()
+
+    outs = (a, g, b, o, y, state, moe.idx, moe.weight)
+    turns = [(torch.randn(T, 512, device="cuda").bfloat16(), 3 + torch.randn(d, device="cuda")) for _ in range(6)]
+    state.zero_()
+    want = []
+    for xt, bt in turns:
+        x.copy_(xt)
+        bias.copy_(bt)
+        calls(True)
+        want.append([t.clone() for t in outs])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        calls(False)
+    for run in (graph.replay, lambda: calls(False)):
+        state.zero_()
+        for (xt, bt), ref in zip(turns, want):
+            x.copy_(xt)
+            bias.copy_(bt)
+            for t in (a, g, b, o, y):
+                t.fill_(float("nan"))
+            run()
+            got = [t.clone() for t in outs]
+            for i, (u, v) in enumerate(zip(got, ref)):
+                assert torch.equal(u, v), i
+    for op in (qkv, gate, step, proj, mix, moe):
+        assert k3.k3moe_device_status(op.ws) == (0, 0)
