@@ -1165,6 +1165,14 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
             }
             tmem_wait_st();
             arrive(sh.r_ready);
+            if (!kChannel && n < kC) {
+                // K's rows past the sequence's end are another's, or nobody's: U is zero there, but zero times a NaN
+                // or an infinity is not.  K S has read them, K^T U has yet to
+#pragma unroll 1
+                for (int i = threadIdx.x; i < 2 * 8 * (kC - n); i += kChChain * 32)
+                    *reinterpret_cast<uint4 *>(stage(c) + (i & 1) * 2 * kChBox + n * 128 + (i >> 1) * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+            }
             if (!wait(sh.d2_full, c)) break;
             tc_fence_after();
             {

@@ -77,3 +77,41 @@ def test_every_chunk_decays_by_its_own(k3, T, channel):
         op(q, k, v, g, beta, out, S0, state, slots=one)
         check(out, state[0], q, k, v, g, beta, S0[0], f"{T} tokens")
     assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+# In a call's tokens: sequences in chunks whose last one holds 1, 15, 16, 17, 63 or all of its 64
+# tokens; None: tokens of no sequence.
+AROUND = [[65, None], [70, 65, 90, None], [64, 33, None], [127, 128, 129, 15, None], [80, 81, 79, 48, 47, 49, None],
+          [64 * 40 + 1, None]]
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf"), 3e38])
+@pytest.mark.parametrize("channel", [False, True])
+@pytest.mark.parametrize("lens", AROUND, ids=str)
+def test_nothing_behind_a_sequence_takes_part(k3, lens, channel, value):
+    """Every other sequence, the tokens after the last one and the tokens before the first are
+    of values that no arithmetic survives; the sequences between them do not know."""
+    H, Hq, before = 4, 2, 5
+    n = len(lens) - 1
+    sizes = [x if x else 70 for x in lens]
+    T = before + sum(sizes)
+    t0 = [before + sum(sizes[:i]) for i in range(n + 1)]
+    q, k, v, g, beta = inputs(T, H, channel, n)
+    q, k = q[:, :Hq].clone(), k[:, :Hq].clone()
+    spoiled = torch.ones(T, dtype=torch.bool, device="cuda")
+    for i in range(0, n, 2):
+        spoiled[t0[i]:t0[i] + sizes[i]] = False
+    for t in (q, k, v, g, beta):
+        t[spoiled] = value
+    if value == value:
+        g[spoiled] = -value if value > 0 else value       # a decay's logarithm is not above zero
+    op = k3.DeltaRule(k3.k3moe_delta_config(H, Hq, gate_dim=D if channel else 1), n, T)
+    S0 = 0.5 * torch.randn(n, H, D, D, device="cuda")
+    out, state = torch.full((T, H, D), 7.0, dtype=torch.bfloat16, device="cuda"), torch.empty_like(S0)
+    op(q, k, v, g, beta, out, S0, state, seq_start=torch.tensor(t0, dtype=torch.int32, device="cuda"))
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
+    heads = lambda t: t.repeat_interleave(H // Hq, 1)  # noqa: E731
+    for i in range(0, n, 2):
+        s = slice(t0[i], t0[i] + sizes[i])
+        check(out[s], state[i], heads(q[s]), heads(k[s]), v[s], g[s], beta[s], S0[i], f"sequence {i}")
+    assert (out[:before] == 7).all() and (out[t0[n]:] == 7).all()
