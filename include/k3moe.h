@@ -305,7 +305,9 @@ k3moe_status k3moe_full_forward(const k3moe_config *cfg, const k3moe_full_dims *
  * gated delta rule between them (the recurrence of the README's k3_kda_step, Part II,
  * the layer's first half; its MoE half is the block above). */
 
-/* Activations of k3moe_linear, on z = x W^T + bias in float. */
+/* Activations of k3moe_linear, on z = x W^T + bias in float, each within (10 + 1.2 |z|) 2^-23 of
+ * its own value (GELU (10 + 0.7 z^2) 2^-23: about what a rounding of z makes of a tail), or
+ * zero below 2^-119. */
 typedef enum k3moe_act {
     K3MOE_ACT_NONE = 0,
     K3MOE_ACT_RELU = 1,        /* max(z, 0) */

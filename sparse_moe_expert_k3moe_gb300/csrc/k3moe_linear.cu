@@ -18,12 +18,13 @@
 namespace k3moe {
 namespace {
 
-// The activations in float, branch-free (256 of them a thread in a tile's epilogue), each
-// within a few 2^-22 of max(|z|, 1) or better:
-//   sigmoid  1 / (1 + e), e = exp(-z); past z = -88 e is infinite and the result 0;
-//   gelu     the complementary error function by Abramowitz and Stegun 7.1.26,
-//            erfc(s) = (a1 t + .. + a5 t^5) exp(-s^2), t = 1 / (1 + p s), s >= 0 (absolute
-//            error at most 1.5e-7), so that the far negative side is a product, not a difference;
+// The activations in float, branch-free (256 of them a thread in a tile's epilogue), each within a few
+// units of its own last place, and in a tail within as many as a rounding of z would make of it:
+//   sigmoid  1 / (1 + e), e = exp(-z); past z = -87 the division gives 0;
+//   gelu     z Phi(z), with Phi(-|z|) = exp(-z^2 / 2) R(t), t = 1 / (1 + 0.3 |z|): R = t times a
+//            polynomial, fitted here to least relative error over |z| <= 14 (1.5e-7; all of the float
+//            arithmetic within (4 + 0.63 z^2) 2^-23), so that the far negative side is a product of relative
+//            accuracy, not a difference;
 //   logsigmoid  min(z, 0) - log(1 + e), e = exp(-|z|), with log(1 + e) = 2 atanh(s),
 //            s = e / (2 + e) <= 1/3, by atanh's series to s^15: relative error 2e-9 and the rounding.
 template <int ACT>
@@ -33,14 +34,18 @@ __device__ __forceinline__ float lin_act(float z)
     if (ACT == K3MOE_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
     if (ACT == K3MOE_ACT_SIGMOID) return __fdividef(1.0f, 1.0f + __expf(-z));
     if (ACT == K3MOE_ACT_GELU) {
-        const float s = fabsf(z) * 0.70710678118654752f;
-        const float t = __fdividef(1.0f, fmaf(0.3275911f, s, 1.0f));
-        float p = fmaf(1.061405429f, t, -1.453152027f);
-        p = fmaf(p, t, 1.421413741f);
-        p = fmaf(p, t, -0.284496736f);
-        p = fmaf(p, t, 0.254829592f);
-        const float half_erfc = 0.5f * p * t * __expf(-s * s);
-        return z * (z > 0.0f ? 1.0f - half_erfc : half_erfc);
+        const float t = __fdividef(1.0f, fmaf(0.3f, fabsf(z), 1.0f));
+        float p = fmaf(0.03567477f, t, -0.15720306f);
+        p = fmaf(p, t, 0.20635349f);
+        p = fmaf(p, t, -0.053683624f);
+        p = fmaf(p, t, 0.12856162f);
+        p = fmaf(p, t, 0.09991349f);
+        p = fmaf(p, t, 0.12075396f);
+        p = fmaf(p, t, 0.1196293f);
+        float e;                                             // exp(-z^2 / 2), as a power of 2
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * z * -0.72134752f));
+        const float tail = p * t * e;
+        return z * (z > 0.0f ? 1.0f - tail : tail);
     }
     if (ACT == K3MOE_ACT_LOGSIGMOID) {
         const float e = __expf(-fabsf(z));
