@@ -1536,19 +1536,17 @@ cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
         !map16s(&mv, a.v, (uint64_t)a.T, (uint64_t)a.H * kD, (uint64_t)a.v_stride, kC))
         return cudaErrorInvalidValue;
     using Shape = ChunkShape<kChannel>;
-    static bool ready = false;
-    if (!ready) {
+    const cudaError_t allowed = once_a_device([] {
         // the shares of setmaxnreg are of the launch's registers: with another count they would never be there
         cudaFuncAttributes fa{};
         if (kChannel && (cudaFuncGetAttributes(&fa, delta_chunk_kernel<kChannel>) != cudaSuccess || fa.numRegs != kChRegs))
             return cudaErrorInvalidConfiguration;
-        cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<kChannel>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::smem);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(delta_prepare_kernel<kChannel>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)pp_smem(kChannel));
-        if (e != cudaSuccess) return e;
-        ready = true;
-    }
+        const cudaError_t e = cudaFuncSetAttribute(delta_chunk_kernel<kChannel>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::smem);
+        return e != cudaSuccess ? e
+                                : cudaFuncSetAttribute(delta_prepare_kernel<kChannel>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (int)pp_smem(kChannel));
+    });
+    if (allowed != cudaSuccess) return allowed;
     int ends[kMaxStretches];
     const int stretches = plan_stretches<kChannel>(a, ends);
     cudaError_t err = cudaSuccess;

@@ -12,6 +12,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "k3moe_internal.cuh"
 #include "k3moe_tc_warp.cuh"
 
@@ -582,10 +584,11 @@ template <int NT>
 cudaError_t launch_rows(const LinearArgs &a, cudaStream_t s)
 {
     const size_t smem = (size_t)NT * a.K * 2;
-    static size_t smem_set = 48 * 1024;
-    if (smem > smem_set) {
-        cudaFuncSetAttribute(linear_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLrSmem);
-        smem_set = kLrSmem;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = once_a_device([] {
+            return cudaFuncSetAttribute(linear_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLrSmem);
+        });
+        if (e != cudaSuccess) return e;
     }
     static thread_local size_t asked = 0;                     // the occupancy of the last shared-memory size
     static thread_local int per_sm = 0;
@@ -612,8 +615,9 @@ constexpr double kLtRate = 48.0;      // bytes a clock an SM
 
 template <int CG> cudaError_t allow_tc()
 {
-    static const cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kLtRing);
-    return e;
+    return once_a_device([] {
+        return cudaFuncSetAttribute(linear_tc_kernel<CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kLtRing);
+    });
 }
 
 // Blocks at work at once in clusters of P: a cluster stays within a group of SMs, so that
@@ -621,8 +625,8 @@ template <int CG> cudaError_t allow_tc()
 // 2048 in 16 of them took 10.9 us, in two goes, and in 16 of P = 6 6.2).
 int lin_slots(int P)
 {
-    static int known[9];
-    int &n = known[P];
+    static std::atomic<int> known[9];
+    int n = known[P].load(std::memory_order_relaxed);
     if (n == 0) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(num_sms() / P * P));
@@ -637,6 +641,7 @@ int lin_slots(int P)
         int fit = 0;
         if (P > 1 && (allow_tc<1>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&fit, linear_tc_kernel<1>, &cfg) != cudaSuccess)) fit = 0;
         n = (fit > 0 ? fit : num_sms() / P) * P;
+        known[P].store(n, std::memory_order_relaxed);
     }
     return n;
 }

@@ -119,5 +119,20 @@ inline bool map16s(CUtensorMap *m, const void *base, uint64_t rows, uint64_t col
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// f's result, from the first call on the current device (a kernel's attributes are the
+// device's), whichever threads call; f's type tells one use from another.
+template <typename F> cudaError_t once_a_device(F f)
+{
+    constexpr int kMaxDevices = 64;
+    static std::once_flag flag[kMaxDevices];
+    static cudaError_t result[kMaxDevices];
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::call_once(flag[dev], [&] { result[dev] = f(); });
+    return result[dev];
+}
+
 }  // namespace
 }  // namespace k3moe

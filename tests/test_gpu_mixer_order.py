@@ -6,6 +6,10 @@ projection or a delta rule that writes these tokens it must not: here the tokens
 poisoned before the call that writes them, so that one element read too early makes the
 output NaN, and the output is compared bit for bit with that of synchronised calls.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -179,3 +183,53 @@ def test_a_chain_of_calls_reads_this_turns_results(k3, T, n_seq):
                 assert torch.equal(u, v), i
     for op in (qkv, gate, step, proj, mix, moe):
         assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+_THREADS = r"""
+import threading, torch
+import sparse_moe_expert_k3moe_gb300 as k3
+D, H, T = 128, 4, 100
+g = torch.Generator("cuda").manual_seed(1)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+x, w = {n: r(n, 16384).bfloat16() for n in (1, 2, 40, 700)}, r(512, 16384).bfloat16()
+q, k, v, beta, state = r(T, H, D).bfloat16(), r(T, H, D).bfloat16(), r(T, H, D).bfloat16(), r(T, H).sigmoid(), r(1, H, D, D)
+gates, one = {n: -r(T, H, n).abs() for n in (1, D)}, torch.zeros(1, dtype=torch.int32, device="cuda")
+n = 8
+results, meet = [None] * n, threading.Barrier(n)
+
+def go(i):
+    out = []
+    with torch.cuda.stream(torch.cuda.Stream()):
+        ops = [k3.Linear(k3.k3moe_linear_config(512, 16384), m) for m in x]
+        mixes = [k3.DeltaRule(k3.k3moe_delta_config(H, H, gate_dim=G), 1, T) for G in gates]
+        ys = [torch.zeros(m, 512, dtype=torch.bfloat16, device="cuda") for m in x]
+        outs = [(torch.zeros_like(v), torch.zeros_like(state)) for _ in gates]
+        torch.cuda.synchronize()
+        if n > 1:
+            meet.wait()
+        for op, y, a in zip(ops, ys, x.values()):
+            op.w = w
+            op(a, y)
+        for m, gate, (o, s) in zip(mixes, gates.values(), outs):
+            m(q, k, v, gate, beta, o, state, s, slots=one)
+        torch.cuda.synchronize()
+    results[i] = ys + [t for pair in outs for t in pair]
+
+threads = [threading.Thread(target=go, args=(i,)) for i in range(n)]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join()
+for other in results[1:]:
+    assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+assert all(torch.isfinite(a).all() and a.any() for a in results[0])
+print("threads agree")
+"""
+
+
+def test_first_calls_from_several_threads(k3):
+    """The first calls of a process, eight threads at once, each on a stream of its own: what the
+    library sets up on first use is there for all."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _THREADS], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0 and "threads agree" in r.stdout, r.stdout + r.stderr
