@@ -336,9 +336,13 @@ k3moe_status k3moe_linear_workspace_bytes(const k3moe_linear_config *lc, int32_t
  *   residual [T][N] of y's type, row stride residual_stride >= N, or NULL; it may be y
  *            itself (same pointer and stride) but not overlap it otherwise
  *   y        [T][N] bf16 or f32 (lc->y_f32), row stride y_stride >= N, written
- * x and w 16-byte aligned; bias, residual and y aligned to their element.  T may be 0
- * (nothing written).  Every sum's order is fixed by T, N and K, so results repeat bit
- * for bit.  ws per k3moe_linear_workspace_bytes(T_max >= T). */
+ * x and w 16-byte aligned; bias, residual and y aligned to their element; y overlaps x,
+ * w and bias nowhere.  T may be 0 (nothing written).  Every sum's order is fixed by T, N and K,
+ * so results repeat bit for bit.  From three to five tokens on the sums are the tensor cores',
+ * which cut off what a float cannot hold after every 16 columns instead of rounding it: with
+ * f32 y and random data 1e-6 (K = 2000) to 1e-5 (K = 7168 and more) of y's 2-norm, several times
+ * what a float loop errs; for fewer tokens the sums are a float loop.
+ * ws per k3moe_linear_workspace_bytes(T_max >= T). */
 k3moe_status k3moe_linear(const k3moe_linear_config *lc, int32_t T, const uint16_t *x, int64_t x_stride,
                           const uint16_t *w, const float *bias, const void *residual,
                           int64_t residual_stride, void *y, int64_t y_stride, void *ws,
@@ -369,12 +373,15 @@ k3moe_status k3moe_delta_workspace_bytes(const k3moe_delta_config *dc, int32_t n
  *   S = S + k_t u^T
  *   o_t = scale * S^T q_t
  *   seq_start [n_seq+1] int32: sequence i has tokens seq_start[i] .. seq_start[i+1]-1
- *             (ascending within 0 .. T, lengths from 0 on).  NULL with T == n_seq means one token
+ *             (ascending within 0 .. T, lengths from 0 on; tokens before the first and behind the
+ *             last are of no sequence and need hold nothing).  NULL with T == n_seq means one token
  *             each (a decode step), and with n_seq == 1 one sequence of T tokens
  *   q, k      [T][n_qk_heads][D] bf16, v [T][H][D] bf16: heads dense within a token, token
  *             strides q_stride, k_stride, v_stride elements (multiples of 8), so that all
  *             three may be slices of one projection's rows
- *   g         [T][H][gate_dim] f32, the decay's logarithm (<= 0; -infinity forgets all)
+ *   g         [T][H][gate_dim] f32, the decay's logarithm (<= 0; -infinity forgets all).  Per
+ *             channel, one channel that sums to less than -60 over 16 tokens of a prompt makes its
+ *             chunk of 64 tokens many times slower
  *   beta      [T][H] f32
  *   state_in  [n_slots][H][D][D] f32 or NULL (every sequence starts from zero)
  *   state_out [n_slots][H][D][D] f32, written for the slots of the call's sequences, the
@@ -383,10 +390,15 @@ k3moe_status k3moe_delta_workspace_bytes(const k3moe_delta_config *dc, int32_t n
  *   out       [T][H][D] bf16, dense, written for the sequences' tokens
  * A sequence of length 0 has its state copied.  A slot outside [0, n_slots) sets
  * K3MOE_DEV_BAD_INDEX, a seq_start pair that is not ascending within [0, T] sets
- * K3MOE_DEV_BAD_OFFSETS, and that sequence is skipped.  States and every sum are float; out
- * is rounded once to bf16.  q, k, v 16-byte aligned, g and the states 16-byte aligned, out
- * 16-byte aligned.  T == 0 or n_seq == 0: with n_seq == 0 nothing is written.  ws per
- * k3moe_delta_workspace_bytes. */
+ * K3MOE_DEV_BAD_OFFSETS, and that sequence is skipped; one after it that shares tokens with an
+ * earlier sequence (as it may where the offsets fall) has no defined result.  States and every sum
+ * are float; out is rounded once to bf16.  A call's sequences are all walked in the same form, token
+ * by token or in chunks of 64 tokens, by their average length: prompts and single tokens are faster
+ * in calls of their own.  In chunks, a NaN or infinity in a token's k, v, g or beta can reach the
+ * outputs of up to 63 tokens before it in its own sequence (no other sequence's); token by token only
+ * those from it on.  q, k, v, g, out and the states 16-byte aligned; out and state_out overlap no input,
+ * but state_out may be state_in.  T may be 0 (the states are copied); n_seq may be 0 when T is (nothing
+ * is written).  ws per k3moe_delta_workspace_bytes. */
 k3moe_status k3moe_delta_rule(const k3moe_delta_config *dc, int32_t n_seq, int32_t T,
                               const int32_t *seq_start, const uint16_t *q, int64_t q_stride,
                               const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,

@@ -445,7 +445,9 @@ __device__ __forceinline__ void invert64(float *A, int warp, int lane)
 // two exponentials multiply to exp(G_t - G_i).  G counts from the half's start.  That holds
 // while no |G_t - m| passes 60 (a factor of 1e26 either way; a token's mean decay of 1e-2
 // over 16 tokens would reach it).  Where one does, the chunk's products are summed one by
-// one, the weight's logarithm accumulated backwards from t: slower, but exact for any decay.
+// one, the weight's logarithm accumulated backwards from t: exact for any decay, and 30
+// times slower (8192 tokens x 56 heads with one channel of each head at -5 a token: 19.9 ms
+// instead of 0.66).
 //
 // What bounds it: its barriers and instructions (half of the issue slots, a tenth of the tensor
 // cores, a quarter of the DRAM).  8192 tokens of eight sequences of 56 heads: 108 us (a block a
@@ -470,7 +472,9 @@ template <bool kChannel> struct PrepShared {
 
 // The record, first token and length of chunk `unit`, false when there is none; by a whole
 // warp.  All chunks at once (the call's only stretch): units are records.  A stretch: units
-// are its chunks of each sequence in turn.
+// are its chunks of each sequence in turn.  The sequences are searched from the first on, 32 at
+// a time, which thousands of them show (65536 tokens x 8 heads as 64 sequences 343 us, as 2048, each a
+// half-empty chunk and a chain of its own, 1454; per channel 626, 3025).
 __device__ __forceinline__ bool find_chunk(const DeltaArgs &a, int unit, int lane, int *rec, int *tok0, int *n)
 {
     auto range = [&](int s, int *s0, int *len) {
@@ -1485,7 +1489,10 @@ __global__ void __launch_bounds__(ChunkShape<kChannel>::threads, 1)
 // blocks have an SM each.  Recurrent against chunks, us, per head: 64 sequences x 32 heads of 16
 // tokens 153, 159 and of 18 173, 161; 8 x 32 heads of 14 23, 24 and of 18 29, 24; alone (one
 // sequence, 56 heads) of 22 13.3, 14.3 and of 26 15.5, 14.3.  Per channel: 37 x 56 heads of 26
-// tokens 252, 253 and of 28 268, 254; alone of 36 20.2, 20.6.
+// tokens 252, 253 and of 28 268, 254; alone of 36 20.2, 20.6.  All of these are sequences of equal
+// lengths, and the choice is the call's: with one prompt of 1000 tokens among 95 single ones (32 heads)
+// all go token by token, 657 us (per channel 719) where two calls take 69 and 63 (97 and 63); of 4000
+// tokens all in chunks, 287 (472), two calls 221 and 63 (323 and 63).
 constexpr int chunk_tokens_avg(bool channel, bool alone) { return channel ? (alone ? 37 : 27) : (alone ? 24 : 17); }
 
 // Where the chains leave SMs free, the sequences are walked in stretches: while the chains go
@@ -1493,8 +1500,8 @@ constexpr int chunk_tokens_avg(bool channel, bool alone) { return channel ? (alo
 // one before as preparing on those SMs is faster than the chains; the number of stretches is
 // the one with the least estimated time (microseconds: a chunk and head prepared on one SM,
 // a chain's chunk, and what one stretch more costs), ends[i] the chunk that ends the i-th.
-// In one and so, us: one sequence of 8192 tokens x 56 heads 524, 451, x 140 heads 666, 649;
-// per channel 856, 667 and 1256, 1218; 512 tokens x 56 heads per channel 61, 63.
+// In one and so, us: one sequence of 8192 tokens x 56 heads 513, 442, x 140 heads 659, 642;
+// per channel 841, 658 and 1241, 1205; 512 tokens x 56 heads per channel 61, 63.
 constexpr int kMaxStretches = 8;
 template <bool kChannel>
 int plan_stretches(const DeltaArgs &a, int (&ends)[kMaxStretches])
@@ -1567,8 +1574,8 @@ cudaError_t launch_chunks(const DeltaArgs &a, cudaStream_t s)
         if (err != cudaSuccess) return err;
         timing_begin("delta_chunk", s);
         // Beside a prepare the chains go in pairs, a cluster of two on the SMs of a TPC: a chain whose
-        // neighbour there runs other code takes a quarter to a half longer (8192 tokens x 56 heads: 451
-        // us in pairs, 490 singly; per channel 667, 793; two sequences 298, 323 and 547, 640).
+        // neighbour there runs other code takes a quarter to a half longer (8192 tokens x 56 heads: 442
+        // us in pairs, 488 singly; per channel 658, 782; two sequences 304, 331 and 548, 641).
         const bool pairs = stretches > 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(pairs ? (a.n_seq * a.H + 1) & ~1 : a.n_seq * a.H));

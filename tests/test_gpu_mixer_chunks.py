@@ -115,3 +115,35 @@ def test_nothing_behind_a_sequence_takes_part(k3, lens, channel, value):
         s = slice(t0[i], t0[i] + sizes[i])
         check(out[s], state[i], heads(q[s]), heads(k[s]), v[s], g[s], beta[s], S0[i], f"sequence {i}")
     assert (out[:before] == 7).all() and (out[t0[n]:] == 7).all()
+
+
+@pytest.mark.parametrize("channel", [False, True])
+@pytest.mark.parametrize("which", ["q", "k", "v", "g", "beta"])
+def test_a_spoiled_token_reaches_no_other_chunk_or_sequence(k3, which, channel):
+    """NaN in one token: with q that token's output alone, else nothing before the token's
+    chunk and nothing of another sequence; bit for bit the same as without it."""
+    H, lens, at = 2, [200, 130, 90], 200 + 64 + 20        # in the second sequence's second chunk
+    T = sum(lens)
+    given = dict(zip(("q", "k", "v", "g", "beta"), inputs(T, H, channel, 5)))
+    op = k3.DeltaRule(k3.k3moe_delta_config(H, H, gate_dim=D if channel else 1), 3, T)
+    start = torch.tensor([0, 200, 330, 420], dtype=torch.int32, device="cuda")
+    S0 = torch.randn(3, H, D, D, device="cuda")
+
+    def go():
+        out, state = torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda"), torch.empty_like(S0)
+        op(**given, out=out, state_in=S0, state_out=state, seq_start=start)
+        assert k3.k3moe_device_status(op.ws) == (0, 0)
+        return out, state
+
+    ref, ref_state = go()
+    given[which] = given[which].clone()
+    given[which][at] = float("nan")
+    out, state = go()
+    same = torch.ones(T, dtype=torch.bool, device="cuda")
+    same[at if which == "q" else slice(264, 330)] = False
+    same[at + 1:330] = which == "q"
+    assert torch.equal(out[same], ref[same]) and torch.isnan(out[at]).all()
+    keeps = [0, 1, 2] if which == "q" else [0, 2]
+    assert torch.equal(state[keeps], ref_state[keeps])
+    if which != "q":
+        assert torch.isnan(out[at:330]).flatten(1).any(1).all() and torch.isnan(state[1]).any()
