@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kLtThreads, CG == 1 ? 2 : 1) linear_tc_kernel(
                 }
             }
         }
-        if (bail && leader)                                          // wait (bounded) for the copies already issued
+        if (leader)                    // the last copies land (or a bounded wait gives up) before the block ends, whoever gave up
             for (uint32_t f = st > (uint32_t)nstg ? st - nstg : 0; f < st; f++)
                 mb_wait_warp(&full[f % nstg], (f / nstg) & 1u);
     } else if (warp == kLtWarpMma) {
