@@ -406,6 +406,162 @@ k3moe_status k3moe_delta_rule(const k3moe_delta_config *dc, int32_t n_seq, int32
                               float *state_out, int32_t n_slots, const int32_t *slots, uint16_t *out,
                               void *ws, size_t ws_bytes, k3moe_stream stream);
 
+/* ---- The latent attention's layer beside the block and the mixer: keys and values of all heads
+ * from one cached vector a token, c of `rank` columns and a rotated part r of `rope_dim`.  A layer is
+ *   k3moe_norm; k3moe_linear for the queries and for [c, r]; k3moe_latent_write;
+ *   prompts: k3moe_linear of the written rows' c for every head's keys and values, k3moe_latent_prompt;
+ *   single tokens and drafts: k3moe_head_linear of the queries into the latent,
+ *   k3moe_latent_attend over the cache, k3moe_head_linear of what it attended back to values;
+ *   k3moe_linear onto the residual, or k3moe_norm with the gate and the residual. */
+
+typedef enum k3moe_gate {
+    K3MOE_GATE_NONE = 0,
+    K3MOE_GATE_SIGMOID = 1,    /* 1 / (1 + exp(-z)) */
+    K3MOE_GATE_SILU = 2        /* z / (1 + exp(-z)) */
+} k3moe_gate;
+
+typedef struct k3moe_norm_config {
+    int32_t n;            /* columns N, a multiple of 8, 8 .. 16384 */
+    int32_t group;        /* columns the norm after the block goes over: N, or 64, 128 or 256 that divide N (each head's own) */
+    int32_t post_norm;    /* 1: x is normed; 0: as given */
+    int32_t pre_norm;     /* 1: the sum is normed for the next block */
+    int32_t gate;         /* K3MOE_GATE_* */
+    int32_t x_f32;        /* 1: x is f32; 0: bf16 */
+    int32_t sum_f32;      /* 1: residual and total are f32; 0: bf16 */
+    float eps;            /* finite and > 0 when one of the norms is on */
+    float alpha;          /* finite; multiplies the scale */
+} k3moe_norm_config;
+
+/* The norms after a block and before the next one, with the block's gate and residual scale, in
+ * one pass; for each of T rows
+ *   y = x / sqrt(mean(x^2) + eps) * post_gain     when post_norm; the mean over each group
+ *   y = y * act(gate)                             unless gate is NONE
+ *   total = residual + alpha * scale * y
+ *   out = total / sqrt(mean(total^2) + eps) * pre_gain    when pre_norm; the mean over the row
+ *   x, gate, residual, total, out [T][N], row strides in elements, multiples of 8 and >= N:
+ *             x by x_f32, residual and total by sum_f32, gate and out bf16
+ *   post_gain [group] f32 (NULL allowed without post_norm), scale [N] f32 or NULL (ones),
+ *   pre_gain  [N] f32 (NULL allowed without pre_norm)
+ *   residual  may be NULL (zeros); gate is NULL exactly when the config has none
+ *   total     may be NULL when pre_norm; out is NULL exactly when not pre_norm
+ * All in float, total and out each rounded once; out is of the sum before it is rounded.  total and
+ * out may be x, gate or residual themselves where pointer, stride and type are the same, but not each
+ * other, and overlap nothing otherwise.  All pointers 16-byte aligned.  T may be 0 (nothing written).
+ * A NaN or an infinity stays in its row. */
+k3moe_status k3moe_norm(const k3moe_norm_config *nc, int32_t T, const void *x, int64_t x_stride,
+                        const uint16_t *gate, int64_t gate_stride, const float *post_gain,
+                        const void *residual, int64_t residual_stride, const float *scale,
+                        void *total, int64_t total_stride, const float *pre_gain, uint16_t *out,
+                        int64_t out_stride, k3moe_stream stream);
+
+typedef struct k3moe_head_linear_config {
+    int32_t n_heads;      /* H, 1 .. 1024 */
+    int32_t n;            /* output columns of a head, 1 .. 8192 */
+    int32_t k;            /* input columns of a head, a multiple of 8, 8 .. 512 */
+} k3moe_head_linear_config;
+
+/* Workspace bytes k3moe_head_linear needs for any 0 <= T <= T_max (as k3moe_linear_workspace_bytes). */
+k3moe_status k3moe_head_linear_workspace_bytes(const k3moe_head_linear_config *hc, int32_t T_max, size_t *bytes);
+
+/* Every head's own projection, y[t][h] = W[h] x[t][h], accumulated in float and rounded once:
+ *   x  [T][H][K] bf16, strides from token to token and from head to head in elements
+ *   w  [H][N][K] bf16, dense
+ *   y  [T][H][N] bf16, strides likewise; written; overlaps x and w nowhere
+ * x's strides are multiples of 8, its heads (and y's) may be columns of wider ones, but no two of y's
+ * elements share an address: head strides >= K and >= N, token strides >= (H - 1) head strides + K (N).
+ * x and w 16-byte aligned, y to its element.  T may be 0 (nothing written).  Sums' orders are fixed, so
+ * results repeat bit for bit.  ws per k3moe_head_linear_workspace_bytes(T_max >= T). */
+k3moe_status k3moe_head_linear(const k3moe_head_linear_config *hc, int32_t T, const uint16_t *x,
+                               int64_t x_stride, int64_t x_head_stride, const uint16_t *w, uint16_t *y,
+                               int64_t y_stride, int64_t y_head_stride, void *ws, size_t ws_bytes,
+                               k3moe_stream stream);
+
+typedef enum k3moe_rope {
+    K3MOE_ROPE_NONE = 0,       /* r as it is */
+    K3MOE_ROPE_PAIRS = 1,      /* columns 2i and 2i + 1 are turned by position * inv_freq[i] */
+    K3MOE_ROPE_HALVES = 2      /* columns i and i + rope_dim / 2 are */
+} k3moe_rope;
+
+typedef struct k3moe_latent_config {
+    int32_t n_heads;      /* query heads H, 1 .. 1024 */
+    int32_t rank;         /* columns of c; must be 512 */
+    int32_t rope_dim;     /* columns of r; must be 64 */
+    int32_t key_dim;      /* a head's own key columns in the expanded form; must be 128 */
+    int32_t value_dim;    /* a head's value columns there; must be 128 */
+    int32_t page_size;    /* tokens a page of the cache: 16, 32, 64, 128 or 256 */
+    int32_t rope;         /* K3MOE_ROPE_* */
+    int32_t norm;         /* 1: the write norms c; 0: as given */
+    float norm_eps;       /* finite and > 0 when norm */
+    float scale;          /* finite and > 0; multiplies every score */
+    int32_t causal;       /* 1: the i-th of a sequence's n queries sees all its keys but the n - 1 - i last; 0: all */
+} k3moe_latent_config;
+
+/* K3MOE_OK when every field of *lc is in range, else K3MOE_EINVAL or K3MOE_ESHAPE. */
+k3moe_status k3moe_latent_validate_config(const k3moe_latent_config *lc);
+
+/* Workspace bytes the three calls below need for any of at most n_seq_max sequences and T_max query
+ * tokens (conventions as k3moe_workspace_bytes). */
+k3moe_status k3moe_latent_workspace_bytes(const k3moe_latent_config *lc, int32_t n_seq_max, int32_t T_max,
+                                          size_t *bytes);
+
+/* The rows of T tokens, into the cache and beside it, and the rotation of their queries:
+ *   row = [c / sqrt(mean(c^2) + norm_eps) * gain, r rotated by the token's position]
+ *   c         [T][rank + rope_dim] bf16, a token's [c, r]; row stride c_stride
+ *   gain      [rank] f32 (NULL allowed when norm == 0)
+ *   positions [T] int32 and inv_freq [rope_dim / 2] f64, finite, radians a position (NULL allowed without
+ *             rope); angles are taken modulo a turn in 64 bits, off by at most 2^-51 of the whole angle and 2^-24 of a turn
+ *   rows      [T][rank + rope_dim] bf16 or NULL, row stride rows_stride; it may be c itself
+ *   cache     [n_pages][page_size][rank + rope_dim] bf16 or NULL, and slots [T] int64: token t's row goes to row slots[t]
+ *             of the cache (page * page_size + place), nowhere when slots[t] < 0; other rows stay as they are.  A slot past the
+ *             cache sets K3MOE_DEV_BAD_INDEX and is not written; one that two tokens share holds either's row, or parts of both
+ *   q         [T][H][rope_dim] bf16 or NULL, the rotated columns of the queries, strides from token to token
+ *             and from head to head; q_rope likewise, written; it may be q itself
+ * Strides in elements, multiples of 8; pointers 16-byte aligned (positions 4, inv_freq and slots 8).  What is
+ * written overlaps no input but as said, nor each other.  T may be 0.  ws per k3moe_latent_workspace_bytes. */
+k3moe_status k3moe_latent_write(const k3moe_latent_config *lc, int32_t T, const uint16_t *c, int64_t c_stride,
+                                const float *gain, const int32_t *positions, const double *inv_freq,
+                                uint16_t *rows, int64_t rows_stride, uint16_t *cache, int32_t n_pages,
+                                const int64_t *slots, const uint16_t *q, int64_t q_stride, int64_t q_head_stride,
+                                uint16_t *q_rope, int64_t q_rope_stride, int64_t q_rope_head_stride, void *ws,
+                                size_t ws_bytes, k3moe_stream stream);
+
+/* Attention in the absorbed form, over the cached rows of n_seq sequences, T query tokens in all:
+ *   s_j = scale * q . row_j,   lse = log(sum_j exp(s_j)),   out = sum_j exp(s_j - lse) c_j
+ *   seq_start [n_seq+1] int32: sequence i's queries are tokens seq_start[i] .. seq_start[i+1]-1 (as k3moe_delta_rule's,
+ *             NULL likewise: one token each, or one sequence)
+ *   q         [T][H][rank + rope_dim] bf16, strides from token to token and from head to head, multiples of 8
+ *   cache     [n_pages][page_size][rank + rope_dim] bf16
+ *   pages     [n_seq][max_pages] int32: the pages that hold sequence i's rows in order; what lies behind the last of its
+ *             kv_len[i] rows is not read
+ *   kv_len    [n_seq] int32, rows of the sequence with its queries' own, 0 .. max_pages * page_size
+ *   out       [T][H][rank] bf16, dense; lse [T][H] f32 or NULL; written for the sequences' tokens alone
+ * A query that sees no row has zeros and minus infinity.  A page outside [0, n_pages) sets K3MOE_DEV_BAD_INDEX and its
+ * rows read as zeros; a seq_start pair that is not ascending within [0, T], or a kv_len out of range, sets
+ * K3MOE_DEV_BAD_OFFSETS and the sequence is skipped; one that shares tokens with another has no defined result.  Scores, sums
+ * and outputs are float, the weights exp(s - m) are rounded to bf16 for their product with c, out once.  Rows that a query
+ * does not see do not reach it, whatever they hold.  q, cache and out 16-byte aligned, the others to their element; out and
+ * lse overlap nothing.  T may be 0.  ws per k3moe_latent_workspace_bytes; calls that share one run on one stream. */
+k3moe_status k3moe_latent_attend(const k3moe_latent_config *lc, int32_t n_seq, int32_t T, const int32_t *seq_start,
+                                 const uint16_t *q, int64_t q_stride, int64_t q_head_stride, const uint16_t *cache,
+                                 int32_t n_pages, const int32_t *pages, int32_t max_pages, const int32_t *kv_len,
+                                 uint16_t *out, float *lse, void *ws, size_t ws_bytes, k3moe_stream stream);
+
+/* Attention in the expanded form: S tokens of keys and values of every head for T query tokens, packed:
+ *   s_j = scale * q . [k_j, r_j],   lse = log(sum_j exp(s_j)),   out = sum_j exp(s_j - lse) v_j
+ *   seq_start [n_seq+1] int32 as above; kv_start [n_seq+1] int32 likewise for the S tokens, NULL with S == T for the
+ *             queries' own
+ *   q         [T][H][key_dim + rope_dim] bf16
+ *   kv        [S][H][key_dim + value_dim] bf16: a head's keys, then its values
+ *   rope_key  [S][rope_dim] bf16, r of all heads, row stride rope_stride
+ *   out       [T][H][value_dim] bf16, dense; lse [T][H] f32 or NULL; written for the sequences' tokens alone
+ * Strides from token to token (q_stride, kv_stride, rope_stride) and from head to head, multiples of 8.  A query that sees
+ * no key, bad offsets, rounding and what is not seen as k3moe_latent_attend's.  q, kv, rope_key and out 16-byte aligned. */
+k3moe_status k3moe_latent_prompt(const k3moe_latent_config *lc, int32_t n_seq, int32_t T, int32_t S,
+                                 const int32_t *seq_start, const int32_t *kv_start, const uint16_t *q,
+                                 int64_t q_stride, int64_t q_head_stride, const uint16_t *kv, int64_t kv_stride,
+                                 int64_t kv_head_stride, const uint16_t *rope_key, int64_t rope_stride, uint16_t *out,
+                                 float *lse, void *ws, size_t ws_bytes, k3moe_stream stream);
+
 /* Synchronises `stream`, returns the device status word of `ws` in *code,
  * and clears it: the report of the README's rule that corruption is counted,
  * never silent (kimi-k3-in-c README, Part II, section 9, the k3_moe listing's

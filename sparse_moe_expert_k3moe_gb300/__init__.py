@@ -2,7 +2,10 @@
 full-width Stable LatentMoE block around it (``k3moe_full_forward``, ``MoEBlock``);
 and the token mixer beside the block: linear projections with their epilogue
 (``k3moe_linear``, ``Linear``) and the gated delta rule (``k3moe_delta_rule``,
-``DeltaRule``).
+``DeltaRule``); and the latent attention's layer beside both: norms around a block
+(``k3moe_norm``, ``Norm``), each head's own projection (``k3moe_head_linear``,
+``HeadLinear``), the latent cache's write and attention in the absorbed and the expanded form
+(``k3moe_latent_write``, ``k3moe_latent_attend``, ``k3moe_latent_prompt``, ``LatentAttention``).
 
 A thin ctypes binding over ``libk3moe.so``; every function has the name of the C
 entry point it calls (``include/k3moe.h``) and only marshals arguments: torch
@@ -27,6 +30,10 @@ __all__ = [
     "K3MoELinearConfig", "k3moe_linear_config", "k3moe_linear_workspace_bytes", "k3moe_linear", "Linear",
     "K3MoEDeltaConfig", "k3moe_delta_config", "k3moe_delta_validate_config", "k3moe_delta_workspace_bytes",
     "k3moe_delta_rule", "DeltaRule", "ACTIVATIONS",
+    "K3MoENormConfig", "k3moe_norm_config", "k3moe_norm", "Norm", "GATES",
+    "K3MoEHeadLinearConfig", "k3moe_head_linear_config", "k3moe_head_linear_workspace_bytes", "k3moe_head_linear", "HeadLinear",
+    "K3MoELatentConfig", "k3moe_latent_config", "k3moe_latent_validate_config", "k3moe_latent_workspace_bytes",
+    "k3moe_latent_write", "k3moe_latent_attend", "k3moe_latent_prompt", "LatentAttention", "ROPES",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -64,6 +71,22 @@ class K3MoEDeltaConfig(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class K3MoENormConfig(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("group", ctypes.c_int32), ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("x_f32", ctypes.c_int32), ("sum_f32", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("alpha", ctypes.c_float)]
+
+
+class K3MoEHeadLinearConfig(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32)]
+
+
+class K3MoELatentConfig(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("rank", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("key_dim", ctypes.c_int32),
+                ("value_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("rope", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("norm_eps", ctypes.c_float), ("scale", ctypes.c_float), ("causal", ctypes.c_int32)]
+
+
 class K3MoEError(RuntimeError):
     def __init__(self, what: str, status: int):
         super().__init__(f"{what}: {STATUS_NAMES.get(status, status)} ({k3moe_strerror(status)})")
@@ -89,6 +112,7 @@ def lib():
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         cp = ctypes.POINTER(K3MoEConfig)
         lp, dp = ctypes.POINTER(K3MoELinearConfig), ctypes.POINTER(K3MoEDeltaConfig)
+        np, hp, ap = ctypes.POINTER(K3MoENormConfig), ctypes.POINTER(K3MoEHeadLinearConfig), ctypes.POINTER(K3MoELatentConfig)
         sig = {
             "k3moe_strerror": (ctypes.c_char_p, [ctypes.c_int]),
             "k3moe_validate_config": (ctypes.c_int, [cp]),
@@ -117,6 +141,16 @@ def lib():
             "k3moe_delta_workspace_bytes": (ctypes.c_int, [dp, i32, i32, ctypes.POINTER(sz)]),
             "k3moe_delta_rule": (ctypes.c_int, [dp, i32, i32, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp,
                                                 i32, vp, vp, vp, sz, vp]),
+            "k3moe_norm": (ctypes.c_int, [np, i32, vp, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, vp, i64, vp]),
+            "k3moe_head_linear_workspace_bytes": (ctypes.c_int, [hp, i32, ctypes.POINTER(sz)]),
+            "k3moe_head_linear": (ctypes.c_int, [hp, i32, vp, i64, i64, vp, vp, i64, i64, vp, sz, vp]),
+            "k3moe_latent_validate_config": (ctypes.c_int, [ap]),
+            "k3moe_latent_workspace_bytes": (ctypes.c_int, [ap, i32, i32, ctypes.POINTER(sz)]),
+            "k3moe_latent_write": (ctypes.c_int, [ap, i32, vp, i64, vp, vp, vp, vp, i64, vp, i32, vp, vp, i64, i64, vp, i64, i64,
+                                                  vp, sz, vp]),
+            "k3moe_latent_attend": (ctypes.c_int, [ap, i32, i32, vp, vp, i64, i64, vp, i32, vp, i32, vp, vp, vp, vp, sz, vp]),
+            "k3moe_latent_prompt": (ctypes.c_int, [ap, i32, i32, i32, vp, vp, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, vp, sz,
+                                                   vp]),
             "k3moe_launch_count": (i64, []),
             "k3moe_set_prefill_gemm": (ctypes.c_int, [i32]),
             "k3moe_get_prefill_gemm": (i32, []),
@@ -328,6 +362,83 @@ def k3moe_delta_rule(dc, n_seq, T, seq_start, q, q_stride, k, k_stride, v, v_str
         ctypes.byref(dc), n_seq, T, _ptr(seq_start), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v),
         v_stride, _ptr(g), _ptr(beta), _ptr(state_in), _ptr(state_out), n_slots, _ptr(slots), _ptr(out),
         _ptr(ws), wb, _stream(stream)))
+
+
+GATES = {"none": 0, "sigmoid": 1, "silu": 2}
+
+
+def k3moe_norm_config(n, group=0, post_norm=1, pre_norm=1, gate="none", x_f32=False, sum_f32=False, eps=1e-6,
+                      alpha=1.0) -> K3MoENormConfig:
+    """group: n when 0; gate: a name of GATES or its number."""
+    return K3MoENormConfig(n, group or n, int(post_norm), int(pre_norm), GATES[gate] if isinstance(gate, str) else gate, int(x_f32),
+                           int(sum_f32), eps, alpha)
+
+
+def k3moe_norm(nc, T, x, x_stride, gate, gate_stride, post_gain, residual, residual_stride, scale, total, total_stride, pre_gain, out,
+               out_stride, stream=None):
+    _check("k3moe_norm", lib().k3moe_norm(
+        ctypes.byref(nc), T, _ptr(x), x_stride, _ptr(gate), gate_stride, _ptr(post_gain), _ptr(residual), residual_stride, _ptr(scale),
+        _ptr(total), total_stride, _ptr(pre_gain), _ptr(out), out_stride, _stream(stream)))
+
+
+def k3moe_head_linear_config(n_heads, n, k) -> K3MoEHeadLinearConfig:
+    return K3MoEHeadLinearConfig(n_heads, n, k)
+
+
+def k3moe_head_linear_workspace_bytes(hc: K3MoEHeadLinearConfig, T_max: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("k3moe_head_linear_workspace_bytes", lib().k3moe_head_linear_workspace_bytes(ctypes.byref(hc), T_max, ctypes.byref(out)))
+    return out.value
+
+
+def k3moe_head_linear(hc, T, x, x_stride, x_head_stride, w, y, y_stride, y_head_stride, ws, ws_bytes=None, stream=None):
+    wb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check("k3moe_head_linear", lib().k3moe_head_linear(
+        ctypes.byref(hc), T, _ptr(x), x_stride, x_head_stride, _ptr(w), _ptr(y), y_stride, y_head_stride, _ptr(ws), wb, _stream(stream)))
+
+
+ROPES = {"none": 0, "pairs": 1, "halves": 2}
+
+
+def k3moe_latent_config(n_heads, rank=512, rope_dim=64, key_dim=128, value_dim=128, page_size=64, rope="pairs", norm=1, norm_eps=1e-6,
+                        scale=None, causal=1) -> K3MoELatentConfig:
+    """rope: a name of ROPES or its number; scale: (key_dim + rope_dim) ** -0.5 when None."""
+    return K3MoELatentConfig(n_heads, rank, rope_dim, key_dim, value_dim, page_size, ROPES[rope] if isinstance(rope, str) else rope,
+                             int(norm), norm_eps, scale if scale is not None else max(key_dim + rope_dim, 1) ** -0.5, int(causal))
+
+
+def k3moe_latent_validate_config(lc: K3MoELatentConfig) -> int:
+    return lib().k3moe_latent_validate_config(ctypes.byref(lc))
+
+
+def k3moe_latent_workspace_bytes(lc: K3MoELatentConfig, n_seq_max: int, T_max: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("k3moe_latent_workspace_bytes", lib().k3moe_latent_workspace_bytes(ctypes.byref(lc), n_seq_max, T_max, ctypes.byref(out)))
+    return out.value
+
+
+def k3moe_latent_write(lc, T, c, c_stride, gain, positions, inv_freq, rows, rows_stride, cache, n_pages, slots, q, q_stride, q_head_stride,
+                       q_rope, q_rope_stride, q_rope_head_stride, ws, ws_bytes=None, stream=None):
+    wb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check("k3moe_latent_write", lib().k3moe_latent_write(
+        ctypes.byref(lc), T, _ptr(c), c_stride, _ptr(gain), _ptr(positions), _ptr(inv_freq), _ptr(rows), rows_stride, _ptr(cache), n_pages,
+        _ptr(slots), _ptr(q), q_stride, q_head_stride, _ptr(q_rope), q_rope_stride, q_rope_head_stride, _ptr(ws), wb, _stream(stream)))
+
+
+def k3moe_latent_attend(lc, n_seq, T, seq_start, q, q_stride, q_head_stride, cache, n_pages, pages, max_pages, kv_len, out, lse, ws,
+                        ws_bytes=None, stream=None):
+    wb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check("k3moe_latent_attend", lib().k3moe_latent_attend(
+        ctypes.byref(lc), n_seq, T, _ptr(seq_start), _ptr(q), q_stride, q_head_stride, _ptr(cache), n_pages, _ptr(pages), max_pages,
+        _ptr(kv_len), _ptr(out), _ptr(lse), _ptr(ws), wb, _stream(stream)))
+
+
+def k3moe_latent_prompt(lc, n_seq, T, S, seq_start, kv_start, q, q_stride, q_head_stride, kv, kv_stride, kv_head_stride, rope_key,
+                        rope_stride, out, lse, ws, ws_bytes=None, stream=None):
+    wb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check("k3moe_latent_prompt", lib().k3moe_latent_prompt(
+        ctypes.byref(lc), n_seq, T, S, _ptr(seq_start), _ptr(kv_start), _ptr(q), q_stride, q_head_stride, _ptr(kv), kv_stride,
+        kv_head_stride, _ptr(rope_key), rope_stride, _ptr(out), _ptr(lse), _ptr(ws), wb, _stream(stream)))
 
 
 def k3moe_device_status(ws, stream=None):
@@ -666,4 +777,202 @@ class DeltaRule:
             self.ws.data_ptr(), self.ws_bytes, self._current() if stream is None else _handle(stream))
         if st:
             _check("k3moe_delta_rule", st)
+        return out
+
+
+# ----------------------------------------------------------------------------- the latent attention's holders
+
+def _heads(what, t, dtypes, shape, index):
+    """The strides from token to token and from head to head of t [T][heads][columns], whose heads may
+    be columns of wider ones; raises ValueError unless t fits."""
+    if not _fits(t, dtypes, shape, index):
+        raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected "
+                         f"{' or '.join(str(d) for d in dtypes)} {tuple(shape)} on "
+                         f"{'the host' if index < 0 else f'cuda:{index}'}")
+    (T, H, n), (ts, hs, es) = shape, t.stride()
+    if n > 1 and es != 1:
+        raise ValueError(f"{what}: strides {tuple(t.stride())} of shape {tuple(shape)}: columns are not dense")
+    hs = hs if H > 1 else n                                # of one head, of one token: whatever its stride says
+    return ts if T > 1 else (H - 1) * hs + (n + 7) // 8 * 8, hs
+
+
+def _exact_fit(what, t, dtypes, shape, index):
+    if not (t.dtype in dtypes and t.shape == shape and t.get_device() == index and t.is_contiguous()):
+        _require(what, t, dtypes, shape, index)
+    return t.data_ptr()
+
+
+class _Holder:
+    """What the holders below share: a device, its current stream and, where asked for, a workspace."""
+
+    def _init(self, device, ws_bytes=0):
+        import torch
+        self.device, self._index = _device(device)
+        self._bf16, self._f32, self._i32 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,)
+        self._current, self._on = _current_stream(self._index), torch.cuda.device
+        self._device_now = torch.cuda.current_device
+        self.ws_bytes = ws_bytes
+        self.ws = torch.zeros(ws_bytes, dtype=torch.uint8, device=self.device) if ws_bytes else None
+
+    def _run(self, what, fn, *args, stream=None):
+        """fn(*args, stream) on the holder's device, whichever is the current one."""
+        if self._index >= 0 and self._device_now() != self._index:
+            with self._on(self._index):
+                st = fn(*args, self._current() if stream is None else _handle(stream))
+        else:
+            st = fn(*args, self._current() if stream is None else _handle(stream))
+        if st:
+            _check(what, st)
+
+
+class Norm(_Holder):
+    """The norms after a block and before the next with the block's gate and residual scale (k3moe_norm): holds
+    post_gain [group], scale [n] or None and pre_gain [n], f32, set by the caller."""
+
+    def __init__(self, nc: K3MoENormConfig, device="cuda"):
+        import torch
+        self._init(device)
+        self.nc = nc
+        self.post_gain = self.scale = self.pre_gain = None
+        self._xtype = self._f32 if nc.x_f32 else (torch.bfloat16, torch.int16)
+        self._stype = self._f32 if nc.sum_f32 else (torch.bfloat16, torch.int16)
+        self._nc, self._call = ctypes.byref(nc), lib().k3moe_norm
+
+    def _rows(self, what, t, types, shape):
+        if t is None:
+            return None, shape[1]
+        if t.dtype in types and t.shape == shape and t.get_device() == self._index:
+            if t.is_contiguous():
+                return t.data_ptr(), shape[1]
+            if t.stride(1) == 1 and shape[0] > 1:
+                return t.data_ptr(), t.stride(0)
+        return t.data_ptr(), _require(what, t, types, shape, self._index, True)
+
+    def __call__(self, x, out=None, gate=None, residual=None, total=None, stream=None):
+        """x [T][n] by x_f32; gate [T][n] bf16; residual and total [T][n] by sum_f32; out [T][n] bf16; rows may be
+        slices of wider ones.  Returns out, or total where nothing is normed for the next block."""
+        nc, dev = self.nc, self._index
+        shape = (x.shape[0], nc.n)
+        gains = []
+        for what, g, n in (("post_gain", self.post_gain, nc.group), ("scale", self.scale, nc.n), ("pre_gain", self.pre_gain, nc.n)):
+            gains.append(None if g is None else _exact_fit(what, g, self._f32, (n,), dev))
+        xp, xs = self._rows("x", x, self._xtype, shape)
+        gp, gs = self._rows("gate", gate, self._bf16, shape)
+        rp, rs = self._rows("residual", residual, self._stype, shape)
+        tp, ts = self._rows("total", total, self._stype, shape)
+        op, os_ = self._rows("out", out, self._bf16, shape)
+        if shape[0]:
+            self._run("k3moe_norm", self._call, self._nc, shape[0], xp, xs, gp, gs, gains[0], rp, rs, gains[1], tp, ts, gains[2], op, os_,
+                      stream=stream)
+        return total if out is None else out
+
+
+class HeadLinear(_Holder):
+    """Every head's own projection (k3moe_head_linear): holds the weights w [n_heads][n][k] bf16, set by
+    the caller, and a workspace."""
+
+    def __init__(self, hc: K3MoEHeadLinearConfig, T_max: int, device="cuda"):
+        self._init(device, k3moe_head_linear_workspace_bytes(hc, T_max))
+        self.hc, self.T_max, self.w = hc, T_max, None
+        self._hc, self._call = ctypes.byref(hc), lib().k3moe_head_linear
+
+    def __call__(self, x, y, stream=None):
+        """x [T][n_heads][k] bf16, y [T][n_heads][n] bf16 written and returned; heads may be columns of wider ones."""
+        T, hc, dev = x.shape[0], self.hc, self._index
+        if T > self.T_max:
+            raise ValueError(f"x: {T} tokens, the holder is for {self.T_max}")
+        xs, xh = _heads("x", x, self._bf16, (T, hc.n_heads, hc.k), dev)
+        ys, yh = _heads("y", y, self._bf16, (T, hc.n_heads, hc.n), dev)
+        w = _exact_fit("w", self.w, self._bf16, (hc.n_heads, hc.n, hc.k), dev)
+        if T:
+            self._run("k3moe_head_linear", self._call, self._hc, T, x.data_ptr(), xs, xh, w, y.data_ptr(), ys, yh, self.ws.data_ptr(),
+                      self.ws_bytes, stream=stream)
+        return y
+
+
+class LatentAttention(_Holder):
+    """The latent cache's write and attention over it (k3moe_latent_write, _attend, _prompt), for up to n_seq_max
+    sequences and T_max query tokens a call: holds gain [rank] f32 and inv_freq [rope_dim / 2] f64, set by the caller, and
+    a workspace; the cache is the caller's."""
+
+    def __init__(self, lc: K3MoELatentConfig, n_seq_max: int, T_max: int, device="cuda"):
+        import torch
+        self._init(device, k3moe_latent_workspace_bytes(lc, n_seq_max, T_max))
+        self.lc, self.n_seq_max, self.T_max = lc, n_seq_max, T_max
+        self.gain = self.inv_freq = None
+        self._i64, self._f64 = (torch.int64,), (torch.float64,)
+        self._row = lc.rank + lc.rope_dim
+        self._lc, L = ctypes.byref(lc), lib()
+        self._write, self._attend, self._prompt = L.k3moe_latent_write, L.k3moe_latent_attend, L.k3moe_latent_prompt
+
+    def new_cache(self, n_pages):
+        """A zeroed cache of n_pages pages [n_pages][page_size][rank + rope_dim] bf16."""
+        import torch
+        return torch.zeros((n_pages, self.lc.page_size, self._row), dtype=torch.bfloat16, device=self.device)
+
+    def _room(self, n_seq, T):
+        if n_seq > self.n_seq_max or T > self.T_max:
+            raise ValueError(f"{n_seq} sequences of {T} tokens, the holder is for {self.n_seq_max} and {self.T_max}")
+
+    def _pool(self, cache):
+        shape = (cache.shape[0], self.lc.page_size, self._row)
+        return _exact_fit("cache", cache, self._bf16, shape, self._index), shape[0]
+
+    def _lse(self, lse, T):
+        return None if lse is None else _exact_fit("lse", lse, self._f32, (T, self.lc.n_heads), self._index)
+
+    def write(self, c, positions=None, cache=None, slots=None, rows=None, q=None, q_rope=None, stream=None):
+        """c [T][rank + rope_dim] bf16, positions [T] int32; the rows go to slots [T] int64 of the cache and to rows
+        [T][rank + rope_dim]; q [T][n_heads][rope_dim], the queries' rotated columns, to q_rope, which may be q."""
+        lc, dev, T = self.lc, self._index, c.shape[0]
+        if T > self.T_max:
+            raise ValueError(f"c: {T} tokens, the holder is for {self.T_max}")
+        cs = _require("c", c, self._bf16, (T, self._row), dev, True)
+        gain = None if self.gain is None else _exact_fit("gain", self.gain, self._f32, (lc.rank,), dev)
+        freq = None if self.inv_freq is None else _exact_fit("inv_freq", self.inv_freq, self._f64, (lc.rope_dim // 2,), dev)
+        at = None if positions is None else _exact_fit("positions", positions, self._i32, (T,), dev)
+        rs = self._row if rows is None else _require("rows", rows, self._bf16, (T, self._row), dev, True)
+        pool, n_pages = (None, 0) if cache is None else self._pool(cache)
+        sl = None if slots is None else _exact_fit("slots", slots, self._i64, (T,), dev)
+        shape = (T, lc.n_heads, lc.rope_dim)
+        (qs, qh), (os_, oh) = ((0, 0) if t is None else _heads(w, t, self._bf16, shape, dev) for w, t in (("q", q), ("q_rope", q_rope)))
+        if T:
+            self._run("k3moe_latent_write", self._write, self._lc, T, c.data_ptr(), cs, gain, at, freq,
+                      None if rows is None else rows.data_ptr(), rs, pool, n_pages, sl, None if q is None else q.data_ptr(), qs, qh,
+                      None if q_rope is None else q_rope.data_ptr(), os_, oh, self.ws.data_ptr(), self.ws_bytes, stream=stream)
+        return cache if rows is None else rows
+
+    def attend(self, q, cache, pages, kv_len, out, seq_start=None, lse=None, stream=None):
+        """q [T][n_heads][rank + rope_dim] bf16, pages [n_seq][max_pages] int32, kv_len [n_seq] int32; out
+        [T][n_heads][rank] bf16 written and returned, lse [T][n_heads] f32 or None; seq_start [n_seq+1] int32, or None for
+        one token each (with one sequence: all)."""
+        lc, dev, T, n_seq = self.lc, self._index, q.shape[0], kv_len.shape[0]
+        self._room(n_seq, T)
+        qs, qh = _heads("q", q, self._bf16, (T, lc.n_heads, self._row), dev)
+        pool, n_pages = self._pool(cache)
+        table = _exact_fit("pages", pages, self._i32, (n_seq, pages.shape[-1]), dev)
+        lens = _exact_fit("kv_len", kv_len, self._i32, (n_seq,), dev)
+        o = _exact_fit("out", out, self._bf16, (T, lc.n_heads, lc.rank), dev)
+        start = None if seq_start is None else _exact_fit("seq_start", seq_start, self._i32, (n_seq + 1,), dev)
+        if T:
+            self._run("k3moe_latent_attend", self._attend, self._lc, n_seq, T, start, q.data_ptr(), qs, qh, pool, n_pages, table,
+                      pages.shape[-1], lens, o, self._lse(lse, T), self.ws.data_ptr(), self.ws_bytes, stream=stream)
+        return out
+
+    def prompt(self, q, kv, rope_key, out, seq_start=None, kv_start=None, lse=None, stream=None):
+        """q [T][n_heads][key_dim + rope_dim], kv [S][n_heads][key_dim + value_dim], rope_key [S][rope_dim] bf16, the last's
+        rows at any stride; out [T][n_heads][value_dim] bf16 written and returned, lse [T][n_heads] f32 or None; seq_start and
+        kv_start [n_seq+1] int32, or None: one sequence, or the queries' own."""
+        lc, dev, T, S = self.lc, self._index, q.shape[0], kv.shape[0]
+        n_seq = 1 if seq_start is None else seq_start.shape[0] - 1
+        self._room(n_seq, T)
+        qs, qh = _heads("q", q, self._bf16, (T, lc.n_heads, lc.key_dim + lc.rope_dim), dev)
+        ks, kh = _heads("kv", kv, self._bf16, (S, lc.n_heads, lc.key_dim + lc.value_dim), dev)
+        rs = _require("rope_key", rope_key, self._bf16, (S, lc.rope_dim), dev, True)
+        o = _exact_fit("out", out, self._bf16, (T, lc.n_heads, lc.value_dim), dev)
+        start, keys = (None if t is None else _exact_fit(w, t, self._i32, (n_seq + 1,), dev)
+                       for w, t in (("seq_start", seq_start), ("kv_start", kv_start)))
+        if T:
+            self._run("k3moe_latent_prompt", self._prompt, self._lc, n_seq, T, S, start, keys, q.data_ptr(), qs, qh, kv.data_ptr(), ks, kh,
+                      rope_key.data_ptr(), rs, o, self._lse(lse, T), self.ws.data_ptr(), self.ws_bytes, stream=stream)
         return out

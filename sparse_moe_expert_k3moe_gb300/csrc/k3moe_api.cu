@@ -507,6 +507,201 @@ k3moe_status k3moe_delta_rule(const k3moe_delta_config *dc, int32_t n_seq, int32
     return launch_delta(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
 }
 
+// Row strides of 16-byte accesses: within [width, kMaxStride], a multiple of 8.
+static bool row_stride(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0 && stride <= kMaxStride; }
+// A token's and a head's stride of `heads` heads of `width` columns: no two overlap.
+static bool head_strides(int64_t stride, int64_t head, int64_t heads, int64_t width, int64_t each)
+{
+    return head >= width && head <= kMaxStride && head % each == 0 && stride >= (heads - 1) * head + width &&
+           stride <= kMaxStride && stride % each == 0;
+}
+
+k3moe_status k3moe_norm(const k3moe_norm_config *nc, int32_t T, const void *x, int64_t x_stride,
+                        const uint16_t *gate, int64_t gate_stride, const float *post_gain,
+                        const void *residual, int64_t residual_stride, const float *scale,
+                        void *total, int64_t total_stride, const float *pre_gain, uint16_t *out,
+                        int64_t out_stride, k3moe_stream stream)
+{
+    if (!nc || nc->n <= 0 || nc->group <= 0) return K3MOE_EINVAL;
+    const auto flag = [](int32_t f) { return f == 0 || f == 1; };
+    if (!flag(nc->post_norm) || !flag(nc->pre_norm) || !flag(nc->x_f32) || !flag(nc->sum_f32) ||
+        nc->gate < K3MOE_GATE_NONE || nc->gate > K3MOE_GATE_SILU || !std::isfinite(nc->alpha) ||
+        ((nc->post_norm || nc->pre_norm) && !finite_pos(nc->eps)))
+        return K3MOE_EINVAL;
+    if (nc->n > kMaxNorm || nc->n % 8) return K3MOE_ESHAPE;
+    if (nc->group != nc->n && ((nc->group != 64 && nc->group != 128 && nc->group != 256) || nc->n % nc->group)) return K3MOE_ESHAPE;
+    if (T < 0 || T > kMaxT) return K3MOE_ESHAPE;
+    if (T == 0) return K3MOE_OK;
+    if (!x || (nc->post_norm && !post_gain) || (nc->pre_norm && !pre_gain) || !out != !nc->pre_norm ||
+        (!total && !out) || !gate != (nc->gate == K3MOE_GATE_NONE))
+        return K3MOE_EINVAL;
+    if (!row_stride(x_stride, nc->n) || (gate && !row_stride(gate_stride, nc->n)) ||
+        (residual && !row_stride(residual_stride, nc->n)) || (total && !row_stride(total_stride, nc->n)) ||
+        (out && !row_stride(out_stride, nc->n)))
+        return K3MOE_ESHAPE;
+    // in place where each element is read and written by one thread; not otherwise
+    const auto same = [&](const void *w, int64_t ws, int wf, const void *r, int64_t rs, int rf) {
+        return w && w == r && (ws != rs || wf != rf);
+    };
+    if (same(total, total_stride, nc->sum_f32, x, x_stride, nc->x_f32) || same(total, total_stride, nc->sum_f32, gate, gate_stride, 0) ||
+        same(total, total_stride, nc->sum_f32, residual, residual_stride, nc->sum_f32) || same(out, out_stride, 0, x, x_stride, nc->x_f32) ||
+        same(out, out_stride, 0, gate, gate_stride, 0) || same(out, out_stride, 0, residual, residual_stride, nc->sum_f32) ||
+        (total && total == out))
+        return K3MOE_EINVAL;
+    for (const void *p : {x, (const void *)gate, (const void *)post_gain, residual, (const void *)scale, (const void *)total,
+                          (const void *)pre_gain, (const void *)out})
+        if (!aligned(p, 16)) return K3MOE_EALIGN;
+    const NormArgs a{T, nc->n, nc->group, nc->post_norm, nc->pre_norm, nc->gate, nc->x_f32, nc->sum_f32, nc->eps, nc->alpha, x, x_stride,
+                     gate, gate_stride, post_gain, residual, residual_stride, scale, total, total_stride, pre_gain, out, out_stride};
+    result_pending_begin((cudaStream_t)stream);
+    return launch_norm(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
+}
+
+static k3moe_status check_head_linear(const k3moe_head_linear_config *hc)
+{
+    if (!hc || hc->n_heads <= 0 || hc->n <= 0 || hc->k <= 0) return K3MOE_EINVAL;
+    if (hc->n_heads > kMaxLatHeads || hc->n > kMaxHeadN || hc->k > kMaxHeadK || hc->k % 8) return K3MOE_ESHAPE;
+    return K3MOE_OK;
+}
+
+k3moe_status k3moe_head_linear_workspace_bytes(const k3moe_head_linear_config *hc, int32_t T_max, size_t *bytes)
+{
+    const k3moe_status st = check_head_linear(hc);
+    if (st != K3MOE_OK) return st;
+    if (!bytes) return K3MOE_EINVAL;
+    if (T_max < 0 || T_max > kMaxT) return K3MOE_ESHAPE;
+    *bytes = kCtrOffset + kCtrBytes;
+    return K3MOE_OK;
+}
+
+k3moe_status k3moe_head_linear(const k3moe_head_linear_config *hc, int32_t T, const uint16_t *x,
+                               int64_t x_stride, int64_t x_head_stride, const uint16_t *w, uint16_t *y,
+                               int64_t y_stride, int64_t y_head_stride, void *ws, size_t ws_bytes,
+                               k3moe_stream stream)
+{
+    const k3moe_status st = check_head_linear(hc);
+    if (st != K3MOE_OK) return st;
+    if (T < 0 || T > kMaxT) return K3MOE_ESHAPE;
+    if (T == 0) return K3MOE_OK;
+    if (!x || !w || !y) return K3MOE_EINVAL;
+    if (!head_strides(x_stride, x_head_stride, hc->n_heads, hc->k, 8) || !head_strides(y_stride, y_head_stride, hc->n_heads, hc->n, 1))
+        return K3MOE_ESHAPE;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 2)) return K3MOE_EALIGN;
+    if (!ws || !aligned(ws, 256) || ws_bytes < kCtrOffset + kCtrBytes) return K3MOE_EWORKSPACE;
+    const HeadLinearArgs a{T, hc->n_heads, hc->n, hc->k, x, x_stride, x_head_stride, w, y, y_stride, y_head_stride,
+                           static_cast<int32_t *>(ws)};
+    result_pending_begin((cudaStream_t)stream);
+    return launch_head_linear(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
+}
+
+k3moe_status k3moe_latent_validate_config(const k3moe_latent_config *lc)
+{
+    if (!lc || lc->n_heads <= 0 || lc->rank <= 0 || lc->rope_dim <= 0 || lc->key_dim <= 0 || lc->value_dim <= 0 || lc->page_size <= 0 ||
+        lc->rope < K3MOE_ROPE_NONE || lc->rope > K3MOE_ROPE_HALVES || (lc->norm != 0 && lc->norm != 1) ||
+        (lc->norm && !finite_pos(lc->norm_eps)) || !finite_pos(lc->scale) || (lc->causal != 0 && lc->causal != 1))
+        return K3MOE_EINVAL;
+    if (lc->n_heads > kMaxLatHeads || lc->rank != kLatC || lc->rope_dim != kLatR || lc->key_dim != kLatK || lc->value_dim != kLatV ||
+        lc->page_size < 16 || lc->page_size > 256 || (lc->page_size & (lc->page_size - 1)))
+        return K3MOE_ESHAPE;
+    return K3MOE_OK;
+}
+
+k3moe_status k3moe_latent_workspace_bytes(const k3moe_latent_config *lc, int32_t n_seq_max, int32_t T_max,
+                                          size_t *bytes)
+{
+    const k3moe_status st = k3moe_latent_validate_config(lc);
+    if (st != K3MOE_OK) return st;
+    if (!bytes) return K3MOE_EINVAL;
+    if (T_max < 0 || T_max > kMaxT || n_seq_max < 0 || n_seq_max > kMaxSeqs) return K3MOE_ESHAPE;
+    *bytes = latent_workspace(*lc, n_seq_max, T_max);
+    return K3MOE_OK;
+}
+
+k3moe_status k3moe_latent_write(const k3moe_latent_config *lc, int32_t T, const uint16_t *c, int64_t c_stride,
+                                const float *gain, const int32_t *positions, const double *inv_freq,
+                                uint16_t *rows, int64_t rows_stride, uint16_t *cache, int32_t n_pages,
+                                const int64_t *slots, const uint16_t *q, int64_t q_stride, int64_t q_head_stride,
+                                uint16_t *q_rope, int64_t q_rope_stride, int64_t q_rope_head_stride, void *ws,
+                                size_t ws_bytes, k3moe_stream stream)
+{
+    const k3moe_status st = k3moe_latent_validate_config(lc);
+    if (st != K3MOE_OK) return st;
+    if (T < 0 || T > kMaxT) return K3MOE_ESHAPE;
+    if (T == 0) return K3MOE_OK;
+    if (!c || (lc->norm && !gain) || (lc->rope != K3MOE_ROPE_NONE && (!positions || !inv_freq)) || !cache != !slots || !q != !q_rope ||
+        (!rows && !cache && !q))
+        return K3MOE_EINVAL;
+    if (!row_stride(c_stride, kLatRow) || (rows && !row_stride(rows_stride, kLatRow)) || (cache && n_pages < 1) ||
+        (q && (!head_strides(q_stride, q_head_stride, lc->n_heads, kLatR, 8) ||
+               !head_strides(q_rope_stride, q_rope_head_stride, lc->n_heads, kLatR, 8))))
+        return K3MOE_ESHAPE;
+    if ((rows == c && rows_stride != c_stride) || (q && q == q_rope && (q_stride != q_rope_stride || q_head_stride != q_rope_head_stride)))
+        return K3MOE_EINVAL;
+    if (!aligned(c, 16) || !aligned(gain, 16) || !aligned(positions, 4) || !aligned(inv_freq, 8) || !aligned(rows, 16) ||
+        !aligned(cache, 16) || !aligned(slots, 8) || !aligned(q, 16) || !aligned(q_rope, 16))
+        return K3MOE_EALIGN;
+    if (!ws || !aligned(ws, 256) || ws_bytes < kCtrOffset + kCtrBytes) return K3MOE_EWORKSPACE;
+    const LatentWriteArgs a{T, lc->n_heads, lc->rope, lc->norm, lc->norm_eps, c, c_stride, gain, positions, inv_freq, rows, rows_stride,
+                            cache, (int64_t)n_pages * lc->page_size, slots, q, q_stride, q_head_stride, q_rope, q_rope_stride,
+                            q_rope_head_stride, static_cast<int32_t *>(ws)};
+    result_pending_begin((cudaStream_t)stream);
+    return launch_latent_write(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
+}
+
+k3moe_status k3moe_latent_attend(const k3moe_latent_config *lc, int32_t n_seq, int32_t T, const int32_t *seq_start,
+                                 const uint16_t *q, int64_t q_stride, int64_t q_head_stride, const uint16_t *cache,
+                                 int32_t n_pages, const int32_t *pages, int32_t max_pages, const int32_t *kv_len,
+                                 uint16_t *out, float *lse, void *ws, size_t ws_bytes, k3moe_stream stream)
+{
+    const k3moe_status st = k3moe_latent_validate_config(lc);
+    if (st != K3MOE_OK) return st;
+    if (T < 0 || T > kMaxT || n_seq < 0 || n_seq > kMaxSeqs) return K3MOE_ESHAPE;
+    if (n_seq == 0) return T == 0 ? K3MOE_OK : K3MOE_ESHAPE;
+    if (T == 0) return K3MOE_OK;
+    if (!seq_start && n_seq != 1 && T != n_seq) return K3MOE_EINVAL;
+    if (!q || !cache || !pages || !kv_len || !out) return K3MOE_EINVAL;
+    // a row of the cache is a 32-bit coordinate of its loads
+    if (!head_strides(q_stride, q_head_stride, lc->n_heads, kLatRow, 8) || n_pages < 1 || max_pages < 1 ||
+        (int64_t)n_pages * lc->page_size > INT32_MAX - 1024 || (int64_t)max_pages * lc->page_size > INT32_MAX - 1024)
+        return K3MOE_ESHAPE;
+    if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(out, 16) || !aligned(seq_start, 4) || !aligned(pages, 4) ||
+        !aligned(kv_len, 4) || !aligned(lse, 4))
+        return K3MOE_EALIGN;
+    if (!ws || !aligned(ws, 256) || ws_bytes < latent_workspace(*lc, n_seq, T)) return K3MOE_EWORKSPACE;
+    const AttendArgs a{n_seq, T, lc->n_heads, lc->page_size, lc->causal, lc->scale, seq_start, q, q_stride, q_head_stride, cache, n_pages,
+                       pages, max_pages, kv_len, out, lse, static_cast<uint8_t *>(ws)};
+    result_pending_begin((cudaStream_t)stream);
+    return launch_attend(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
+}
+
+k3moe_status k3moe_latent_prompt(const k3moe_latent_config *lc, int32_t n_seq, int32_t T, int32_t S,
+                                 const int32_t *seq_start, const int32_t *kv_start, const uint16_t *q,
+                                 int64_t q_stride, int64_t q_head_stride, const uint16_t *kv, int64_t kv_stride,
+                                 int64_t kv_head_stride, const uint16_t *rope_key, int64_t rope_stride, uint16_t *out,
+                                 float *lse, void *ws, size_t ws_bytes, k3moe_stream stream)
+{
+    const k3moe_status st = k3moe_latent_validate_config(lc);
+    if (st != K3MOE_OK) return st;
+    if (T < 0 || T > kMaxT || S < 0 || S > kMaxT || n_seq < 0 || n_seq > kMaxSeqs) return K3MOE_ESHAPE;
+    if (n_seq == 0) return T == 0 ? K3MOE_OK : K3MOE_ESHAPE;
+    if (T == 0) return K3MOE_OK;
+    if (!seq_start && n_seq != 1 && T != n_seq) return K3MOE_EINVAL;
+    // without offsets of their own the keys are the queries' tokens; one sequence has all of both
+    if (!kv_start && S != T && !(n_seq == 1 && !seq_start)) return K3MOE_EINVAL;
+    if (!q || !out || (S > 0 && (!kv || !rope_key))) return K3MOE_EINVAL;
+    if (!head_strides(q_stride, q_head_stride, lc->n_heads, kLatK + kLatR, 8) ||
+        !head_strides(kv_stride, kv_head_stride, lc->n_heads, kLatK + kLatV, 8) || !row_stride(rope_stride, kLatR))
+        return K3MOE_ESHAPE;
+    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(rope_key, 16) || !aligned(out, 16) || !aligned(seq_start, 4) ||
+        !aligned(kv_start, 4) || !aligned(lse, 4))
+        return K3MOE_EALIGN;
+    if (!ws || !aligned(ws, 256) || ws_bytes < latent_workspace(*lc, n_seq, T)) return K3MOE_EWORKSPACE;
+    const PromptArgs a{n_seq, T, S, lc->n_heads, lc->causal, lc->scale, seq_start, kv_start, q, q_stride, q_head_stride, kv, kv_stride,
+                       kv_head_stride, rope_key, rope_stride, out, lse, static_cast<uint8_t *>(ws)};
+    result_pending_begin((cudaStream_t)stream);
+    return launch_prompt(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
+}
+
 k3moe_status k3moe_device_status(void *ws, k3moe_stream stream, int32_t *code)
 {
     if (!ws || !aligned(ws, 256) || !code) return K3MOE_EINVAL;

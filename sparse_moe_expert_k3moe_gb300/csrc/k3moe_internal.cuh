@@ -383,6 +383,93 @@ struct DeltaArgs {
 size_t delta_workspace(const k3moe_delta_config &dc, int n_seq, int T);
 cudaError_t launch_delta(const DeltaArgs &a, cudaStream_t s);
 
+// ---- norms around a block, a head's own projection (k3moe_norm.cu, k3moe_head.cu)
+constexpr int32_t kMaxNorm = 16384, kMaxHeadK = 512, kMaxHeadN = 8192;
+struct NormArgs {
+    int32_t T, N, group, post_norm, pre_norm, gate_act, x_f32, sum_f32;
+    float eps, alpha;
+    const void *x;
+    int64_t x_stride;
+    const uint16_t *gate;
+    int64_t gate_stride;
+    const float *post_gain;
+    const void *residual;
+    int64_t residual_stride;
+    const float *scale;
+    void *total;
+    int64_t total_stride;
+    const float *pre_gain;
+    uint16_t *out;
+    int64_t out_stride;
+};
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t s);
+struct HeadLinearArgs {
+    int32_t T, H, N, K;
+    const uint16_t *x;
+    int64_t x_stride, x_head;
+    const uint16_t *w;
+    uint16_t *y;
+    int64_t y_stride, y_head;
+    int32_t *status;
+};
+cudaError_t launch_head_linear(const HeadLinearArgs &a, cudaStream_t s);
+
+// ---- latent attention (k3moe_norm.cu: the write; k3moe_attend.cu, k3moe_prompt.cu)
+constexpr int kLatC = 512, kLatR = 64, kLatRow = kLatC + kLatR, kLatK = 128, kLatV = 128;
+constexpr int32_t kMaxLatHeads = 1024;
+struct LatentWriteArgs {
+    int32_t T, H, rope, norm;
+    float eps;
+    const uint16_t *c;
+    int64_t c_stride;
+    const float *gain;
+    const int32_t *positions;
+    const double *inv_freq;
+    uint16_t *rows;
+    int64_t rows_stride;
+    uint16_t *cache;
+    int64_t n_slots;
+    const int64_t *slots;
+    const uint16_t *q;
+    int64_t q_stride, q_head;
+    uint16_t *q_rope;
+    int64_t r_stride, r_head;
+    int32_t *status;
+};
+cudaError_t launch_latent_write(const LatentWriteArgs &a, cudaStream_t s);
+struct AttendArgs {
+    int32_t n_seq, T, H, page, causal;
+    float scale;
+    const int32_t *seq_start;                             // NULL: T / n_seq tokens each
+    const uint16_t *q;
+    int64_t q_stride, q_head;
+    const uint16_t *cache;
+    int32_t n_pages;
+    const int32_t *pages;
+    int32_t max_pages;
+    const int32_t *kv_len;
+    uint16_t *out;
+    float *lse;
+    uint8_t *ws;
+};
+size_t latent_workspace(const k3moe_latent_config &lc, int n_seq, int T);
+cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s);
+struct PromptArgs {
+    int32_t n_seq, T, S, H, causal;
+    float scale;
+    const int32_t *seq_start, *kv_start;                  // NULL: as AttendArgs'; NULL: the queries'
+    const uint16_t *q;
+    int64_t q_stride, q_head;
+    const uint16_t *kv;
+    int64_t kv_stride, kv_head;
+    const uint16_t *rope_key;
+    int64_t rope_stride;
+    uint16_t *out;
+    float *lse;
+    uint8_t *ws;
+};
+cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t s);
+
 // Host launchers implemented in the kernel files.
 cudaError_t launch_pack(const k3moe_config &c, int expert_lo, int n, const uint8_t *w1p,
                         const uint8_t *w1s, const uint8_t *w3p, const uint8_t *w3s,

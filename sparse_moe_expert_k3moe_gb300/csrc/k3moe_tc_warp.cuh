@@ -57,6 +57,15 @@ __device__ __forceinline__ void tma2d_warp(void *dst, const CUtensorMap *m, int 
         "l"(m), "r"(c0), "r"(c1), "r"(saddr(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma3d_warp(void *dst, const CUtensorMap *m, int c0, int c1, int c2, uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n\t}" ::"r"(saddr(dst)),
+        "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(saddr(bar))
+        : "memory");
+}
 // A operand in tensor memory (two 16-bit elements of K a column), B in shared memory.
 template <uint32_t kHi = kDescSw128>
 __device__ __forceinline__ void umma_ts_warp(uint32_t dtmem, uint32_t atmem, uint32_t b, uint32_t id, uint32_t acc)
@@ -109,6 +118,22 @@ inline bool map16s(CUtensorMap *m, const void *base, uint64_t rows, uint64_t col
     const cuuint32_t box[2] = {64u, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 16-bit array [outer][middle][cols] with strides in elements: boxes of 64 columns x box_middle x
+// box_outer, 128-byte swizzle; what a box has outside reads as zero.
+inline bool map16x3(CUtensorMap *m, const void *base, uint64_t outer, uint64_t outer_stride, uint64_t middle,
+                    uint64_t middle_stride, uint64_t cols, uint32_t box_middle, uint32_t box_outer)
+{
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {cols, middle, outer};
+    const cuuint64_t strides[2] = {middle_stride * 2, outer_stride * 2};
+    const cuuint32_t box[3] = {64u, box_middle, box_outer};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
