@@ -108,20 +108,6 @@ struct CacheKeys {
     }
 };
 
-struct HeadKeys {
-    const uint16_t *kv, *rope;
-    int64_t kv_stride, rope_stride;
-    __device__ float score(int j, const float *q) const
-    {
-        const uint16_t *k = kv + (size_t)j * kv_stride, *r = rope + (size_t)j * rope_stride;
-        float s = 0.0f;
-        for (int c = 0; c < kLatK; c++) s = fmaf(q[c], bf16_bits_to_f32(k[c]), s);
-        for (int c = 0; c < kLatR; c++) s = fmaf(q[kLatK + c], bf16_bits_to_f32(r[c]), s);
-        return s;
-    }
-    __device__ float value(int j, int d) const { return bf16_bits_to_f32(kv[(size_t)j * kv_stride + kLatK + d]); }
-};
-
 __global__ void __launch_bounds__(kSimpleThreads) attend_simple_kernel(const AttendArgs a)
 {
     __shared__ Simple<kLatC> sh;
@@ -143,36 +129,6 @@ __global__ void __launch_bounds__(kSimpleThreads) attend_simple_kernel(const Att
                             CacheKeys{a.cache, a.pages + (size_t)i * a.max_pages, a.page, a.n_pages, status});
 }
 
-__global__ void __launch_bounds__(kSimpleThreads) prompt_simple_kernel(const PromptArgs a)
-{
-    __shared__ Simple<kLatV> sh;
-    const int t = blockIdx.x / a.H, h = blockIdx.x % a.H;
-    int32_t *status = reinterpret_cast<int32_t *>(a.ws);
-    int first, n;
-    const int i = sequence_of(a.seq_start, a.n_seq, a.T, t, &first, &n, status);
-    if (i < 0) return;
-    int k0 = first, k1 = first + n;
-    if (a.kv_start) {
-        k0 = a.kv_start[i];
-        k1 = a.kv_start[i + 1];
-    } else if (!a.seq_start && a.n_seq == 1) {
-        k0 = 0;
-        k1 = a.S;
-    }
-    if (k0 < 0 || k1 < k0 || k1 > a.S) {
-        set_status(status, K3MOE_DEV_BAD_OFFSETS);
-        return;
-    }
-    for (int c = threadIdx.x; c < kLatK + kLatR; c += kSimpleThreads)
-        sh.q[c] = bf16_bits_to_f32(a.q[(size_t)t * a.q_stride + (size_t)h * a.q_head + c]);
-    __syncthreads();
-    const size_t o = (size_t)t * a.H + h;
-    const int len = k1 - k0;
-    simple_attention<kLatV>(sh, a.causal ? max(0, len - (n - 1 - (t - first))) : len, a.scale, a.out + o * kLatV, a.lse ? a.lse + o : nullptr,
-                            HeadKeys{a.kv + (size_t)k0 * a.kv_stride + (size_t)h * a.kv_head, a.rope_key + (size_t)k0 * a.rope_stride,
-                                     a.kv_stride, a.rope_stride});
-}
-
 }  // namespace
 
 size_t latent_workspace(const k3moe_latent_config &lc, int n_seq, int T)
@@ -189,15 +145,6 @@ cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
     attend_simple_kernel<<<(unsigned)(a.T * a.H), kSimpleThreads, 0, s>>>(a);
     count_launch();
     timing_end("latent_attend", s);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t s)
-{
-    timing_begin("latent_prompt", s);
-    prompt_simple_kernel<<<(unsigned)(a.T * a.H), kSimpleThreads, 0, s>>>(a);
-    count_launch();
-    timing_end("latent_prompt", s);
     return cudaGetLastError();
 }
 

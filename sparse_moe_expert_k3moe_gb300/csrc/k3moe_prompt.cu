@@ -1,0 +1,395 @@
+// k3moe_prompt.cu -- latent attention in the expanded form: every head has keys [k, r] of 192
+// columns (r shared by all heads) and values of 128, packed sequences, causal or not.
+//
+// One pass over the keys with a running maximum m and sum l (softmax in powers of two):
+//   p_j = 2^(c s_j - m),  l = sum p_j,  O = sum p_j v_j,  out = O / l,  lse = (m + log2 l) ln 2,
+// c = scale log2 e.  A block has 256 queries of one head in two halves of 128 and walks its keys in tiles of
+// 128.  The scores S = Q K^T go to tensor memory, a thread owns a row of one half: it reads its 128 scores, and
+// its weights go back over them as the A operand of O += P V, so that the softmax of one half runs
+// beside the products of the other.  m moves only when a row outdoes it by 2^8 (weights stay below that, and
+// float sums do not mind); the rescaling of O in tensor memory is then rare.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "k3moe_internal.cuh"
+#include "k3moe_latent.cuh"
+
+namespace k3moe {
+namespace {
+
+constexpr int kPrRows = 128, kPrTile = 128;                   // rows of a half; keys of a tile
+constexpr int kPrBox = kPrTile * 128;                         // 64 columns of 128 rows: 16 KB
+constexpr int kPrQBoxes = (kLatK + kLatR) / 64;               // boxes of a half's queries, and of a tile's keys
+constexpr int kPrTileBoxes = kPrQBoxes + kLatV / 64;          // with its values
+constexpr int kPrSlots = 8;                                   // the ring of key and value boxes
+constexpr int kPrSmem = 1024 + (2 * kPrQBoxes + kPrSlots) * kPrBox;
+// Warps: four of softmax for each half, then MMA issue, loads and two that mend values
+constexpr int kPrThreads = 384, kPrWarpMma = 8, kPrWarpLoad = 9, kPrWarpMend = 10;
+// Registers a thread: 168 at launch, moved from the last warpgroup to the rows' threads
+constexpr int kPrRegs = 168, kPrRegsRows = 216, kPrRegsLast = 72;
+static_assert(2 * kPrRegsRows + kPrRegsLast <= 3 * kPrRegs, "shares within the launch's");
+// Tensor memory: S (P over its first half) and O of both halves
+constexpr uint32_t kPrTmS = 0, kPrTmO = 2 * kPrTile;
+constexpr float kPrSlack = 8.0f;
+
+struct PromptShared {
+    uint64_t q_full[2], full[kPrSlots], empty[kPrSlots], s_full[2], p_ready[2], o_full[2], mend[2], mended[2], drain;
+    uint32_t tmem;
+    volatile int bail, spoiled;
+    UnitSearch search;
+};
+
+// A row of scores becomes weights in tensor memory, packed; returns their sum.
+__device__ __forceinline__ float weigh(uint32_t (&v)[128], uint32_t taddr, float c, float m)
+{
+    const uint64_t cc = pack2(c, c), mm = pack2(-m, -m);
+    uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+    for (int b = 0; b < 4; b++) {
+        float w[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+            const int i = 32 * b + 2 * j;
+            const float2 e = unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), cc, mm));
+            const float x = exp2_fast(e.x), y = exp2_fast(e.y);
+            if (j & 1)
+                sum1 = add2(sum1, pack2(x, y));
+            else
+                sum0 = add2(sum0, pack2(x, y));
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+            w[j] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&h));
+        }
+        tmem_st16(taddr + 16 * b, w);
+    }
+    const float2 s = unpack2(add2(sum0, sum1));
+    return s.x + s.y;
+}
+
+__global__ void __launch_bounds__(kPrThreads, 1)
+    prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
+                  const __grid_constant__ CUtensorMap mr, const int blocks)
+{
+    extern __shared__ __align__(1024) uint8_t psm_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(psm_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *ring = sm + 2 * kPrQBoxes * kPrBox;
+    __shared__ PromptShared sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int32_t *status = reinterpret_cast<int32_t *>(a.ws);
+    pdl_wait();
+    pdl_trigger();
+    // ---- the block's queries: all blocks of a head together, so that its keys stay in the L2, the longest first
+    const int h = blockIdx.x / blocks;
+    auto queries = [&](int i, int *t0, int *n, int *k0, int *nk) {
+        bool ok = latent_queries(a.seq_start, a.n_seq, a.T, i, t0, n);
+        if (a.kv_start) {
+            const int s0 = a.kv_start[i], s1 = a.kv_start[i + 1];
+            *k0 = s0;
+            *nk = s1 - s0;
+            ok = ok && s0 >= 0 && s1 >= s0 && s1 <= a.S;
+        } else if (!a.seq_start && a.n_seq == 1) {
+            *k0 = 0;
+            *nk = a.S;
+        } else {
+            *k0 = *t0;
+            *nk = *n;
+        }
+        return ok;
+    };
+    int before, t0 = 0, n = 0, k0 = 0, nk = 0;
+    const int seq = find_unit<kPrThreads>(sh.search, a.n_seq, blockIdx.x % blocks, &before, [&](int i) {
+        int t0, n, k0, nk;
+        if (!queries(i, &t0, &n, &k0, &nk)) {
+            set_status(status, K3MOE_DEV_BAD_OFFSETS);
+            return 0;
+        }
+        return (n + 2 * kPrRows - 1) / (2 * kPrRows);
+    });
+    if (seq < 0) return;
+    queries(seq, &t0, &n, &k0, &nk);
+    const int row0 = ((n + 2 * kPrRows - 1) / (2 * kPrRows) - 1 - before) * 2 * kPrRows;
+    // keys that row r of the sequence sees, the tiles of each half, and the first tile that some row does not see whole
+    auto limit = [&](int r) { return a.causal ? min(max(nk - n + 1 + r, 0), nk) : nk; };
+    auto tiles_of = [&](int half) {
+        const int first = row0 + kPrRows * half;
+        return first < n ? (limit(min(n, first + kPrRows) - 1) + kPrTile - 1) / kPrTile : 0;
+    };
+    const int tiles0 = tiles_of(0), tiles1 = tiles_of(1), tiles = max(tiles0, tiles1), whole = limit(row0) / kPrTile;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; i++) {
+            mb_init(&sh.q_full[i], 1);
+            mb_init(&sh.s_full[i], 1);
+            mb_init(&sh.p_ready[i], 4);
+            mb_init(&sh.o_full[i], 1);
+        }
+        for (int i = 0; i < kPrSlots; i++) {
+            mb_init(&sh.full[i], 1);
+            mb_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mb_init(&sh.mend[i], 1);
+            mb_init(&sh.mended[i], 2);
+        }
+        mb_init(&sh.drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sh.bail = 0;
+        sh.spoiled = 0;
+    }
+    if (warp == kPrWarpMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sh.tmem)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    constexpr uint32_t tmem = 0;                              // all 512 columns: the allocation starts at the first
+    auto wait = [&](uint64_t &b, int phase) {
+        const bool ok = mb_wait_asleep(&b, (uint32_t)phase & 1u);
+        if (!ok) {
+            set_status(status, K3MOE_DEV_TIMEOUT);
+            sh.bail = 1;
+        }
+        return (bool)__all_sync(0xffffffffu, ok && !sh.bail);
+    };
+    // the ring's slot of a tile's box: keys, r, values
+    auto slot_of = [](int tile, int box) { return (kPrTileBoxes * tile + box) % kPrSlots; };
+
+    if (warp < kPrWarpMma) {
+        // ---------------- softmax and output of a half
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrRegsRows));
+        const int half = warp >> 2, q = warp & 3, r = row0 + kPrRows * half + 32 * q + lane;
+        const int mine = half ? tiles1 : tiles0;
+        const uint32_t la = tmem + ((uint32_t)(32 * q) << 16), la_s = la + kPrTmS + kPrTile * half, la_o = la + kPrTmO + kLatV * half;
+        const int lim = r < n ? limit(r) : nk;
+        const float c = a.scale * kLatLog2e;
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int i = 0; i < mine; i++) {
+            if (!(ok = wait(sh.s_full[half], i))) break;
+            tc_fence_after();
+            uint32_t v[128];
+#pragma unroll
+            for (int b = 0; b < 8; b++) tmem_ld16_nowait(la_s + 16 * b, *reinterpret_cast<uint32_t(*)[16]>(&v[16 * b]));
+            tmem_wait_ld();
+            if (i >= whole) {
+                const int left = lim - kPrTile * i;
+#pragma unroll
+                for (int j = 0; j < 128; j++) v[j] = j < left ? v[j] : 0xFF800000u;
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 128; j += 8)
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1])));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            if (i == 0) {
+                m = top;
+            } else if (__any_sync(0xffffffffu, top > m + kPrSlack)) {
+                // in order behind S: the product before is done with O
+                const float m1 = top > m + kPrSlack ? top : m, f = m1 == -INFINITY ? 1.0f : exp2_fast(m - m1);
+                m = m1;
+                l *= f;
+#pragma unroll 1
+                for (int b = 0; b < kLatV; b += 16) {
+                    float o[16];
+                    tmem_ld16(la_o + b, o);
+#pragma unroll
+                    for (int j = 0; j < 16; j++) o[j] *= f;
+                    tmem_st16(la_o + b, o);
+                }
+            }
+            l += weigh(v, la_s, c, m == -INFINITY ? 0.0f : m);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mb_arrive(&sh.p_ready[half]);
+        }
+        if (ok && mine > 0) ok = wait(sh.o_full[half], 0);
+        if (ok && __any_sync(0xffffffffu, r < n)) {
+            tc_fence_after();
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const size_t row = (size_t)(t0 + r) * a.H + h;
+            const bool spoiled = sh.spoiled != 0;
+#pragma unroll 1
+            for (int b = 0; b < kLatV; b += 16) {
+                float o[16];
+#pragma unroll
+                for (int j = 0; j < 16; j++) o[j] = 0.0f;
+                if (mine > 0) tmem_ld16(la_o + b, o);
+                if (spoiled && r < n)                         // what was cleared, for the rows that see it
+                    for (int k = kPrTile * whole; k < lim; k++) {
+                        const uint16_t *p = a.kv + (size_t)(k0 + k) * a.kv_stride + (size_t)h * a.kv_head + kLatK + b;
+#pragma unroll
+                        for (int j = 0; j < 16; j++) {
+                            const uint32_t u = p[j];
+                            if ((u & 0x7F80u) == 0x7F80u) o[j] += bf16_bits_to_f32(u);
+                        }
+                    }
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const __nv_bfloat162 x = l == 0.0f ? __floats2bfloat162_rn(0.0f, 0.0f) : __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
+                    w[j] = *reinterpret_cast<const uint32_t *>(&x);
+                }
+                if (r < n) {
+                    uint4 *p = reinterpret_cast<uint4 *>(a.out + row * kLatV + b);
+                    p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
+            if (a.lse && r < n) a.lse[row] = (m + log2f(l)) * kLatLn2;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsLast));
+        if (warp == kPrWarpMma) {
+            // ---------------- products
+            const uint32_t ids = idesc(1, kPrTile), idv = idesc(1, kLatV) | (1u << 16);     // V with its columns contiguous
+            auto scores = [&](int half, int i) {
+                if (i == 0 && !wait(sh.q_full[half], 0)) return false;
+                for (int b = 0; b < kPrQBoxes; b++) {
+                    const int s = slot_of(i, b);
+                    if (!wait(sh.full[s], (kPrTileBoxes * i + b) / kPrSlots)) return false;
+                    tc_fence_after();
+                    const uint32_t A = desc_lo(saddr(sm) + (uint32_t)((half * kPrQBoxes + b) * kPrBox)), B = desc_lo(saddr(ring) + (uint32_t)(s * kPrBox));
+#pragma unroll
+                    for (int k = 0; k < 4; k++) umma_warp(kPrTmS + kPrTile * half, A + 2 * k, B + 2 * k, ids, b > 0 || k > 0);
+                    if (half == 1 || i >= tiles1) umma_commit_warp(&sh.empty[s]);
+                }
+                umma_commit_warp(&sh.s_full[half]);
+                return true;
+            };
+            auto values = [&](int half, int i) {
+                const int s0 = slot_of(i, kPrQBoxes), s1 = slot_of(i, kPrQBoxes + 1), lo = min(s0, s1);
+                if (!wait(sh.full[s0], (kPrTileBoxes * i + kPrQBoxes) / kPrSlots) ||
+                    !wait(sh.full[s1], (kPrTileBoxes * i + kPrQBoxes + 1) / kPrSlots) || (i >= whole && !wait(sh.mended[(i - whole) & 1], (i - whole) >> 1)) ||
+                    !wait(sh.p_ready[half], i))
+                    return false;
+                tc_fence_after();
+                const uint32_t B = desc_lo(saddr(ring) + (uint32_t)(lo * kPrBox), (uint32_t)((max(s0, s1) - lo) * kPrBox));
+#pragma unroll
+                for (int k = 0; k < kPrTile / 16; k++)
+                    umma_ts_warp(kPrTmO + kLatV * half, kPrTmS + kPrTile * half + 8 * k, B + (uint32_t)(k * 16 * 128 >> 4), idv, i > 0 || k > 0);
+                if (half == 1 || i >= tiles1) {
+                    umma_commit_warp(&sh.empty[s0]);
+                    umma_commit_warp(&sh.empty[s1]);
+                }
+                if (i == (half ? tiles1 : tiles0) - 1) umma_commit_warp(&sh.o_full[half]);
+                return true;
+            };
+            // scores a tile ahead of the products with values, a half at a time
+            bool ok = (tiles0 < 1 || scores(0, 0)) && (tiles1 < 1 || scores(1, 0));
+            for (int i = 0; ok && i < tiles; i++) {
+                if (i < tiles0) ok = values(0, i) && (i + 1 >= tiles0 || scores(0, i + 1));
+                if (ok && i < tiles1) ok = values(1, i) && (i + 1 >= tiles1 || scores(1, i + 1));
+            }
+            __syncwarp();
+            umma_commit_warp(&sh.drain);                       // every issued MMA done before the dealloc
+            mb_wait_warp(&sh.drain, 0);
+        } else if (warp == kPrWarpLoad) {
+            // ---------------- loads
+            auto load_q = [&](int half) {
+                mb_expect_tx_warp(&sh.q_full[half], kPrQBoxes * kPrBox);
+                for (int b = 0; b < kPrQBoxes; b++)
+                    tma3d_warp(sm + (half * kPrQBoxes + b) * kPrBox, &mq, 64 * b, h, t0 + row0 + kPrRows * half, &sh.q_full[half]);
+            };
+            int loaded = 0;
+            bool q0 = false, q1 = false;
+            for (int i = 0; i < tiles && !sh.bail; i++) {
+                if (i == 0 && tiles0 > 0) {
+                    load_q(0);
+                    q0 = true;
+                }
+                const int tok = k0 + kPrTile * i;
+                bool ok = true;
+                for (int b = 0; b < kPrTileBoxes; b++, loaded++) {
+                    const int s = loaded % kPrSlots;
+                    if (loaded >= kPrSlots && !(ok = wait(sh.empty[s], loaded / kPrSlots - 1))) break;
+                    uint8_t *dst = ring + s * kPrBox;
+                    mb_expect_tx_warp(&sh.full[s], kPrBox);
+                    if (b < kLatK / 64) {
+                        tma3d_warp(dst, &mkv, 64 * b, h, tok, &sh.full[s]);
+                    } else if (b < kPrQBoxes) {
+                        tma2d_warp(dst, &mr, 0, tok, &sh.full[s]);
+                    } else {
+                        // the values' first columns to the lower slot of the two
+                        const int other = slot_of(i, kPrQBoxes + (b == kPrQBoxes));
+                        tma3d_warp(dst, &mkv, kLatK + (s < other ? 0 : 64), h, tok, &sh.full[s]);
+                    }
+                    if (i == 0 && b == kPrQBoxes - 1 && tiles1 > 0) {
+                        load_q(1);
+                        q1 = true;
+                    }
+                }
+                if (!ok) break;
+                if (i >= whole && lane == 0) mb_arrive(&sh.mend[(i - whole) & 1]);
+            }
+            // the block's shared memory stays until its last copies have landed, when another role gave up too
+            for (int f = max(0, loaded - kPrSlots); f < loaded; f++) mb_wait_warp(&sh.full[f % kPrSlots], (uint32_t)(f / kPrSlots) & 1u);
+            if (q0) mb_wait_warp(&sh.q_full[0], 0);
+            if (q1) mb_wait_warp(&sh.q_full[1], 0);
+        } else {
+            // ---------------- values of tiles that not every row sees whole: tokens behind the sequence's last are cleared, and so is
+            // what is infinite or NaN, which a weight of zero would not keep out (rows that see it add it at the end)
+            const int id = threadIdx.x - 32 * kPrWarpMend;
+            for (int i = whole; i < tiles; i++) {
+                const int s0 = slot_of(i, kPrQBoxes), s1 = slot_of(i, kPrQBoxes + 1);
+                // first for the loads to be on their way: until then the slots' barriers stand at an earlier box
+                if (!wait(sh.mend[(i - whole) & 1], (i - whole) >> 1) || !wait(sh.full[s0], (kPrTileBoxes * i + kPrQBoxes) / kPrSlots) || !wait(sh.full[s1], (kPrTileBoxes * i + kPrQBoxes + 1) / kPrSlots))
+                    break;
+                const int last = nk - kPrTile * i;
+                bool any = false;
+#pragma unroll 4
+                for (int e = id; e < 2 * kPrTile * 8; e += 64) {
+                    const int t = (e >> 3) & (kPrTile - 1);
+                    uint4 *p = reinterpret_cast<uint4 *>(ring + (e >> 10 ? s1 : s0) * kPrBox) + (e & 1023);
+                    uint4 w = *p;
+                    if (t >= last) {
+                        *p = make_uint4(0, 0, 0, 0);
+                    } else if (clear_spoiled(w)) {
+                        *p = w;
+                        any = true;
+                    }
+                }
+                if (any) sh.spoiled = 1;
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mb_arrive(&sh.mended[(i - whole) & 1]);       // two tiles' values are there at most
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kPrWarpMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(512));
+}
+
+}  // namespace
+
+cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t s)
+{
+    CUtensorMap mq{}, mkv{}, mr{};
+    // without keys nothing is loaded by the last two
+    const bool keys = a.S > 0;
+    if (!map16x3(&mq, a.q, (uint64_t)a.T, (uint64_t)a.q_stride, (uint64_t)a.H, (uint64_t)a.q_head, kLatK + kLatR, 1, kPrRows) ||
+        !map16x3(&mkv, keys ? a.kv : a.q, keys ? (uint64_t)a.S : 1, (uint64_t)a.kv_stride, (uint64_t)a.H, (uint64_t)a.kv_head, kLatK + kLatV, 1,
+                 kPrTile) ||
+        !map16s(&mr, keys ? a.rope_key : a.q, keys ? (uint64_t)a.S : 1, kLatR, (uint64_t)a.rope_stride, kPrTile))
+        return cudaErrorInvalidValue;
+    const cudaError_t allowed = once_a_device([] {
+        // the shares of setmaxnreg are of the launch's registers: with another count they would never be there
+        cudaFuncAttributes fa{};
+        if (cudaFuncGetAttributes(&fa, prompt_kernel) != cudaSuccess || fa.numRegs != kPrRegs) return cudaErrorInvalidConfiguration;
+        return cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrSmem);
+    });
+    if (allowed != cudaSuccess) return allowed;
+    const int blocks = a.seq_start ? a.T / (2 * kPrRows) + std::min(a.n_seq, a.T)
+                                   : a.n_seq == 1 ? (a.T + 2 * kPrRows - 1) / (2 * kPrRows) : a.n_seq;
+    timing_begin("latent_prompt", s);
+    const cudaError_t err = launch_pdl(prompt_kernel, dim3((unsigned)(blocks * a.H)), dim3(kPrThreads), kPrSmem, s, a, mq, mkv, mr, blocks);
+    count_launch();
+    timing_end("latent_prompt", s);
+    return err;
+}
+
+}  // namespace k3moe
