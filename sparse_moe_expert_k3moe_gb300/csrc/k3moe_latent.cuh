@@ -27,41 +27,58 @@ __device__ __forceinline__ bool latent_queries(const int32_t *start, int n_seq, 
     return s0 >= 0 && s1 >= s0 && s1 <= T;
 }
 
-// A block's search for unit `want` over the sequences, count(i) units each, all threads at once: the sequence
-// it is of (-1: there are not as many) and how many units of it come before.
+// A block's search over the sequences, count(i) units each, by all threads at once: which one unit want(total) is
+// of (-1: there are not as many), how many units of it come before, and the units in all.
 struct UnitSearch {
-    int sums[32], seq, before;
+    long long sums[32], before;
+    int seq;
 };
-template <int THREADS, typename Count>
-__device__ __forceinline__ int find_unit(UnitSearch &sh, int n_seq, int want, int *before, Count count)
+template <int THREADS, typename Count, typename Want>
+__device__ __forceinline__ int find_unit(UnitSearch &sh, int n_seq, long long *before, long long *total, Count count, Want want)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) sh.seq = -1;
-    int base = 0;
-    for (int i0 = 0; i0 < n_seq; i0 += THREADS) {
-        const int i = i0 + threadIdx.x;
-        const int mine = i < n_seq ? count(i) : 0;
-        int upto = mine;                                      // of the warp's lanes up to this one
+    // units of this thread's sequence of the THREADS from i0 on, those before it (from `base` on), and all of them
+    auto scan = [&](int i0, long long *mine, long long *all) {
+        *mine = i0 + (int)threadIdx.x < n_seq ? count(i0 + threadIdx.x) : 0;
+        long long upto = *mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += v;
         }
         __syncthreads();
         if (lane == 31) sh.sums[warp] = upto;
         __syncthreads();
-        int ahead = base, all = base;
+        long long ahead = 0;
+        *all = 0;
         for (int w = 0; w < THREADS / 32; w++) {
             if (w < warp) ahead += sh.sums[w];
-            all += sh.sums[w];
+            *all += sh.sums[w];
         }
-        const int from = ahead + upto - mine;
-        if (mine > 0 && want >= from && want < from + mine) {
-            sh.seq = i;
-            sh.before = want - from;
+        return ahead + upto - *mine;
+    };
+    auto keep = [&](int i0, long long from, long long mine, long long unit) {
+        if (unit >= from && unit < from + mine) {
+            sh.seq = i0 + threadIdx.x;
+            sh.before = unit - from;
         }
-        base = all;
-        if (want < base) break;
+    };
+    long long mine, all, from = scan(0, &mine, &all);
+    *total = all;
+    if (n_seq <= THREADS) {
+        keep(0, from, mine, want(all));
+    } else {
+        for (int i0 = THREADS; i0 < n_seq; i0 += THREADS) {
+            scan(i0, &mine, &all);
+            *total += all;
+        }
+        long long base = 0;
+        const long long unit = want(*total);
+        for (int i0 = 0; i0 < n_seq && base <= unit; i0 += THREADS, base += all) {
+            from = base + scan(i0, &mine, &all);
+            keep(i0, from, mine, unit);
+        }
     }
     __syncthreads();
     *before = sh.before;

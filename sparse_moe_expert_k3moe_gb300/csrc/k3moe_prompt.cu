@@ -95,18 +95,22 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         return ok;
     };
-    int before, t0 = 0, n = 0, k0 = 0, nk = 0;
-    const int seq = find_unit<kPrThreads>(sh.search, a.n_seq, blockIdx.x % blocks, &before, [&](int i) {
-        int t0, n, k0, nk;
-        if (!queries(i, &t0, &n, &k0, &nk)) {
-            set_status(status, K3MOE_DEV_BAD_OFFSETS);
-            return 0;
-        }
-        return (n + 2 * kPrRows - 1) / (2 * kPrRows);
-    });
+    int t0 = 0, n = 0, k0 = 0, nk = 0;
+    long long before, total;
+    const int seq = find_unit<kPrThreads>(
+        sh.search, a.n_seq, &before, &total,
+        [&](int i) -> long long {
+            int t0, n, k0, nk;
+            if (!queries(i, &t0, &n, &k0, &nk)) {
+                set_status(status, K3MOE_DEV_BAD_OFFSETS);
+                return 0;
+            }
+            return (n + 2 * kPrRows - 1) / (2 * kPrRows);
+        },
+        [&](long long) { return (long long)(blockIdx.x % blocks); });
     if (seq < 0) return;
     queries(seq, &t0, &n, &k0, &nk);
-    const int row0 = ((n + 2 * kPrRows - 1) / (2 * kPrRows) - 1 - before) * 2 * kPrRows;
+    const int row0 = ((n + 2 * kPrRows - 1) / (2 * kPrRows) - 1 - (int)before) * 2 * kPrRows;
     // keys that row r of the sequence sees, the tiles of each half, and the first tile that some row does not see whole
     auto limit = [&](int r) { return a.causal ? min(max(nk - n + 1 + r, 0), nk) : nk; };
     auto tiles_of = [&](int half) {
