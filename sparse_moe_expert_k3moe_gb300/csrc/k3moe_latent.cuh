@@ -27,6 +27,19 @@ __device__ __forceinline__ bool latent_queries(const int32_t *start, int n_seq, 
     return s0 >= 0 && s1 >= s0 && s1 <= T;
 }
 
+// A warp's wait on a barrier's phase, asleep and bounded; false when it gave up (with the status bit) or another role
+// did.  A call of its own, not in line: the roles of a block share the instruction cache, and with every wait, walk and
+// loop written out (181 KB of code) each step of a role waited for its instructions.
+__device__ __noinline__ bool role_wait(uint64_t *b, int phase, int32_t *status, volatile int *bail)
+{
+    const bool ok = mb_wait_asleep(b, (uint32_t)phase & 1u);
+    if (!ok) {
+        set_status(status, K3MOE_DEV_TIMEOUT);
+        *bail = 1;
+    }
+    return (bool)__all_sync(0xffffffffu, ok && !*bail);
+}
+
 // A block's search over the sequences, count(i) units each, by all threads at once: which one unit want(total) is
 // of (-1: there are not as many), how many units of it come before, and the units in all.
 struct UnitSearch {

@@ -249,16 +249,21 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (warp == kPrWarpMma) {
             // ---------------- products
             const uint32_t ids = idesc(1, kPrTile), idv = idesc(1, kLatV) | (1u << 16);     // V with its columns contiguous
+            const int n0 = uniform(tiles0), n1 = uniform(tiles1), n = max(n0, n1), mend0 = uniform(whole);
+            const uint32_t sm_q = desc_lo(saddr(sm)), sm_kv = desc_lo(saddr(ring), 0);
+            constexpr uint32_t box = kPrBox >> 4;
             auto scores = [&](int half, int i) {
                 if (i == 0 && !wait(sh.q_full[half], 0)) return false;
-                for (int b = 0; b < kPrQBoxes; b++) {
+                uint32_t A = sm_q + (uint32_t)half * kPrQBoxes * box;
+#pragma unroll
+                for (int b = 0; b < kPrQBoxes; b++, A += box) {
                     const int s = slot_of(i, b);
                     if (!wait(sh.full[s], (kPrTileBoxes * i + b) / kPrSlots)) return false;
                     tc_fence_after();
-                    const uint32_t A = desc_lo(saddr(sm) + (uint32_t)((half * kPrQBoxes + b) * kPrBox)), B = desc_lo(saddr(ring) + (uint32_t)(s * kPrBox));
+                    const uint32_t B = sm_kv + (uint32_t)s * box;
 #pragma unroll
                     for (int k = 0; k < 4; k++) umma_warp(kPrTmS + kPrTile * half, A + 2 * k, B + 2 * k, ids, b > 0 || k > 0);
-                    if (half == 1 || i >= tiles1) umma_commit_warp(&sh.empty[s]);
+                    if (half == 1 || i >= n1) umma_commit_warp(&sh.empty[s]);
                 }
                 umma_commit_warp(&sh.s_full[half]);
                 return true;
@@ -266,26 +271,26 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             auto values = [&](int half, int i) {
                 const int s0 = slot_of(i, kPrQBoxes), s1 = slot_of(i, kPrQBoxes + 1), lo = min(s0, s1);
                 if (!wait(sh.full[s0], (kPrTileBoxes * i + kPrQBoxes) / kPrSlots) ||
-                    !wait(sh.full[s1], (kPrTileBoxes * i + kPrQBoxes + 1) / kPrSlots) || (i >= whole && !wait(sh.mended[(i - whole) & 1], (i - whole) >> 1)) ||
-                    !wait(sh.p_ready[half], i))
+                    !wait(sh.full[s1], (kPrTileBoxes * i + kPrQBoxes + 1) / kPrSlots) ||
+                    (i >= mend0 && !wait(sh.mended[(i - mend0) & 1], (i - mend0) >> 1)) || !wait(sh.p_ready[half], i))
                     return false;
                 tc_fence_after();
-                const uint32_t B = desc_lo(saddr(ring) + (uint32_t)(lo * kPrBox), (uint32_t)((max(s0, s1) - lo) * kPrBox));
+                const uint32_t B = sm_kv + (uint32_t)lo * box + ((uint32_t)(max(s0, s1) - lo) * box << 16);
 #pragma unroll
                 for (int k = 0; k < kPrTile / 16; k++)
                     umma_ts_warp(kPrTmO + kLatV * half, kPrTmS + kPrTile * half + 8 * k, B + (uint32_t)(k * 16 * 128 >> 4), idv, i > 0 || k > 0);
-                if (half == 1 || i >= tiles1) {
+                if (half == 1 || i >= n1) {
                     umma_commit_warp(&sh.empty[s0]);
                     umma_commit_warp(&sh.empty[s1]);
                 }
-                if (i == (half ? tiles1 : tiles0) - 1) umma_commit_warp(&sh.o_full[half]);
+                if (i == (half ? n1 : n0) - 1) umma_commit_warp(&sh.o_full[half]);
                 return true;
             };
             // scores a tile ahead of the products with values, a half at a time
-            bool ok = (tiles0 < 1 || scores(0, 0)) && (tiles1 < 1 || scores(1, 0));
-            for (int i = 0; ok && i < tiles; i++) {
-                if (i < tiles0) ok = values(0, i) && (i + 1 >= tiles0 || scores(0, i + 1));
-                if (ok && i < tiles1) ok = values(1, i) && (i + 1 >= tiles1 || scores(1, i + 1));
+            bool ok = (n0 < 1 || scores(0, 0)) && (n1 < 1 || scores(1, 0));
+            for (int i = 0; ok && i < n; i++) {
+                if (i < n0) ok = values(0, i) && (i + 1 >= n0 || scores(0, i + 1));
+                if (ok && i < n1) ok = values(1, i) && (i + 1 >= n1 || scores(1, i + 1));
             }
             __syncwarp();
             umma_commit_warp(&sh.drain);                       // every issued MMA done before the dealloc

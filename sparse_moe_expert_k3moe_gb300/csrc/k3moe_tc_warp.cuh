@@ -25,6 +25,9 @@ __device__ __forceinline__ void prefetch_bulk(const void *src, uint32_t bytes)
 // addresses stay uniform over the warp, which makes the issue of a small MMA several times
 // cheaper than from inside a single lane's branch (measured 160 clocks apart there for
 // 128 x 64 x 16 MMAs that take 32).
+// A value that all lanes hold, as one that the compiler knows to be the same: what descriptors and
+// the loops around them come from, read from memory, is passed through this.
+__device__ __forceinline__ int uniform(int v) { return (int)__reduce_max_sync(0xffffffffu, (unsigned)v); }
 // A descriptor's halves: `lo` has the address (and the leading offset), the upper half is a
 // constant of the layout, so that one addition makes the next descriptor.  In a cluster a
 // shared address holds the block's rank above its low 18 bits, which are all that go in.
@@ -65,6 +68,17 @@ __device__ __forceinline__ void tma3d_warp(void *dst, const CUtensorMap *m, int 
         "[%5];\n\t}" ::"r"(saddr(dst)),
         "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(saddr(bar))
         : "memory");
+}
+// Whether a barrier's phase is complete, without waiting.
+__device__ __forceinline__ bool mb_test_warp(uint64_t *b, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(saddr(b)), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, done != 0);
 }
 // A operand in tensor memory (two 16-bit elements of K a column), B in shared memory.
 template <uint32_t kHi = kDescSw128>
