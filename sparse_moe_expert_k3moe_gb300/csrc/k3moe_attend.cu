@@ -7,8 +7,8 @@
 // c.  Softmax in powers of two as in the expanded form; a query's maximum moves only when it is outdone by 2^8, so that a
 // tile mostly needs no more than a vote.
 //
-// Bound by the cache's bytes: 1152 a row against 64 x 2176 flops.  A tile is 72 KB, and the ring beside the queries (72 KB)
-// holds not quite two: with tiles of 128 rows nothing could be loaded under a tile's softmax, all SMs loaded and computed in
+// Bound by the cache's bytes: 1152 a row against 64 x 2176 flops.  A tile is 72 KB, and beside the queries (72 KB) there is
+// room for two: with tiles of 128 rows nothing could be loaded under a tile's softmax, all SMs loaded and computed in
 // step, and the DRAM was idle half of the time (96 sequences: 158 us).  All tiles of all sequences are one line that is cut
 // into as many even parts as there are SMs; a query block that a cut goes through leaves its parts' sums (float) in the
 // workspace, and a second kernel joins them.
@@ -24,7 +24,7 @@ namespace {
 constexpr int kAtRows = 64, kAtTile = 64;                     // queries of a block, cached rows of a tile
 constexpr int kAtBoxes = kLatRow / 64;                        // 64-column boxes of a tile: c's eight, then r's
 constexpr int kAtBox = kAtTile * 128;                         // 8 KB
-constexpr int kAtSlots = 17;                                  // c of even tiles, c of odd tiles, r of either
+constexpr int kAtSlots = 2 * kAtBoxes;                        // c of even and of odd tiles, then r of both
 constexpr int kAtQBox = kAtRows * 128;
 constexpr int kAtQ = kAtBoxes * kAtQBox, kAtP = kAtTile * kAtRows * 2;
 constexpr int kAtSmem = 1024 + kAtQ + kAtP + kAtSlots * kAtBox;
@@ -43,14 +43,22 @@ struct AttendJoin {
 };
 
 struct AttendShared {
-    uint64_t q_full, full[2][2], empty[2][4], r_empty, s_full[2], p_ready[2], pv_done, drain[2];    // by the tile's turn: half of c; its pairs
+    uint64_t q_full, full[2][2], empty[2][2], r_empty[2], s_full[2], p_ready[2], pv_done, drain[2];    // by the tile's turn, halves of c
     uint32_t tmem;
     volatile int bail;
     int spoiled[2];                                           // by the query block's turn
-    float top[2][4][32], m[kAtRows], f[kAtRows], sum[2][4][32], inv[kAtRows];
-    int lim[2][kAtRows];
-    UnitSearch search;
+    union {                                                   // (one after the other)
+        UnitSearch search;
+        float top[2][4][32], sum[2][4][32];
+    };
+    float m[kAtRows];
+    union {
+        float f[kAtRows], inv[kAtRows];
+    };
+    int lim[2][32];
 };
+
+static_assert(sizeof(AttendShared) <= 2048 && kAtSmem + 2048 <= 227 * 1024, "an SM's shared memory");
 
 // Sequence i: its queries, cached rows, blocks of queries and tiles of each; false when something does not fit.
 struct AttendSeq {
@@ -81,7 +89,7 @@ struct AttendWalk {
         base = from - before;
         if (u < end) s.read(a, i);
     }
-    __device__ __noinline__ bool next(const AttendArgs &a)
+    __device__ bool next(const AttendArgs &a)
     {
         if (u >= end) return false;
         while (u >= base + s.units()) {
@@ -89,7 +97,7 @@ struct AttendWalk {
             s.read(a, ++seq);
         }
         const long long at = u - base;
-        const int block = (int)(at / s.tiles);
+        const int block = (int)quotient(at, s.tiles);
         row0 = block * kAtRows;
         tile0 = (int)(at - (long long)block * s.tiles);
         tile1 = (int)min((long long)s.tiles, tile0 + (end - u));
@@ -135,7 +143,7 @@ __device__ __forceinline__ bool group_any(int group, bool p)
     return r != 0;
 }
 __global__ void __launch_bounds__(kAtThreads, 1)
-    attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap mc, float *parts, AttendJoin *joins)
+    attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap m4, const __grid_constant__ CUtensorMap m1, float *parts, AttendJoin *joins)
 {
     extern __shared__ __align__(1024) uint8_t asm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(asm_raw) + 1023) & ~(uintptr_t)1023);
@@ -146,27 +154,29 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     if (threadIdx.x == 0) {
         mb_init(&sh.q_full, 8);
         for (int i = 0; i < 2; i++) {
-            for (int j = 0; j < 2; j++) mb_init(&sh.full[i][j], 1);
-            for (int j = 0; j < 4; j++) mb_init(&sh.empty[i][j], 1);
+            for (int j = 0; j < 2; j++) {
+                mb_init(&sh.full[i][j], 1);
+                mb_init(&sh.empty[i][j], 1);
+            }
+            mb_init(&sh.r_empty[i], 1);
             mb_init(&sh.s_full[i], 1);
             mb_init(&sh.p_ready[i], 8);
             mb_init(&sh.drain[i], 1);
         }
-        mb_init(&sh.r_empty, 1);
         mb_init(&sh.pv_done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.bail = 0;
         sh.spoiled[0] = sh.spoiled[1] = 0;
-        prefetch_map(&mc);
+        prefetch_map(&m4);
+        prefetch_map(&m1);
     }
     pdl_wait();
     pdl_trigger();
     long long before, units;
-    // even shares, fewer of them than blocks where there are fewer tiles
-    const auto share = [&](long long i, long long all) {
-        if (all <= gridDim.x) return min(i, all);
-        const long long each = all / gridDim.x, more = all - each * gridDim.x;
-        return i * each + min(i, more);
+    // even shares of `each` tiles and the first ones a tile more; fewer shares than blocks where there are fewer tiles
+    const auto share = [&](int i, long long all) {
+        const long long each = quotient(all, gridDim.x);
+        return i * each + min((long long)i, all - each * gridDim.x);
     };
     const int seq0 = find_unit<kAtThreads>(
         sh.search, a.n_seq, &before, &units,
@@ -374,33 +384,46 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             tc_fence_after();
             const bool spoiled = *const_cast<volatile int *>(&sh.spoiled[seg & 1]) != 0;
             const int count = ok ? min(32, rows - 32 * g) : 0;
+            // 16 queries at a time, a thread four columns of c
 #pragma unroll 1
-            for (int b = 0; b < 8; b++) {
-                const int at_c = 128 * (b >> 1) + 32 * q + lane, r0 = 32 * g + 16 * (b & 1);   // of c; the first of 16 queries
-                float o[16];
-                tmem_ld16(la + kAtTmO + 64 * (b >> 1) + r0, o);
+            for (int b = 0; b < 2; b++) {
+                const int r0 = 32 * g + 16 * b, left = min(16, count - 16 * b);
+                if (left <= 0) break;
+                uint32_t o[4][16];
+#pragma unroll
+                for (int k = 0; k < 4; k++) tmem_ld16_nowait(la + kAtTmO + 64 * k + r0, o[k]);
+                tmem_wait_ld();
                 if (spoiled)
 #pragma unroll 1
                     for (int at = max(least, kAtTile * now.tile0); at < min(now.s.len, kAtTile * now.tile1); at++) {
                         const int page = a.pages[(size_t)now.seq * a.max_pages + at / a.page];
                         if (page < 0 || page >= a.n_pages) continue;
-                        const uint32_t x = a.cache[((size_t)page * a.page + at % a.page) * kLatRow + at_c];
-                        if ((x & 0x7F80u) != 0x7F80u) continue;
+                        const uint16_t *from = a.cache + ((size_t)page * a.page + at % a.page) * kLatRow + 32 * q + lane;
 #pragma unroll
-                        for (int j = 0; j < 16; j++)
-                            if (at < lim[16 * (b & 1) + j]) o[j] += bf16_bits_to_f32(x);
+                        for (int k = 0; k < 4; k++) {
+                            const uint32_t x = from[128 * k];
+                            if ((x & 0x7F80u) != 0x7F80u) continue;
+#pragma unroll
+                            for (int j = 0; j < 16; j++)
+                                if (at < lim[16 * b + j]) o[k][j] = __float_as_uint(__uint_as_float(o[k][j]) + bf16_bits_to_f32(x));
+                        }
                     }
-                const int left = min(16, count - 16 * (b & 1));
                 if (whole) {
-                    __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(a.out) + ((size_t)now.s.t0 * a.H + now.row0 + r0) * kLatC + at_c;
+                    __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(a.out) + ((size_t)now.s.t0 * a.H + now.row0 + r0) * kLatC + 32 * q + lane;
 #pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        if (j < left) p[(size_t)j * kLatC] = __float2bfloat16_rn(sh.inv[r0 + j] == 0.0f ? 0.0f : o[j] * sh.inv[r0 + j]);
+                    for (int j = 0; j < 16; j++) {
+                        const float inv = sh.inv[r0 + j];
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            if (j < left) to[j * kLatC + 128 * k] = __float2bfloat16_rn(inv == 0.0f ? 0.0f : __uint_as_float(o[k][j]) * inv);
+                    }
                 } else {
-                    float *p = part + (size_t)r0 * kLatC + at_c;
+                    uint32_t *to = reinterpret_cast<uint32_t *>(part) + (size_t)r0 * kLatC + 32 * q + lane;
 #pragma unroll
                     for (int j = 0; j < 16; j++)
-                        if (j < left) p[(size_t)j * kLatC] = o[j];
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            if (j < left) to[j * kLatC + 128 * k] = o[k][j];
                 }
             }
             tc_fence_before();                                // the next query block's first product is after its weights
@@ -429,8 +452,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 };
                 if (!(ok = wait(sh.full[turn][0], tile >> 1))) break;
                 tc_fence_after();
-                product(c0 + 16 * box, q0 + 8 * q_box, true);
-                umma_commit_warp(&sh.r_empty);
+                product(c0 + (16 + turn) * box, q0 + 8 * q_box, true);
+                umma_commit_warp(&sh.r_empty[turn]);
 #pragma unroll
                 for (int b = 0; b < 4; b++) product(c0 + (8 * turn + b) * box, q0 + b * q_box, false);
                 if (!(ok = wait(sh.full[turn][1], tile >> 1))) break;
@@ -463,7 +486,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kAtTile / 16; k++)
                         umma_warp(kAtTmO + 64 * b, A + 2 * b * box + (uint32_t)(k * 16 * 128 >> 4), p0 + (uint32_t)(k * 16 * 128 >> 4), id, t > 0 || k > 0);
-                    umma_commit_warp(&sh.empty[turn][b]);
+                    if (b & 1) umma_commit_warp(&sh.empty[turn][b >> 1]);
                 }
                 umma_commit_warp(&sh.pv_done);
             }
@@ -495,32 +518,30 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 const int n = uniform(__popc(__ballot_sync(0xffffffffu, row >= 0)));
                 const int row0 = uniform(__shfl_sync(0xffffffffu, row, 0));
                 uint64_t *full = &sh.full[turn][half];
-                auto load = [&](int slot, int col) {
+                const uint32_t rows_bytes = (uint32_t)(box_rows * 128);
+                auto load = [&](int slot, int group) {
                     uint8_t *dst = ring + slot * kAtBox;
-                    if (n > 0) tma2d_warp(dst, &mc, col, row0, full);
+                    if (n > 0) tma3d_warp(dst, &m1, 0, row0, group, full);
 #pragma unroll 1
-                    for (int j = 1; j < n; j++)
-                        tma2d_warp(dst + j * box_rows * 128, &mc, col, uniform(__shfl_sync(0xffffffffu, row, j)), full);
+                    for (int j = 1; j < n; j++) tma3d_warp(dst + j * rows_bytes, &m1, 0, uniform(__shfl_sync(0xffffffffu, row, j)), group, full);
                 };
-                if (tile >= 2 && !(ok = wait(sh.empty[turn][2 * half], phase - 1))) break;
-                mb_expect_tx_warp(full, (uint32_t)((half == 0 ? 5 : 4) * n * box_rows * 128));
-                load(8 * turn + 4 * half, 256 * half);
-                load(8 * turn + 4 * half + 1, 256 * half + 64);
-                if (tile >= 2 && !(ok = wait(sh.empty[turn][2 * half + 1], phase - 1))) break;
-                load(8 * turn + 4 * half + 2, 256 * half + 128);
-                load(8 * turn + 4 * half + 3, 256 * half + 192);
-                if (half == 0) {
-                    if (tile >= 1 && !(ok = wait(sh.r_empty, tile - 1))) break;
-                    load(16, kLatC);
+                if (tile >= 2 && (!(ok = wait(sh.empty[turn][half], phase - 1)) || (half == 0 && !(ok = wait(sh.r_empty[turn], phase - 1))))) break;
+                mb_expect_tx_warp(full, (half == 0 ? 5 : 4) * n * rows_bytes);
+                if (box_rows == kAtTile) {                    // half of c's boxes are one copy
+                    if (n > 0) tma3d_warp(ring + (8 * turn + 4 * half) * kAtBox, &m4, 0, row0, 4 * half, full);
+                } else {
+#pragma unroll 1
+                    for (int b = 0; b < 4; b++) load(8 * turn + 4 * half + b, 4 * half + b);
                 }
+                if (half == 0) load(16 + turn, 8);
             }
             // the query block that a cut leaves unfinished, for the second kernel: its first part writes it down
             last = w.u >= w.end && w.tile0 == 0 && w.tile1 < w.s.tiles;
             if (last && half == 0 && lane == 0) {
-                const long long done = w.u + (w.s.tiles - w.tile1);
-                int parts = 1;
-                while (share(blockIdx.x + parts, units) < done) parts++;
-                joins[blockIdx.x] = AttendJoin{w.s.t0, w.row0, w.rows(a), seg > 0, parts};
+                // the share that has the query block's last tile
+                const long long at = w.u + (w.s.tiles - w.tile1) - 1, each = quotient(units, gridDim.x), more = units - each * gridDim.x;
+                const long long in = at < more * (each + 1) ? at / (each + 1) : more + (at - more * (each + 1)) / each;
+                joins[blockIdx.x] = AttendJoin{w.s.t0, w.row0, w.rows(a), seg > 0, (int)(in - blockIdx.x) + 1};
             }
         }
         if (!last && half == 0 && lane == 0) joins[blockIdx.x].rows = 0;
@@ -535,23 +556,28 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining
-// out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over the parts i in order, M the largest m.  A block takes one query at
-// a time, a thread four columns, sixteen parts' loads in flight.
-constexpr int kJoinThreads = 128, kJoinDeep = 16, kMaxShares = 512;
+// out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over the parts i, M the largest m.  Where a query block has few parts a
+// warp takes a query, a lane 16 columns; where it has many, a block takes 128 columns of a query, its warps every fourth part.
+constexpr int kJoinThreads = 128, kMaxShares = 512, kJoinMany = 8;
 
 __global__ void __launch_bounds__(kJoinThreads)
     attend_join_kernel(const AttendArgs a, const float *parts, const AttendJoin *joins, const int shares)
 {
     pdl_wait();
     pdl_trigger();
-    __shared__ int upto[kMaxShares];                          // queries of the joins up to each
-    __shared__ float weight[kMaxShares], sums[kMaxShares];
+    __shared__ int upto[kMaxShares];                          // pieces of work of the joins up to each
     __shared__ int warp_sum[kJoinThreads / 32];
+    __shared__ float4 sum[3][32];
+    __shared__ float weights[3];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int total = 0;
     for (int i0 = 0; i0 < shares; i0 += kJoinThreads) {
         const int i = i0 + threadIdx.x;
-        int v = i < shares ? joins[i].rows : 0;
+        int v = 0;
+        if (i < shares) {
+            const int rows = joins[i].rows;
+            if (rows > 0) v = joins[i].parts >= kJoinMany ? 4 * rows : (rows + 3) / 4;
+        }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, v, o);
@@ -577,40 +603,95 @@ __global__ void __launch_bounds__(kJoinThreads)
                 lo = mid + 1;
         }
         const AttendJoin j = joins[lo];
-        const int r = unit - (upto[lo] - j.rows);
+        const bool many = j.parts >= kJoinMany;
+        const int piece = unit - (lo > 0 ? upto[lo - 1] : 0), r = many ? piece >> 2 : 4 * piece + warp;
         const float *p0 = parts + (size_t)(2 * lo + j.second) * kAtPart, *p1 = parts + (size_t)(2 * lo + 2) * kAtPart;
         auto part = [&](int p) { return p == 0 ? p0 : p1 + (size_t)(p - 1) * 2 * kAtPart; };
-        for (int p = threadIdx.x; p < j.parts; p += kJoinThreads) {
-            weight[p] = part(p)[kAtRows * kLatC + r];
-            sums[p] = part(p)[kAtRows * kLatC + kAtRows + r];
-        }
-        __syncthreads();
-        float M = -INFINITY, L = 0.0f;
-        for (int p = 0; p < j.parts; p++) M = fmaxf(M, weight[p]);
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const size_t at = (size_t)r * kLatC + 4 * threadIdx.x;
-        for (int p = 0; p < j.parts; p += kJoinDeep) {
-            float4 x[kJoinDeep];
+        if (!many && r >= j.rows) continue;
+        float M = -INFINITY;                                  // of all parts
+        for (int p = lane; p < j.parts; p += 32) M = fmaxf(M, part(p)[kAtRows * kLatC + r]);
 #pragma unroll
-            for (int k = 0; k < kJoinDeep; k++)
-                if (p + k < j.parts) x[k] = __ldcg(reinterpret_cast<const float4 *>(part(p + k) + at));
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        // a warp's parts `from`, `from` + step ..: their factors by the lanes, the columns four parts at a time
+        const int from = many ? warp : 0, step = many ? 4 : 1, n = (j.parts - from + step - 1) / step;
+        const size_t col = (size_t)r * kLatC + (many ? 128 * (piece & 3) : 0) + 4 * lane;
+        float4 o[4] = {};
+        float L = 0.0f;
+        for (int b = 0; b < n; b += 32) {
+            float f = 0.0f, l = 0.0f;
+            if (b + lane < n) {
+                const float *x = part(from + (b + lane) * step) + kAtRows * kLatC + r;
+                f = x[0] == -INFINITY ? 0.0f : exp2_fast(x[0] - M);
+                l = f == 0.0f ? 0.0f : f * x[kAtRows];
+            }
+            L += l;
+            const int left = min(32, n - b);
+            if (many) {
+#pragma unroll 1
+                for (int k = 0; k < left; k += 8) {
+                    float4 x[8];
 #pragma unroll
-            for (int k = 0; k < kJoinDeep; k++)
-                if (p + k < j.parts && weight[p + k] != -INFINITY) {
-                    const float f = exp2_fast(weight[p + k] - M);
-                    L = fmaf(f, sums[p + k], L);
-                    o.x = fmaf(f, x[k].x, o.x);
-                    o.y = fmaf(f, x[k].y, o.y);
-                    o.z = fmaf(f, x[k].z, o.z);
-                    o.w = fmaf(f, x[k].w, o.w);
+                    for (int i = 0; i < 8; i++)
+                        if (k + i < left) x[i] = __ldcg(reinterpret_cast<const float4 *>(part(from + (b + k + i) * step) + col));
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const float w = __shfl_sync(0xffffffffu, f, (k + i) & 31);
+                        if (k + i < left && w != 0.0f) {
+                            o[0].x = fmaf(w, x[i].x, o[0].x);
+                            o[0].y = fmaf(w, x[i].y, o[0].y);
+                            o[0].z = fmaf(w, x[i].z, o[0].z);
+                            o[0].w = fmaf(w, x[i].w, o[0].w);
+                        }
+                    }
                 }
+            } else {
+#pragma unroll 2
+                for (int k = 0; k < left; k++) {
+                    const float w = __shfl_sync(0xffffffffu, f, k);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(part(b + k) + col + 128 * i));
+                        if (w != 0.0f) {
+                            o[i].x = fmaf(w, x.x, o[i].x);
+                            o[i].y = fmaf(w, x.y, o[i].y);
+                            o[i].z = fmaf(w, x.z, o[i].z);
+                            o[i].w = fmaf(w, x.w, o[i].w);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
+        if (many) {                                           // the first warp adds the others'
+            if (warp > 0) {
+                sum[warp - 1][lane] = o[0];
+                if (lane == 0) weights[warp - 1] = L;
+            }
+            __syncthreads();
+            if (warp == 0)
+#pragma unroll
+                for (int k = 0; k < 3; k++) {
+                    const float4 x = sum[k][lane];
+                    o[0].x += x.x;
+                    o[0].y += x.y;
+                    o[0].z += x.z;
+                    o[0].w += x.w;
+                    L += weights[k];
+                }
+            __syncthreads();
+            if (warp > 0) continue;
         }
         const size_t row = (size_t)j.t0 * a.H + j.row0 + r;
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
-        *reinterpret_cast<uint2 *>(a.out + row * kLatC + 4 * threadIdx.x) = *reinterpret_cast<const uint2 *>(w);
-        if (a.lse && threadIdx.x == 0) a.lse[row] = (M + log2f(L)) * kLatLn2;
-        __syncthreads();
+        uint16_t *to = a.out + row * kLatC + (many ? 128 * (piece & 3) : 0) + 4 * lane;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if (many && i > 0) break;
+            const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o[i].x * inv, o[i].y * inv), __floats2bfloat162_rn(o[i].z * inv, o[i].w * inv)};
+            *reinterpret_cast<uint2 *>(to + 128 * i) = *reinterpret_cast<const uint2 *>(w);
+        }
+        if (a.lse && lane == 0 && (!many || (piece & 3) == 0)) a.lse[row] = (M + log2f(L)) * kLatLn2;
     }
 }
 
@@ -627,8 +708,12 @@ size_t latent_workspace(const k3moe_latent_config &lc, int n_seq, int T)
 
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
 {
-    CUtensorMap mc{};
-    if (!map16s(&mc, a.cache, (uint64_t)a.n_pages * a.page, kLatRow, kLatRow, (uint32_t)std::min(a.page, kAtTile))) return cudaErrorInvalidValue;
+    // the cache as [9 boxes of columns][rows][64]: boxes of a page's or a tile's rows, four of columns at once or one
+    CUtensorMap m4{}, m1{};
+    const uint64_t rows = (uint64_t)a.n_pages * a.page;
+    const uint32_t box_rows = (uint32_t)std::min(a.page, kAtTile);
+    if (!map16x3(&m4, a.cache, kAtBoxes, 64, rows, kLatRow, 64, box_rows, 4) || !map16x3(&m1, a.cache, kAtBoxes, 64, rows, kLatRow, 64, box_rows, 1))
+        return cudaErrorInvalidValue;
     const cudaError_t allowed =
         once_a_device([] { return cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem); });
     if (allowed != cudaSuccess) return allowed;
@@ -636,7 +721,7 @@ cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
     AttendJoin *joins = reinterpret_cast<AttendJoin *>(a.ws + kCtrOffset + kCtrBytes);
     float *parts = reinterpret_cast<float *>(a.ws + kCtrOffset + kCtrBytes + align256((size_t)shares * sizeof(AttendJoin)));
     timing_begin("latent_attend", s);
-    cudaError_t err = launch_pdl(attend_kernel, dim3((unsigned)shares), dim3(kAtThreads), kAtSmem, s, a, mc, parts, joins);
+    cudaError_t err = launch_pdl(attend_kernel, dim3((unsigned)shares), dim3(kAtThreads), kAtSmem, s, a, m4, m1, parts, joins);
     count_launch();
     timing_end("latent_attend", s);
     if (err != cudaSuccess) return err;

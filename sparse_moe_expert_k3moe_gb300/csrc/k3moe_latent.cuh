@@ -27,18 +27,8 @@ __device__ __forceinline__ bool latent_queries(const int32_t *start, int n_seq, 
     return s0 >= 0 && s1 >= s0 && s1 <= T;
 }
 
-// A warp's wait on a barrier's phase, asleep and bounded; false when it gave up (with the status bit) or another role
-// did.  A call of its own, not in line: the roles of a block share the instruction cache, and with every wait, walk and
-// loop written out (181 KB of code) each step of a role waited for its instructions.
-__device__ __noinline__ bool role_wait(uint64_t *b, int phase, int32_t *status, volatile int *bail)
-{
-    const bool ok = mb_wait_asleep(b, (uint32_t)phase & 1u);
-    if (!ok) {
-        set_status(status, K3MOE_DEV_TIMEOUT);
-        *bail = 1;
-    }
-    return (bool)__all_sync(0xffffffffu, ok && !*bail);
-}
+// a / b of positive numbers, in 32 bits where they fit: the long division is a hundred instructions.
+__device__ __forceinline__ long long quotient(long long a, int b) { return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b); }
 
 // A block's search over the sequences, count(i) units each, by all threads at once: which one unit want(total) is
 // of (-1: there are not as many), how many units of it come before, and the units in all.
@@ -50,6 +40,20 @@ template <int THREADS, typename Count, typename Want>
 __device__ __forceinline__ int find_unit(UnitSearch &sh, int n_seq, long long *before, long long *total, Count count, Want want)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (n_seq <= 32) {                                        // every warp for itself
+        const long long mine = lane < n_seq ? count(lane) : 0;
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        *total = __shfl_sync(0xffffffffu, upto, 31);
+        const long long unit = want(*total);
+        const int seq = __popc(__ballot_sync(0xffffffffu, upto <= unit));        // as many end before it
+        *before = unit - __shfl_sync(0xffffffffu, upto - mine, seq & 31);
+        return seq < n_seq ? seq : -1;
+    }
     if (threadIdx.x == 0) sh.seq = -1;
     // units of this thread's sequence of the THREADS from i0 on, those before it (from `base` on), and all of them
     auto scan = [&](int i0, long long *mine, long long *all) {
