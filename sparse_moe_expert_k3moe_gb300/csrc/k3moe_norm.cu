@@ -25,122 +25,115 @@ __device__ __forceinline__ Eight load8(const void *base, bool f32, size_t at)
     }
     return e;
 }
-// As pairs of floats, the form that most of the arithmetic here takes.
-__device__ __forceinline__ void bf16x8(uint4 w, uint64_t (&x)[4])
+__device__ __forceinline__ void bf16x8(uint4 w, float (&x)[8])
 {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; i++) x[i] = pack2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+    for (int i = 0; i < 4; i++) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
 }
-__device__ __forceinline__ void pairs(const Eight &e, bool f32, uint64_t (&x)[4])
+__device__ __forceinline__ void floats(const Eight &e, bool f32, float (&x)[8])
 {
     if (f32) {
         const uint32_t u[8] = {e.lo.x, e.lo.y, e.lo.z, e.lo.w, e.hi.x, e.hi.y, e.hi.z, e.hi.w};
 #pragma unroll
-        for (int i = 0; i < 4; i++) x[i] = pack2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+        for (int i = 0; i < 8; i++) x[i] = __uint_as_float(u[i]);
     } else {
         bf16x8(e.lo, x);
     }
 }
-__device__ __forceinline__ uint4 pack8(const uint64_t (&x)[4])
+__device__ __forceinline__ uint4 pack8(const float (&x)[8])
 {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const float2 v = unpack2(x[i]);
-        const __nv_bfloat162 w = __floats2bfloat162_rn(v.x, v.y);
+        const __nv_bfloat162 w = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
         u[i] = *reinterpret_cast<const uint32_t *>(&w);
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ void store8(void *base, bool f32, size_t at, const uint64_t (&x)[4])
+__device__ __forceinline__ void store8(void *base, bool f32, size_t at, const float (&x)[8])
 {
     if (f32) {
         float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(base) + at);
-        const float2 a = unpack2(x[0]), b = unpack2(x[1]), c = unpack2(x[2]), d = unpack2(x[3]);
-        p[0] = make_float4(a.x, a.y, b.x, b.y);
-        p[1] = make_float4(c.x, c.y, d.x, d.y);
+        p[0] = make_float4(x[0], x[1], x[2], x[3]);
+        p[1] = make_float4(x[4], x[5], x[6], x[7]);
     } else {
         *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(base) + at) = pack8(x);
     }
 }
-__device__ __forceinline__ void load_gain8(const float *g, size_t at, uint64_t (&x)[4])
+__device__ __forceinline__ void load_gain8(const float *g, size_t at, float (&x)[8])
 {
     const float4 *p = reinterpret_cast<const float4 *>(g + at);
     const float4 a = p[0], b = p[1];
-    x[0] = pack2(a.x, a.y);
-    x[1] = pack2(a.z, a.w);
-    x[2] = pack2(b.x, b.y);
-    x[3] = pack2(b.z, b.w);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
-__device__ __forceinline__ float squares(const uint64_t (&x)[4])
+__device__ __forceinline__ float squares(const float (&x)[8])
 {
-    uint64_t s = mul2(x[0], x[0]);
+    float s = x[0] * x[0];
 #pragma unroll
-    for (int i = 1; i < 4; i++) s = fma2(x[i], x[i], s);
-    const float2 v = unpack2(s);
-    return v.x + v.y;
+    for (int i = 1; i < 8; i++) s = fmaf(x[i], x[i], s);
+    return s;
 }
 // Sum over the lanes that share lane / width, width a power of two up to 32.
 __device__ __forceinline__ float lanes_sum(float v, int width)
 {
-    for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, v, o);
+        v += o < width ? x : 0.0f;
+    }
     return v;
 }
 
 // ---------------------------------------------------------------- norms around a block
-// 1 / (1 + exp(-z)) of two within a few units of their last place, or zero below 2^-125: the exponential's argument in
-// powers of two is a rounded product t and its remainder r, exp(-z) = 2^t (1 + r ln 2).
-__device__ __forceinline__ uint64_t sigmoid2(uint64_t z2)
+// 1 / (1 + exp(-z)) within a few units of its last place, or zero below 2^-125: with t = -z log2 e rounded and
+// r = -z - t ln 2 (ln 2 in two floats), exp(-z) = 2^t (1 + r).
+__device__ __forceinline__ float sigmoid(float z)
 {
-    float2 z = unpack2(z2);
-    asm("max.NaN.f32 %0, %0, 0fC2B10000;" : "+f"(z.x));       // -88.5: 2^t stays finite, its reciprocal is zero
-    asm("max.NaN.f32 %0, %0, 0fC2B10000;" : "+f"(z.y));
-    z2 = pack2(z.x, z.y);
-    const uint64_t log2e = pack2(-1.442695022f, -1.442695022f), rest = pack2(-1.925963033e-8f, -1.925963033e-8f);
-    const uint64_t t2 = mul2(z2, log2e), minus = pack2(-1.0f, -1.0f);
-    const uint64_t r = fma2(z2, rest, fma2(z2, log2e, mul2(t2, minus)));
-    const float2 t = unpack2(t2);
-    const uint64_t e = pack2(exp2_fast(t.x), exp2_fast(t.y));
-    const float2 d = unpack2(add2(fma2(mul2(e, pack2(0.6931471806f, 0.6931471806f)), r, e), pack2(1.0f, 1.0f)));
-    float2 s;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
-    return pack2(s.x, s.y);
+    asm("max.NaN.f32 %0, %0, 0fC2B10000;\n\tmin.NaN.f32 %0, %0, 0f42B10000;" : "+f"(z));    // within 88.5: 2^t stays finite
+    const float t = z * -1.442695041f, r = fmaf(t, 1.904654300e-9f, fmaf(t, -0.6931471825f, -z)), e = exp2_fast(t);
+    float s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(fmaf(e, r, e) + 1.0f));
+    return s;
 }
 
 // A row is `tpr` threads', each V pieces of 8 columns, held in registers from the one read to
 // the writes; blocks of short rows hold several.  A group's sum is of 8, 16 or 32 neighbouring
 // lanes, a row's of all its warps.  Many rows are bound by their bytes (8192 x 7168, each head's norm with a gate:
-// MANY us, RATE TB/s); a row alone by latency, so it takes as many threads as it has pieces, and their gains are asked for
-// with the row (1 x 7168 with all there is: ONE us in a graph; four pieces a thread, gains when they are needed 7.0).
-template <int V> constexpr int kNormMax = V == 4 ? 512 : 1024;
+// 65.5 us, 5.4 TB/s: two thirds of the issue slots go to
+// the sigmoid; two blocks an SM 72); a row alone by latency, so it takes as many threads as it has pieces, and their gains are asked for
+// with the row (1 x 7168 with all there is: 3.9 us in a graph; four pieces a thread, gains when they are needed 7.0).
+template <int V> constexpr int kNormMax = V == 1 ? 1024 : 512;
 constexpr int kNormThreads = 256;
 
-template <int V>
-__global__ void __launch_bounds__(kNormMax<V>) norm_kernel(const NormArgs a, const int tpr)
+template <int V, bool kX32, bool kSum32, int kGate>
+__global__ void __launch_bounds__(kNormMax<V>, V == 2 ? 3 : 1) norm_kernel(const NormArgs a, const float per_row, const float per_group)
 {
     constexpr bool kEarly = V == 1;
     pdl_wait();
     pdl_trigger();
     __shared__ float part[2][32];
-    const int in_row = threadIdx.x % tpr, row_in_block = threadIdx.x / tpr, rows = blockDim.x / tpr;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row_warps = tpr >> 5;
-    const int t = blockIdx.x * rows + row_in_block;
+    const int tpr = blockDim.x, in_row = threadIdx.x, row_in_block = threadIdx.y;
+    const int lane = in_row & 31, row_warps = tpr >> 5, warp = row_in_block * row_warps + (in_row >> 5);
+    const int t = blockIdx.x * blockDim.y + row_in_block;
     const int pieces = a.N >> 3;
     const bool live = t < a.T;
     Eight xe[V], re[V];
     uint4 ge[V];
-    uint64_t post[4], scale[4], pre[4];
+    float post[8], scale[8], pre[8];
     auto post_at = [&](int p) { return a.group == a.N ? 8 * p : (8 * p) & (a.group - 1); };
 #pragma unroll
     for (int i = 0; i < V; i++) {
         const int p = in_row + i * tpr;
         const bool in = live && p < pieces;
         xe[i].lo = xe[i].hi = re[i].lo = re[i].hi = ge[i] = make_uint4(0, 0, 0, 0);
-        if (in) xe[i] = load8(a.x, a.x_f32, (size_t)t * a.x_stride + 8 * p);
-        if (in && a.gate) ge[i] = *reinterpret_cast<const uint4 *>(a.gate + (size_t)t * a.gate_stride + 8 * p);
-        if (in && a.residual) re[i] = load8(a.residual, a.sum_f32, (size_t)t * a.residual_stride + 8 * p);
+        if (in) xe[i] = load8(a.x, kX32, (size_t)t * a.x_stride + 8 * p);
+        if (in && kGate != K3MOE_GATE_NONE) ge[i] = *reinterpret_cast<const uint4 *>(a.gate + (size_t)t * a.gate_stride + 8 * p);
+        if (in && a.residual) re[i] = load8(a.residual, kSum32, (size_t)t * a.residual_stride + 8 * p);
         if (kEarly && in) {
             if (a.post_norm) load_gain8(a.post_gain, post_at(p), post);
             if (a.scale) load_gain8(a.scale, 8 * p, scale);
@@ -156,11 +149,10 @@ __global__ void __launch_bounds__(kNormMax<V>) norm_kernel(const NormArgs a, con
         v = lane < row_warps ? part[turn][row_in_block * row_warps + lane] : 0.0f;
         return lanes_sum(v, 32);
     };
-    uint64_t y[V][4];                                         // pairs of columns
-    float inv[V];
+    float y[V][8], inv[V];
 #pragma unroll
     for (int i = 0; i < V; i++) {
-        pairs(xe[i], a.x_f32, y[i]);
+        floats(xe[i], kX32, y[i]);
         inv[i] = 1.0f;
     }
     if (a.post_norm) {
@@ -171,12 +163,12 @@ __global__ void __launch_bounds__(kNormMax<V>) norm_kernel(const NormArgs a, con
             all += ss[i];
         }
         if (a.group == a.N) {
-            const float r = 1.0f / sqrtf(row_sum(all, 0) / (float)a.N + a.eps);
+            const float r = rsqrtf(fmaf(row_sum(all, 0), per_row, a.eps));
 #pragma unroll
             for (int i = 0; i < V; i++) inv[i] = r;
         } else {
 #pragma unroll
-            for (int i = 0; i < V; i++) inv[i] = 1.0f / sqrtf(lanes_sum(ss[i], a.group >> 3) / (float)a.group + a.eps);
+            for (int i = 0; i < V; i++) inv[i] = rsqrtf(fmaf(lanes_sum(ss[i], a.group >> 3), per_group, a.eps));
         }
     }
     float sq = 0.0f;
@@ -186,54 +178,66 @@ __global__ void __launch_bounds__(kNormMax<V>) norm_kernel(const NormArgs a, con
         if (!live || p >= pieces) continue;
         const float f = inv[i] * a.alpha;
 #pragma unroll
-        for (int j = 0; j < 4; j++) y[i][j] = mul2(y[i][j], pack2(f, f));
+        for (int j = 0; j < 8; j++) y[i][j] *= f;
         if (a.post_norm) {
             if (!kEarly) load_gain8(a.post_gain, post_at(p), post);
 #pragma unroll
-            for (int j = 0; j < 4; j++) y[i][j] = mul2(y[i][j], post[j]);
+            for (int j = 0; j < 8; j++) y[i][j] *= post[j];
         }
-        if (a.gate_act != K3MOE_GATE_NONE) {
-            uint64_t w[4];
+        if (kGate != K3MOE_GATE_NONE) {
+            float w[8];
             bf16x8(ge[i], w);
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                y[i][j] = mul2(y[i][j], sigmoid2(w[j]));
-                if (a.gate_act == K3MOE_GATE_SILU) y[i][j] = mul2(y[i][j], w[j]);
+            for (int j = 0; j < 8; j++) {
+                y[i][j] *= sigmoid(w[j]);
+                if (kGate == K3MOE_GATE_SILU) y[i][j] *= w[j];
             }
         }
         if (a.scale) {
             if (!kEarly) load_gain8(a.scale, 8 * p, scale);
 #pragma unroll
-            for (int j = 0; j < 4; j++) y[i][j] = mul2(y[i][j], scale[j]);
+            for (int j = 0; j < 8; j++) y[i][j] *= scale[j];
         }
         if (a.residual) {
-            uint64_t w[4];
-            pairs(re[i], a.sum_f32, w);
+            float w[8];
+            floats(re[i], kSum32, w);
 #pragma unroll
-            for (int j = 0; j < 4; j++) y[i][j] = add2(y[i][j], w[j]);
+            for (int j = 0; j < 8; j++) y[i][j] += w[j];
         }
-        if (a.total) store8(a.total, a.sum_f32, (size_t)t * a.total_stride + 8 * p, y[i]);
+        if (a.total) store8(a.total, kSum32, (size_t)t * a.total_stride + 8 * p, y[i]);
         if (a.pre_norm) sq += squares(y[i]);
     }
     if (!a.pre_norm) return;
-    const float r = 1.0f / sqrtf(row_sum(sq, 1) / (float)a.N + a.eps);
+    const float r = rsqrtf(fmaf(row_sum(sq, 1), per_row, a.eps));
 #pragma unroll
     for (int i = 0; i < V; i++) {
         const int p = in_row + i * tpr;
         if (!live || p >= pieces) continue;
         if (!kEarly) load_gain8(a.pre_gain, 8 * p, pre);
-        uint64_t w[4];
+        float w[8];
 #pragma unroll
-        for (int j = 0; j < 4; j++) w[j] = mul2(pre[j], mul2(y[i][j], pack2(r, r)));
+        for (int j = 0; j < 8; j++) w[j] = pre[j] * (y[i][j] * r);
         store8(a.out, false, (size_t)t * a.out_stride + 8 * p, w);
     }
 }
 
-template <int V>
+template <int V, bool kX32, bool kSum32, int kGate>
 cudaError_t launch_norm_as(const NormArgs &a, cudaStream_t s)
 {
     const int tpr = (a.N / 8 + 32 * V - 1) / (32 * V) * 32, rows = std::max(1, kNormThreads / tpr);
-    return launch_pdl(norm_kernel<V>, dim3((unsigned)((a.T + rows - 1) / rows)), dim3((unsigned)(tpr * rows)), 0, s, a, tpr);
+    return launch_pdl(norm_kernel<V, kX32, kSum32, kGate>, dim3((unsigned)((a.T + rows - 1) / rows)), dim3((unsigned)tpr, (unsigned)rows), 0, s, a,
+                      1.0f / (float)a.N, 1.0f / (float)a.group);
+}
+template <int V, bool kX32, bool kSum32> cudaError_t launch_norm_gate(const NormArgs &a, cudaStream_t s)
+{
+    return a.gate_act == K3MOE_GATE_SIGMOID ? launch_norm_as<V, kX32, kSum32, K3MOE_GATE_SIGMOID>(a, s)
+           : a.gate_act == K3MOE_GATE_SILU  ? launch_norm_as<V, kX32, kSum32, K3MOE_GATE_SILU>(a, s)
+                                            : launch_norm_as<V, kX32, kSum32, K3MOE_GATE_NONE>(a, s);
+}
+template <int V> cudaError_t launch_norm_types(const NormArgs &a, cudaStream_t s)
+{
+    return a.x_f32 ? (a.sum_f32 ? launch_norm_gate<V, true, true>(a, s) : launch_norm_gate<V, true, false>(a, s))
+                   : (a.sum_f32 ? launch_norm_gate<V, false, true>(a, s) : launch_norm_gate<V, false, false>(a, s));
 }
 
 // ---------------------------------------------------------------- the cache's write
@@ -247,33 +251,25 @@ constexpr int kWriteThreads = 128, kWriteDeep = 2;
 __device__ __forceinline__ int rope_first(int how, int j) { return how == K3MOE_ROPE_PAIRS ? 16 * j : 8 * j; }
 __device__ __forceinline__ int rope_second(int how, int j) { return how == K3MOE_ROPE_PAIRS ? 16 * j + 8 : 8 * j + kLatR / 2; }
 // Turns pair j's 16 columns u, v by the angles 8 j .. 8 j + 7: of (x, y), (x cos - y sin, y cos + x sin).
-__device__ __forceinline__ void rope_turn(int how, const float *cosine, const float *sine, int j, uint64_t (&u)[4], uint64_t (&v)[4])
+__device__ __forceinline__ void rope_turn(int how, const float *cosine, const float *sine, int j, float (&u)[8], float (&v)[8])
 {
-    const float4 *c = reinterpret_cast<const float4 *>(cosine + 8 * j), *s = reinterpret_cast<const float4 *>(sine + 8 * j);
-    const float4 c0 = c[0], c1 = c[1], s0 = s[0], s1 = s[1];
-    if (how == K3MOE_ROPE_HALVES) {
-        const uint64_t cs[4] = {pack2(c0.x, c0.y), pack2(c0.z, c0.w), pack2(c1.x, c1.y), pack2(c1.z, c1.w)};
-        const uint64_t sn[4] = {pack2(s0.x, s0.y), pack2(s0.z, s0.w), pack2(s1.x, s1.y), pack2(s1.z, s1.w)};
-        const uint64_t minus = pack2(-1.0f, -1.0f);
+    if (how == K3MOE_ROPE_NONE) return;
+    float c[8], s[8];
+    load_gain8(cosine, 8 * j, c);
+    load_gain8(sine, 8 * j, s);
+    auto turn = [](float &x, float &y, float c, float s) {
+        const float z = x;
+        x = fmaf(z, c, -(y * s));
+        y = fmaf(y, c, z * s);
+    };
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint64_t x = u[i], y = v[i];
-            u[i] = fma2(x, cs[i], mul2(mul2(y, sn[i]), minus));
-            v[i] = fma2(y, cs[i], mul2(x, sn[i]));
-        }
-    } else if (how == K3MOE_ROPE_PAIRS) {
-        auto one = [](uint64_t p, float c, float s) {
-            const float2 x = unpack2(p);
-            return fma2(p, pack2(c, c), mul2(pack2(x.y, x.x), pack2(-s, s)));
-        };
-        u[0] = one(u[0], c0.x, s0.x);
-        u[1] = one(u[1], c0.y, s0.y);
-        u[2] = one(u[2], c0.z, s0.z);
-        u[3] = one(u[3], c0.w, s0.w);
-        v[0] = one(v[0], c1.x, s1.x);
-        v[1] = one(v[1], c1.y, s1.y);
-        v[2] = one(v[2], c1.z, s1.z);
-        v[3] = one(v[3], c1.w, s1.w);
+    for (int i = 0; i < 8; i++) {
+        if (how == K3MOE_ROPE_HALVES)
+            turn(u[i], v[i], c[i], s[i]);
+        else if (i < 4)
+            turn(u[2 * i], u[2 * i + 1], c[i], s[i]);
+        else
+            turn(v[2 * i - 8], v[2 * i - 7], c[i], s[i]);
     }
 }
 
@@ -300,7 +296,7 @@ __global__ void __launch_bounds__(kWriteThreads) latent_write_kernel(const Laten
     };
     ask(threadIdx.x >> 2);
     int64_t slot = a.cache ? a.slots[t] : -1;
-    uint64_t x[4], g[4], v[4];
+    float x[8], g[8], v[8];
     float ss = 0.0f;
     if (threadIdx.x < kLatC / 8) {
         bf16x8(*reinterpret_cast<const uint4 *>(c + 8 * threadIdx.x), x);
@@ -325,16 +321,16 @@ __global__ void __launch_bounds__(kWriteThreads) latent_write_kernel(const Laten
     }
     uint16_t *row = a.rows ? a.rows + (size_t)t * a.rows_stride : nullptr;
     uint16_t *cached = slot >= 0 ? a.cache + (size_t)slot * kLatRow : nullptr;
-    auto put = [&](int at, const uint64_t (&v)[4]) {
+    auto put = [&](int at, const float (&v)[8]) {
         const uint4 w = pack8(v);
         if (row) *reinterpret_cast<uint4 *>(row + at) = w;
         if (cached) *reinterpret_cast<uint4 *>(cached + at) = w;
     };
     if (threadIdx.x < kLatC / 8) {
         if (a.norm) {
-            const float r = 1.0f / sqrtf((part[0] + part[1]) * (1.0f / kLatC) + a.eps);
+            const float r = rsqrtf(fmaf(part[0] + part[1], 1.0f / kLatC, a.eps));
 #pragma unroll
-            for (int i = 0; i < 4; i++) x[i] = mul2(mul2(x[i], pack2(r, r)), g[i]);
+            for (int i = 0; i < 8; i++) x[i] = x[i] * r * g[i];
         }
         put(8 * threadIdx.x, x);
     } else if (threadIdx.x < kLatC / 8 + 4) {
@@ -364,9 +360,9 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t s)
     timing_begin("norm", s);
     // a piece a thread for rows of up to 2048 columns and for a few longer ones, else two, and four for the longest
     const bool few = a.T <= num_sms();
-    const cudaError_t err = a.N <= 2048 || (few && a.N <= 8192) ? launch_norm_as<1>(a, s)
-                            : a.N <= 8192 || few               ? launch_norm_as<2>(a, s)
-                                                               : launch_norm_as<4>(a, s);
+    const cudaError_t err = a.N <= 2048 || (few && a.N <= 8192) ? launch_norm_types<1>(a, s)
+                            : a.N <= 8192                      ? launch_norm_types<2>(a, s)
+                                                               : launch_norm_types<4>(a, s);
     count_launch();
     timing_end("norm", s);
     return err;
