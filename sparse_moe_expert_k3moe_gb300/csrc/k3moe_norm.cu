@@ -111,7 +111,7 @@ template <int V> constexpr int kNormMax = V == 1 ? 1024 : 512;
 constexpr int kNormThreads = 256;
 
 template <int V, bool kX32, bool kSum32, int kGate>
-__global__ void __launch_bounds__(kNormMax<V>, V == 2 ? 3 : 1) norm_kernel(const NormArgs a, const float per_row, const float per_group)
+__global__ void __launch_bounds__(kNormMax<V>, V == 2 && !kX32 && !kSum32 ? 3 : 1) norm_kernel(const NormArgs a, const float per_row, const float per_group)
 {
     constexpr bool kEarly = V == 1;
     pdl_wait();

@@ -33,19 +33,20 @@ constexpr uint32_t kPrTmS = 0, kPrTmO = 2 * kPrTile;
 constexpr float kPrSlack = 8.0f;
 
 struct PromptShared {
-    uint64_t q_full[2], full[kPrSlots], empty[kPrSlots], s_full[2], p_ready[2], o_full[2], mend[2], mended[2], drain;
+    // by the tile's turn: keys and values there, and free again; by the half: its queries, scores, weights (first and
+    // second half of a tile's) and output
+    uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], q_full[2], s_full[2], p_ready[2][2], o_full[2], mend[2], mended[2], drain;
     uint32_t tmem;
     volatile int bail, spoiled;
     UnitSearch search;
 };
 
-// A row of scores becomes weights in tensor memory, packed; returns their sum.
-__device__ __forceinline__ float weigh(uint32_t (&v)[128], uint32_t taddr, float c, float m)
+// 64 of a row's scores become weights in tensor memory, packed; returns their sum.
+__device__ __forceinline__ float weigh(const uint32_t *v, uint32_t taddr, uint64_t cc, uint64_t mm)
 {
-    const uint64_t cc = pack2(c, c), mm = pack2(-m, -m);
     uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
-    for (int b = 0; b < 4; b++) {
+    for (int b = 0; b < 2; b++) {
         float w[16];
 #pragma unroll
         for (int j = 0; j < 16; j++) {
@@ -121,16 +122,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; i++) {
+            mb_init(&sh.k_full[i], 1);
+            mb_init(&sh.v_full[i], 1);
+            mb_init(&sh.k_empty[i], 1);
+            mb_init(&sh.v_empty[i], 1);
             mb_init(&sh.q_full[i], 1);
             mb_init(&sh.s_full[i], 1);
-            mb_init(&sh.p_ready[i], 4);
+            mb_init(&sh.p_ready[i][0], 4);
+            mb_init(&sh.p_ready[i][1], 4);
             mb_init(&sh.o_full[i], 1);
-        }
-        for (int i = 0; i < kPrSlots; i++) {
-            mb_init(&sh.full[i], 1);
-            mb_init(&sh.empty[i], 1);
-        }
-        for (int i = 0; i < 2; i++) {
             mb_init(&sh.mend[i], 1);
             mb_init(&sh.mended[i], 2);
         }
@@ -148,12 +148,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     tc_fence_after();
     constexpr uint32_t tmem = 0;                              // all 512 columns: the allocation starts at the first
     auto wait = [&](uint64_t &b, int phase) {
-        const bool ok = mb_wait_asleep(&b, (uint32_t)phase & 1u);
+        const bool ok = mb_wait_warp(&b, (uint32_t)phase & 1u);
         if (!ok) {
             set_status(status, K3MOE_DEV_TIMEOUT);
             sh.bail = 1;
         }
-        return (bool)__all_sync(0xffffffffu, ok && !sh.bail);
+        return ok;
     };
     // the ring's slot of a tile's box: keys, r, values
     auto slot_of = [](int tile, int box) { return (kPrTileBoxes * tile + box) % kPrSlots; };
@@ -180,13 +180,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 128; j++) v[j] = j < left ? v[j] : 0xFF800000u;
             }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float mx[4];
 #pragma unroll
-            for (int j = 0; j < 128; j += 8)
+            for (int k = 0; k < 4; k++) mx[k] = fmaxf(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
 #pragma unroll
-                for (int k = 0; k < 4; k++)
-                    mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1])));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            for (int j = 8; j < 128; j += 8)
+#pragma unroll
+                for (int k = 0; k < 4; k++) mx[k] = max3(mx[k], __uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1]));
+            const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
             if (i == 0) {
                 m = top;
             } else if (__any_sync(0xffffffffu, top > m + kPrSlack)) {
@@ -203,11 +204,16 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                     tmem_st16(la_o + b, o);
                 }
             }
-            l += weigh(v, la_s, c, m == -INFINITY ? 0.0f : m);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mb_arrive(&sh.p_ready[half]);
+            const float m0 = m == -INFINITY ? 0.0f : -m;
+            const uint64_t cc = pack2(c, c), mm = pack2(m0, m0);
+#pragma unroll
+            for (int b = 0; b < 2; b++) {                     // the product of the first 64 keys begins under the second
+                l += weigh(&v[64 * b], la_s + 32 * b, cc, mm);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mb_arrive(&sh.p_ready[half][b]);
+            }
         }
         if (ok && mine > 0) ok = wait(sh.o_full[half], 0);
         if (ok && __any_sync(0xffffffffu, r < n)) {
@@ -247,50 +253,47 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsLast));
         if (warp == kPrWarpMma) {
-            // ---------------- products
+            // ---------------- products: of a half with values, then its scores of the tile after
             const uint32_t ids = idesc(1, kPrTile), idv = idesc(1, kLatV) | (1u << 16);     // V with its columns contiguous
             const int n0 = uniform(tiles0), n1 = uniform(tiles1), n = max(n0, n1), mend0 = uniform(whole);
             const uint32_t sm_q = desc_lo(saddr(sm)), sm_kv = desc_lo(saddr(ring), 0);
             constexpr uint32_t box = kPrBox >> 4;
-            auto scores = [&](int half, int i) {
-                if (i == 0 && !wait(sh.q_full[half], 0)) return false;
-                uint32_t A = sm_q + (uint32_t)half * kPrQBoxes * box;
+            bool ok = true;
+#pragma unroll 1
+            for (int step = -2; ok && step < 2 * n; step++) {
+                const int half = step & 1, i = step >> 1, mine = half ? n1 : n0;
+                const bool last = half == 1 || i >= n1, last_next = half == 1 || i + 1 >= n1;      // of the tile's two
+                if (i >= 0 && i < mine) {
+                    const int s0 = slot_of(i, kPrQBoxes), s1 = slot_of(i, kPrQBoxes + 1), lo = min(s0, s1);
+                    if (!(ok = wait(sh.v_full[i & 1], i >> 1) && (i < mend0 || wait(sh.mended[(i - mend0) & 1], (i - mend0) >> 1)))) break;
+                    const uint32_t B = sm_kv + (uint32_t)lo * box + ((uint32_t)(max(s0, s1) - lo) * box << 16);
+                    const uint32_t D = kPrTmO + kLatV * half, A = kPrTmS + kPrTile * half;
+#pragma unroll 1
+                    for (int b = 0; b < 2; b++) {
+                        if (!(ok = wait(sh.p_ready[half][b], i))) break;
+                        tc_fence_after();
 #pragma unroll
-                for (int b = 0; b < kPrQBoxes; b++, A += box) {
-                    const int s = slot_of(i, b);
-                    if (!wait(sh.full[s], (kPrTileBoxes * i + b) / kPrSlots)) return false;
+                        for (int k = 0; k < 4; k++)
+                            umma_ts_warp(D, A + 32 * b + 8 * k, B + (uint32_t)((4 * b + k) * 16 * 128 >> 4), idv, i > 0 || b > 0 || k > 0);
+                    }
+                    if (!ok) break;
+                    if (last) umma_commit_warp(&sh.v_empty[i & 1]);
+                    if (i == mine - 1) umma_commit_warp(&sh.o_full[half]);
+                }
+                if (i + 1 < mine) {
+                    if (i < 0 && !(ok = wait(sh.q_full[half], 0))) break;
+                    if (!(ok = wait(sh.k_full[(i + 1) & 1], (i + 1) >> 1))) break;
                     tc_fence_after();
-                    const uint32_t B = sm_kv + (uint32_t)s * box;
+                    const uint32_t D = kPrTmS + kPrTile * half, A = sm_q + (uint32_t)half * kPrQBoxes * box;
 #pragma unroll
-                    for (int k = 0; k < 4; k++) umma_warp(kPrTmS + kPrTile * half, A + 2 * k, B + 2 * k, ids, b > 0 || k > 0);
-                    if (half == 1 || i >= n1) umma_commit_warp(&sh.empty[s]);
-                }
-                umma_commit_warp(&sh.s_full[half]);
-                return true;
-            };
-            auto values = [&](int half, int i) {
-                const int s0 = slot_of(i, kPrQBoxes), s1 = slot_of(i, kPrQBoxes + 1), lo = min(s0, s1);
-                if (!wait(sh.full[s0], (kPrTileBoxes * i + kPrQBoxes) / kPrSlots) ||
-                    !wait(sh.full[s1], (kPrTileBoxes * i + kPrQBoxes + 1) / kPrSlots) ||
-                    (i >= mend0 && !wait(sh.mended[(i - mend0) & 1], (i - mend0) >> 1)) || !wait(sh.p_ready[half], i))
-                    return false;
-                tc_fence_after();
-                const uint32_t B = sm_kv + (uint32_t)lo * box + ((uint32_t)(max(s0, s1) - lo) * box << 16);
+                    for (int b = 0; b < kPrQBoxes; b++) {
+                        const uint32_t B = sm_kv + (uint32_t)slot_of(i + 1, b) * box;
 #pragma unroll
-                for (int k = 0; k < kPrTile / 16; k++)
-                    umma_ts_warp(kPrTmO + kLatV * half, kPrTmS + kPrTile * half + 8 * k, B + (uint32_t)(k * 16 * 128 >> 4), idv, i > 0 || k > 0);
-                if (half == 1 || i >= n1) {
-                    umma_commit_warp(&sh.empty[s0]);
-                    umma_commit_warp(&sh.empty[s1]);
+                        for (int k = 0; k < 4; k++) umma_warp(D, A + b * box + 2 * k, B + 2 * k, ids, b > 0 || k > 0);
+                    }
+                    if (last_next) umma_commit_warp(&sh.k_empty[(i + 1) & 1]);
+                    umma_commit_warp(&sh.s_full[half]);
                 }
-                if (i == (half ? n1 : n0) - 1) umma_commit_warp(&sh.o_full[half]);
-                return true;
-            };
-            // scores a tile ahead of the products with values, a half at a time
-            bool ok = (n0 < 1 || scores(0, 0)) && (n1 < 1 || scores(1, 0));
-            for (int i = 0; ok && i < n; i++) {
-                if (i < n0) ok = values(0, i) && (i + 1 >= n0 || scores(0, i + 1));
-                if (ok && i < n1) ok = values(1, i) && (i + 1 >= n1 || scores(1, i + 1));
             }
             __syncwarp();
             umma_commit_warp(&sh.drain);                       // every issued MMA done before the dealloc
@@ -302,53 +305,46 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 for (int b = 0; b < kPrQBoxes; b++)
                     tma3d_warp(sm + (half * kPrQBoxes + b) * kPrBox, &mq, 64 * b, h, t0 + row0 + kPrRows * half, &sh.q_full[half]);
             };
-            int loaded = 0;
-            bool q0 = false, q1 = false;
-            for (int i = 0; i < tiles && !sh.bail; i++) {
-                if (i == 0 && tiles0 > 0) {
-                    load_q(0);
-                    q0 = true;
-                }
-                const int tok = k0 + kPrTile * i;
-                bool ok = true;
-                for (int b = 0; b < kPrTileBoxes; b++, loaded++) {
-                    const int s = loaded % kPrSlots;
-                    if (loaded >= kPrSlots && !(ok = wait(sh.empty[s], loaded / kPrSlots - 1))) break;
-                    uint8_t *dst = ring + s * kPrBox;
-                    mb_expect_tx_warp(&sh.full[s], kPrBox);
-                    if (b < kLatK / 64) {
-                        tma3d_warp(dst, &mkv, 64 * b, h, tok, &sh.full[s]);
-                    } else if (b < kPrQBoxes) {
-                        tma2d_warp(dst, &mr, 0, tok, &sh.full[s]);
-                    } else {
-                        // the values' first columns to the lower slot of the two
-                        const int other = slot_of(i, kPrQBoxes + (b == kPrQBoxes));
-                        tma3d_warp(dst, &mkv, kLatK + (s < other ? 0 : 64), h, tok, &sh.full[s]);
-                    }
-                    if (i == 0 && b == kPrQBoxes - 1 && tiles1 > 0) {
-                        load_q(1);
-                        q1 = true;
-                    }
-                }
-                if (!ok) break;
-                if (i >= whole && lane == 0) mb_arrive(&sh.mend[(i - whole) & 1]);
+            const int n = uniform(tiles), mend0 = uniform(whole), tok0 = uniform(k0);
+            int k_loads = 0, v_loads = 0;
+            if (tiles0 > 0) load_q(0);
+#pragma unroll 1
+            for (int i = 0; i < n; i++) {
+                // slots: the keys' were the last of the keys and the values of the tile before the last, the values' the first two
+                // of the keys of the last
+                if (i >= 2 && !wait(sh.v_empty[i & 1], (i >> 1) - 1)) break;
+                const int tok = tok0 + kPrTile * i;
+                mb_expect_tx_warp(&sh.k_full[i & 1], kPrQBoxes * kPrBox);
+#pragma unroll
+                for (int b = 0; b < kLatK / 64; b++) tma3d_warp(ring + slot_of(i, b) * kPrBox, &mkv, 64 * b, h, tok, &sh.k_full[i & 1]);
+                tma2d_warp(ring + slot_of(i, kLatK / 64) * kPrBox, &mr, 0, tok, &sh.k_full[i & 1]);
+                k_loads++;
+                if (i == 0 && tiles1 > 0) load_q(1);
+                if (i >= 1 && !wait(sh.k_empty[(i - 1) & 1], (i - 1) >> 1)) break;
+                // the values' first columns to the lower slot of the two
+                const int s0 = slot_of(i, kPrQBoxes), s1 = slot_of(i, kPrQBoxes + 1);
+                mb_expect_tx_warp(&sh.v_full[i & 1], 2 * kPrBox);
+                tma3d_warp(ring + min(s0, s1) * kPrBox, &mkv, kLatK, h, tok, &sh.v_full[i & 1]);
+                tma3d_warp(ring + max(s0, s1) * kPrBox, &mkv, kLatK + 64, h, tok, &sh.v_full[i & 1]);
+                v_loads++;
+                if (i >= mend0 && lane == 0) mb_arrive(&sh.mend[(i - mend0) & 1]);
             }
             // the block's shared memory stays until its last copies have landed, when another role gave up too
-            for (int f = max(0, loaded - kPrSlots); f < loaded; f++) mb_wait_warp(&sh.full[f % kPrSlots], (uint32_t)(f / kPrSlots) & 1u);
-            if (q0) mb_wait_warp(&sh.q_full[0], 0);
-            if (q1) mb_wait_warp(&sh.q_full[1], 0);
+            for (int i = max(0, k_loads - 2); i < k_loads; i++) mb_wait_warp(&sh.k_full[i & 1], (uint32_t)(i >> 1) & 1u);
+            for (int i = max(0, v_loads - 2); i < v_loads; i++) mb_wait_warp(&sh.v_full[i & 1], (uint32_t)(i >> 1) & 1u);
+            if (tiles0 > 0) mb_wait_warp(&sh.q_full[0], 0);
+            if (tiles1 > 0 && k_loads > 0) mb_wait_warp(&sh.q_full[1], 0);
         } else {
             // ---------------- values of tiles that not every row sees whole: tokens behind the sequence's last are cleared, and so is
             // what is infinite or NaN, which a weight of zero would not keep out (rows that see it add it at the end)
             const int id = threadIdx.x - 32 * kPrWarpMend;
             for (int i = whole; i < tiles; i++) {
                 const int s0 = slot_of(i, kPrQBoxes), s1 = slot_of(i, kPrQBoxes + 1);
-                // first for the loads to be on their way: until then the slots' barriers stand at an earlier box
-                if (!wait(sh.mend[(i - whole) & 1], (i - whole) >> 1) || !wait(sh.full[s0], (kPrTileBoxes * i + kPrQBoxes) / kPrSlots) || !wait(sh.full[s1], (kPrTileBoxes * i + kPrQBoxes + 1) / kPrSlots))
-                    break;
+                // first for the loads to be on their way: until then the barrier stands at an earlier tile
+                if (!wait(sh.mend[(i - whole) & 1], (i - whole) >> 1) || !wait(sh.v_full[i & 1], i >> 1)) break;
                 const int last = nk - kPrTile * i;
                 bool any = false;
-#pragma unroll 4
+#pragma unroll 1
                 for (int e = id; e < 2 * kPrTile * 8; e += 64) {
                     const int t = (e >> 3) & (kPrTile - 1);
                     uint4 *p = reinterpret_cast<uint4 *>(ring + (e >> 10 ? s1 : s0) * kPrBox) + (e & 1023);
