@@ -6,8 +6,12 @@
 // c = scale log2 e.  A block has 256 queries of one head in two halves of 128 and walks its keys in tiles of
 // 128.  The scores S = Q K^T go to tensor memory, a thread owns a row of one half: it reads its 128 scores, and
 // its weights go back over them as the A operand of O += P V, so that the softmax of one half runs
-// beside the products of the other.  m moves only when a row outdoes it by 2^8 (weights stay below that, and
-// float sums do not mind); the rescaling of O in tensor memory is then rare.
+// beside the products of the other.
+//
+// m need not be the maximum, only not far below it: the weights are taken with the m of the keys before, and their sum,
+// which is needed anyway, says whether they have grown beyond 2^30; only then (and for a row's first keys) is the maximum
+// looked for, O scaled down and the weights taken again.  A product's chain of steps, scores, weights, values, is
+// what a tile takes, and a maximum ahead of the exponentials was a quarter of the weights' part.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -23,47 +27,46 @@ constexpr int kPrQBoxes = (kLatK + kLatR) / 64;               // boxes of a half
 constexpr int kPrTileBoxes = kPrQBoxes + kLatV / 64;          // with its values
 constexpr int kPrSlots = 8;                                   // the ring of key and value boxes
 constexpr int kPrSmem = 1024 + (2 * kPrQBoxes + kPrSlots) * kPrBox;
-// Warps: four of softmax for each half, then MMA issue, loads and two that mend values
-constexpr int kPrThreads = 384, kPrWarpMma = 8, kPrWarpLoad = 9, kPrWarpMend = 10;
+// Warps: four of softmax for each half, then one each that issues its products, and one of loads (whole warpgroups:
+// registers move)
+constexpr int kPrThreads = 384, kPrWarpMma = 8, kPrWarpLoad = 10;
 // Registers a thread: 168 at launch, moved from the last warpgroup to the rows' threads
 constexpr int kPrRegs = 168, kPrRegsRows = 216, kPrRegsLast = 72;
 static_assert(2 * kPrRegsRows + kPrRegsLast <= 3 * kPrRegs, "shares within the launch's");
 // Tensor memory: S (P over its first half) and O of both halves
 constexpr uint32_t kPrTmS = 0, kPrTmO = 2 * kPrTile;
-constexpr float kPrSlack = 8.0f;
+constexpr float kPrLimit = 1073741824.0f;                     // 2^30: a sum of 64 weights that calls for a new m
 
 struct PromptShared {
-    // by the tile's turn: keys and values there, and free again; by the half: its queries, scores, weights (first and
-    // second half of a tile's) and output
-    uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], q_full[2], s_full[2], p_ready[2][2], o_full[2], mend[2], mended[2], drain;
+    // by the tile's turn: keys and values there, and free again; by the half: its queries, scores, weights (of the first and
+    // the last 64 keys of a tile), its product with the first 64 values and its output
+    uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], q_full[2], s_full[2], p_ready[2][2], first_done[2], o_full[2], turn[2], drain[2];
     uint32_t tmem;
     volatile int bail, spoiled;
     UnitSearch search;
 };
 
-// 64 of a row's scores become weights in tensor memory, packed; returns their sum.
-__device__ __forceinline__ float weigh(const uint32_t *v, uint32_t taddr, uint64_t cc, uint64_t mm)
+// 64 of a row's scores become weights in tensor memory, packed; returns their sum.  Single floats: pairs of them cost
+// more moves than they save here (5.7 instructions a weight, 4 this way).
+__device__ __forceinline__ float weigh(const uint32_t *v, uint32_t taddr, float c, float m)
 {
-    uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
+    const float minus = m == -INFINITY ? 0.0f : -m;
+    float sum[4] = {};
 #pragma unroll
     for (int b = 0; b < 2; b++) {
         float w[16];
 #pragma unroll
         for (int j = 0; j < 16; j++) {
             const int i = 32 * b + 2 * j;
-            const float2 e = unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), cc, mm));
-            const float x = exp2_fast(e.x), y = exp2_fast(e.y);
-            if (j & 1)
-                sum1 = add2(sum1, pack2(x, y));
-            else
-                sum0 = add2(sum0, pack2(x, y));
+            const float x = exp2_fast(fmaf(__uint_as_float(v[i]), c, minus)), y = exp2_fast(fmaf(__uint_as_float(v[i + 1]), c, minus));
+            sum[2 * (j & 1)] += x;
+            sum[2 * (j & 1) + 1] += y;
             const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
             w[j] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&h));
         }
         tmem_st16(taddr + 16 * b, w);
     }
-    const float2 s = unpack2(add2(sum0, sum1));
-    return s.x + s.y;
+    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
 __global__ void __launch_bounds__(kPrThreads, 1)
@@ -124,17 +127,17 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         for (int i = 0; i < 2; i++) {
             mb_init(&sh.k_full[i], 1);
             mb_init(&sh.v_full[i], 1);
-            mb_init(&sh.k_empty[i], 1);
-            mb_init(&sh.v_empty[i], 1);
+            mb_init(&sh.k_empty[i], 2);
+            mb_init(&sh.v_empty[i], 2);
             mb_init(&sh.q_full[i], 1);
             mb_init(&sh.s_full[i], 1);
             mb_init(&sh.p_ready[i][0], 4);
             mb_init(&sh.p_ready[i][1], 4);
             mb_init(&sh.o_full[i], 1);
-            mb_init(&sh.mend[i], 1);
-            mb_init(&sh.mended[i], 2);
+            mb_init(&sh.first_done[i], 1);
+            mb_init(&sh.turn[i], 1);
+            mb_init(&sh.drain[i], 1);
         }
-        mb_init(&sh.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.bail = 0;
         sh.spoiled = 0;
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         return ok;
     };
     // the ring's slot of a tile's box: keys, r, values
-    auto slot_of = [](int tile, int box) { return (kPrTileBoxes * tile + box) % kPrSlots; };
+    auto slot_of = [](int tile, int box) { return (uint32_t)(kPrTileBoxes * tile + box) % (uint32_t)kPrSlots; };
 
     if (warp < kPrWarpMma) {
         // ---------------- softmax and output of a half
@@ -180,40 +183,64 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 128; j++) v[j] = j < left ? v[j] : 0xFF800000u;
             }
-            float mx[4];
-#pragma unroll
-            for (int k = 0; k < 4; k++) mx[k] = fmaxf(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-#pragma unroll
-            for (int j = 8; j < 128; j += 8)
-#pragma unroll
-                for (int k = 0; k < 4; k++) mx[k] = max3(mx[k], __uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1]));
-            const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
-            if (i == 0) {
-                m = top;
-            } else if (__any_sync(0xffffffffu, top > m + kPrSlack)) {
-                // in order behind S: the product before is done with O
-                const float m1 = top > m + kPrSlack ? top : m, f = m1 == -INFINITY ? 1.0f : exp2_fast(m - m1);
-                m = m1;
-                l *= f;
+            if (i >= whole) {
+                // a tile that not every row sees whole: values behind the sequence's last are cleared, and so is what is infinite or
+                // NaN, which a weight of zero would not keep out (rows that see it add it at the end)
+                if (!(ok = wait(sh.v_full[i & 1], i >> 1))) break;
+                const int last = nk - kPrTile * i;
 #pragma unroll 1
-                for (int b = 0; b < kLatV; b += 16) {
-                    float o[16];
-                    tmem_ld16(la_o + b, o);
-#pragma unroll
-                    for (int j = 0; j < 16; j++) o[j] *= f;
-                    tmem_st16(la_o + b, o);
+                for (int e = threadIdx.x & 127; e < 2 * kPrTile * 8; e += 128) {
+                    uint4 *p = reinterpret_cast<uint4 *>(ring + slot_of(i, kPrQBoxes + (e >> 10)) * kPrBox) + (e & 1023);
+                    uint4 w = *p;
+                    if (((e >> 3) & (kPrTile - 1)) >= last) {
+                        *p = make_uint4(0, 0, 0, 0);
+                    } else if (clear_spoiled(w)) {
+                        sh.spoiled = 1;
+                        __threadfence_block();
+                        *p = w;
+                    }
                 }
+                fence_async_smem();
             }
-            const float m0 = m == -INFINITY ? 0.0f : -m;
-            const uint64_t cc = pack2(c, c), mm = pack2(m0, m0);
 #pragma unroll
-            for (int b = 0; b < 2; b++) {                     // the product of the first 64 keys begins under the second
-                l += weigh(&v[64 * b], la_s + 32 * b, cc, mm);
+            for (int b = 0; b < 2; b++) {                     // the product of the first 64 keys begins under the last
+                float sum = weigh(&v[64 * b], la_s + 32 * b, c, m);
+                const bool grown = sum > kPrLimit || m == -INFINITY;      // of this row: the others' stay as they are, bit for bit
+                if (__any_sync(0xffffffffu, grown)) {
+                    float mx[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) mx[k] = __uint_as_float(v[64 * b + k]);
+#pragma unroll
+                    for (int j = 4; j < 60; j += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; k++) mx[k] = max3(mx[k], __uint_as_float(v[64 * b + j + 2 * k]), __uint_as_float(v[64 * b + j + 2 * k + 1]));
+#pragma unroll
+                    for (int k = 0; k < 4; k++) mx[k] = fmaxf(mx[k], __uint_as_float(v[64 * b + 60 + k]));
+                    const float m1 = grown ? fmaxf(m, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c) : m, f = m1 == -INFINITY ? 1.0f : exp2_fast(m - m1);
+                    m = m1;
+                    l *= f;
+                    if (i > 0 || b > 0) {
+                        // the products so far are done: those of the tile before in order ahead of S
+                        if (b > 0 && !(ok = wait(sh.first_done[half], i))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int d = 0; d < kLatV; d += 16) {
+                            float o[16];
+                            tmem_ld16(la_o + d, o);
+#pragma unroll
+                            for (int j = 0; j < 16; j++) o[j] *= f;
+                            tmem_st16(la_o + d, o);
+                        }
+                    }
+                    sum = weigh(&v[64 * b], la_s + 32 * b, c, m);
+                }
+                l += sum;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mb_arrive(&sh.p_ready[half][b]);
             }
+            if (!ok) break;
         }
         if (ok && mine > 0) ok = wait(sh.o_full[half], 0);
         if (ok && __any_sync(0xffffffffu, r < n)) {
@@ -252,52 +279,66 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsLast));
-        if (warp == kPrWarpMma) {
-            // ---------------- products: of a half with values, then its scores of the tile after
+        if (warp < kPrWarpLoad) {
+            // ---------------- products of a half: with values, then its scores of the tile after, in order, so that the weights
+            // may lie over the scores.  A warp a half: while one looks for its next operands the other's products run
+            // (one warp for both 949 us, 8192 tokens x 56 heads).
             const uint32_t ids = idesc(1, kPrTile), idv = idesc(1, kLatV) | (1u << 16);     // V with its columns contiguous
-            const int n0 = uniform(tiles0), n1 = uniform(tiles1), n = max(n0, n1), mend0 = uniform(whole);
-            const uint32_t sm_q = desc_lo(saddr(sm)), sm_kv = desc_lo(saddr(ring), 0);
+            const int half = uniform(warp - kPrWarpMma), mine = uniform(half ? tiles1 : tiles0), others = uniform(half ? tiles0 : tiles1);
             constexpr uint32_t box = kPrBox >> 4;
-            bool ok = true;
+            const uint32_t sm_q = desc_lo(saddr(sm)) + (uint32_t)half * kPrQBoxes * box, sm_kv = desc_lo(saddr(ring), 0);
+            const uint32_t S = kPrTmS + kPrTile * half, O = kPrTmO + kLatV * half;
+            // a tile's keys or values are free when both halves are done with them; this one speaks for one that has no such tile
+            auto done = [&](uint64_t *b, int i) {
+                umma_commit_warp(b);
+                if (i >= others) umma_commit_warp(b);
+            };
+            if (mine > 0 && wait(sh.q_full[half], 0)) {
+                bool ok = true;
 #pragma unroll 1
-            for (int step = -2; ok && step < 2 * n; step++) {
-                const int half = step & 1, i = step >> 1, mine = half ? n1 : n0;
-                const bool last = half == 1 || i >= n1, last_next = half == 1 || i + 1 >= n1;      // of the tile's two
-                if (i >= 0 && i < mine) {
-                    const int s0 = slot_of(i, kPrQBoxes), s1 = slot_of(i, kPrQBoxes + 1), lo = min(s0, s1);
-                    if (!(ok = wait(sh.v_full[i & 1], i >> 1) && (i < mend0 || wait(sh.mended[(i - mend0) & 1], (i - mend0) >> 1)))) break;
-                    const uint32_t B = sm_kv + (uint32_t)lo * box + ((uint32_t)(max(s0, s1) - lo) * box << 16);
-                    const uint32_t D = kPrTmO + kLatV * half, A = kPrTmS + kPrTile * half;
-#pragma unroll 1
-                    for (int b = 0; b < 2; b++) {
-                        if (!(ok = wait(sh.p_ready[half][b], i))) break;
-                        tc_fence_after();
+                for (int i = -1; ok && i < mine; i++) {
+                    // in turn, the first half first: in step both would wait for products, then both for exponentials
+                    const int turn = half ? i + 1 : i;        // the other's that has to be through
+                    if (turn >= 0 && others > 0 && turn <= others && !(ok = wait(sh.turn[half], turn))) break;
+                    if (i >= 0) {
+                        const uint32_t s0 = slot_of(i, kPrQBoxes), s1 = slot_of(i, kPrQBoxes + 1), lo = min(s0, s1);
+                        const uint32_t B = sm_kv + lo * box + ((max(s0, s1) - lo) * box << 16);
+                        if (!(ok = wait(sh.v_full[i & 1], i >> 1))) break;
 #pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            umma_ts_warp(D, A + 32 * b + 8 * k, B + (uint32_t)((4 * b + k) * 16 * 128 >> 4), idv, i > 0 || b > 0 || k > 0);
+                        for (int b = 0; b < 2; b++) {
+                            if (!(ok = wait(sh.p_ready[half][b], i))) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 0; k < 4; k++)
+                                umma_ts_warp(O, S + 32 * b + 8 * k, B + (uint32_t)((4 * b + k) * 16 * 128 >> 4), idv, i > 0 || b > 0 || k > 0);
+                            if (b == 0) umma_commit_warp(&sh.first_done[half]);
+                        }
+                        if (!ok) break;
+                        done(&sh.v_empty[i & 1], i);
+                        if (i == mine - 1) {
+                            umma_commit_warp(&sh.o_full[half]);
+                            if (lane == 0) mb_arrive(&sh.turn[half ^ 1]);
+                            break;
+                        }
                     }
-                    if (!ok) break;
-                    if (last) umma_commit_warp(&sh.v_empty[i & 1]);
-                    if (i == mine - 1) umma_commit_warp(&sh.o_full[half]);
-                }
-                if (i + 1 < mine) {
-                    if (i < 0 && !(ok = wait(sh.q_full[half], 0))) break;
-                    if (!(ok = wait(sh.k_full[(i + 1) & 1], (i + 1) >> 1))) break;
+                    const int j = i + 1;
+                    uint32_t B[kPrQBoxes];
+#pragma unroll
+                    for (int b = 0; b < kPrQBoxes; b++) B[b] = sm_kv + slot_of(j, b) * box;
+                    if (!(ok = wait(sh.k_full[j & 1], j >> 1))) break;
                     tc_fence_after();
-                    const uint32_t D = kPrTmS + kPrTile * half, A = sm_q + (uint32_t)half * kPrQBoxes * box;
 #pragma unroll
-                    for (int b = 0; b < kPrQBoxes; b++) {
-                        const uint32_t B = sm_kv + (uint32_t)slot_of(i + 1, b) * box;
+                    for (int b = 0; b < kPrQBoxes; b++)
 #pragma unroll
-                        for (int k = 0; k < 4; k++) umma_warp(D, A + b * box + 2 * k, B + 2 * k, ids, b > 0 || k > 0);
-                    }
-                    if (last_next) umma_commit_warp(&sh.k_empty[(i + 1) & 1]);
+                        for (int k = 0; k < 4; k++) umma_warp(S, sm_q + b * box + 2 * k, B[b] + 2 * k, ids, b > 0 || k > 0);
                     umma_commit_warp(&sh.s_full[half]);
+                    done(&sh.k_empty[j & 1], j);
+                    if (lane == 0) mb_arrive(&sh.turn[half ^ 1]);
                 }
             }
             __syncwarp();
-            umma_commit_warp(&sh.drain);                       // every issued MMA done before the dealloc
-            mb_wait_warp(&sh.drain, 0);
+            umma_commit_warp(&sh.drain[half]);                 // every issued MMA done before the dealloc
+            mb_wait_warp(&sh.drain[half], 0);
         } else if (warp == kPrWarpLoad) {
             // ---------------- loads
             auto load_q = [&](int half) {
@@ -305,7 +346,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 for (int b = 0; b < kPrQBoxes; b++)
                     tma3d_warp(sm + (half * kPrQBoxes + b) * kPrBox, &mq, 64 * b, h, t0 + row0 + kPrRows * half, &sh.q_full[half]);
             };
-            const int n = uniform(tiles), mend0 = uniform(whole), tok0 = uniform(k0);
+            const int n = uniform(tiles), tok0 = uniform(k0);
             int k_loads = 0, v_loads = 0;
             if (tiles0 > 0) load_q(0);
 #pragma unroll 1
@@ -327,40 +368,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 tma3d_warp(ring + min(s0, s1) * kPrBox, &mkv, kLatK, h, tok, &sh.v_full[i & 1]);
                 tma3d_warp(ring + max(s0, s1) * kPrBox, &mkv, kLatK + 64, h, tok, &sh.v_full[i & 1]);
                 v_loads++;
-                if (i >= mend0 && lane == 0) mb_arrive(&sh.mend[(i - mend0) & 1]);
             }
             // the block's shared memory stays until its last copies have landed, when another role gave up too
             for (int i = max(0, k_loads - 2); i < k_loads; i++) mb_wait_warp(&sh.k_full[i & 1], (uint32_t)(i >> 1) & 1u);
             for (int i = max(0, v_loads - 2); i < v_loads; i++) mb_wait_warp(&sh.v_full[i & 1], (uint32_t)(i >> 1) & 1u);
             if (tiles0 > 0) mb_wait_warp(&sh.q_full[0], 0);
             if (tiles1 > 0 && k_loads > 0) mb_wait_warp(&sh.q_full[1], 0);
-        } else {
-            // ---------------- values of tiles that not every row sees whole: tokens behind the sequence's last are cleared, and so is
-            // what is infinite or NaN, which a weight of zero would not keep out (rows that see it add it at the end)
-            const int id = threadIdx.x - 32 * kPrWarpMend;
-            for (int i = whole; i < tiles; i++) {
-                const int s0 = slot_of(i, kPrQBoxes), s1 = slot_of(i, kPrQBoxes + 1);
-                // first for the loads to be on their way: until then the barrier stands at an earlier tile
-                if (!wait(sh.mend[(i - whole) & 1], (i - whole) >> 1) || !wait(sh.v_full[i & 1], i >> 1)) break;
-                const int last = nk - kPrTile * i;
-                bool any = false;
-#pragma unroll 1
-                for (int e = id; e < 2 * kPrTile * 8; e += 64) {
-                    const int t = (e >> 3) & (kPrTile - 1);
-                    uint4 *p = reinterpret_cast<uint4 *>(ring + (e >> 10 ? s1 : s0) * kPrBox) + (e & 1023);
-                    uint4 w = *p;
-                    if (t >= last) {
-                        *p = make_uint4(0, 0, 0, 0);
-                    } else if (clear_spoiled(w)) {
-                        *p = w;
-                        any = true;
-                    }
-                }
-                if (any) sh.spoiled = 1;
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mb_arrive(&sh.mended[(i - whole) & 1]);       // two tiles' values are there at most
-            }
         }
     }
     tc_fence_before();
