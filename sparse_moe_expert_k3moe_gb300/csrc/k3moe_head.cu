@@ -1,10 +1,12 @@
 // k3moe_head.cu -- y[t][h] = W[h] x[t][h]: each head's own projection (a latent attention's
 // queries into the latent, and what they attended back to values).
 //
-// A block has 128 of a head's output columns and up to 64 tokens: the weights [128][K] are
-// the A operand and the tokens [64][K] B, both loaded whole by TMA (K <= 512 fits the shared
-// memory), a barrier for every 64 columns of K, so that the products follow the loads.  A thread of the
-// epilogue owns an output column and its warp's lanes 32 neighbouring ones.
+// A block has 128 of a head's output columns and up to 128 tokens: the weights are the A operand and the tokens B, 64
+// columns of K a stage of the ring, which leaves room for a second block on the SM whose loads run under this one's
+// epilogue.  A thread of the epilogue owns an output column and its warp's lanes 32 neighbouring ones.
+// What bounds it: one token (56 heads, 128 to 512) start and the first loads, 3.2 us in a graph; a batch the loads from
+// the L2 and an epilogue, once each (333 tokens of 56 heads, 512 to 128: 6.0 us; all of K loaded before a block's end, 64 tokens a
+// block, one block an SM: 13.0).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -14,23 +16,29 @@
 namespace k3moe {
 namespace {
 
-constexpr int kHdBN = 64, kHdABytes = 128 * 128;              // tokens a block; a 64-column chunk of weights
-constexpr int kHdThreads = 192, kHdMaxChunks = kMaxHeadK / 64;    // four epilogue warps, loads, MMAs
+constexpr int kHdMaxBN = 128, kHdABytes = 128 * 128;          // tokens a block; 64 columns of its weights
+constexpr int kHdThreads = 192, kHdRing = 100 * 1024, kHdMaxStages = 5;   // four epilogue warps, loads, MMAs; two blocks an SM
 
-__global__ void __launch_bounds__(kHdThreads) head_linear_kernel(const HeadLinearArgs a, const int bn,
+struct HeadTile {
+    int bn, stages, cols;                                     // tokens; ring; columns of tensor memory
+};
+
+__global__ void __launch_bounds__(kHdThreads, 2) head_linear_kernel(const HeadLinearArgs a, const HeadTile tl,
                                                                 const __grid_constant__ CUtensorMap mw,
                                                                 const __grid_constant__ CUtensorMap mx)
 {
     extern __shared__ __align__(1024) uint8_t hsm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(hsm_raw) + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[kHdMaxChunks], done;
+    __shared__ uint64_t full[kHdMaxStages], empty[kHdMaxStages], done;
     __shared__ uint32_t tmem_base;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int chunks = (a.K + 63) / 64, chunk_bytes = kHdABytes + bn * 128;
-    const int n0 = blockIdx.x * 128, h = blockIdx.y, t0 = blockIdx.z * bn;
-    const uint32_t cols = bn <= 32 ? 32 : 64;
+    const int chunks = (a.K + 63) / 64, stage_bytes = kHdABytes + tl.bn * 128;
+    const int n0 = blockIdx.x * 128, h = blockIdx.y, t0 = blockIdx.z * tl.bn;
     if (threadIdx.x == 0) {
-        for (int c = 0; c < chunks; c++) mb_init(&full[c], 1);
+        for (int i = 0; i < tl.stages; i++) {
+            mb_init(&full[i], 1);
+            mb_init(&empty[i], 1);
+        }
         mb_init(&done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&mw);
@@ -39,71 +47,101 @@ __global__ void __launch_bounds__(kHdThreads) head_linear_kernel(const HeadLinea
     pdl_wait();
     pdl_trigger();
     if (warp == 5) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&tmem_base)), "r"(cols));
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&tmem_base)), "r"(tl.cols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    auto wait = [&](uint64_t *b, uint32_t phase) {
+        const bool ok = mb_wait_warp(b, phase & 1u);
+        if (!ok) set_status(a.status, K3MOE_DEV_TIMEOUT);
+        return ok;
+    };
     if (warp == 4) {
-        for (int c = 0; c < chunks; c++) {
-            mb_expect_tx_warp(&full[c], (uint32_t)chunk_bytes);
-            tma3d_warp(sm + c * chunk_bytes, &mw, 64 * c, n0, h, &full[c]);
-            tma3d_warp(sm + c * chunk_bytes + kHdABytes, &mx, 64 * c, h, t0, &full[c]);
+        int c = 0;
+        for (int s = 0, phase = 1; c < chunks; c++) {
+            if (c >= tl.stages && !wait(&empty[s], phase)) break;
+            mb_expect_tx_warp(&full[s], (uint32_t)stage_bytes);
+            tma3d_warp(sm + s * stage_bytes, &mw, 64 * c, n0, h, &full[s]);
+            tma3d_warp(sm + s * stage_bytes + kHdABytes, &mx, 64 * c, h, t0, &full[s]);
+            if (++s == tl.stages) {
+                s = 0;
+                phase ^= 1;
+            }
         }
-        bool ok = true;                                       // the copies land before the block ends
-        for (int c = 0; c < chunks; c++) ok = mb_wait_warp(&full[c], 0) && ok;
-        if (!ok && lane == 0) set_status(a.status, K3MOE_DEV_TIMEOUT);
+        for (int f = max(0, c - tl.stages); f < c; f++) mb_wait_warp(&full[f % tl.stages], (f / tl.stages) & 1u);   // the copies land before the block ends
     } else if (warp == 5) {
-        const uint32_t A = desc_lo(saddr(sm)), base = __reduce_max_sync(0xffffffffu, tmem), id = idesc(1, bn);
-        for (int c = 0; c < chunks; c++) {
-            if (!mb_wait_warp(&full[c], 0)) break;
+        const uint32_t A = desc_lo(saddr(sm)), base = __reduce_max_sync(0xffffffffu, tmem), id = idesc(1, tl.bn);
+        for (int c = 0, s = 0, phase = 0; c < chunks; c++) {
+            if (!wait(&full[s], phase)) break;
             tc_fence_after();
-            const uint32_t at = A + (uint32_t)(c * chunk_bytes >> 4);
+            const uint32_t at = A + (uint32_t)(s * stage_bytes >> 4);
 #pragma unroll
             for (int k = 0; k < 4; k++) umma_warp(base, at + 2 * k, at + (kHdABytes >> 4) + 2 * k, id, c > 0 || k > 0);
+            umma_commit_warp(&empty[s]);
+            if (++s == tl.stages) {
+                s = 0;
+                phase ^= 1;
+            }
         }
         umma_commit_warp(&done);
         mb_wait_warp(&done, 0);
-    } else if (mb_wait_warp(&done, 0)) {
+    } else if (wait(&done, 0)) {
         tc_fence_after();
-        const int n = n0 + 32 * warp + lane, left = min(bn, a.T - t0);
+        const int n = n0 + 32 * warp + lane, left = min(tl.bn, a.T - t0), odd = lane & 1;
         const uint32_t la = tmem + ((uint32_t)(32 * warp) << 16);
-        uint16_t *y = a.y + (size_t)h * a.y_head + n;
+        // where rows start on a word neighbouring lanes trade a token each, two columns of one token a store
+        const bool pairs = a.N % 2 == 0 && a.y_stride % 2 == 0 && a.y_head % 2 == 0 && reinterpret_cast<uintptr_t>(a.y) % 4 == 0;
+        uint16_t *y = a.y + (size_t)h * a.y_head + (size_t)t0 * a.y_stride;
         for (int c0 = 0; c0 < left; c0 += 16) {
             uint32_t v[16];
             tmem_ld16_nowait(la + c0, v);
             tmem_wait_ld();
+            if (pairs) {
+                uint16_t *p = y + (size_t)(c0 + odd) * a.y_stride + (n & ~1);
 #pragma unroll
-            for (int j = 0; j < 16; j++)
-                if (n < a.N && c0 + j < left)
-                    *reinterpret_cast<__nv_bfloat16 *>(y + (size_t)(t0 + c0 + j) * a.y_stride) = __float2bfloat16_rn(__uint_as_float(v[j]));
+                for (int j = 0; j < 8; j++, p += 2 * a.y_stride) {
+                    const float z0 = __uint_as_float(v[2 * j]), z1 = __uint_as_float(v[2 * j + 1]);
+                    const float got = __shfl_xor_sync(0xffffffffu, odd ? z0 : z1, 1);
+                    const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(got, z1) : __floats2bfloat162_rn(z0, got);
+                    if (n < a.N && c0 + 2 * j + odd < left) *reinterpret_cast<__nv_bfloat162 *>(p) = w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; j++)
+                    if (n < a.N && c0 + j < left)
+                        *reinterpret_cast<__nv_bfloat16 *>(y + (size_t)(c0 + j) * a.y_stride + n) = __float2bfloat16_rn(__uint_as_float(v[j]));
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+    if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tl.cols));
 }
 
 }  // namespace
 
 cudaError_t launch_head_linear(const HeadLinearArgs &a, cudaStream_t s)
 {
-    const int bn = std::min(kHdBN, (a.T + 15) & ~15), chunks = (a.K + 63) / 64;
+    HeadTile tl{};
+    const int tiles = (a.T + kHdMaxBN - 1) / kHdMaxBN;
+    tl.bn = ((a.T + tiles - 1) / tiles + 15) & ~15;
+    tl.cols = tl.bn <= 32 ? 32 : tl.bn <= 64 ? 64 : 128;
+    const int stage_bytes = kHdABytes + tl.bn * 128;
+    tl.stages = std::min(std::min(kHdMaxStages, kHdRing / stage_bytes), (a.K + 63) / 64);
     CUtensorMap mw{}, mx{};
     if (!map16x3(&mw, a.w, (uint64_t)a.H, (uint64_t)a.N * a.K, (uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.K, 128, 1) ||
-        !map16x3(&mx, a.x, (uint64_t)a.T, (uint64_t)a.x_stride, (uint64_t)a.H, (uint64_t)a.x_head, (uint64_t)a.K, 1, (uint32_t)bn))
+        !map16x3(&mx, a.x, (uint64_t)a.T, (uint64_t)a.x_stride, (uint64_t)a.H, (uint64_t)a.x_head, (uint64_t)a.K, 1, (uint32_t)tl.bn))
         return cudaErrorInvalidValue;
-    const cudaError_t allowed = once_a_device([] {
-        return cudaFuncSetAttribute(head_linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    1024 + kHdMaxChunks * (kHdABytes + kHdBN * 128));
-    });
+    const cudaError_t allowed =
+        once_a_device([] { return cudaFuncSetAttribute(head_linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kHdRing); });
     if (allowed != cudaSuccess) return allowed;
     timing_begin("head_linear", s);
-    const cudaError_t err = launch_pdl(head_linear_kernel, dim3((unsigned)((a.N + 127) / 128), (unsigned)a.H, (unsigned)((a.T + bn - 1) / bn)),
-                                       dim3(kHdThreads), (size_t)(1024 + chunks * (kHdABytes + bn * 128)), s, a, bn, mw, mx);
+    const cudaError_t err = launch_pdl(head_linear_kernel, dim3((unsigned)((a.N + 127) / 128), (unsigned)a.H, (unsigned)((a.T + tl.bn - 1) / tl.bn)),
+                                       dim3(kHdThreads), (size_t)(1024 + tl.stages * stage_bytes), s, a, tl, mw, mx);
     count_launch();
     timing_end("head_linear", s);
     return err;

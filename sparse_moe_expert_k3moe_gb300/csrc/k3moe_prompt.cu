@@ -328,12 +328,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                     if (!(ok = wait(sh.k_full[j & 1], j >> 1))) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int b = 0; b < kPrQBoxes; b++)
+                    for (int b = 0; b < kPrQBoxes; b++) {
+                        if (b == kPrQBoxes - 1 && lane == 0) mb_arrive(&sh.turn[half ^ 1]);     // the other gets ready under the last ones
 #pragma unroll
                         for (int k = 0; k < 4; k++) umma_warp(S, sm_q + b * box + 2 * k, B[b] + 2 * k, ids, b > 0 || k > 0);
+                    }
                     umma_commit_warp(&sh.s_full[half]);
                     done(&sh.k_empty[j & 1], j);
-                    if (lane == 0) mb_arrive(&sh.turn[half ^ 1]);
                 }
             }
             __syncwarp();
