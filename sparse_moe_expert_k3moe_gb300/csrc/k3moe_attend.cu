@@ -37,18 +37,77 @@ constexpr float kAtSlack = 8.0f;
 // A part's sums in the workspace: O [query][c], then the maxima and the sums of the weights.
 constexpr size_t kAtPart = (size_t)kAtRows * kLatC + 2 * kAtRows;
 // What a cut leaves to join: the query block's first part is share i's last (its first or second), the others
-// are the first ones of the shares after it.
+// are the first ones of the shares after it, whose `owner` i is.
 struct AttendJoin {
-    int t0, row0, rows, second, parts;                        // its queries; rows = 0: nothing to join
+    int t0, row0, rows, second, parts, owner;                 // rows = 0: none begins here; owner = -1: none goes on here
 };
 
-struct AttendShared {
+// Sequence i: its queries, cached rows, blocks of 1 << shift queries and tiles of each; false when something does not fit.
+struct AttendSeq {
+    int t0, n, len, blocks, tiles;
+    __device__ bool read(const AttendArgs &a, int i, int shift)
+    {
+        bool ok = latent_queries(a.seq_start, a.n_seq, a.T, i, &t0, &n);
+        len = a.kv_len[i];
+        ok = ok && len >= 0 && len <= a.max_pages * a.page;
+        blocks = ok ? (n * a.H + (1 << shift) - 1) >> shift : 0;
+        tiles = max(1, (len + kAtTile - 1) / kAtTile);        // one that has nothing where no row is cached
+        return ok;
+    }
+};
+
+// The walk of a block's share of tiles, query block by query block.
+template <typename I> struct AttendWalk {
+    I u, end, base;                                           // next tile, the share's end, the sequence's first tile
+    int seq, shift;
+    AttendSeq s;
+    int row0, tile0, tile1;                                   // the query block and its tiles here
+    __device__ bool next(const AttendArgs &a)
+    {
+        if (u >= end) return false;
+        while (u >= base + (I)s.blocks * s.tiles) {
+            base += (I)s.blocks * s.tiles;
+            s.read(a, ++seq, shift);
+        }
+        const I at = u - base;
+        const int block = (int)quotient(at, s.tiles);
+        row0 = block << shift;
+        tile0 = (int)(at - (I)block * s.tiles);
+        tile1 = (int)min((I)s.tiles, tile0 + (end - u));
+        u += tile1 - tile0;
+        return true;
+    }
+    __device__ int rows(const AttendArgs &a) const { return min(1 << shift, s.n * a.H - row0); }
+    __device__ bool whole() const { return tile0 == 0 && tile1 == s.tiles; }
+};
+
+// Even shares of all tiles, the first `more` of them a tile longer; where there are fewer tiles than shares the last are empty.
+template <typename I> struct AttendShares {
+    I each, more;
+    __device__ void cut(I all, int n)
+    {
+        each = quotient(all, n);
+        more = all - each * n;
+    }
+    __device__ I begin(int i) const { return i * each + min((I)i, more); }
+    __device__ int of(I tile) const                           // the share that has it
+    {
+        return (int)(tile < more * (each + 1) ? tile / (each + 1) : more + (tile - more * (each + 1)) / each);
+    }
+};
+
+template <typename I> struct AttendShared {
     uint64_t q_full, full[2][2], empty[2][2], r_empty[2], s_full[2], p_ready[2], pv_done, drain[2];    // by the tile's turn, halves of c
     uint32_t tmem;
     volatile int bail;
     int spoiled[2];                                           // by the query block's turn
     union {                                                   // (one after the other)
-        UnitSearch search;
+        struct {
+            UnitSearch<I> search;
+            AttendWalk<I> walk;
+            AttendShares<I> shares;
+            int have;
+        } first;
         float top[2][4][32], sum[2][4][32];
     };
     float m[kAtRows];
@@ -57,56 +116,79 @@ struct AttendShared {
     };
     int lim[2][32];
 };
+static_assert(sizeof(AttendShared<long long>) <= 2048 && kAtSmem + 2048 <= 227 * 1024, "an SM's shared memory");
 
-static_assert(sizeof(AttendShared) <= 2048 && kAtSmem + 2048 <= 227 * 1024, "an SM's shared memory");
-
-// Sequence i: its queries, cached rows, blocks of queries and tiles of each; false when something does not fit.
-struct AttendSeq {
-    int t0, n, len, blocks, tiles;
-    __device__ bool read(const AttendArgs &a, int i)
-    {
-        bool ok = latent_queries(a.seq_start, a.n_seq, a.T, i, &t0, &n);
-        len = a.kv_len[i];
-        ok = ok && len >= 0 && len <= a.max_pages * a.page;
-        blocks = ok ? (int)(((long long)n * a.H + kAtRows - 1) / kAtRows) : 0;
-        tiles = max(1, (len + kAtTile - 1) / kAtTile);        // one that has nothing where no row is cached
-        return ok;
-    }
-    __device__ long long units() const { return (long long)blocks * tiles; }
-};
-
-// The walk of a block's share of tiles, query block by query block.
-struct AttendWalk {
-    long long u, end, base;                                   // next tile, the share's end, the sequence's first tile
-    int seq;
-    AttendSeq s;
-    int row0, tile0, tile1;                                   // the query block and its tiles here
-    __device__ void begin(const AttendArgs &a, int i, long long before, long long from, long long to)
-    {
-        u = from;
-        end = to;
-        seq = i;
-        base = from - before;
-        if (u < end) s.read(a, i);
-    }
-    __device__ bool next(const AttendArgs &a)
-    {
-        if (u >= end) return false;
-        while (u >= base + s.units()) {
-            base += s.units();
-            s.read(a, ++seq);
+// The block's share and its first query block, into shared memory.  Up to 128 sequences are one warp's, four a lane, and with few
+// tiles the query blocks get smaller, so that more SMs have one.
+constexpr int kAtPlanSeqs = 128;
+template <typename I> __device__ __forceinline__ void attend_plan(const AttendArgs &a, AttendShared<I> &sh, int32_t *status)
+{
+    const int lane = threadIdx.x & 31;
+    AttendShares<I> shares;
+    AttendWalk<I> w;
+    w.shift = 6;
+    bool mine = false;                                        // this thread has found the share's first tile
+    I before = 0;
+    if (a.n_seq <= kAtPlanSeqs) {
+        int rows[4], tiles[4];
+        I all = 0;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            AttendSeq s;
+            s.blocks = s.n = s.tiles = 0;
+            if (4 * lane + k < a.n_seq && !s.read(a, 4 * lane + k, 6)) set_status(status, K3MOE_DEV_BAD_OFFSETS);
+            rows[k] = s.blocks > 0 ? s.n * a.H : 0;
+            tiles[k] = s.tiles;
+            all += (I)s.blocks * s.tiles;
         }
-        const long long at = u - base;
-        const int block = (int)quotient(at, s.tiles);
-        row0 = block * kAtRows;
-        tile0 = (int)(at - (long long)block * s.tiles);
-        tile1 = (int)min((long long)s.tiles, tile0 + (end - u));
-        u += tile1 - tile0;
-        return true;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        const int n = gridDim.x;
+        if (all <= n / 2) w.shift = all <= n / 4 ? 4 : 5;
+        I units[4], each = 0;
+#pragma unroll
+        for (int k = 0; k < 4; k++) each += units[k] = (I)((rows[k] + (1 << w.shift) - 1) >> w.shift) * tiles[k];
+        const I upto = warp_scan(each, lane);
+        shares.cut(__shfl_sync(0xffffffffu, upto, 31), gridDim.x);
+        w.u = shares.begin(blockIdx.x);
+        before = w.u - (upto - each);
+        mine = before >= 0 && before < each;
+        w.seq = 4 * lane;
+#pragma unroll
+        for (int k = 0; k < 3; k++)
+            if (mine && w.seq == 4 * lane + k && before >= units[k]) {
+                before -= units[k];
+                w.seq++;
+            }
+    } else {
+        I all;
+        w.seq = find_unit<kAtThreads, I>(
+            sh.first.search, a.n_seq, &before, &all,
+            [&](int i) -> I {
+                AttendSeq s;
+                if (!s.read(a, i, 6)) set_status(status, K3MOE_DEV_BAD_OFFSETS);
+                return (I)s.blocks * s.tiles;
+            },
+            [&](I all) {
+                shares.cut(all, gridDim.x);
+                return shares.begin(blockIdx.x);
+            });
+        w.u = shares.begin(blockIdx.x);
+        mine = w.seq >= 0 && threadIdx.x == 0;
     }
-    __device__ int rows(const AttendArgs &a) const { return (int)min((long long)kAtRows, (long long)s.n * a.H - row0); }
-    __device__ bool whole() const { return tile0 == 0 && tile1 == s.tiles; }
-};
+    w.end = shares.begin(blockIdx.x + 1);
+    if (w.u >= w.end) {
+        if ((threadIdx.x & 31) == 0) sh.first.have = 0;
+        return;
+    }
+    if (!mine) return;
+    w.base = w.u - before;
+    w.s.read(a, w.seq, w.shift);
+    w.next(a);
+    sh.first.walk = w;
+    sh.first.shares = shares;
+    sh.first.have = 1;
+}
 
 // S^T's 16 lanes of a warp, 32 columns: v[4 k + 2 i + j] is row lane / 4 + 8 i, column 8 k + 2 (lane % 4) + j.
 __device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[16])
@@ -142,13 +224,14 @@ __device__ __forceinline__ bool group_any(int group, bool p)
         : "memory");
     return r != 0;
 }
+template <typename I>
 __global__ void __launch_bounds__(kAtThreads, 1)
     attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap m4, const __grid_constant__ CUtensorMap m1, float *parts, AttendJoin *joins)
 {
     extern __shared__ __align__(1024) uint8_t asm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(asm_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *sm_p = sm + kAtQ, *ring = sm_p + kAtP;
-    __shared__ AttendShared sh;
+    __shared__ AttendShared<I> sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t *status = reinterpret_cast<int32_t *>(a.ws);
     if (threadIdx.x == 0) {
@@ -172,32 +255,24 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
     pdl_wait();
     pdl_trigger();
-    long long before, units;
-    // even shares of `each` tiles and the first ones a tile more; fewer shares than blocks where there are fewer tiles
-    const auto share = [&](int i, long long all) {
-        const long long each = quotient(all, gridDim.x);
-        return i * each + min((long long)i, all - each * gridDim.x);
-    };
-    const int seq0 = find_unit<kAtThreads>(
-        sh.search, a.n_seq, &before, &units,
-        [&](int i) -> long long {
-            AttendSeq s;
-            if (!s.read(a, i)) set_status(status, K3MOE_DEV_BAD_OFFSETS);
-            return s.units();
-        },
-        [&](long long all) { return share(blockIdx.x, all); });
-    const long long from = share(blockIdx.x, units), to = share(blockIdx.x + 1, units);
-    if (from >= to) {
-        if (threadIdx.x == 0) joins[blockIdx.x].rows = 0;
-        return;
-    }
     if (warp == kAtWarpS) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sh.tmem)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    if (a.n_seq > kAtPlanSeqs || warp == kAtWarpLoad) attend_plan<I>(a, sh, status);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    const bool have = sh.first.have;
+    AttendWalk<I> w = sh.first.walk;
+    const AttendShares<I> shares = sh.first.shares;
+    const int shift = w.shift;
+    __syncthreads();                                          // what is read here is written over by the softmax
+    if (!have) {
+        if (threadIdx.x == 0) joins[blockIdx.x] = AttendJoin{0, 0, 0, 0, 0, -1};
+        if (warp == kAtWarpS) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(512));
+        return;
+    }
     constexpr uint32_t tmem = 0;                              // all 512 columns: the allocation starts at the first
     auto wait = [&](uint64_t &b, int phase) {
         const bool ok = mb_wait_warp(&b, (uint32_t)phase & 1u);
@@ -209,8 +284,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     };
     // the same for the warps that meet at barriers: after a wait that gave up they go on without waiting, to the end
     auto go_on = [&](uint64_t &b, int phase) { return !sh.bail && wait(b, phase); };
-    AttendWalk w;
-    w.begin(a, seq0, before, from, to);
 
     if (warp < kAtWarpS) {
         // ---------------- queries, softmax and output: cached rows 16 q + lane / 4 and 8 more of a tile, queries 32 g ..
@@ -220,6 +293,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         // the next query block's rows, in the order the tensor core reads: 64 columns of 64 rows a box, 128-byte swizzle
         auto load_q = [&]() {
             const int r = threadIdx.x >> 2, rows = w.rows(a), gr = w.row0 + (r < rows ? r : 0);
+            if (r >= 1 << shift) return;
             const uint16_t *src = a.q + (size_t)(w.s.t0 + gr / a.H) * a.q_stride + (size_t)(gr % a.H) * a.q_head;
             const uint32_t dst = saddr(sm) + (uint32_t)(r * 128);
 #pragma unroll
@@ -235,11 +309,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (lane == 0) mb_arrive(&sh.q_full);
         };
         int tile = 0;                                         // so far
-        bool more = w.next(a);
+        bool more = true;
         load_q();
         q_loaded();
+        const bool idle = 32 * g >= 1 << shift;               // no query of this group's
         for (int seg = 0; more; seg++) {
-            const AttendWalk now = w;
+            const AttendWalk<I> now = w;
             const int rows = w.rows(a);
             // rows of the cache that each query sees
             auto limit = [&](int r) { return a.causal ? max(0, now.s.len - (now.s.n - 1 - (now.row0 + r) / a.H)) : now.s.len; };
@@ -267,6 +342,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         const int see = lim[8 * (j >> 2) + col + (j & 1)];
                         v[j] = at + 4 * (j & 2) < see ? v[j] : -INFINITY;
                     }
+                if (idle || shift == 4)                       // columns that no product has written
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        if (idle || j >= 8) v[j] = -INFINITY;
                 float over = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 16; j++) over = fmaxf(over, v[j] + m[(j >> 2) * 2 + (j & 1)]);
@@ -433,12 +512,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
     } else if (warp == kAtWarpS) {
         // ---------------- scores, a tile ahead of the products with c where its boxes have landed
-        const uint32_t id = (idesc(1, kAtRows) & ~(31u << 24)) | (4u << 24);                          // M = 64 rows of the cache
+        const uint32_t id = (idesc(1, 1 << uniform(shift)) & ~(31u << 24)) | (4u << 24);              // M = 64 rows of the cache
         const uint32_t q0 = desc_lo(saddr(sm)), c0 = desc_lo(saddr(ring));
         constexpr uint32_t box = kAtBox >> 4, q_box = kAtQBox >> 4;
         int tile = 0;
         bool ok = true;
-        for (int seg = 0; ok && w.next(a); seg++) {
+        for (int seg = 0; ok && (seg == 0 || w.next(a)); seg++) {
             if (!(ok = wait(sh.q_full, seg))) break;
             const int n = uniform(w.tile1 - w.tile0);
 #pragma unroll 1
@@ -468,12 +547,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         mb_wait_warp(&sh.drain[0], 0);
     } else if (warp == kAtWarpV) {
         // ---------------- products of the weights with c
-        const uint32_t id = idesc(1, kAtRows) | (1u << 15) | (1u << 16);                              // both with M, N contiguous
+        const uint32_t id = idesc(1, 1 << uniform(shift)) | (1u << 15) | (1u << 16);                  // both with M, N contiguous
         const uint32_t p0 = desc_lo(saddr(sm_p)), c0 = desc_lo(saddr(ring), kAtBox);
         constexpr uint32_t box = kAtBox >> 4;
         int tile = 0;
         bool ok = true;
-        while (ok && w.next(a)) {
+        for (bool more = true; ok && more; more = ok && w.next(a)) {
             const int n = uniform(w.tile1 - w.tile0);
 #pragma unroll 1
             for (int t = 0; t < n; t++, tile++) {
@@ -498,8 +577,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         // ---------------- the cache's rows: half of c, of a page's rows each box, a lane a page; the first half's warp loads r
         const int box_rows = min(a.page, kAtTile), pieces = kAtTile / box_rows, half = uniform(warp - kAtWarpLoad);
         int tile = 0;
-        bool ok = true, last = false;
-        for (int seg = 0; ok && w.next(a); seg++) {
+        bool ok = true;
+        AttendJoin join{0, 0, 0, 0, 0, -1};
+        for (int seg = 0; ok && (seg == 0 || w.next(a)); seg++) {
+            const int begun = w.tile0, left = w.s.tiles - w.tile1;
+            if (seg == 0 && begun > 0) join.owner = shares.of(shares.begin(blockIdx.x) - begun);
             const int n_tiles = uniform(w.tile1 - w.tile0), len = w.s.len, tile0 = w.tile0;
             const int32_t *pages = a.pages + (size_t)w.seq * a.max_pages;
 #pragma unroll 1
@@ -536,15 +618,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 if (half == 0) load(16 + turn, 8);
             }
             // the query block that a cut leaves unfinished, for the second kernel: its first part writes it down
-            last = w.u >= w.end && w.tile0 == 0 && w.tile1 < w.s.tiles;
-            if (last && half == 0 && lane == 0) {
-                // the share that has the query block's last tile
-                const long long at = w.u + (w.s.tiles - w.tile1) - 1, each = quotient(units, gridDim.x), more = units - each * gridDim.x;
-                const long long in = at < more * (each + 1) ? at / (each + 1) : more + (at - more * (each + 1)) / each;
-                joins[blockIdx.x] = AttendJoin{w.s.t0, w.row0, w.rows(a), seg > 0, (int)(in - blockIdx.x) + 1};
+            if (begun == 0 && left > 0) {
+                join.t0 = w.s.t0;
+                join.row0 = w.row0;
+                join.rows = w.rows(a);
+                join.second = seg > 0;
+                join.parts = shares.of(w.u + left - 1) - blockIdx.x + 1;
             }
         }
-        if (!last && half == 0 && lane == 0) joins[blockIdx.x].rows = 0;
+        if (half == 0 && lane == 0) joins[blockIdx.x] = join;
         // the block's shared memory stays until its last copies have landed, when another role gave up too (boxes that a
         // wait cut short do not complete: that wait is bounded as well)
         for (int f = max(0, tile - 2 + !ok); f < tile + !ok; f++) mb_wait_warp(&sh.full[f & 1][half], (uint32_t)(f >> 1) & 1u);
@@ -556,143 +638,143 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining
-// out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over the parts i, M the largest m.  Where a query block has few parts a
-// warp takes a query, a lane 16 columns; where it has many, a block takes 128 columns of a query, its warps every fourth part.
-constexpr int kJoinThreads = 128, kMaxShares = 512, kJoinMany = 8;
+// out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over the parts i, M the largest m.  Blocks (x, y) for share x: of a query
+// block with few parts, the share's that begins it have four queries each, a warp a query, a lane 16 columns; with many, all its
+// shares' have a quarter of a query's columns each, their warps every fourth part.
+constexpr int kJoinThreads = 128, kJoinBlocks = kAtRows / 4, kMaxShares = 512, kJoinMany = 8;
+
+struct JoinParts {
+    const float *p0, *p1;                                     // the first part, and the second
+    __device__ JoinParts(const float *parts, int share, int second)
+        : p0(parts + (size_t)(2 * share + second) * kAtPart), p1(parts + (size_t)(2 * share + 2) * kAtPart)
+    {
+    }
+    __device__ const float *operator()(int p) const { return p == 0 ? p0 : p1 + (size_t)(p - 1) * 2 * kAtPart; }
+};
+__device__ __forceinline__ void join_add(float4 &o, float f, const float4 &x)
+{
+    if (f == 0.0f) return;
+    o.x = fmaf(f, x.x, o.x);
+    o.y = fmaf(f, x.y, o.y);
+    o.z = fmaf(f, x.z, o.z);
+    o.w = fmaf(f, x.w, o.w);
+}
+__device__ __forceinline__ void join_put(uint16_t *to, const float4 &o, float inv)
+{
+    const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
+    *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<const uint2 *>(w);
+}
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
 
 __global__ void __launch_bounds__(kJoinThreads)
-    attend_join_kernel(const AttendArgs a, const float *parts, const AttendJoin *joins, const int shares)
+    attend_join_kernel(const AttendArgs a, const float *parts, const AttendJoin *joins)
 {
     pdl_wait();
     pdl_trigger();
-    __shared__ int upto[kMaxShares];                          // pieces of work of the joins up to each
-    __shared__ int warp_sum[kJoinThreads / 32];
+    __shared__ float factor[kMaxShares], red[2][4];
     __shared__ float4 sum[3][32];
-    __shared__ float weights[3];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int total = 0;
-    for (int i0 = 0; i0 < shares; i0 += kJoinThreads) {
-        const int i = i0 + threadIdx.x;
-        int v = 0;
-        if (i < shares) {
-            const int rows = joins[i].rows;
-            if (rows > 0) v = joins[i].parts >= kJoinMany ? 4 * rows : (rows + 3) / 4;
-        }
+    const AttendJoin j = joins[blockIdx.x];
+    auto row_of = [&](const AttendJoin &j, int r) { return (size_t)j.t0 * a.H + j.row0 + r; };
+    auto inverse = [](float L) { return L == 0.0f ? 0.0f : 1.0f / L; };
+    const int r = 4 * blockIdx.y + warp;
+    if (j.parts < kJoinMany && r < j.rows) {
+        const JoinParts part(parts, blockIdx.x, j.second);
+        float m = -INFINITY, l = 0.0f;
+        float4 x[2][4];
+        const size_t at = (size_t)r * kLatC + 4 * lane;
+        auto load = [&](int p) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += x;
+            for (int i = 0; i < 4; i++) x[p & 1][i] = __ldcg(reinterpret_cast<const float4 *>(part(p) + at + 128 * i));
+        };
+        load(0);
+        load(1);                                              // a join has two parts at least
+        if (lane < j.parts) {
+            m = part(lane)[kAtRows * kLatC + r];
+            l = part(lane)[kAtRows * kLatC + kAtRows + r];
         }
-        if (lane == 31) warp_sum[warp] = v;
-        __syncthreads();
-        int before = total;
-        for (int k = 0; k < kJoinThreads / 32; k++) {
-            if (k < warp) before += warp_sum[k];
-            total += warp_sum[k];
-        }
-        if (i < shares) upto[i] = before + v;
-        __syncthreads();
-    }
-    for (int unit = blockIdx.x; unit < total; unit += gridDim.x) {
-        int lo = 0, hi = shares - 1;                          // the first share with upto > unit
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (upto[mid] > unit)
-                hi = mid;
-            else
-                lo = mid + 1;
-        }
-        const AttendJoin j = joins[lo];
-        const bool many = j.parts >= kJoinMany;
-        const int piece = unit - (lo > 0 ? upto[lo - 1] : 0), r = many ? piece >> 2 : 4 * piece + warp;
-        const float *p0 = parts + (size_t)(2 * lo + j.second) * kAtPart, *p1 = parts + (size_t)(2 * lo + 2) * kAtPart;
-        auto part = [&](int p) { return p == 0 ? p0 : p1 + (size_t)(p - 1) * 2 * kAtPart; };
-        if (!many && r >= j.rows) continue;
-        float M = -INFINITY;                                  // of all parts
-        for (int p = lane; p < j.parts; p += 32) M = fmaxf(M, part(p)[kAtRows * kLatC + r]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        // a warp's parts `from`, `from` + step ..: their factors by the lanes, the columns four parts at a time
-        const int from = many ? warp : 0, step = many ? 4 : 1, n = (j.parts - from + step - 1) / step;
-        const size_t col = (size_t)r * kLatC + (many ? 128 * (piece & 3) : 0) + 4 * lane;
+        const float M = warp_max(m), f = m == -INFINITY ? 0.0f : exp2_fast(m - M), L = warp_sum(f == 0.0f ? 0.0f : f * l), inv = inverse(L);
         float4 o[4] = {};
-        float L = 0.0f;
-        for (int b = 0; b < n; b += 32) {
-            float f = 0.0f, l = 0.0f;
-            if (b + lane < n) {
-                const float *x = part(from + (b + lane) * step) + kAtRows * kLatC + r;
-                f = x[0] == -INFINITY ? 0.0f : exp2_fast(x[0] - M);
-                l = f == 0.0f ? 0.0f : f * x[kAtRows];
-            }
-            L += l;
-            const int left = min(32, n - b);
-            if (many) {
-#pragma unroll 1
-                for (int k = 0; k < left; k += 8) {
-                    float4 x[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        if (k + i < left) x[i] = __ldcg(reinterpret_cast<const float4 *>(part(from + (b + k + i) * step) + col));
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const float w = __shfl_sync(0xffffffffu, f, (k + i) & 31);
-                        if (k + i < left && w != 0.0f) {
-                            o[0].x = fmaf(w, x[i].x, o[0].x);
-                            o[0].y = fmaf(w, x[i].y, o[0].y);
-                            o[0].z = fmaf(w, x[i].z, o[0].z);
-                            o[0].w = fmaf(w, x[i].w, o[0].w);
-                        }
-                    }
-                }
-            } else {
 #pragma unroll 2
-                for (int k = 0; k < left; k++) {
-                    const float w = __shfl_sync(0xffffffffu, f, k);
+        for (int p = 0; p < j.parts; p++) {
+            const float w = __shfl_sync(0xffffffffu, f, p);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(part(b + k) + col + 128 * i));
-                        if (w != 0.0f) {
-                            o[i].x = fmaf(w, x.x, o[i].x);
-                            o[i].y = fmaf(w, x.y, o[i].y);
-                            o[i].z = fmaf(w, x.z, o[i].z);
-                            o[i].w = fmaf(w, x.w, o[i].w);
-                        }
-                    }
-                }
-            }
+            for (int i = 0; i < 4; i++) join_add(o[i], w, x[p & 1][i]);
+            if (p + 2 < j.parts) load(p + 2);
         }
+        uint16_t *to = a.out + row_of(j, r) * kLatC + 4 * lane;
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
-        if (many) {                                           // the first warp adds the others'
-            if (warp > 0) {
-                sum[warp - 1][lane] = o[0];
-                if (lane == 0) weights[warp - 1] = L;
-            }
-            __syncthreads();
-            if (warp == 0)
-#pragma unroll
-                for (int k = 0; k < 3; k++) {
-                    const float4 x = sum[k][lane];
-                    o[0].x += x.x;
-                    o[0].y += x.y;
-                    o[0].z += x.z;
-                    o[0].w += x.w;
-                    L += weights[k];
-                }
-            __syncthreads();
-            if (warp > 0) continue;
-        }
-        const size_t row = (size_t)j.t0 * a.H + j.row0 + r;
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        uint16_t *to = a.out + row * kLatC + (many ? 128 * (piece & 3) : 0) + 4 * lane;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            if (many && i > 0) break;
-            const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o[i].x * inv, o[i].y * inv), __floats2bfloat162_rn(o[i].z * inv, o[i].w * inv)};
-            *reinterpret_cast<uint2 *>(to + 128 * i) = *reinterpret_cast<const uint2 *>(w);
-        }
-        if (a.lse && lane == 0 && (!many || (piece & 3) == 0)) a.lse[row] = (M + log2f(L)) * kLatLn2;
+        for (int i = 0; i < 4; i++) join_put(to + 128 * i, o[i], inv);
+        if (a.lse && lane == 0) a.lse[row_of(j, r)] = (M + log2f(L)) * kLatLn2;
     }
+    // pieces of the join `j` that share `first` begins: quarters of rows
+    auto many = [&](const AttendJoin &j, int first) {
+        if (j.rows == 0 || j.parts < kJoinMany) return;
+        const JoinParts part(parts, first, j.second);
+        for (int piece = (blockIdx.x - first) * kJoinBlocks + blockIdx.y; piece < 4 * j.rows; piece += j.parts * kJoinBlocks) {
+            const int r = piece >> 2, quarter = 128 * (piece & 3);
+            float m[kMaxShares / kJoinThreads], l[kMaxShares / kJoinThreads], top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kMaxShares / kJoinThreads; k++) {
+                const int p = threadIdx.x + k * kJoinThreads;
+                m[k] = -INFINITY;
+                if (p < j.parts) {
+                    m[k] = part(p)[kAtRows * kLatC + r];
+                    l[k] = part(p)[kAtRows * kLatC + kAtRows + r];
+                }
+                top = fmaxf(top, m[k]);
+            }
+            top = warp_max(top);
+            if (lane == 0) red[0][warp] = top;
+            __syncthreads();
+            const float M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+            float L = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kMaxShares / kJoinThreads; k++) {
+                const int p = threadIdx.x + k * kJoinThreads;
+                const float f = m[k] == -INFINITY ? 0.0f : exp2_fast(m[k] - M);
+                if (p < j.parts) factor[p] = f;
+                if (f != 0.0f) L += f * l[k];
+            }
+            L = warp_sum(L);
+            if (lane == 0) red[1][warp] = L;
+            __syncthreads();
+            L = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const size_t at = (size_t)r * kLatC + quarter + 4 * lane;
+            for (int p0 = warp; p0 < j.parts; p0 += 4 * 10) {
+                float4 x[10];
+#pragma unroll
+                for (int i = 0; i < 10; i++)
+                    if (p0 + 4 * i < j.parts) x[i] = __ldcg(reinterpret_cast<const float4 *>(part(p0 + 4 * i) + at));
+#pragma unroll
+                for (int i = 0; i < 10; i++)
+                    if (p0 + 4 * i < j.parts) join_add(o, factor[p0 + 4 * i], x[i]);
+            }
+            if (warp > 0) sum[warp - 1][lane] = o;
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int k = 0; k < 3; k++) join_add(o, 1.0f, sum[k][lane]);
+                join_put(a.out + row_of(j, r) * kLatC + quarter + 4 * lane, o, inverse(L));
+                if (a.lse && lane == 0 && quarter == 0) a.lse[row_of(j, r)] = (M + log2f(L)) * kLatLn2;
+            }
+            __syncthreads();
+        }
+    };
+    many(j, blockIdx.x);
+    if (j.owner >= 0) many(joins[j.owner], j.owner);
 }
 
 int attend_shares() { return std::min(num_sms(), kMaxShares); }
@@ -714,19 +796,24 @@ cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
     const uint32_t box_rows = (uint32_t)std::min(a.page, kAtTile);
     if (!map16x3(&m4, a.cache, kAtBoxes, 64, rows, kLatRow, 64, box_rows, 4) || !map16x3(&m1, a.cache, kAtBoxes, 64, rows, kLatRow, 64, box_rows, 1))
         return cudaErrorInvalidValue;
-    const cudaError_t allowed =
-        once_a_device([] { return cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem); });
+    const cudaError_t allowed = once_a_device([] {
+        const cudaError_t e = cudaFuncSetAttribute(attend_kernel<int>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem);
+        return e != cudaSuccess ? e : cudaFuncSetAttribute(attend_kernel<long long>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem);
+    });
     if (allowed != cudaSuccess) return allowed;
+    // whether every count of tiles fits 32 bits, whatever the lengths are
+    const long long most = ((long long)a.T * a.H / kAtRows + std::min(a.n_seq, a.T)) * ((long long)a.max_pages * a.page / kAtTile + 1);
     const int shares = attend_shares();
     AttendJoin *joins = reinterpret_cast<AttendJoin *>(a.ws + kCtrOffset + kCtrBytes);
     float *parts = reinterpret_cast<float *>(a.ws + kCtrOffset + kCtrBytes + align256((size_t)shares * sizeof(AttendJoin)));
     timing_begin("latent_attend", s);
-    cudaError_t err = launch_pdl(attend_kernel, dim3((unsigned)shares), dim3(kAtThreads), kAtSmem, s, a, m4, m1, parts, joins);
+    cudaError_t err = launch_pdl(most < INT32_MAX ? attend_kernel<int> : attend_kernel<long long>, dim3((unsigned)shares), dim3(kAtThreads), kAtSmem, s, a,
+                                 m4, m1, parts, joins);
     count_launch();
     timing_end("latent_attend", s);
     if (err != cudaSuccess) return err;
     timing_begin("latent_attend_join", s);
-    err = launch_pdl(attend_join_kernel, dim3((unsigned)(shares * 8)), dim3(kJoinThreads), 0, s, a, (const float *)parts, (const AttendJoin *)joins, shares);
+    err = launch_pdl(attend_join_kernel, dim3((unsigned)shares, kJoinBlocks), dim3(kJoinThreads), 0, s, a, (const float *)parts, (const AttendJoin *)joins);
     count_launch();
     timing_end("latent_attend_join", s);
     return err;

@@ -29,59 +29,58 @@ __device__ __forceinline__ bool latent_queries(const int32_t *start, int n_seq, 
 
 // a / b of positive numbers, in 32 bits where they fit: the long division is a hundred instructions.
 __device__ __forceinline__ long long quotient(long long a, int b) { return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b); }
+__device__ __forceinline__ int quotient(int a, int b) { return (int)((uint32_t)a / (uint32_t)b); }
 
-// A block's search over the sequences, count(i) units each, by all threads at once: which one unit want(total) is
-// of (-1: there are not as many), how many units of it come before, and the units in all.
-struct UnitSearch {
-    long long sums[32], before;
+// A block's search over the sequences, count(i) units each: which one unit want(total) is of (-1: there are not as
+// many), how many units of it come before, and the units in all.  I: int where the units are known to fit.
+template <typename I> struct UnitSearch {
+    I sums[32], before;
     int seq;
 };
-template <int THREADS, typename Count, typename Want>
-__device__ __forceinline__ int find_unit(UnitSearch &sh, int n_seq, long long *before, long long *total, Count count, Want want)
+template <typename I> __device__ __forceinline__ I warp_scan(I v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const I x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    return v;
+}
+template <int THREADS, typename I, typename Count, typename Want>
+__device__ __forceinline__ int find_unit(UnitSearch<I> &sh, int n_seq, I *before, I *total, Count count, Want want)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (n_seq <= 32) {                                        // every warp for itself
-        const long long mine = lane < n_seq ? count(lane) : 0;
-        long long upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
+        const I mine = lane < n_seq ? count(lane) : 0, upto = warp_scan(mine, lane);
         *total = __shfl_sync(0xffffffffu, upto, 31);
-        const long long unit = want(*total);
+        const I unit = want(*total);
         const int seq = __popc(__ballot_sync(0xffffffffu, upto <= unit));        // as many end before it
         *before = unit - __shfl_sync(0xffffffffu, upto - mine, seq & 31);
         return seq < n_seq ? seq : -1;
     }
     if (threadIdx.x == 0) sh.seq = -1;
     // units of this thread's sequence of the THREADS from i0 on, those before it (from `base` on), and all of them
-    auto scan = [&](int i0, long long *mine, long long *all) {
+    auto scan = [&](int i0, I *mine, I *all) {
         *mine = i0 + (int)threadIdx.x < n_seq ? count(i0 + threadIdx.x) : 0;
-        long long upto = *mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
+        const I upto = warp_scan(*mine, lane);
         __syncthreads();
         if (lane == 31) sh.sums[warp] = upto;
         __syncthreads();
-        long long ahead = 0;
+        I ahead = 0;
         *all = 0;
         for (int w = 0; w < THREADS / 32; w++) {
             if (w < warp) ahead += sh.sums[w];
             *all += sh.sums[w];
         }
-        return ahead + upto - *mine;
+        return (I)(ahead + upto - *mine);
     };
-    auto keep = [&](int i0, long long from, long long mine, long long unit) {
+    auto keep = [&](int i0, I from, I mine, I unit) {
         if (unit >= from && unit < from + mine) {
             sh.seq = i0 + threadIdx.x;
             sh.before = unit - from;
         }
     };
-    long long mine, all, from = scan(0, &mine, &all);
+    I mine, all, from = scan(0, &mine, &all);
     *total = all;
     if (n_seq <= THREADS) {
         keep(0, from, mine, want(all));
@@ -90,8 +89,8 @@ __device__ __forceinline__ int find_unit(UnitSearch &sh, int n_seq, long long *b
             scan(i0, &mine, &all);
             *total += all;
         }
-        long long base = 0;
-        const long long unit = want(*total);
+        I base = 0;
+        const I unit = want(*total);
         for (int i0 = 0; i0 < n_seq && base <= unit; i0 += THREADS, base += all) {
             from = base + scan(i0, &mine, &all);
             keep(i0, from, mine, unit);

@@ -43,7 +43,7 @@ struct PromptShared {
     uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], q_full[2], s_full[2], p_ready[2][2], first_done[2], o_full[2], turn[2], drain[2];
     uint32_t tmem;
     volatile int bail, spoiled;
-    UnitSearch search;
+    UnitSearch<int> search;
 };
 
 // 64 of a row's scores become weights in tensor memory, packed; returns their sum.  Single floats: pairs of them cost
@@ -100,10 +100,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         return ok;
     };
     int t0 = 0, n = 0, k0 = 0, nk = 0;
-    long long before, total;
-    const int seq = find_unit<kPrThreads>(
+    int before, total;
+    const int seq = find_unit<kPrThreads, int>(
         sh.search, a.n_seq, &before, &total,
-        [&](int i) -> long long {
+        [&](int i) -> int {
             int t0, n, k0, nk;
             if (!queries(i, &t0, &n, &k0, &nk)) {
                 set_status(status, K3MOE_DEV_BAD_OFFSETS);
@@ -111,10 +111,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
             return (n + 2 * kPrRows - 1) / (2 * kPrRows);
         },
-        [&](long long) { return (long long)(blockIdx.x % blocks); });
+        [&](int) { return (int)(blockIdx.x % blocks); });
     if (seq < 0) return;
     queries(seq, &t0, &n, &k0, &nk);
-    const int row0 = ((n + 2 * kPrRows - 1) / (2 * kPrRows) - 1 - (int)before) * 2 * kPrRows;
+    const int row0 = ((n + 2 * kPrRows - 1) / (2 * kPrRows) - 1 - before) * 2 * kPrRows;
     // keys that row r of the sequence sees, the tiles of each half, and the first tile that some row does not see whole
     auto limit = [&](int r) { return a.causal ? min(max(nk - n + 1 + r, 0), nk) : nk; };
     auto tiles_of = [&](int half) {
