@@ -782,24 +782,49 @@ class DeltaRule:
 
 # ----------------------------------------------------------------------------- the latent attention's holders
 
-def _heads(what, t, dtypes, shape, index):
-    """The strides from token to token and from head to head of t [T][heads][columns], whose heads may
-    be columns of wider ones; raises ValueError unless t fits."""
-    if not _fits(t, dtypes, shape, index):
-        raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, expected "
-                         f"{' or '.join(str(d) for d in dtypes)} {tuple(shape)} on "
-                         f"{'the host' if index < 0 else f'cuda:{index}'}")
-    (T, H, n), (ts, hs, es) = shape, t.stride()
-    if n > 1 and es != 1:
-        raise ValueError(f"{what}: strides {tuple(t.stride())} of shape {tuple(shape)}: columns are not dense")
-    hs = hs if H > 1 else n                                # of one head, of one token: whatever its stride says
-    return ts if T > 1 else (H - 1) * hs + (n + 7) // 8 * 8, hs
+# One line a tensor where it fits, in a function that returns what the entry point takes; what does not hold is said at
+# length by _require.
 
-
-def _exact_fit(what, t, dtypes, shape, index):
-    if not (t.dtype in dtypes and t.shape == shape and t.get_device() == index and t.is_contiguous()):
-        _require(what, t, dtypes, shape, index)
+def _dense(what, t, types, shape, index):
+    """The pointer of a contiguous tensor, or None for None."""
+    if t is None:
+        return None
+    if t.dtype in types and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    _require(what, t, types, shape, index)
     return t.data_ptr()
+
+
+def _rowed(what, t, types, shape, index):
+    """(pointer, row stride) of a tensor whose rows may be slices of wider ones, or (None, n) for None."""
+    if t is None:
+        return None, shape[1]
+    if t.dtype in types and t.shape == shape and t.get_device() == index:
+        if shape[0] <= 1:
+            if shape[1] <= 1 or t.stride(1) == 1:
+                return t.data_ptr(), shape[1]
+        else:
+            s0, s1 = t.stride()
+            if s1 == 1:
+                return t.data_ptr(), s0
+    return t.data_ptr(), _require(what, t, types, shape, index, True)
+
+
+def _headed(what, t, types, shape, index):
+    """(pointer, stride from token to token, from head to head) of t [T][heads][columns], whose heads may be columns of
+    wider ones, or (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    T, H, n = shape
+    if t.dtype in types and t.shape == shape and t.get_device() == index:
+        ts, hs, es = t.stride()
+        if es == 1 or n <= 1:
+            if H <= 1:
+                hs = n                                     # of one head, of one token: whatever its stride says
+            return t.data_ptr(), ts if T > 1 else (H - 1) * hs + (n + 7) // 8 * 8, hs
+        raise ValueError(f"{what}: strides {tuple(t.stride())} of shape {tuple(shape)}: columns are not dense")
+    _require(what, t, types, shape, index)                  # says what is wrong
+    return t.data_ptr(), 0, 0
 
 
 class _Holder:
@@ -810,11 +835,11 @@ class _Holder:
         self.device, self._index = _device(device)
         self._bf16, self._f32, self._i32 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,)
         self._current, self._on = _current_stream(self._index), torch.cuda.device
-        self._device_now = torch.cuda.current_device
+        self._device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         self.ws_bytes = ws_bytes
         self.ws = torch.zeros(ws_bytes, dtype=torch.uint8, device=self.device) if ws_bytes else None
 
-    def _run(self, what, fn, *args, stream=None):
+    def _run(self, what, fn, args, stream):
         """fn(*args, stream) on the holder's device, whichever is the current one."""
         if self._index >= 0 and self._device_now() != self._index:
             with self._on(self._index):
@@ -830,40 +855,29 @@ class Norm(_Holder):
     post_gain [group], scale [n] or None and pre_gain [n], f32, set by the caller."""
 
     def __init__(self, nc: K3MoENormConfig, device="cuda"):
-        import torch
         self._init(device)
         self.nc = nc
         self.post_gain = self.scale = self.pre_gain = None
-        self._xtype = self._f32 if nc.x_f32 else (torch.bfloat16, torch.int16)
-        self._stype = self._f32 if nc.sum_f32 else (torch.bfloat16, torch.int16)
+        self._xtype = self._f32 if nc.x_f32 else self._bf16
+        self._stype = self._f32 if nc.sum_f32 else self._bf16
+        self._n, self._group = (nc.n,), (nc.group,)
         self._nc, self._call = ctypes.byref(nc), lib().k3moe_norm
-
-    def _rows(self, what, t, types, shape):
-        if t is None:
-            return None, shape[1]
-        if t.dtype in types and t.shape == shape and t.get_device() == self._index:
-            if t.is_contiguous():
-                return t.data_ptr(), shape[1]
-            if t.stride(1) == 1 and shape[0] > 1:
-                return t.data_ptr(), t.stride(0)
-        return t.data_ptr(), _require(what, t, types, shape, self._index, True)
 
     def __call__(self, x, out=None, gate=None, residual=None, total=None, stream=None):
         """x [T][n] by x_f32; gate [T][n] bf16; residual and total [T][n] by sum_f32; out [T][n] bf16; rows may be
         slices of wider ones.  Returns out, or total where nothing is normed for the next block."""
-        nc, dev = self.nc, self._index
-        shape = (x.shape[0], nc.n)
-        gains = []
-        for what, g, n in (("post_gain", self.post_gain, nc.group), ("scale", self.scale, nc.n), ("pre_gain", self.pre_gain, nc.n)):
-            gains.append(None if g is None else _exact_fit(what, g, self._f32, (n,), dev))
-        xp, xs = self._rows("x", x, self._xtype, shape)
-        gp, gs = self._rows("gate", gate, self._bf16, shape)
-        rp, rs = self._rows("residual", residual, self._stype, shape)
-        tp, ts = self._rows("total", total, self._stype, shape)
-        op, os_ = self._rows("out", out, self._bf16, shape)
-        if shape[0]:
-            self._run("k3moe_norm", self._call, self._nc, shape[0], xp, xs, gp, gs, gains[0], rp, rs, gains[1], tp, ts, gains[2], op, os_,
-                      stream=stream)
+        dev, bf16, f32, stype = self._index, self._bf16, self._f32, self._stype
+        T = x.shape[0]
+        shape = (T, self._n[0])
+        post, scale = _dense("post_gain", self.post_gain, f32, self._group, dev), _dense("scale", self.scale, f32, self._n, dev)
+        pre = _dense("pre_gain", self.pre_gain, f32, self._n, dev)
+        xp, xs = _rowed("x", x, self._xtype, shape, dev)
+        gp, gs = _rowed("gate", gate, bf16, shape, dev)
+        rp, rs = _rowed("residual", residual, stype, shape, dev)
+        tp, ts = (rp, rs) if total is residual else _rowed("total", total, stype, shape, dev)
+        op, os_ = _rowed("out", out, bf16, shape, dev)
+        if T:
+            self._run("k3moe_norm", self._call, (self._nc, T, xp, xs, gp, gs, post, rp, rs, scale, tp, ts, pre, op, os_), stream)
         return total if out is None else out
 
 
@@ -874,19 +888,20 @@ class HeadLinear(_Holder):
     def __init__(self, hc: K3MoEHeadLinearConfig, T_max: int, device="cuda"):
         self._init(device, k3moe_head_linear_workspace_bytes(hc, T_max))
         self.hc, self.T_max, self.w = hc, T_max, None
+        self._shape = (hc.n_heads, hc.n, hc.k)
         self._hc, self._call = ctypes.byref(hc), lib().k3moe_head_linear
 
     def __call__(self, x, y, stream=None):
         """x [T][n_heads][k] bf16, y [T][n_heads][n] bf16 written and returned; heads may be columns of wider ones."""
-        T, hc, dev = x.shape[0], self.hc, self._index
+        T, dev, bf16 = x.shape[0], self._index, self._bf16
+        H, n, k = self._shape
         if T > self.T_max:
             raise ValueError(f"x: {T} tokens, the holder is for {self.T_max}")
-        xs, xh = _heads("x", x, self._bf16, (T, hc.n_heads, hc.k), dev)
-        ys, yh = _heads("y", y, self._bf16, (T, hc.n_heads, hc.n), dev)
-        w = _exact_fit("w", self.w, self._bf16, (hc.n_heads, hc.n, hc.k), dev)
+        xp, xs, xh = _headed("x", x, bf16, (T, H, k), dev)
+        yp, ys, yh = _headed("y", y, bf16, (T, H, n), dev)
+        w = _dense("w", self.w, bf16, self._shape, dev)
         if T:
-            self._run("k3moe_head_linear", self._call, self._hc, T, x.data_ptr(), xs, xh, w, y.data_ptr(), ys, yh, self.ws.data_ptr(),
-                      self.ws_bytes, stream=stream)
+            self._run("k3moe_head_linear", self._call, (self._hc, T, xp, xs, xh, w, yp, ys, yh, self.ws.data_ptr(), self.ws_bytes), stream)
         return y
 
 
@@ -901,78 +916,74 @@ class LatentAttention(_Holder):
         self.lc, self.n_seq_max, self.T_max = lc, n_seq_max, T_max
         self.gain = self.inv_freq = None
         self._i64, self._f64 = (torch.int64,), (torch.float64,)
-        self._row = lc.rank + lc.rope_dim
+        self._H, self._C, self._R = lc.n_heads, lc.rank, lc.rope_dim
+        self._row, self._page = lc.rank + lc.rope_dim, lc.page_size
+        self._kr, self._kv, self._v = lc.key_dim + lc.rope_dim, lc.key_dim + lc.value_dim, lc.value_dim
         self._lc, L = ctypes.byref(lc), lib()
         self._write, self._attend, self._prompt = L.k3moe_latent_write, L.k3moe_latent_attend, L.k3moe_latent_prompt
 
     def new_cache(self, n_pages):
         """A zeroed cache of n_pages pages [n_pages][page_size][rank + rope_dim] bf16."""
         import torch
-        return torch.zeros((n_pages, self.lc.page_size, self._row), dtype=torch.bfloat16, device=self.device)
+        return torch.zeros((n_pages, self._page, self._row), dtype=torch.bfloat16, device=self.device)
 
     def _room(self, n_seq, T):
         if n_seq > self.n_seq_max or T > self.T_max:
             raise ValueError(f"{n_seq} sequences of {T} tokens, the holder is for {self.n_seq_max} and {self.T_max}")
 
-    def _pool(self, cache):
-        shape = (cache.shape[0], self.lc.page_size, self._row)
-        return _exact_fit("cache", cache, self._bf16, shape, self._index), shape[0]
-
-    def _lse(self, lse, T):
-        return None if lse is None else _exact_fit("lse", lse, self._f32, (T, self.lc.n_heads), self._index)
-
     def write(self, c, positions=None, cache=None, slots=None, rows=None, q=None, q_rope=None, stream=None):
         """c [T][rank + rope_dim] bf16, positions [T] int32; the rows go to slots [T] int64 of the cache and to rows
-        [T][rank + rope_dim]; q [T][n_heads][rope_dim], the queries' rotated columns, to q_rope, which may be q."""
-        lc, dev, T = self.lc, self._index, c.shape[0]
+        [T][rank + rope_dim]; q [T][n_heads][rope_dim], the queries' rotated columns, to q_rope, which may be q.  Returns
+        rows, or the cache where they go there alone."""
+        dev, bf16, T, row = self._index, self._bf16, c.shape[0], self._row
         if T > self.T_max:
             raise ValueError(f"c: {T} tokens, the holder is for {self.T_max}")
-        cs = _require("c", c, self._bf16, (T, self._row), dev, True)
-        gain = None if self.gain is None else _exact_fit("gain", self.gain, self._f32, (lc.rank,), dev)
-        freq = None if self.inv_freq is None else _exact_fit("inv_freq", self.inv_freq, self._f64, (lc.rope_dim // 2,), dev)
-        at = None if positions is None else _exact_fit("positions", positions, self._i32, (T,), dev)
-        rs = self._row if rows is None else _require("rows", rows, self._bf16, (T, self._row), dev, True)
-        pool, n_pages = (None, 0) if cache is None else self._pool(cache)
-        sl = None if slots is None else _exact_fit("slots", slots, self._i64, (T,), dev)
-        shape = (T, lc.n_heads, lc.rope_dim)
-        (qs, qh), (os_, oh) = ((0, 0) if t is None else _heads(w, t, self._bf16, shape, dev) for w, t in (("q", q), ("q_rope", q_rope)))
+        cp, cs = _rowed("c", c, bf16, (T, row), dev)
+        gain = _dense("gain", self.gain, self._f32, (self._C,), dev)
+        freq = _dense("inv_freq", self.inv_freq, self._f64, (self._R // 2,), dev)
+        at = _dense("positions", positions, self._i32, (T,), dev)
+        rp, rs = (cp, cs) if rows is c else _rowed("rows", rows, bf16, (T, row), dev)
+        n_pages = 0 if cache is None else cache.shape[0]
+        pool = _dense("cache", cache, bf16, (n_pages, self._page, row), dev)
+        sl = _dense("slots", slots, self._i64, (T,), dev)
+        shape = (T, self._H, self._R)
+        qp, qs, qh = _headed("q", q, bf16, shape, dev)
+        op, os_, oh = (qp, qs, qh) if q_rope is q else _headed("q_rope", q_rope, bf16, shape, dev)
         if T:
-            self._run("k3moe_latent_write", self._write, self._lc, T, c.data_ptr(), cs, gain, at, freq,
-                      None if rows is None else rows.data_ptr(), rs, pool, n_pages, sl, None if q is None else q.data_ptr(), qs, qh,
-                      None if q_rope is None else q_rope.data_ptr(), os_, oh, self.ws.data_ptr(), self.ws_bytes, stream=stream)
+            self._run("k3moe_latent_write", self._write, (self._lc, T, cp, cs, gain, at, freq, rp, rs, pool, n_pages, sl, qp, qs, qh, op, os_, oh,
+                                                          self.ws.data_ptr(), self.ws_bytes), stream)
         return cache if rows is None else rows
 
     def attend(self, q, cache, pages, kv_len, out, seq_start=None, lse=None, stream=None):
         """q [T][n_heads][rank + rope_dim] bf16, pages [n_seq][max_pages] int32, kv_len [n_seq] int32; out
         [T][n_heads][rank] bf16 written and returned, lse [T][n_heads] f32 or None; seq_start [n_seq+1] int32, or None for
         one token each (with one sequence: all)."""
-        lc, dev, T, n_seq = self.lc, self._index, q.shape[0], kv_len.shape[0]
+        dev, bf16, i32, T, n_seq, H = self._index, self._bf16, self._i32, q.shape[0], kv_len.shape[0], self._H
         self._room(n_seq, T)
-        qs, qh = _heads("q", q, self._bf16, (T, lc.n_heads, self._row), dev)
-        pool, n_pages = self._pool(cache)
-        table = _exact_fit("pages", pages, self._i32, (n_seq, pages.shape[-1]), dev)
-        lens = _exact_fit("kv_len", kv_len, self._i32, (n_seq,), dev)
-        o = _exact_fit("out", out, self._bf16, (T, lc.n_heads, lc.rank), dev)
-        start = None if seq_start is None else _exact_fit("seq_start", seq_start, self._i32, (n_seq + 1,), dev)
+        qp, qs, qh = _headed("q", q, bf16, (T, H, self._row), dev)
+        n_pages, max_pages = cache.shape[0], pages.shape[-1]
+        pool = _dense("cache", cache, bf16, (n_pages, self._page, self._row), dev)
+        table, lens = _dense("pages", pages, i32, (n_seq, max_pages), dev), _dense("kv_len", kv_len, i32, (n_seq,), dev)
+        o, start = _dense("out", out, bf16, (T, H, self._C), dev), _dense("seq_start", seq_start, i32, (n_seq + 1,), dev)
+        ls = _dense("lse", lse, self._f32, (T, H), dev)
         if T:
-            self._run("k3moe_latent_attend", self._attend, self._lc, n_seq, T, start, q.data_ptr(), qs, qh, pool, n_pages, table,
-                      pages.shape[-1], lens, o, self._lse(lse, T), self.ws.data_ptr(), self.ws_bytes, stream=stream)
+            self._run("k3moe_latent_attend", self._attend, (self._lc, n_seq, T, start, qp, qs, qh, pool, n_pages, table, max_pages, lens, o, ls,
+                                                            self.ws.data_ptr(), self.ws_bytes), stream)
         return out
 
     def prompt(self, q, kv, rope_key, out, seq_start=None, kv_start=None, lse=None, stream=None):
         """q [T][n_heads][key_dim + rope_dim], kv [S][n_heads][key_dim + value_dim], rope_key [S][rope_dim] bf16, the last's
         rows at any stride; out [T][n_heads][value_dim] bf16 written and returned, lse [T][n_heads] f32 or None; seq_start and
         kv_start [n_seq+1] int32, or None: one sequence, or the queries' own."""
-        lc, dev, T, S = self.lc, self._index, q.shape[0], kv.shape[0]
+        dev, bf16, i32, T, S, H = self._index, self._bf16, self._i32, q.shape[0], kv.shape[0], self._H
         n_seq = 1 if seq_start is None else seq_start.shape[0] - 1
         self._room(n_seq, T)
-        qs, qh = _heads("q", q, self._bf16, (T, lc.n_heads, lc.key_dim + lc.rope_dim), dev)
-        ks, kh = _heads("kv", kv, self._bf16, (S, lc.n_heads, lc.key_dim + lc.value_dim), dev)
-        rs = _require("rope_key", rope_key, self._bf16, (S, lc.rope_dim), dev, True)
-        o = _exact_fit("out", out, self._bf16, (T, lc.n_heads, lc.value_dim), dev)
-        start, keys = (None if t is None else _exact_fit(w, t, self._i32, (n_seq + 1,), dev)
-                       for w, t in (("seq_start", seq_start), ("kv_start", kv_start)))
+        qp, qs, qh = _headed("q", q, bf16, (T, H, self._kr), dev)
+        kp, ks, kh = _headed("kv", kv, bf16, (S, H, self._kv), dev)
+        rp, rs = _rowed("rope_key", rope_key, bf16, (S, self._R), dev)
+        o, ls = _dense("out", out, bf16, (T, H, self._v), dev), _dense("lse", lse, self._f32, (T, H), dev)
+        start, keys = _dense("seq_start", seq_start, i32, (n_seq + 1,), dev), _dense("kv_start", kv_start, i32, (n_seq + 1,), dev)
         if T:
-            self._run("k3moe_latent_prompt", self._prompt, self._lc, n_seq, T, S, start, keys, q.data_ptr(), qs, qh, kv.data_ptr(), ks, kh,
-                      rope_key.data_ptr(), rs, o, self._lse(lse, T), self.ws.data_ptr(), self.ws_bytes, stream=stream)
+            self._run("k3moe_latent_prompt", self._prompt, (self._lc, n_seq, T, S, start, keys, qp, qs, qh, kp, ks, kh, rp, rs, o, ls,
+                                                            self.ws.data_ptr(), self.ws_bytes), stream)
         return out

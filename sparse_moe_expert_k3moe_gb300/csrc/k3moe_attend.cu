@@ -35,7 +35,7 @@ constexpr uint32_t kAtTmS = 0, kAtTmO = 128;                  // S^T of two tile
 constexpr float kAtSlack = 8.0f;
 
 // A part's sums in the workspace: O [query][c], then the maxima and the sums of the weights.
-constexpr size_t kAtPart = (size_t)kAtRows * kLatC + 2 * kAtRows;
+constexpr size_t kAtPart = kLatPart;
 // What a cut leaves to join: the query block's first part is share i's last (its first or second), the others
 // are the first ones of the shares after it, whose `owner` i is.
 struct AttendJoin {
@@ -189,6 +189,8 @@ template <typename I> __device__ __forceinline__ void attend_plan(const AttendAr
     sh.first.shares = shares;
     sh.first.have = 1;
 }
+
+static_assert(sizeof(AttendJoin) <= 32 && kAtRows == 64, "as the workspace is laid out");
 
 // S^T's 16 lanes of a warp, 32 columns: v[4 k + 2 i + j] is row lane / 4 + 8 i, column 8 k + 2 (lane % 4) + j.
 __device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[16])
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 // out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over the parts i, M the largest m.  Blocks (x, y) for share x: of a query
 // block with few parts, the share's that begins it have four queries each, a warp a query, a lane 16 columns; with many, all its
 // shares' have a quarter of a query's columns each, their warps every fourth part.
-constexpr int kJoinThreads = 128, kJoinBlocks = kAtRows / 4, kMaxShares = 512, kJoinMany = 8;
+constexpr int kJoinThreads = 128, kJoinBlocks = kAtRows / 4, kJoinMany = 8;
 
 struct JoinParts {
     const float *p0, *p1;                                     // the first part, and the second
@@ -653,7 +655,6 @@ struct JoinParts {
 };
 __device__ __forceinline__ void join_add(float4 &o, float f, const float4 &x)
 {
-    if (f == 0.0f) return;
     o.x = fmaf(f, x.x, o.x);
     o.y = fmaf(f, x.y, o.y);
     o.z = fmaf(f, x.z, o.z);
@@ -785,7 +786,7 @@ size_t latent_workspace(const k3moe_latent_config &lc, int n_seq, int T)
 {
     (void)lc;
     const size_t base = kCtrOffset + kCtrBytes;
-    return n_seq > 0 && T > 0 ? base + align256((size_t)attend_shares() * sizeof(AttendJoin)) + (size_t)attend_shares() * 2 * kAtPart * 4 : base;
+    return n_seq > 0 && T > 0 ? base + kLatJoinBytes + (size_t)attend_shares() * 2 * kAtPart * 4 : base;
 }
 
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
@@ -805,7 +806,7 @@ cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
     const long long most = ((long long)a.T * a.H / kAtRows + std::min(a.n_seq, a.T)) * ((long long)a.max_pages * a.page / kAtTile + 1);
     const int shares = attend_shares();
     AttendJoin *joins = reinterpret_cast<AttendJoin *>(a.ws + kCtrOffset + kCtrBytes);
-    float *parts = reinterpret_cast<float *>(a.ws + kCtrOffset + kCtrBytes + align256((size_t)shares * sizeof(AttendJoin)));
+    float *parts = latent_parts(a.ws);
     timing_begin("latent_attend", s);
     cudaError_t err = launch_pdl(most < INT32_MAX ? attend_kernel<int> : attend_kernel<long long>, dim3((unsigned)shares), dim3(kAtThreads), kAtSmem, s, a,
                                  m4, m1, parts, joins);

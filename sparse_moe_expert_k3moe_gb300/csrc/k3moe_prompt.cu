@@ -37,6 +37,15 @@ static_assert(2 * kPrRegsRows + kPrRegsLast <= 3 * kPrRegs, "shares within the l
 constexpr uint32_t kPrTmS = 0, kPrTmO = 2 * kPrTile;
 constexpr float kPrLimit = 1073741824.0f;                     // 2^30: a sum of 64 weights that calls for a new m
 
+// Few queries against many keys: `splits` blocks have an even part of the key tiles each, leave their sums in the
+// workspace, O [16 columns][row] in float and then m and l of the rows, and a second kernel joins them.
+constexpr int kPrBlock = 2 * kPrRows, kPrGroups = kLatV / 16, kPrMaxSplits = 16;
+constexpr size_t kPrPart = (size_t)kPrBlock * kLatV + 2 * kPrBlock;
+static_assert(kPrPart <= 2 * kLatPart, "a part a block, in the room of two of the absorbed form's");
+struct PromptPlace {
+    int token, rows;                                          // a block's first query, and how many
+};
+
 struct PromptShared {
     // by the tile's turn: keys and values there, and free again; by the half: its queries, scores, weights (of the first and
     // the last 64 keys of a tile), its product with the first 64 values and its output
@@ -69,9 +78,10 @@ __device__ __forceinline__ float weigh(const uint32_t *v, uint32_t taddr, float 
     return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
+template <bool kParts>
 __global__ void __launch_bounds__(kPrThreads, 1)
     prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
-                  const __grid_constant__ CUtensorMap mr, const int blocks)
+                  const __grid_constant__ CUtensorMap mr, const int blocks, float *parts, PromptPlace *places)
 {
     extern __shared__ __align__(1024) uint8_t psm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(psm_raw) + 1023) & ~(uintptr_t)1023);
@@ -112,11 +122,25 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             return (n + 2 * kPrRows - 1) / (2 * kPrRows);
         },
         [&](int) { return (int)(blockIdx.x % blocks); });
-    if (seq < 0) return;
+    const int splits = kParts ? gridDim.y : 1;
+    if (seq < 0) {
+        if (kParts && blockIdx.y == 0 && threadIdx.x == 0) places[blockIdx.x].rows = 0;
+        return;
+    }
     queries(seq, &t0, &n, &k0, &nk);
     const int row0 = ((n + 2 * kPrRows - 1) / (2 * kPrRows) - 1 - before) * 2 * kPrRows;
-    // keys that row r of the sequence sees, the tiles of each half, and the first tile that some row does not see whole
-    auto limit = [&](int r) { return a.causal ? min(max(nk - n + 1 + r, 0), nk) : nk; };
+    // keys that row r of the sequence sees: nk + ahead + r of them, within the nk of this block's part
+    int ahead = a.causal ? 1 - n : n;
+    if (kParts) {
+        if (blockIdx.y == 0 && threadIdx.x == 0) places[blockIdx.x] = PromptPlace{t0 + row0, min(n - row0, kPrBlock)};
+        const int most = min(nk, max(0, nk + ahead + min(n, row0 + kPrBlock) - 1)), tiles = (most + kPrTile - 1) / kPrTile;
+        const int first = tiles * (int)blockIdx.y / splits * kPrTile, end = min(nk, tiles * (int)(blockIdx.y + 1) / splits * kPrTile);
+        k0 += first;
+        ahead += nk - end;                                    // as many keys are left out at the part's end ..
+        nk = max(0, end - first);                             // .. and the others before it
+    }
+    // the tiles of each half, and the first tile that some row does not see whole
+    auto limit = [&](int r) { return min(max(nk + ahead + r, 0), nk); };
     auto tiles_of = [&](int half) {
         const int first = row0 + kPrRows * half;
         return first < n ? (limit(min(n, first + kPrRows) - 1) + kPrTile - 1) / kPrTile : 0;
@@ -248,6 +272,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const size_t row = (size_t)(t0 + r) * a.H + h;
             const bool spoiled = sh.spoiled != 0;
+            float *part = kParts ? parts + ((size_t)blockIdx.x * splits + blockIdx.y) * kPrPart + (r - row0) * 16 : nullptr;
 #pragma unroll 1
             for (int b = 0; b < kLatV; b += 16) {
                 float o[16];
@@ -263,19 +288,30 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                             if ((u & 0x7F80u) == 0x7F80u) o[j] += bf16_bits_to_f32(u);
                         }
                     }
-                uint32_t w[8];
+                if (kParts && r < n) {
+                    float4 *p = reinterpret_cast<float4 *>(part + (size_t)b * kPrBlock);
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const __nv_bfloat162 x = l == 0.0f ? __floats2bfloat162_rn(0.0f, 0.0f) : __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
-                    w[j] = *reinterpret_cast<const uint32_t *>(&x);
-                }
-                if (r < n) {
+                    for (int j = 0; j < 4; j++) p[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                } else if (r < n) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const __nv_bfloat162 x = l == 0.0f ? __floats2bfloat162_rn(0.0f, 0.0f) : __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
+                        w[j] = *reinterpret_cast<const uint32_t *>(&x);
+                    }
                     uint4 *p = reinterpret_cast<uint4 *>(a.out + row * kLatV + b);
                     p[0] = make_uint4(w[0], w[1], w[2], w[3]);
                     p[1] = make_uint4(w[4], w[5], w[6], w[7]);
                 }
+                __syncwarp();
             }
-            if (a.lse && r < n) a.lse[row] = (m + log2f(l)) * kLatLn2;
+            if (kParts && r < n) {
+                part += (size_t)kPrBlock * kLatV - (r - row0) * 15;
+                part[0] = m;
+                part[kPrBlock] = l;
+            } else if (a.lse && r < n) {
+                a.lse[row] = (m + log2f(l)) * kLatLn2;
+            }
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsLast));
@@ -383,6 +419,52 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     if (warp == kPrWarpMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(512));
 }
 
+// The join of a block's parts: a thread 16 columns of a row.
+__global__ void __launch_bounds__(kPrBlock) prompt_join_kernel(const PromptArgs a, const int blocks, const int splits, const float *parts, const PromptPlace *places)
+{
+    pdl_wait();
+    pdl_trigger();
+    const PromptPlace place = places[blockIdx.x];
+    const int r = threadIdx.x, group = blockIdx.y;
+    if (r >= place.rows) return;
+    const float *from = parts + (size_t)blockIdx.x * splits * kPrPart, *ml = from + (size_t)kPrBlock * kLatV + r;
+    float m[kPrMaxSplits], l[kPrMaxSplits], M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int p = 0; p < kPrMaxSplits; p++) {
+        m[p] = p < splits ? ml[p * kPrPart] : -INFINITY;
+        l[p] = p < splits ? ml[p * kPrPart + kPrBlock] : 0.0f;
+        M = fmaxf(M, m[p]);
+    }
+    float o[16] = {};
+#pragma unroll
+    for (int p = 0; p < kPrMaxSplits; p++) {
+        if (p >= splits) break;
+        const float f = m[p] == -INFINITY ? 0.0f : exp2_fast(m[p] - M);
+        L = fmaf(f, l[p], L);
+        const float4 *x = reinterpret_cast<const float4 *>(from + p * kPrPart + ((size_t)group * kPrBlock + r) * 16);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float4 v = x[j];
+            o[4 * j] = fmaf(f, v.x, o[4 * j]);
+            o[4 * j + 1] = fmaf(f, v.y, o[4 * j + 1]);
+            o[4 * j + 2] = fmaf(f, v.z, o[4 * j + 2]);
+            o[4 * j + 3] = fmaf(f, v.w, o[4 * j + 3]);
+        }
+    }
+    const size_t row = (size_t)(place.token + r) * a.H + blockIdx.x / blocks;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const __nv_bfloat162 x = L == 0.0f ? __floats2bfloat162_rn(0.0f, 0.0f) : __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
+        w[j] = *reinterpret_cast<const uint32_t *>(&x);
+    }
+    uint4 *to = reinterpret_cast<uint4 *>(a.out + row * kLatV + 16 * group);
+    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (a.lse && group == 0) a.lse[row] = (M + log2f(L)) * kLatLn2;
+}
+
 }  // namespace
 
 cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t s)
@@ -398,16 +480,32 @@ cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t s)
     const cudaError_t allowed = once_a_device([] {
         // the shares of setmaxnreg are of the launch's registers: with another count they would never be there
         cudaFuncAttributes fa{};
-        if (cudaFuncGetAttributes(&fa, prompt_kernel) != cudaSuccess || fa.numRegs != kPrRegs) return cudaErrorInvalidConfiguration;
-        return cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrSmem);
+        for (const void *kernel : {(const void *)prompt_kernel<false>, (const void *)prompt_kernel<true>}) {
+            if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != kPrRegs) return cudaErrorInvalidConfiguration;
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrSmem);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
     });
     if (allowed != cudaSuccess) return allowed;
     const int blocks = a.seq_start ? a.T / (2 * kPrRows) + std::min(a.n_seq, a.T)
                                    : a.n_seq == 1 ? (a.T + 2 * kPrRows - 1) / (2 * kPrRows) : a.n_seq;
+    // parts of the keys while the blocks leave SMs without one, of four tiles at least by the sequences' average; their sums
+    // are where the absorbed form has its own
+    const int items = blocks * a.H;
+    int splits = std::min(std::min(num_sms(), kMaxShares) / items, a.S / std::min(a.n_seq, a.T) / (4 * kPrTile));
+    splits = std::max(1, std::min(splits, kPrMaxSplits));
+    float *parts = latent_parts(a.ws);
+    PromptPlace *places = reinterpret_cast<PromptPlace *>(a.ws + kCtrOffset + kCtrBytes);
     timing_begin("latent_prompt", s);
-    const cudaError_t err = launch_pdl(prompt_kernel, dim3((unsigned)(blocks * a.H)), dim3(kPrThreads), kPrSmem, s, a, mq, mkv, mr, blocks);
+    cudaError_t err = launch_pdl(splits > 1 ? prompt_kernel<true> : prompt_kernel<false>, dim3((unsigned)items, (unsigned)splits), dim3(kPrThreads), kPrSmem, s, a, mq, mkv, mr, blocks, parts, places);
     count_launch();
     timing_end("latent_prompt", s);
+    if (err != cudaSuccess || splits == 1) return err;
+    timing_begin("latent_prompt_join", s);
+    err = launch_pdl(prompt_join_kernel, dim3((unsigned)items, kPrGroups), dim3(kPrBlock), 0, s, a, blocks, splits, (const float *)parts, (const PromptPlace *)places);
+    count_launch();
+    timing_end("latent_prompt_join", s);
     return err;
 }
 

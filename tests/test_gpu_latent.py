@@ -480,7 +480,10 @@ PROMPT = [  # queries, keys (None: the queries' own), heads, causal, padded stri
     ([513, 1030], None, 1, 1, False),
     ([1] * 9, [1, 2, 64, 127, 128, 129, 511, 512, 513], 8, 1, False),
     ([3000], None, 1, 1, False),
-    ([17], [5000], 2, 1, False),
+    ([17], [5000], 2, 1, False),                                # few queries, many keys: parts of the keys
+    ([200, 3], [6000, 0], 3, 1, True),
+    ([1, 130], [4097, 4000], 1, 0, False),
+    ([260], [2600], 5, 1, False),
 ]
 
 
@@ -583,6 +586,21 @@ def test_prompt_leaves_other_rows(k3):
     c(op, seq_start=c.start[1:4].contiguous())
     assert (c.out[:50] == 7.5).all() and (c.out[350:] == 7.5).all() and (c.lse[:50] == 7.5).all() and (c.lse[350:] == 7.5).all()
     c.check(cfg, skip=[0, 3])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("at", [100, 2000, 2850, 2997])
+def test_prompt_parts_what_is_not_seen_does_not_matter(k3, value, at):
+    """As below, with the keys in parts: a value reaches the queries that see it whichever part it is in."""
+    c = Expanded([150], [3000], 2, False, 13)
+    op, cfg = c.holder(k3)
+    c(op)
+    out, lse = c.out.clone(), c.lse.clone()
+    c.kv[at, :, K] = value
+    c(op)
+    first = max(0, at - 2850)                              # the first query that sees it
+    assert torch.equal(c.out[:first], out[:first]) and torch.equal(c.lse, lse) and torch.equal(c.out[first:, :, 1:], out[first:, :, 1:])
+    assert not torch.isfinite(c.out[first:, :, 0]).any()
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
