@@ -148,6 +148,49 @@ def test_norm_edges(k3):
     assert torch.equal(gated(x, gate=-gate, total=total), (x.float() * 200).bfloat16())
 
 
+def test_norm_in_place(k3):
+    """total and out over x, the gate and the residual, where type and stride are the same."""
+    T, N = 37, 2064
+    r = randn(5)
+    op = k3.Norm(k3.k3moe_norm_config(N, gate="silu"))
+    op.post_gain, op.scale, op.pre_gain = r(N), r(N), r(N)
+    x, gate, res = (r(T, N).bfloat16() for _ in range(3))
+    total, out = torch.empty_like(x), torch.empty_like(x)
+    op(x, out=out, gate=gate, residual=res, total=total)
+    for names in (("x", "gate"), ("gate", "x"), ("residual", "x"), ("x", "residual")):
+        given = dict(x=x.clone(), gate=gate.clone(), residual=res.clone())
+        op(**given, total=given[names[0]], out=given[names[1]])
+        assert torch.equal(given[names[0]], total) and torch.equal(given[names[1]], out), names
+
+
+@pytest.mark.parametrize("T", [1, 3])
+def test_forward_reads_what_a_norm_wrote(k3, T):
+    """The experts' mat-vec path reads its tokens ahead of its wait for the routing; not those a norm may still be
+    writing.  The buffer is poisoned before the norm that writes it."""
+    d, E, f = 1024, 64, 256
+    g = torch.Generator("cuda").manual_seed(T)
+    m = k3.MoELayer(k3.k3moe_config(d=d, f=f, n_experts=E, top_k=4, n_shared=1), T)
+    codes = lambda *s: torch.randint(0, 256, s, generator=g, dtype=torch.uint8, device="cuda")  # noqa: E731
+    scale = lambda *s: torch.full(s, 121, dtype=torch.uint8, device="cuda")  # noqa: E731
+    w = lambda *s: (torch.randn(*s, generator=g, device="cuda") / s[-1] ** 0.5).bfloat16()  # noqa: E731
+    m.pack_experts(0, E, codes(E, f, d // 2), scale(E, f, d // 32), codes(E, f, d // 2), scale(E, f, d // 32), codes(E, d, f // 2), scale(E, d, f // 32))
+    m.w_router, m.sh_w1, m.sh_w3, m.sh_w2 = w(E, d), w(1, f, d), w(1, f, d), w(1, d, f)
+    op = k3.Norm(k3.k3moe_norm_config(d, post_norm=0))
+    op.pre_gain = torch.ones(d, device="cuda")
+    h, x, out = torch.randn(T, d, device="cuda").bfloat16(), torch.empty(T, d, dtype=torch.bfloat16, device="cuda"), torch.empty(T, d, device="cuda")
+    op(h, out=x)
+    m.route(x)
+    torch.cuda.synchronize()
+    m.forward(x, out)
+    torch.cuda.synchronize()
+    want = out.clone()
+    for _ in range(50):
+        x.fill_(float("nan"))
+        op(h, out=x)
+        m.forward(x, out)
+        assert torch.equal(out, want)
+
+
 # ----------------------------------------------------------------------------- a head's own projection
 
 @pytest.mark.parametrize("T,H,K_,N,pad", [(1, 56, 128, 512, 0), (1, 1, 8, 1, 0), (2, 3, 64, 129, 8), (16, 5, 200, 128, 0), (17, 2, 512, 130, 64),
