@@ -45,15 +45,21 @@ struct AttendJoin {
 // Sequence i: its queries, cached rows, blocks of 1 << shift queries and tiles of each; false when something does not fit.
 struct AttendSeq {
     int t0, n, len, blocks, tiles;
-    __device__ bool read(const AttendArgs &a, int i, int shift)
+    __device__ bool set(const AttendArgs &a, int from, int to, int kv, int shift)
     {
-        bool ok = latent_queries(a.seq_start, a.n_seq, a.T, i, &t0, &n);
-        len = a.kv_len[i];
-        ok = ok && len >= 0 && len <= a.max_pages * a.page;
+        t0 = from;
+        n = to - from;
+        len = kv;
+        const bool ok = from >= 0 && to >= from && to <= a.T && len >= 0 && len <= a.max_pages << a.page_shift;
         blocks = ok ? (n * a.H + (1 << shift) - 1) >> shift : 0;
         tiles = max(1, (len + kAtTile - 1) / kAtTile);        // one that has nothing where no row is cached
         return ok;
     }
+    __device__ static int start(const AttendArgs &a, int i)
+    {
+        return a.seq_start ? a.seq_start[i] : a.n_seq == 1 ? i * a.T : i;
+    }
+    __device__ bool read(const AttendArgs &a, int i, int shift) { return set(a, start(a, i), start(a, i + 1), a.kv_len[i], shift); }
 };
 
 // The walk of a block's share of tiles, query block by query block.
@@ -130,35 +136,46 @@ template <typename I> __device__ __forceinline__ void attend_plan(const AttendAr
     bool mine = false;                                        // this thread has found the share's first tile
     I before = 0;
     if (a.n_seq <= kAtPlanSeqs) {
-        int rows[4], tiles[4];
+        int from[5], kv[4];                                   // all asked for before any is looked at
+#pragma unroll
+        for (int k = 0; k < 5; k++) {
+            const int i = 4 * lane + k;
+            from[k] = i <= a.n_seq ? AttendSeq::start(a, i) : 0;
+            if (k < 4) kv[k] = i < a.n_seq ? a.kv_len[i] : 0;
+        }
+        AttendSeq s[4];
+        bool bad = false;
         I all = 0;
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            AttendSeq s;
-            s.blocks = s.n = s.tiles = 0;
-            if (4 * lane + k < a.n_seq && !s.read(a, 4 * lane + k, 6)) set_status(status, K3MOE_DEV_BAD_OFFSETS);
-            rows[k] = s.blocks > 0 ? s.n * a.H : 0;
-            tiles[k] = s.tiles;
-            all += (I)s.blocks * s.tiles;
+            s[k].blocks = 0;
+            if (4 * lane + k < a.n_seq) bad = !s[k].set(a, from[k], from[k + 1], kv[k], 6) || bad;
+            all += s[k].blocks ? (I)s[k].blocks * s[k].tiles : 0;
         }
+        if (bad) set_status(status, K3MOE_DEV_BAD_OFFSETS);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
         const int n = gridDim.x;
         if (all <= n / 2) w.shift = all <= n / 4 ? 4 : 5;
         I units[4], each = 0;
 #pragma unroll
-        for (int k = 0; k < 4; k++) each += units[k] = (I)((rows[k] + (1 << w.shift) - 1) >> w.shift) * tiles[k];
+        for (int k = 0; k < 4; k++) {
+            if (s[k].blocks) s[k].blocks = (s[k].n * a.H + (1 << w.shift) - 1) >> w.shift;
+            each += units[k] = s[k].blocks ? (I)s[k].blocks * s[k].tiles : 0;
+        }
         const I upto = warp_scan(each, lane);
         shares.cut(__shfl_sync(0xffffffffu, upto, 31), gridDim.x);
         w.u = shares.begin(blockIdx.x);
         before = w.u - (upto - each);
         mine = before >= 0 && before < each;
         w.seq = 4 * lane;
+        w.s = s[0];
 #pragma unroll
         for (int k = 0; k < 3; k++)
             if (mine && w.seq == 4 * lane + k && before >= units[k]) {
                 before -= units[k];
                 w.seq++;
+                w.s = s[k + 1];
             }
     } else {
         I all;
@@ -183,7 +200,7 @@ template <typename I> __device__ __forceinline__ void attend_plan(const AttendAr
     }
     if (!mine) return;
     w.base = w.u - before;
-    w.s.read(a, w.seq, w.shift);
+    if (a.n_seq > kAtPlanSeqs) w.s.read(a, w.seq, w.shift);
     w.next(a);
     sh.first.walk = w;
     sh.first.shares = shares;
@@ -276,14 +293,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         return;
     }
     constexpr uint32_t tmem = 0;                              // all 512 columns: the allocation starts at the first
-    auto wait = [&](uint64_t &b, int phase) {
-        const bool ok = mb_wait_warp(&b, (uint32_t)phase & 1u);
-        if (!ok) {
-            set_status(status, K3MOE_DEV_TIMEOUT);
-            sh.bail = 1;
-        }
-        return ok;
-    };
+    auto wait = [&](uint64_t &b, int phase) { return role_wait(&b, phase, status, &sh.bail); };
     // the same for the warps that meet at barriers: after a wait that gave up they go on without waiting, to the end
     auto go_on = [&](uint64_t &b, int phase) { return !sh.bail && wait(b, phase); };
 
@@ -477,9 +487,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 if (spoiled)
 #pragma unroll 1
                     for (int at = max(least, kAtTile * now.tile0); at < min(now.s.len, kAtTile * now.tile1); at++) {
-                        const int page = a.pages[(size_t)now.seq * a.max_pages + at / a.page];
+                        const int page = a.pages[(size_t)now.seq * a.max_pages + (at >> a.page_shift)];
                         if (page < 0 || page >= a.n_pages) continue;
-                        const uint16_t *from = a.cache + ((size_t)page * a.page + at % a.page) * kLatRow + 32 * q + lane;
+                        const uint16_t *from = a.cache + ((size_t)page * a.page + (at & (a.page - 1))) * kLatRow + 32 * q + lane;
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
                             const uint32_t x = from[128 * k];
@@ -535,11 +545,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 tc_fence_after();
                 product(c0 + (16 + turn) * box, q0 + 8 * q_box, true);
                 umma_commit_warp(&sh.r_empty[turn]);
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < 4; b++) product(c0 + (8 * turn + b) * box, q0 + b * q_box, false);
                 if (!(ok = wait(sh.full[turn][1], tile >> 1))) break;
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int b = 4; b < 8; b++) product(c0 + (8 * turn + b) * box, q0 + b * q_box, false);
                 umma_commit_warp(&sh.s_full[turn]);
             }
@@ -562,7 +572,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 if (!(ok = wait(sh.p_ready[turn], tile >> 1))) break;
                 tc_fence_after();
                 const uint32_t A = c0 + 8 * turn * box;
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < 4; b++) {
 #pragma unroll
                     for (int k = 0; k < kAtTile / 16; k++)
@@ -577,7 +587,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         mb_wait_warp(&sh.drain[1], 0);
     } else {
         // ---------------- the cache's rows: half of c, of a page's rows each box, a lane a page; the first half's warp loads r
-        const int box_rows = min(a.page, kAtTile), pieces = kAtTile / box_rows, half = uniform(warp - kAtWarpLoad);
+        const int box_rows = min(a.page, kAtTile), pieces = kAtTile >> min(a.page_shift, 6), half = uniform(warp - kAtWarpLoad);
         int tile = 0;
         bool ok = true;
         AttendJoin join{0, 0, 0, 0, 0, -1};
@@ -591,12 +601,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 const int at = kAtTile * (tile0 + t) + lane * box_rows, turn = uniform(tile & 1), phase = tile >> 1;
                 int row = -1;                                 // nothing to load
                 if (lane < pieces && at < len) {
-                    const int page = pages[at / a.page];
+                    const int page = pages[at >> a.page_shift];
                     if (page < 0 || page >= a.n_pages) {
                         set_status(status, K3MOE_DEV_BAD_INDEX);
                         row = a.n_pages * a.page;             // past the cache: zeros
                     } else {
-                        row = page * a.page + at % a.page;
+                        row = page * a.page + (at & (a.page - 1));
                     }
                 }
                 const int n = uniform(__popc(__ballot_sync(0xffffffffu, row >= 0)));

@@ -33,6 +33,28 @@ __device__ __forceinline__ bool latent_queries(const int32_t *start, int n_seq, 
     return s0 >= 0 && s1 >= s0 && s1 <= T;
 }
 
+// A warp's wait on a barrier's phase.  What follows when it is not complete at the first try, which itself waits a while, is a
+// call: the roles of a block share the instruction cache, and every wait written out in full was a fifth of their code.
+__device__ __noinline__ bool role_wait_long(uint64_t *b, uint32_t parity, int32_t *status, volatile int *bail)
+{
+    const bool ok = mb_wait_warp(b, parity);
+    if (!ok) {
+        set_status(status, K3MOE_DEV_TIMEOUT);
+        *bail = 1;
+    }
+    return ok;
+}
+__device__ __forceinline__ bool role_wait(uint64_t *b, int phase, int32_t *status, volatile int *bail)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(saddr(b)), "r"((uint32_t)phase & 1u)
+        : "memory");
+    return __all_sync(0xffffffffu, done != 0) || role_wait_long(b, (uint32_t)phase & 1u, status, bail);
+}
+
 // a / b of positive numbers, in 32 bits where they fit: the long division is a hundred instructions.
 __device__ __forceinline__ long long quotient(long long a, int b) { return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b); }
 __device__ __forceinline__ int quotient(int a, int b) { return (int)((uint32_t)a / (uint32_t)b); }
