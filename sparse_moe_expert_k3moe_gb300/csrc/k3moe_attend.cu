@@ -812,8 +812,8 @@ cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
         return e != cudaSuccess ? e : cudaFuncSetAttribute(attend_kernel<long long>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem);
     });
     if (allowed != cudaSuccess) return allowed;
-    // whether every count of tiles fits 32 bits, whatever the lengths are
-    const long long most = ((long long)a.T * a.H / kAtRows + std::min(a.n_seq, a.T)) * ((long long)a.max_pages * a.page / kAtTile + 1);
+    // whether every count of tiles fits 32 bits, whatever the offsets and lengths are: each sequence may claim all tokens
+    const double most = (double)a.n_seq * ((double)a.T * a.H / 16 + 1) * ((double)a.max_pages * a.page / kAtTile + 1);
     const int shares = attend_shares();
     AttendJoin *joins = reinterpret_cast<AttendJoin *>(a.ws + kCtrOffset + kCtrBytes);
     float *parts = latent_parts(a.ws);

@@ -69,17 +69,6 @@ __device__ __forceinline__ void tma3d_warp(void *dst, const CUtensorMap *m, int 
         "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(saddr(bar))
         : "memory");
 }
-// Whether a barrier's phase is complete, without waiting.
-__device__ __forceinline__ bool mb_test_warp(uint64_t *b, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(saddr(b)), "r"(parity)
-        : "memory");
-    return __all_sync(0xffffffffu, done != 0);
-}
 // A operand in tensor memory (two 16-bit elements of K a column), B in shared memory.
 template <uint32_t kHi = kDescSw128>
 __device__ __forceinline__ void umma_ts_warp(uint32_t dtmem, uint32_t atmem, uint32_t b, uint32_t id, uint32_t acc)

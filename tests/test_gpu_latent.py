@@ -510,6 +510,59 @@ def test_attend_on_a_side_stream(k3):
     c.check(cfg)
 
 
+@pytest.mark.parametrize("n_seq", [128, 129, 200, 500])
+def test_attend_many_sequences(k3, n_seq):
+    """Empty ones, drafts, ones without rows, in more than a warp and more than a block looks over at once."""
+    queries = [(0, 1, 1, 2, 1, 5)[i % 6] for i in range(n_seq)]
+    lens = [(41 * i) % 300 if i % 7 else 0 for i in range(n_seq)]
+    c = Cached(queries, lens, 16, 64, n_seq)
+    op, cfg = c.holder(k3)
+    c(op)
+    c.check(cfg)
+    c.start[n_seq // 2 + 1] = -3                           # two that do not fit leave the others' to do, cut in other places
+    c.out[:] = 7.5
+    c(op)
+    a, b = sum(queries[:n_seq // 2]), sum(queries[:n_seq // 2 + 2])
+    assert (c.out[a:b] == 7.5).all()
+    c.check(cfg, skip=[n_seq // 2, n_seq // 2 + 1])
+    assert k3.k3moe_device_status(op.ws) == (6, 0x2)
+
+
+@pytest.mark.parametrize("n_seq,tables", [(40, 50000), (200, 10000)])
+def test_attend_wide_tables(k3, n_seq, tables):
+    """Tables so wide that the tiles of all sequences would not be counted in 32 bits, were they full."""
+    queries = [8] * n_seq
+    c = Cached(queries, [(77 * i) % 700 for i in range(n_seq)], 64, 256, n_seq + 1)
+    assert n_seq * sum(queries) * c.H / 64 * tables * 4 > 2 ** 31
+    wide = torch.full((n_seq, tables), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, :c.pages.shape[1]] = c.pages
+    c.pages = wide
+    op, cfg = c.holder(k3)
+    c(op)
+    c.check(cfg)
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+def test_attend_twice_at_once(k3):
+    """Two holders on two streams, beside each other; and two captured graphs of one holder, in turn."""
+    c, d = Cached([1] * 4, [3000, 500, 0, 77], 56, 64, 31), Cached([3, 1], [900, 4000], 16, 64, 32)
+    (op, cfg), (op2, cfg2) = c.holder(k3), d.holder(k3)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        c(op, stream=streams[0])
+        d(op2, stream=streams[1])
+    torch.cuda.synchronize()
+    c.check(cfg)
+    d.check(cfg2)
+    e = Cached([2] * 2, [1500, 33], 56, 64, 33)
+    graphs = k3._capture(lambda x, out: c(op), c.q, c.out), k3._capture(lambda x, out: e(op), e.q, e.out)
+    for g in graphs + graphs:
+        g.replay()
+    c.check(cfg)
+    e.check(cfg)
+
+
 PROMPT = [  # queries, keys (None: the queries' own), heads, causal, padded strides
     ([1], None, 1, 1, False),
     ([2], [5], 3, 1, True),
@@ -579,6 +632,30 @@ def test_prompt(k3, case):
         c(op, seq_start=None, kv_start=None)
         assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
     assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+@pytest.mark.parametrize("n_seq", [33, 384, 500])
+def test_prompt_many_sequences(k3, n_seq):
+    queries = [(0, 1, 7, 30)[i % 4] for i in range(n_seq)]
+    c = Expanded(queries, [(13 * i) % 150 if i % 5 else 0 for i in range(n_seq)], 3, True, n_seq)
+    op, cfg = c.holder(k3)
+    c(op)
+    c.check(cfg)
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+def test_prompt_twice_at_once(k3):
+    """Two holders on two streams beside each other, one of them with its keys in parts."""
+    c, d = Expanded([300, 500], None, 8, False, 41), Expanded([20], [6000], 4, False, 42)
+    (op, cfg), (op2, cfg2) = c.holder(k3), d.holder(k3)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        c(op, stream=streams[0])
+        d(op2, stream=streams[1])
+    torch.cuda.synchronize()
+    c.check(cfg)
+    d.check(cfg2)
 
 
 @pytest.mark.parametrize("q_scale", [0.0, 8.0])
