@@ -562,6 +562,18 @@ k3moe_status k3moe_latent_prompt(const k3moe_latent_config *lc, int32_t n_seq, i
                                  int64_t kv_head_stride, const uint16_t *rope_key, int64_t rope_stride, uint16_t *out,
                                  float *lse, void *ws, size_t ws_bytes, k3moe_stream stream);
 
+/* The five calls above, for bindings whose calls cost by the argument: words[0] is the entry, words[1] the number of its
+ * arguments, which follow in their order, a word each (addresses as numbers; no float is among them).  K3MOE_EINVAL when the entry or
+ * the number is not one of these or words is NULL, K3MOE_ESHAPE when a number does not fit the argument's type; else the entry's status. */
+typedef enum k3moe_entry {
+    K3MOE_ENTRY_NORM = 0,
+    K3MOE_ENTRY_HEAD_LINEAR = 1,
+    K3MOE_ENTRY_LATENT_WRITE = 2,
+    K3MOE_ENTRY_LATENT_ATTEND = 3,
+    K3MOE_ENTRY_LATENT_PROMPT = 4
+} k3moe_entry;
+k3moe_status k3moe_call(const int64_t *words);
+
 /* Synchronises `stream`, returns the device status word of `ws` in *code,
  * and clears it: the report of the README's rule that corruption is counted,
  * never silent (kimi-k3-in-c README, Part II, section 9, the k3_moe listing's

@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "K3MoEConfig", "K3MOE_OK", "K3MoEError", "lib", "k3moe_config", "k3moe_validate_config",
@@ -151,6 +152,7 @@ def lib():
             "k3moe_latent_attend": (ctypes.c_int, [ap, i32, i32, vp, vp, i64, i64, vp, i32, vp, i32, vp, vp, vp, vp, sz, vp]),
             "k3moe_latent_prompt": (ctypes.c_int, [ap, i32, i32, i32, vp, vp, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, vp, sz,
                                                    vp]),
+            "k3moe_call": (ctypes.c_int, [ctypes.c_char_p]),
             "k3moe_launch_count": (i64, []),
             "k3moe_set_prefill_gemm": (ctypes.c_int, [i32]),
             "k3moe_get_prefill_gemm": (i32, []),
@@ -786,9 +788,9 @@ class DeltaRule:
 # length by _require.
 
 def _dense(what, t, types, shape, index):
-    """The pointer of a contiguous tensor, or None for None."""
+    """The pointer of a contiguous tensor, or 0 for None."""
     if t is None:
-        return None
+        return 0
     if t.dtype in types and t.shape == shape and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
     _require(what, t, types, shape, index)
@@ -796,9 +798,9 @@ def _dense(what, t, types, shape, index):
 
 
 def _rowed(what, t, types, shape, index):
-    """(pointer, row stride) of a tensor whose rows may be slices of wider ones, or (None, n) for None."""
+    """(pointer, row stride) of a tensor whose rows may be slices of wider ones, or (0, n) for None."""
     if t is None:
-        return None, shape[1]
+        return 0, shape[1]
     if t.dtype in types and t.shape == shape and t.get_device() == index:
         if shape[0] <= 1:
             if shape[1] <= 1 or t.stride(1) == 1:
@@ -812,9 +814,9 @@ def _rowed(what, t, types, shape, index):
 
 def _headed(what, t, types, shape, index):
     """(pointer, stride from token to token, from head to head) of t [T][heads][columns], whose heads may be columns of
-    wider ones, or (None, 0, 0) for None."""
+    wider ones, or (0, 0, 0) for None."""
     if t is None:
-        return None, 0, 0
+        return 0, 0, 0
     T, H, n = shape
     if t.dtype in types and t.shape == shape and t.get_device() == index:
         ts, hs, es = t.stride()
@@ -836,18 +838,25 @@ class _Holder:
         self._bf16, self._f32, self._i32 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,)
         self._current, self._on = _current_stream(self._index), torch.cuda.device
         self._device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        self._words = lib().k3moe_call
         self.ws_bytes = ws_bytes
         self.ws = torch.zeros(ws_bytes, dtype=torch.uint8, device=self.device) if ws_bytes else None
 
-    def _run(self, what, fn, args, stream):
-        """fn(*args, stream) on the holder's device, whichever is the current one."""
+    def _entry(self, entry, name, n):
+        """What _run calls: one of k3moe.h's k3moe_entry, its name and its n arguments.  They go as one string of words:
+        converted one by one twenty of them took longer than the launch (4.3 us; 1.6 us packed)."""
+        return struct.Struct(f"<{n + 2}q").pack, entry, n, name
+
+    def _run(self, entry, args, stream):
+        """The entry's call with args and the stream, on the holder's device, whichever is the current one."""
+        pack, number, n, name = entry
         if self._index >= 0 and self._device_now() != self._index:
             with self._on(self._index):
-                st = fn(*args, self._current() if stream is None else _handle(stream))
+                st = self._words(pack(number, n, *args, self._current() if stream is None else _handle(stream)))
         else:
-            st = fn(*args, self._current() if stream is None else _handle(stream))
+            st = self._words(pack(number, n, *args, self._current() if stream is None else _handle(stream)))
         if st:
-            _check(what, st)
+            _check(name, st)
 
 
 class Norm(_Holder):
@@ -861,7 +870,7 @@ class Norm(_Holder):
         self._xtype = self._f32 if nc.x_f32 else self._bf16
         self._stype = self._f32 if nc.sum_f32 else self._bf16
         self._n, self._group = (nc.n,), (nc.group,)
-        self._nc, self._call = ctypes.byref(nc), lib().k3moe_norm
+        self._config, self._at, self._norm = nc, ctypes.addressof(nc), self._entry(0, "k3moe_norm", 16)
 
     def __call__(self, x, out=None, gate=None, residual=None, total=None, stream=None):
         """x [T][n] by x_f32; gate [T][n] bf16; residual and total [T][n] by sum_f32; out [T][n] bf16; rows may be
@@ -877,7 +886,7 @@ class Norm(_Holder):
         tp, ts = (rp, rs) if total is residual else _rowed("total", total, stype, shape, dev)
         op, os_ = _rowed("out", out, bf16, shape, dev)
         if T:
-            self._run("k3moe_norm", self._call, (self._nc, T, xp, xs, gp, gs, post, rp, rs, scale, tp, ts, pre, op, os_), stream)
+            self._run(self._norm, (self._at, T, xp, xs, gp, gs, post, rp, rs, scale, tp, ts, pre, op, os_), stream)
         return total if out is None else out
 
 
@@ -889,7 +898,7 @@ class HeadLinear(_Holder):
         self._init(device, k3moe_head_linear_workspace_bytes(hc, T_max))
         self.hc, self.T_max, self.w = hc, T_max, None
         self._shape = (hc.n_heads, hc.n, hc.k)
-        self._hc, self._call = ctypes.byref(hc), lib().k3moe_head_linear
+        self._config, self._at, self._linear = hc, ctypes.addressof(hc), self._entry(1, "k3moe_head_linear", 12)
 
     def __call__(self, x, y, stream=None):
         """x [T][n_heads][k] bf16, y [T][n_heads][n] bf16 written and returned; heads may be columns of wider ones."""
@@ -901,7 +910,7 @@ class HeadLinear(_Holder):
         yp, ys, yh = _headed("y", y, bf16, (T, H, n), dev)
         w = _dense("w", self.w, bf16, self._shape, dev)
         if T:
-            self._run("k3moe_head_linear", self._call, (self._hc, T, xp, xs, xh, w, yp, ys, yh, self.ws.data_ptr(), self.ws_bytes), stream)
+            self._run(self._linear, (self._at, T, xp, xs, xh, w, yp, ys, yh, self.ws.data_ptr(), self.ws_bytes), stream)
         return y
 
 
@@ -919,8 +928,8 @@ class LatentAttention(_Holder):
         self._H, self._C, self._R = lc.n_heads, lc.rank, lc.rope_dim
         self._row, self._page = lc.rank + lc.rope_dim, lc.page_size
         self._kr, self._kv, self._v = lc.key_dim + lc.rope_dim, lc.key_dim + lc.value_dim, lc.value_dim
-        self._lc, L = ctypes.byref(lc), lib()
-        self._write, self._attend, self._prompt = L.k3moe_latent_write, L.k3moe_latent_attend, L.k3moe_latent_prompt
+        self._config, self._at, self._write = lc, ctypes.addressof(lc), self._entry(2, "k3moe_latent_write", 21)
+        self._attend, self._prompt = self._entry(3, "k3moe_latent_attend", 17), self._entry(4, "k3moe_latent_prompt", 19)
 
     def new_cache(self, n_pages):
         """A zeroed cache of n_pages pages [n_pages][page_size][rank + rope_dim] bf16."""
@@ -950,8 +959,8 @@ class LatentAttention(_Holder):
         qp, qs, qh = _headed("q", q, bf16, shape, dev)
         op, os_, oh = (qp, qs, qh) if q_rope is q else _headed("q_rope", q_rope, bf16, shape, dev)
         if T:
-            self._run("k3moe_latent_write", self._write, (self._lc, T, cp, cs, gain, at, freq, rp, rs, pool, n_pages, sl, qp, qs, qh, op, os_, oh,
-                                                          self.ws.data_ptr(), self.ws_bytes), stream)
+            self._run(self._write, (self._at, T, cp, cs, gain, at, freq, rp, rs, pool, n_pages, sl, qp, qs, qh, op, os_, oh,
+                      self.ws.data_ptr(), self.ws_bytes), stream)
         return cache if rows is None else rows
 
     def attend(self, q, cache, pages, kv_len, out, seq_start=None, lse=None, stream=None):
@@ -967,8 +976,8 @@ class LatentAttention(_Holder):
         o, start = _dense("out", out, bf16, (T, H, self._C), dev), _dense("seq_start", seq_start, i32, (n_seq + 1,), dev)
         ls = _dense("lse", lse, self._f32, (T, H), dev)
         if T:
-            self._run("k3moe_latent_attend", self._attend, (self._lc, n_seq, T, start, qp, qs, qh, pool, n_pages, table, max_pages, lens, o, ls,
-                                                            self.ws.data_ptr(), self.ws_bytes), stream)
+            self._run(self._attend, (self._at, n_seq, T, start, qp, qs, qh, pool, n_pages, table, max_pages, lens, o, ls,
+                      self.ws.data_ptr(), self.ws_bytes), stream)
         return out
 
     def prompt(self, q, kv, rope_key, out, seq_start=None, kv_start=None, lse=None, stream=None):
@@ -984,6 +993,6 @@ class LatentAttention(_Holder):
         o, ls = _dense("out", out, bf16, (T, H, self._v), dev), _dense("lse", lse, self._f32, (T, H), dev)
         start, keys = _dense("seq_start", seq_start, i32, (n_seq + 1,), dev), _dense("kv_start", kv_start, i32, (n_seq + 1,), dev)
         if T:
-            self._run("k3moe_latent_prompt", self._prompt, (self._lc, n_seq, T, S, start, keys, qp, qs, qh, kp, ks, kh, rp, rs, o, ls,
-                                                            self.ws.data_ptr(), self.ws_bytes), stream)
+            self._run(self._prompt, (self._at, n_seq, T, S, start, keys, qp, qs, qh, kp, ks, kh, rp, rs, o, ls,
+                      self.ws.data_ptr(), self.ws_bytes), stream)
         return out

@@ -8,6 +8,8 @@
 #include <map>
 #include <mutex>
 #include <string>
+#include <type_traits>
+#include <utility>
 #include <vector>
 
 #include "k3moe_internal.cuh"
@@ -190,6 +192,27 @@ static size_t max_total(const k3moe_config &c, int32_t T_max, Total total)
 __global__ void check_bounds_kernel(int32_t *status, int32_t index, int32_t limit)
 {
     (void)dguard(status, index >= 0 && index < limit);
+}
+
+// ----------------------------------------------------------------------------------- calls by words
+template <typename A> static bool word_fits(int64_t v)
+{
+    if constexpr (std::is_pointer_v<A>) return true;
+    else return std::is_same_v<A, size_t> ? v >= 0 : (int64_t)(A)v == v;
+}
+template <typename A> static A word_as(int64_t v)
+{
+    if constexpr (std::is_pointer_v<A>) return reinterpret_cast<A>((uintptr_t)v);
+    else return (A)v;
+}
+template <typename... A, size_t... I>
+static k3moe_status spread_words(k3moe_status (*f)(A...), const int64_t *args, std::index_sequence<I...>)
+{
+    return (word_fits<A>(args[I]) && ...) ? f(word_as<A>(args[I])...) : K3MOE_ESHAPE;
+}
+template <typename... A> static k3moe_status call_words(k3moe_status (*f)(A...), const int64_t *words)
+{
+    return words[1] == (int64_t)sizeof...(A) ? spread_words(f, words + 2, std::index_sequence_for<A...>()) : K3MOE_EINVAL;
 }
 
 }  // namespace k3moe
@@ -702,6 +725,19 @@ k3moe_status k3moe_latent_prompt(const k3moe_latent_config *lc, int32_t n_seq, i
                        kv_head_stride, rope_key, rope_stride, out, lse, static_cast<uint8_t *>(ws)};
     result_pending_begin((cudaStream_t)stream);
     return launch_prompt(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;
+}
+
+k3moe_status k3moe_call(const int64_t *words)
+{
+    if (!words) return K3MOE_EINVAL;
+    switch (words[0]) {
+    case K3MOE_ENTRY_NORM: return call_words(k3moe_norm, words);
+    case K3MOE_ENTRY_HEAD_LINEAR: return call_words(k3moe_head_linear, words);
+    case K3MOE_ENTRY_LATENT_WRITE: return call_words(k3moe_latent_write, words);
+    case K3MOE_ENTRY_LATENT_ATTEND: return call_words(k3moe_latent_attend, words);
+    case K3MOE_ENTRY_LATENT_PROMPT: return call_words(k3moe_latent_prompt, words);
+    default: return K3MOE_EINVAL;
+    }
 }
 
 k3moe_status k3moe_device_status(void *ws, k3moe_stream stream, int32_t *code)

@@ -1,6 +1,7 @@
 """Refusals and sizes of the latent attention's entry points (no GPU needed): every check is on
 the host and comes before any CUDA call."""
 import ctypes
+import struct
 
 import pytest
 
@@ -157,6 +158,41 @@ def test_latent_prompt_refusals(k3):
         assert prompt(k3, **{name: C + by}) == EALIGN
     need = k3.k3moe_latent_workspace_bytes(k3.k3moe_latent_config(8), 3, 10)
     assert prompt(k3, ws=0) == prompt(k3, ws=A + 8) == prompt(k3, wb=need - 1) == EWORKSPACE
+
+
+def test_calls_by_words(k3):
+    """The same entries with their arguments as 64-bit words: the same statuses, and refusals of what the words cannot be."""
+    call = k3.lib().k3moe_call
+    words = lambda *w: ctypes.c_char_p(struct.pack(f"{len(w)}q", *w))  # noqa: E731
+    nc, lc = k3.k3moe_norm_config(256), k3.k3moe_latent_config(8)
+    at, la = ctypes.addressof(nc), ctypes.addressof(lc)
+    args = [at, 0, A, 256, 0, 256, A, C, 256, A, C + 4096, 256, A, C + 8192, 256, 0]
+    assert call(words(0, 16, *args)) == OK                 # no rows
+    assert call(words(0, 16, 0, *args[1:])) == EINVAL      # no config
+    assert call(words(0, 16, at, 4, A + 2, *args[3:])) == EALIGN
+    assert call(words(0, 15, *args)) == EINVAL
+    assert call(words(0, 17, *args, 0)) == EINVAL
+    for entry in (-1, 5, 1 << 32):
+        assert call(words(entry, 16, *args)) == EINVAL
+    assert call(None) == EINVAL
+    for T in (1 << 31, 1 << 32, -(1 << 31) - 1, (1 << 32) + 1):     # would be another number in 32 bits
+        assert call(words(0, 16, at, T, *args[2:])) == ESHAPE
+    hc = k3.k3moe_head_linear_config(8, 512, 128)
+    args = [ctypes.addressof(hc), 0, A, 1024, 128, A, B, 4096, 512, A, BIG, 0]
+    assert call(words(1, 12, *args)) == OK
+    args[1], args[10] = 4, 0
+    assert call(words(1, 12, *args)) == EWORKSPACE
+    args[10] = -1                                          # no size
+    assert call(words(1, 12, *args)) == ESHAPE
+    args = [la, 0, A, 576, A, A, A, B, 576, C, 4, A, A, 1536, 192, A, 1536, 192, A, BIG, 0]
+    assert call(words(2, 21, *args)) == OK
+    assert call(words(2, 21, la, 4, A, 575, *args[4:])) == ESHAPE
+    args = [la, 3, 0, A, A, 4608, 576, C, 4, A, 2, A, B, A, A, BIG, 0]
+    assert call(words(3, 17, *args)) == OK
+    assert call(words(3, 17, la, 3, 10, A, 0, *args[5:])) == EINVAL
+    args = [la, 3, 0, 12, A, A, A, 1536, 192, C, 2048, 256, A, 576, B, A, A, BIG, 0]
+    assert call(words(4, 19, *args)) == OK
+    assert call(words(4, 19, la, 3, 10, -1, *args[4:])) == ESHAPE
 
 
 def test_latent_workspace_covers_every_smaller_call(k3):
