@@ -33,6 +33,8 @@ constexpr int kAtSmem = 1024 + kAtQ + kAtP + kAtSlots * kAtBox;
 constexpr int kAtThreads = 384, kAtWarpS = 8, kAtWarpV = 9, kAtWarpLoad = 10;
 constexpr uint32_t kAtTmS = 0, kAtTmO = 128;                  // S^T of two tiles, and O^T in four blocks of 128 of c
 constexpr float kAtSlack = 8.0f;
+// A query block's queries, first product and output take about as long as this many tiles: the cuts count it so
+constexpr int kAtAhead = 2;
 
 // A part's sums in the workspace: O [query][c], then the maxima and the sums of the weights.
 constexpr size_t kAtPart = kLatPart;
@@ -45,6 +47,7 @@ struct AttendJoin {
 // Sequence i: its queries, cached rows, blocks of 1 << shift queries and tiles of each; false when something does not fit.
 struct AttendSeq {
     int t0, n, len, blocks, tiles;
+    __device__ int each() const { return kAtAhead + tiles; }  // units of a query block: what comes ahead of its tiles, and they
     __device__ bool set(const AttendArgs &a, int from, int to, int kv, int shift)
     {
         t0 = from;
@@ -62,32 +65,33 @@ struct AttendSeq {
     __device__ bool read(const AttendArgs &a, int i, int shift) { return set(a, start(a, i), start(a, i + 1), a.kv_len[i], shift); }
 };
 
-// The walk of a block's share of tiles, query block by query block.
+// The walk of a block's share of units, query block by query block.
 template <typename I> struct AttendWalk {
-    I u, end, base;                                           // next tile, the share's end, the sequence's first tile
+    I u, end, base;                                           // next unit, the share's end, the sequence's first unit
     int seq, shift;
     AttendSeq s;
     int row0, tile0, tile1;                                   // the query block and its tiles here
     __device__ bool next(const AttendArgs &a)
     {
         if (u >= end) return false;
-        while (u >= base + (I)s.blocks * s.tiles) {
-            base += (I)s.blocks * s.tiles;
+        while (u >= base + (I)s.blocks * s.each()) {
+            base += (I)s.blocks * s.each();
             s.read(a, ++seq, shift);
         }
         const I at = u - base;
-        const int block = (int)quotient(at, s.tiles);
+        const int block = (int)quotient(at, s.each()), from = (int)(at - (I)block * s.each()), to = (int)min((I)s.each(), from + (end - u));
         row0 = block << shift;
-        tile0 = (int)(at - (I)block * s.tiles);
-        tile1 = (int)min((I)s.tiles, tile0 + (end - u));
-        u += tile1 - tile0;
-        return true;
+        tile0 = max(0, from - kAtAhead);
+        tile1 = max(0, to - kAtAhead);
+        u += to - from;
+        return tile1 > 0;                                     // a share that ends ahead of the first tile leaves the block to the next
     }
+    __device__ I unit(int tile) const { return base + (I)(row0 >> shift) * s.each() + kAtAhead + tile; }
     __device__ int rows(const AttendArgs &a) const { return min(1 << shift, s.n * a.H - row0); }
     __device__ bool whole() const { return tile0 == 0 && tile1 == s.tiles; }
 };
 
-// Even shares of all tiles, the first `more` of them a tile longer; where there are fewer tiles than shares the last are empty.
+// Even shares of all units, the first `more` of them a unit longer; where there are fewer than shares the last are empty.
 template <typename I> struct AttendShares {
     I each, more;
     __device__ void cut(I all, int n)
@@ -96,9 +100,9 @@ template <typename I> struct AttendShares {
         more = all - each * n;
     }
     __device__ I begin(int i) const { return i * each + min((I)i, more); }
-    __device__ int of(I tile) const                           // the share that has it
+    __device__ int of(I unit) const                           // the share that has it
     {
-        return (int)(tile < more * (each + 1) ? tile / (each + 1) : more + (tile - more * (each + 1)) / each);
+        return (int)(unit < more * (each + 1) ? unit / (each + 1) : more + (unit - more * (each + 1)) / each);
     }
 };
 
@@ -161,7 +165,7 @@ template <typename I> __device__ __forceinline__ void attend_plan(const AttendAr
 #pragma unroll
         for (int k = 0; k < 4; k++) {
             if (s[k].blocks) s[k].blocks = (s[k].n * a.H + (1 << w.shift) - 1) >> w.shift;
-            each += units[k] = s[k].blocks ? (I)s[k].blocks * s[k].tiles : 0;
+            each += units[k] = s[k].blocks ? (I)s[k].blocks * s[k].each() : 0;
         }
         const I upto = warp_scan(each, lane);
         shares.cut(__shfl_sync(0xffffffffu, upto, 31), gridDim.x);
@@ -184,7 +188,7 @@ template <typename I> __device__ __forceinline__ void attend_plan(const AttendAr
             [&](int i) -> I {
                 AttendSeq s;
                 if (!s.read(a, i, 6)) set_status(status, K3MOE_DEV_BAD_OFFSETS);
-                return (I)s.blocks * s.tiles;
+                return (I)s.blocks * s.each();
             },
             [&](I all) {
                 shares.cut(all, gridDim.x);
@@ -201,10 +205,9 @@ template <typename I> __device__ __forceinline__ void attend_plan(const AttendAr
     if (!mine) return;
     w.base = w.u - before;
     if (a.n_seq > kAtPlanSeqs) w.s.read(a, w.seq, w.shift);
-    w.next(a);
+    sh.first.have = w.next(a);
     sh.first.walk = w;
     sh.first.shares = shares;
-    sh.first.have = 1;
 }
 
 static_assert(sizeof(AttendJoin) <= 32 && kAtRows == 64, "as the workspace is laid out");
@@ -593,7 +596,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         AttendJoin join{0, 0, 0, 0, 0, -1};
         for (int seg = 0; ok && (seg == 0 || w.next(a)); seg++) {
             const int begun = w.tile0, left = w.s.tiles - w.tile1;
-            if (seg == 0 && begun > 0) join.owner = shares.of(shares.begin(blockIdx.x) - begun);
+            if (seg == 0 && begun > 0) join.owner = shares.of(w.unit(0));
             const int n_tiles = uniform(w.tile1 - w.tile0), len = w.s.len, tile0 = w.tile0;
             const int32_t *pages = a.pages + (size_t)w.seq * a.max_pages;
 #pragma unroll 1
@@ -635,7 +638,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 join.row0 = w.row0;
                 join.rows = w.rows(a);
                 join.second = seg > 0;
-                join.parts = shares.of(w.u + left - 1) - blockIdx.x + 1;
+                join.parts = shares.of(w.unit(w.s.tiles - 1)) - blockIdx.x + 1;
             }
         }
         if (half == 0 && lane == 0) joins[blockIdx.x] = join;
@@ -813,7 +816,7 @@ cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
     });
     if (allowed != cudaSuccess) return allowed;
     // whether every count of tiles fits 32 bits, whatever the offsets and lengths are: each sequence may claim all tokens
-    const double most = (double)a.n_seq * ((double)a.T * a.H / 16 + 1) * ((double)a.max_pages * a.page / kAtTile + 1);
+    const double most = (double)a.n_seq * ((double)a.T * a.H / 16 + 1) * ((double)a.max_pages * a.page / kAtTile + 1 + kAtAhead);
     const int shares = attend_shares();
     AttendJoin *joins = reinterpret_cast<AttendJoin *>(a.ws + kCtrOffset + kCtrBytes);
     float *parts = latent_parts(a.ws);
