@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 const float sum = (sh.sum[g][0][lane] + sh.sum[g][1][lane]) + (sh.sum[g][2][lane] + sh.sum[g][3][lane]);
                 sh.inv[mine] = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
                 if (!whole) {
-                    part[kAtRows * kLatC + mine] = sh.m[mine];
+                    part[kAtRows * kLatC + mine] = isnan(sum) && sh.m[mine] == -INFINITY ? 0.0f : sh.m[mine];    // not one without keys
                     part[kAtRows * kLatC + kAtRows + mine] = sum;
                 } else if (a.lse && mine < rows) {
                     a.lse[(size_t)now.s.t0 * a.H + now.row0 + mine] = (sh.m[mine] + log2f(sum)) * kLatLn2;
@@ -654,18 +654,19 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
 // ---------------------------------------------------------------- joining
 // out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i over the parts i, M the largest m.  Blocks (x, y) for share x: of a query
-// block with few parts, the share's that begins it have four queries each, a warp a query, a lane 16 columns; with many, all its
-// shares' have a quarter of a query's columns each, their warps every fourth part.
-constexpr int kJoinThreads = 128, kJoinBlocks = kAtRows / 4, kJoinMany = 8;
+// block with few parts, the share's that begins it have eight queries each, a warp a query, a lane 16 columns; with many, all its
+// shares' have a quarter of a query's columns at a time, two, four or eight warps on it by the parts, so that a warp has asked for all
+// of its own, or a good many, before it looks at the first.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinBlocks = 4, kJoinMany = 8, kJoinDeep = 10;
+static_assert(kMaxShares <= 64 * kJoinWarps, "two factors a lane");
 
+// Where a join's parts begin in the workspace, in floats.
 struct JoinParts {
-    const float *p0, *p1;                                     // the first part, and the second
-    __device__ JoinParts(const float *parts, int share, int second)
-        : p0(parts + (size_t)(2 * share + second) * kAtPart), p1(parts + (size_t)(2 * share + 2) * kAtPart)
-    {
-    }
-    __device__ const float *operator()(int p) const { return p == 0 ? p0 : p1 + (size_t)(p - 1) * 2 * kAtPart; }
+    uint32_t p0, p1;                                          // the first part, and the second
+    __device__ JoinParts(int share, int second) : p0((2 * share + second) * (uint32_t)kAtPart), p1((2 * share + 2) * (uint32_t)kAtPart) {}
+    __device__ uint32_t operator()(int p) const { return p == 0 ? p0 : p1 + (uint32_t)(p - 1) * (uint32_t)(2 * kAtPart); }
 };
+static_assert((2 * kMaxShares + 2) * kAtPart < 1ull << 32, "in 32 bits");
 __device__ __forceinline__ void join_add(float4 &o, float f, const float4 &x)
 {
     o.x = fmaf(f, x.x, o.x);
@@ -691,32 +692,30 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 2)
     attend_join_kernel(const AttendArgs a, const float *parts, const AttendJoin *joins)
 {
     pdl_wait();
     pdl_trigger();
-    __shared__ float factor[kMaxShares], red[2][4];
-    __shared__ float4 sum[3][32];
+    __shared__ float4 sum[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const AttendJoin j = joins[blockIdx.x];
     auto row_of = [&](const AttendJoin &j, int r) { return (size_t)j.t0 * a.H + j.row0 + r; };
     auto inverse = [](float L) { return L == 0.0f ? 0.0f : 1.0f / L; };
-    const int r = 4 * blockIdx.y + warp;
-    if (j.parts < kJoinMany && r < j.rows) {
-        const JoinParts part(parts, blockIdx.x, j.second);
+    for (int r = kJoinWarps * blockIdx.y + warp; j.parts < kJoinMany && r < j.rows; r += kJoinWarps * kJoinBlocks) {
+        const JoinParts part(blockIdx.x, j.second);
         float m = -INFINITY, l = 0.0f;
         float4 x[2][4];
-        const size_t at = (size_t)r * kLatC + 4 * lane;
+        const uint32_t at = r * kLatC + 4 * lane;
         auto load = [&](int p) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) x[p & 1][i] = __ldcg(reinterpret_cast<const float4 *>(part(p) + at + 128 * i));
+            for (int i = 0; i < 4; i++) x[p & 1][i] = __ldcg(reinterpret_cast<const float4 *>(parts + (part(p) + at + 128 * i)));
         };
         load(0);
         load(1);                                              // a join has two parts at least
         if (lane < j.parts) {
-            m = part(lane)[kAtRows * kLatC + r];
-            l = part(lane)[kAtRows * kLatC + kAtRows + r];
+            m = parts[part(lane) + kAtRows * kLatC + r];
+            l = parts[part(lane) + kAtRows * kLatC + kAtRows + r];
         }
         const float M = warp_max(m), f = m == -INFINITY ? 0.0f : exp2_fast(m - M), L = warp_sum(f == 0.0f ? 0.0f : f * l), inv = inverse(L);
         float4 o[4] = {};
@@ -735,54 +734,48 @@ __global__ void __launch_bounds__(kJoinThreads)
     // pieces of the join `j` that share `first` begins: quarters of rows
     auto many = [&](const AttendJoin &j, int first) {
         if (j.rows == 0 || j.parts < kJoinMany) return;
-        const JoinParts part(parts, first, j.second);
-        for (int piece = (blockIdx.x - first) * kJoinBlocks + blockIdx.y; piece < 4 * j.rows; piece += j.parts * kJoinBlocks) {
-            const int r = piece >> 2, quarter = 128 * (piece & 3);
-            float m[kMaxShares / kJoinThreads], l[kMaxShares / kJoinThreads], top = -INFINITY;
+        const JoinParts part(first, j.second);
+        const int share = j.parts <= 20 ? 2 : j.parts <= 40 ? 4 : kJoinWarps, sets = kJoinWarps / share;      // warps of a piece
+        const int mine = warp % share, pieces = 4 * j.rows;
+        for (int p0 = (blockIdx.y * j.parts + blockIdx.x - first) * sets; p0 < pieces; p0 += j.parts * kJoinBlocks * sets) {
+            const int piece = p0 + warp / share, r = min(piece, pieces - 1) >> 2, quarter = 128 * (piece & 3);
+            const uint32_t at = r * kLatC + quarter + 4 * lane;
+            float4 x[kJoinDeep];
+            auto load = [&](int i0) {
 #pragma unroll
-            for (int k = 0; k < kMaxShares / kJoinThreads; k++) {
-                const int p = threadIdx.x + k * kJoinThreads;
-                m[k] = -INFINITY;
-                if (p < j.parts) {
-                    m[k] = part(p)[kAtRows * kLatC + r];
-                    l[k] = part(p)[kAtRows * kLatC + kAtRows + r];
-                }
-                top = fmaxf(top, m[k]);
+                for (int i = 0; i < kJoinDeep; i++)
+                    if (mine + share * (i0 + i) < j.parts) x[i] = __ldcg(reinterpret_cast<const float4 *>(parts + (part(mine + share * (i0 + i)) + at)));
+            };
+            load(0);
+            auto max_of = [&](int p) { return p < j.parts ? parts[part(p) + kAtRows * kLatC + r] : -INFINITY; };
+            const float m0 = max_of(mine + share * lane), m1 = share == kJoinWarps ? max_of(mine + share * (lane + 32)) : -INFINITY;
+            float M = -INFINITY, L = 0.0f;                    // of the parts lane, lane + 32 ..
+#pragma unroll 4
+            for (int p = lane; p < j.parts; p += 32) {
+                const float m = max_of(p), l = parts[part(p) + kAtRows * kLatC + kAtRows + r];
+                if (m == -INFINITY) continue;
+                const float top = fmaxf(m, M);
+                L = fmaf(L, exp2_fast(M - top), l * exp2_fast(m - top));
+                M = top;
             }
-            top = warp_max(top);
-            if (lane == 0) red[0][warp] = top;
-            __syncthreads();
-            const float M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-            float L = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kMaxShares / kJoinThreads; k++) {
-                const int p = threadIdx.x + k * kJoinThreads;
-                const float f = m[k] == -INFINITY ? 0.0f : exp2_fast(m[k] - M);
-                if (p < j.parts) factor[p] = f;
-                if (f != 0.0f) L += f * l[k];
-            }
-            L = warp_sum(L);
-            if (lane == 0) red[1][warp] = L;
-            __syncthreads();
-            L = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+            const float top = warp_max(M);
+            L = warp_sum(M == -INFINITY ? 0.0f : L * exp2_fast(M - top));
+            const float f0 = m0 == -INFINITY ? 0.0f : exp2_fast(m0 - top), f1 = m1 == -INFINITY ? 0.0f : exp2_fast(m1 - top);
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const size_t at = (size_t)r * kLatC + quarter + 4 * lane;
-            for (int p0 = warp; p0 < j.parts; p0 += 4 * 10) {
-                float4 x[10];
+            for (int i0 = 0; mine + share * i0 < j.parts; i0 += kJoinDeep) {
+                if (i0 > 0) load(i0);
 #pragma unroll
-                for (int i = 0; i < 10; i++)
-                    if (p0 + 4 * i < j.parts) x[i] = __ldcg(reinterpret_cast<const float4 *>(part(p0 + 4 * i) + at));
-#pragma unroll
-                for (int i = 0; i < 10; i++)
-                    if (p0 + 4 * i < j.parts) join_add(o, factor[p0 + 4 * i], x[i]);
+                for (int i = 0; i < kJoinDeep; i++) {
+                    const float f = __shfl_sync(0xffffffffu, i0 + i < 32 ? f0 : f1, (i0 + i) & 31);
+                    if (mine + share * (i0 + i) < j.parts) join_add(o, f, x[i]);
+                }
             }
-            if (warp > 0) sum[warp - 1][lane] = o;
+            if (mine > 0) sum[warp][lane] = o;
             __syncthreads();
-            if (warp == 0) {
-#pragma unroll
-                for (int k = 0; k < 3; k++) join_add(o, 1.0f, sum[k][lane]);
+            if (mine == 0 && piece < pieces) {
+                for (int k = 1; k < share; k++) join_add(o, 1.0f, sum[warp + k][lane]);
                 join_put(a.out + row_of(j, r) * kLatC + quarter + 4 * lane, o, inverse(L));
-                if (a.lse && lane == 0 && quarter == 0) a.lse[row_of(j, r)] = (M + log2f(L)) * kLatLn2;
+                if (a.lse && lane == 0 && quarter == 0) a.lse[row_of(j, r)] = (top + log2f(L)) * kLatLn2;
             }
             __syncthreads();
         }

@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
             if (kParts && r < n) {
                 part += (size_t)kPrBlock * kLatV - (r - row0) * 15;
-                part[0] = m;
+                part[0] = isnan(l) && m == -INFINITY ? 0.0f : m;      // not one without keys
                 part[kPrBlock] = l;
             } else if (a.lse && r < n) {
                 a.lse[row] = (m + log2f(l)) * kLatLn2;

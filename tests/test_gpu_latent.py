@@ -510,6 +510,21 @@ def test_attend_on_a_side_stream(k3):
     c.check(cfg)
 
 
+@pytest.mark.parametrize("queries,lens", [([1, 1, 1], [64, 20000, 900]), ([2, 3], [500, 700])])
+def test_attend_nan_queries(k3, queries, lens):
+    """A NaN in a query is all of its outputs, however many parts its rows are cut into, and nothing of another's."""
+    c = Cached(queries, lens, 16, 64, 43)
+    op, cfg = c.holder(k3)
+    c(op)
+    out, lse = c.out.clone(), c.lse.clone()
+    bad = torch.zeros(c.T, 16, dtype=torch.bool, device="cuda")
+    bad[1, 3] = bad[-1, 15] = bad[0, 0] = True
+    c.q[bad] = float("nan")
+    c(op)
+    assert torch.isnan(c.out[bad]).all() and torch.isnan(c.lse[bad]).all()
+    assert torch.equal(c.out[~bad], out[~bad]) and torch.equal(c.lse[~bad], lse[~bad])
+
+
 @pytest.mark.parametrize("n_seq", [128, 129, 200, 500])
 def test_attend_many_sequences(k3, n_seq):
     """Empty ones, drafts, ones without rows, in more than a warp and more than a block looks over at once."""
@@ -632,6 +647,20 @@ def test_prompt(k3, case):
         c(op, seq_start=None, kv_start=None)
         assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
     assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+@pytest.mark.parametrize("queries,keys", [([300], [300]), ([40], [6000])])
+def test_prompt_nan_queries(k3, queries, keys):
+    c = Expanded(queries, keys, 2, False, 44)
+    op, cfg = c.holder(k3)
+    c(op)
+    out, lse = c.out.clone(), c.lse.clone()
+    bad = torch.zeros(c.T, 2, dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[17, 0] = bad[-1, 1] = True
+    c.q[bad] = float("nan")
+    c(op)
+    assert torch.isnan(c.out[bad]).all() and torch.isnan(c.lse[bad]).all()
+    assert torch.equal(c.out[~bad], out[~bad]) and torch.equal(c.lse[~bad], lse[~bad])
 
 
 @pytest.mark.parametrize("n_seq", [33, 384, 500])
