@@ -42,6 +42,10 @@ constexpr float kPrLimit = 1073741824.0f;                     // 2^30: a sum of 
 constexpr int kPrBlock = 2 * kPrRows, kPrGroups = kLatV / 16, kPrMaxSplits = 16;
 constexpr size_t kPrPart = (size_t)kPrBlock * kLatV + 2 * kPrBlock;
 static_assert(kPrPart <= 2 * kLatPart, "a part a block, in the room of two of the absorbed form's");
+// Few query blocks of unlike lengths: the longest of all sequences first, every head's, so that what is begun last is short.
+// Their order is each block's own reckoning; only while all keys stay in the L2, which else wants a head's blocks together.
+constexpr int kPrSorted = 128;
+constexpr size_t kPrSortedBytes = 64u << 20;
 struct PromptPlace {
     int token, rows;                                          // a block's first query, and how many
 };
@@ -52,8 +56,13 @@ struct PromptShared {
     uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], q_full[2], s_full[2], p_ready[2][2], first_done[2], o_full[2], turn[2], drain[2];
     uint32_t tmem;
     volatile int bail, spoiled;
-    UnitSearch<int> search;
+    int pick;
+    union {
+        UnitSearch<int> search;
+        uint32_t order[kPrSorted];                            // work << 14 | sequence << 7 | query block
+    };
 };
+static_assert(kPrSmem + sizeof(PromptShared) <= 227 * 1024, "an SM's shared memory");
 
 // 64 of a row's scores become weights in tensor memory, packed; returns their sum.  Single floats: pairs of them cost
 // more moves than they save here (5.7 instructions a weight, 4 this way).
@@ -81,7 +90,7 @@ __device__ __forceinline__ float weigh(const uint32_t *v, uint32_t taddr, float 
 template <bool kParts>
 __global__ void __launch_bounds__(kPrThreads, 1)
     prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mkv,
-                  const __grid_constant__ CUtensorMap mr, const int blocks, float *parts, PromptPlace *places)
+                  const __grid_constant__ CUtensorMap mr, const int blocks, const int sorted, float *parts, PromptPlace *places)
 {
     extern __shared__ __align__(1024) uint8_t psm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(psm_raw) + 1023) & ~(uintptr_t)1023);
@@ -91,8 +100,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     int32_t *status = reinterpret_cast<int32_t *>(a.ws);
     pdl_wait();
     pdl_trigger();
-    // ---- the block's queries: all blocks of a head together, so that its keys stay in the L2, the longest first
-    const int h = blockIdx.x / blocks;
+    // ---- the block's queries: all blocks of a head together, so that its keys stay in the L2, the longest first; or sorted
+    const int h = !kParts && sorted ? blockIdx.x % a.H : blockIdx.x / blocks;
     auto queries = [&](int i, int *t0, int *n, int *k0, int *nk) {
         bool ok = latent_queries(a.seq_start, a.n_seq, a.T, i, t0, n);
         if (a.kv_start) {
@@ -110,25 +119,59 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         return ok;
     };
     int t0 = 0, n = 0, k0 = 0, nk = 0;
-    int before, total;
-    const int seq = find_unit<kPrThreads, int>(
-        sh.search, a.n_seq, &before, &total,
-        [&](int i) -> int {
-            int t0, n, k0, nk;
-            if (!queries(i, &t0, &n, &k0, &nk)) {
-                set_status(status, K3MOE_DEV_BAD_OFFSETS);
-                return 0;
+    auto count = [&](int i, int *t0, int *n, int *k0, int *nk) {      // its query blocks
+        if (!queries(i, t0, n, k0, nk)) {
+            set_status(status, K3MOE_DEV_BAD_OFFSETS);
+            return 0;
+        }
+        return (*n + 2 * kPrRows - 1) / (2 * kPrRows);
+    };
+    int seq, block;
+    if (!kParts && sorted) {
+        if (threadIdx.x < kPrSorted) sh.order[threadIdx.x] = 0;
+        __syncthreads();
+        if (warp == 0) {
+            int all = 0;
+            for (int i0 = 0; i0 < a.n_seq; i0 += 32) {
+                const int mine = i0 + lane < a.n_seq ? count(i0 + lane, &t0, &n, &k0, &nk) : 0, upto = all + warp_scan(mine, lane);
+                for (int b = 0, at = upto - mine; b < mine && at < blocks; b++, at++) {
+                    const int rows = min(n, (b + 1) * kPrBlock), most = a.causal ? min(nk, max(0, nk - n + rows)) : nk;
+                    // a tile takes 5 for both halves' queries, 3 for one half's
+                    const int work = 1 + (most + kPrTile - 1) / kPrTile * (rows - b * kPrBlock > kPrRows ? 5 : 3);
+                    sh.order[at] = (uint32_t)(work << 14 | (i0 + lane) << 7 | b);
+                }
+                all = __shfl_sync(0xffffffffu, upto, 31);
             }
-            return (n + 2 * kPrRows - 1) / (2 * kPrRows);
-        },
-        [&](int) { return (int)(blockIdx.x % blocks); });
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < blocks) {
+            const uint32_t mine = sh.order[threadIdx.x];
+            int rank = 0;
+            for (int i = 0; i < blocks; i++) rank += sh.order[i] > mine || (sh.order[i] == mine && i < (int)threadIdx.x);
+            if (rank == (int)blockIdx.x / a.H) sh.pick = (int)mine;
+        }
+        __syncthreads();
+        seq = sh.pick ? sh.pick >> 7 & (kPrSorted - 1) : -1;
+        block = sh.pick & (kPrSorted - 1);
+    } else {
+        int before, total;
+        seq = find_unit<kPrThreads, int>(
+            sh.search, a.n_seq, &before, &total,
+            [&](int i) -> int {
+                int t0, n, k0, nk;
+                return count(i, &t0, &n, &k0, &nk);
+            },
+            [&](int) { return (int)(blockIdx.x % blocks); });
+        block = -1 - before;
+    }
     const int splits = kParts ? gridDim.y : 1;
     if (seq < 0) {
         if (kParts && blockIdx.y == 0 && threadIdx.x == 0) places[blockIdx.x].rows = 0;
         return;
     }
     queries(seq, &t0, &n, &k0, &nk);
-    const int row0 = ((n + 2 * kPrRows - 1) / (2 * kPrRows) - 1 - before) * 2 * kPrRows;
+    if (block < 0) block += (n + kPrBlock - 1) / kPrBlock;    // counted from the last
+    const int row0 = block * kPrBlock;
     // keys that row r of the sequence sees: nk + ahead + r of them, within the nk of this block's part
     int ahead = a.causal ? 1 - n : n;
     if (kParts) {
@@ -495,10 +538,11 @@ cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t s)
     const int items = blocks * a.H;
     int splits = std::min(std::min(num_sms(), kMaxShares) / items, a.S / std::min(a.n_seq, a.T) / (4 * kPrTile));
     splits = std::max(1, std::min(splits, kPrMaxSplits));
+    const int sorted = splits == 1 && a.n_seq <= kPrSorted && blocks <= kPrSorted && (size_t)a.S * a.H * (kLatK + kLatV) * 2 <= kPrSortedBytes;
     float *parts = latent_parts(a.ws);
     PromptPlace *places = reinterpret_cast<PromptPlace *>(a.ws + kCtrOffset + kCtrBytes);
     timing_begin("latent_prompt", s);
-    cudaError_t err = launch_pdl(splits > 1 ? prompt_kernel<true> : prompt_kernel<false>, dim3((unsigned)items, (unsigned)splits), dim3(kPrThreads), kPrSmem, s, a, mq, mkv, mr, blocks, parts, places);
+    cudaError_t err = launch_pdl(splits > 1 ? prompt_kernel<true> : prompt_kernel<false>, dim3((unsigned)items, (unsigned)splits), dim3(kPrThreads), kPrSmem, s, a, mq, mkv, mr, blocks, sorted, parts, places);
     count_launch();
     timing_end("latent_prompt", s);
     if (err != cudaSuccess || splits == 1) return err;
