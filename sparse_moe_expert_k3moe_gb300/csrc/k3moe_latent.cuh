@@ -129,6 +129,15 @@ __device__ __forceinline__ int find_unit(UnitSearch<I> &sh, int n_seq, I *before
     return sh.seq;
 }
 
+// Not zero when one of eight bf16 is infinite or NaN.
+__device__ __forceinline__ uint32_t spoiled_in(const uint4 &w)
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) any |= (u[i] & 0x7F807F80u) + 0x00800080u;       // an exponent of all ones carries
+    return any & 0x80008000u;
+}
 // Clears the elements of eight bf16 that are infinite or NaN; true when there was one.
 __device__ __forceinline__ bool clear_spoiled(uint4 &w)
 {

@@ -98,6 +98,32 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     __shared__ PromptShared sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t *status = reinterpret_cast<int32_t *>(a.ws);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; i++) {
+            mb_init(&sh.k_full[i], 1);
+            mb_init(&sh.v_full[i], 1);
+            mb_init(&sh.k_empty[i], 2);
+            mb_init(&sh.v_empty[i], 2);
+            mb_init(&sh.q_full[i], 1);
+            mb_init(&sh.s_full[i], 1);
+            mb_init(&sh.p_ready[i][0], 4);
+            mb_init(&sh.p_ready[i][1], 4);
+            mb_init(&sh.o_full[i], 1);
+            mb_init(&sh.first_done[i], 1);
+            mb_init(&sh.turn[i], 1);
+            mb_init(&sh.drain[i], 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sh.bail = 0;
+        sh.spoiled = 0;
+        prefetch_map(&mq);
+        prefetch_map(&mkv);
+        prefetch_map(&mr);
+    }
+    if (warp == kPrWarpMma) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sh.tmem)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
     pdl_wait();
     pdl_trigger();
     // ---- the block's queries: all blocks of a head together, so that its keys stay in the L2, the longest first; or sorted
@@ -136,8 +162,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 const int mine = i0 + lane < a.n_seq ? count(i0 + lane, &t0, &n, &k0, &nk) : 0, upto = all + warp_scan(mine, lane);
                 for (int b = 0, at = upto - mine; b < mine && at < blocks; b++, at++) {
                     const int rows = min(n, (b + 1) * kPrBlock), most = a.causal ? min(nk, max(0, nk - n + rows)) : nk;
-                    // a tile takes 5 for both halves' queries, 3 for one half's
-                    const int work = 1 + (most + kPrTile - 1) / kPrTile * (rows - b * kPrBlock > kPrRows ? 5 : 3);
+                    const int work = 1 + (most + kPrTile - 1) / kPrTile;      // a tile takes one half's queries as long as both's
                     sh.order[at] = (uint32_t)(work << 14 | (i0 + lane) << 7 | b);
                 }
                 all = __shfl_sync(0xffffffffu, upto, 31);
@@ -167,6 +192,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const int splits = kParts ? gridDim.y : 1;
     if (seq < 0) {
         if (kParts && blockIdx.y == 0 && threadIdx.x == 0) places[blockIdx.x].rows = 0;
+        __syncwarp();
+        if (warp == kPrWarpMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(0), "r"(512));    // as below: all
         return;
     }
     queries(seq, &t0, &n, &k0, &nk);
@@ -188,31 +215,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const int first = row0 + kPrRows * half;
         return first < n ? (limit(min(n, first + kPrRows) - 1) + kPrTile - 1) / kPrTile : 0;
     };
-    const int tiles0 = tiles_of(0), tiles1 = tiles_of(1), tiles = max(tiles0, tiles1), whole = limit(row0) / kPrTile;
+    const int tiles0 = tiles_of(0), tiles1 = tiles_of(1), tiles = max(tiles0, tiles1), least = limit(row0), whole = least / kPrTile;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; i++) {
-            mb_init(&sh.k_full[i], 1);
-            mb_init(&sh.v_full[i], 1);
-            mb_init(&sh.k_empty[i], 2);
-            mb_init(&sh.v_empty[i], 2);
-            mb_init(&sh.q_full[i], 1);
-            mb_init(&sh.s_full[i], 1);
-            mb_init(&sh.p_ready[i][0], 4);
-            mb_init(&sh.p_ready[i][1], 4);
-            mb_init(&sh.o_full[i], 1);
-            mb_init(&sh.first_done[i], 1);
-            mb_init(&sh.turn[i], 1);
-            mb_init(&sh.drain[i], 1);
-        }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        sh.bail = 0;
-        sh.spoiled = 0;
-    }
-    if (warp == kPrWarpMma) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sh.tmem)), "r"(512));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -251,27 +255,36 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 for (int j = 0; j < 128; j++) v[j] = j < left ? v[j] : 0xFF800000u;
             }
             if (i >= whole) {
-                // a tile that not every row sees whole: values behind the sequence's last are cleared, and so is what is infinite or
-                // NaN, which a weight of zero would not keep out (rows that see it add it at the end)
+                // of keys that not every row sees the values that are infinite or NaN are cleared, which a weight of zero would not
+                // keep out (rows that see them add them at the end)
                 if (!(ok = wait(sh.v_full[i & 1], i >> 1))) break;
-                const int last = nk - kPrTile * i;
+                const int from = 8 * max(0, least - kPrTile * i) + (threadIdx.x & 127);
+                for (int box = 0; box < 2; box++) {
+                    uint4 *p = reinterpret_cast<uint4 *>(ring + slot_of(i, kPrQBoxes + box) * kPrBox);
 #pragma unroll 1
-                for (int e = threadIdx.x & 127; e < 2 * kPrTile * 8; e += 128) {
-                    uint4 *p = reinterpret_cast<uint4 *>(ring + slot_of(i, kPrQBoxes + (e >> 10)) * kPrBox) + (e & 1023);
-                    uint4 w = *p;
-                    if (((e >> 3) & (kPrTile - 1)) >= last) {
-                        *p = make_uint4(0, 0, 0, 0);
-                    } else if (clear_spoiled(w)) {
+                    for (int e = from; e < 8 * kPrTile; e += 4 * 128) {
+                        uint4 w[4];
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; k++) w[k] = e + 128 * k < 8 * kPrTile ? p[e + 128 * k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int k = 0; k < 4; k++) any |= spoiled_in(w[k]);
+                        if (!any) continue;
                         sh.spoiled = 1;
                         __threadfence_block();
-                        *p = w;
+#pragma unroll 1
+                        for (int at = e; at < 8 * kPrTile && at < e + 4 * 128; at += 128) {
+                            uint4 x = p[at];
+                            if (clear_spoiled(x)) p[at] = x;
+                        }
                     }
                 }
                 fence_async_smem();
             }
 #pragma unroll
             for (int b = 0; b < 2; b++) {                     // the product of the first 64 keys begins under the last
-                float sum = weigh(&v[64 * b], la_s + 32 * b, c, m);
+                float sum = 0.0f;
+                if (b > 0 || i > 0) sum = weigh(&v[64 * b], la_s + 32 * b, c, m);
                 const bool grown = sum > kPrLimit || m == -INFINITY;      // of this row: the others' stay as they are, bit for bit
                 if (__any_sync(0xffffffffu, grown)) {
                     float mx[4];
@@ -313,47 +326,61 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (ok && __any_sync(0xffffffffu, r < n)) {
             tc_fence_after();
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            const size_t row = (size_t)(t0 + r) * a.H + h;
             const bool spoiled = sh.spoiled != 0;
             float *part = kParts ? parts + ((size_t)blockIdx.x * splits + blockIdx.y) * kPrPart + (r - row0) * 16 : nullptr;
+            // 32 columns at a time; rows of out go through where the queries were, so that a warp stores whole ones
+            uint4 *stage = reinterpret_cast<uint4 *>(sm + half * kPrQBoxes * kPrBox) + 512 * q;
 #pragma unroll 1
-            for (int b = 0; b < kLatV; b += 16) {
-                float o[16];
+            for (int b = 0; b < kLatV; b += 32) {
+                uint32_t o[32];
 #pragma unroll
-                for (int j = 0; j < 16; j++) o[j] = 0.0f;
-                if (mine > 0) tmem_ld16(la_o + b, o);
+                for (int j = 0; j < 32; j++) o[j] = 0;
+                if (mine > 0) {
+                    tmem_ld16_nowait(la_o + b, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+                    tmem_ld16_nowait(la_o + b + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+                    tmem_wait_ld();
+                }
                 if (spoiled && r < n)                         // what was cleared, for the rows that see it
-                    for (int k = kPrTile * whole; k < lim; k++) {
+#pragma unroll 1
+                    for (int k = least; k < lim; k++) {
                         const uint16_t *p = a.kv + (size_t)(k0 + k) * a.kv_stride + (size_t)h * a.kv_head + kLatK + b;
 #pragma unroll
-                        for (int j = 0; j < 16; j++) {
+                        for (int j = 0; j < 32; j++) {
                             const uint32_t u = p[j];
-                            if ((u & 0x7F80u) == 0x7F80u) o[j] += bf16_bits_to_f32(u);
+                            if ((u & 0x7F80u) == 0x7F80u) o[j] = __float_as_uint(__uint_as_float(o[j]) + bf16_bits_to_f32(u));
                         }
                     }
-                if (kParts && r < n) {
-                    float4 *p = reinterpret_cast<float4 *>(part + (size_t)b * kPrBlock);
+                if (kParts) {
 #pragma unroll
-                    for (int j = 0; j < 4; j++) p[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                } else if (r < n) {
-                    uint32_t w[8];
+                    for (int j = 0; j < 8; j++)
+                        if (r < n)
+                            *reinterpret_cast<uint4 *>(part + (size_t)(b + (j & 4) * 4) * kPrBlock + 4 * (j & 3)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                } else {
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const __nv_bfloat162 x = l == 0.0f ? __floats2bfloat162_rn(0.0f, 0.0f) : __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
-                        w[j] = *reinterpret_cast<const uint32_t *>(&x);
+                    for (int j = 0; j < 4; j++) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const float x = __uint_as_float(o[8 * j + 2 * k]) * inv, y = __uint_as_float(o[8 * j + 2 * k + 1]) * inv;
+                            const __nv_bfloat162 z = l == 0.0f ? __floats2bfloat162_rn(0.0f, 0.0f) : __floats2bfloat162_rn(x, y);
+                            w[k] = *reinterpret_cast<const uint32_t *>(&z);
+                        }
+                        stage[16 * lane + ((b / 8 + j) ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    uint4 *p = reinterpret_cast<uint4 *>(a.out + row * kLatV + b);
-                    p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    p[1] = make_uint4(w[4], w[5], w[6], w[7]);
                 }
                 __syncwarp();
+            }
+            if (!kParts) {
+                uint4 *to = reinterpret_cast<uint4 *>(a.out + ((size_t)(t0 + r - lane) * a.H + h) * kLatV) + (lane & 15);
+#pragma unroll 4
+                for (int i = lane >> 4; i < min(32, n - (r - lane)); i += 2) to[(size_t)i * a.H * (kLatV / 8)] = stage[16 * i + ((lane & 15) ^ (i & 7))];
             }
             if (kParts && r < n) {
                 part += (size_t)kPrBlock * kLatV - (r - row0) * 15;
                 part[0] = isnan(l) && m == -INFINITY ? 0.0f : m;      // not one without keys
                 part[kPrBlock] = l;
             } else if (a.lse && r < n) {
-                a.lse[row] = (m + log2f(l)) * kLatLn2;
+                a.lse[(size_t)(t0 + r) * a.H + h] = (m + log2f(l)) * kLatLn2;
             }
         }
     } else {
