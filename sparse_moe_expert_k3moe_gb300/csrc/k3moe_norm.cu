@@ -100,6 +100,13 @@ __device__ __forceinline__ float sigmoid(float z)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(fmaf(e, r, e) + 1.0f));
     return s;
 }
+// The same to (6 + |z|) 2^-24 of it, for sums that are rounded to bf16: t's rounding is left where it is, and 2^t may pass into infinity.
+__device__ __forceinline__ float sigmoid_short(float z)
+{
+    float s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(exp2_fast(z * -1.442695041f) + 1.0f));
+    return s;
+}
 
 // A row is `tpr` threads', each V pieces of 8 columns, held in registers from the one read to
 // the writes; blocks of short rows hold several.  A group's sum is of 8, 16 or 32 neighbouring
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(kNormMax<V>, V == 2 && !kX32 && !kSum32 ? 3 : 
             bf16x8(ge[i], w);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                y[i][j] *= sigmoid(w[j]);
+                y[i][j] *= kSum32 ? sigmoid(w[j]) : sigmoid_short(w[j]);
                 if (kGate == K3MOE_GATE_SILU) y[i][j] *= w[j];
             }
         }
