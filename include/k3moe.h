@@ -444,7 +444,7 @@ typedef struct k3moe_norm_config {
  *   pre_gain  [N] f32 (NULL allowed without pre_norm)
  *   residual  may be NULL (zeros); gate is NULL exactly when the config has none
  *   total     may be NULL when pre_norm; out is NULL exactly when not pre_norm
- * All in float, total and out each rounded once; out is of the sum before it is rounded.  total and
+ * All in float (act below 2^-125 is zero), total and out each rounded once; out is of the sum before it is rounded.  total and
  * out may be x, gate or residual themselves where pointer, stride and type are the same, but not each
  * other, and overlap nothing otherwise.  All pointers 16-byte aligned.  T may be 0 (nothing written).
  * A NaN or an infinity stays in its row. */
@@ -500,7 +500,7 @@ typedef struct k3moe_latent_config {
 k3moe_status k3moe_latent_validate_config(const k3moe_latent_config *lc);
 
 /* Workspace bytes the three calls below need for any of at most n_seq_max sequences and T_max query
- * tokens (conventions as k3moe_workspace_bytes). */
+ * tokens (conventions as k3moe_workspace_bytes): about 40 MB, whatever their number, for the parts that several SMs leave to be joined. */
 k3moe_status k3moe_latent_workspace_bytes(const k3moe_latent_config *lc, int32_t n_seq_max, int32_t T_max,
                                           size_t *bytes);
 

@@ -110,10 +110,10 @@ __device__ __forceinline__ float sigmoid_short(float z)
 
 // A row is `tpr` threads', each V pieces of 8 columns, held in registers from the one read to
 // the writes; blocks of short rows hold several.  A group's sum is of 8, 16 or 32 neighbouring
-// lanes, a row's of all its warps.  Many rows are bound by their bytes (8192 x 7168, each head's norm with a gate:
-// 65.5 us, 5.4 TB/s: two thirds of the issue slots go to
-// the sigmoid; two blocks an SM 72); a row alone by latency, so it takes as many threads as it has pieces, and their gains are asked for
-// with the row (1 x 7168 with all there is: 3.9 us in a graph; four pieces a thread, gains when they are needed 7.0).
+// lanes, a row's of all its warps.  Many rows are bound by their bytes and instructions (8192 x 7168, each head's norm with a gate:
+// 60.6 us, 5.8 TB/s; with the longer sigmoid 65.5; two blocks an SM 66.6, four with spilled registers 82); a row alone by latency, so
+// it takes as many threads as it has pieces, and their gains are asked for with the row (1 x 7168 with all there is: 3.3 us in a
+// graph; four pieces a thread, gains when they are needed 7.0).
 template <int V> constexpr int kNormMax = V == 1 ? 1024 : 512;
 constexpr int kNormThreads = 256;
 
