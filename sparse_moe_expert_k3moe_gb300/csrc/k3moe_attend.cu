@@ -29,6 +29,9 @@ constexpr int kAtRows = 64, kAtTile = 64;                     // queries of a bl
 constexpr int kAtBoxes = kLatRow / 64;                        // 64-column boxes of a tile: c's eight, then r's
 constexpr int kAtBox = kAtTile * 128;                         // 8 KB
 constexpr int kAtSlots = 2 * kAtBoxes;                        // c of even and of odd tiles, then r of both
+// Boxes of c are loaded, waited for and freed in pairs, the first with r: the scores of what has landed are taken while the rest
+// is on its way, and the next tile but one is asked for pair by pair as the outputs get done
+constexpr int kAtPairs = kLatC / 128;
 constexpr int kAtQBox = kAtRows * 128;
 constexpr int kAtQ = kAtBoxes * kAtQBox, kAtP = kAtTile * kAtRows * 2;
 constexpr int kAtSmem = 1024 + kAtQ + kAtP + kAtSlots * kAtBox;
@@ -111,7 +114,7 @@ template <typename I> struct AttendShares {
 };
 
 template <typename I> struct AttendShared {
-    uint64_t q_full, full[2][2], empty[2][2], r_empty[2], s_full[2], p_ready[2], pv_done, drain[2];    // by the tile's turn, halves of c
+    uint64_t q_full, full[2][kAtPairs], empty[2][kAtPairs], r_empty[2], s_full[2], p_ready[2], pv_done, drain[2];    // by the tile's turn, pairs of c's boxes
     uint32_t tmem;
     volatile int bail;
     int spoiled[2];                                           // by the query block's turn
@@ -252,7 +255,7 @@ __device__ __forceinline__ bool group_any(int group, bool p)
 }
 template <typename I>
 __global__ void __launch_bounds__(kAtThreads, 1)
-    attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap m4, const __grid_constant__ CUtensorMap m1, float *parts, AttendJoin *joins)
+    attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap m2, const __grid_constant__ CUtensorMap m1, float *parts, AttendJoin *joins)
 {
     extern __shared__ __align__(1024) uint8_t asm_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(asm_raw) + 1023) & ~(uintptr_t)1023);
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     if (threadIdx.x == 0) {
         mb_init(&sh.q_full, 8);
         for (int i = 0; i < 2; i++) {
-            for (int j = 0; j < 2; j++) {
+            for (int j = 0; j < kAtPairs; j++) {
                 mb_init(&sh.full[i][j], 1);
                 mb_init(&sh.empty[i][j], 1);
             }
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.bail = 0;
         sh.spoiled[0] = sh.spoiled[1] = 0;
-        prefetch_map(&m4);
+        prefetch_map(&m2);
         prefetch_map(&m1);
     }
     pdl_wait();
@@ -365,6 +368,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; j++)
                         if (idle || j >= 8) v[j] = -INFINITY;
+                const bool free = role_done(sh.pv_done, tile - 1);      // asked ahead of where it is needed
                 float over = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 16; j++) over = fmaxf(over, v[j] + m[(j >> 2) * 2 + (j & 1)]);
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         p[2 * k + i] = *reinterpret_cast<const uint32_t *>(&h);
                     }
                 // a row's weights of 64 queries are 128 bytes of P, 128-byte swizzle; the product before has read its own
-                if (tile > 0) go_on(sh.pv_done, tile - 1);
+                if (!__all_sync(0xffffffffu, free)) go_on(sh.pv_done, tile - 1);
 #pragma unroll
                 for (int k = 0; k < 4; k++)
 #pragma unroll
@@ -548,16 +552,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 4; k++) umma_warp(D, A + 2 * k, B + 2 * k, id, !first || k > 0);
                 };
-                if (!(ok = wait(sh.full[turn][0], tile >> 1))) break;
-                tc_fence_after();
-                product(c0 + (16 + turn) * box, q0 + 8 * q_box, true);
-                umma_commit_warp(&sh.r_empty[turn]);
 #pragma unroll 1
-                for (int b = 0; b < 4; b++) product(c0 + (8 * turn + b) * box, q0 + b * q_box, false);
-                if (!(ok = wait(sh.full[turn][1], tile >> 1))) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int b = 4; b < 8; b++) product(c0 + (8 * turn + b) * box, q0 + b * q_box, false);
+                for (int j = 0; j < kAtPairs; j++) {
+                    if (!(ok = wait(sh.full[turn][j], tile >> 1))) break;
+                    tc_fence_after();
+                    if (j == 0) {
+                        product(c0 + (16 + turn) * box, q0 + 8 * q_box, true);
+                        umma_commit_warp(&sh.r_empty[turn]);
+                    }
+                    product(c0 + (8 * turn + 2 * j) * box, q0 + 2 * j * q_box, false);
+                    product(c0 + (8 * turn + 2 * j + 1) * box, q0 + (2 * j + 1) * q_box, false);
+                }
+                if (!ok) break;
                 umma_commit_warp(&sh.s_full[turn]);
             }
         }
@@ -580,11 +586,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 tc_fence_after();
                 const uint32_t A = c0 + 8 * turn * box;
 #pragma unroll 1
-                for (int b = 0; b < 4; b++) {
+                for (int b = 0; b < kAtPairs; b++) {
 #pragma unroll
                     for (int k = 0; k < kAtTile / 16; k++)
                         umma_warp(kAtTmO + 64 * b, A + 2 * b * box + (uint32_t)(k * 16 * 128 >> 4), p0 + (uint32_t)(k * 16 * 128 >> 4), id, t > 0 || k > 0);
-                    if (b & 1) umma_commit_warp(&sh.empty[turn][b >> 1]);
+                    umma_commit_warp(&sh.empty[turn][b]);
                 }
                 umma_commit_warp(&sh.pv_done);
             }
@@ -593,10 +599,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         umma_commit_warp(&sh.drain[1]);
         mb_wait_warp(&sh.drain[1], 0);
     } else {
-        // ---------------- the cache's rows: half of c, of a page's rows each box, a lane a page; the first half's warp loads r
+        // ---------------- the cache's rows: every other pair of boxes of c, of a page's rows each, a lane a page; the first warp loads r
         const int box_rows = min(a.page, kAtTile), pieces = kAtTile >> min(a.page_shift, 6), half = uniform(warp - kAtWarpLoad);
         int tile = 0;
         bool ok = true;
+        int asked = 0;                                        // pairs, two of a tile
         AttendJoin join{0, 0, 0, 0, 0, -1};
         for (int seg = 0; ok && (seg == 0 || w.next(a)); seg++) {
             const int begun = w.tile0, left = w.s.tiles - w.tile1;
@@ -618,23 +625,28 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 }
                 const int n = uniform(__popc(__ballot_sync(0xffffffffu, row >= 0)));
                 const int row0 = uniform(__shfl_sync(0xffffffffu, row, 0));
-                uint64_t *full = &sh.full[turn][half];
                 const uint32_t rows_bytes = (uint32_t)(box_rows * 128);
-                auto load = [&](int slot, int group) {
+                auto load = [&](int slot, int group, uint64_t *full) {
                     uint8_t *dst = ring + slot * kAtBox;
                     if (n > 0) tma3d_warp(dst, &m1, 0, row0, group, full);
 #pragma unroll 1
                     for (int j = 1; j < n; j++) tma3d_warp(dst + j * rows_bytes, &m1, 0, uniform(__shfl_sync(0xffffffffu, row, j)), group, full);
                 };
-                if (tile >= 2 && (!(ok = wait(sh.empty[turn][half], phase - 1)) || (half == 0 && !(ok = wait(sh.r_empty[turn], phase - 1))))) break;
-                mb_expect_tx_warp(full, (half == 0 ? 5 : 4) * n * rows_bytes);
-                if (box_rows == kAtTile) {                    // half of c's boxes are one copy
-                    if (n > 0) tma3d_warp(ring + (8 * turn + 4 * half) * kAtBox, &m4, 0, row0, 4 * half, full);
-                } else {
 #pragma unroll 1
-                    for (int b = 0; b < 4; b++) load(8 * turn + 4 * half + b, 4 * half + b);
+                for (int j = half; j < kAtPairs; j += 2) {
+                    uint64_t *full = &sh.full[turn][j];
+                    if (tile >= 2 && (!(ok = wait(sh.empty[turn][j], phase - 1)) || (j == 0 && !(ok = wait(sh.r_empty[turn], phase - 1))))) break;
+                    mb_expect_tx_warp(full, (j == 0 ? 3 : 2) * n * rows_bytes);
+                    if (j == 0) load(16 + turn, 8, full);
+                    if (box_rows == kAtTile) {                // a pair is one copy
+                        if (n > 0) tma3d_warp(ring + (8 * turn + 2 * j) * kAtBox, &m2, 0, row0, 2 * j, full);
+                    } else {
+#pragma unroll 1
+                        for (int b = 2 * j; b < 2 * j + 2; b++) load(8 * turn + b, b, full);
+                    }
+                    asked++;
                 }
-                if (half == 0) load(16 + turn, 8);
+                if (!ok) break;
             }
             // the query block that a cut leaves unfinished, for the second kernel: its first part writes it down
             if (begun == 0 && left > 0) {
@@ -646,9 +658,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
         }
         if (half == 0 && lane == 0) joins[blockIdx.x] = join;
-        // the block's shared memory stays until its last copies have landed, when another role gave up too (boxes that a
-        // wait cut short do not complete: that wait is bounded as well)
-        for (int f = max(0, tile - 2 + !ok); f < tile + !ok; f++) mb_wait_warp(&sh.full[f & 1][half], (uint32_t)(f >> 1) & 1u);
+        // the block's shared memory stays until its last copies have landed, when another role gave up too
+        for (int i = max(0, asked - 4); i < asked; i++) mb_wait_warp(&sh.full[(i >> 1) & 1][half + 2 * (i & 1)], (uint32_t)(i >> 2) & 1u);
     }
     tc_fence_before();
     __syncthreads();
@@ -803,11 +814,11 @@ size_t latent_workspace(const k3moe_latent_config &lc, int n_seq, int T)
 
 cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
 {
-    // the cache as [9 boxes of columns][rows][64]: boxes of a page's or a tile's rows, four of columns at once or one
-    CUtensorMap m4{}, m1{};
+    // the cache as [9 boxes of columns][rows][64]: boxes of a page's or a tile's rows, two of columns at once or one
+    CUtensorMap m2{}, m1{};
     const uint64_t rows = (uint64_t)a.n_pages * a.page;
     const uint32_t box_rows = (uint32_t)std::min(a.page, kAtTile);
-    if (!map16x3(&m4, a.cache, kAtBoxes, 64, rows, kLatRow, 64, box_rows, 4) || !map16x3(&m1, a.cache, kAtBoxes, 64, rows, kLatRow, 64, box_rows, 1))
+    if (!map16x3(&m2, a.cache, kAtBoxes, 64, rows, kLatRow, 64, box_rows, 2) || !map16x3(&m1, a.cache, kAtBoxes, 64, rows, kLatRow, 64, box_rows, 1))
         return cudaErrorInvalidValue;
     const cudaError_t allowed = once_a_device([] {
         const cudaError_t e = cudaFuncSetAttribute(attend_kernel<int>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem);
@@ -821,7 +832,7 @@ cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
     float *parts = latent_parts(a.ws);
     timing_begin("latent_attend", s);
     cudaError_t err = launch_pdl(most < INT32_MAX ? attend_kernel<int> : attend_kernel<long long>, dim3((unsigned)shares), dim3(kAtThreads), kAtSmem, s, a,
-                                 m4, m1, parts, joins);
+                                 m2, m1, parts, joins);
     count_launch();
     timing_end("latent_attend", s);
     if (err != cudaSuccess) return err;

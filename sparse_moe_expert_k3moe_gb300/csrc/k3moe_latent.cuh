@@ -55,6 +55,17 @@ __device__ __forceinline__ bool role_wait(uint64_t *b, int phase, int32_t *statu
     return __all_sync(0xffffffffu, done != 0) || role_wait_long(b, (uint32_t)phase & 1u, status, bail);
 }
 
+// A lane's look at a phase, without a wait.
+__device__ __forceinline__ bool role_done(uint64_t &b, int phase)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(saddr(&b)), "r"((uint32_t)phase & 1u)
+        : "memory");
+    return done != 0;
+}
 // a / b of positive numbers, in 32 bits where they fit: the long division is a hundred instructions.
 __device__ __forceinline__ long long quotient(long long a, int b) { return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b); }
 __device__ __forceinline__ int quotient(int a, int b) { return (int)((uint32_t)a / (uint32_t)b); }
