@@ -552,10 +552,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 4; k++) umma_warp(D, A + 2 * k, B + 2 * k, id, !first || k > 0);
                 };
-#pragma unroll 1
+                bool there = false;                           // looked for under the products before
+#pragma unroll
                 for (int j = 0; j < kAtPairs; j++) {
-                    if (!(ok = wait(sh.full[turn][j], tile >> 1))) break;
-                    tc_fence_after();
+                    if (!__all_sync(0xffffffffu, there) && !(ok = wait(sh.full[turn][j], tile >> 1))) break;
+                    if (j == 0) tc_fence_after();
+                    there = j + 1 < kAtPairs && role_done(sh.full[turn][j + 1], tile >> 1);
                     if (j == 0) {
                         product(c0 + (16 + turn) * box, q0 + 8 * q_box, true);
                         umma_commit_warp(&sh.r_empty[turn]);
