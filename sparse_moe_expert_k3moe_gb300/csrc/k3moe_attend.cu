@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 float v[16];
                 const int at = kAtTile * t + row;             // of the sequence's rows
 #pragma unroll
-                for (int j = 0; j < 16; j++) v[j] = __uint_as_float(u[j]) * c;
+                for (int j = 0; j < 16; j++) v[j] = fmaf(__uint_as_float(u[j]), c, m[(j >> 2) * 2 + (j & 1)]);     // the weights' exponents
                 if (kAtTile * (t + 1) > least)
 #pragma unroll
                     for (int j = 0; j < 16; j++) {
@@ -369,13 +369,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     for (int j = 0; j < 16; j++)
                         if (idle || j >= 8) v[j] = -INFINITY;
                 const bool free = role_done(sh.pv_done, tile - 1);      // asked ahead of where it is needed
-                float over = -INFINITY;
+                float over = v[0];
 #pragma unroll
-                for (int j = 0; j < 16; j++) over = fmaxf(over, v[j] + m[(j >> 2) * 2 + (j & 1)]);
+                for (int j = 1; j < 15; j += 2) over = max3(over, v[j], v[j + 1]);
+                over = fmaxf(over, v[15]);
                 if (group_any(g, first || over > kAtSlack)) {
                     float x[8];
 #pragma unroll
-                    for (int j = 0; j < 8; j++) x[j] = fmaxf(v[4 * (j >> 1) + (j & 1)], v[4 * (j >> 1) + 2 + (j & 1)]);
+                    for (int j = 0; j < 8; j++) x[j] = fmaxf(v[4 * (j >> 1) + (j & 1)], v[4 * (j >> 1) + 2 + (j & 1)]) - m[j];
                     over_rows(x, [](float p, float r) { return fmaxf(p, r); });
                     if (lane < 4)
 #pragma unroll
@@ -391,8 +392,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
                         const int at = 32 * g + 8 * (j >> 1) + col + (j & 1);
-                        m[j] = sh.m[at] == -INFINITY ? 0.0f : -sh.m[at];
+                        const float to = sh.m[at] == -INFINITY ? 0.0f : -sh.m[at], by = to - m[j];
+                        m[j] = to;
                         l[j] *= sh.f[at];
+                        v[4 * (j >> 1) + (j & 1)] += by;
+                        v[4 * (j >> 1) + 2 + (j & 1)] += by;
                     }
                     if (!first) {
                         go_on(sh.pv_done, tile - 1);
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 for (int k = 0; k < 4; k++)
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
-                        const float x = exp2_fast(v[4 * k + 2 * i] + m[2 * k]), y = exp2_fast(v[4 * k + 2 * i + 1] + m[2 * k + 1]);
+                        const float x = exp2_fast(v[4 * k + 2 * i]), y = exp2_fast(v[4 * k + 2 * i + 1]);
                         l[2 * k] += x;
                         l[2 * k + 1] += y;
                         const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
