@@ -13,9 +13,11 @@
 // into as many even parts as there are SMs; a query block that a cut goes through leaves its parts' sums (float) in the
 // workspace, and a second kernel joins them.
 //
-// Measured, both kernels, 56 heads: 96 tokens of up to 8192 rows 102 us (489 MB: 4.8 TB/s over all, 5.5 in the middle), one token of
-// 131071 rows 44.7 (27 of them loads), of 777 rows 12.7 (every step's latency once).  40 drafted tokens of 11 sequences,
-// 16 heads, pages of 16: 24.5; with cuts that count nothing ahead of a query block some SMs had four of its starts (29.4 against 27.0 then).
+// Measured, both kernels, 56 heads: 96 tokens of up to 8192 rows 100 us (489 MB: 4.9 TB/s over all, 5.6 in the middle), one token of
+// 131071 rows 43.4 (26 of them loads), of 777 rows 12.4 (every step's latency once).  40 drafted tokens of 11 sequences,
+// 16 heads, pages of 16: 24.5; with cuts that count nothing ahead of a query block some SMs had four of its starts (29.4
+// against 27.0 then).  A tile is in its place for about 8000 clocks: 4300 until its first boxes have landed, 700 to 2400 of scores,
+// 900 of weights, 250 to 1100 of outputs.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
