@@ -47,10 +47,10 @@ constexpr int kAtAhead = 2;
 
 // A part's sums in the workspace: O [query][c], then the maxima and the sums of the weights.
 constexpr size_t kAtPart = kLatPart;
-// What a cut leaves to join: the query block's first part is share i's last (its first or second), the others
-// are the first ones of the shares after it, whose `owner` i is.
+// A query block that cuts leave to join: its first part is share `first`'s last (its first or second), the others are the
+// first ones of the shares after it.  Each share writes down the one that begins in it and the one that goes on there.
 struct AttendJoin {
-    int t0, row0, rows, second, parts, owner;                 // rows = 0: none begins here; owner = -1: none goes on here
+    int t0, row0, rows, first, second, parts;                 // rows = 0: none
 };
 
 // Sequence i: its queries, cached rows, blocks of 1 << shift queries and tiles of each; false when something does not fit.
@@ -214,12 +214,14 @@ template <typename I> __device__ __forceinline__ void attend_plan(const AttendAr
     if (!mine) return;
     w.base = w.u - before;
     if (a.n_seq > kAtPlanSeqs) w.s.read(a, w.seq, w.shift);
-    sh.first.have = w.next(a);
+    const bool any = w.next(a);
+    if (any) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.pages + (size_t)w.seq * a.max_pages + min(kAtTile * w.tile0 >> a.page_shift, a.max_pages - 1)));
+    sh.first.have = any;
     sh.first.walk = w;
     sh.first.shares = shares;
 }
 
-static_assert(sizeof(AttendJoin) <= 32 && kAtRows == 64, "as the workspace is laid out");
+static_assert(2 * sizeof(AttendJoin) * kMaxShares <= kLatJoinBytes && kAtRows == 64, "as the workspace is laid out");
 
 // S^T's 16 lanes of a warp, 32 columns: v[4 k + 2 i + j] is row lane / 4 + 8 i, column 8 k + 2 (lane % 4) + j.
 __device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[16])
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int shift = w.shift;
     __syncthreads();                                          // what is read here is written over by the softmax
     if (!have) {
-        if (threadIdx.x == 0) joins[blockIdx.x] = AttendJoin{0, 0, 0, 0, 0, -1};
+        if (threadIdx.x < 2) joins[2 * blockIdx.x + threadIdx.x].rows = 0;
         if (warp == kAtWarpS) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(512));
         return;
     }
@@ -612,10 +614,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         int tile = 0;
         bool ok = true;
         int asked = 0;                                        // pairs, two of a tile
-        AttendJoin join{0, 0, 0, 0, 0, -1};
+        if (half == 0 && lane < 2) joins[2 * blockIdx.x + lane].rows = 0;
+        __syncwarp();
         for (int seg = 0; ok && (seg == 0 || w.next(a)); seg++) {
             const int begun = w.tile0, left = w.s.tiles - w.tile1;
-            if (seg == 0 && begun > 0) join.owner = shares.of(w.unit(0));
             const int n_tiles = uniform(w.tile1 - w.tile0), len = w.s.len, tile0 = w.tile0;
             const int32_t *pages = a.pages + (size_t)w.seq * a.max_pages;
 #pragma unroll 1
@@ -656,16 +658,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 }
                 if (!ok) break;
             }
-            // the query block that a cut leaves unfinished, for the second kernel: its first part writes it down
-            if (begun == 0 && left > 0) {
-                join.t0 = w.s.t0;
-                join.row0 = w.row0;
-                join.rows = w.rows(a);
-                join.second = seg > 0;
-                join.parts = shares.of(w.unit(w.s.tiles - 1)) - blockIdx.x + 1;
+            // the query blocks that cuts leave unfinished, for the second kernel
+            if (half == 0 && lane == 0 && (begun > 0 || left > 0)) {
+                const int first = begun > 0 ? shares.of(w.unit(0)) : blockIdx.x;
+                const bool second = shares.begin(first) < w.unit(-kAtAhead);      // another one's last tile comes before it there
+                joins[2 * blockIdx.x + (begun > 0)] = AttendJoin{w.s.t0, w.row0, w.rows(a), first, second, shares.of(w.unit(w.s.tiles - 1)) - first + 1};
             }
         }
-        if (half == 0 && lane == 0) joins[blockIdx.x] = join;
         // the block's shared memory stays until its last copies have landed, when another role gave up too
         for (int i = max(0, asked - 4); i < asked; i++) mb_wait_warp(&sh.full[(i >> 1) & 1][half + 2 * (i & 1)], (uint32_t)(i >> 2) & 1u);
     }
@@ -724,11 +723,11 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
     pdl_trigger();
     __shared__ float4 sum[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const AttendJoin j = joins[blockIdx.x];
+    const AttendJoin j = joins[2 * blockIdx.x], on = joins[2 * blockIdx.x + 1];
     auto row_of = [&](const AttendJoin &j, int r) { return (size_t)j.t0 * a.H + j.row0 + r; };
     auto inverse = [](float L) { return L == 0.0f ? 0.0f : 1.0f / L; };
     for (int r = kJoinWarps * blockIdx.y + warp; j.parts < kJoinMany && r < j.rows; r += kJoinWarps * kJoinBlocks) {
-        const JoinParts part(blockIdx.x, j.second);
+        const JoinParts part(j.first, j.second);
         float m = -INFINITY, l = 0.0f;
         float4 x[2][4];
         const uint32_t at = r * kLatC + 4 * lane;
@@ -756,13 +755,13 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
         for (int i = 0; i < 4; i++) join_put(to + 128 * i, o[i], inv);
         if (a.lse && lane == 0) a.lse[row_of(j, r)] = (M + log2f(L)) * kLatLn2;
     }
-    // pieces of the join `j` that share `first` begins: quarters of rows
-    auto many = [&](const AttendJoin &j, int first) {
+    // pieces of a join: quarters of rows
+    auto many = [&](const AttendJoin &j) {
         if (j.rows == 0 || j.parts < kJoinMany) return;
-        const JoinParts part(first, j.second);
+        const JoinParts part(j.first, j.second);
         const int share = j.parts <= 20 ? 2 : j.parts <= 40 ? 4 : kJoinWarps, sets = kJoinWarps / share;      // warps of a piece
         const int mine = warp % share, pieces = 4 * j.rows;
-        for (int p0 = (blockIdx.y * j.parts + blockIdx.x - first) * sets; p0 < pieces; p0 += j.parts * kJoinBlocks * sets) {
+        for (int p0 = (blockIdx.y * j.parts + blockIdx.x - j.first) * sets; p0 < pieces; p0 += j.parts * kJoinBlocks * sets) {
             const int piece = p0 + warp / share, r = min(piece, pieces - 1) >> 2, quarter = 128 * (piece & 3);
             const uint32_t at = r * kLatC + quarter + 4 * lane;
             float4 x[kJoinDeep];
@@ -805,8 +804,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
             __syncthreads();
         }
     };
-    many(j, blockIdx.x);
-    if (j.owner >= 0) many(joins[j.owner], j.owner);
+    many(j);
+    many(on);
 }
 
 int attend_shares() { return std::min(num_sms(), kMaxShares); }

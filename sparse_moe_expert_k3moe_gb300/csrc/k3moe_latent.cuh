@@ -15,7 +15,7 @@ constexpr float kLatLog2e = 1.4426950408889634f, kLatLn2 = 0.6931471805599453f;
 // The workspace behind the counters: what joins parts (of each of up to kMaxShares blocks), then two parts' sums a block,
 // 64 queries x 512 columns with their maxima and sums in the absorbed form.
 constexpr int kMaxShares = 512;
-constexpr size_t kLatPart = (size_t)64 * kLatC + 2 * 64, kLatJoinBytes = (size_t)kMaxShares * 32;
+constexpr size_t kLatPart = (size_t)64 * kLatC + 2 * 64, kLatJoinBytes = (size_t)kMaxShares * 64;
 inline float *latent_parts(uint8_t *ws) { return reinterpret_cast<float *>(ws + kCtrOffset + kCtrBytes + kLatJoinBytes); }
 
 // Queries [first, first + n) of sequence i; false when its offsets are not ascending within 0 .. T.
