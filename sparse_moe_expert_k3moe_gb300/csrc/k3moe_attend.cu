@@ -13,9 +13,9 @@
 // into as many even parts as there are SMs; a query block that a cut goes through leaves its parts' sums (float) in the
 // workspace, and a second kernel joins them.
 //
-// Measured, both kernels, 56 heads: 96 tokens of up to 8192 rows 100 us (489 MB: 4.9 TB/s over all, 5.6 in the middle), one token of
-// 131071 rows 43.4 (26 of them loads), of 777 rows 12.4 (every step's latency once).  40 drafted tokens of 11 sequences,
-// 16 heads, pages of 16: 24.5; with cuts that count nothing ahead of a query block some SMs had four of its starts (29.4
+// Measured, both kernels, 56 heads: 96 tokens of up to 8192 rows 99.5 us (489 MB: 4.9 TB/s over all, 5.6 in the middle), one token of
+// 131071 rows 42.8 (26 of them loads), of 777 rows 12.1 (every step's latency once).  40 drafted tokens of 11 sequences,
+// 16 heads, pages of 16: 24.2; with cuts that count nothing ahead of a query block some SMs had four of its starts (29.4
 // against 27.0 then).  A tile is in its place for about 8000 clocks: 4300 until its first boxes have landed, 700 to 2400 of scores,
 // 900 of weights, 250 to 1100 of outputs.
 #include <cuda.h>
@@ -679,8 +679,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 // block with few parts, the share's that begins it have eight queries each, a warp a query, a lane 16 columns; with many, all its
 // shares' have a quarter of a query's columns at a time, two, four or eight warps on it by the parts, so that a warp has asked for all
 // of its own, or a good many, before it looks at the first.  Its loads' latency is what it takes: two blocks an SM that go on to
-// their next piece, rather than eight that wait for a place (draft of 11: 24.5 us for both kernels; a block a piece with barriers for
-// the factors 27.0).
+// their next piece, rather than eight that wait for a place (draft of 11: 24.5 us for both kernels then; a block a piece with barriers
+// for the factors 27.0).
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinBlocks = 4, kJoinMany = 8, kJoinDeep = 10;
 static_assert(kMaxShares <= 64 * kJoinWarps, "two factors a lane");
 
