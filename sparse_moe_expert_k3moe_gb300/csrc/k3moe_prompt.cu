@@ -569,7 +569,7 @@ cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t s)
     const int items = blocks * a.H;
     int splits = std::min(std::min(num_sms(), kMaxShares) / items, a.S / std::min(a.n_seq, a.T) / (4 * kPrTile));
     splits = std::max(1, std::min(splits, kPrMaxSplits));
-    const int sorted = splits == 1 && a.n_seq <= kPrSorted && blocks <= kPrSorted && (size_t)a.S * a.H * (kLatK + kLatV) * 2 <= kPrSortedBytes;
+    const int sorted = splits == 1 && items > num_sms() && a.n_seq <= kPrSorted && blocks <= kPrSorted && (size_t)a.S * a.H * (kLatK + kLatV) * 2 <= kPrSortedBytes;
     float *parts = latent_parts(a.ws);
     PromptPlace *places = reinterpret_cast<PromptPlace *>(a.ws + kCtrOffset + kCtrBytes);
     timing_begin("latent_prompt", s);
