@@ -1,12 +1,13 @@
 // k3moe_head.cu -- y[t][h] = W[h] x[t][h]: each head's own projection (a latent attention's
 // queries into the latent, and what they attended back to values).
 //
-// A block has 128 of a head's output columns and up to 128 tokens: the weights are the A operand and the tokens B, 64
+// A block has 128 of a head's output columns and up to 256 tokens: the weights are the A operand and the tokens B, 64
 // columns of K a stage of the ring, which leaves room for a second block on the SM whose loads run under this one's
-// epilogue.  A thread of the epilogue owns an output column and its warp's lanes 32 neighbouring ones.
-// What bounds it: one token (56 heads, 128 to 512) start and the first loads, 3.2 us in a graph; a batch the loads from
-// the L2 and an epilogue, once each (333 tokens of 56 heads, 512 to 128: 6.0 us; all of K loaded before a block's end, 64 tokens a
-// block, one block an SM: 13.0).
+// epilogue; where there are no more blocks than SMs the ring has the room of both.  A thread of the epilogue owns an
+// output column and its warp's lanes 32 neighbouring ones.
+// What bounds it: one token (56 heads, 128 to 512) start and the first loads, 3.1 us in a graph; a batch the bytes that an SM takes
+// from the L2, and an epilogue, once each.  With inputs from the DRAM, 56 heads, 512 to 128: 100 tokens 6.3 us, 333 tokens 9.2 (5.7 where
+// the L2 has them), 28 heads 6.4; with up to 128 tokens a block, however many blocks that makes, 7.7, 9.4 and 7.8.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -16,8 +17,9 @@
 namespace k3moe {
 namespace {
 
-constexpr int kHdMaxBN = 128, kHdABytes = 128 * 128;          // tokens a block; 64 columns of its weights
-constexpr int kHdThreads = 192, kHdRing = 100 * 1024, kHdMaxStages = 5;   // four epilogue warps, loads, MMAs; two blocks an SM
+constexpr int kHdMaxBN = 256, kHdABytes = 128 * 128;          // tokens a block; 64 columns of its weights
+constexpr int kHdThreads = 192, kHdMaxStages = 8;             // four epilogue warps, loads, MMAs
+constexpr int kHdRing = 100 * 1024, kHdRingAlone = 200 * 1024;            // two blocks an SM; no more blocks than SMs
 
 struct HeadTile {
     int bn, stages, cols;                                     // tokens; ring; columns of tensor memory
@@ -127,17 +129,28 @@ __global__ void __launch_bounds__(kHdThreads, 2) head_linear_kernel(const HeadLi
 cudaError_t launch_head_linear(const HeadLinearArgs &a, cudaStream_t s)
 {
     HeadTile tl{};
-    const int tiles = (a.T + kHdMaxBN - 1) / kHdMaxBN;
-    tl.bn = ((a.T + tiles - 1) / tiles + 15) & ~15;
-    tl.cols = tl.bn <= 32 ? 32 : tl.bn <= 64 ? 64 : 128;
-    const int stage_bytes = kHdABytes + tl.bn * 128;
-    tl.stages = std::min(std::min(kHdMaxStages, kHdRing / stage_bytes), (a.K + 63) / 64);
+    // as many tokens a block as leaves the SM with the most blocks the fewest rows of weights and tokens to load; 128 at most where K
+    // is short and an epilogue longer than the loads (333 tokens, 56 heads, 128 to 512: 10.0 us, with 176 a block 10.9)
+    const int most = a.K >= 256 ? kHdMaxBN : 128;
+    const long long columns = (long long)((a.N + 127) / 128) * a.H;
+    long long least = 0;
+    for (int tiles = (a.T + most - 1) / most, i = 0; i < 8; tiles++, i++) {
+        const int bn = ((a.T + tiles - 1) / tiles + 15) & ~15;
+        const long long blocks = columns * ((a.T + bn - 1) / bn), rows = (blocks + num_sms() - 1) / num_sms() * (128 + bn);
+        if (i == 0 || rows < least) {
+            least = rows;
+            tl.bn = bn;
+        }
+    }
+    tl.cols = tl.bn <= 32 ? 32 : tl.bn <= 64 ? 64 : tl.bn <= 128 ? 128 : 256;
+    const int stage_bytes = kHdABytes + tl.bn * 128, ring = columns * ((a.T + tl.bn - 1) / tl.bn) <= num_sms() ? kHdRingAlone : kHdRing;
+    tl.stages = std::min(std::min(kHdMaxStages, ring / stage_bytes), (a.K + 63) / 64);
     CUtensorMap mw{}, mx{};
     if (!map16x3(&mw, a.w, (uint64_t)a.H, (uint64_t)a.N * a.K, (uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.K, 128, 1) ||
         !map16x3(&mx, a.x, (uint64_t)a.T, (uint64_t)a.x_stride, (uint64_t)a.H, (uint64_t)a.x_head, (uint64_t)a.K, 1, (uint32_t)tl.bn))
         return cudaErrorInvalidValue;
     const cudaError_t allowed =
-        once_a_device([] { return cudaFuncSetAttribute(head_linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kHdRing); });
+        once_a_device([] { return cudaFuncSetAttribute(head_linear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kHdRingAlone); });
     if (allowed != cudaSuccess) return allowed;
     timing_begin("head_linear", s);
     const cudaError_t err = launch_pdl(head_linear_kernel, dim3((unsigned)((a.N + 127) / 128), (unsigned)a.H, (unsigned)((a.T + tl.bn - 1) / tl.bn)),
