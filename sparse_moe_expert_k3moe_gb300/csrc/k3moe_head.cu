@@ -6,7 +6,7 @@
 // epilogue; where there are no more blocks than SMs the ring has the room of both.  A thread of the epilogue owns an
 // output column and its warp's lanes 32 neighbouring ones.
 // What bounds it: one token (56 heads, 128 to 512) start and the first loads, 3.1 us in a graph; a batch the bytes that an SM takes
-// from the L2, and an epilogue, once each.  With inputs from the DRAM, 56 heads, 512 to 128: 100 tokens 6.3 us, 333 tokens 9.2 (5.7 where
+// from the L2, and an epilogue, once each.  With inputs from the DRAM, 56 heads, 512 to 128: 100 tokens 6.2 us, 333 tokens 9.1 (5.9 where
 // the L2 has them), 28 heads 6.4; with up to 128 tokens a block, however many blocks that makes, 7.7, 9.4 and 7.8.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -97,24 +97,25 @@ __global__ void __launch_bounds__(kHdThreads, 2) head_linear_kernel(const HeadLi
         // where rows start on a word neighbouring lanes trade a token each, two columns of one token a store
         const bool pairs = a.N % 2 == 0 && a.y_stride % 2 == 0 && a.y_head % 2 == 0 && reinterpret_cast<uintptr_t>(a.y) % 4 == 0;
         uint16_t *y = a.y + (size_t)h * a.y_head + (size_t)t0 * a.y_stride;
-        for (int c0 = 0; c0 < left; c0 += 16) {
-            uint32_t v[16];
-            tmem_ld16_nowait(la + c0, v);
+        for (int c0 = 0; c0 < left; c0 += 32) {               // (32 columns of tensor memory at a time are always there)
+            uint32_t v[2][16];
+            tmem_ld16_nowait(la + c0, v[0]);
+            tmem_ld16_nowait(la + c0 + 16, v[1]);
             tmem_wait_ld();
             if (pairs) {
                 uint16_t *p = y + (size_t)(c0 + odd) * a.y_stride + (n & ~1);
 #pragma unroll
-                for (int j = 0; j < 8; j++, p += 2 * a.y_stride) {
-                    const float z0 = __uint_as_float(v[2 * j]), z1 = __uint_as_float(v[2 * j + 1]);
+                for (int j = 0; j < 16; j++, p += 2 * a.y_stride) {
+                    const float z0 = __uint_as_float(v[j >> 3][2 * (j & 7)]), z1 = __uint_as_float(v[j >> 3][2 * (j & 7) + 1]);
                     const float got = __shfl_xor_sync(0xffffffffu, odd ? z0 : z1, 1);
                     const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(got, z1) : __floats2bfloat162_rn(z0, got);
                     if (n < a.N && c0 + 2 * j + odd < left) *reinterpret_cast<__nv_bfloat162 *>(p) = w;
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 16; j++)
+                for (int j = 0; j < 32; j++)
                     if (n < a.N && c0 + j < left)
-                        *reinterpret_cast<__nv_bfloat16 *>(y + (size_t)(c0 + j) * a.y_stride + n) = __float2bfloat16_rn(__uint_as_float(v[j]));
+                        *reinterpret_cast<__nv_bfloat16 *>(y + (size_t)(c0 + j) * a.y_stride + n) = __float2bfloat16_rn(__uint_as_float(v[j >> 4][j & 15]));
             }
         }
     }
