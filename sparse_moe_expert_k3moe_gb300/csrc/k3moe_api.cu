@@ -693,7 +693,7 @@ k3moe_status k3moe_latent_attend(const k3moe_latent_config *lc, int32_t n_seq, i
     if (!ws || !aligned(ws, 256) || ws_bytes < latent_workspace(*lc, n_seq, T)) return K3MOE_EWORKSPACE;
     int32_t page_shift = 4;
     while ((1 << page_shift) < lc->page_size) page_shift++;
-    const AttendArgs a{n_seq, T, lc->n_heads, lc->page_size, page_shift, lc->causal, lc->scale, seq_start, q, q_stride, q_head_stride, cache, n_pages,
+    const AttendArgs a{n_seq, T, lc->n_heads, lc->page_size, page_shift, lc->causal, 0, lc->scale, seq_start, q, q_stride, q_head_stride, cache, n_pages,
                        pages, max_pages, kv_len, out, lse, static_cast<uint8_t *>(ws)};
     result_pending_begin((cudaStream_t)stream);
     return launch_attend(a, (cudaStream_t)stream) == cudaSuccess ? K3MOE_OK : K3MOE_ECUDA;

@@ -21,6 +21,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <cmath>
+
 #include "k3moe_internal.cuh"
 #include "k3moe_latent.cuh"
 
@@ -55,8 +57,7 @@ struct AttendJoin {
 
 // Sequence i: its queries, cached rows, blocks of 1 << shift queries and tiles of each; false when something does not fit.
 struct AttendSeq {
-    int t0, n, len, blocks, tiles;
-    __device__ int each() const { return kAtAhead + tiles; }  // units of a query block: what comes ahead of its tiles, and they
+    int t0, n, len, blocks, tiles, each;                      // units of a query block: what comes ahead of its tiles, and they
     __device__ bool set(const AttendArgs &a, int from, int to, int kv, int shift)
     {
         t0 = from;
@@ -65,6 +66,7 @@ struct AttendSeq {
         const bool ok = from >= 0 && to >= from && to <= a.T && len >= 0 && len <= a.max_pages << a.page_shift;
         blocks = ok ? (n * a.H + (1 << shift) - 1) >> shift : 0;
         tiles = max(1, (len + kAtTile - 1) / kAtTile);        // one that has nothing where no row is cached
+        each = a.whole ? 1 : kAtAhead + tiles;
         return ok;
     }
     __device__ static int start(const AttendArgs &a, int i)
@@ -83,19 +85,19 @@ template <typename I> struct AttendWalk {
     __device__ bool next(const AttendArgs &a)
     {
         if (u >= end) return false;
-        while (u >= base + (I)s.blocks * s.each()) {
-            base += (I)s.blocks * s.each();
+        while (u >= base + (I)s.blocks * s.each) {
+            base += (I)s.blocks * s.each;
             s.read(a, ++seq, shift);
         }
         const I at = u - base;
-        const int block = (int)quotient(at, s.each()), from = (int)(at - (I)block * s.each()), to = (int)min((I)s.each(), from + (end - u));
+        const int block = (int)quotient(at, s.each), from = (int)(at - (I)block * s.each), to = (int)min((I)s.each, from + (end - u));
         row0 = block << shift;
-        tile0 = max(0, from - kAtAhead);
-        tile1 = max(0, to - kAtAhead);
+        tile0 = a.whole ? 0 : max(0, from - kAtAhead);
+        tile1 = a.whole ? s.tiles : max(0, to - kAtAhead);
         u += to - from;
         return tile1 > 0;                                     // a share that ends ahead of the first tile leaves the block to the next
     }
-    __device__ I unit(int tile) const { return base + (I)(row0 >> shift) * s.each() + kAtAhead + tile; }
+    __device__ I unit(int tile) const { return base + (I)(row0 >> shift) * s.each + kAtAhead + tile; }
     __device__ int rows(const AttendArgs &a) const { return min(1 << shift, s.n * a.H - row0); }
     __device__ bool whole() const { return tile0 == 0 && tile1 == s.tiles; }
 };
@@ -163,7 +165,7 @@ template <typename I> __device__ __forceinline__ void attend_plan(const AttendAr
         for (int k = 0; k < 4; k++) {
             s[k].blocks = 0;
             if (4 * lane + k < a.n_seq) bad = !s[k].set(a, from[k], from[k + 1], kv[k], 6) || bad;
-            all += s[k].blocks ? (I)s[k].blocks * s[k].tiles : 0;
+            all += s[k].blocks ? (I)s[k].blocks * (a.whole ? 1 : s[k].tiles) : 0;
         }
         if (bad) set_status(status, K3MOE_DEV_BAD_OFFSETS);
 #pragma unroll
@@ -174,7 +176,7 @@ template <typename I> __device__ __forceinline__ void attend_plan(const AttendAr
 #pragma unroll
         for (int k = 0; k < 4; k++) {
             if (s[k].blocks) s[k].blocks = (s[k].n * a.H + (1 << w.shift) - 1) >> w.shift;
-            each += units[k] = s[k].blocks ? (I)s[k].blocks * s[k].each() : 0;
+            each += units[k] = s[k].blocks ? (I)s[k].blocks * s[k].each : 0;
         }
         const I upto = warp_scan(each, lane);
         shares.cut(__shfl_sync(0xffffffffu, upto, 31), gridDim.x);
@@ -197,7 +199,7 @@ template <typename I> __device__ __forceinline__ void attend_plan(const AttendAr
             [&](int i) -> I {
                 AttendSeq s;
                 if (!s.read(a, i, 6)) set_status(status, K3MOE_DEV_BAD_OFFSETS);
-                return (I)s.blocks * s.each();
+                return (I)s.blocks * s.each;
             },
             [&](I all) {
                 shares.cut(all, gridDim.x);
@@ -819,8 +821,9 @@ size_t latent_workspace(const k3moe_latent_config &lc, int n_seq, int T)
     return n_seq > 0 && T > 0 ? base + kLatJoinBytes + (size_t)attend_shares() * 2 * kAtPart * 4 : base;
 }
 
-cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
+cudaError_t launch_attend(const AttendArgs &args, cudaStream_t s)
 {
+    AttendArgs a = args;
     // the cache as [9 boxes of columns][rows][64]: boxes of a page's or a tile's rows, two of columns at once or one
     CUtensorMap m2{}, m1{};
     const uint64_t rows = (uint64_t)a.n_pages * a.page;
@@ -835,6 +838,12 @@ cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
     // whether every count of tiles fits 32 bits, whatever the offsets and lengths are: each sequence may claim all tokens
     const double most = (double)a.n_seq * ((double)a.T * a.H / 16 + 1) * ((double)a.max_pages * a.page / kAtTile + 1 + kAtAhead);
     const int shares = attend_shares();
+    // With short tables a query block is one SM's, whole, and nothing is joined: that saves the second kernel and costs the tiles by which
+    // the busiest SM has more than its even part, here of sequences half as long as the tables on average; six and a half of them
+    // are even (one token x 56 heads behind 250 rows 10.1 us either way, behind 60 7.0 against 8.9, 380 12.1 against 10.7; 96 tokens behind
+    // 500 18.6 against 22.4).
+    const double blocks = std::ceil((double)a.T * a.H / kAtRows), tiles = std::ceil((double)a.max_pages * a.page / kAtTile);
+    a.whole = tiles * (std::ceil(blocks / shares) - 0.5 * blocks / shares) <= 6.5;
     AttendJoin *joins = reinterpret_cast<AttendJoin *>(a.ws + kCtrOffset + kCtrBytes);
     float *parts = latent_parts(a.ws);
     timing_begin("latent_attend", s);
@@ -842,7 +851,7 @@ cudaError_t launch_attend(const AttendArgs &a, cudaStream_t s)
                                  m2, m1, parts, joins);
     count_launch();
     timing_end("latent_attend", s);
-    if (err != cudaSuccess) return err;
+    if (err != cudaSuccess || a.whole) return err;
     timing_begin("latent_attend_join", s);
     err = launch_pdl(attend_join_kernel, dim3((unsigned)shares, kJoinBlocks), dim3(kJoinThreads), 0, s, a, (const float *)parts, (const AttendJoin *)joins);
     count_launch();

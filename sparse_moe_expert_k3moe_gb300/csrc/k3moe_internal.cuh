@@ -438,7 +438,7 @@ struct LatentWriteArgs {
 };
 cudaError_t launch_latent_write(const LatentWriteArgs &a, cudaStream_t s);
 struct AttendArgs {
-    int32_t n_seq, T, H, page, page_shift, causal;
+    int32_t n_seq, T, H, page, page_shift, causal, whole; // whole: no query block is cut (the launch says)
     float scale;
     const int32_t *seq_start;                             // NULL: T / n_seq tokens each
     const uint16_t *q;
