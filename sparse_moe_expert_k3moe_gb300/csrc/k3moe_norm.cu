@@ -58,8 +58,14 @@ __device__ __forceinline__ void store8(void *base, bool f32, size_t at, const fl
 {
     if (f32) {
         float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(base) + at);
-        p[0] = make_float4(x[0], x[1], x[2], x[3]);
-        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {      // a sector at once
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
+                         "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                         : "memory");
+        } else {
+            p[0] = make_float4(x[0], x[1], x[2], x[3]);
+            p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
     } else {
         *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(base) + at) = pack8(x);
     }
@@ -110,12 +116,12 @@ __device__ __forceinline__ float sigmoid_short(float z)
 
 // A row is `tpr` threads', each V pieces of 8 columns, held in registers from the one read to
 // the writes; blocks of short rows hold several.  A group's sum is of 8, 16 or 32 neighbouring
-// lanes, a row's of all its warps.  Many rows are bound by their bytes and instructions (8192 x 7168, each head's norm with a gate:
-// 60.6 us, 5.8 TB/s; with the longer sigmoid 65.5; two blocks an SM 66.6, four with spilled registers 82); a row alone by latency, so
-// it takes as many threads as it has pieces, and their gains are asked for with the row (1 x 7168 with all there is: 3.3 us in a
-// graph; four pieces a thread, gains when they are needed 7.0).
+// lanes, a row's of all its warps.  Fewer rows are bound by latency: one alone takes as many threads as it has pieces, and their
+// gains are asked for with the row (1 x 7168 with all there is: 3.3 us in a graph; four pieces a thread, gains when they are needed 7.0).
+// Many long ones are the kernel's below.
 template <int V> constexpr int kNormMax = V == 1 ? 1024 : 512;
 constexpr int kNormThreads = 256;
+constexpr int kStreamN = 2560, kStreamRows = 4, kStreamRing = 208 * 1024;         // rows that are long, and as many an SM that are many
 
 template <int V, bool kX32, bool kSum32, int kGate>
 __global__ void __launch_bounds__(kNormMax<V>, V == 2 && !kX32 && !kSum32 ? 3 : 1) norm_kernel(const NormArgs a, const float per_row, const float per_group)
@@ -228,9 +234,125 @@ __global__ void __launch_bounds__(kNormMax<V>, V == 2 && !kX32 && !kSum32 ? 3 : 
     }
 }
 
+// Many long rows: the blocks that fill an SM take every so many rows, a thread 8 columns of each.  Its gains stay in registers (all
+// three have three times the bytes of a bf16 row), and the next rows' pieces are asked for ahead (kStages - 1 of them) into shared
+// memory, so that the two sums over a row cost no load's wait.  Bound by the bytes: 8192 x 7168, each head's norm with a gate, 54 us
+// (6.5 TB/s; a row a block 60.7), 4096 x 7168 with a residual and both norms 41.2 (47.9), with f32 sums 53.9 (69.8), 4000 x 3000 25.4
+// (28.2).  8192 x 2200 took 34 against 29.8, so shorter rows stay a block's own.  Two or four stages are within 2% but for 4000 x 3000 (31.7, 26).
+__device__ __forceinline__ void ahead16(uint8_t *to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr(to)), "l"(from) : "memory");
+}
+template <int kStages, bool kX32, bool kSum32, int kGate>
+__global__ void __launch_bounds__(1024, 1) norm_stream_kernel(const NormArgs a, const float per_row, const float per_group)
+{
+    extern __shared__ __align__(128) uint8_t ring[];          // [stage]: x, gate and residual, each thread's 8 columns side by side
+    __shared__ float part[2][2][32];
+    constexpr int kX = kX32 ? 2 : 1, kG = kGate != K3MOE_GATE_NONE ? 1 : 0, kR = kSum32 ? 2 : 1, kPieces = kX + kG + kR;
+    const int p = threadIdx.x, lane = p & 31, warp = p >> 5, warps = blockDim.x >> 5;
+    const bool in = p < a.N >> 3;
+    auto place = [&](int stage, int piece) { return ring + (stage * kPieces + piece) * blockDim.x * 16; };
+    // a warp's 32 bytes a thread of an f32 row, in the order of their addresses: whole sectors
+    auto ask_f32 = [&](int stage, int piece, const void *x, int64_t at) {
+        const float *row = static_cast<const float *>(x) + at;
+#pragma unroll
+        for (int q = 64 * warp + lane, k = 0; k < 2; k++, q += 32)
+            if (q < a.N >> 2) ahead16(place(stage, piece) + 16 * q, row + 4 * q);
+    };
+    auto ask_bf16 = [&](int stage, int piece, const void *x, int64_t at) { ahead16(place(stage, piece) + 16 * p, static_cast<const uint16_t *>(x) + at + 8 * p); };
+    pdl_wait();
+    pdl_trigger();
+    auto ask = [&](int t, int stage) {
+        if (in && t < a.T) {
+            if (!kX32) ask_bf16(stage, 0, a.x, t * a.x_stride);
+            if (kG) ask_bf16(stage, kX, a.gate, t * a.gate_stride);
+            if (!kSum32 && a.residual) ask_bf16(stage, kX + kG, a.residual, t * a.residual_stride);
+        }
+        if (kX32 && t < a.T) ask_f32(stage, 0, a.x, t * a.x_stride);
+        if (kSum32 && a.residual && t < a.T) ask_f32(stage, kX + kG, a.residual, t * a.residual_stride);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; i++) ask(blockIdx.x + i * gridDim.x, i);
+    float post[8], scale[8], pre[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) post[j] = scale[j] = pre[j] = 1.0f;
+    if (in && a.post_norm) load_gain8(a.post_gain, a.group == a.N ? 8 * p : (8 * p) & (a.group - 1), post);
+    if (in && a.scale) load_gain8(a.scale, 8 * p, scale);
+    if (in && a.pre_norm) load_gain8(a.pre_gain, 8 * p, pre);
+#pragma unroll
+    for (int j = 0; j < 8; j++) post[j] *= a.alpha;
+    auto row_sum = [&](float v, float *mine) {
+        v = lanes_sum(v, 32);
+        if (lane == 0) mine[warp] = v;
+        __syncthreads();
+        return lanes_sum(lane < warps ? mine[lane] : 0.0f, 32);
+    };
+    int stage = 0;
+    for (int t = blockIdx.x, turn = 0; t < a.T; t += gridDim.x, turn ^= 1, stage = stage + 1 == kStages ? 0 : stage + 1) {
+        if (kX32 || kSum32) __syncwarp();                     // the row before has been read: pieces are other lanes' too
+        ask(t + (kStages - 1) * gridDim.x, stage == 0 ? kStages - 1 : stage - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        if (kX32 || kSum32) __syncwarp();
+        float y[8] = {}, w[8];
+        auto floats_at = [&](int first, bool f32, float(&v)[8]) { floats(load8(place(stage, first), f32, 8 * p), f32, v); };
+        if (in) floats_at(0, kX32, y);
+        if (a.post_norm) {
+            const float ss = squares(y);
+            const float r = a.group == a.N ? rsqrtf(fmaf(row_sum(ss, part[turn][0]), per_row, a.eps)) : rsqrtf(fmaf(lanes_sum(ss, a.group >> 3), per_group, a.eps));
+#pragma unroll
+            for (int j = 0; j < 8; j++) y[j] *= r;
+        }
+        float sq = 0.0f;
+        if (in) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) y[j] *= post[j];
+            if (kG) {
+                floats_at(kX, false, w);
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    y[j] *= kSum32 ? sigmoid(w[j]) : sigmoid_short(w[j]);
+                    if (kGate == K3MOE_GATE_SILU) y[j] *= w[j];
+                }
+            }
+            if (a.scale)
+#pragma unroll
+                for (int j = 0; j < 8; j++) y[j] *= scale[j];
+            if (a.residual) {
+                floats_at(kX + kG, kSum32, w);
+#pragma unroll
+                for (int j = 0; j < 8; j++) y[j] += w[j];
+            }
+            if (a.total) store8(a.total, kSum32, (size_t)t * a.total_stride + 8 * p, y);
+            sq = squares(y);
+        }
+        if (a.pre_norm) {
+            const float r = rsqrtf(fmaf(row_sum(sq, part[turn][1]), per_row, a.eps));
+            if (in) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) w[j] = pre[j] * (y[j] * r);
+                store8(a.out, false, (size_t)t * a.out_stride + 8 * p, w);
+            }
+        }
+    }
+}
+
 template <int V, bool kX32, bool kSum32, int kGate>
 cudaError_t launch_norm_as(const NormArgs &a, cudaStream_t s)
 {
+    if (V == 2 && a.N >= kStreamN && a.T >= kStreamRows * num_sms()) {
+        const int threads = (a.N / 8 + 31) / 32 * 32, stage = threads * 16 * ((kX32 ? 2 : 1) + (kGate != K3MOE_GATE_NONE ? 1 : 0) + (kSum32 ? 2 : 1));
+        const bool deep = 3 * stage <= kStreamRing;
+        const auto kernel = deep ? norm_stream_kernel<3, kX32, kSum32, kGate> : norm_stream_kernel<2, kX32, kSum32, kGate>;
+        const cudaError_t allowed = once_a_device([] {
+            const cudaError_t e = cudaFuncSetAttribute(norm_stream_kernel<3, kX32, kSum32, kGate>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamRing);
+            return e != cudaSuccess ? e : cudaFuncSetAttribute(norm_stream_kernel<2, kX32, kSum32, kGate>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamRing);
+        });
+        if (allowed != cudaSuccess) return allowed;
+        const int blocks = std::max(1, std::min(1024 / threads, kStreamRing / (stage * (deep ? 3 : 2))));     // an SM's
+        return launch_pdl(kernel, dim3((unsigned)std::min(blocks * num_sms(), a.T)), dim3((unsigned)threads), (size_t)stage * (deep ? 3 : 2), s, a, 1.0f / (float)a.N,
+                          1.0f / (float)a.group);
+    }
     const int tpr = (a.N / 8 + 32 * V - 1) / (32 * V) * 32, rows = std::max(1, kNormThreads / tpr);
     return launch_pdl(norm_kernel<V, kX32, kSum32, kGate>, dim3((unsigned)((a.T + rows - 1) / rows)), dim3((unsigned)tpr, (unsigned)rows), 0, s, a,
                       1.0f / (float)a.N, 1.0f / (float)a.group);

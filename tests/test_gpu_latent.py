@@ -71,6 +71,14 @@ NORM = [  # T, N, group, gate, x f32, sum f32, residual, scale, post, pre, pad
     (257, 264, 0, "none", False, False, True, True, False, True, 0),
     (19, 520, 0, "silu", False, True, True, True, False, False, 0),
     (1000, 24, 0, "none", False, False, False, False, True, True, 0),
+    (1300, 7168, 128, "sigmoid", False, False, False, False, True, False, 0),     # many long rows: a block takes several
+    (901, 7168, 0, "none", False, False, True, True, True, True, 8),
+    (700, 4104, 0, "silu", True, True, True, True, True, True, 16),
+    (650, 8192, 256, "silu", True, True, True, False, True, True, 0),
+    (1111, 2056, 0, "sigmoid", False, True, False, True, True, True, 0),
+    (620, 5120, 64, "none", True, False, True, False, True, False, 8),
+    (777, 6000, 0, "sigmoid", False, False, True, True, False, True, 0),
+    (640, 2568, 0, "sigmoid", True, True, True, True, True, True, 8),
 ]
 
 
