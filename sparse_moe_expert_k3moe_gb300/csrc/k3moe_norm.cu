@@ -118,10 +118,10 @@ __device__ __forceinline__ float sigmoid_short(float z)
 // the writes; blocks of short rows hold several.  A group's sum is of 8, 16 or 32 neighbouring
 // lanes, a row's of all its warps.  Fewer rows are bound by latency: one alone takes as many threads as it has pieces, and their
 // gains are asked for with the row (1 x 7168 with all there is: 3.3 us in a graph; four pieces a thread, gains when they are needed 7.0).
-// Many long ones are the kernel's below.
+// Many rows are the kernel's below.
 template <int V> constexpr int kNormMax = V == 1 ? 1024 : 512;
 constexpr int kNormThreads = 256;
-constexpr int kStreamN = 2560, kStreamRows = 4, kStreamRing = 208 * 1024;         // rows that are long, and as many an SM that are many
+constexpr int kStreamN = 512, kStreamRows = 4, kStreamRing = 208 * 1024;         // rows that are long, and as many an SM that are many
 
 template <int V, bool kX32, bool kSum32, int kGate>
 __global__ void __launch_bounds__(kNormMax<V>, V == 2 && !kX32 && !kSum32 ? 3 : 1) norm_kernel(const NormArgs a, const float per_row, const float per_group)
@@ -234,11 +234,13 @@ __global__ void __launch_bounds__(kNormMax<V>, V == 2 && !kX32 && !kSum32 ? 3 : 
     }
 }
 
-// Many long rows: the blocks that fill an SM take every so many rows, a thread 8 columns of each.  Its gains stay in registers (all
+// Many rows of 512 columns and more: the blocks that fill an SM take every so many rows, a thread 8 columns of each.  Its gains stay in registers (all
 // three have three times the bytes of a bf16 row), and the next rows' pieces are asked for ahead (kStages - 1 of them) into shared
 // memory, so that the two sums over a row cost no load's wait.  Bound by the bytes: 8192 x 7168, each head's norm with a gate, 54 us
-// (6.5 TB/s; a row a block 60.7), 4096 x 7168 with a residual and both norms 41.2 (47.9), with f32 sums 53.9 (69.8), 4000 x 3000 25.4
-// (28.2).  8192 x 2200 took 34 against 29.8, so shorter rows stay a block's own.  Two or four stages are within 2% but for 4000 x 3000 (31.7, 26).
+// (6.5 TB/s; a row a block, or several short ones, 60.7), 4096 x 7168 with a residual and both norms 41.2 (47.9), with f32 sums 53.9
+// (69.8), 8192 x 1024 13.4 (18.1), 4000 x 2048 13.0 (17.8), 8192 x 512 5.7 either way.  Of blocks as many as the registers hold: one less
+// leaves loads unasked (8192 x 2200 33.0 against 26.5), one more waits for a place (4000 x 2048 17.0).  Two or four stages are
+// within 2% where a row is long, but for 4000 x 3000 (31.7, 26.0 against 25.4).
 __device__ __forceinline__ void ahead16(uint8_t *to, const void *from)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr(to)), "l"(from) : "memory");
@@ -340,18 +342,29 @@ __global__ void __launch_bounds__(1024, 1) norm_stream_kernel(const NormArgs a, 
 template <int V, bool kX32, bool kSum32, int kGate>
 cudaError_t launch_norm_as(const NormArgs &a, cudaStream_t s)
 {
-    if (V == 2 && a.N >= kStreamN && a.T >= kStreamRows * num_sms()) {
-        const int threads = (a.N / 8 + 31) / 32 * 32, stage = threads * 16 * ((kX32 ? 2 : 1) + (kGate != K3MOE_GATE_NONE ? 1 : 0) + (kSum32 ? 2 : 1));
-        const bool deep = 3 * stage <= kStreamRing;
-        const auto kernel = deep ? norm_stream_kernel<3, kX32, kSum32, kGate> : norm_stream_kernel<2, kX32, kSum32, kGate>;
-        const cudaError_t allowed = once_a_device([] {
-            const cudaError_t e = cudaFuncSetAttribute(norm_stream_kernel<3, kX32, kSum32, kGate>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamRing);
-            return e != cudaSuccess ? e : cudaFuncSetAttribute(norm_stream_kernel<2, kX32, kSum32, kGate>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamRing);
-        });
-        if (allowed != cudaSuccess) return allowed;
-        const int blocks = std::max(1, std::min(1024 / threads, kStreamRing / (stage * (deep ? 3 : 2))));     // an SM's
-        return launch_pdl(kernel, dim3((unsigned)std::min(blocks * num_sms(), a.T)), dim3((unsigned)threads), (size_t)stage * (deep ? 3 : 2), s, a, 1.0f / (float)a.N,
-                          1.0f / (float)a.group);
+    const int threads = (a.N / 8 + 31) / 32 * 32, stage = threads * 16 * ((kX32 ? 2 : 1) + (kGate != K3MOE_GATE_NONE ? 1 : 0) + (kSum32 ? 2 : 1));
+    if (V <= 2 && a.N >= kStreamN && a.T >= kStreamRows * num_sms()) {
+        const bool three = 3 * stage <= kStreamRing;
+        const auto kernel = three ? norm_stream_kernel<3, kX32, kSum32, kGate> : norm_stream_kernel<2, kX32, kSum32, kGate>;
+        static const int warps = [] {                         // that fit an SM's registers, eight a thread at a time
+            int most = 64;
+            for (const void *k : {(const void *)norm_stream_kernel<3, kX32, kSum32, kGate>, (const void *)norm_stream_kernel<2, kX32, kSum32, kGate>}) {
+                cudaFuncAttributes fa{};
+                if (cudaFuncGetAttributes(&fa, k) != cudaSuccess) return 32;
+                most = std::min(most, 65536 / 32 / ((fa.numRegs + 7) / 8 * 8));
+            }
+            return most;
+        }();
+        const int blocks = std::max(1, std::min(warps / (threads / 32), kStreamRing / (stage * (three ? 3 : 2))));    // an SM's
+        if (a.T >= kStreamRows * blocks * num_sms()) {
+            const cudaError_t allowed = once_a_device([] {
+                const cudaError_t e = cudaFuncSetAttribute(norm_stream_kernel<3, kX32, kSum32, kGate>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamRing);
+                return e != cudaSuccess ? e : cudaFuncSetAttribute(norm_stream_kernel<2, kX32, kSum32, kGate>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamRing);
+            });
+            if (allowed != cudaSuccess) return allowed;
+            return launch_pdl(kernel, dim3((unsigned)(blocks * num_sms())), dim3((unsigned)threads), (size_t)stage * (three ? 3 : 2), s, a, 1.0f / (float)a.N,
+                              1.0f / (float)a.group);
+        }
     }
     const int tpr = (a.N / 8 + 32 * V - 1) / (32 * V) * 32, rows = std::max(1, kNormThreads / tpr);
     return launch_pdl(norm_kernel<V, kX32, kSum32, kGate>, dim3((unsigned)((a.T + rows - 1) / rows)), dim3((unsigned)tpr, (unsigned)rows), 0, s, a,

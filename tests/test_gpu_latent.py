@@ -79,6 +79,12 @@ NORM = [  # T, N, group, gate, x f32, sum f32, residual, scale, post, pre, pad
     (620, 5120, 64, "none", True, False, True, False, True, False, 8),
     (777, 6000, 0, "sigmoid", False, False, True, True, False, True, 0),
     (640, 2568, 0, "sigmoid", True, True, True, True, True, True, 8),
+    (1400, 4104, 0, "silu", True, True, True, True, True, True, 16),              # and several of the shorter ones on an SM
+    (1900, 2568, 0, "sigmoid", True, True, True, True, True, True, 8),
+    (2500, 2056, 0, "sigmoid", False, True, False, True, True, True, 0),
+    (2500, 2048, 64, "silu", False, False, False, False, True, False, 24),
+    (5600, 1024, 256, "none", True, False, True, True, True, True, 0),
+    (7400, 520, 0, "silu", False, False, True, False, False, True, 0),
 ]
 
 
