@@ -564,10 +564,11 @@ cudaError_t launch_prompt(const PromptArgs &a, cudaStream_t s)
     if (allowed != cudaSuccess) return allowed;
     const int blocks = a.seq_start ? a.T / (2 * kPrRows) + std::min(a.n_seq, a.T)
                                    : a.n_seq == 1 ? (a.T + 2 * kPrRows - 1) / (2 * kPrRows) : a.n_seq;
-    // parts of the keys while the blocks leave SMs without one, of four tiles at least by the sequences' average; their sums
-    // are where the absorbed form has its own
+    // parts of the keys while the blocks leave SMs without one, of four tiles at least by the sequences' average, or as if half of all
+    // keys were one sequence's (4 prompts of 55 tokens in all behind up to 2561: 15.7 us, by the average alone 22.4; 12 of 300 behind up to
+    // 1000, 3 heads, 13.8 and 19.0; even ones take the same either way); their sums are where the absorbed form has its own
     const int items = blocks * a.H;
-    int splits = std::min(std::min(num_sms(), kMaxShares) / items, a.S / std::min(a.n_seq, a.T) / (4 * kPrTile));
+    int splits = std::min(std::min(num_sms(), kMaxShares) / items, std::max(a.S / std::min(a.n_seq, a.T) / (4 * kPrTile), a.S / (8 * kPrTile)));
     splits = std::max(1, std::min(splits, kPrMaxSplits));
     const int sorted = splits == 1 && items > num_sms() && a.n_seq <= kPrSorted && blocks <= kPrSorted && (size_t)a.S * a.H * (kLatK + kLatV) * 2 <= kPrSortedBytes;
     float *parts = latent_parts(a.ws);

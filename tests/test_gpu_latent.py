@@ -612,6 +612,7 @@ PROMPT = [  # queries, keys (None: the queries' own), heads, causal, padded stri
     ([17], [5000], 2, 1, False),                                # few queries, many keys: parts of the keys
     ([200, 3], [6000, 0], 3, 1, True),
     ([1, 130], [4097, 4000], 1, 0, False),
+    ([5, 40, 0, 7], [5, 3000, 100, 8], 1, 1, False),            # one long among short ones: parts that have no keys
     ([260], [2600], 5, 1, False),
 ]
 
