@@ -576,6 +576,34 @@ def test_attend_wide_tables(k3, n_seq, tables):
     assert k3.k3moe_device_status(op.ws) == (0, 0)
 
 
+def test_write_and_attend_far_rows(k3):
+    """A cache whose last rows are past 2^32 bytes and 2^31 elements: written, read, and a spoiled one added."""
+    H, n_pages = 8, 70000
+    cfg = k3.k3moe_latent_config(H, page_size=64, rope="none", norm=0)
+    op = k3.LatentAttention(cfg, 2, 130)
+    cache = torch.empty(n_pages, 64, ROW, dtype=torch.bfloat16, device="cuda")
+    r = randn(51)
+    rows, q = r(130, ROW).bfloat16(), r(2, H, ROW).bfloat16()
+    pages = torch.tensor([[n_pages - 1, 3, n_pages - 2], [n_pages - 3, 0, 0]], dtype=torch.int32, device="cuda")
+    at = torch.arange(130, device="cuda")
+    slots = pages[0].long()[at // 64] * 64 + at % 64
+    op.write(rows, cache=cache, slots=slots)
+    op.write(rows[:5].contiguous(), cache=cache, slots=(n_pages - 3) * 64 + at[:5])
+    assert torch.equal(cache[n_pages - 1], rows[:64]) and torch.equal(cache[n_pages - 2, :2], rows[128:])
+    out, lse = torch.empty(2, H, C, dtype=torch.bfloat16, device="cuda"), torch.empty(2, H, device="cuda")
+    op.attend(q, cache, pages, torch.tensor([130, 5], dtype=torch.int32, device="cuda"), out, lse=lse)
+    for i, n in enumerate((130, 5)):
+        k = rows[:n, None]
+        check_attention(out[i:i + 1], lse[i:i + 1], attention64(q[i:i + 1], k, k[..., :C], cfg.scale, 1), f"sequence {i}")
+    cache[n_pages - 2, 1, 7] = float("inf")                # the last row of one sequence that two queries share: the second sees it
+    start = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    op.attend(q, cache, pages[:1], torch.tensor([130], dtype=torch.int32, device="cuda"), out, seq_start=start, lse=lse)
+    k = rows[:129, None]
+    check_attention(out[:1], lse[:1], attention64(q[:1], k, k[..., :C], cfg.scale, 1), "before it")
+    assert not torch.isfinite(out[1, :, 7]).any()
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
 def test_attend_twice_at_once(k3):
     """Two holders on two streams, beside each other; and two captured graphs of one holder, in turn."""
     c, d = Cached([1] * 4, [3000, 500, 0, 77], 56, 64, 31), Cached([3, 1], [900, 4000], 16, 64, 32)
