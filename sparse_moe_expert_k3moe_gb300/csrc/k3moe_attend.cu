@@ -352,9 +352,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             float m[8], l[8];                                 // maxima (minus; 0 where there is none) and sums of columns 8 k + col, + 1
 #pragma unroll
             for (int j = 0; j < 8; j++) m[j] = l[j] = 0.0f;
-            if (q == 0) sh.m[32 * g + lane] = -INFINITY;
+            if (q == 0) sh.m[32 * g + lane] = 32 * g + lane < rows ? -INFINITY : 0.0f;
             group_sync(g);
-            bool first = true;
+            // none: a query of this thread's columns has had no score above minus infinity yet, so that its weights' exponents are
+            // not of a maximum; one is looked for tile by tile until it has (rows of the cache whose scores are infinite may come first)
+            bool first = true, none = true;
             for (int t = now.tile0; t < now.tile1; t++, tile++) {
                 go_on(sh.s_full[tile & 1], tile >> 1);
                 tc_fence_after();
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                 for (int j = 1; j < 15; j += 2) over = max3(over, v[j], v[j + 1]);
                 over = fmaxf(over, v[15]);
-                if (group_any(g, first || over > kAtSlack)) {
+                if (group_any(g, none || over > kAtSlack)) {
                     float x[8];
 #pragma unroll
                     for (int j = 0; j < 8; j++) x[j] = fmaxf(v[4 * (j >> 1) + (j & 1)], v[4 * (j >> 1) + 2 + (j & 1)]) - m[j];
@@ -395,10 +397,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         sh.f[32 * g + lane] = m1 == -INFINITY || first ? 1.0f : exp2_fast(m0 - m1);
                     }
                     group_sync(g);
+                    none = false;
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
                         const int at = 32 * g + 8 * (j >> 1) + col + (j & 1);
-                        const float to = sh.m[at] == -INFINITY ? 0.0f : -sh.m[at], by = to - m[j];
+                        const bool has = sh.m[at] != -INFINITY;
+                        const float to = has ? -sh.m[at] : 0.0f, by = to - m[j];
+                        none = none || !has;
                         m[j] = to;
                         l[j] *= sh.f[at];
                         v[4 * (j >> 1) + (j & 1)] += by;

@@ -1,0 +1,50 @@
+"""The latent attention's operators on the paths that go by the number of blocks: query blocks sorted by their length, several
+whole ones on an SM, the head projection's ring used over; captured calls that replay on other lengths; and rows
+whose scores leave nothing.  Definitions, tolerances and inputs are those of test_gpu_latent.py."""
+import pytest
+
+from test_gpu_latent import C, K, Cached, Expanded, attention64, check_attention, k3  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+# ----------------------------------------------------------------------------- scores that leave nothing
+
+LOWEST = -3.3895313892515355e38                                # bf16's
+
+
+@pytest.mark.parametrize("value", [-float("inf"), LOWEST])
+@pytest.mark.parametrize("masked,more,other", [(1, 300, 700), (64, 3, 700), (200, 300, 700), (130, 20000, 700), (64, 3, 60), (130, 100, 60), (200, 150, 60)])
+def test_attend_first_rows_of_no_weight(k3, masked, more, other, value):
+    """A sequence's first rows hold minus infinity, or the lowest value, in a rotated column and finite values in c: their scores are
+    minus infinity (4 times the lowest passes float's), their weights zero, and the rows behind them, whose scores are
+    about -173, have all the weight; with a short other sequence one SM has all of them."""
+    c = Cached([1, 2], [masked + more, other], 16, 64, masked + more)
+    c.q[..., C] = 4
+    rows = c.rows[0]
+    rows[:masked, C], rows[masked:, C] = value, -600
+    at = torch.arange(masked + more, device="cuda")
+    c.cache[c.pages[0].long()[at // 64], at % 64] = rows
+    op, cfg = c.holder(k3)
+    c(op)
+    k = rows[masked:, None]
+    check_attention(c.out[:1], c.lse[:1], attention64(c.q[:1], k, k[..., :C], cfg.scale, 1), "masked")
+    c.check(cfg, skip=[0])
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+@pytest.mark.parametrize("value", [-float("inf"), LOWEST])
+@pytest.mark.parametrize("masked,more", [(1, 300), (128, 40), (200, 300), (130, 6000)])
+def test_prompt_first_keys_of_no_weight(k3, masked, more, value):
+    c = Expanded([40, 30], [masked + more, 30], 2, False, masked + more)
+    c.q[..., K] = 4
+    c.rope[:masked, 0], c.rope[masked:masked + more, 0] = value, -600
+    op, cfg = c.holder(k3)
+    c(op)
+    kv = c.kv[masked:masked + more]
+    k = torch.cat([kv[..., :K], c.rope[masked:masked + more, None].expand(-1, 2, -1)], -1)
+    check_attention(c.out[:40], c.lse[:40], attention64(c.q[:40], k, kv[..., K:], cfg.scale, 1), "masked")
+    c.check(cfg, skip=[0])
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
