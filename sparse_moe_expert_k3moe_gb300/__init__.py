@@ -842,6 +842,8 @@ class _Holder:
         self._words = lib().k3moe_call
         self.ws_bytes = ws_bytes
         self.ws = torch.zeros(ws_bytes, dtype=torch.uint8, device=self.device) if ws_bytes else None
+        if ws_bytes and self._index >= 0 and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self._index).synchronize()    # the zeros are there before a call on any other stream
 
     def _entry(self, entry, name, n):
         """What _run calls: one of k3moe.h's k3moe_entry, its name and its n arguments.  They go as one string of words:

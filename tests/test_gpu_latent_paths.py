@@ -48,3 +48,21 @@ def test_prompt_first_keys_of_no_weight(k3, masked, more, value):
     check_attention(c.out[:40], c.lse[:40], attention64(c.q[:40], k, kv[..., K:], cfg.scale, 1), "masked")
     c.check(cfg, skip=[0])
     assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+# ----------------------------------------------------------------------------- holders
+
+def test_holder_made_on_a_busy_stream(k3):
+    """A holder serves every stream from the first call on, whatever the stream it was made on is still busy with: what
+    the call reports stays reported."""
+    c = Cached([1], [100], 8, 64, 61)
+    c.pages[0, 1] = -1
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)                         # about a tenth of a second
+    op, cfg = c.holder(k3)
+    c(op, stream=side)
+    torch.cuda.synchronize()
+    assert k3.k3moe_device_status(op.ws) == (6, 0x1)
+    c.rows[0][64:] = 0                                      # the page reads as zeros
+    c.check(cfg)
