@@ -44,6 +44,7 @@ class LatentLayer:
         # any order will do: here the sequences' pages take turns
         self.pages = torch.arange(n_seq * each, dtype=torch.int32, device=dev).view(each, n_seq).t().contiguous()
         self.lens = torch.zeros(n_seq, dtype=torch.int32, device=dev)
+        self._every = torch.arange(n_seq, device=dev)
         new = lambda *s, dtype=torch.bfloat16: torch.empty((T_max, *s), dtype=dtype, device=dev)  # noqa: E731
         self._h, self._z, self._y, self._c = new(d), new(d), new(d), new(C + R)
         self._q, self._qa, self._kv = new(H, K + R), new(H, C + R), new(H, K + V)
@@ -85,9 +86,17 @@ class LatentLayer:
         x += self.moe(self._h[:T], self._moe[:T])
         return x
 
+    def _slots(self, sequences, positions):
+        """The rows of the cache for tokens of these sequences at these positions.  -1, which writes nothing, for one that no page holds:
+        a captured step may be replayed once too often, and an index out of range ends the process."""
+        page = torch.div(positions, self.page, rounding_mode="floor").long()
+        held = (page >= 0) & (page < self.pages.shape[1]) & (sequences >= 0) & (sequences < self.n_seq)
+        rows = self.pages[torch.where(held, sequences, 0), torch.where(held, page, 0)].long() * self.page + positions % self.page
+        return torch.where(held, rows, -1)
+
     def prompt(self, x, seq_start, positions, sequences):
         """Prompts of all sequences, from position 0 on: x [T][d]; positions, sequences [T] of each token."""
-        slots = self.pages[sequences, (positions // self.page).long()].long() * self.page + positions % self.page
+        slots = self._slots(sequences, positions)
 
         def attend(q, c):
             T = q.shape[0]
@@ -99,10 +108,10 @@ class LatentLayer:
         return self._half(x, attend)
 
     def step(self, x):
-        """One token of each sequence: x [n_seq][d]."""
+        """One token of each sequence: x [n_seq][d].  A sequence whose pages are full is left out, and
+        k3moe_device_status(attn.ws) says so."""
         positions = self.lens.clone()
-        which = (positions // self.page).long()
-        slots = self.pages.gather(1, which[:, None])[:, 0].long() * self.page + positions % self.page
+        slots = self._slots(self._every, positions)
         self.lens += 1
 
         def attend(q, c):

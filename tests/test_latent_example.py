@@ -57,3 +57,34 @@ def test_prompt_then_captured_steps():
             err = (token[s].double() - ref).norm() / ref.norm()
             assert torch.isfinite(token).all() and err <= TOL, f"step {i}, sequence {s}: {err:.3e}"
     assert made.lens.tolist() == whole
+
+
+def test_slots_past_the_pages():
+    """Tokens that no page holds are written nowhere, and indexed nowhere."""
+    made = layer(example(), 2, 40, 6, "cpu")                 # three pages of 16 each
+    sequences, positions = torch.tensor([0, 1, 1, 0, 1, 0, 2, -1]), torch.tensor([0, 47, 17, 48, 1 << 30, -1, 5, 5], dtype=torch.int32)
+    want = [made.pages[0, 0] * 16, made.pages[1, 2] * 16 + 15, made.pages[1, 1] * 16 + 1, -1, -1, -1, -1, -1]
+    assert made._slots(sequences, positions).tolist() == [int(x) for x in want]
+
+
+def test_step_with_full_pages_is_laid_out():
+    made = layer(example(), 2, 40, 6, "cpu")
+    made._half = lambda x, attend: x
+    made.lens.copy_(torch.tensor([48, 7]))
+    made.step(torch.zeros(2, d, dtype=torch.bfloat16))
+    assert made.lens.tolist() == [49, 8]
+
+
+@pytest.mark.gpu
+def test_step_with_full_pages():
+    """The full sequence is left out and reported, the other one goes on; nothing but its row is written."""
+    mod = example()
+    made = layer(mod, 2, 40, 60).randomise(3)
+    made.prompt(torch.randn(55, d, device="cuda").bfloat16(), *mod.places([48, 7]))
+    assert mod.k3.k3moe_device_status(made.attn.ws) == (0, 0)
+    cache, token = made.cache.clone(), torch.randn(2, d, device="cuda").bfloat16()
+    made.step(token)
+    assert mod.k3.k3moe_device_status(made.attn.ws) == (6, 0x2)
+    written = (made.cache != cache).any(-1).flatten().nonzero().flatten()
+    assert written.tolist() == [int(made.pages[1, 0]) * 16 + 7]
+    assert torch.isfinite(token[1]).all()
