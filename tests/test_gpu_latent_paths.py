@@ -3,7 +3,7 @@ whole ones on an SM, the head projection's ring used over; captured calls that r
 whose scores leave nothing.  Definitions, tolerances and inputs are those of test_gpu_latent.py."""
 import pytest
 
-from test_gpu_latent import C, K, Cached, Expanded, attention64, check_attention, k3  # noqa: F401
+from test_gpu_latent import C, K, ROW, Cached, Expanded, attention64, check_attention, k3  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,42 @@ def test_holder_made_on_a_busy_stream(k3):
     assert k3.k3moe_device_status(op.ws) == (6, 0x1)
     c.rows[0][64:] = 0                                      # the page reads as zeros
     c.check(cfg)
+
+
+# ----------------------------------------------------------------------------- absorbed
+
+@pytest.mark.parametrize("width,lens", [
+    (330, ([500, 64, 3, 0], [3, 20000, 65, 700], [20000, 0, 1, 64], [9000, 9001, 63, 1], [1, 2, 3, 4])),        # cut, and joined
+    (4, ([200, 64, 3, 0], [0, 129, 256, 255], [1, 2, 3, 4]))])                                                   # whole
+def test_attend_captured_follows(k3, width, lens):
+    """One captured call replays on other lengths, pages, queries and offsets: other cuts, other blocks to join."""
+    queries = [[1, 0, 2, 1], [2, 1, 1, 0], [0, 0, 4, 0], [1, 1, 1, 1], [0, 3, 0, 1]]
+    first = Cached(queries[0], lens[0], 56, 64, 91)
+    op, cfg = first.holder(k3)
+    room = 400
+    cache = torch.zeros(room, 64, ROW, dtype=torch.bfloat16, device="cuda")
+    pages = torch.zeros(4, width, dtype=torch.int32, device="cuda")
+    q, start, kv_len = torch.zeros_like(first.q), torch.zeros_like(first.start), torch.zeros_like(first.kv_len)
+    out, lse = torch.empty_like(first.out), torch.empty_like(first.lse)
+
+    def put(d):
+        assert d.n_pages <= room and d.pages.shape[1] - 1 <= width and d.T == 4
+        cache.fill_(float("nan"))
+        cache[:d.n_pages].copy_(d.cache)
+        pages.fill_(-1)
+        w = min(width, d.pages.shape[1])                   # the last column of theirs is no page
+        pages[:, :w].copy_(d.pages[:, :w])
+        for mine, other in ((q, d.q), (start, d.start), (kv_len, d.kv_len)):
+            mine.copy_(other)
+        out.fill_(7.5)
+        lse.fill_(7.5)
+
+    put(first)
+    graph = k3._capture(lambda x, y: op.attend(x, cache, pages, kv_len, y, seq_start=start, lse=lse), q, out)
+    for i in [*range(len(lens)), 0]:
+        d = Cached(queries[i], lens[i], 56, 64, 91 + i)
+        put(d)
+        graph.replay()
+        d.out, d.lse = out, lse
+        d.check(cfg)
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
