@@ -10,6 +10,10 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
 # ----------------------------------------------------------------------------- scores that leave nothing
 
 LOWEST = -3.3895313892515355e38                                # bf16's
@@ -104,4 +108,21 @@ def test_attend_captured_follows(k3, width, lens):
         graph.replay()
         d.out, d.lse = out, lse
         d.check(cfg)
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+@pytest.mark.parametrize("n,H,longest", [(96, 128, 192), (200, 128, 120), (130, 100, 64)])
+def test_attend_whole_blocks_in_turn(k3, n, H, longest):
+    """Short tables and more query blocks of 64 than SMs, none cut: an SM has several, one after the other."""
+    queries = [(1, 1, 2, 0, 3)[i % 5] for i in range(n)]
+    lens = [(37 * i) % (longest + 1) if i else longest for i in range(n)]
+    c = Cached(queries, lens, H, 64, n + H)
+    blocks, tiles = -(-c.T * H // 64), c.pages.shape[1]
+    assert blocks > sms() and tiles * (-(-blocks // sms()) - 0.5 * blocks / sms()) <= 6.5
+    op, cfg = c.holder(k3)
+    c(op)
+    c.check(cfg)
+    out, lse = c.out.clone(), c.lse.clone()
+    c(op)
+    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
     assert k3.k3moe_device_status(op.ws) == (0, 0)
