@@ -126,3 +126,15 @@ def test_attend_whole_blocks_in_turn(k3, n, H, longest):
     c(op)
     assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
     assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+@pytest.mark.parametrize("lens", [[300, 20000, 5, 700], [60, 130, 5, 100]])
+def test_attend_leaves_other_rows(k3, lens):
+    """Tokens before the first sequence and behind the last stay as they are, whatever their queries hold."""
+    c = Cached([3, 2, 4, 5], lens, 16, 64, 63)
+    op, cfg = c.holder(k3)
+    c.q[:3], c.q[9:] = float("nan"), float("inf")
+    op.attend(c.q, c.cache, c.pages[1:3].contiguous(), c.kv_len[1:3].contiguous(), c.out, seq_start=c.start[1:4].contiguous(), lse=c.lse)
+    assert (c.out[:3] == 7.5).all() and (c.out[9:] == 7.5).all() and (c.lse[:3] == 7.5).all() and (c.lse[9:] == 7.5).all()
+    c.check(cfg, skip=[0, 3])
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
