@@ -1,9 +1,11 @@
 """The latent attention's operators on the paths that go by the number of blocks: query blocks sorted by their length, several
 whole ones on an SM, the head projection's ring used over; captured calls that replay on other lengths; and rows
 whose scores leave nothing.  Definitions, tolerances and inputs are those of test_gpu_latent.py."""
+import itertools
+
 import pytest
 
-from test_gpu_latent import C, K, ROW, Cached, Expanded, attention64, check_attention, k3  # noqa: F401
+from test_gpu_latent import C, K, R, ROW, Cached, Expanded, attention64, check_attention, k3  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -137,4 +139,71 @@ def test_attend_leaves_other_rows(k3, lens):
     op.attend(c.q, c.cache, c.pages[1:3].contiguous(), c.kv_len[1:3].contiguous(), c.out, seq_start=c.start[1:4].contiguous(), lse=c.lse)
     assert (c.out[:3] == 7.5).all() and (c.out[9:] == 7.5).all() and (c.lse[:3] == 7.5).all() and (c.lse[9:] == 7.5).all()
     c.check(cfg, skip=[0, 3])
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+# ----------------------------------------------------------------------------- expanded, sorted
+
+RAGGED = [429, 1, 700, 429, 0, 942, 500], [429, 101, 900, 929, 50, 1442, 100]     # prefixes, an empty one, more queries than keys
+SORTED = [  # queries, keys, heads, causal
+    (*RAGGED, 16, 1),
+    (*RAGGED, 16, 0),
+    ([300] * 8, None, 16, 1),                                  # alike
+    ([256] * 8, [256, 0, 600, 256, 256, 0, 600, 1], 16, 1),    # some without keys
+    ([1] * 128, [(11 * i) % 140 for i in range(128)], 3, 1),
+    ([3] * 127, [(29 * i) % 300 for i in range(127)], 3, 0),
+    ([0, 5, 1, 0] * 32, [(7 * i) % 90 for i in range(128)], 3, 1),     # half of the places have no block
+    ([2000, 40], [2000, 2000], 17, 1),
+    ([5000], None, 8, 1),
+]
+
+
+def in_order(c):
+    """Asserts what a call has to have for its query blocks to be sorted."""
+    blocks, S = c.T // 256 + min(len(c.queries), c.T), sum(c.keys)
+    assert blocks * c.H > sms() and blocks <= 128 and len(c.queries) <= 128 and S * c.H * (K + R + R) * 2 <= 64 << 20
+
+
+@pytest.mark.parametrize("case", SORTED, ids=lambda c: f"{len(c[0])}-{sum(c[0])}x{c[2]}-{sum(c[1] or c[0])}-{c[3]}")
+def test_prompt_sorted(k3, case):
+    queries, keys, H, causal = case
+    c = Expanded(queries, keys, H, True, sum(queries) + H)
+    in_order(c)
+    op, cfg = c.holder(k3, causal=causal)
+    c(op)
+    c.check(cfg)
+    out, lse = c.out.clone(), c.lse.clone()
+    c(op)
+    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+@pytest.mark.parametrize("name,at,bad,lost", [("start", 3, -1, [2, 3]), ("start", 7, 3002, [6]), ("kv_start", 1, 1 << 30, [0, 1]), ("kv_start", 6, -7, [5, 6])])
+def test_prompt_sorted_reports_what_does_not_fit(k3, name, at, bad, lost):
+    c = Expanded(*RAGGED, 16, False, 77)
+    in_order(c)
+    op, cfg = c.holder(k3)
+    getattr(c, name)[at] = bad
+    c(op)
+    c.check(cfg, skip=lost)
+    first = list(itertools.accumulate([0, *c.queries]))
+    for i in lost:
+        assert (c.out[first[i]:first[i + 1]] == 7.5).all() and (c.lse[first[i]:first[i + 1]] == 7.5).all()
+    assert k3.k3moe_device_status(op.ws) == (6, 0x2)
+
+
+def test_prompt_sorted_captured(k3):
+    """A captured call replays on other lengths: another order."""
+    c = Expanded(*RAGGED, 16, False, 78)
+    op, cfg = c.holder(k3)
+    graph = k3._capture(lambda x, out: c(op), c.q, c.out)
+    d = Expanded([1, 1500, 0, 300, 300, 899, 1], [700, 1500, 0, 251, 300, 1000, 200], 16, False, 79)
+    assert d.T == c.T and sum(d.keys) == sum(c.keys)
+    for name in ("q", "kv", "rope", "start", "kv_start"):
+        getattr(c, name).copy_(getattr(d, name))
+    c.out.fill_(7.5)
+    c.lse.fill_(7.5)
+    graph.replay()
+    c.queries, c.keys = d.queries, d.keys
+    c.check(cfg)
     assert k3.k3moe_device_status(op.ws) == (0, 0)
