@@ -5,7 +5,7 @@ import itertools
 
 import pytest
 
-from test_gpu_latent import C, K, R, ROW, Cached, Expanded, attention64, check_attention, k3  # noqa: F401
+from test_gpu_latent import C, K, R, ROW, Cached, Expanded, attention64, check_attention, k3, randn, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -206,4 +206,36 @@ def test_prompt_sorted_captured(k3):
     graph.replay()
     c.queries, c.keys = d.queries, d.keys
     c.check(cfg)
+    assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+# ----------------------------------------------------------------------------- a head's own projection
+
+@pytest.mark.parametrize("T,H,K_,N,xpad,ypad", [
+    (333, 56, 512, 128, 64, 64),                               # 176 tokens a block, five places of the ring for eight chunks
+    (512, 56, 512, 128, 0, 8),                                 # 256 a block, four places
+    (500, 56, 512, 128, 8, 1),                                 # a ragged last tile, y's heads at odd places
+    (250, 28, 512, 600, 0, 0),
+    (240, 100, 512, 127, 16, 0),
+    (600, 56, 512, 128, 0, 0),                                 # more blocks than SMs: three places, two blocks an SM
+    (1000, 56, 512, 129, 64, 0),                               # two places
+    (1000, 60, 328, 72, 8, 3),
+    (4096, 56, 512, 128, 0, 64),
+])
+def test_head_linear_ring(k3, T, H, K_, N, xpad, ypad):
+    """Rings with fewer places than there are chunks of K, and blocks of up to 256 tokens."""
+    r = randn(T + H)
+    x = r(T, H, K_ + xpad).bfloat16()[..., :K_]
+    w = (r(H, N, K_) / K_ ** 0.5).bfloat16()
+    op = k3.HeadLinear(k3.k3moe_head_linear_config(H, N, K_), T)
+    op.w = w
+    wide = torch.full((T, H, N + ypad), 7.5, dtype=torch.bfloat16, device="cuda")
+    y = op(x, wide[..., :N])
+    for t in range(0, T, 1024):
+        a, b = x[t:t + 1024].double(), w.double()
+        ref, mag = torch.einsum("thk,hnk->thn", a, b), torch.einsum("thk,hnk->thn", a.abs(), b.abs())
+        within(y[t:t + 1024], ref, 4 * K_ ** 0.5 * 2.0 ** -23 * mag)
+    assert (wide[..., N:] == 7.5).all()
+    for _ in range(2):
+        assert torch.equal(op(x, torch.full_like(y, 7.5)), y)
     assert k3.k3moe_device_status(op.ws) == (0, 0)
