@@ -59,6 +59,37 @@ __device__ __forceinline__ float4 bf4(uint2 w)
 }
 __device__ __forceinline__ float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + (a.z * b.z + a.w * b.w); }
 
+// Two floats side by side, for the instructions that work on both.
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t p)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
 // One block per (sequence, head, 64 value columns).  A warp holds 16 key rows of the state, a
 // lane two value columns of them, rows in pairs for the instructions that take two floats.
 // The tokens' k, q and exp(g) are made ready eight at a time, one by each warp, so that a
@@ -254,6 +285,25 @@ __device__ __forceinline__ void split2(uint64_t xy, uint32_t *hi, uint32_t *mid)
     *mid = *reinterpret_cast<const uint32_t *>(&m);
 }
 __device__ __forceinline__ void split2(float x, float y, uint32_t *hi, uint32_t *mid) { split2(pack2(x, y), hi, mid); }
+// A whole warp's wait, asleep in the barrier's own wait (up to 20 us a time) rather than
+// polling beside the warps at work; bounded as mb_wait.
+__device__ __forceinline__ bool mb_wait_asleep(uint64_t *b, uint32_t parity)
+{
+    const uint32_t a = saddr(b);
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(a), "r"(parity), "r"(20000u)
+            : "memory");
+        const bool ok = __all_sync(0xffffffffu, done != 0);
+        if (ok) return true;
+        if (clock64() - t0 > kTcWaitCyc) return false;
+    }
+}
 __device__ __forceinline__ float max_nan(float x, float y)
 {
     float r;

@@ -1,6 +1,6 @@
-// k3moe_latent.cuh -- what both forms of the latent attention share: which tokens are a
-// sequence's, the search for a block's piece of work over the sequences, and the repair of values that
-// no arithmetic survives where a query does not see them.
+// k3moe_latent.cuh -- what the forms of the latent attention share: the workspace's layout, the search
+// for a block's piece of work over the sequences, and the repair of values that no arithmetic
+// survives where a query does not see them; and the absorbed form's waits.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -17,21 +17,6 @@ constexpr float kLatLog2e = 1.4426950408889634f, kLatLn2 = 0.6931471805599453f;
 constexpr int kMaxShares = 512;
 constexpr size_t kLatPart = (size_t)64 * kLatC + 2 * 64, kLatJoinBytes = (size_t)kMaxShares * 64;
 inline float *latent_parts(uint8_t *ws) { return reinterpret_cast<float *>(ws + kCtrOffset + kCtrBytes + kLatJoinBytes); }
-
-// Queries [first, first + n) of sequence i; false when its offsets are not ascending within 0 .. T.
-__device__ __forceinline__ bool latent_queries(const int32_t *start, int n_seq, int T, int i, int *first, int *n)
-{
-    if (!start) {
-        const int each = n_seq == 1 ? T : 1;
-        *first = i * each;
-        *n = each;
-        return true;
-    }
-    const int s0 = start[i], s1 = start[i + 1];
-    *first = s0;
-    *n = s1 - s0;
-    return s0 >= 0 && s1 >= s0 && s1 <= T;
-}
 
 // A warp's wait on a barrier's phase.  What follows when it is not complete at the first try, which itself waits a while, is a
 // call: the roles of a block share the instruction cache, and every wait written out in full was a fifth of their code.

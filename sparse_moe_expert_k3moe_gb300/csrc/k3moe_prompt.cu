@@ -68,6 +68,21 @@ struct PromptShared {
 };
 static_assert(kPrSmem + sizeof(PromptShared) <= 227 * 1024, "an SM's shared memory");
 
+// Queries [first, first + n) of sequence i; false when its offsets are not ascending within 0 .. T.
+__device__ __forceinline__ bool latent_queries(const int32_t *start, int n_seq, int T, int i, int *first, int *n)
+{
+    if (!start) {
+        const int each = n_seq == 1 ? T : 1;
+        *first = i * each;
+        *n = each;
+        return true;
+    }
+    const int s0 = start[i], s1 = start[i + 1];
+    *first = s0;
+    *n = s1 - s0;
+    return s0 >= 0 && s1 >= s0 && s1 <= T;
+}
+
 // 64 of a row's scores become weights in tensor memory, packed; returns their sum.  Single floats: pairs of them cost
 // more moves than they save here (5.7 instructions a weight, 4 this way).
 __device__ __forceinline__ float weigh(const uint32_t *v, uint32_t taddr, float c, float m)

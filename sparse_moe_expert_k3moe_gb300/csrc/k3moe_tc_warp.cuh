@@ -1,7 +1,7 @@
 // k3moe_tc_warp.cuh -- more inline-PTX helpers of tensor-core kernels (sm_103a), for the
 // operators whose operands also live in tensor memory: MMA issue, commit and tile loads by a
-// converged warp, A operands in and stores to tensor memory, prefetches to the L2; pairs of
-// floats; and tensor maps of matrices whose rows are slices of wider ones.
+// converged warp, A operands in and stores to tensor memory, prefetches to the L2; and tensor maps
+// of matrices whose rows are slices of wider ones.
 #pragma once
 #include "k3moe_tc.cuh"
 
@@ -109,56 +109,6 @@ __device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t (&r)[8]
                  : "r"(taddr));
 }
 
-// A whole warp's wait, asleep in the barrier's own wait (up to 20 us a time) rather than
-// polling beside the warps at work; bounded as mb_wait.
-__device__ __forceinline__ bool mb_wait_asleep(uint64_t *b, uint32_t parity)
-{
-    const uint32_t a = saddr(b);
-    const long long t0 = clock64();
-    for (;;) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(a), "r"(parity), "r"(20000u)
-            : "memory");
-        const bool ok = __all_sync(0xffffffffu, done != 0);
-        if (ok) return true;
-        if (clock64() - t0 > kTcWaitCyc) return false;
-    }
-}
-// Two floats side by side, for the instructions that work on both.
-__device__ __forceinline__ uint64_t pack2(float x, float y)
-{
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
-    return p;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t p)
-{
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
 __device__ __forceinline__ float max3(float x, float y, float z)
 {
     float r;
