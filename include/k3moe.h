@@ -538,9 +538,10 @@ k3moe_status k3moe_latent_write(const k3moe_latent_config *lc, int32_t T, const 
  * A query that sees no row has zeros and minus infinity.  A page outside [0, n_pages) sets K3MOE_DEV_BAD_INDEX and its
  * rows read as zeros; a seq_start pair that is not ascending within [0, T], or a kv_len out of range, sets
  * K3MOE_DEV_BAD_OFFSETS and the sequence is skipped; one that shares tokens with another has no defined result.  Scores, sums
- * and outputs are float, the weights exp(s - m) are rounded to bf16 for their product with c, out once.  Rows that a query
- * does not see do not reach it, whatever they hold.  q, cache and out 16-byte aligned, the others to their element; out and
- * lse overlap nothing.  T may be 0.  ws per k3moe_latent_workspace_bytes; calls that share one run on one stream. */
+ * and outputs are float, the weights exp(s - m) are rounded to bf16 for their product with c, out once.  A weight is up to 2^8
+ * before the division by their sum (2^30 in the expanded form), so that values beyond 2^119 / rows (2^97 / keys) may overflow.  A score of
+ * minus infinity is a weight of zero.  Rows that a query does not see do not reach it, whatever they hold.  q, cache and out
+ * 16-byte aligned, the others to their element; out and lse overlap nothing.  T may be 0.  ws per k3moe_latent_workspace_bytes; calls that share one run on one stream. */
 k3moe_status k3moe_latent_attend(const k3moe_latent_config *lc, int32_t n_seq, int32_t T, const int32_t *seq_start,
                                  const uint16_t *q, int64_t q_stride, int64_t q_head_stride, const uint16_t *cache,
                                  int32_t n_pages, const int32_t *pages, int32_t max_pages, const int32_t *kv_len,

@@ -917,7 +917,8 @@ class HeadLinear(_Holder):
 class LatentAttention(_Holder):
     """The latent cache's write and attention over it (k3moe_latent_write, _attend, _prompt), for up to n_seq_max
     sequences and T_max query tokens a call: holds gain [rank] f32 and inv_freq [rope_dim / 2] f64, set by the caller, and
-    a workspace; the cache is the caller's."""
+    a workspace; the cache is the caller's.  Calls and captured graphs of one holder share its workspace: one stream at a time has
+    them, and the holder is kept until they are done."""
 
     def __init__(self, lc: K3MoELatentConfig, n_seq_max: int, T_max: int, device="cuda"):
         import torch

@@ -425,6 +425,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     }
                 }
                 first = false;
+                // the sums are of the weights in float; the product takes them in bf16, as it takes c, each off by 2^-8 of itself at most
                 uint32_t p[8];
 #pragma unroll
                 for (int k = 0; k < 4; k++)

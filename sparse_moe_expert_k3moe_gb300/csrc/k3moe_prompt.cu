@@ -83,8 +83,9 @@ __device__ __forceinline__ bool latent_queries(const int32_t *start, int n_seq, 
     return s0 >= 0 && s1 >= s0 && s1 <= T;
 }
 
-// 64 of a row's scores become weights in tensor memory, packed; returns their sum.  Single floats: pairs of them cost
-// more moves than they save here (5.7 instructions a weight, 4 this way).
+// 64 of a row's scores become weights in tensor memory, packed; returns their sum, of the weights as they are in float.  The
+// product takes them in bf16, as it takes the values: each is off by 2^-8 of itself at most, whatever m is, and in f32 they would not
+// fit over the scores.  Single floats: pairs of them cost more moves than they save here (5.7 instructions a weight, 4 this way).
 __device__ __forceinline__ float weigh(const uint32_t *v, uint32_t taddr, float c, float m)
 {
     const float minus = m == -INFINITY ? 0.0f : -m;
@@ -139,6 +140,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         prefetch_map(&mkv);
         prefetch_map(&mr);
     }
+    // Ahead of the wait for the kernel before, and held through it.  That one's blocks have all begun by then, so one of them that has
+    // yet to take tensor memory has its SM already; it cannot be this block's SM, whose shared memory leaves 2 KB beside a block,
+    // and every kernel that takes tensor memory has tens of KB.
     if (warp == kPrWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sh.tmem)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");

@@ -239,3 +239,28 @@ def test_head_linear_ring(k3, T, H, K_, N, xpad, ypad):
     for _ in range(2):
         assert torch.equal(op(x, torch.full_like(y, 7.5)), y)
     assert k3.k3moe_device_status(op.ws) == (0, 0)
+
+
+# ----------------------------------------------------------------------------- large values
+
+@pytest.mark.parametrize("power", [100, -60])
+def test_attention_of_large_and_small_values(k3, power):
+    """Values 2^power as large have outputs 2^power as large, bit for bit: weights and sums are the same, and nothing overflows within
+    the documented bound (2^119 / 2000 rows, 2^97 / 900 keys of values below 8, so 2^80 there) or is lost: products are of
+    weights above 2^-30 and values above 2^-90."""
+    c = Cached([1, 2], [2000, 70], 16, 64, 5)
+    op, _ = c.holder(k3)
+    c.q[..., :C] = 0                                       # scores are of the rotated columns alone
+    c(op)
+    out, lse = c.out.clone(), c.lse.clone()
+    c.cache[..., :C] *= 2.0 ** power
+    c(op)
+    assert torch.equal(c.out.double(), out.double() * 2.0 ** power) and torch.equal(c.lse, lse)
+    power = min(power, 80)
+    e = Expanded([100, 300], [900, 300], 2, False, 6)
+    op, _ = e.holder(k3)
+    e(op)
+    out, lse = e.out.clone(), e.lse.clone()
+    e.kv[..., K:] *= 2.0 ** power
+    e(op)
+    assert torch.equal(e.out.double(), out.double() * 2.0 ** power) and torch.equal(e.lse, lse)
