@@ -830,8 +830,8 @@ def _headed(what, t, types, shape, index):
 
 
 class _Holder:
-    """What the holders below share: a device, its current stream and, where asked for, a workspace.  A call reads its config when
-    it is made: the entry point does, so the tensors' checks do."""
+    """What the holders below share: a device, its current stream and, where asked for, a workspace; and the config, which the
+    entry point reads at each call: _read takes from it what the tensors' checks need, again whenever it has changed."""
 
     def _init(self, device, ws_bytes=0):
         import torch
@@ -844,6 +844,10 @@ class _Holder:
         self.ws = torch.zeros(ws_bytes, dtype=torch.uint8, device=self.device) if ws_bytes else None
         if ws_bytes and self._index >= 0 and not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream(self._index).synchronize()    # the zeros are there before a call on any other stream
+
+    def _follow(self, config):
+        self._config, self._at = config, ctypes.addressof(config)
+        self._bytes, self._seen = (ctypes.c_char * ctypes.sizeof(config)).from_buffer(config), None
 
     def _entry(self, entry, name, n):
         """What _run calls: one of k3moe.h's k3moe_entry, its name and its n arguments.  They go as one string of words:
@@ -870,17 +874,25 @@ class Norm(_Holder):
         self._init(device)
         self.nc = nc
         self.post_gain = self.scale = self.pre_gain = None
-        self._config, self._at, self._norm = nc, ctypes.addressof(nc), self._entry(0, "k3moe_norm", 16)
+        self._follow(nc)
+        self._norm = self._entry(0, "k3moe_norm", 16)
+
+    def _read(self):
+        nc, self._seen = self._config, self._bytes.raw
+        self._n, self._group = (nc.n,), (nc.group,)
+        self._xtype, self._stype = self._f32 if nc.x_f32 else self._bf16, self._f32 if nc.sum_f32 else self._bf16
 
     def __call__(self, x, out=None, gate=None, residual=None, total=None, stream=None):
         """x [T][n] by x_f32; gate [T][n] bf16; residual and total [T][n] by sum_f32; out [T][n] bf16; rows may be
         slices of wider ones.  Returns out, or total where nothing is normed for the next block."""
-        dev, bf16, f32, nc = self._index, self._bf16, self._f32, self._config
-        T, n, stype = x.shape[0], nc.n, f32 if nc.sum_f32 else bf16
-        shape = (T, n)
-        post, scale = _dense("post_gain", self.post_gain, f32, (nc.group,), dev), _dense("scale", self.scale, f32, (n,), dev)
-        pre = _dense("pre_gain", self.pre_gain, f32, (n,), dev)
-        xp, xs = _rowed("x", x, f32 if nc.x_f32 else bf16, shape, dev)
+        if self._bytes.raw != self._seen:
+            self._read()
+        dev, bf16, f32, stype = self._index, self._bf16, self._f32, self._stype
+        T = x.shape[0]
+        shape = (T, self._n[0])
+        post, scale = _dense("post_gain", self.post_gain, f32, self._group, dev), _dense("scale", self.scale, f32, self._n, dev)
+        pre = _dense("pre_gain", self.pre_gain, f32, self._n, dev)
+        xp, xs = _rowed("x", x, self._xtype, shape, dev)
         gp, gs = _rowed("gate", gate, bf16, shape, dev)
         rp, rs = _rowed("residual", residual, stype, shape, dev)
         tp, ts = (rp, rs) if total is residual else _rowed("total", total, stype, shape, dev)
@@ -897,18 +909,24 @@ class HeadLinear(_Holder):
     def __init__(self, hc: K3MoEHeadLinearConfig, T_max: int, device="cuda"):
         self._init(device, k3moe_head_linear_workspace_bytes(hc, T_max))
         self.hc, self.T_max, self.w = hc, T_max, None
-        self._config, self._at, self._linear = hc, ctypes.addressof(hc), self._entry(1, "k3moe_head_linear", 12)
+        self._follow(hc)
+        self._linear = self._entry(1, "k3moe_head_linear", 12)
+
+    def _read(self):
+        hc, self._seen = self._config, self._bytes.raw
+        self._shape = (hc.n_heads, hc.n, hc.k)
 
     def __call__(self, x, y, stream=None):
         """x [T][n_heads][k] bf16, y [T][n_heads][n] bf16 written and returned; heads may be columns of wider ones."""
         T, dev, bf16 = x.shape[0], self._index, self._bf16
-        hc = self._config
-        H, n, k = hc.n_heads, hc.n, hc.k
+        if self._bytes.raw != self._seen:
+            self._read()
+        H, n, k = self._shape
         if T > self.T_max:
             raise ValueError(f"x: {T} tokens, the holder is for {self.T_max}")
         xp, xs, xh = _headed("x", x, bf16, (T, H, k), dev)
         yp, ys, yh = _headed("y", y, bf16, (T, H, n), dev)
-        w = _dense("w", self.w, bf16, (H, n, k), dev)
+        w = _dense("w", self.w, bf16, self._shape, dev)
         if T:
             self._run(self._linear, (self._at, T, xp, xs, xh, w, yp, ys, yh, self.ws.data_ptr(), self.ws_bytes), stream)
         return y
@@ -926,16 +944,21 @@ class LatentAttention(_Holder):
         self.lc, self.n_seq_max, self.T_max = lc, n_seq_max, T_max
         self.gain = self.inv_freq = None
         self._i64, self._f64 = (torch.int64,), (torch.float64,)
-        # the columns are what every config has to have; heads and pages are the config's of the moment
+        # the columns are what every config has to have
         self._C, self._R, self._row = lc.rank, lc.rope_dim, lc.rank + lc.rope_dim
         self._kr, self._kv, self._v = lc.key_dim + lc.rope_dim, lc.key_dim + lc.value_dim, lc.value_dim
-        self._config, self._at, self._write = lc, ctypes.addressof(lc), self._entry(2, "k3moe_latent_write", 21)
-        self._attend, self._prompt = self._entry(3, "k3moe_latent_attend", 17), self._entry(4, "k3moe_latent_prompt", 19)
+        self._follow(lc)
+        self._write, self._attend = self._entry(2, "k3moe_latent_write", 21), self._entry(3, "k3moe_latent_attend", 17)
+        self._prompt = self._entry(4, "k3moe_latent_prompt", 19)
+
+    def _read(self):
+        self._seen, self._H, self._page = self._bytes.raw, self._config.n_heads, self._config.page_size
 
     def new_cache(self, n_pages):
         """A zeroed cache of n_pages pages [n_pages][page_size][rank + rope_dim] bf16."""
         import torch
-        return torch.zeros((n_pages, self._config.page_size, self._row), dtype=torch.bfloat16, device=self.device)
+        self._read()
+        return torch.zeros((n_pages, self._page, self._row), dtype=torch.bfloat16, device=self.device)
 
     def _room(self, n_seq, T):
         if n_seq > self.n_seq_max or T > self.T_max:
@@ -945,6 +968,8 @@ class LatentAttention(_Holder):
         """c [T][rank + rope_dim] bf16, positions [T] int32; the rows go to slots [T] int64 of the cache and to rows
         [T][rank + rope_dim]; q [T][n_heads][rope_dim], the queries' rotated columns, to q_rope, which may be q.  Returns
         rows, or the cache where they go there alone."""
+        if self._bytes.raw != self._seen:
+            self._read()
         dev, bf16, T, row = self._index, self._bf16, c.shape[0], self._row
         if T > self.T_max:
             raise ValueError(f"c: {T} tokens, the holder is for {self.T_max}")
@@ -954,9 +979,9 @@ class LatentAttention(_Holder):
         at = _dense("positions", positions, self._i32, (T,), dev)
         rp, rs = (cp, cs) if rows is c else _rowed("rows", rows, bf16, (T, row), dev)
         n_pages = 0 if cache is None else cache.shape[0]
-        pool = _dense("cache", cache, bf16, (n_pages, self._config.page_size, row), dev)
+        pool = _dense("cache", cache, bf16, (n_pages, self._page, row), dev)
         sl = _dense("slots", slots, self._i64, (T,), dev)
-        shape = (T, self._config.n_heads, self._R)
+        shape = (T, self._H, self._R)
         qp, qs, qh = _headed("q", q, bf16, shape, dev)
         op, os_, oh = (qp, qs, qh) if q_rope is q else _headed("q_rope", q_rope, bf16, shape, dev)
         if T:
@@ -968,11 +993,13 @@ class LatentAttention(_Holder):
         """q [T][n_heads][rank + rope_dim] bf16, pages [n_seq][max_pages] int32, kv_len [n_seq] int32; out
         [T][n_heads][rank] bf16 written and returned, lse [T][n_heads] f32 or None; seq_start [n_seq+1] int32, or None for
         one token each (with one sequence: all)."""
-        dev, bf16, i32, T, n_seq, H = self._index, self._bf16, self._i32, q.shape[0], kv_len.shape[0], self._config.n_heads
+        if self._bytes.raw != self._seen:
+            self._read()
+        dev, bf16, i32, T, n_seq, H = self._index, self._bf16, self._i32, q.shape[0], kv_len.shape[0], self._H
         self._room(n_seq, T)
         qp, qs, qh = _headed("q", q, bf16, (T, H, self._row), dev)
         n_pages, max_pages = cache.shape[0], pages.shape[-1]
-        pool = _dense("cache", cache, bf16, (n_pages, self._config.page_size, self._row), dev)
+        pool = _dense("cache", cache, bf16, (n_pages, self._page, self._row), dev)
         table, lens = _dense("pages", pages, i32, (n_seq, max_pages), dev), _dense("kv_len", kv_len, i32, (n_seq,), dev)
         o, start = _dense("out", out, bf16, (T, H, self._C), dev), _dense("seq_start", seq_start, i32, (n_seq + 1,), dev)
         ls = _dense("lse", lse, self._f32, (T, H), dev)
@@ -985,7 +1012,9 @@ class LatentAttention(_Holder):
         """q [T][n_heads][key_dim + rope_dim], kv [S][n_heads][key_dim + value_dim], rope_key [S][rope_dim] bf16, the last's
         rows at any stride; out [T][n_heads][value_dim] bf16 written and returned, lse [T][n_heads] f32 or None; seq_start and
         kv_start [n_seq+1] int32, or None: one sequence, or the queries' own."""
-        dev, bf16, i32, T, S, H = self._index, self._bf16, self._i32, q.shape[0], kv.shape[0], self._config.n_heads
+        if self._bytes.raw != self._seen:
+            self._read()
+        dev, bf16, i32, T, S, H = self._index, self._bf16, self._i32, q.shape[0], kv.shape[0], self._H
         n_seq = 1 if seq_start is None else seq_start.shape[0] - 1
         self._room(n_seq, T)
         qp, qs, qh = _headed("q", q, bf16, (T, H, self._kr), dev)
